@@ -17,6 +17,7 @@ import ctypes
 import math
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -25,7 +26,10 @@ __all__ = ["FAError", "fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_decode
            "fa_bwd_varlen", "fa_bwd_varlen_workspace_bytes", "fa_check_device_error", "fa_status_string",
            "fa_test_withhold_load",
            "flash_attention", "flash_attention_varlen", "flash_attention_bwd", "flash_attention_varlen_bwd",
-           "flash_decode", "flash_decode_paged", "library_path", "load_library", "EXPORTED_SYMBOLS"]
+           "flash_decode", "flash_decode_paged", "fa_kv_write_q4", "fa_kv_read_q4", "fa_decode_paged_window",
+           "fa_decode_paged_q4", "fa_decode_splits", "KVCacheQ4", "kv_cache_q4", "flash_kv_write_q4",
+           "flash_kv_read_q4", "flash_decode_paged_window", "flash_decode_paged_q4",
+           "library_path", "load_library", "EXPORTED_SYMBOLS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libfa.so")
@@ -34,10 +38,12 @@ _lib = None
 
 FA_FP16, FA_BF16 = 0, 1
 FA_MAX_SPLITS = 1024
+FA_Q4_GROUP = 32
 EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_decode_paged_splitkv", "fa_splitkv_merge",
                     "fa_decode_splitkv_fused", "fa_decode_paged_splitkv_fused", "fa_bwd", "fa_bwd_workspace_bytes",
                     "fa_bwd_varlen", "fa_bwd_varlen_workspace_bytes", "fa_check_device_error", "fa_status_string",
-                    "fa_version", "fa_test_withhold_load")
+                    "fa_version", "fa_test_withhold_load", "fa_kv_write_q4", "fa_kv_read_q4", "fa_decode_splits",
+                    "fa_decode_paged_window", "fa_decode_paged_q4")
 
 
 class FAError(RuntimeError):
@@ -81,12 +87,18 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.fa_bwd_varlen.restype = ctypes.c_int
         lib.fa_bwd_varlen_workspace_bytes.argtypes = [i, i, i]
         lib.fa_bwd_varlen_workspace_bytes.restype = ctypes.c_size_t
+        lib.fa_kv_write_q4.argtypes = [vp] * 9 + [i] * 9 + [vp]
+        lib.fa_kv_read_q4.argtypes = [vp] * 9 + [i] * 9 + [vp]
+        lib.fa_decode_splits.argtypes = [i, i, i, i]
+        lib.fa_decode_paged_window.argtypes = [vp] * 11 + [i] * 10 + [f, i, vp]
+        lib.fa_decode_paged_q4.argtypes = [vp] * 13 + [i] * 10 + [f, i, vp]
         lib.fa_check_device_error.argtypes = [vp]
         lib.fa_status_string.argtypes = [i]
         lib.fa_status_string.restype = ctypes.c_char_p
         lib.fa_version.argtypes = []
         for name in ("fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_splitkv_merge", "fa_decode_splitkv_fused",
-                     "fa_decode_paged_splitkv_fused", "fa_check_device_error", "fa_version"):
+                     "fa_decode_paged_splitkv_fused", "fa_check_device_error", "fa_version", "fa_kv_write_q4",
+                     "fa_kv_read_q4", "fa_decode_splits", "fa_decode_paged_window", "fa_decode_paged_q4"):
             getattr(lib, name).restype = ctypes.c_int
         if path is None:
             _lib = lib
@@ -395,3 +407,196 @@ def fa_decode_noalloc(q, k, v, o, lse, num_splits: int, scale: float | None = No
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     _check("fa_decode_noalloc", fn(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Sk, D, int(num_splits),
                                    float(scale), _dtype_code(k), _stream(stream)))
+
+
+# ------------------------------------- shared key heads, windows, 4-bit cache --
+
+def _expect(name: str, t, shape, dtype):
+    """Refuse a tensor that is not a contiguous one of this shape and dtype (None in ``shape``: any size)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _launch(fn: str, stream, args, first, *others):
+    """Call entry point ``fn`` with ``args`` and the stream, on the device that all the tensors share."""
+    dev = first.device
+    if dev.type != "cuda" or any(t.device != dev for t in others if t is not None):
+        raise ValueError(f"{fn}: all tensors must be on one CUDA device")
+    call = getattr(load_library(), fn)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            st = call(*args, _stream(stream))
+    else:
+        st = call(*args, _stream(stream))
+    _check(fn, st)
+
+
+class KVCacheQ4(NamedTuple):
+    """The paged 4-bit cache of include/fa.h: codes uint8 [num_blocks,Hkv,block_size,D/2] and scales (fp16 or
+    bf16) [num_blocks,Hkv,block_size,D/32] of keys and of values."""
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+
+
+def kv_cache_q4(num_blocks: int, Hkv: int, block_size: int, D: int, dtype=torch.bfloat16, device="cuda") -> KVCacheQ4:
+    """An empty 4-bit cache (all zeros: rows that were never written read as zero)."""
+    rows = (num_blocks, Hkv, block_size)
+    one = lambda: (torch.zeros(*rows, D // 2, dtype=torch.uint8, device=device),  # noqa: E731
+                   torch.zeros(*rows, D // FA_Q4_GROUP, dtype=dtype, device=device))
+    return KVCacheQ4(*one(), *one())
+
+
+def _check_q4(k_codes, k_scales, v_codes, v_scales, Hkv, D, dtype):
+    rows = (k_codes.shape[0], Hkv, k_codes.shape[2]) if k_codes.dim() == 4 else (None, Hkv, None)
+    for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
+        _expect(name, t, rows + (D // 2,), torch.uint8)
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        _expect(name, t, rows + (D // FA_Q4_GROUP,), dtype)
+    return rows[0], rows[2]
+
+
+def _kv_q4(fn, k, v, cache, block_table, cu_seqlens, max_seqlen, starts, stream):
+    if k.dim() != 3:
+        raise ValueError(f"k must be [total,Hkv,D], got {tuple(k.shape)}")
+    total, Hkv, D = k.shape
+    code = _dtype_code(k)
+    _expect("k", k, (total, Hkv, D), k.dtype)
+    _expect("v", v, (total, Hkv, D), k.dtype)
+    num_blocks, block_size = _check_q4(*cache, Hkv, D, k.dtype)
+    n = cu_seqlens.numel() - 1
+    _expect("cu_seqlens", cu_seqlens, (n + 1,), torch.int32)
+    _expect("block_table", block_table, (n, None), torch.int32)
+    if starts is not None:
+        _expect("starts", starts, (n,), torch.int32)
+    args = (_ptr(k), _ptr(v), *map(_ptr, cache), _ptr(block_table), _ptr(cu_seqlens), _ptr(starts), n, total,
+            int(max_seqlen), Hkv, D, num_blocks, block_size, block_table.shape[1], code)
+    _launch(fn, stream, args, k, v, *cache, block_table, cu_seqlens, starts)
+
+
+def fa_kv_write_q4(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, max_seqlen: int, starts=None,
+                   stream=None):
+    """Quantise the new tokens' k, v [total,Hkv,D] and store them at positions starts[b].. (zero when None) of their
+    sequences; cu_seqlens int32 [num_seqs+1], block_table int32 [num_seqs,max_blocks], starts int32 [num_seqs]."""
+    _kv_q4("fa_kv_write_q4", k, v, (k_codes, k_scales, v_codes, v_scales), block_table, cu_seqlens, max_seqlen, starts,
+           stream)
+
+
+def fa_kv_read_q4(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, max_seqlen: int, starts=None,
+                  stream=None):
+    """Read positions starts[b].. of each sequence back into k, v [total,Hkv,D] (arguments as fa_kv_write_q4)."""
+    _kv_q4("fa_kv_read_q4", k, v, (k_codes, k_scales, v_codes, v_scales), block_table, cu_seqlens, max_seqlen, starts,
+           stream)
+
+
+def fa_decode_splits(B: int, H: int, Hkv: int, max_keys: int) -> int:
+    """A num_splits that fills the current GPU (see include/fa.h)."""
+    return int(load_library().fa_decode_splits(B, H, Hkv, max_keys))
+
+
+def _decode_gqa(fn, q, cache, page_shape, block_table, seq_lens, o, lse, o_part, m_part, l_part, counters, num_splits,
+                window, sinks, scale, stream):
+    B, H, _, D = q.shape
+    num_blocks, Hkv, block_size = page_shape
+    S = int(num_splits)
+    code = _dtype_code(q)
+    _expect("q", q, (B, H, 1, D), q.dtype)
+    _expect("block_table", block_table, (B, None), torch.int32)
+    _expect("seq_lens", seq_lens, (B,), torch.int32)
+    _expect("o", o, (B, H, 1, D), q.dtype)
+    _expect("lse", lse, (B, H), torch.float32)
+    for name, t, need in (("o_part", o_part, B * H * S * D), ("m_part", m_part, B * H * S),
+                          ("l_part", l_part, B * H * S)):
+        if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() < need:
+            raise ValueError(f"{name} must be contiguous float32 of at least {need} elements")
+    if counters.dtype != torch.int32 or not counters.is_contiguous() or counters.numel() < B * H:
+        raise ValueError(f"counters must be contiguous int32 of at least {B * H} elements")
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    outs = (o, lse, o_part, m_part, l_part, counters)
+    args = (_ptr(q), *map(_ptr, cache), _ptr(block_table), _ptr(seq_lens), *map(_ptr, outs), B, H, Hkv, D, num_blocks,
+            block_size, block_table.shape[1], S, int(window), int(sinks), float(scale), code)
+    _launch(fn, stream, args, q, *cache, block_table, seq_lens, *outs)
+
+
+def fa_decode_paged_window(q, k_cache, v_cache, block_table, seq_lens, o, lse, o_part, m_part, l_part, counters,
+                           num_splits: int, window: int, sinks: int = 0, scale: float | None = None, stream=None):
+    """One-token attention over a paged cache: q [B,H,1,D]; k_cache, v_cache [num_blocks,Hkv,block_size,D]; the token
+    sees its last ``window`` keys (0: all) and the first ``sinks``. o_part [B,H,num_splits,D], m_part and l_part
+    [B,H,num_splits] fp32 and counters int32 [B*H] (zero between calls) may be larger than that."""
+    if q.dim() != 4 or k_cache.dim() != 4:
+        raise ValueError("q must be [B,H,1,D] and the caches [num_blocks,Hkv,block_size,D]")
+    num_blocks, Hkv, block_size, _ = k_cache.shape
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _expect(name, t, (num_blocks, Hkv, block_size, q.shape[3]), q.dtype)
+    _decode_gqa("fa_decode_paged_window", q, (k_cache, v_cache), (num_blocks, Hkv, block_size), block_table, seq_lens,
+                o, lse, o_part, m_part, l_part, counters, num_splits, window, sinks, scale, stream)
+
+
+def fa_decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, o, lse, o_part, m_part, l_part,
+                       counters, num_splits: int, window: int = 0, sinks: int = 0, scale: float | None = None,
+                       stream=None):
+    """fa_decode_paged_window over the 4-bit cache (scales in the dtype of q)."""
+    if q.dim() != 4 or k_codes.dim() != 4:
+        raise ValueError("q must be [B,H,1,D] and the codes [num_blocks,Hkv,block_size,D/2]")
+    Hkv = k_codes.shape[1]
+    num_blocks, block_size = _check_q4(k_codes, k_scales, v_codes, v_scales, Hkv, q.shape[3], q.dtype)
+    _decode_gqa("fa_decode_paged_q4", q, (k_codes, k_scales, v_codes, v_scales), (num_blocks, Hkv, block_size),
+                block_table, seq_lens, o, lse, o_part, m_part, l_part, counters, num_splits, window, sinks, scale,
+                stream)
+
+
+def flash_kv_write_q4(k, v, cache: KVCacheQ4, block_table, cu_seqlens, max_seqlen: int, starts=None, stream=None):
+    """fa_kv_write_q4 into the four tensors of ``cache``."""
+    fa_kv_write_q4(k, v, *cache, block_table, cu_seqlens, max_seqlen, starts, stream)
+
+
+def flash_kv_read_q4(cache: KVCacheQ4, block_table, cu_seqlens, total: int, max_seqlen: int, starts=None, stream=None):
+    """Returns (k, v) [total,Hkv,D] with positions starts[b].. of each sequence, packed by cu_seqlens. Rows that belong
+    to no sequence are not initialised."""
+    codes, scales = cache[0], cache[1]
+    k = torch.empty(int(total), codes.shape[1], 2 * codes.shape[3], dtype=scales.dtype, device=codes.device)
+    v = torch.empty_like(k)
+    fa_kv_read_q4(k, v, *cache, block_table, cu_seqlens, max_seqlen, starts, stream)
+    return k, v
+
+
+def _flash_decode_gqa(fn, q, cache, block_table, seq_lens, window, sinks, num_splits, scale, stream, workspace):
+    if q.dim() != 4 or cache[0].dim() != 4 or block_table.dim() != 2:
+        raise ValueError("q must be [B,H,1,D], pages 4-dimensional and block_table [B,max_blocks]")
+    B, H, _, D = q.shape
+    if num_splits is None:
+        keys = block_table.shape[1] * cache[0].shape[2]
+        if window > 0:
+            keys = min(keys, window + sinks)
+        num_splits = fa_decode_splits(B, H, cache[0].shape[1], keys)
+        if workspace is not None:
+            num_splits = min(num_splits, workspace[1].numel() // (B * H))
+    if workspace is None:
+        workspace = _decode_workspace(B, H, num_splits, D, q.device, True)
+    o = torch.empty(B, H, 1, D, dtype=q.dtype, device=q.device)
+    lse = torch.empty(B, H, dtype=torch.float32, device=q.device)
+    fn(q, *cache, block_table, seq_lens, o, lse, *workspace, num_splits, window, sinks, scale, stream)
+    return o, lse
+
+
+def flash_decode_paged_window(q, k_cache, v_cache, block_table, seq_lens, window: int, sinks: int = 0,
+                              num_splits: int | None = None, scale: float | None = None, stream=None, workspace=None):
+    """One-token attention over a paged cache with shared key heads, a sliding window (0: none) and sinks. Returns
+    (o [B,H,1,D], lse [B,H]). ``workspace`` may pass (o_part, m_part, l_part, counters), counters zero; num_splits
+    None takes fa_decode_splits, within the workspace."""
+    return _flash_decode_gqa(fa_decode_paged_window, q, (k_cache, v_cache), block_table, seq_lens, window, sinks,
+                             num_splits, scale, stream, workspace)
+
+
+def flash_decode_paged_q4(q, cache: KVCacheQ4, block_table, seq_lens, window: int = 0, sinks: int = 0,
+                          num_splits: int | None = None, scale: float | None = None, stream=None, workspace=None):
+    """flash_decode_paged_window over the 4-bit cache."""
+    return _flash_decode_gqa(fa_decode_paged_q4, q, tuple(cache), block_table, seq_lens, window, sinks, num_splits,
+                             scale, stream, workspace)

@@ -131,6 +131,18 @@ long long fwd_work_items(int D, long long heads, int Sq) {
 }
 constexpr int kMaxLen = 1 << 30;
 
+// Page geometry of a paged cache: block_size a power of two up to 1024, and
+// positions and (page, head) indices within 32 bits.
+bool pages_ok(int Hkv, int num_blocks, int block_size, int max_blocks, int &log2_bs) {
+    if (num_blocks < 1 || max_blocks < 1) return false;
+    if (block_size < 1 || block_size > 1024 || (block_size & (block_size - 1)) != 0) return false;
+    if (static_cast<long long>(max_blocks) * block_size > kMaxLen) return false;
+    if (static_cast<long long>(num_blocks) * Hkv > INT_MAX) return false;
+    log2_bs = 0;
+    while ((1 << log2_bs) < block_size) ++log2_bs;
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -572,6 +584,142 @@ fa_status_t fa_splitkv_merge(const float *o_part, const float *m_part, const flo
                                                    static_cast<int>(BH), num_splits,
                                                    static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+static fa_status_t kv_q4(bool write, const void *k, const void *v, const void *k_codes, const void *k_scales,
+                         const void *v_codes, const void *v_scales, const int32_t *block_table,
+                         const int32_t *cu_seqlens, const int32_t *starts, int num_seqs, int total, int max_seqlen,
+                         int Hkv, int D, int num_blocks, int block_size, int max_blocks_per_seq, fa_dtype_t dtype,
+                         void *stream) {
+    if (!k_codes || !k_scales || !v_codes || !v_scales || !block_table || !cu_seqlens) return FA_ERR_NULL;
+    if ((!k || !v) && total != 0) return FA_ERR_NULL;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_DTYPE;
+    if (D != 64 && D != 128) return FA_ERR_HEADDIM;
+    if (num_seqs < 1 || total < 0 || total > kMaxLen || max_seqlen < 1 || max_seqlen > kMaxLen || Hkv < 1)
+        return FA_ERR_SHAPE;
+    int log2_bs = 0;
+    if (!pages_ok(Hkv, num_blocks, block_size, max_blocks_per_seq, log2_bs)) return FA_ERR_SHAPE;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_codes) || !aligned16(k_scales) || !aligned16(v_codes) ||
+        !aligned16(v_scales) || !aligned4(block_table) || !aligned4(cu_seqlens) || !aligned4(starts))
+        return FA_ERR_ALIGN;
+    fa::KvQ4Params p{};
+    p.k = const_cast<void *>(k);
+    p.v = const_cast<void *>(v);
+    p.k_codes = const_cast<void *>(k_codes);
+    p.k_scales = const_cast<void *>(k_scales);
+    p.v_codes = const_cast<void *>(v_codes);
+    p.v_scales = const_cast<void *>(v_scales);
+    p.block_table = block_table;
+    p.cu_seqlens = cu_seqlens;
+    p.starts = starts;
+    p.total = total;
+    p.max_seqlen = max_seqlen;
+    p.Hkv = Hkv;
+    p.num_blocks = num_blocks;
+    p.log2_bs = log2_bs;
+    p.max_blocks = max_blocks_per_seq;
+    const long long grid = fa::kv_q4_grid(D, num_seqs, p);
+    if (grid > INT_MAX) return FA_ERR_SHAPE;
+    if (total == 0) return FA_OK;
+    p.err = device_error_word();
+    if (p.err == nullptr) return FA_ERR_CUDA;
+    const cudaError_t e = fa::launch_kv_q4(D, dtype == FA_BF16, write, p, static_cast<int>(grid),
+                                           static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status_t fa_kv_write_q4(const void *k, const void *v, void *k_codes, void *k_scales, void *v_codes, void *v_scales,
+                           const int32_t *block_table, const int32_t *cu_seqlens, const int32_t *starts, int num_seqs,
+                           int total, int max_seqlen, int Hkv, int D, int num_blocks, int block_size,
+                           int max_blocks_per_seq, fa_dtype_t dtype, void *stream) {
+    return kv_q4(true, k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, starts, num_seqs, total,
+                 max_seqlen, Hkv, D, num_blocks, block_size, max_blocks_per_seq, dtype, stream);
+}
+
+fa_status_t fa_kv_read_q4(void *k, void *v, const void *k_codes, const void *k_scales, const void *v_codes,
+                          const void *v_scales, const int32_t *block_table, const int32_t *cu_seqlens,
+                          const int32_t *starts, int num_seqs, int total, int max_seqlen, int Hkv, int D,
+                          int num_blocks, int block_size, int max_blocks_per_seq, fa_dtype_t dtype, void *stream) {
+    return kv_q4(false, k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, starts, num_seqs, total,
+                 max_seqlen, Hkv, D, num_blocks, block_size, max_blocks_per_seq, dtype, stream);
+}
+
+int fa_decode_splits(int B, int H, int Hkv, int max_keys) {
+    if (B < 1 || H < 1 || Hkv < 1 || max_keys < 1) return 1;
+    const int sms = num_sms();
+    return fa::decode_gqa_splits(sms > 0 ? sms : 152, B, H, Hkv, max_keys);
+}
+
+static fa_status_t decode_gqa(bool q4, const void *q, const void *k, const void *ks, const void *v, const void *vs,
+                              const int32_t *block_table, const int32_t *seq_lens, void *o, float *lse,
+                              float *o_part, float *m_part, float *l_part, int32_t *counters, int B, int H, int Hkv,
+                              int D, int num_blocks, int block_size, int max_blocks_per_seq, int num_splits,
+                              int window, int sinks, float scale, fa_dtype_t dtype, void *stream) {
+    if (!q || !k || !v || (q4 && (!ks || !vs)) || !block_table || !seq_lens || !o || !lse || !o_part || !m_part ||
+        !l_part || !counters)
+        return FA_ERR_NULL;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_DTYPE;
+    if (D != 64 && D != 128) return FA_ERR_HEADDIM;
+    if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || window < 0 || sinks < 0) return FA_ERR_SHAPE;
+    int log2_bs = 0;
+    if (!pages_ok(Hkv, num_blocks, block_size, max_blocks_per_seq, log2_bs)) return FA_ERR_SHAPE;
+    if (num_splits < 1 || num_splits > FA_MAX_SPLITS) return FA_ERR_SPLITS;
+    if (static_cast<long long>(B) * H * num_splits > INT_MAX) return FA_ERR_SHAPE;
+    if (!scale_ok(scale)) return FA_ERR_SCALE;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(ks) || !aligned16(vs) ||
+        !aligned4(block_table) || !aligned4(seq_lens) || !aligned16(o) || !aligned4(lse) || !aligned16(o_part) ||
+        !aligned4(m_part) || !aligned4(l_part) || !aligned4(counters))
+        return FA_ERR_ALIGN;
+    fa::GqaDecodeParams p{};
+    p.q = static_cast<const uint16_t *>(q);
+    p.k = k;
+    p.v = v;
+    p.ks = ks;
+    p.vs = vs;
+    p.o_part = o_part;
+    p.m_part = m_part;
+    p.l_part = l_part;
+    p.o = o;
+    p.lse = lse;
+    p.counters = counters;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.group = H / Hkv;
+    p.num_splits = num_splits;
+    p.window = window;
+    p.sinks = sinks;
+    p.max_blocks = max_blocks_per_seq;
+    p.log2_bs = log2_bs;
+    p.num_blocks = num_blocks;
+    p.scale_log2 = scale * kLog2e;
+    p.err = device_error_word();
+    if (p.err == nullptr) return FA_ERR_CUDA;
+    const cudaError_t e = fa::launch_decode_gqa(D, dtype == FA_BF16, q4, p, B * Hkv * num_splits,
+                                                static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status_t fa_decode_paged_window(const void *q, const void *k_cache, const void *v_cache,
+                                   const int32_t *block_table, const int32_t *seq_lens, void *o, float *lse,
+                                   float *o_part, float *m_part, float *l_part, int32_t *counters, int B, int H,
+                                   int Hkv, int D, int num_blocks, int block_size, int max_blocks_per_seq,
+                                   int num_splits, int window, int sinks, float scale, fa_dtype_t dtype,
+                                   void *stream) {
+    return decode_gqa(false, q, k_cache, nullptr, v_cache, nullptr, block_table, seq_lens, o, lse, o_part, m_part,
+                      l_part, counters, B, H, Hkv, D, num_blocks, block_size, max_blocks_per_seq, num_splits, window,
+                      sinks, scale, dtype, stream);
+}
+
+fa_status_t fa_decode_paged_q4(const void *q, const void *k_codes, const void *k_scales, const void *v_codes,
+                               const void *v_scales, const int32_t *block_table, const int32_t *seq_lens, void *o,
+                               float *lse, float *o_part, float *m_part, float *l_part, int32_t *counters, int B,
+                               int H, int Hkv, int D, int num_blocks, int block_size, int max_blocks_per_seq,
+                               int num_splits, int window, int sinks, float scale, fa_dtype_t dtype, void *stream) {
+    return decode_gqa(true, q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, o, lse, o_part, m_part,
+                      l_part, counters, B, H, Hkv, D, num_blocks, block_size, max_blocks_per_seq, num_splits, window,
+                      sinks, scale, dtype, stream);
 }
 
 fa_status_t fa_test_withhold_load(int load, unsigned long long wait_limit_ns) {

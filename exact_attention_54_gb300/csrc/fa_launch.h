@@ -149,4 +149,45 @@ cudaError_t launch_splitkv_merge(int D, bool bf16, const float *o_part, const fl
                                  const float *l_part, void *o, float *lse, int BH,
                                  int num_splits, cudaStream_t stream);
 
+// Parameters of the 4-bit cache's write and read kernels.
+struct KvQ4Params {
+    void *k, *v;                // packed rows [total, Hkv, D] (write: input, read: output)
+    void *k_codes, *k_scales;   // pages [num_blocks, Hkv, block_size, D/2 and D/32]
+    void *v_codes, *v_scales;
+    const int *block_table;     // [num_seqs, max_blocks]
+    const int *cu_seqlens;      // [num_seqs + 1]
+    const int *starts;          // [num_seqs] or nullptr
+    int total, max_seqlen, Hkv;
+    int num_blocks, log2_bs, max_blocks;
+    int tokens, chunks;         // tokens per CTA, CTAs per sequence (set by kv_q4_grid)
+    int *err;                   // device error word
+};
+
+// CTAs of the write or read launch (sets p.tokens and p.chunks).
+long long kv_q4_grid(int D, int num_seqs, KvQ4Params &p);
+cudaError_t launch_kv_q4(int D, bool bf16, bool write, const KvQ4Params &p, int grid, cudaStream_t stream);
+
+// Parameters of the paged decode kernels with shared key heads.
+struct GqaDecodeParams {
+    const uint16_t *q;          // [B, H, D]
+    const void *k, *v;          // pages: 16-bit rows, or code rows (4-bit)
+    const void *ks, *vs;        // 4-bit: scale rows
+    float *o_part, *m_part, *l_part;  // [B, H, num_splits(, D)]
+    void *o;                    // [B, H, D]
+    float *lse;                 // [B, H]
+    int *counters;              // [B * H], the first B * Hkv are used: zero between calls
+    const int *block_table;     // [B, max_blocks]
+    const int *seq_lens;        // [B]
+    int H, Hkv, group;          // query heads, key heads, H / Hkv
+    int num_splits;
+    int window, sinks;          // window 0: every key is visible
+    int max_blocks, log2_bs, num_blocks;
+    float scale_log2;
+    int *err;                   // device error word
+};
+
+cudaError_t launch_decode_gqa(int D, bool bf16, bool q4, const GqaDecodeParams &p, int grid, cudaStream_t stream);
+// Partitions that fill `sms` SMs (fa_decode_splits).
+int decode_gqa_splits(int sms, int B, int H, int Hkv, int max_keys);
+
 }  // namespace fa

@@ -9,6 +9,11 @@
  *   fa_decode_splitkv_fused, fa_decode_paged_splitkv_fused
  *                      both phases in one launch (last partition merges).
  *   fa_bwd             backward pass: dQ, dK, dV from dO and the forward LSE.
+ *   fa_kv_write_q4, fa_kv_read_q4
+ *                      keys and values into a paged 4-bit cache, and back.
+ *   fa_decode_paged_window, fa_decode_paged_q4
+ *                      one-token attention over a paged 16-bit or 4-bit cache
+ *                      with shared key heads, a sliding window and sinks.
  *
  * Common rules
  *   - Every tensor pointer is a DEVICE pointer owned by the caller. The library
@@ -326,6 +331,137 @@ FA_API fa_status_t fa_bwd_varlen(const void *q, const void *k, const void *v, co
                                  const int32_t *cu_seqlens_k, int num_seqs, int total_q, int total_k,
                                  int max_seqlen_q, int max_seqlen_k, int H, int D, int causal, float scale,
                                  fa_dtype_t dtype, void *stream);
+
+/*
+ * The paged 4-bit cache of keys and values (fa_kv_write_q4, fa_kv_read_q4,
+ * fa_decode_paged_q4). Keys and values are held alike, each as two arrays:
+ *
+ *   codes   uint8   [num_blocks, Hkv, block_size, D / 2]
+ *   scales  fp16/bf16 [num_blocks, Hkv, block_size, D / FA_Q4_GROUP]
+ *
+ * FA_Q4_GROUP = 32 consecutive columns of a row share a scale
+ *   s = max|x| / 7, rounded to the 16-bit type (nearest, ties to even), and
+ *   n = x / s rounded to the nearest integer (ties to even), within [-7, 7];
+ * a group whose s rounds to zero has n = 0. The cache stands for s * n. A
+ * group that holds an infinity or a NaN gets s = NaN and stands for NaNs.
+ * Column d = 32 w + 4 g + i (g < 8, i < 4) of a row is held as n + 8 in nibble
+ * i % 2 (0: bits 0-3) of byte g * (D / 16) + 2 w + i / 2 of the row.
+ */
+#define FA_Q4_GROUP 32
+
+/*
+ * fa_kv_write_q4 - quantise new keys and values and store them in the cache.
+ *
+ *   k, v         [total,Hkv,D] fp16/bf16, the new tokens of all sequences,
+ *                packed; D is 64 or 128
+ *   k_codes, k_scales, v_codes, v_scales   the cache (see above), scales in
+ *                the dtype of k and v; only the rows of the new tokens change
+ *   block_table  device int32 [num_seqs, max_blocks_per_seq]: page of each
+ *                logical block of a sequence
+ *   cu_seqlens   device int32 [num_seqs + 1], 0 <= cu[0] <= cu[1] <= ... <=
+ *                total: sequence b's new tokens are rows [cu[b], cu[b+1])
+ *   starts       device int32 [num_seqs]: position in its sequence of the
+ *                first new token of each sequence (>= 0), or NULL: all zero
+ *   max_seqlen   >= every number of new tokens (sizes the launch)
+ *   block_size   a power of two, 1..1024
+ * Position p of sequence b is row p % block_size of page
+ * block_table[b][p / block_size]. Two tokens of one call must not fall on the
+ * same row of the same page (each group of such a row ends up as either's).
+ * A sequence whose offsets do not fit [0, total] and max_seqlen, or whose
+ * start is negative, is skipped and the next fa_check_device_error returns
+ * FA_ERR_DEVICE_SEQLENS; a position past max_blocks_per_seq * block_size or a
+ * page number outside [0, num_blocks) is skipped and reported as
+ * FA_ERR_DEVICE_INDEX. total = 0 is allowed and does nothing.
+ * Errors: FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_HEADDIM, FA_ERR_DTYPE,
+ * FA_ERR_ALIGN, FA_ERR_CUDA.
+ */
+FA_API fa_status_t fa_kv_write_q4(const void *k, const void *v, void *k_codes, void *k_scales, void *v_codes,
+                                  void *v_scales, const int32_t *block_table, const int32_t *cu_seqlens,
+                                  const int32_t *starts, int num_seqs, int total, int max_seqlen, int Hkv, int D,
+                                  int num_blocks, int block_size, int max_blocks_per_seq, fa_dtype_t dtype,
+                                  void *stream);
+
+/*
+ * fa_kv_read_q4 - read stretches of the cache back as 16-bit keys and values
+ * (s * n rounded to the 16-bit type), packed as fa_fwd_varlen and
+ * fa_fwd_window_varlen take them.
+ *
+ *   k, v         [total,Hkv,D] outputs, dtype of the scales; rows outside
+ *                every sequence, and rows that are skipped, are left as they
+ *                were
+ *   all other arguments as fa_kv_write_q4: row cu[b] + i receives position
+ *   starts[b] + i of sequence b.
+ * Offsets, positions and page numbers are checked on the device as by
+ * fa_kv_write_q4.
+ * Errors: as fa_kv_write_q4.
+ */
+FA_API fa_status_t fa_kv_read_q4(void *k, void *v, const void *k_codes, const void *k_scales, const void *v_codes,
+                                 const void *v_scales, const int32_t *block_table, const int32_t *cu_seqlens,
+                                 const int32_t *starts, int num_seqs, int total, int max_seqlen, int Hkv, int D,
+                                 int num_blocks, int block_size, int max_blocks_per_seq, fa_dtype_t dtype,
+                                 void *stream);
+
+/*
+ * fa_decode_splits - a number of partitions for fa_decode_paged_window and
+ * fa_decode_paged_q4 that fills the current GPU: for a batch of B sequences,
+ * Hkv key heads and at most max_keys visible keys a sequence (window + sinks,
+ * or the longest sequence). At least 1, at most FA_MAX_SPLITS; 1 where the
+ * arguments are not positive.
+ */
+FA_API int fa_decode_splits(int B, int H, int Hkv, int max_keys);
+
+/*
+ * fa_decode_paged_window - attention of one new token per sequence over a
+ * paged cache, with shared key heads, a sliding window and sinks, in one
+ * launch: split-KV decoding as fa_decode_paged_splitkv_fused does it, over the
+ * keys that the token sees.
+ *
+ * The query is at position L - 1 of a sequence of L = seq_lens[b] keys (its
+ * own key is in the cache) and sees key j if L - 1 - j < window, or window is
+ * 0 (all keys), or j < sinks.
+ *
+ *   q            [B,H,1,D] fp16/bf16; query head h reads key head
+ *                h / (H / Hkv); Hkv divides H; D is 64 or 128
+ *   k_cache, v_cache [num_blocks,Hkv,block_size,D], same dtype
+ *   block_table  device int32 [B, max_blocks_per_seq]; entries whose keys are
+ *                not visible are never read
+ *   seq_lens     device int32 [B] (clamped to [0, max_blocks_per_seq *
+ *                block_size]); a length of 0 gives o = 0 and lse = -inf
+ *   o [B,H,1,D] (dtype), lse [B,H] fp32: outputs
+ *   o_part       [B,H,num_splits,D], m_part and l_part [B,H,num_splits] fp32:
+ *                workspace (the visible keys of a sequence are cut into up to
+ *                num_splits partitions); contents on entry and exit mean
+ *                nothing
+ *   counters     device int32 [B*H]: all zero before the first call, left all
+ *                zero by every completed call
+ *   window >= 0, sinks >= 0; block_size a power of two, 1..1024
+ * Rows of a page that the token does not see may hold anything, NaNs
+ * included. Page numbers outside [0, num_blocks) are not dereferenced: their
+ * keys are skipped and fa_check_device_error returns FA_ERR_DEVICE_INDEX.
+ * Calls that share counters or partial buffers must not overlap on the GPU.
+ * Errors: FA_ERR_NULL, FA_ERR_SHAPE (Hkv does not divide H; window or sinks
+ * negative; sizes), FA_ERR_HEADDIM, FA_ERR_DTYPE, FA_ERR_ALIGN (o_part too is
+ * 16-byte aligned), FA_ERR_SPLITS, FA_ERR_SCALE, FA_ERR_CUDA.
+ */
+FA_API fa_status_t fa_decode_paged_window(const void *q, const void *k_cache, const void *v_cache,
+                                          const int32_t *block_table, const int32_t *seq_lens, void *o, float *lse,
+                                          float *o_part, float *m_part, float *l_part, int32_t *counters, int B,
+                                          int H, int Hkv, int D, int num_blocks, int block_size,
+                                          int max_blocks_per_seq, int num_splits, int window, int sinks,
+                                          float scale, fa_dtype_t dtype, void *stream);
+
+/*
+ * fa_decode_paged_q4 - fa_decode_paged_window over the 4-bit cache: the keys
+ * and values are s * n, not rounded to 16 bits. Scales have the dtype of q.
+ * Arguments, rules and errors as fa_decode_paged_window, with the cache of
+ * fa_kv_write_q4 in place of k_cache and v_cache.
+ */
+FA_API fa_status_t fa_decode_paged_q4(const void *q, const void *k_codes, const void *k_scales, const void *v_codes,
+                                      const void *v_scales, const int32_t *block_table, const int32_t *seq_lens,
+                                      void *o, float *lse, float *o_part, float *m_part, float *l_part,
+                                      int32_t *counters, int B, int H, int Hkv, int D, int num_blocks,
+                                      int block_size, int max_blocks_per_seq, int num_splits, int window, int sinks,
+                                      float scale, fa_dtype_t dtype, void *stream);
 
 /*
  * fa_check_device_error - synchronise `stream`, then read and clear the

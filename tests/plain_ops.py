@@ -1,0 +1,118 @@
+"""Plain 64-bit statements of the window and 4-bit-cache operators (CPU, torch
+double, one definition per function, no tiling), and the error bounds that the
+tests of their kernels use."""
+from __future__ import annotations
+
+import math
+
+import torch
+
+GROUP = 32
+
+
+def half_step(dtype) -> float:
+    """Largest relative error of one rounding to ``dtype``."""
+    return torch.finfo(dtype).eps / 2
+
+
+# ------------------------------------------------------------ 4-bit cache --
+
+def q4_quantise(x):
+    """Rows [..., D] of a 16-bit type -> integers n (int64) [..., D] and scales [..., D/32] (the type of x)."""
+    g = x.double().unflatten(-1, (-1, GROUP))
+    amax = g.abs().amax(-1)
+    fine = torch.isfinite(g).all(-1)
+    s = (torch.where(fine, amax, torch.zeros_like(amax)) / 7).to(x.dtype)
+    sd = s.double().unsqueeze(-1)
+    n = torch.where((sd > 0) & fine.unsqueeze(-1), torch.round(g / torch.where(sd > 0, sd, torch.ones_like(sd))),
+                    torch.zeros_like(g))
+    s = torch.where(fine, s, torch.full_like(s, math.nan))
+    return n.clamp(-7, 7).to(torch.int64).flatten(-2), s
+
+
+def q4_pack(n):
+    """Integers n [..., D] -> code bytes [..., D/2]: column d = 32 w + 4 g + i in nibble i % 2 of byte
+    g (D/16) + 2 w + i // 2."""
+    D = n.shape[-1]
+    out = torch.zeros(n.shape[:-1] + (D // 2,), dtype=torch.int64)
+    for d in range(D):
+        w, g, i = d // 32, d % 32 // 4, d % 4
+        out[..., g * (D // 16) + 2 * w + i // 2] |= (n[..., d] + 8) << (4 * (i % 2))
+    return out.to(torch.uint8)
+
+
+def q4_unpack(codes):
+    """Code bytes [..., D/2] -> integers n [..., D]."""
+    D = codes.shape[-1] * 2
+    c = codes.to(torch.int64)
+    cols = []
+    for d in range(D):
+        w, g, i = d // 32, d % 32 // 4, d % 4
+        cols.append(((c[..., g * (D // 16) + 2 * w + i // 2] >> (4 * (i % 2))) & 15) - 8)
+    return torch.stack(cols, -1)
+
+
+def q4_values(codes, scales):
+    """What rows of the cache stand for: s * n (double)."""
+    return q4_unpack(codes).double() * scales.double().repeat_interleave(GROUP, -1)
+
+
+# -------------------------------------------------------------- attention --
+
+def visible(nq, nk, window, sinks):
+    """[nq, nk] truth values: key j <= query i, and i - j < window (0: no window) or j < sinks."""
+    i, j = torch.arange(nq)[:, None], torch.arange(nk)[None, :]
+    near = (i - j < window) if window > 0 else torch.ones(nq, nk, dtype=torch.bool)
+    return (j <= i) & (near | (j < sinks))
+
+
+def softmax_attention(q, k, v, seen, scale):
+    """One head in double: q [nq,D], k and v [nk,D], seen [nq,nk] -> o, lse, p, and the size of what meets in o
+    (sum_j p_j |v_j|). Rows that see nothing: o = 0, lse = -inf."""
+    s = (q @ k.t() * scale).masked_fill(~seen, -math.inf)
+    lse = torch.logsumexp(s, -1) if k.shape[0] else torch.full(q.shape[:1], -math.inf, dtype=torch.float64)
+    p = torch.exp(s - lse.masked_fill(torch.isinf(lse), 0.0)[:, None])
+    return p @ v, lse, p, p @ v.abs()
+
+
+def decode(q, values, table, lens, block, window, sinks, scale):
+    """q [B,H,1,D]; values(page, head) -> (k, v) double [block, D] of one page; the definition of the paged decode.
+    Returns o [B,H,D], lse [B,H] and sum p|v| [B,H,D]."""
+    B, H, _, D = q.shape
+    o, size = torch.zeros(B, H, D, dtype=torch.float64), torch.zeros(B, H, D, dtype=torch.float64)
+    lse = torch.full((B, H), -math.inf, dtype=torch.float64)
+    for b in range(B):
+        n = int(lens[b])
+        if n == 0:
+            continue
+        seen = visible(n, n, window, sinks)[n - 1]
+        keys = torch.nonzero(seen).flatten()
+        for h in range(H):
+            pages = {int(x): values(int(table[b, x]), h) for x in torch.unique(keys // block)}
+            k = torch.stack([pages[int(j) // block][0][int(j) % block] for j in keys])
+            v = torch.stack([pages[int(j) // block][1][int(j) % block] for j in keys])
+            r = softmax_attention(q[b, h].double(), k, v, torch.ones(1, len(keys), dtype=torch.bool), scale)
+            o[b, h], lse[b, h], size[b, h] = r[0][0], r[1][0], r[3][0]
+    return o, lse, size
+
+
+def assert_attention_close(o, lse, ro, rl, size, dtype, what=""):
+    """O within half a step of its own rounding, half a step of the 16-bit type on each weight, and 2^-13 of
+    what meets in the sum for the rest; LSE within 4e-5 + 2^-21 |LSE|.
+
+    The rest: a score is an fp32 sum of D products, |error| <= 2^-24 * 16 * sum |q k| scale (16: depth of the
+    sums), under 2^-24 * 16 * 40 = 2^-14.7 for the inputs here; it enters a weight as a relative error, once in
+    the numerator and once in the sum; 2^x and the fp32 sums add a few 2^-22. LSE carries the score's error and
+    the rounding of its own value (fp32, two operations)."""
+    o, lse = o.double().cpu().reshape(ro.shape), lse.double().cpu().reshape(rl.shape)
+    assert torch.equal(torch.isnan(o), torch.isnan(ro)) and torch.equal(torch.isnan(lse), torch.isnan(rl)), what
+    h = half_step(dtype)
+    tiny = torch.finfo(dtype).smallest_normal * h * 2
+    bound = h * ro.abs() * (1 + 2 * h) + (h * (1 + h) + 2.0 ** -13) * size + tiny
+    bad = ((o - ro).abs() > bound) & ~torch.isnan(ro)
+    assert not bad.any(), (what, "o", float(((o - ro).abs() / bound).nan_to_num().max()), torch.nonzero(bad)[0].tolist())
+    empty = torch.isinf(rl)
+    assert torch.equal(empty, torch.isinf(lse)) and torch.equal(lse[empty], rl[empty]), what
+    off = (lse - rl).abs()[~empty & ~torch.isnan(rl)]
+    room = (4e-5 + 2.0 ** -21 * rl.abs())[~empty & ~torch.isnan(rl)]
+    assert (off <= room).all(), (what, "lse", float(off.max()))
