@@ -26,6 +26,9 @@ __all__ = ["FAError", "fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_decode
            "fa_bwd_varlen", "fa_bwd_varlen_workspace_bytes", "fa_check_device_error", "fa_status_string",
            "fa_test_withhold_load",
            "flash_attention", "flash_attention_varlen", "flash_attention_bwd", "flash_attention_varlen_bwd",
+           "fa_fwd_window", "fa_fwd_window_varlen", "fa_bwd_window", "fa_bwd_window_varlen",
+           "flash_attention_window", "flash_attention_window_bwd", "flash_attention_window_varlen",
+           "flash_attention_window_varlen_bwd",
            "flash_decode", "flash_decode_paged", "fa_kv_write_q4", "fa_kv_read_q4", "fa_decode_paged_window",
            "fa_decode_paged_q4", "fa_decode_splits", "KVCacheQ4", "kv_cache_q4", "flash_kv_write_q4",
            "flash_kv_read_q4", "flash_decode_paged_window", "flash_decode_paged_q4",
@@ -43,6 +46,7 @@ EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_decode_p
                     "fa_decode_splitkv_fused", "fa_decode_paged_splitkv_fused", "fa_bwd", "fa_bwd_workspace_bytes",
                     "fa_bwd_varlen", "fa_bwd_varlen_workspace_bytes", "fa_check_device_error", "fa_status_string",
                     "fa_version", "fa_test_withhold_load", "fa_kv_write_q4", "fa_kv_read_q4", "fa_decode_splits",
+                    "fa_fwd_window", "fa_fwd_window_varlen", "fa_bwd_window", "fa_bwd_window_varlen",
                     "fa_decode_paged_window", "fa_decode_paged_q4")
 
 
@@ -87,6 +91,11 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.fa_bwd_varlen.restype = ctypes.c_int
         lib.fa_bwd_varlen_workspace_bytes.argtypes = [i, i, i]
         lib.fa_bwd_varlen_workspace_bytes.restype = ctypes.c_size_t
+        sz = ctypes.c_size_t
+        lib.fa_fwd_window.argtypes = [vp] * 5 + [i] * 8 + [f, i, vp]
+        lib.fa_fwd_window_varlen.argtypes = [vp] * 7 + [i] * 9 + [f, i, vp]
+        lib.fa_bwd_window.argtypes = [vp] * 10 + [sz] + [i] * 8 + [f, i, vp]
+        lib.fa_bwd_window_varlen.argtypes = [vp] * 10 + [sz, vp, vp] + [i] * 10 + [f, i, vp]
         lib.fa_kv_write_q4.argtypes = [vp] * 9 + [i] * 9 + [vp]
         lib.fa_kv_read_q4.argtypes = [vp] * 9 + [i] * 9 + [vp]
         lib.fa_decode_splits.argtypes = [i, i, i, i]
@@ -98,6 +107,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.fa_version.argtypes = []
         for name in ("fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_splitkv_merge", "fa_decode_splitkv_fused",
                      "fa_decode_paged_splitkv_fused", "fa_check_device_error", "fa_version", "fa_kv_write_q4",
+                     "fa_fwd_window", "fa_fwd_window_varlen", "fa_bwd_window", "fa_bwd_window_varlen",
                      "fa_kv_read_q4", "fa_decode_splits", "fa_decode_paged_window", "fa_decode_paged_q4"):
             getattr(lib, name).restype = ctypes.c_int
         if path is None:
@@ -435,6 +445,130 @@ def _launch(fn: str, stream, args, first, *others):
     else:
         st = call(*args, _stream(stream))
     _check(fn, st)
+
+
+def fa_fwd_window(q, k, v, o, lse, window: int, sinks: int = 0, scale: float | None = None, stream=None):
+    """Causal attention with a sliding window and sinks: q, o [B,H,Sq,D]; k, v [B,Hkv,Sk,D]; lse [B,H,Sq] fp32."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B,H,Sq,D] and k, v [B,Hkv,Sk,D]")
+    B, H, Sq, D = q.shape
+    _, Hkv, Sk, _ = k.shape
+    code = _dtype_code(q)
+    for name, t, shape in (("q", q, (B, H, Sq, D)), ("k", k, (B, Hkv, Sk, D)), ("v", v, (B, Hkv, Sk, D)),
+                           ("o", o, (B, H, Sq, D))):
+        _expect(name, t, shape, q.dtype)
+    _expect("lse", lse, (B, H, Sq), torch.float32)
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    ts = (q, k, v, o, lse)
+    _launch("fa_fwd_window", stream, (*map(_ptr, ts), B, H, Hkv, Sq, Sk, D, int(window), int(sinks), float(scale),
+                                      code), *ts)
+
+
+def fa_fwd_window_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, window: int, sinks: int = 0,
+                         scale: float | None = None, stream=None):
+    """fa_fwd_window over packed sequences: q, o [total_q,H,D]; k, v [total_k,Hkv,D]; lse [H,total_q]."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [total_q,H,D] and k, v [total_k,Hkv,D]")
+    Tq, H, D = q.shape
+    Tk, Hkv, _ = k.shape
+    n = cu_seqlens_q.numel() - 1
+    code = _dtype_code(q)
+    for name, t, shape in (("q", q, (Tq, H, D)), ("k", k, (Tk, Hkv, D)), ("v", v, (Tk, Hkv, D)), ("o", o, (Tq, H, D))):
+        _expect(name, t, shape, q.dtype)
+    _expect("lse", lse, (H, Tq), torch.float32)
+    _expect("cu_seqlens_q", cu_seqlens_q, (n + 1,), torch.int32)
+    _expect("cu_seqlens_k", cu_seqlens_k, (n + 1,), torch.int32)
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    ts = (q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k)
+    _launch("fa_fwd_window_varlen", stream, (*map(_ptr, ts), n, Tq, Tk, int(max_seqlen_q), H, Hkv, D, int(window),
+                                             int(sinks), float(scale), code), *ts)
+
+
+def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sinks: int = 0,
+                  scale: float | None = None, stream=None):
+    """Gradients of fa_fwd_window: q, o, dout, dq [B,H,Sq,D]; k, v, dk, dv [B,Hkv,Sk,D]; workspace of at least
+    fa_bwd_workspace_bytes(B, H, Sq, D) bytes."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B,H,Sq,D] and k, v [B,Hkv,Sk,D]")
+    B, H, Sq, D = q.shape
+    _, Hkv, Sk, _ = k.shape
+    code = _dtype_code(q)
+    for name, t in (("q", q), ("o", o), ("dout", dout), ("dq", dq)):
+        _expect(name, t, (B, H, Sq, D), q.dtype)
+    for name, t in (("k", k), ("v", v), ("dk", dk), ("dv", dv)):
+        _expect(name, t, (B, Hkv, Sk, D), q.dtype)
+    _expect("lse", lse, (B, H, Sq), torch.float32)
+    _need_contig(workspace)
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    ts = (q, k, v, o, dout, lse, dq, dk, dv, workspace)
+    _launch("fa_bwd_window", stream, (*map(_ptr, ts), workspace.numel() * workspace.element_size(), B, H, Hkv, Sq, Sk,
+                                      D, int(window), int(sinks), float(scale), code), *ts)
+
+
+def fa_bwd_window_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
+                         max_seqlen_k: int, window: int, sinks: int = 0, scale: float | None = None, stream=None):
+    """Gradients of fa_fwd_window_varlen: q, o, dout, dq [total_q,H,D]; k, v, dk, dv [total_k,Hkv,D]; workspace of at
+    least fa_bwd_varlen_workspace_bytes(total_q, H, D) bytes."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [total_q,H,D] and k, v [total_k,Hkv,D]")
+    Tq, H, D = q.shape
+    Tk, Hkv, _ = k.shape
+    n = cu_seqlens_q.numel() - 1
+    code = _dtype_code(q)
+    for name, t in (("q", q), ("o", o), ("dout", dout), ("dq", dq)):
+        _expect(name, t, (Tq, H, D), q.dtype)
+    for name, t in (("k", k), ("v", v), ("dk", dk), ("dv", dv)):
+        _expect(name, t, (Tk, Hkv, D), q.dtype)
+    _expect("lse", lse, (H, Tq), torch.float32)
+    _expect("cu_seqlens_q", cu_seqlens_q, (n + 1,), torch.int32)
+    _expect("cu_seqlens_k", cu_seqlens_k, (n + 1,), torch.int32)
+    _need_contig(workspace)
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    ts = (q, k, v, o, dout, lse, dq, dk, dv, workspace)
+    _launch("fa_bwd_window_varlen", stream,
+            (*map(_ptr, ts), workspace.numel() * workspace.element_size(), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), n,
+             Tq, Tk, int(max_seqlen_q), int(max_seqlen_k), H, Hkv, D, int(window), int(sinks), float(scale), code),
+            *ts, cu_seqlens_q, cu_seqlens_k)
+
+
+def flash_attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None, stream=None):
+    """Returns (o, lse) of causal attention with a sliding window and sinks: q [B,H,Sq,D], k, v [B,Hkv,Sk,D]."""
+    o = torch.empty_like(q)
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    fa_fwd_window(q, k, v, o, lse, window, sinks, scale, stream)
+    return o, lse
+
+
+def flash_attention_window_bwd(q, k, v, o, lse, dout, window: int, sinks: int = 0, scale: float | None = None,
+                               stream=None, workspace=None):
+    """Returns (dq, dk, dv) of flash_attention_window, given its o and lse."""
+    if workspace is None:
+        workspace = torch.empty(fa_bwd_workspace_bytes(*q.shape) // 4, dtype=torch.float32, device=q.device)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window, sinks, scale, stream)
+    return dq, dk, dv
+
+
+def flash_attention_window_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, window: int, sinks: int = 0,
+                                  scale: float | None = None, stream=None):
+    """Returns (o [total_q,H,D], lse [H,total_q]) for packed sequences; k, v [total_k,Hkv,D]."""
+    o = torch.empty_like(q)
+    lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device)
+    fa_fwd_window_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, window, sinks, scale, stream)
+    return o, lse
+
+
+def flash_attention_window_varlen_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
+                                      max_seqlen_k: int, window: int, sinks: int = 0, scale: float | None = None,
+                                      stream=None, workspace=None):
+    """Returns (dq, dk, dv) of flash_attention_window_varlen, given its o and lse."""
+    Tq, H, D = q.shape
+    if workspace is None:
+        workspace = torch.empty(fa_bwd_varlen_workspace_bytes(Tq, H, D) // 4, dtype=torch.float32, device=q.device)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    fa_bwd_window_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                         max_seqlen_k, window, sinks, scale, stream)
+    return dq, dk, dv
 
 
 class KVCacheQ4(NamedTuple):

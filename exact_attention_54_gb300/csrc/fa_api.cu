@@ -130,6 +130,7 @@ long long fwd_work_items(int D, long long heads, int Sq) {
     return heads * ((n_qtiles + 1) / 2);
 }
 constexpr int kMaxLen = 1 << 30;
+constexpr int kMaxWindowLen = 1 << 29;  // window functions: key + window stays within 32 bits
 
 // Page geometry of a paged cache: block_size a power of two up to 1024, and
 // positions and (page, head) indices within 32 bits.
@@ -584,6 +585,197 @@ fa_status_t fa_splitkv_merge(const float *o_part, const float *m_part, const flo
                                                    static_cast<int>(BH), num_splits,
                                                    static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// Sliding-window attention, dense (cu_q == nullptr: B sequences of Sq queries
+// and Sk keys) or packed (B sequences, at most Sq queries and Sk keys each).
+static bool window_ok(int H, int Hkv, int Sq, int Sk, int window, int sinks) {
+    return H >= 1 && Hkv >= 1 && H % Hkv == 0 && Sq >= 1 && Sk >= 1 && Sq <= kMaxWindowLen && Sk <= kMaxWindowLen &&
+           window >= 1 && sinks >= 0;
+}
+
+static fa_status_t fwd_window(const void *q, const void *k, const void *v, void *o, float *lse,
+                              const int32_t *cu_q, const int32_t *cu_k, int B, int total_q, int total_k, int H,
+                              int Hkv, int Sq, int Sk, int D, int window, int sinks, float scale, fa_dtype_t dtype,
+                              void *stream) {
+    const bool varlen = cu_q != nullptr;
+    const long long SH = static_cast<long long>(B) * H;
+    const long long n_work = fwd_work_items(D, SH, Sq);
+    if (SH > INT_MAX || n_work > INT_MAX) return FA_ERR_SHAPE;
+    if (!scale_ok(scale)) return FA_ERR_SCALE;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned4(lse) || !aligned4(cu_q) ||
+        !aligned4(cu_k))
+        return FA_ERR_ALIGN;
+
+    const bool bf16 = dtype == FA_BF16;
+    CUtensorMap maps[3];
+    const uint64_t row = static_cast<uint64_t>(D) * 2;
+    const bool maps_ok =
+        varlen ? encode_map(&maps[0], bf16, q, D, H, total_q, row, row * H, 1, 128) &&
+                     encode_map(&maps[1], bf16, k, D, Hkv, total_k, row, row * Hkv, 1, 128) &&
+                     encode_map(&maps[2], bf16, v, D, Hkv, total_k, row, row * Hkv, 1, 128)
+               : encode_map(&maps[0], bf16, q, D, Sq, SH, row, row * Sq, 128, 1) &&
+                     encode_map(&maps[1], bf16, k, D, Sk, SH / H * Hkv, row, row * Sk, 128, 1) &&
+                     encode_map(&maps[2], bf16, v, D, Sk, SH / H * Hkv, row, row * Sk, 128, 1);
+    int *err = device_error_word();
+    const int sms = num_sms();
+    if (!maps_ok || err == nullptr || sms <= 0) return FA_ERR_CUDA;
+
+    fa::FwdParams p{};
+    p.o = o;
+    p.lse = lse;
+    p.cu_q = cu_q;
+    p.cu_k = cu_k;
+    p.B = B;
+    p.H = H;
+    p.Sq = Sq;
+    p.Sk = Sk;
+    p.total_q = total_q;
+    p.total_k = total_k;
+    p.n_qtiles = (Sq + 127) / 128;
+    p.n_pairs = (p.n_qtiles + 1) / 2;
+    p.num_work = static_cast<int>(n_work);
+    p.scale_log2 = scale * kLog2e;
+    p.err = err;
+    p.timeout_ns = g_wait_limit_ns.load();
+    p.withhold = g_withhold.load();
+    p.window = window < kMaxWindowLen ? window : kMaxWindowLen;
+    p.sinks = sinks < kMaxWindowLen ? sinks : kMaxWindowLen;
+    p.group = H / Hkv;
+    const int grid = p.num_work < sms ? p.num_work : sms;
+    const cudaError_t e =
+        fa::launch_fwd_window(D, bf16, varlen, maps, p, grid, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status_t fa_fwd_window(const void *q, const void *k, const void *v, void *o, float *lse, int B, int H, int Hkv,
+                          int Sq, int Sk, int D, int window, int sinks, float scale, fa_dtype_t dtype, void *stream) {
+    if (!q || !k || !v || !o || !lse) return FA_ERR_NULL;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_DTYPE;
+    if (D != 64 && D != 128) return FA_ERR_HEADDIM;
+    if (B < 1 || !window_ok(H, Hkv, Sq, Sk, window, sinks)) return FA_ERR_SHAPE;
+    return fwd_window(q, k, v, o, lse, nullptr, nullptr, B, 0, 0, H, Hkv, Sq, Sk, D, window, sinks, scale, dtype,
+                      stream);
+}
+
+fa_status_t fa_fwd_window_varlen(const void *q, const void *k, const void *v, void *o, float *lse,
+                                 const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int num_seqs, int total_q,
+                                 int total_k, int max_seqlen_q, int H, int Hkv, int D, int window, int sinks,
+                                 float scale, fa_dtype_t dtype, void *stream) {
+    if (!q || !k || !v || !o || !lse || !cu_seqlens_q || !cu_seqlens_k) return FA_ERR_NULL;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_DTYPE;
+    if (D != 64 && D != 128) return FA_ERR_HEADDIM;
+    if (num_seqs < 1 || total_q < 1 || total_q > kMaxWindowLen ||
+        !window_ok(H, Hkv, max_seqlen_q, total_k, window, sinks))
+        return FA_ERR_SHAPE;
+    return fwd_window(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, num_seqs, total_q, total_k, H, Hkv, max_seqlen_q,
+                      0, D, window, sinks, scale, dtype, stream);
+}
+
+static fa_status_t bwd_window(const void *q, const void *k, const void *v, const void *o, const void *dout,
+                              const float *lse, void *dq, void *dk, void *dv, float *workspace,
+                              size_t workspace_bytes, const int32_t *cu_q, const int32_t *cu_k, int B, int total_q,
+                              int total_k, int H, int Hkv, int Sq, int Sk, int D, int window, int sinks, float scale,
+                              fa_dtype_t dtype, void *stream) {
+    const bool varlen = cu_q != nullptr;
+    const long long BH = static_cast<long long>(B) * H, units = static_cast<long long>(B) * Hkv;
+    const long long n_kt = (Sk + 127) / 128;
+    if (BH > INT_MAX || units * n_kt > INT_MAX || static_cast<long long>(total_q) * H > INT_MAX ||
+        static_cast<long long>(total_k) * Hkv > INT_MAX)
+        return FA_ERR_SHAPE;
+    if (!scale_ok(scale)) return FA_ERR_SCALE;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dout) || !aligned4(lse) ||
+        !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(workspace) || !aligned4(cu_q) ||
+        !aligned4(cu_k))
+        return FA_ERR_ALIGN;
+    const size_t need = varlen ? fa_bwd_varlen_workspace_bytes(total_q, H, D) : fa_bwd_workspace_bytes(B, H, Sq, D);
+    if (need == 0) return FA_ERR_SHAPE;
+    if (workspace_bytes < need) return FA_ERR_WORKSPACE;
+
+    const bool bf16 = dtype == FA_BF16;
+    CUtensorMap maps[5];
+    const uint64_t row = static_cast<uint64_t>(D) * 2, row4 = row * 2;
+    const uint32_t q_rows = D == 128 ? 64 : 128;  // query rows per step of the kernel that runs
+    const bool maps_ok =
+        varlen ? encode_map(&maps[0], bf16, q, D, H, total_q, row, row * H, 1, q_rows) &&
+                     encode_map(&maps[1], bf16, k, D, Hkv, total_k, row, row * Hkv, 1, 128) &&
+                     encode_map(&maps[2], bf16, v, D, Hkv, total_k, row, row * Hkv, 1, 128) &&
+                     encode_map(&maps[3], bf16, dout, D, H, total_q, row, row * H, 1, q_rows) &&
+                     encode_map_f32(&maps[4], workspace, D, H, total_q, row4, row4 * H, 1, q_rows)
+               : encode_map(&maps[0], bf16, q, D, Sq, BH, row, row * Sq, q_rows, 1) &&
+                     encode_map(&maps[1], bf16, k, D, Sk, units, row, row * Sk, 128, 1) &&
+                     encode_map(&maps[2], bf16, v, D, Sk, units, row, row * Sk, 128, 1) &&
+                     encode_map(&maps[3], bf16, dout, D, Sq, BH, row, row * Sq, q_rows, 1) &&
+                     encode_map_f32(&maps[4], workspace, D, Sq, BH, row4, row4 * Sq, q_rows, 1);
+    int *err = device_error_word();
+    const int sms = num_sms();
+    if (!maps_ok || err == nullptr || sms <= 0) return FA_ERR_CUDA;
+
+    fa::BwdParams p{};
+    p.BH = static_cast<int>(BH);
+    p.units = static_cast<int>(units);
+    p.group = H / Hkv;
+    p.Sq = Sq;
+    p.Sk = Sk;
+    p.n_qtiles = (Sq + 127) / 128;
+    p.n_ktiles = static_cast<int>(n_kt);
+    p.Sq_pad = varlen ? 0 : p.n_qtiles * 128;
+    p.heads_per_group = bwd_units_per_group(units, static_cast<long long>(Sq) * p.group, D);
+    p.cu_q = cu_q;
+    p.cu_k = cu_k;
+    p.H = H;
+    p.total_q = total_q;
+    p.total_k = total_k;
+    const size_t rows = varlen ? static_cast<size_t>(total_q) * H : static_cast<size_t>(BH) * Sq;
+    const size_t stat_rows = varlen ? rows : static_cast<size_t>(BH) * p.Sq_pad;
+    p.dq_acc = workspace;
+    p.lse2 = workspace + rows * D;
+    p.delta = p.lse2 + stat_rows;
+    p.work_counter = reinterpret_cast<int *>(p.delta + stat_rows);
+    p.total_units = static_cast<int>(units * n_kt);
+    p.grid = sms;
+    p.dk = dk;
+    p.dv = dv;
+    p.scale = scale;
+    p.scale_log2 = scale * kLog2e;
+    p.err = err;
+    p.timeout_ns = g_wait_limit_ns.load();
+    p.withhold = g_withhold.load();
+    p.window = window < kMaxWindowLen ? window : kMaxWindowLen;
+    p.sinks = sinks < kMaxWindowLen ? sinks : kMaxWindowLen;
+    const cudaError_t e = fa::launch_bwd_window(D, bf16, varlen, maps, o, dout, lse, dq, p,
+                                                static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status_t fa_bwd_window(const void *q, const void *k, const void *v, const void *o, const void *dout,
+                          const float *lse, void *dq, void *dk, void *dv, float *workspace, size_t workspace_bytes,
+                          int B, int H, int Hkv, int Sq, int Sk, int D, int window, int sinks, float scale,
+                          fa_dtype_t dtype, void *stream) {
+    if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv || !workspace) return FA_ERR_NULL;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_DTYPE;
+    if (D != 64 && D != 128) return FA_ERR_HEADDIM;
+    if (B < 1 || !window_ok(H, Hkv, Sq, Sk, window, sinks)) return FA_ERR_SHAPE;
+    return bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, workspace_bytes, nullptr, nullptr, B, 0, 0, H,
+                      Hkv, Sq, Sk, D, window, sinks, scale, dtype, stream);
+}
+
+fa_status_t fa_bwd_window_varlen(const void *q, const void *k, const void *v, const void *o, const void *dout,
+                                 const float *lse, void *dq, void *dk, void *dv, float *workspace,
+                                 size_t workspace_bytes, const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                 int num_seqs, int total_q, int total_k, int max_seqlen_q, int max_seqlen_k, int H,
+                                 int Hkv, int D, int window, int sinks, float scale, fa_dtype_t dtype,
+                                 void *stream) {
+    if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv || !workspace || !cu_seqlens_q || !cu_seqlens_k)
+        return FA_ERR_NULL;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_DTYPE;
+    if (D != 64 && D != 128) return FA_ERR_HEADDIM;
+    if (num_seqs < 1 || total_q < 1 || total_k < 1 || total_q > kMaxWindowLen || total_k > kMaxWindowLen ||
+        !window_ok(H, Hkv, max_seqlen_q, max_seqlen_k, window, sinks))
+        return FA_ERR_SHAPE;
+    return bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, workspace_bytes, cu_seqlens_q, cu_seqlens_k,
+                      num_seqs, total_q, total_k, H, Hkv, max_seqlen_q, max_seqlen_k, D, window, sinks, scale, dtype,
+                      stream);
 }
 
 static fa_status_t kv_q4(bool write, const void *k, const void *v, const void *k_codes, const void *k_scales,

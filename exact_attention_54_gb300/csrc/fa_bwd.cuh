@@ -213,19 +213,15 @@ __global__ void __launch_bounds__(256) fa_bwd_dq_kernel(const float *__restrict_
 // Every CTA of a head re-reads its Q and dO and adds into its dQ accumulator,
 // so running a few heads at once keeps that set (8 Sq D bytes per head)
 // within L2 instead of streaming every head's through it at once.
+template <bool WIN>
 __device__ __forceinline__ void bwd_work_at(const BwdParams &p, int w, int &kt, int &bh) {
     const int per_group = p.heads_per_group * p.n_ktiles;
     const int g = w / per_group;
     const int i = w % per_group;
-    const int rest = p.BH - g * p.heads_per_group;
+    const int rest = (WIN ? p.units : p.BH) - g * p.heads_per_group;
     const int g_heads = rest < p.heads_per_group ? rest : p.heads_per_group;
     kt = i / g_heads;
     bh = g * p.heads_per_group + i % g_heads;
-}
-
-// The unit of this CTA (one unit per CTA, in block order).
-__device__ __forceinline__ void bwd_work(const BwdParams &p, int &kt, int &bh) {
-    bwd_work_at(p, static_cast<int>(blockIdx.x), kt, bh);
 }
 
 // This CTA's key tile and what it needs of its unit: the unit's index (dense
@@ -241,15 +237,16 @@ struct BwdUnit {
     bool ok;
 };
 
-template <bool VARLEN>
+template <bool VARLEN, bool WIN>
 __device__ __forceinline__ BwdUnit bwd_unit_at(const BwdParams &p, int w) {
     BwdUnit u;
     int unit;
-    bwd_work_at(p, w, u.kt, unit);
+    bwd_work_at<WIN>(p, w, u.kt, unit);
     if constexpr (VARLEN) {
-        const int b = unit / p.H;
+        const int heads = WIN ? p.H / p.group : p.H;  // of the keys
+        const int b = unit / heads;
         u.z = 0;
-        u.hh = unit % p.H;
+        u.hh = unit % heads;
         const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
         u.ok = !(q0 < 0 || q1 < q0 || q1 > p.total_q || q1 - q0 > p.Sq || k0 < 0 || k1 < k0 || k1 > p.total_k ||
                  k1 - k0 > p.Sk);
@@ -268,9 +265,46 @@ __device__ __forceinline__ BwdUnit bwd_unit_at(const BwdParams &p, int w) {
     return u;
 }
 
-template <bool VARLEN>
+template <bool VARLEN, bool WIN>
 __device__ __forceinline__ BwdUnit bwd_unit(const BwdParams &p) {
-    return bwd_unit_at<VARLEN>(p, static_cast<int>(blockIdx.x));
+    return bwd_unit_at<VARLEN, WIN>(p, static_cast<int>(blockIdx.x));
+}
+
+// Sliding window (WIN). A unit is a key tile of a key head; its steps go
+// through the group's query heads one after the other, and for each through
+// the blocks of BLOCK queries that see any of its keys: from the tile's first
+// key on, to the last query whose window reaches the tile's last key, or to
+// the end where the tile holds sinks. dK and dV of the shared head so add up
+// in the same accumulators, in a fixed order. (Lengths, window and sinks are
+// at most 2^29: the sums below stay within 32 bits.)
+template <bool CAUSAL, bool WIN, int BLOCK>
+__device__ __forceinline__ int query_blocks(const BwdParams &p, const BwdUnit &u, int k0) {
+    const int q_begin = CAUSAL ? k0 : 0;
+    int q_end = u.Lq;
+    if (WIN && k0 >= p.sinks) q_end = min(q_end, k0 + kBlock - 1 + p.window);
+    return q_end > q_begin ? (q_end - q_begin + BLOCK - 1) / BLOCK : 0;
+}
+
+// The unit as its step `step` sees it on the query side: u.z and u.hh become
+// those of the step's query head, `block` the step's block of queries.
+template <bool WIN>
+__device__ __forceinline__ BwdUnit query_side(const BwdParams &p, const BwdUnit &u, int step, int blocks, int &block) {
+    BwdUnit q = u;
+    block = step;
+    if constexpr (WIN) {
+        const int g = step / blocks;
+        block = step - g * blocks;
+        q.z = u.z * p.group + g;
+        q.hh = u.hh * p.group + g;
+    }
+    return q;
+}
+
+// Queries of a chunk [qc, qc + 32) that see `key`: lo <= i < hi.
+template <bool CAUSAL, bool WIN>
+__device__ __forceinline__ void seen_queries(const BwdParams &p, const BwdUnit &u, int key, int qc, int &lo, int &hi) {
+    lo = key >= u.Lk ? 32 : (CAUSAL ? key - qc : 0);
+    hi = WIN && key >= p.sinks ? key + p.window - qc : 32;
 }
 
 // Tensor-map coordinates (y, z) of row `row` of the unit's queries or keys:
@@ -323,7 +357,7 @@ __device__ __forceinline__ void load_tile(const CUtensorMap *tm, uint32_t dst, u
     for (int c = 0; c < D / 64; ++c) ptx::tma_load_3d(dst + c * Shape<D>::kBoxBytes, tm, bar, c * 64, row0, bh);
 }
 
-template <int D, bool BF16, bool CAUSAL, bool VARLEN>
+template <int D, bool BF16, bool CAUSAL, bool VARLEN, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_bwd_d64_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -345,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     // work item: key tile kt of a head (dense) or of a sequence's head (packed)
-    const BwdUnit u = bwd_unit<VARLEN>(p);
+    const BwdUnit u = bwd_unit<VARLEN, WIN>(p);
     if constexpr (VARLEN) {
         // packed: offsets outside the tensors are reported and skipped; a
         // key tile past the sequence's keys has nothing to compute or write
@@ -358,12 +392,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kt = u.kt;
     const int k0 = kt * kBlock;
     const int qt0 = CAUSAL ? kt : 0;  // first query tile that sees any of these keys
-    const int n_qt = (u.Lq + kBlock - 1) / kBlock;
-    const int n = n_qt > qt0 ? n_qt - qt0 : 0;
+    const int n_blocks = query_blocks<CAUSAL, WIN, kBlock>(p, u, k0);
+    const int n = WIN ? n_blocks * p.group : n_blocks;
     // 128 rows of the unit's queries (keys = false) or keys, every 64-column box
-    auto load_rows = [&](const CUtensorMap *tm, uint32_t dst, uint32_t bar_addr, int row0, bool keys) {
+    auto load_rows = [&](const CUtensorMap *tm, const BwdUnit &unit, uint32_t dst, uint32_t bar_addr, int row0,
+                         bool keys) {
         int y, z;
-        unit_coords<VARLEN>(u, keys, row0, y, z);
+        unit_coords<VARLEN>(unit, keys, row0, y, z);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) ptx::tma_load_3d(dst + c * S::kBoxBytes, tm, bar_addr, c * 64, y, z);
     };
@@ -399,19 +434,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool leader = ptx::elect_one();
         if (leader) {
             ptx::bar_arrive_expect_tx(bar(S::kKVFull), 2 * S::kTileBytes);
-            load_rows(&tm_k, sbase + S::kOffK, bar(S::kKVFull), k0, true);
-            load_rows(&tm_v, sbase + S::kOffV, bar(S::kKVFull), k0, true);
+            load_rows(&tm_k, u, sbase + S::kOffK, bar(S::kKVFull), k0, true);
+            load_rows(&tm_v, u, sbase + S::kOffV, bar(S::kKVFull), k0, true);
         }
         int nq = 0, nl = 0;  // Q/dO steps and row-value steps loaded
         for (int it = 0; it < n; ++it) {
             const int s = it & 1;
             // stage s is free once the bulk reduction of step it-2 has read it
             if (it >= 2 && !wait(S::kStageFree + s, ((it >> 1) - 1) & 1)) break;
-            const int q0 = (qt0 + it) * kBlock;
+            int qb;
+            const BwdUnit uq = query_side<WIN>(p, u, it, n_blocks, qb);
+            const int q0 = (qt0 + qb) * kBlock;
             if (leader && !withheld(p.withhold, static_cast<uint32_t>(it))) {
                 ptx::bar_arrive_expect_tx(bar(S::kQFull + s), 2 * S::kTileBytes);
-                load_rows(&tm_q, sbase + S::kOffQ + s * S::kTileBytes, bar(S::kQFull + s), q0, false);
-                load_rows(&tm_do, sbase + S::kOffDO + s * S::kTileBytes, bar(S::kQFull + s), q0, false);
+                load_rows(&tm_q, uq, sbase + S::kOffQ + s * S::kTileBytes, bar(S::kQFull + s), q0, false);
+                load_rows(&tm_do, uq, sbase + S::kOffDO + s * S::kTileBytes, bar(S::kQFull + s), q0, false);
             }
             ++nq;
             // the single row-value buffer is free once every compute warp has
@@ -422,10 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!got) break;
             }
             if constexpr (VARLEN) {
-                load_rows_packed<128>(p, u, q0, reinterpret_cast<float *>(smem_raw + S::kOffRows), bar(S::kLFull),
+                load_rows_packed<128>(p, uq, q0, reinterpret_cast<float *>(smem_raw + S::kOffRows), bar(S::kLFull),
                                       leader);
             } else if (leader) {
-                const size_t ro = static_cast<size_t>(u.z) * p.Sq_pad + q0;
+                const size_t ro = static_cast<size_t>(uq.z) * p.Sq_pad + q0;
                 ptx::bar_arrive_expect_tx(bar(S::kLFull), 2 * 128 * 4);
                 ptx::bulk_load(ssmall + S::kOffRows, p.lse2 + ro, 128 * 4, bar(S::kLFull));
                 ptx::bulk_load(ssmall + S::kOffRows + 128 * 4, p.delta + ro, 128 * 4, bar(S::kLFull));
@@ -530,7 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int it = 0; it < n; ++it) {
             const int s = it & 1;
-            const int q0 = (qt0 + it) * kBlock;
+            int qb;
+            query_side<WIN>(p, u, it, n_blocks, qb);
+            const int q0 = (qt0 + qb) * kBlock;
             // the step's LSE and D values and the free dS^T buffer are ready
             // well before S^T and dP^T: wait for them first, so that only one
             // wait separates the tensor core's commit from the key-row work
@@ -548,10 +587,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::reg_fence(sv);
                 ptx::reg_fence(dpv);
                 const int qc = q0 + 32 * c;
-                const bool need_mask = (CAUSAL && key > qc) || key >= u.Lk;
                 // queries j < lo of the chunk do not see this key (causal: a
-                // key is seen from its own position on; a key past Lk by none)
-                const int lo = key >= u.Lk ? 32 : (CAUSAL ? key - qc : 0);
+                // key is seen from its own position on; a key past Lk by none),
+                // nor do those from hi on (its window does not reach them)
+                int lo, hi;
+                seen_queries<CAUSAL, WIN>(p, u, key, qc, lo, hi);
+                const bool need_mask = (CAUSAL && key > qc) || key >= u.Lk || (WIN && hi < 32);
                 uint32_t pp[16], dd[16];
                 const float4 *lq = reinterpret_cast<const float4 *>(rows_lse + 32 * c);
                 const float4 *dq4 = reinterpret_cast<const float4 *>(rows_lse + 128 + 32 * c);
@@ -564,8 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float e0 = ptx::ex2(fmaf(__uint_as_float(sv[j]), p.scale_log2, -l0));
                     float e1 = ptx::ex2(fmaf(__uint_as_float(sv[j + 1]), p.scale_log2, -l1));
                     if (need_mask) {
-                        if (j < lo) e0 = 0.f;
-                        if (j + 1 < lo) e1 = 0.f;
+                        if (j < lo || (WIN && j >= hi)) e0 = 0.f;
+                        if (j + 1 < lo || (WIN && j + 1 >= hi)) e1 = 0.f;
                     }
                     pp[j / 2] = ptx::pack2<BF16>(e0, e1);
                     dd[j / 2] = ptx::pack2<BF16>(e0 * (__uint_as_float(dpv[j]) - d0),
@@ -628,7 +669,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // them; only the global stores are limited to keys that exist.
         if (ok) {
             const bool row_valid = key < u.Lk;
-            const size_t row_g = (VARLEN ? (static_cast<size_t>(u.tk0) + key) * p.H + u.hh
+            const int heads = WIN ? p.H / p.group : p.H;  // of the keys
+            const size_t row_g = (VARLEN ? (static_cast<size_t>(u.tk0) + key) * heads + u.hh
                                          : static_cast<size_t>(u.z) * p.Sk + key) * D + h * (D / 2);
             const uint64_t once = ptx::l2_policy_evict_first();
             // 32-byte stores when both outputs are 32-byte aligned
@@ -676,13 +718,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int s = it & 1;
             if (!wait(S::kStageReady, it & 1)) break;
             if (leader) {
-                const int q0 = (qt0 + it) * kBlock;
+                int qb;
+                const BwdUnit uq = query_side<WIN>(p, u, it, n_blocks, qb);
+                const int q0 = (qt0 + qb) * kBlock;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     const uint32_t box = sbase + (c < D / 64 ? S::kOffQ + s * S::kTileBytes + c * S::kBoxBytes
                                                              : S::kOffDO + s * S::kTileBytes + (c - D / 64) * S::kBoxBytes);
                     int y, z;
-                    unit_coords<VARLEN>(u, false, q0, y, z);
+                    unit_coords<VARLEN>(uq, false, q0, y, z);
                     ptx::tma_reduce_add_3d(&tm_dq, box, 32 * c, y, z);  // rows past the tensor are clipped
                 }
                 ptx::bulk_commit();
@@ -793,7 +837,7 @@ struct ShapeQ64 {
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
-template <bool BF16, bool CAUSAL, bool VARLEN>
+template <bool BF16, bool CAUSAL, bool VARLEN, bool WIN>
 __global__ void __launch_bounds__(kThreadsQ64, 1)
     fa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -858,11 +902,11 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
     ptx::grid_launch_dependents();
 
     // A published unit as every role sees it; n: its 64-query sub-steps from
-    // the first query that sees any of its keys.
+    // the first query that sees any of its keys (blocks for each query head).
     struct UnitView {
         bool live;  // false: no unit is left
         BwdUnit u;
-        int k0, qs0, n;
+        int k0, qs0, n, blocks;
     };
     // Unit slot i of this CTA: waits until warp 0 has published it, copies it
     // and releases the slot. False when the wait gave up.
@@ -881,7 +925,8 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
         uv.u.ok = true;
         uv.k0 = uv.u.kt * kBlock;
         uv.qs0 = CAUSAL ? uv.k0 : 0;
-        uv.n = uv.u.Lq > uv.qs0 ? (uv.u.Lq - uv.qs0 + S::kQ - 1) / S::kQ : 0;
+        uv.blocks = query_blocks<CAUSAL, WIN, S::kQ>(p, uv.u, uv.k0);
+        uv.n = WIN ? uv.blocks * p.group : uv.blocks;
         __syncwarp();
         if (lane == 0) ptx::bar_arrive(bar(S::kUnitFree + s));
         return true;
@@ -909,7 +954,7 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
                 if (lane == 0) got = atomicAdd(p.work_counter, 1);
                 w = __shfl_sync(0xffffffffu, got, 0);
                 if (w >= p.total_units) break;
-                u = bwd_unit_at<VARLEN>(p, w);
+                u = bwd_unit_at<VARLEN, WIN>(p, w);
                 if constexpr (VARLEN) {
                     if (!u.ok) {
                         if (lane == 0) atomicExch(p.err, kDeviceErrSeqLens);
@@ -935,7 +980,8 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
             __syncwarp();
             if (!live) break;
             const int k0 = u.kt * kBlock, qs0 = CAUSAL ? k0 : 0;
-            const int n = u.Lq > qs0 ? (u.Lq - qs0 + S::kQ - 1) / S::kQ : 0;
+            const int blocks = query_blocks<CAUSAL, WIN, S::kQ>(p, u, k0);
+            const int n = WIN ? blocks * p.group : blocks;
             if (n == 0) continue;  // no query sees these keys: zero dK and dV only
             // K and V of the unit once the previous unit's products are done with theirs
             if (wi >= 1 && !(ok = wait(S::kKVEmpty, (wi - 1) & 1))) break;
@@ -955,10 +1001,12 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
                 const int st = J % S::kStages, b = J & 1;
                 // each half of the stage held part of sub-step J-4's staged dQ_t
                 // until its reductions read it: Q_J first (S^T needs it), then dO_J
-                const int q0 = qs0 + j * S::kQ;
+                int block;
+                const BwdUnit uq = query_side<WIN>(p, u, j, blocks, block);
+                const int q0 = qs0 + block * S::kQ;
                 const uint32_t qb = sbase + S::kOffQ + st * S::kStageBytes;
                 int qy, qz;
-                unit_coords<VARLEN>(u, false, q0, qy, qz);
+                unit_coords<VARLEN>(uq, false, q0, qy, qz);
                 if (J >= S::kStages && !(ok = wait(S::kStageFreeQ + st, ((J / S::kStages) - 1) & 1))) break;
                 if (leader && !withheld(p.withhold, static_cast<uint32_t>(J))) {
                     ptx::bar_arrive_expect_tx(bar(S::kQFull + st), S::kQTileBytes);
@@ -976,12 +1024,12 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
                 // row buffer b is free once the key-row warps are done with sub-step J-2
                 if (J >= 2 && !(ok = wait(S::kPFull + b, ((J - 2) >> 1) & 1))) break;
                 if constexpr (VARLEN) {
-                    load_rows_packed<S::kQ>(p, u, q0,
+                    load_rows_packed<S::kQ>(p, uq, q0,
                                             reinterpret_cast<float *>(smem_raw + S::kOffRows + b * 2 * S::kQ * 4),
                                             bar(S::kLFull + b), leader);
                 } else if (leader) {
                     const uint32_t rows = ssmall + S::kOffRows + b * 2 * S::kQ * 4;
-                    const size_t ro = static_cast<size_t>(u.z) * p.Sq_pad + q0;
+                    const size_t ro = static_cast<size_t>(uq.z) * p.Sq_pad + q0;
                     ptx::bar_arrive_expect_tx(bar(S::kLFull + b), 2 * S::kQ * 4);
                     ptx::bulk_load(rows, p.lse2 + ro, S::kQ * 4, bar(S::kLFull + b));
                     ptx::bulk_load(rows + S::kQ * 4, p.delta + ro, S::kQ * 4, bar(S::kLFull + b));
@@ -1140,7 +1188,9 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
           const int key = k0 + r;
           for (int j = 0; j < n; ++j, ++J) {
             const int b = J & 1;
-            const int qc = qs0 + j * S::kQ + 32 * h;  // first query of this warp's chunk
+            int block;
+            query_side<WIN>(p, u, j, uv.blocks, block);
+            const int qc = qs0 + block * S::kQ + 32 * h;  // first query of this warp's chunk
             const uint32_t tb = tmem + lane_base + S::kTmemBuf + 128 * b;
             // the sub-step's rows, then S^T: one test of both first, the
             // bounded waits only when one is open
@@ -1155,8 +1205,9 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
             ptx::tmem_ld32(tb + 32 * h, sv);
             ptx::tmem_ld_wait();
             ptx::reg_fence(sv);
-            const bool need_mask = (CAUSAL && key > qc) || key >= u.Lk;
-            const int lo = key >= u.Lk ? 32 : (CAUSAL ? key - qc : 0);  // queries i < lo do not see the key
+            int lo, hi;  // queries i < lo and i >= hi do not see the key
+            seen_queries<CAUSAL, WIN>(p, u, key, qc, lo, hi);
+            const bool need_mask = (CAUSAL && key > qc) || key >= u.Lk || (WIN && hi < 32);
             const float *rows = reinterpret_cast<const float *>(smem_raw + S::kOffRows + b * 2 * S::kQ * 4);
             const float4 *lq = reinterpret_cast<const float4 *>(rows + 32 * h);
             const float4 *dq4 = reinterpret_cast<const float4 *>(rows + S::kQ + 32 * h);
@@ -1168,8 +1219,8 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
                 float e0 = ptx::ex2(fmaf(__uint_as_float(sv[i]), p.scale_log2, -l0));
                 float e1 = ptx::ex2(fmaf(__uint_as_float(sv[i + 1]), p.scale_log2, -l1));
                 if (need_mask) {
-                    if (i < lo) e0 = 0.f;
-                    if (i + 1 < lo) e1 = 0.f;
+                    if (i < lo || (WIN && i >= hi)) e0 = 0.f;
+                    if (i + 1 < lo || (WIN && i + 1 >= hi)) e1 = 0.f;
                 }
                 pp[i / 2] = ptx::pack2<BF16>(e0, e1);
             }
@@ -1270,7 +1321,8 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
                     const int key_r = k0 + wq * 32 + rr;
                     if (key_r < u.Lk) {
                         // written once: evict first
-                        const size_t row_g = (VARLEN ? (static_cast<size_t>(u.tk0) + key_r) * p.H + u.hh
+                        const int heads = WIN ? p.H / p.group : p.H;  // of the keys
+                        const size_t row_g = (VARLEN ? (static_cast<size_t>(u.tk0) + key_r) * heads + u.hh
                                                      : static_cast<size_t>(u.z) * p.Sk + key_r) * D + h * (D / 2);
                         ptx::st_global_v4_hint(reinterpret_cast<uint4 *>(out + row_g) + q, val.x, val.y, val.z,
                                                val.w, once);
@@ -1334,10 +1386,12 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
             const int st = J % S::kStages;
             if (!(ok = wait(S::kStageReady + st, (J / S::kStages) & 1))) break;
             if (leader) {
-                const int q0 = uv.qs0 + j * S::kQ;
+                int block;
+                const BwdUnit uq = query_side<WIN>(p, u, j, uv.blocks, block);
+                const int q0 = uv.qs0 + block * S::kQ;
                 const uint32_t tile = sbase + S::kOffQ + st * S::kStageBytes;
                 int y, z;
-                unit_coords<VARLEN>(u, false, q0, y, z);
+                unit_coords<VARLEN>(uq, false, q0, y, z);
                 // boxes 0, 1 (over Q_J), then 2, 3 (over dO_J), as two groups
                 for (int c = 0; c < D / 32; ++c) {
                     ptx::tma_reduce_add_3d(&tm_dq, tile + c * S::kDQBoxBytes, 32 * c, y, z);
@@ -1365,7 +1419,7 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
     if (threadIdx.x == 0 && *abort_flag) atomicExch(p.err, kDeviceErrTimeout);
 }
 
-template <int D, bool BF16, bool CAUSAL, bool VARLEN>
+template <int D, bool BF16, bool CAUSAL, bool VARLEN, bool WIN = false>
 cudaError_t launch_t(const CUtensorMap *maps, const void *o, const void *dout, const float *lse, void *dq,
                      const BwdParams &p, cudaStream_t st) {
     // prep grid: row chunks x heads (heads split over y and z: at most 65535 each)
@@ -1379,12 +1433,13 @@ cudaError_t launch_t(const CUtensorMap *maps, const void *o, const void *dout, c
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // D = 64: 128-query steps; D = 128: 64-query sub-steps, double-buffered in TMEM
-    auto kern = D == 64 ? fa_bwd_d64_kernel<64, BF16, CAUSAL, VARLEN> : fa_bwd_kernel<BF16, CAUSAL, VARLEN>;
+    auto kern = D == 64 ? fa_bwd_d64_kernel<64, BF16, CAUSAL, VARLEN, WIN>
+                        : fa_bwd_kernel<BF16, CAUSAL, VARLEN, WIN>;
     constexpr int kSmem = D == 64 ? Shape<64>::kSmemBytes : ShapeQ64::kSmemBytes;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     // D = 64: one CTA per work unit; D = 128: persistent CTAs take units from a counter
-    const long long units = static_cast<long long>(p.BH) * p.n_ktiles;
+    const long long units = static_cast<long long>(WIN ? p.units : p.BH) * p.n_ktiles;
     const long long grid = D == 64 ? units : (units < p.grid ? units : p.grid);
     // D = 128: the main and the conversion kernels are launched as programmatic
     // dependents (each waits for its predecessor in the kernel itself)

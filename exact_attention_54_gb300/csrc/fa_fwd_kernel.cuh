@@ -142,15 +142,63 @@ struct Work {
     int q_start[2];      // first query row of each tile (relative to the sequence)
     int rows[2];         // valid rows of each tile (0 = inactive)
     int n_kv[2];         // K/V tiles each query tile visits
-    int n_kv_max;
+    int n_kv_max;        // K/V tiles the item loads: steps 0 .. n_kv_max - 1
+    // sliding window (WIN) only, in K/V tiles: the item's steps are tiles
+    // [0, ns), which hold sinks, then the tiles from lo on; query tile t
+    // visits tiles [0, sink[t]) and [wlo[t], hi[t])
+    int ns, lo;
+    int sink[2], wlo[2], hi[2];
 };
 
+// K/V tile of step j of an item, and whether query tile t visits it.
+template <bool WIN>
+__device__ __forceinline__ int kv_tile(const Work &k, int j) {
+    if constexpr (WIN) return j < k.ns ? j : j - k.ns + k.lo;
+    return j;
+}
+
+template <bool WIN>
+__device__ __forceinline__ bool visits(const Work &k, int t, int j) {
+    if constexpr (WIN) {
+        const int x = kv_tile<WIN>(k, j);
+        return x < k.hi[t] && (x < k.sink[t] || x >= k.wlo[t]);
+    }
+    return j < k.n_kv[t];
+}
+
 // Query tiles, rows and key-tile counts of a work item from its sequence
-// lengths and pair index.
-template <bool CAUSAL>
-__device__ __forceinline__ void finish_work(Work &k, int pair) {
+// lengths and pair index. With a window, query i sees the keys j <= i with
+// i - j < window or j < sinks: two runs of key tiles, of which each is read
+// once for both query tiles.
+template <bool CAUSAL, bool WIN>
+__device__ __forceinline__ void finish_work(const FwdParams &p, Work &k, int pair) {
     const int nk_all = (k.Lk + kBlockN - 1) / kBlockN;
     k.n_kv_max = 0;
+    if constexpr (WIN) {
+        const int sink_tiles = p.sinks / kBlockN + (p.sinks % kBlockN != 0 ? 1 : 0);
+        k.ns = 0;
+        k.lo = nk_all;
+        int end = 0;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int qs = (2 * pair + t) * kBlockM;
+            k.q_start[t] = qs;
+            const int rows = k.Lq - qs;
+            k.rows[t] = rows <= 0 ? 0 : (rows < kBlockM ? rows : kBlockM);
+            k.hi[t] = k.rows[t] > 0 ? min((qs + k.rows[t] - 1) / kBlockN + 1, nk_all) : 0;
+            k.wlo[t] = max(qs - p.window + 1, 0) / kBlockN;  // the first row reaches back furthest
+            k.sink[t] = min(sink_tiles, k.hi[t]);
+            k.n_kv[t] = k.sink[t] + max(k.hi[t] - max(k.wlo[t], k.sink[t]), 0);
+            if (k.n_kv[t] > 0) {
+                k.ns = max(k.ns, k.sink[t]);
+                k.lo = min(k.lo, k.wlo[t]);
+                end = max(end, k.hi[t]);
+            }
+        }
+        k.lo = max(k.lo, k.ns);
+        k.n_kv_max = k.ns + max(end - k.lo, 0);
+        return;
+    }
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const int qs = (2 * pair + t) * kBlockM;
@@ -173,7 +221,7 @@ __device__ __forceinline__ void finish_work(Work &k, int pair) {
 // Work item w, resolved from the launch parameters (dense), the schedule
 // table or the plain enumeration (packed sequences). `pair_out` receives its
 // query-tile pair index.
-template <bool CAUSAL, bool VARLEN>
+template <bool CAUSAL, bool VARLEN, bool WIN>
 __device__ __forceinline__ Work resolve_work(const FwdParams &p, int w, uint32_t sched, int *pair_out = nullptr) {
     Work k;
     const int BH = p.B * p.H;
@@ -205,7 +253,7 @@ __device__ __forceinline__ Work resolve_work(const FwdParams &p, int w, uint32_t
         k.Lk = p.Sk;
     }
     if (pair_out != nullptr) *pair_out = pair;
-    finish_work<CAUSAL>(k, pair);
+    finish_work<CAUSAL, WIN>(p, k, pair);
     return k;
 }
 
@@ -213,7 +261,7 @@ __device__ __forceinline__ int work_index(int r);
 
 // The work item of this CTA's round r (an item of the launch: callers check
 // work_index(r) < num_items first).
-template <bool CAUSAL, bool VARLEN>
+template <bool CAUSAL, bool VARLEN, bool WIN>
 __device__ __forceinline__ Work get_work(const FwdParams &p, int r, uint32_t sched) {
     if constexpr (VARLEN) {
         if (r < lds_int(sched + 4 * VarlenSched::kRecs)) {
@@ -226,11 +274,11 @@ __device__ __forceinline__ Work get_work(const FwdParams &p, int r, uint32_t sch
             k.seq_k0 = c.x;
             k.Lq = c.y;
             k.Lk = c.z;
-            finish_work<CAUSAL>(k, a.z);
+            finish_work<CAUSAL, WIN>(p, k, a.z);
             return k;
         }
     }
-    return resolve_work<CAUSAL, VARLEN>(p, work_index(r), sched);
+    return resolve_work<CAUSAL, VARLEN, WIN>(p, work_index(r), sched);
 }
 
 // Static persistent schedule: round r hands out work items [r*G, (r+1)*G),
@@ -244,24 +292,28 @@ __device__ __forceinline__ int work_index(int r) {
 
 // ------------------------------------------------------------------ roles --
 
-// Loads one K or V tile (all 64-column boxes) of key tile j into `dst`.
-template <int D, bool VARLEN>
+// Loads one K or V tile (all 64-column boxes) of the item's step j into `dst`.
+// With WIN, p.group query heads share a key head.
+template <int D, bool VARLEN, bool WIN>
 __device__ __forceinline__ void load_kv_tile(const CUtensorMap *tm, uint32_t dst, uint32_t bar, const Work &wk,
-                                             int j, int H) {
+                                             int step, const FwdParams &p) {
     using S = FwdShape<D>;
+    const int j = kv_tile<WIN>(wk, step);
+    const int h = WIN ? wk.h / p.group : wk.h;
+    const int H = WIN ? p.H / p.group : p.H;
 #pragma unroll
     for (int c = 0; c < S::kColBlocks; ++c) {
         if constexpr (VARLEN)
-            ptx::tma_load_3d(dst + c * S::kBlockBytes, tm, bar, c * 64, wk.h, wk.seq_k0 + j * kBlockN);
+            ptx::tma_load_3d(dst + c * S::kBlockBytes, tm, bar, c * 64, h, wk.seq_k0 + j * kBlockN);
         else
-            ptx::tma_load_3d(dst + c * S::kBlockBytes, tm, bar, c * 64, j * kBlockN, wk.b * H + wk.h);
+            ptx::tma_load_3d(dst + c * S::kBlockBytes, tm, bar, c * 64, j * kBlockN, wk.b * H + h);
     }
 }
 
 // Q and K producer (one thread). It issues no L2 prefetches: asking L2 for
 // the next item's Q while the current item ran cost 1.5 % (dense) and 4 %
 // (packed sequences), and K/V tiles prefetched ahead of the ring cost more.
-template <int D, bool CAUSAL, bool VARLEN>
+template <int D, bool CAUSAL, bool VARLEN, bool WIN>
 __device__ void fwd_producer_qk(const CUtensorMap *tq, const CUtensorMap *tk, const FwdParams &p, uint32_t sbase,
                                 volatile int *abort_flag) {
     using S = FwdShape<D>;
@@ -277,7 +329,7 @@ __device__ void fwd_producer_qk(const CUtensorMap *tq, const CUtensorMap *tk, co
     for (int r = 0; ok; ++r) {
         const int w = work_index(r);
         if (w >= num_items<VARLEN>(p, sched)) break;
-        const Work wk = get_work<CAUSAL, VARLEN>(p, r, sched);
+        const Work wk = get_work<CAUSAL, VARLEN, WIN>(p, r, sched);
         if (wk.n_kv_max == 0) continue;
         // The item's Q pair, once the previous item's last Q K^T has read
         // the buffer.
@@ -326,8 +378,8 @@ __device__ void fwd_producer_qk(const CUtensorMap *tq, const CUtensorMap *tk, co
                 break;
             if (leader) {
                 ptx::bar_arrive_expect_tx(bar(S::kKFull + stage), S::kTileBytes);
-                load_kv_tile<D, VARLEN>(tk, sbase + S::kOffK + stage * S::kTileBytes, bar(S::kKFull + stage), wk, j,
-                                        p.H);
+                load_kv_tile<D, VARLEN, WIN>(tk, sbase + S::kOffK + stage * S::kTileBytes, bar(S::kKFull + stage), wk,
+                                             j, p);
             }
             if (wi > 0 && j == 0 && !(ok = load_q())) break;
         }
@@ -344,7 +396,7 @@ __device__ void fwd_producer_qk(const CUtensorMap *tq, const CUtensorMap *tk, co
 }
 
 // V producer (one thread): runs ahead of the P V products as far as its ring allows.
-template <int D, bool CAUSAL, bool VARLEN>
+template <int D, bool CAUSAL, bool VARLEN, bool WIN>
 __device__ void fwd_producer_v(const CUtensorMap *tv, const FwdParams &p, uint32_t sbase, volatile int *abort_flag) {
     using S = FwdShape<D>;
     const uint32_t sched = sbase + S::kOffSched;
@@ -356,7 +408,7 @@ __device__ void fwd_producer_v(const CUtensorMap *tv, const FwdParams &p, uint32
     for (int r = 0; ok; ++r) {
         const int w = work_index(r);
         if (w >= num_items<VARLEN>(p, sched)) break;
-        const Work wk = get_work<CAUSAL, VARLEN>(p, r, sched);
+        const Work wk = get_work<CAUSAL, VARLEN, WIN>(p, r, sched);
         for (int j = 0; j < wk.n_kv_max; ++j, ++it) {
             // V tile 0 goes with the first Q and K tiles; later V tiles wait
             // until the first Q pair has landed (see the Q/K producer).
@@ -368,8 +420,8 @@ __device__ void fwd_producer_v(const CUtensorMap *tv, const FwdParams &p, uint32
                 break;
             if (leader && !withheld(p.withhold, it)) {
                 ptx::bar_arrive_expect_tx(bar(S::kVFull + stage), S::kTileBytes);
-                load_kv_tile<D, VARLEN>(tv, sbase + S::kOffV + stage * S::kTileBytes, bar(S::kVFull + stage), wk, j,
-                                        p.H);
+                load_kv_tile<D, VARLEN, WIN>(tv, sbase + S::kOffV + stage * S::kTileBytes, bar(S::kVFull + stage), wk,
+                                             j, p);
             }
         }
     }
@@ -379,7 +431,7 @@ __device__ void fwd_producer_v(const CUtensorMap *tv, const FwdParams &p, uint32
     }
 }
 
-template <int D, bool BF16, bool CAUSAL, bool VARLEN>
+template <int D, bool BF16, bool CAUSAL, bool VARLEN, bool WIN>
 __device__ void fwd_mma(const FwdParams &p, uint32_t sbase, uint32_t tmem, volatile int *abort_flag) {
     using S = FwdShape<D>;
     const uint32_t sched = sbase + S::kOffSched;
@@ -429,7 +481,7 @@ __device__ void fwd_mma(const FwdParams &p, uint32_t sbase, uint32_t tmem, volat
     for (int r = 0; ok; ++r) {
         const int w = work_index(r);
         if (w >= num_items<VARLEN>(p, sched)) break;
-        const Work wk = get_work<CAUSAL, VARLEN>(p, r, sched);
+        const Work wk = get_work<CAUSAL, VARLEN, WIN>(p, r, sched);
         if (wk.n_kv_max == 0) continue;
         if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kQFull), wi & 1, abort_flag, p.timeout_ns)))) break;
         if (wi == 0 && leader) ptx::bar_arrive(bar(S::kFirstQ));  // releases the V producer's ring fill
@@ -440,7 +492,7 @@ __device__ void fwd_mma(const FwdParams &p, uint32_t sbase, uint32_t tmem, volat
             ptx::tc_fence_after();
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                if (wk.n_kv[t] == 0) continue;
+                if (!visits<WIN>(wk, t, 0)) continue;
                 if (leader) {
                     issue_qk(t, ks);
                     ptx::mma_commit(bar(S::kSFull + t));
@@ -452,6 +504,7 @@ __device__ void fwd_mma(const FwdParams &p, uint32_t sbase, uint32_t tmem, volat
             // this item's last P V products run.
             if (wk.n_kv_max == 1 && leader) ptx::mma_commit(bar(S::kQEmpty));
         }
+        int done[2] = {0, 0};  // P V steps of this item per query tile (WIN: not j, where a tile skips steps)
         for (int j = 0; j < wk.n_kv_max && ok; ++j) {
             const uint32_t itj = it + j;
             const uint32_t vs = itj % S::kVStages;
@@ -459,27 +512,33 @@ __device__ void fwd_mma(const FwdParams &p, uint32_t sbase, uint32_t tmem, volat
             bool v_ready = false, k_next_used = false;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                if (j >= wk.n_kv[t]) continue;
-                if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kPFull + t), cnt[t] & 1, abort_flag, p.timeout_ns)))) break;
-                if (!v_ready) {
-                    if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kVFull + vs), (itj / S::kVStages) & 1, abort_flag,
-                                             p.timeout_ns))))
+                const bool here = visits<WIN>(wk, t, j);
+                if (!WIN && !here) continue;
+                if (here) {
+                    if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kPFull + t), cnt[t] & 1, abort_flag, p.timeout_ns))))
                         break;
-                    v_ready = true;
+                    if (!v_ready) {
+                        if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kVFull + vs), (itj / S::kVStages) & 1, abort_flag,
+                                                 p.timeout_ns))))
+                            break;
+                        v_ready = true;
+                    }
+                    ptx::tc_fence_after();
+                    const int n_done = WIN ? done[t] : j;
+                    if (leader) issue_pv(t, vs, n_done > 0, 0);
+                    // the second half of P V once the softmax has published keys [64,128)
+                    if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kPFull2 + t), cnt[t] & 1, abort_flag, p.timeout_ns))))
+                        break;
+                    ptx::tc_fence_after();
+                    if (leader) {
+                        issue_pv(t, vs, true, 1);
+                        // the epilogue needs the last product; earlier ones are covered by S_FULL
+                        if (n_done + 1 == wk.n_kv[t]) ptx::mma_commit(bar(S::kODone + t));
+                    }
+                    ++cnt[t];
+                    if (WIN) ++done[t];
                 }
-                ptx::tc_fence_after();
-                if (leader) issue_pv(t, vs, j > 0, 0);
-                // the second half of P V once the softmax has published keys [64,128)
-                if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kPFull2 + t), cnt[t] & 1, abort_flag, p.timeout_ns))))
-                    break;
-                ptx::tc_fence_after();
-                if (leader) {
-                    issue_pv(t, vs, true, 1);
-                    // the epilogue needs the last product; earlier ones are covered by S_FULL
-                    if (j + 1 == wk.n_kv[t]) ptx::mma_commit(bar(S::kODone + t));
-                }
-                ++cnt[t];
-                if (j + 1 < wk.n_kv[t]) {
+                if (WIN ? (j + 1 < wk.n_kv_max && visits<WIN>(wk, t, j + 1)) : (j + 1 < wk.n_kv[t])) {
                     if (!k_next_used) {
                         if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kKFull + kn), ((itj + 1) / S::kKStages) & 1, abort_flag,
                                                  p.timeout_ns))))
@@ -510,7 +569,7 @@ __device__ void fwd_mma(const FwdParams &p, uint32_t sbase, uint32_t tmem, volat
     ptx::bar_wait(bar(S::kTeardown), 0, nullptr, p.timeout_ns);
 }
 
-template <int D, bool BF16, bool CAUSAL, bool VARLEN>
+template <int D, bool BF16, bool CAUSAL, bool VARLEN, bool WIN>
 __device__ void fwd_softmax(const FwdParams &p, uint32_t sbase, uint32_t tmem, int t, int wq, int lane,
                             volatile int *abort_flag) {
     using S = FwdShape<D>;
@@ -532,7 +591,7 @@ __device__ void fwd_softmax(const FwdParams &p, uint32_t sbase, uint32_t tmem, i
     for (int r = 0; ok; ++r) {
         const int w = work_index(r);
         if (w >= num_items<VARLEN>(p, sched)) break;
-        const Work wk = get_work<CAUSAL, VARLEN>(p, r, sched);
+        const Work wk = get_work<CAUSAL, VARLEN, WIN>(p, r, sched);
         if (wk.rows[t] == 0) continue;
         const int q_row = wk.q_start[t] + row;
         const bool row_valid = row < wk.rows[t];
@@ -540,7 +599,10 @@ __device__ void fwd_softmax(const FwdParams &p, uint32_t sbase, uint32_t tmem, i
         float m_used = -CUDART_INF_F;  // running max in base-2 units of the scaled score
         float l = 0.f;
 
-        for (int j = 0; j < nkv; ++j) {
+        bool first = true;             // no tile of this item consumed yet
+        const int steps = WIN ? wk.n_kv_max : nkv;
+        for (int j = 0; j < steps; ++j) {
+            if (WIN && !visits<WIN>(wk, t, j)) continue;
             ok = ptx::bar_wait(bar(S::kSFull + t), cnt & 1, abort_flag, p.timeout_ns);
             if (!__all_sync(kFull, ok)) { ok = false; break; }
             ptx::tc_fence_after();
@@ -548,8 +610,12 @@ __device__ void fwd_softmax(const FwdParams &p, uint32_t sbase, uint32_t tmem, i
             // the sequence ends at Lk and, causal, the row sees keys up to its
             // own position. Tiles inside both limits (need_mask false, the
             // same for the whole warpgroup) are not tested.
-            const int k0 = j * kBlockN;
+            const int k0 = kv_tile<WIN>(wk, j) * kBlockN;
             const bool need_mask = (k0 + kBlockN > wk.Lk) || (CAUSAL && k0 + kBlockN - 1 > wk.q_start[t]);
+            // With a window the row also loses the columns c with sk <= c < wl:
+            // keys behind its window that are no sinks. The tile's last row
+            // loses the most.
+            const bool need_lo = WIN && k0 + kBlockN > p.sinks && k0 <= wk.q_start[t] + wk.rows[t] - 1 - p.window;
             // The row maximum comes with the loads (one wait for all four).
             uint32_t s[4][32];
             float mx4[4];
@@ -561,13 +627,21 @@ __device__ void fwd_softmax(const FwdParams &p, uint32_t sbase, uint32_t tmem, i
                 ptx::reg_fence(s[c]);
                 asm volatile("" : "+f"(mx4[c]));
             }
-            if (need_mask) {
+            if (need_mask || need_lo) {
                 // masked tile: the maximum is taken again after the mask
-                int lim = wk.Lk - k0;
-                if (CAUSAL) lim = min(lim, q_row + 1 - k0);
+                if (!WIN || need_mask) {
+                    int lim = wk.Lk - k0;
+                    if (CAUSAL) lim = min(lim, q_row + 1 - k0);
 #pragma unroll
-                for (int c = 0; c < kBlockN; ++c)
-                    if (c >= lim) s[c / 32][c % 32] = 0xff800000u;  // -inf
+                    for (int c = 0; c < kBlockN; ++c)
+                        if (c >= lim) s[c / 32][c % 32] = 0xff800000u;  // -inf
+                }
+                if (WIN && need_lo) {
+                    const int wl = q_row - p.window + 1 - k0, sk = p.sinks - k0;
+#pragma unroll
+                    for (int c = 0; c < kBlockN; ++c)
+                        if (c >= sk && c < wl) s[c / 32][c % 32] = 0xff800000u;
+                }
 #pragma unroll
                 for (int c = 0; c < 4; ++c) mx4[c] = -CUDART_INF_F;
 #pragma unroll
@@ -613,7 +687,7 @@ __device__ void fwd_softmax(const FwdParams &p, uint32_t sbase, uint32_t tmem, i
                 // (only when a row of this warp moved its maximum). The previous
                 // P V has landed: Q K^T j was issued after it, and S_FULL tracks
                 // every MMA issued before that Q K^T.
-                if (h == 0 && j > 0 && __any_sync(kFull, need)) {
+                if (h == 0 && (WIN ? !first : j > 0) && __any_sync(kFull, need)) {
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
@@ -637,6 +711,7 @@ __device__ void fwd_softmax(const FwdParams &p, uint32_t sbase, uint32_t tmem, i
                 l += (a0 + a1) + (b0 + b1);
             }
             ++cnt;
+            first = false;
         }
         if (!ok) break;
 
@@ -703,7 +778,7 @@ __device__ void fwd_softmax(const FwdParams &p, uint32_t sbase, uint32_t tmem, i
 
 // ----------------------------------------------------------------- kernel --
 
-template <int D, bool BF16, bool CAUSAL, bool VARLEN>
+template <int D, bool BF16, bool CAUSAL, bool VARLEN, bool WIN>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
@@ -787,7 +862,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const bool mine = rounds <= VarlenSched::kMaxRecs && r < rounds && work_index(r) < items;
             int pair = 0;
             Work wk{};
-            if (mine) wk = resolve_work<CAUSAL, VARLEN>(p, work_index(r), sbase + S::kOffSched, &pair);
+            if (mine) wk = resolve_work<CAUSAL, VARLEN, WIN>(p, work_index(r), sbase + S::kOffSched, &pair);
             __syncthreads();
             if (mine) {
                 int *rec = sch + VarlenSched::kRec0 + VarlenSched::kRecInts * r;
@@ -814,14 +889,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // Whole warps run the producer and MMA loops (uniform control flow and
         // operands); the TMA, MMA and commit instructions come from one elected lane.
         if (warp == 0) {
-            fwd_producer_qk<D, CAUSAL, VARLEN>(&tm_q, &tm_k, p, sbase, abort_flag);
+            fwd_producer_qk<D, CAUSAL, VARLEN, WIN>(&tm_q, &tm_k, p, sbase, abort_flag);
         } else if (warp == 1) {
-            fwd_mma<D, BF16, CAUSAL, VARLEN>(p, sbase, tmem, abort_flag);
+            fwd_mma<D, BF16, CAUSAL, VARLEN, WIN>(p, sbase, tmem, abort_flag);
         } else if (warp == 2) {
-            fwd_producer_v<D, CAUSAL, VARLEN>(&tm_v, p, sbase, abort_flag);
+            fwd_producer_v<D, CAUSAL, VARLEN, WIN>(&tm_v, p, sbase, abort_flag);
         }
     } else {
-        fwd_softmax<D, BF16, CAUSAL, VARLEN>(p, sbase, tmem, (warp - 4) / 4, warp % 4, lane, abort_flag);
+        fwd_softmax<D, BF16, CAUSAL, VARLEN, WIN>(p, sbase, tmem, (warp - 4) / 4, warp % 4, lane, abort_flag);
     }
 
     ptx::tc_fence_before();
@@ -834,9 +909,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (threadIdx.x == 0 && *abort_flag) atomicExch(p.err, kDeviceErrTimeout);
 }
 
-template <int D, bool BF16, bool CAUSAL, bool VARLEN>
+template <int D, bool BF16, bool CAUSAL, bool VARLEN, bool WIN = false>
 cudaError_t launch_fwd_t(const CUtensorMap *maps, const FwdParams &p, int grid, cudaStream_t stream) {
-    auto kern = fa_fwd_kernel<D, BF16, CAUSAL, VARLEN>;
+    auto kern = fa_fwd_kernel<D, BF16, CAUSAL, VARLEN, WIN>;
     constexpr int kSmem = FwdShape<D>::kSmemBytes;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;

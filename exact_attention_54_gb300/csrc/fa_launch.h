@@ -38,6 +38,8 @@ struct FwdParams {
     int *err;              // device error word
     unsigned long long timeout_ns;
     int withhold;          // test support, 0 = off: CTA 0 never issues its V tile load number withhold - 1
+    int window, sinks;     // sliding window only: keys a query sees back to itself; first keys always visible
+    int group;             // sliding window only: query heads per key head
 };
 
 int fwd_smem_bytes(int D);
@@ -104,6 +106,9 @@ struct BwdParams {
     int *work_counter;     // D = 128: next work unit to hand out (in the workspace, zeroed by the prep kernel)
     int total_units;       // D = 128: work units of the launch (BH * n_ktiles)
     int grid;              // D = 128: persistent CTAs (at most one per SM)
+    int window, sinks;     // sliding window only: keys a query sees back to itself; first keys always visible
+    int group;             // sliding window only: query heads per key head
+    int units;             // sliding window only: key heads (dense B*Hkv, packed num_seqs*Hkv) that key tiles belong to
 };
 
 // Test support: a launch that withholds one load (see FwdParams::withhold)
@@ -121,11 +126,20 @@ cudaError_t launch_bwd_dense(int D, bool bf16, bool causal, const CUtensorMap *m
 cudaError_t launch_bwd_varlen(int D, bool bf16, bool causal, const CUtensorMap *maps, const void *o,
                               const void *dout, const float *lse, void *dq, const BwdParams &p, cudaStream_t stream);
 
+// Sliding window and sinks, shared key heads: maps as above, K and V maps over
+// H / p.group heads; p.BH and p.H count query heads.
+cudaError_t launch_bwd_window(int D, bool bf16, bool varlen, const CUtensorMap *maps, const void *o,
+                              const void *dout, const float *lse, void *dq, const BwdParams &p, cudaStream_t stream);
+
 // maps: {Q, K, V} tensor maps (see fa_api.cu for their geometry).
 cudaError_t launch_fwd_dense(int D, bool bf16, bool causal, const CUtensorMap *maps,
                              const FwdParams &p, int grid, cudaStream_t stream);
 cudaError_t launch_fwd_varlen(int D, bool bf16, bool causal, const CUtensorMap *maps,
                               const FwdParams &p, int grid, cudaStream_t stream);
+// Sliding window and sinks, shared key heads (D = 64, 128): maps as above, K
+// and V maps over H / p.group heads.
+cudaError_t launch_fwd_window(int D, bool bf16, bool varlen, const CUtensorMap *maps, const FwdParams &p, int grid,
+                              cudaStream_t stream);
 // D = 256: one query tile per work item; maps: Q boxes of 128 rows, K/V boxes of 64.
 cudaError_t launch_fwd_d256(bool bf16, bool causal, bool varlen, const CUtensorMap *maps, const FwdParams &p,
                             int grid, cudaStream_t stream);

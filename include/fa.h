@@ -9,6 +9,9 @@
  *   fa_decode_splitkv_fused, fa_decode_paged_splitkv_fused
  *                      both phases in one launch (last partition merges).
  *   fa_bwd             backward pass: dQ, dK, dV from dO and the forward LSE.
+ *   fa_fwd_window, fa_bwd_window (and _varlen)
+ *                      forward and backward with a sliding window, sinks and
+ *                      shared key heads.
  *   fa_kv_write_q4, fa_kv_read_q4
  *                      keys and values into a paged 4-bit cache, and back.
  *   fa_decode_paged_window, fa_decode_paged_q4
@@ -331,6 +334,65 @@ FA_API fa_status_t fa_bwd_varlen(const void *q, const void *k, const void *v, co
                                  const int32_t *cu_seqlens_k, int num_seqs, int total_q, int total_k,
                                  int max_seqlen_q, int max_seqlen_k, int H, int D, int causal, float scale,
                                  fa_dtype_t dtype, void *stream);
+
+/*
+ * fa_fwd_window - fa_fwd with a sliding window, sinks and shared key heads.
+ *
+ * Query i sees key j if j <= i (top-left, as fa_fwd's causal rule) and either
+ * i - j < window or j < sinks: its own key and the window - 1 before it, and
+ * the first `sinks` keys. window >= 1, sinks >= 0; a window of Sq or more is
+ * plain causal attention. Key tiles that no query of a tile sees are not read,
+ * so the work grows with Sq * (window + sinks).
+ *
+ *   q, o [B,H,Sq,D], lse [B,H,Sq], k, v [B,Hkv,Sk,D] as in fa_fwd; query head
+ *   h reads key head h / (H / Hkv); Hkv divides H; D is 64 or 128.
+ * A query that sees no key (Sq > Sk, beyond the window) gets o = 0 and
+ * lse = -inf. Hidden keys and values must be finite: a tile that a query sees
+ * in part is multiplied whole, with zero weights.
+ * Errors: as fa_fwd; FA_ERR_SHAPE also when Hkv does not divide H, window < 1,
+ * sinks < 0, or a length is above 2^29.
+ */
+FA_API fa_status_t fa_fwd_window(const void *q, const void *k, const void *v, void *o, float *lse, int B, int H,
+                                 int Hkv, int Sq, int Sk, int D, int window, int sinks, float scale,
+                                 fa_dtype_t dtype, void *stream);
+
+/*
+ * fa_fwd_window_varlen - fa_fwd_window over packed sequences: arguments and
+ * device-side checks as fa_fwd_varlen (positions, the window and the sinks
+ * count from each sequence's start), k and v [total_k,Hkv,D].
+ * Errors: as fa_fwd_varlen and fa_fwd_window.
+ */
+FA_API fa_status_t fa_fwd_window_varlen(const void *q, const void *k, const void *v, void *o, float *lse,
+                                        const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int num_seqs,
+                                        int total_q, int total_k, int max_seqlen_q, int H, int Hkv, int D,
+                                        int window, int sinks, float scale, fa_dtype_t dtype, void *stream);
+
+/*
+ * fa_bwd_window - the gradients of fa_fwd_window, as fa_bwd computes those of
+ * fa_fwd: dq [B,H,Sq,D], and dk, dv [B,Hkv,Sk,D] summed over the query heads
+ * that share a key head. workspace: at least fa_bwd_workspace_bytes(B, H, Sq,
+ * D) bytes, as for fa_bwd. Queries that see no key get dq = 0, keys that no
+ * query sees dk = dv = 0. dk and dv are deterministic, dq rounds as in fa_bwd.
+ * Errors: as fa_bwd and fa_fwd_window.
+ */
+FA_API fa_status_t fa_bwd_window(const void *q, const void *k, const void *v, const void *o, const void *dout,
+                                 const float *lse, void *dq, void *dk, void *dv, float *workspace,
+                                 size_t workspace_bytes, int B, int H, int Hkv, int Sq, int Sk, int D, int window,
+                                 int sinks, float scale, fa_dtype_t dtype, void *stream);
+
+/*
+ * fa_bwd_window_varlen - the gradients of fa_fwd_window_varlen: arguments,
+ * device-side checks and rows outside the sequences as fa_bwd_varlen, the
+ * workspace of fa_bwd_varlen_workspace_bytes(total_q, H, D), dk and dv
+ * [total_k,Hkv,D].
+ * Errors: as fa_bwd_varlen and fa_fwd_window.
+ */
+FA_API fa_status_t fa_bwd_window_varlen(const void *q, const void *k, const void *v, const void *o, const void *dout,
+                                        const float *lse, void *dq, void *dk, void *dv, float *workspace,
+                                        size_t workspace_bytes, const int32_t *cu_seqlens_q,
+                                        const int32_t *cu_seqlens_k, int num_seqs, int total_q, int total_k,
+                                        int max_seqlen_q, int max_seqlen_k, int H, int Hkv, int D, int window,
+                                        int sinks, float scale, fa_dtype_t dtype, void *stream);
 
 /*
  * The paged 4-bit cache of keys and values (fa_kv_write_q4, fa_kv_read_q4,

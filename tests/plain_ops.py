@@ -116,3 +116,65 @@ def assert_attention_close(o, lse, ro, rl, size, dtype, what=""):
     off = (lse - rl).abs()[~empty & ~torch.isnan(rl)]
     room = (4e-5 + 2.0 ** -21 * rl.abs())[~empty & ~torch.isnan(rl)]
     assert (off <= room).all(), (what, "lse", float(off.max()))
+
+
+# ----------------------------------------------------------- window, whole --
+
+def window_attention(q, k, v, window, sinks, scale, dout=None, dtype=torch.bfloat16):
+    """One sequence: q [H,Sq,D], k and v [Hkv,Sk,D] -> dict of doubles: o, lse, and with dout [H,Sq,D] also dq, dk,
+    dv; each of them but lse with "<name>_bound", the largest error that the kernels' roundings allow.
+
+    Roundings, each by at most h = half a step of the 16-bit type (relative): every output once; P before P V and
+    before P^T dO; dS = P (dP - D_i), of the rounded P, before dS^T Q and dS K; O before D_i = dO . O. Beside them P
+    carries 2^-13 relative (scores, LSE and 2^x in fp32, as in assert_attention_close), and sums of fp32 products
+    2^-18 of what meets in them."""
+    H, Sq, D = q.shape
+    Hkv, Sk, _ = k.shape
+    G, h, e = H // Hkv, half_step(dtype), 2.0 ** -13
+    tiny = torch.finfo(dtype).smallest_normal * 2 * h
+    q, k, v = q.double(), k.double(), v.double()
+    seen = visible(Sq, Sk, window, sinks)
+    r = {n: torch.zeros_like(x) for n, x in (("o", q), ("dq", q), ("dk", k), ("dv", v))}
+    r.update({n + "_bound": torch.zeros_like(x) for n, x in list(r.items())})
+    r["lse"] = torch.zeros(H, Sq, dtype=torch.float64)
+    for x in range(H):
+        y = x // G
+        o, lse, p, size = softmax_attention(q[x], k[y], v[y], seen, scale)
+        r["o"][x], r["lse"][x] = o, lse
+        o_err = h * o.abs() * (1 + 2 * h) + (h * (1 + h) + e) * size + tiny
+        r["o_bound"][x] = o_err
+        if dout is None:
+            continue
+        do = dout[x].double()
+        dp, di = do @ v[y].t(), (do * o).sum(-1, keepdim=True)
+        ds = p * (dp - di)
+        di_err = (do.abs() * o_err).sum(-1, keepdim=True) + 2.0 ** -18 * (do * o).abs().sum(-1, keepdim=True)
+        dp_err = 2.0 ** -18 * (do.abs() @ v[y].abs().t())
+        # fp16 loses relative precision below its normal numbers: P and dS are off by up to tiny there
+        p_err = p * (h + e) * (1 + h) + tiny * seen
+        ds_err = (p + p_err) * (di_err + dp_err) + p_err * (dp - di).abs() + h * ds.abs() * (1 + 4 * h) + tiny * seen
+        r["dq"][x] = scale * ds @ k[y]
+        r["dk"][y] += scale * ds.t() @ q[x]
+        r["dv"][y] += p.t() @ do
+        r["dq_bound"][x] = scale * (ds_err + 2.0 ** -18 * ds.abs()) @ k[y].abs()
+        r["dk_bound"][y] += scale * (ds_err + 2.0 ** -18 * ds.abs()).t() @ q[x].abs()
+        r["dv_bound"][y] += (p_err + 2.0 ** -18 * p).t() @ do.abs()
+    for n in ("dq", "dk", "dv"):
+        r[n + "_bound"] += h * r[n].abs() * (1 + 4 * h) + h * r[n + "_bound"] + tiny
+    return r
+
+
+def assert_window_close(got, ref, what=""):
+    """``got``: dict of tensors of one sequence by the names of window_attention."""
+    for n, x in got.items():
+        x, y = x.double().cpu(), ref[n]
+        assert x.shape == y.shape, (what, n, x.shape, y.shape)
+        if n == "lse":
+            empty = torch.isinf(y)
+            assert torch.equal(empty, torch.isinf(x)) and torch.equal(x[empty], y[empty]), (what, n)
+            off, room = (x - y).abs()[~empty], (4e-5 + 2.0 ** -21 * y.abs())[~empty]
+            assert (off <= room).all(), (what, n, float(off.max()))
+            continue
+        bad = ~((x - y).abs() <= ref[n + "_bound"])
+        assert not bad.any(), (what, n, torch.nonzero(bad)[0].tolist(),
+                               float(((x - y).abs() / ref[n + "_bound"]).max()), int(bad.sum()))
