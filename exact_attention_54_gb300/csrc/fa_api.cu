@@ -888,7 +888,7 @@ static fa_status_t decode_gqa(bool q4, const void *q, const void *k, const void 
     p.scale_log2 = scale * kLog2e;
     p.err = device_error_word();
     if (p.err == nullptr) return FA_ERR_CUDA;
-    const cudaError_t e = fa::launch_decode_gqa(D, dtype == FA_BF16, q4, p, B * Hkv * num_splits,
+    const cudaError_t e = fa::launch_decode_gqa(D, dtype == FA_BF16, q4, p, B,
                                                 static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -189,7 +189,7 @@ struct GqaDecodeParams {
     float *o_part, *m_part, *l_part;  // [B, H, num_splits(, D)]
     void *o;                    // [B, H, D]
     float *lse;                 // [B, H]
-    int *counters;              // [B * H], the first B * Hkv are used: zero between calls
+    int *counters;              // [B * H], one per key head and head tile: zero between calls
     const int *block_table;     // [B, max_blocks]
     const int *seq_lens;        // [B]
     int H, Hkv, group;          // query heads, key heads, H / Hkv
@@ -200,7 +200,7 @@ struct GqaDecodeParams {
     int *err;                   // device error word
 };
 
-cudaError_t launch_decode_gqa(int D, bool bf16, bool q4, const GqaDecodeParams &p, int grid, cudaStream_t stream);
+cudaError_t launch_decode_gqa(int D, bool bf16, bool q4, const GqaDecodeParams &p, int B, cudaStream_t stream);
 // Partitions that fill `sms` SMs (fa_decode_splits).
 int decode_gqa_splits(int sms, int B, int H, int Hkv, int max_keys);
 

@@ -76,8 +76,8 @@ def softmax_attention(q, k, v, seen, scale):
 
 
 def decode(q, values, table, lens, block, window, sinks, scale):
-    """q [B,H,1,D]; values(page, head) -> (k, v) double [block, D] of one page; the definition of the paged decode.
-    Returns o [B,H,D], lse [B,H] and sum p|v| [B,H,D]."""
+    """q [B,H,1,D]; values(page, head) -> (k, v, s) double [block, D] of one page, s the value's scale (4-bit cache) or
+    0; the definition of the paged decode. Returns o [B,H,D], lse [B,H] and what meets in o: sum p (|v| + s / 4)."""
     B, H, _, D = q.shape
     o, size = torch.zeros(B, H, D, dtype=torch.float64), torch.zeros(B, H, D, dtype=torch.float64)
     lse = torch.full((B, H), -math.inf, dtype=torch.float64)
@@ -91,8 +91,9 @@ def decode(q, values, table, lens, block, window, sinks, scale):
             pages = {int(x): values(int(table[b, x]), h) for x in torch.unique(keys // block)}
             k = torch.stack([pages[int(j) // block][0][int(j) % block] for j in keys])
             v = torch.stack([pages[int(j) // block][1][int(j) % block] for j in keys])
+            step = torch.stack([pages[int(j) // block][2][int(j) % block] for j in keys])
             r = softmax_attention(q[b, h].double(), k, v, torch.ones(1, len(keys), dtype=torch.bool), scale)
-            o[b, h], lse[b, h], size[b, h] = r[0][0], r[1][0], r[3][0]
+            o[b, h], lse[b, h], size[b, h] = r[0][0], r[1][0], r[3][0] + (r[2] @ step)[0] / 4
     return o, lse, size
 
 
@@ -103,7 +104,11 @@ def assert_attention_close(o, lse, ro, rl, size, dtype, what=""):
     The rest: a score is an fp32 sum of D products, |error| <= 2^-24 * 16 * sum |q k| scale (16: depth of the
     sums), under 2^-24 * 16 * 40 = 2^-14.7 for the inputs here; it enters a weight as a relative error, once in
     the numerator and once in the sum; 2^x and the fp32 sums add a few 2^-22. LSE carries the score's error and
-    the rounding of its own value (fp32, two operations)."""
+    the rounding of its own value (fp32, two operations).
+
+    The 4-bit cache's sum of s n is taken as that of s (n + 8) less 8 times that of s: its fp32 terms are up to 23 s
+    where n may be 0. A warp adds up to 11 tiles of 16 keys there, each time off by at most 2^-23 of the partial
+    sum: 11 * 23 * 2^-23 < 2^-15 of sum p s, the 2^-13 of ``size``'s sum p s / 4."""
     o, lse = o.double().cpu().reshape(ro.shape), lse.double().cpu().reshape(rl.shape)
     assert torch.equal(torch.isnan(o), torch.isnan(ro)) and torch.equal(torch.isnan(lse), torch.isnan(rl)), what
     h = half_step(dtype)

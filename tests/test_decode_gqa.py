@@ -108,8 +108,10 @@ def values(cache, q4, G):
     def f(page, h):
         if q4:
             return (plain_ops.q4_values(cache[0][page, h // G], cache[1][page, h // G]),
-                    plain_ops.q4_values(cache[2][page, h // G], cache[3][page, h // G]))
-        return cache[0][page, h // G].double(), cache[1][page, h // G].double()
+                    plain_ops.q4_values(cache[2][page, h // G], cache[3][page, h // G]),
+                    cache[3][page, h // G].double().repeat_interleave(32, -1))
+        v = cache[1][page, h // G].double()
+        return cache[0][page, h // G].double(), v, torch.zeros_like(v)
     return f
 
 
