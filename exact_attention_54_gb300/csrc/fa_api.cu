@@ -879,6 +879,7 @@ static fa_status_t decode_gqa(bool q4, const void *q, const void *k, const void 
     p.H = H;
     p.Hkv = Hkv;
     p.group = H / Hkv;
+    p.B = B;
     p.num_splits = num_splits;
     p.window = window;
     p.sinks = sinks;
@@ -887,9 +888,11 @@ static fa_status_t decode_gqa(bool q4, const void *q, const void *k, const void 
     p.num_blocks = num_blocks;
     p.scale_log2 = scale * kLog2e;
     p.err = device_error_word();
-    if (p.err == nullptr) return FA_ERR_CUDA;
-    const cudaError_t e = fa::launch_decode_gqa(D, dtype == FA_BF16, q4, p, B,
-                                                static_cast<cudaStream_t>(stream));
+    const int sms = num_sms();
+    if (p.err == nullptr || sms <= 0) return FA_ERR_CUDA;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = q4 ? fa::launch_decode_q4(D, dtype == FA_BF16, p, sms, st)
+                             : fa::launch_decode_window(D, dtype == FA_BF16, p, sms, st);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

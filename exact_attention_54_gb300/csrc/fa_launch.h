@@ -192,7 +192,8 @@ struct GqaDecodeParams {
     int *counters;              // [B * H], one per key head and head tile: zero between calls
     const int *block_table;     // [B, max_blocks]
     const int *seq_lens;        // [B]
-    int H, Hkv, group;          // query heads, key heads, H / Hkv
+    int B, H, Hkv, group;       // sequences, query heads, key heads, H / Hkv
+    bool balanced;              // the plan (set by decode_gqa_grid)
     int num_splits;
     int window, sinks;          // window 0: every key is visible
     int max_blocks, log2_bs, num_blocks;
@@ -200,7 +201,11 @@ struct GqaDecodeParams {
     int *err;                   // device error word
 };
 
-cudaError_t launch_decode_gqa(int D, bool bf16, bool q4, const GqaDecodeParams &p, int B, cudaStream_t stream);
+cudaError_t launch_decode_window(int D, bool bf16, GqaDecodeParams p, int sms, cudaStream_t stream);
+cudaError_t launch_decode_q4(int D, bool bf16, GqaDecodeParams p, int sms, cudaStream_t stream);
+// CTAs of either launch: a wave of ctas_per_sm per SM where the balanced plan
+// serves, else one per unit (heads_per_unit query heads) and partition (sets p.balanced).
+unsigned decode_gqa_grid(GqaDecodeParams &p, int sms, int ctas_per_sm, int heads_per_unit);
 // Partitions that fill `sms` SMs (fa_decode_splits).
 int decode_gqa_splits(int sms, int B, int H, int Hkv, int max_keys);
 
