@@ -423,6 +423,8 @@ def fa_decode_noalloc(q, k, v, o, lse, num_splits: int, scale: float | None = No
 
 def _expect(name: str, t, shape, dtype):
     """Refuse a tensor that is not a contiguous one of this shape and dtype (None in ``shape``: any size)."""
+    if t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
@@ -431,20 +433,29 @@ def _expect(name: str, t, shape, dtype):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _launch(fn: str, stream, args, first, *others):
-    """Call entry point ``fn`` with ``args`` and the stream, on the device that all the tensors share."""
-    dev = first.device
-    if dev.type != "cuda" or any(t.device != dev for t in others if t is not None):
+_entry = {}  # entry points of the loaded library by name
+
+
+def _launch(fn: str, stream, args, tensors):
+    """Call entry point ``fn`` with ``args`` and the stream, on the device that all of ``tensors`` (None: skipped)
+    share."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            dev = -1
+    if dev < 0:
         raise ValueError(f"{fn}: all tensors must be on one CUDA device")
-    call = getattr(load_library(), fn)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if torch.cuda.current_device() != dev.index:
+    call = _entry.get(fn)
+    if call is None:
+        call = _entry[fn] = getattr(load_library(), fn)
+    st = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+    if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
-            st = call(*args, _stream(stream))
+            st = call(*args, st)
     else:
-        st = call(*args, _stream(stream))
-    _check(fn, st)
+        st = call(*args, st)
+    if st != 0:
+        _check(fn, st)
 
 
 def fa_fwd_window(q, k, v, o, lse, window: int, sinks: int = 0, scale: float | None = None, stream=None):
@@ -461,7 +472,7 @@ def fa_fwd_window(q, k, v, o, lse, window: int, sinks: int = 0, scale: float | N
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     ts = (q, k, v, o, lse)
     _launch("fa_fwd_window", stream, (*map(_ptr, ts), B, H, Hkv, Sq, Sk, D, int(window), int(sinks), float(scale),
-                                      code), *ts)
+                                      code), ts)
 
 
 def fa_fwd_window_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, window: int, sinks: int = 0,
@@ -481,7 +492,7 @@ def fa_fwd_window_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     ts = (q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k)
     _launch("fa_fwd_window_varlen", stream, (*map(_ptr, ts), n, Tq, Tk, int(max_seqlen_q), H, Hkv, D, int(window),
-                                             int(sinks), float(scale), code), *ts)
+                                             int(sinks), float(scale), code), ts)
 
 
 def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sinks: int = 0,
@@ -502,7 +513,7 @@ def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sin
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     ts = (q, k, v, o, dout, lse, dq, dk, dv, workspace)
     _launch("fa_bwd_window", stream, (*map(_ptr, ts), workspace.numel() * workspace.element_size(), B, H, Hkv, Sq, Sk,
-                                      D, int(window), int(sinks), float(scale), code), *ts)
+                                      D, int(window), int(sinks), float(scale), code), ts)
 
 
 def fa_bwd_window_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
@@ -528,7 +539,7 @@ def fa_bwd_window_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlen
     _launch("fa_bwd_window_varlen", stream,
             (*map(_ptr, ts), workspace.numel() * workspace.element_size(), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), n,
              Tq, Tk, int(max_seqlen_q), int(max_seqlen_k), H, Hkv, D, int(window), int(sinks), float(scale), code),
-            *ts, cu_seqlens_q, cu_seqlens_k)
+            (*ts, cu_seqlens_q, cu_seqlens_k))
 
 
 def flash_attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None, stream=None):
@@ -607,12 +618,12 @@ def _kv_q4(fn, k, v, cache, block_table, cu_seqlens, max_seqlen, starts, stream)
     num_blocks, block_size = _check_q4(*cache, Hkv, D, k.dtype)
     n = cu_seqlens.numel() - 1
     _expect("cu_seqlens", cu_seqlens, (n + 1,), torch.int32)
-    _expect("block_table", block_table, (n, None), torch.int32)
+    _expect("block_table", block_table, (n, block_table.shape[-1]), torch.int32)
     if starts is not None:
         _expect("starts", starts, (n,), torch.int32)
     args = (_ptr(k), _ptr(v), *map(_ptr, cache), _ptr(block_table), _ptr(cu_seqlens), _ptr(starts), n, total,
             int(max_seqlen), Hkv, D, num_blocks, block_size, block_table.shape[1], code)
-    _launch(fn, stream, args, k, v, *cache, block_table, cu_seqlens, starts)
+    _launch(fn, stream, args, (k, v, *cache, block_table, cu_seqlens, starts))
 
 
 def fa_kv_write_q4(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, max_seqlen: int, starts=None,
@@ -642,7 +653,7 @@ def _decode_gqa(fn, q, cache, page_shape, block_table, seq_lens, o, lse, o_part,
     S = int(num_splits)
     code = _dtype_code(q)
     _expect("q", q, (B, H, 1, D), q.dtype)
-    _expect("block_table", block_table, (B, None), torch.int32)
+    _expect("block_table", block_table, (B, block_table.shape[-1]), torch.int32)
     _expect("seq_lens", seq_lens, (B,), torch.int32)
     _expect("o", o, (B, H, 1, D), q.dtype)
     _expect("lse", lse, (B, H), torch.float32)
@@ -656,7 +667,7 @@ def _decode_gqa(fn, q, cache, page_shape, block_table, seq_lens, o, lse, o_part,
     outs = (o, lse, o_part, m_part, l_part, counters)
     args = (_ptr(q), *map(_ptr, cache), _ptr(block_table), _ptr(seq_lens), *map(_ptr, outs), B, H, Hkv, D, num_blocks,
             block_size, block_table.shape[1], S, int(window), int(sinks), float(scale), code)
-    _launch(fn, stream, args, q, *cache, block_table, seq_lens, *outs)
+    _launch(fn, stream, args, (q, *cache, block_table, seq_lens, *outs))
 
 
 def fa_decode_paged_window(q, k_cache, v_cache, block_table, seq_lens, o, lse, o_part, m_part, l_part, counters,

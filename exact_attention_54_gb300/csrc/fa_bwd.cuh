@@ -1223,6 +1223,10 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
                     if (i + 1 < lo || (WIN && i + 1 >= hi)) e1 = 0.f;
                 }
                 pp[i / 2] = ptx::pack2<BF16>(e0, e1);
+                if constexpr (WIN) {  // for dS, below
+                    sv[i] = __float_as_uint(e0);
+                    sv[i + 1] = __float_as_uint(e1);
+                }
             }
             // P^T over the first 16 of this half's own S^T columns, published
             // at once: dV starts while dS^T is formed
@@ -1237,12 +1241,14 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
             ptx::tmem_ld32(tb + 64 + 32 * h, dpv);
             ptx::tmem_ld_wait();
             ptx::reg_fence(dpv);
-            // dS = P (dP - D_i), with P as rounded for dV
+            // dS = P (dP - D_i), with P as rounded for dV (WIN: with P in fp32,
+            // one rounding less in dQ and dK)
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
                 const float4 dv4 = dq4[i / 4];
                 const float d0 = (i % 4 == 0) ? dv4.x : dv4.z, d1 = (i % 4 == 0) ? dv4.y : dv4.w;
-                const float e0 = ptx::unpack_lo<BF16>(pp[i / 2]), e1 = ptx::unpack_hi<BF16>(pp[i / 2]);
+                const float e0 = WIN ? __uint_as_float(sv[i]) : ptx::unpack_lo<BF16>(pp[i / 2]);
+                const float e1 = WIN ? __uint_as_float(sv[i + 1]) : ptx::unpack_hi<BF16>(pp[i / 2]);
                 dd[i / 2] = ptx::pack2<BF16>(e0 * (__uint_as_float(dpv[i]) - d0),
                                              e1 * (__uint_as_float(dpv[i + 1]) - d1));
             }

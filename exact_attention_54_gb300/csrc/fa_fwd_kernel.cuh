@@ -599,10 +599,9 @@ __device__ void fwd_softmax(const FwdParams &p, uint32_t sbase, uint32_t tmem, i
         float m_used = -CUDART_INF_F;  // running max in base-2 units of the scaled score
         float l = 0.f;
 
-        bool first = true;             // no tile of this item consumed yet
-        const int steps = WIN ? wk.n_kv_max : nkv;
-        for (int j = 0; j < steps; ++j) {
-            if (WIN && !visits<WIN>(wk, t, j)) continue;
+        // WIN: this query tile's own tiles are [0, sink) and, `skip` tiles on, the window's
+        const int sink = WIN ? wk.sink[t] : 0, skip = WIN ? max(wk.wlo[t], sink) - sink : 0;
+        for (int j = 0; j < nkv; ++j) {
             ok = ptx::bar_wait(bar(S::kSFull + t), cnt & 1, abort_flag, p.timeout_ns);
             if (!__all_sync(kFull, ok)) { ok = false; break; }
             ptx::tc_fence_after();
@@ -610,7 +609,7 @@ __device__ void fwd_softmax(const FwdParams &p, uint32_t sbase, uint32_t tmem, i
             // the sequence ends at Lk and, causal, the row sees keys up to its
             // own position. Tiles inside both limits (need_mask false, the
             // same for the whole warpgroup) are not tested.
-            const int k0 = kv_tile<WIN>(wk, j) * kBlockN;
+            const int k0 = (WIN && j >= sink ? j + skip : j) * kBlockN;
             const bool need_mask = (k0 + kBlockN > wk.Lk) || (CAUSAL && k0 + kBlockN - 1 > wk.q_start[t]);
             // With a window the row also loses the columns c with sk <= c < wl:
             // keys behind its window that are no sinks. The tile's last row
@@ -687,7 +686,7 @@ __device__ void fwd_softmax(const FwdParams &p, uint32_t sbase, uint32_t tmem, i
                 // (only when a row of this warp moved its maximum). The previous
                 // P V has landed: Q K^T j was issued after it, and S_FULL tracks
                 // every MMA issued before that Q K^T.
-                if (h == 0 && (WIN ? !first : j > 0) && __any_sync(kFull, need)) {
+                if (h == 0 && j > 0 && __any_sync(kFull, need)) {
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
@@ -711,7 +710,6 @@ __device__ void fwd_softmax(const FwdParams &p, uint32_t sbase, uint32_t tmem, i
                 l += (a0 + a1) + (b0 + b1);
             }
             ++cnt;
-            first = false;
         }
         if (!ok) break;
 
