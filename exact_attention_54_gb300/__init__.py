@@ -27,6 +27,7 @@ __all__ = ["FAError", "fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_decode
            "fa_test_withhold_load",
            "flash_attention", "flash_attention_varlen", "flash_attention_bwd", "flash_attention_varlen_bwd",
            "fa_fwd_window", "fa_fwd_window_varlen", "fa_bwd_window", "fa_bwd_window_varlen",
+           "fa_bwd_window_workspace_bytes", "fa_bwd_window_varlen_workspace_bytes",
            "flash_attention_window", "flash_attention_window_bwd", "flash_attention_window_varlen",
            "flash_attention_window_varlen_bwd",
            "flash_decode", "flash_decode_paged", "fa_kv_write_q4", "fa_kv_read_q4", "fa_decode_paged_window",
@@ -47,6 +48,7 @@ EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_decode_p
                     "fa_bwd_varlen", "fa_bwd_varlen_workspace_bytes", "fa_check_device_error", "fa_status_string",
                     "fa_version", "fa_test_withhold_load", "fa_kv_write_q4", "fa_kv_read_q4", "fa_decode_splits",
                     "fa_fwd_window", "fa_fwd_window_varlen", "fa_bwd_window", "fa_bwd_window_varlen",
+                    "fa_bwd_window_workspace_bytes", "fa_bwd_window_varlen_workspace_bytes",
                     "fa_decode_paged_window", "fa_decode_paged_q4")
 
 
@@ -95,6 +97,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.fa_fwd_window.argtypes = [vp] * 5 + [i] * 8 + [f, i, vp]
         lib.fa_fwd_window_varlen.argtypes = [vp] * 7 + [i] * 9 + [f, i, vp]
         lib.fa_bwd_window.argtypes = [vp] * 10 + [sz] + [i] * 8 + [f, i, vp]
+        lib.fa_bwd_window_workspace_bytes.argtypes = [i] * 8
+        lib.fa_bwd_window_workspace_bytes.restype = sz
+        lib.fa_bwd_window_varlen_workspace_bytes.argtypes = [i] * 9
+        lib.fa_bwd_window_varlen_workspace_bytes.restype = sz
         lib.fa_bwd_window_varlen.argtypes = [vp] * 10 + [sz, vp, vp] + [i] * 10 + [f, i, vp]
         lib.fa_kv_write_q4.argtypes = [vp] * 9 + [i] * 9 + [vp]
         lib.fa_kv_read_q4.argtypes = [vp] * 9 + [i] * 9 + [vp]
@@ -495,10 +501,21 @@ def fa_fwd_window_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen
                                              int(sinks), float(scale), code), ts)
 
 
+def fa_bwd_window_workspace_bytes(B: int, H: int, Hkv: int, Sq: int, Sk: int, D: int, window: int,
+                                  sinks: int = 0) -> int:
+    return int(load_library().fa_bwd_window_workspace_bytes(B, H, Hkv, Sq, Sk, D, window, sinks))
+
+
+def fa_bwd_window_varlen_workspace_bytes(num_seqs: int, total_q: int, max_seqlen_q: int, max_seqlen_k: int, H: int,
+                                         Hkv: int, D: int, window: int, sinks: int = 0) -> int:
+    return int(load_library().fa_bwd_window_varlen_workspace_bytes(num_seqs, total_q, max_seqlen_q, max_seqlen_k, H,
+                                                                   Hkv, D, window, sinks))
+
+
 def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sinks: int = 0,
                   scale: float | None = None, stream=None):
     """Gradients of fa_fwd_window: q, o, dout, dq [B,H,Sq,D]; k, v, dk, dv [B,Hkv,Sk,D]; workspace of at least
-    fa_bwd_workspace_bytes(B, H, Sq, D) bytes."""
+    fa_bwd_window_workspace_bytes(B, H, Hkv, Sq, Sk, D, window, sinks) bytes."""
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B,H,Sq,D] and k, v [B,Hkv,Sk,D]")
     B, H, Sq, D = q.shape
@@ -519,7 +536,7 @@ def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sin
 def fa_bwd_window_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
                          max_seqlen_k: int, window: int, sinks: int = 0, scale: float | None = None, stream=None):
     """Gradients of fa_fwd_window_varlen: q, o, dout, dq [total_q,H,D]; k, v, dk, dv [total_k,Hkv,D]; workspace of at
-    least fa_bwd_varlen_workspace_bytes(total_q, H, D) bytes."""
+    least fa_bwd_window_varlen_workspace_bytes bytes."""
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [total_q,H,D] and k, v [total_k,Hkv,D]")
     Tq, H, D = q.shape
@@ -554,7 +571,11 @@ def flash_attention_window_bwd(q, k, v, o, lse, dout, window: int, sinks: int = 
                                stream=None, workspace=None):
     """Returns (dq, dk, dv) of flash_attention_window, given its o and lse."""
     if workspace is None:
-        workspace = torch.empty(fa_bwd_workspace_bytes(*q.shape) // 4, dtype=torch.float32, device=q.device)
+        if q.dim() != 4 or k.dim() != 4:
+            raise ValueError("q must be [B,H,Sq,D] and k, v [B,Hkv,Sk,D]")
+        (B, H, Sq, D), (_, Hkv, Sk, _) = q.shape, k.shape
+        workspace = torch.empty(fa_bwd_window_workspace_bytes(B, H, Hkv, Sq, Sk, D, window, sinks) // 4,
+                                dtype=torch.float32, device=q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window, sinks, scale, stream)
     return dq, dk, dv
@@ -573,9 +594,13 @@ def flash_attention_window_varlen_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_se
                                       max_seqlen_k: int, window: int, sinks: int = 0, scale: float | None = None,
                                       stream=None, workspace=None):
     """Returns (dq, dk, dv) of flash_attention_window_varlen, given its o and lse."""
-    Tq, H, D = q.shape
     if workspace is None:
-        workspace = torch.empty(fa_bwd_varlen_workspace_bytes(Tq, H, D) // 4, dtype=torch.float32, device=q.device)
+        if q.dim() != 3 or k.dim() != 3:
+            raise ValueError("q must be [total_q,H,D] and k, v [total_k,Hkv,D]")
+        Tq, H, D = q.shape
+        n = fa_bwd_window_varlen_workspace_bytes(cu_seqlens_q.numel() - 1, Tq, max_seqlen_q, max_seqlen_k, H,
+                                                 k.shape[1], D, window, sinks)
+        workspace = torch.empty(n // 4, dtype=torch.float32, device=q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fa_bwd_window_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                          max_seqlen_k, window, sinks, scale, stream)

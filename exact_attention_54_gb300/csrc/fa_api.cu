@@ -672,6 +672,60 @@ fa_status_t fa_fwd_window_varlen(const void *q, const void *k, const void *v, vo
                       0, D, window, sinks, scale, dtype, stream);
 }
 
+// How the window backward cuts its key tiles' steps into segments, and the
+// workspace that takes: fa_bwd's (base bytes) and the segments' dV and dK.
+struct WindowCut {
+    int sink_tiles, segs_sink, segs;
+    size_t bytes;
+};
+
+static WindowCut window_cut(size_t base, long long units, int H, int Hkv, int Sq, int Sk, int D, int window,
+                            int sinks) {
+    WindowCut c{};
+    const long long n_kt = (Sk + 127) / 128, block = D == 64 ? 128 : 64, group = H / Hkv;
+    const long long sink_tiles = (static_cast<long long>(sinks) + 127) / 128;
+    c.sink_tiles = static_cast<int>(sink_tiles < n_kt ? sink_tiles : n_kt);
+    // steps of the longest plain tile and of the longest tile with sinks, in
+    // the longest sequence
+    const long long reach = 128LL + window < Sq ? 128LL + window : Sq;
+    const long long plain = group * ((reach + block - 1) / block), sunk = group * ((Sq + block - 1) / block);
+    // Plain tiles: at least two units for each SM, in up to four segments.
+    // Tiles with sinks: no longer than the plain ones, or a quarter of an SM's
+    // share where that is more.
+    constexpr long long kSms = 152;
+    const long long tiles = units * n_kt;
+    long long segs = (2 * kSms + tiles - 1) / tiles;
+    segs = segs < 4 ? segs : 4;
+    if (segs * 8 > plain) segs = 1;
+    const long long others = units * (n_kt - c.sink_tiles);
+    const long long share = (others * plain + units * c.sink_tiles * sunk) / (4 * kSms);
+    const long long most = others > 0 && plain / segs > share ? plain / segs : (share > 8 ? share : 8);
+    long long segs_sink = c.sink_tiles > 0 ? (sunk + most - 1) / most : 1;
+    segs_sink = segs_sink < 1 ? 1 : (segs_sink < 64 ? segs_sink : 64);
+    c.segs = static_cast<int>(segs);
+    c.segs_sink = static_cast<int>(segs_sink);
+    const long long slots = units * ((segs_sink > 1 ? c.sink_tiles * segs_sink : 0) +
+                                     (segs > 1 ? (n_kt - c.sink_tiles) * segs : 0));
+    c.bytes = (base + 15) / 16 * 16 + static_cast<size_t>(slots) * 2 * 128 * D * sizeof(float);
+    return c;
+}
+
+size_t fa_bwd_window_workspace_bytes(int B, int H, int Hkv, int Sq, int Sk, int D, int window, int sinks) {
+    if (B < 1 || !window_ok(H, Hkv, Sq, Sk, window, sinks)) return 0;
+    const size_t base = fa_bwd_workspace_bytes(B, H, Sq, D);
+    if (base == 0) return 0;
+    return window_cut(base, static_cast<long long>(B) * Hkv, H, Hkv, Sq, Sk, D, window, sinks).bytes;
+}
+
+size_t fa_bwd_window_varlen_workspace_bytes(int num_seqs, int total_q, int max_seqlen_q, int max_seqlen_k, int H,
+                                            int Hkv, int D, int window, int sinks) {
+    if (num_seqs < 1 || !window_ok(H, Hkv, max_seqlen_q, max_seqlen_k, window, sinks)) return 0;
+    const size_t base = fa_bwd_varlen_workspace_bytes(total_q, H, D);
+    if (base == 0) return 0;
+    return window_cut(base, static_cast<long long>(num_seqs) * Hkv, H, Hkv, max_seqlen_q, max_seqlen_k, D, window,
+                      sinks).bytes;
+}
+
 static fa_status_t bwd_window(const void *q, const void *k, const void *v, const void *o, const void *dout,
                               const float *lse, void *dq, void *dk, void *dv, float *workspace,
                               size_t workspace_bytes, const int32_t *cu_q, const int32_t *cu_k, int B, int total_q,
@@ -688,9 +742,13 @@ static fa_status_t bwd_window(const void *q, const void *k, const void *v, const
         !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(workspace) || !aligned4(cu_q) ||
         !aligned4(cu_k))
         return FA_ERR_ALIGN;
-    const size_t need = varlen ? fa_bwd_varlen_workspace_bytes(total_q, H, D) : fa_bwd_workspace_bytes(B, H, Sq, D);
-    if (need == 0) return FA_ERR_SHAPE;
-    if (workspace_bytes < need) return FA_ERR_WORKSPACE;
+    const size_t base = varlen ? fa_bwd_varlen_workspace_bytes(total_q, H, D) : fa_bwd_workspace_bytes(B, H, Sq, D);
+    if (base == 0) return FA_ERR_SHAPE;
+    const WindowCut cut = window_cut(base, units, H, Hkv, Sq, Sk, D, window, sinks);
+    const long long per_head = static_cast<long long>(cut.sink_tiles) * cut.segs_sink +
+                               (n_kt - cut.sink_tiles) * cut.segs;
+    if (units * per_head > INT_MAX) return FA_ERR_SHAPE;
+    if (workspace_bytes < cut.bytes) return FA_ERR_WORKSPACE;
 
     const bool bf16 = dtype == FA_BF16;
     CUtensorMap maps[5];
@@ -732,7 +790,11 @@ static fa_status_t bwd_window(const void *q, const void *k, const void *v, const
     p.lse2 = workspace + rows * D;
     p.delta = p.lse2 + stat_rows;
     p.work_counter = reinterpret_cast<int *>(p.delta + stat_rows);
-    p.total_units = static_cast<int>(units * n_kt);
+    p.total_units = static_cast<int>(units * per_head);
+    p.sink_tiles = cut.sink_tiles;
+    p.segs_sink = cut.segs_sink;
+    p.segs = cut.segs;
+    p.segments = workspace + (base + 15) / 16 * 4;
     p.grid = sms;
     p.dk = dk;
     p.dv = dv;

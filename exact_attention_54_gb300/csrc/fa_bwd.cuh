@@ -213,15 +213,30 @@ __global__ void __launch_bounds__(256) fa_bwd_dq_kernel(const float *__restrict_
 // Every CTA of a head re-reads its Q and dO and adds into its dQ accumulator,
 // so running a few heads at once keeps that set (8 Sq D bytes per head)
 // within L2 instead of streaming every head's through it at once.
+// WIN: a key tile's steps may be cut into segments (see WinSteps), `seg`; a
+// head's work items are its sink tiles' segments, then the others'.
 template <bool WIN>
-__device__ __forceinline__ void bwd_work_at(const BwdParams &p, int w, int &kt, int &bh) {
-    const int per_group = p.heads_per_group * p.n_ktiles;
+__device__ __forceinline__ void bwd_work_at(const BwdParams &p, int w, int &kt, int &bh, int &seg) {
+    const int sink_items = WIN ? p.sink_tiles * p.segs_sink : 0;
+    const int per_head = WIN ? sink_items + (p.n_ktiles - p.sink_tiles) * p.segs : p.n_ktiles;
+    const int per_group = p.heads_per_group * per_head;
     const int g = w / per_group;
     const int i = w % per_group;
     const int rest = (WIN ? p.units : p.BH) - g * p.heads_per_group;
     const int g_heads = rest < p.heads_per_group ? rest : p.heads_per_group;
     kt = i / g_heads;
     bh = g * p.heads_per_group + i % g_heads;
+    seg = 0;
+    if constexpr (WIN) {
+        const int item = kt;
+        if (item < sink_items) {
+            kt = item / p.segs_sink;
+            seg = item % p.segs_sink;
+        } else {
+            kt = p.sink_tiles + (item - sink_items) / p.segs;
+            seg = (item - sink_items) % p.segs;
+        }
+    }
 }
 
 // This CTA's key tile and what it needs of its unit: the unit's index (dense
@@ -235,18 +250,27 @@ struct BwdUnit {
     int tq0, tk0;  // packed: first query and key token of the sequence
     int Lq, Lk;
     bool ok;
+    int seg;       // WIN: segment of the tile's steps
+    int seq;       // WIN, packed: the sequence
 };
+
+// WIN: index of the unit's key head (dense) or of the sequence's key head (packed).
+template <bool VARLEN>
+__device__ __forceinline__ int unit_index(const BwdParams &p, const BwdUnit &u) {
+    return VARLEN ? u.seq * (p.H / p.group) + u.hh : u.z;
+}
 
 template <bool VARLEN, bool WIN>
 __device__ __forceinline__ BwdUnit bwd_unit_at(const BwdParams &p, int w) {
     BwdUnit u;
     int unit;
-    bwd_work_at<WIN>(p, w, u.kt, unit);
+    bwd_work_at<WIN>(p, w, u.kt, unit, u.seg);
     if constexpr (VARLEN) {
         const int heads = WIN ? p.H / p.group : p.H;  // of the keys
         const int b = unit / heads;
         u.z = 0;
         u.hh = unit % heads;
+        u.seq = b;
         const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
         u.ok = !(q0 < 0 || q1 < q0 || q1 > p.total_q || q1 - q0 > p.Sq || k0 < 0 || k1 < k0 || k1 > p.total_k ||
                  k1 - k0 > p.Sk);
@@ -257,6 +281,7 @@ __device__ __forceinline__ BwdUnit bwd_unit_at(const BwdParams &p, int w) {
     } else {
         u.z = unit;
         u.hh = 0;
+        u.seq = 0;
         u.tq0 = u.tk0 = 0;
         u.Lq = p.Sq;
         u.Lk = p.Sk;
@@ -283,6 +308,49 @@ __device__ __forceinline__ int query_blocks(const BwdParams &p, const BwdUnit &u
     int q_end = u.Lq;
     if (WIN && k0 >= p.sinks) q_end = min(q_end, k0 + kBlock - 1 + p.window);
     return q_end > q_begin ? (q_end - q_begin + BLOCK - 1) / BLOCK : 0;
+}
+
+// The steps of a unit's segment: [first, first + n) of the tile's; `blocks`
+// query blocks for each of the group's heads; `parts` segments have steps (at
+// least one, which writes the gradients of a tile that no query sees).
+//
+// Segments: a unit's steps grow with the query heads that share its key head,
+// and a tile of sinks is seen by all later queries, so one CTA would still be
+// busy with a few such units when the others are done. Cut, each segment's dK
+// and dV go to the workspace in fp32 and fa_bwd_join_kernel adds them up in
+// order. (32 query heads on 8 key heads, 4096 tokens, window 1024, 4 sinks: the
+// longest units have 256 steps of 64 queries, the others 72.)
+struct WinSteps {
+    int blocks, first, n, parts;
+};
+
+template <bool CAUSAL, bool WIN, int BLOCK>
+__device__ __forceinline__ WinSteps unit_steps(const BwdParams &p, const BwdUnit &u, int k0) {
+    WinSteps s;
+    s.blocks = query_blocks<CAUSAL, WIN, BLOCK>(p, u, k0);
+    s.first = 0;
+    s.n = s.blocks;
+    s.parts = 1;
+    if constexpr (WIN) {
+        const int all = s.blocks * p.group, segs = u.kt < p.sink_tiles ? p.segs_sink : p.segs;
+        const int each = (all + segs - 1) / segs;
+        s.parts = all > 0 ? (all + each - 1) / each : 1;
+        s.first = min(u.seg * each, all);
+        s.n = min(each, all - s.first);
+    }
+    return s;
+}
+
+// WIN: the segment's slot in the workspace, 2 x 128 x D floats (dV, dK): column
+// c of row r at (c / 4 * 128 + r) * 4 + c % 4. `unit`: key head (dense) or key
+// head of a sequence (packed).
+template <int D>
+__device__ __forceinline__ float *segment_slot(const BwdParams &p, int unit, int kt, int seg) {
+    const int sink_items = p.sink_tiles * p.segs_sink;
+    const int per_head = (p.segs_sink > 1 ? sink_items : 0) + (p.segs > 1 ? (p.n_ktiles - p.sink_tiles) * p.segs : 0);
+    const int item = kt < p.sink_tiles ? kt * p.segs_sink + seg
+                                       : (p.segs_sink > 1 ? sink_items : 0) + (kt - p.sink_tiles) * p.segs + seg;
+    return p.segments + (static_cast<size_t>(unit) * per_head + item) * (2 * kBlock * D);
 }
 
 // The unit as its step `step` sees it on the query side: u.z and u.hh become
@@ -392,8 +460,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kt = u.kt;
     const int k0 = kt * kBlock;
     const int qt0 = CAUSAL ? kt : 0;  // first query tile that sees any of these keys
-    const int n_blocks = query_blocks<CAUSAL, WIN, kBlock>(p, u, k0);
-    const int n = WIN ? n_blocks * p.group : n_blocks;
+    const WinSteps steps = unit_steps<CAUSAL, WIN, kBlock>(p, u, k0);
+    const int n_blocks = steps.blocks, first = steps.first;
+    const int n = steps.n;
+    if (WIN && u.seg >= steps.parts) return;  // nothing left for this segment
     // 128 rows of the unit's queries (keys = false) or keys, every 64-column box
     auto load_rows = [&](const CUtensorMap *tm, const BwdUnit &unit, uint32_t dst, uint32_t bar_addr, int row0,
                          bool keys) {
@@ -443,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // stage s is free once the bulk reduction of step it-2 has read it
             if (it >= 2 && !wait(S::kStageFree + s, ((it >> 1) - 1) & 1)) break;
             int qb;
-            const BwdUnit uq = query_side<WIN>(p, u, it, n_blocks, qb);
+            const BwdUnit uq = query_side<WIN>(p, u, first + it, n_blocks, qb);
             const int q0 = (qt0 + qb) * kBlock;
             if (leader && !withheld(p.withhold, static_cast<uint32_t>(it))) {
                 ptx::bar_arrive_expect_tx(bar(S::kQFull + s), 2 * S::kTileBytes);
@@ -568,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int it = 0; it < n; ++it) {
             const int s = it & 1;
             int qb;
-            query_side<WIN>(p, u, it, n_blocks, qb);
+            query_side<WIN>(p, u, first + it, n_blocks, qb);
             const int q0 = (qt0 + qb) * kBlock;
             // the step's LSE and D values and the free dS^T buffer are ready
             // well before S^T and dP^T: wait for them first, so that only one
@@ -691,6 +761,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 32; ++k) w[k] = 0u;
                     }
+                    if (WIN && steps.parts > 1) {
+                        float4 *part = reinterpret_cast<float4 *>(
+                            segment_slot<D>(p, unit_index<VARLEN>(p, u), kt, u.seg) + t * kBlock * D);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            part[(h * (D / 8) + c * 8 + k) * kBlock + r] =
+                                make_float4(__uint_as_float(w[4 * k]), __uint_as_float(w[4 * k + 1]),
+                                            __uint_as_float(w[4 * k + 2]), __uint_as_float(w[4 * k + 3]));
+                        continue;
+                    }
                     uint32_t pk[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
@@ -719,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait(S::kStageReady, it & 1)) break;
             if (leader) {
                 int qb;
-                const BwdUnit uq = query_side<WIN>(p, u, it, n_blocks, qb);
+                const BwdUnit uq = query_side<WIN>(p, u, first + it, n_blocks, qb);
                 const int q0 = (qt0 + qb) * kBlock;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
@@ -907,6 +987,7 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
         bool live;  // false: no unit is left
         BwdUnit u;
         int k0, qs0, n, blocks;
+        int first, parts;  // WIN: first step of the segment, segments of the tile (see unit_steps)
     };
     // Unit slot i of this CTA: waits until warp 0 has published it, copies it
     // and releases the slot. False when the wait gave up.
@@ -915,8 +996,10 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
         if (!wait(S::kUnitReady + s, (i / S::kRing) & 1)) return false;
         const volatile int *e = reinterpret_cast<const volatile int *>(smem_raw + S::kOffUnits + s * 32);
         uv.live = e[0] != 0;
-        uv.u.kt = e[1];
-        uv.u.z = e[2];
+        uv.u.kt = WIN ? e[1] & 0xffffff : e[1];
+        uv.u.seg = WIN ? e[1] >> 24 : 0;
+        uv.u.z = WIN && VARLEN ? 0 : e[2];
+        uv.u.seq = WIN && VARLEN ? e[2] : 0;
         uv.u.hh = e[3];
         uv.u.tq0 = e[4];
         uv.u.tk0 = e[5];
@@ -925,8 +1008,11 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
         uv.u.ok = true;
         uv.k0 = uv.u.kt * kBlock;
         uv.qs0 = CAUSAL ? uv.k0 : 0;
-        uv.blocks = query_blocks<CAUSAL, WIN, S::kQ>(p, uv.u, uv.k0);
-        uv.n = WIN ? uv.blocks * p.group : uv.blocks;
+        const WinSteps ws = unit_steps<CAUSAL, WIN, S::kQ>(p, uv.u, uv.k0);
+        uv.blocks = ws.blocks;
+        uv.n = ws.n;
+        uv.first = ws.first;
+        uv.parts = ws.parts;
         __syncwarp();
         if (lane == 0) ptx::bar_arrive(bar(S::kUnitFree + s));
         return true;
@@ -962,14 +1048,17 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
                     }
                     if (u.kt * kBlock >= u.Lk) continue;  // a key tile past the sequence's keys
                 }
+                if constexpr (WIN) {  // nothing left for this segment
+                    if (u.seg >= unit_steps<CAUSAL, WIN, S::kQ>(p, u, u.kt * kBlock).parts) continue;
+                }
                 break;
             }
             const bool live = w < p.total_units;
             if (lane == 0) {
                 volatile int *e = reinterpret_cast<volatile int *>(smem_raw + S::kOffUnits + s * 32);
                 e[0] = live ? 1 : 0;
-                e[1] = u.kt;
-                e[2] = u.z;
+                e[1] = WIN ? u.kt | u.seg << 24 : u.kt;
+                e[2] = WIN && VARLEN ? u.seq : u.z;
                 e[3] = u.hh;
                 e[4] = u.tq0;
                 e[5] = u.tk0;
@@ -980,8 +1069,8 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
             __syncwarp();
             if (!live) break;
             const int k0 = u.kt * kBlock, qs0 = CAUSAL ? k0 : 0;
-            const int blocks = query_blocks<CAUSAL, WIN, S::kQ>(p, u, k0);
-            const int n = WIN ? blocks * p.group : blocks;
+            const WinSteps ws = unit_steps<CAUSAL, WIN, S::kQ>(p, u, k0);
+            const int blocks = ws.blocks, n = ws.n;
             if (n == 0) continue;  // no query sees these keys: zero dK and dV only
             // K and V of the unit once the previous unit's products are done with theirs
             if (wi >= 1 && !(ok = wait(S::kKVEmpty, (wi - 1) & 1))) break;
@@ -1002,7 +1091,7 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
                 // each half of the stage held part of sub-step J-4's staged dQ_t
                 // until its reductions read it: Q_J first (S^T needs it), then dO_J
                 int block;
-                const BwdUnit uq = query_side<WIN>(p, u, j, blocks, block);
+                const BwdUnit uq = query_side<WIN>(p, u, ws.first + j, blocks, block);
                 const int q0 = qs0 + block * S::kQ;
                 const uint32_t qb = sbase + S::kOffQ + st * S::kStageBytes;
                 int qy, qz;
@@ -1189,7 +1278,7 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
           for (int j = 0; j < n; ++j, ++J) {
             const int b = J & 1;
             int block;
-            query_side<WIN>(p, u, j, uv.blocks, block);
+            query_side<WIN>(p, u, uv.first + j, uv.blocks, block);
             const int qc = qs0 + block * S::kQ + 32 * h;  // first query of this warp's chunk
             const uint32_t tb = tmem + lane_base + S::kTmemBuf + 128 * b;
             // the sub-step's rows, then S^T: one test of both first, the
@@ -1306,6 +1395,18 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
 #pragma unroll
                         for (int k = 0; k < 32; ++k) w[c][k] = 0u;
                 }
+                if (WIN && uv.parts > 1) {
+                    float4 *part = reinterpret_cast<float4 *>(
+                        segment_slot<D>(p, unit_index<VARLEN>(p, u), u.kt, u.seg) + t * kBlock * D);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            part[(h * (D / 8) + c * 8 + k) * kBlock + r] =
+                                make_float4(__uint_as_float(w[c][4 * k]), __uint_as_float(w[c][4 * k + 1]),
+                                            __uint_as_float(w[c][4 * k + 2]), __uint_as_float(w[c][4 * k + 3]));
+                    continue;
+                }
                 // row `lane` of the block: 16-byte chunk q at (q ^ (row & 7)) * 16
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
@@ -1393,7 +1494,7 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
             if (!(ok = wait(S::kStageReady + st, (J / S::kStages) & 1))) break;
             if (leader) {
                 int block;
-                const BwdUnit uq = query_side<WIN>(p, u, j, uv.blocks, block);
+                const BwdUnit uq = query_side<WIN>(p, u, uv.first + j, uv.blocks, block);
                 const int q0 = uv.qs0 + block * S::kQ;
                 const uint32_t tile = sbase + S::kOffQ + st * S::kStageBytes;
                 int y, z;
@@ -1425,6 +1526,55 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
     if (threadIdx.x == 0 && *abort_flag) atomicExch(p.err, kDeviceErrTimeout);
 }
 
+// WIN: dK and dV of the key tiles that were cut into segments: the segments'
+// sums in order, scaled (dK) and rounded. A CTA per key tile and key head, 8
+// columns of a row per thread.
+template <int D, bool BF16, bool VARLEN>
+__global__ void __launch_bounds__(256) fa_bwd_join_kernel(const BwdParams p) {
+    constexpr int kBlockQ = D == 64 ? 128 : ShapeQ64::kQ;
+    const int unit = static_cast<int>(blockIdx.x) / p.n_ktiles, kt = static_cast<int>(blockIdx.x) % p.n_ktiles;
+    BwdUnit u{};
+    u.kt = kt;
+    int heads = 1;
+    if constexpr (VARLEN) {
+        heads = p.H / p.group;
+        const int b = unit / heads;
+        u.hh = unit % heads;
+        const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
+        if (q0 < 0 || q1 < q0 || q1 > p.total_q || q1 - q0 > p.Sq || k0 < 0 || k1 < k0 || k1 > p.total_k ||
+            k1 - k0 > p.Sk)
+            return;  // skipped by the main kernel too, which reports it
+        u.tk0 = k0;
+        u.Lq = q1 - q0;
+        u.Lk = k1 - k0;
+    } else {
+        u.z = unit;
+        u.Lq = p.Sq;
+        u.Lk = p.Sk;
+    }
+    const int k0 = kt * kBlock;
+    if (k0 >= u.Lk) return;
+    const int parts = unit_steps<true, true, kBlockQ>(p, u, k0).parts;
+    if (parts < 2) return;
+    for (int i = threadIdx.x; i < 2 * kBlock * (D / 8); i += 256) {
+        const int r = i % kBlock, c8 = i / kBlock % (D / 8), t = i / (kBlock * (D / 8));
+        if (k0 + r >= u.Lk) continue;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+        for (int s = 0; s < parts; ++s) {
+            const float4 *x = reinterpret_cast<const float4 *>(segment_slot<D>(p, unit, kt, s) + t * kBlock * D);
+            const float4 v = x[2 * c8 * kBlock + r], w = x[(2 * c8 + 1) * kBlock + r];
+            a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+            b.x += w.x, b.y += w.y, b.z += w.z, b.w += w.w;
+        }
+        const float f = t == 0 ? 1.f : p.scale;
+        const size_t row = VARLEN ? (static_cast<size_t>(u.tk0) + k0 + r) * heads + u.hh
+                                  : static_cast<size_t>(u.z) * p.Sk + k0 + r;
+        reinterpret_cast<uint4 *>(static_cast<uint16_t *>(t == 0 ? p.dv : p.dk) + row * D)[c8] =
+            make_uint4(ptx::pack2<BF16>(a.x * f, a.y * f), ptx::pack2<BF16>(a.z * f, a.w * f),
+                       ptx::pack2<BF16>(b.x * f, b.y * f), ptx::pack2<BF16>(b.z * f, b.w * f));
+    }
+}
+
 template <int D, bool BF16, bool CAUSAL, bool VARLEN, bool WIN = false>
 cudaError_t launch_t(const CUtensorMap *maps, const void *o, const void *dout, const float *lse, void *dq,
                      const BwdParams &p, cudaStream_t st) {
@@ -1445,7 +1595,7 @@ cudaError_t launch_t(const CUtensorMap *maps, const void *o, const void *dout, c
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     // D = 64: one CTA per work unit; D = 128: persistent CTAs take units from a counter
-    const long long units = static_cast<long long>(WIN ? p.units : p.BH) * p.n_ktiles;
+    const long long units = WIN ? p.total_units : static_cast<long long>(p.BH) * p.n_ktiles;
     const long long grid = D == 64 ? units : (units < p.grid ? units : p.grid);
     // D = 128: the main and the conversion kernels are launched as programmatic
     // dependents (each waits for its predecessor in the kernel itself)
@@ -1468,8 +1618,14 @@ cudaError_t launch_t(const CUtensorMap *maps, const void *o, const void *dout, c
     cfg2.stream = st;
     cfg2.attrs = pdl;
     cfg2.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg2, fa_bwd_dq_kernel<BF16>, static_cast<const float *>(p.dq_acc),
-                              static_cast<uint16_t *>(dq), n8, p.scale);
+    e = cudaLaunchKernelEx(&cfg2, fa_bwd_dq_kernel<BF16>, static_cast<const float *>(p.dq_acc),
+                           static_cast<uint16_t *>(dq), n8, p.scale);
+    if constexpr (WIN) {
+        if (e != cudaSuccess || (p.segs == 1 && p.segs_sink == 1)) return e;
+        fa_bwd_join_kernel<D, BF16, VARLEN><<<static_cast<unsigned>(p.units) * p.n_ktiles, 256, 0, st>>>(p);
+        e = cudaGetLastError();
+    }
+    return e;
 }
 
 }  // namespace bwd

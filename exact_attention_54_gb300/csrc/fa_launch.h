@@ -109,6 +109,9 @@ struct BwdParams {
     int window, sinks;     // sliding window only: keys a query sees back to itself; first keys always visible
     int group;             // sliding window only: query heads per key head
     int units;             // sliding window only: key heads (dense B*Hkv, packed num_seqs*Hkv) that key tiles belong to
+    int sink_tiles;        // sliding window only: key tiles that hold sinks (at most n_ktiles)
+    int segs_sink, segs;   // sliding window only: segments of their steps, and of the other key tiles'
+    float *segments;       // sliding window only: the segments' dV and dK (unused where both counts are 1)
 };
 
 // Test support: a launch that withholds one load (see FwdParams::withhold)

@@ -368,11 +368,23 @@ FA_API fa_status_t fa_fwd_window_varlen(const void *q, const void *k, const void
                                         int window, int sinks, float scale, fa_dtype_t dtype, void *stream);
 
 /*
+ * fa_bwd_window_workspace_bytes, fa_bwd_window_varlen_workspace_bytes - bytes
+ * of workspace that fa_bwd_window and fa_bwd_window_varlen need: those of
+ * fa_bwd (fa_bwd_varlen), and 1024 D bytes (fp32 dV and dK of 128 keys) for
+ * each segment into which the work of a key tile is cut where shared heads or
+ * sinks make it long. 0 for an invalid shape.
+ */
+FA_API size_t fa_bwd_window_workspace_bytes(int B, int H, int Hkv, int Sq, int Sk, int D, int window, int sinks);
+FA_API size_t fa_bwd_window_varlen_workspace_bytes(int num_seqs, int total_q, int max_seqlen_q, int max_seqlen_k,
+                                                   int H, int Hkv, int D, int window, int sinks);
+
+/*
  * fa_bwd_window - the gradients of fa_fwd_window, as fa_bwd computes those of
  * fa_fwd: dq [B,H,Sq,D], and dk, dv [B,Hkv,Sk,D] summed over the query heads
- * that share a key head. workspace: at least fa_bwd_workspace_bytes(B, H, Sq,
- * D) bytes, as for fa_bwd. Queries that see no key get dq = 0, keys that no
- * query sees dk = dv = 0. dk and dv are deterministic, dq rounds as in fa_bwd.
+ * that share a key head. workspace: at least fa_bwd_window_workspace_bytes
+ * bytes, otherwise as for fa_bwd. Queries that see no key get dq = 0, keys that
+ * no query sees dk = dv = 0. dk and dv are deterministic, dq rounds as in
+ * fa_bwd. Three launches, or four.
  * Errors: as fa_bwd and fa_fwd_window.
  */
 FA_API fa_status_t fa_bwd_window(const void *q, const void *k, const void *v, const void *o, const void *dout,
@@ -383,8 +395,7 @@ FA_API fa_status_t fa_bwd_window(const void *q, const void *k, const void *v, co
 /*
  * fa_bwd_window_varlen - the gradients of fa_fwd_window_varlen: arguments,
  * device-side checks and rows outside the sequences as fa_bwd_varlen, the
- * workspace of fa_bwd_varlen_workspace_bytes(total_q, H, D), dk and dv
- * [total_k,Hkv,D].
+ * workspace of fa_bwd_window_varlen_workspace_bytes, dk and dv [total_k,Hkv,D].
  * Errors: as fa_bwd_varlen and fa_fwd_window.
  */
 FA_API fa_status_t fa_bwd_window_varlen(const void *q, const void *k, const void *v, const void *o, const void *dout,

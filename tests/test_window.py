@@ -70,7 +70,11 @@ def test_bwd_validation(lib):
 
     _refusals(call, [n for n in names if n != "lse"], ["lse"],
               HEADS + [{"B": 0}, {"Sq": 0}, {"Sk": 0}, {"Sq": LONG}, {"Sk": LONG}])
-    assert call(wsb=lib.fa_bwd_workspace_bytes(1, 4, 200, 128) - 1) == WORKSPACE
+    need = lib.fa_bwd_window_workspace_bytes(1, 4, 2, 200, 300, 128, 10, 2)
+    assert need >= lib.fa_bwd_workspace_bytes(1, 4, 200, 128) and call(wsb=need - 1) == WORKSPACE
+    for bad in ((0, 4, 2, 200, 300, 128, 10, 2), (1, 4, 3, 200, 300, 128, 10, 2), (1, 4, 2, 0, 300, 128, 10, 2),
+                (1, 4, 2, 200, LONG, 128, 10, 2), (1, 4, 2, 200, 300, 96, 10, 2), (1, 4, 2, 200, 300, 128, 0, 2)):
+        assert lib.fa_bwd_window_workspace_bytes(*bad) == 0
 
 
 def test_bwd_varlen_validation(lib):
@@ -82,7 +86,11 @@ def test_bwd_varlen_validation(lib):
 
     _refusals(call, [x for x in names if x != "lse"], ["lse", "cq", "ck"],
               HEADS + [{"n": 0}, {"Tq": 0}, {"Tk": 0}, {"mq": 0}, {"mk": 0}, {"mq": LONG}, {"mk": LONG}])
-    assert call(wsb=lib.fa_bwd_varlen_workspace_bytes(100, 4, 64) - 1) == WORKSPACE
+    need = lib.fa_bwd_window_varlen_workspace_bytes(2, 100, 60, 70, 4, 2, 64, 10, 2)
+    assert need >= lib.fa_bwd_varlen_workspace_bytes(100, 4, 64) and call(wsb=need - 1) == WORKSPACE
+    for bad in ((0, 100, 60, 70, 4, 2, 64, 10, 2), (2, 0, 60, 70, 4, 2, 64, 10, 2), (2, 100, 0, 70, 4, 2, 64, 10, 2),
+                (2, 100, 60, 70, 4, 2, 32, 10, 2), (2, 100, 60, 70, 4, 2, 64, 10, -1)):
+        assert lib.fa_bwd_window_varlen_workspace_bytes(*bad) == 0
 
 
 def test_binding_refuses():
@@ -256,7 +264,7 @@ def test_scale_stream_and_given_workspace():
     q, k, v, do = draw(1, 4, 2, 333, 333, 128, torch.float16, seed=7)
     ref = plain_ops.window_attention(q[0], k[0], v[0], 77, 3, 0.3, do[0], torch.float16)
     qd, kd, vd, dd = (x.cuda() for x in (q, k, v, do))
-    ws = torch.full((fa.fa_bwd_workspace_bytes(1, 4, 333, 128) // 4,), math.nan, device="cuda")
+    ws = torch.full((fa.fa_bwd_window_workspace_bytes(1, 4, 2, 333, 333, 128, 77, 3) // 4,), math.nan, device="cuda")
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):
@@ -301,7 +309,7 @@ def test_bad_offsets_are_reported():
         with pytest.raises(fa.FAError) as e:
             fa.fa_check_device_error()
         assert e.value.status == -13 and (o == 3).all() and (lse == 3).all()
-        ws = torch.empty(fa.fa_bwd_varlen_workspace_bytes(100, 2, 64) // 4, device="cuda")
+        ws = torch.empty(fa.fa_bwd_window_varlen_workspace_bytes(2, 100, mx, mx, 2, 1, 64, 20) // 4, device="cuda")
         dk = torch.full_like(k, 3.0)
         fa.fa_bwd_window_varlen(q, k, k, q, q, lse, torch.empty_like(q), dk, torch.empty_like(k), ws, c, c, mx, mx, 20)
         with pytest.raises(fa.FAError) as e:
