@@ -1527,12 +1527,16 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
 }
 
 // WIN: dK and dV of the key tiles that were cut into segments: the segments'
-// sums in order, scaled (dK) and rounded. A CTA per key tile and key head, 8
-// columns of a row per thread.
+// sums in order, scaled (dK) and rounded. kJoinCtas CTAs per key tile and key
+// head (the sink tiles alone where the others are whole), 8 columns of a row
+// per thread and pass.
+constexpr int kJoinCtas = 8;
+
 template <int D, bool BF16, bool VARLEN>
 __global__ void __launch_bounds__(256) fa_bwd_join_kernel(const BwdParams p) {
     constexpr int kBlockQ = D == 64 ? 128 : ShapeQ64::kQ;
-    const int unit = static_cast<int>(blockIdx.x) / p.n_ktiles, kt = static_cast<int>(blockIdx.x) % p.n_ktiles;
+    const int tiles = p.segs > 1 ? p.n_ktiles : p.sink_tiles;
+    const int unit = static_cast<int>(blockIdx.x) / tiles, kt = static_cast<int>(blockIdx.x) % tiles;
     BwdUnit u{};
     u.kt = kt;
     int heads = 1;
@@ -1556,7 +1560,7 @@ __global__ void __launch_bounds__(256) fa_bwd_join_kernel(const BwdParams p) {
     if (k0 >= u.Lk) return;
     const int parts = unit_steps<true, true, kBlockQ>(p, u, k0).parts;
     if (parts < 2) return;
-    for (int i = threadIdx.x; i < 2 * kBlock * (D / 8); i += 256) {
+    for (int i = blockIdx.y * 256 + threadIdx.x; i < 2 * kBlock * (D / 8); i += kJoinCtas * 256) {
         const int r = i % kBlock, c8 = i / kBlock % (D / 8), t = i / (kBlock * (D / 8));
         if (k0 + r >= u.Lk) continue;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
@@ -1622,7 +1626,8 @@ cudaError_t launch_t(const CUtensorMap *maps, const void *o, const void *dout, c
                            static_cast<uint16_t *>(dq), n8, p.scale);
     if constexpr (WIN) {
         if (e != cudaSuccess || (p.segs == 1 && p.segs_sink == 1)) return e;
-        fa_bwd_join_kernel<D, BF16, VARLEN><<<static_cast<unsigned>(p.units) * p.n_ktiles, 256, 0, st>>>(p);
+        const unsigned tiles = p.segs > 1 ? p.n_ktiles : p.sink_tiles;
+        fa_bwd_join_kernel<D, BF16, VARLEN><<<dim3(p.units * tiles, kJoinCtas), 256, 0, st>>>(p);
         e = cudaGetLastError();
     }
     return e;

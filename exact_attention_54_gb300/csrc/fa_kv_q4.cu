@@ -6,9 +6,10 @@
 // bandwidth, or by launch latency for a few tokens.
 //
 // Grid: a chunk of tokens of one sequence per CTA (sequence = blockIdx.x /
-// chunks), so that a token's sequence needs no search in cu_seqlens. D / 8
-// lanes share a row of one key head, 8 columns (16 bytes) each; a thread takes
-// the key row and the value row of the same token and head.
+// chunks), so that a token's sequence needs no search in cu_seqlens; the
+// chunk's cache rows are looked up once, into shared memory. D / 8 lanes share
+// a row of one key head, 8 columns (16 bytes) each; a thread takes the key row
+// and the value row of kPasses (token, head) pairs with all loads in flight.
 #include "fa_kv_q4.cuh"
 #include "fa_launch.h"
 
@@ -16,7 +17,8 @@ namespace fa {
 namespace q4 {
 
 constexpr int kThreads = 256;
-constexpr int kPasses = 4;  // rows per lane group and CTA, when a sequence has that many
+constexpr int kPasses = 4;  // (token, head) pairs per lane group and CTA, when a sequence has that many
+constexpr int kMaxTokens = kPasses * kThreads / 8;  // of a CTA: D = 64, one key head
 
 // Tokens of one CTA: kPasses rows for each of its lane groups.
 static int tokens_per_cta(int D, int Hkv) {
@@ -47,17 +49,68 @@ __device__ __forceinline__ bool chunk_of(const KvQ4Params &p, Chunk &c) {
     return c.count > 0;
 }
 
-// Row of the cache (in rows of a key head) that holds token i of the chunk, or
-// -1 if the table names no page for it.
-__device__ __forceinline__ long long cache_row(const KvQ4Params &p, const Chunk &c, int i, int h) {
-    const long long pos = c.pos + i;
-    const long long blk = pos >> p.log2_bs;
-    const int page = blk < p.max_blocks ? c.table[blk] : -1;
-    if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_blocks)) {
-        atomicExch(p.err, kDeviceErrBadIndex);
-        return -1;
+// First key head's cache row of each token of the chunk, or -1 if the table
+// names no page for it (reported once: by the call that writes or reads it).
+// The whole CTA calls it.
+__device__ __forceinline__ void look_up(const KvQ4Params &p, const Chunk &c, long long *rows) {
+    for (int i = threadIdx.x; i < c.count; i += kThreads) {
+        const long long pos = c.pos + i, blk = pos >> p.log2_bs;
+        const int page = blk < p.max_blocks ? c.table[blk] : -1;
+        const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_blocks);
+        if (!ok) atomicExch(p.err, kDeviceErrBadIndex);
+        rows[i] = ok ? ((static_cast<long long>(page) * p.Hkv) << p.log2_bs) + (pos & ((1 << p.log2_bs) - 1)) : -1;
     }
-    return ((static_cast<long long>(page) * p.Hkv + h) << p.log2_bs) + (pos & ((1 << p.log2_bs) - 1));
+    __syncthreads();
+}
+
+// This lane group's (token, head) pairs: the first, then every `step`-th.
+struct Walk {
+    int t, h, dt, dh, Hkv;
+    __device__ __forceinline__ Walk(int first, int step, int Hkv_)
+        : t(first / Hkv_), h(first % Hkv_), dt(step / Hkv_), dh(step % Hkv_), Hkv(Hkv_) {}
+    __device__ __forceinline__ void next() {
+        t += dt;
+        h += dh;
+        if (h >= Hkv) {
+            h -= Hkv;
+            ++t;
+        }
+    }
+};
+
+// Codes (n + 8 in nibble e: column e of x's eight) for scale s.
+template <bool BF16>
+__device__ __forceinline__ uint32_t quantise8(const uint4 &x, float s) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    // Where s is a normal number (and 1 / s is one): x / s is a tie n + 1/2 or
+    // at least 2^-12 away from one, for x and s of at most 11 bits, and at most
+    // 7.04. x * (1 / s) is off by less than 2^-20, so rounding it to multiples
+    // of 2^-14 restores the ties and moves nothing else across one; adding 1.5
+    // 2^23 + 8 then rounds to the nearest even integer, which stands, plus 8,
+    // in the sum's low bits. The sum of 16^e times those words (mod 2^32) holds
+    // the nibbles, but for a constant.
+    if (s >= (BF16 ? 1e-30f : 6.103515625e-5f)) {
+        constexpr float kSnap = 768.f;          // 1.5 2^23 2^-14
+        constexpr float kInt = 12582920.f;      // 1.5 2^23 + 8: bits 0x4b400008
+        const float inv = 1.f / s;
+        uint32_t word = 0u - 0x4b400000u * 0x11111111u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float v = from16<BF16>(static_cast<uint16_t>(w[e / 2] >> (16 * (e % 2))));
+            const float t = __fsub_rn(__fmaf_rn(v, inv, kSnap), kSnap);
+            word += __float_as_uint(__fadd_rn(t, kInt)) * (1u << (4 * e));
+        }
+        return word;
+    }
+    uint32_t word = 0;
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t pair = e < 2 ? w[0] : e < 4 ? w[1] : e < 6 ? w[2] : w[3];
+        const float v = from16<BF16>(static_cast<uint16_t>(pair >> (16 * (e % 2))));
+        const float n = s > 0.f ? fminf(fmaxf(rintf(v / s), -7.f), 7.f) : 0.f;
+        word |= static_cast<uint32_t>(static_cast<int>(n) + 8) << (4 * e);
+    }
+    return word;
 }
 
 template <int D, bool BF16>
@@ -67,23 +120,12 @@ __device__ __forceinline__ void quantise_row(const uint4 &x, uint8_t *codes, uin
     // like integers, infinities and NaNs last)
     uint32_t mx = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
                            __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     mx = max(mx & 0xffffu, mx >> 16);
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const bool finite = mx < (BF16 ? 0x7f80u : 0x7c00u);
     const uint16_t s16 = finite ? to16<BF16>(from16<BF16>(static_cast<uint16_t>(mx)) / 7.f) : uint16_t(0x7fff);
-    const float s = from16<BF16>(s16);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t word = 0;  // nibble e: column 8 sub + e
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float v = from16<BF16>(static_cast<uint16_t>(w[e / 2] >> (16 * (e % 2))));
-        // The quotient of two values of at most 11 bits is a tie or at least
-        // 2^-12 (relative) away from one, so rounding it to fp32 first does
-        // not change the integer it rounds to.
-        const float n = s > 0.f ? fminf(fmaxf(rintf(v / s), -7.f), 7.f) : 0.f;
-        word |= static_cast<uint32_t>(static_cast<int>(n) + 8) << (4 * e);
-    }
+    const uint32_t word = quantise8<BF16>(x, from16<BF16>(s16));  // a NaN scale takes the slow way: all n = 0
     // Lane (w, c) of a row has columns 32 w + 8 c + (0..7): the 16 bits of
     // group w in pieces 2 c and 2 c + 1. The lanes of groups w and w ^ 1
     // exchange halves: even w keeps piece 2 c, odd w piece 2 c + 1, and each
@@ -100,62 +142,113 @@ __device__ __forceinline__ void quantise_row(const uint4 &x, uint8_t *codes, uin
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads) fa_kv_write_q4_kernel(const KvQ4Params p) {
+    __shared__ long long rows[kMaxTokens];
     Chunk c;
     if (!chunk_of(p, c)) return;
-    constexpr int kLanes = D / 8;
+    constexpr int kLanes = D / 8, kStep = kThreads / kLanes;
     const int sub = threadIdx.x % kLanes;
-    const int rows = c.count * p.Hkv;
+    const int pairs = c.count * p.Hkv;
     // whole warps run every pass: the group maxima are exchanged within a warp
-    for (int r0 = 0; r0 < rows; r0 += kThreads / kLanes) {
+    for (int r0 = 0; r0 < pairs; r0 += kPasses * kStep) {
         const int r = r0 + static_cast<int>(threadIdx.x) / kLanes;
-        const bool there = r < rows;
-        uint4 kx = make_uint4(0u, 0u, 0u, 0u), vx = kx;
-        long long row = -1;
-        if (there) {
-            const size_t at = (static_cast<size_t>(c.first) * p.Hkv + r) * D + sub * 8;
-            kx = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.k) + at));
-            vx = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.v) + at));
-            row = cache_row(p, c, r / p.Hkv, r % p.Hkv);
+        uint4 kx[kPasses], vx[kPasses];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            kx[i] = vx[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r + i * kStep < pairs) {
+                const size_t at = (static_cast<size_t>(c.first) * p.Hkv + r + i * kStep) * D + sub * 8;
+                kx[i] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.k) + at));
+                vx[i] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.v) + at));
+            }
         }
-        quantise_row<D, BF16>(kx, static_cast<uint8_t *>(p.k_codes), static_cast<uint16_t *>(p.k_scales), row, sub);
-        quantise_row<D, BF16>(vx, static_cast<uint8_t *>(p.v_codes), static_cast<uint16_t *>(p.v_scales), row, sub);
+        if (r0 == 0) look_up(p, c, rows);  // behind the loads
+        Walk w(r, kStep, p.Hkv);
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            if (r0 + i * kStep >= pairs) break;  // the same for the whole CTA
+            const long long first = r + i * kStep < pairs ? rows[w.t] : -1;
+            const long long row = first < 0 ? -1 : first + (static_cast<long long>(w.h) << p.log2_bs);
+            quantise_row<D, BF16>(kx[i], static_cast<uint8_t *>(p.k_codes), static_cast<uint16_t *>(p.k_scales), row,
+                                  sub);
+            quantise_row<D, BF16>(vx[i], static_cast<uint8_t *>(p.v_codes), static_cast<uint16_t *>(p.v_scales), row,
+                                  sub);
+            w.next();
+        }
     }
 }
 
-template <int D, bool BF16>
-__device__ __forceinline__ uint4 read_row(const uint8_t *codes, const uint16_t *scales, long long row, int sub) {
+// Eight columns of a row as loaded: the words that hold piece 2c and piece
+// 2c + 1 of the lane's group, and its scale.
+struct Packed8 {
+    uint32_t a, b;
+    uint16_t s;
+};
+
+template <int D>
+__device__ __forceinline__ Packed8 load8(const uint8_t *codes, const uint16_t *scales, long long row, int sub) {
     const int grp = sub / 4, c = sub % 4;
     const uint32_t *src = reinterpret_cast<const uint32_t *>(codes + row * (D / 2));
-    const uint32_t a = src[2 * c * (D / 64) + grp / 2], b = src[(2 * c + 1) * (D / 64) + grp / 2];
-    const float s = from16<BF16>(scales[row * (D / kGroup) + grp]);
-    const uint32_t word = grp % 2 == 0 ? __byte_perm(a, b, 0x5410) : __byte_perm(a, b, 0x7632);
-    uint32_t out[4];
+    return {src[2 * c * (D / 64) + grp / 2], src[(2 * c + 1) * (D / 64) + grp / 2], scales[row * (D / kGroup) + grp]};
+}
+
+// s * n of the eight, rounded once: n is exact in either 16-bit type (u + 1024
+// or u + 128, as masked into the mantissa, less 1032 or 136), so a 16-bit
+// product is the rounded one.
+template <int D, bool BF16>
+__device__ __forceinline__ uint4 unpack8(const Packed8 &x, int sub) {
+    const uint32_t word = __byte_perm(x.a, x.b, sub / 4 % 2 == 0 ? 0x5410 : 0x7632);
+    uint32_t v[4];  // columns i and 4 + i
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float lo = static_cast<float>(static_cast<int>((word >> (8 * i)) & 15u) - 8);
-        const float hi = static_cast<float>(static_cast<int>((word >> (8 * i + 4)) & 15u) - 8);
-        out[i] = ptx::pack2<BF16>(lo * s, hi * s);  // the fp32 product is exact: one rounding
+        const uint32_t u = ((word >> (4 * i)) & 0x000f000fu) | (BF16 ? 0x43004300u : 0x64006400u);
+        if constexpr (BF16) {
+            const __nv_bfloat162 n = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&u),
+                                             __bfloat162bfloat162(__ushort_as_bfloat16(0x4308)));  // 136
+            const __nv_bfloat162 y = __hmul2_rn(n, __bfloat162bfloat162(__ushort_as_bfloat16(x.s)));
+            v[i] = *reinterpret_cast<const uint32_t *>(&y);
+        } else {
+            const __half2 n = __hsub2(*reinterpret_cast<const __half2 *>(&u), __half2half2(__ushort_as_half(0x6408)));  // 1032
+            const __half2 y = __hmul2_rn(n, __half2half2(__ushort_as_half(x.s)));
+            v[i] = *reinterpret_cast<const uint32_t *>(&y);
+        }
     }
-    return make_uint4(out[0], out[1], out[2], out[3]);
+    return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                      __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
 }
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads) fa_kv_read_q4_kernel(const KvQ4Params p) {
+    __shared__ long long rows[kMaxTokens];
     Chunk c;
     if (!chunk_of(p, c)) return;
-    constexpr int kLanes = D / 8;
+    constexpr int kLanes = D / 8, kStep = kThreads / kLanes;
     const int sub = threadIdx.x % kLanes;
-    const int rows = c.count * p.Hkv;
-    for (int r = static_cast<int>(threadIdx.x) / kLanes; r < rows; r += kThreads / kLanes) {
-        const long long row = cache_row(p, c, r / p.Hkv, r % p.Hkv);
-        if (row < 0) continue;
-        const uint4 kx = read_row<D, BF16>(static_cast<const uint8_t *>(p.k_codes),
-                                           static_cast<const uint16_t *>(p.k_scales), row, sub);
-        const uint4 vx = read_row<D, BF16>(static_cast<const uint8_t *>(p.v_codes),
-                                           static_cast<const uint16_t *>(p.v_scales), row, sub);
-        const size_t at = (static_cast<size_t>(c.first) * p.Hkv + r) * D + sub * 8;
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.k) + at) = kx;
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.v) + at) = vx;
+    const int pairs = c.count * p.Hkv;
+    look_up(p, c, rows);
+    for (int r = static_cast<int>(threadIdx.x) / kLanes; r < pairs; r += kPasses * kStep) {
+        Walk w(r, kStep, p.Hkv);
+        Packed8 k[kPasses], v[kPasses];
+        bool there[kPasses];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const long long first = r + i * kStep < pairs ? rows[w.t] : -1;
+            there[i] = first >= 0;
+            if (there[i]) {
+                const long long row = first + (static_cast<long long>(w.h) << p.log2_bs);
+                k[i] = load8<D>(static_cast<const uint8_t *>(p.k_codes), static_cast<const uint16_t *>(p.k_scales),
+                                row, sub);
+                v[i] = load8<D>(static_cast<const uint8_t *>(p.v_codes), static_cast<const uint16_t *>(p.v_scales),
+                                row, sub);
+            }
+            w.next();
+        }
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            if (!there[i]) continue;
+            const size_t at = (static_cast<size_t>(c.first) * p.Hkv + r + i * kStep) * D + sub * 8;
+            __stcs(reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.k) + at), unpack8<D, BF16>(k[i], sub));
+            __stcs(reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.v) + at), unpack8<D, BF16>(v[i], sub));
+        }
     }
 }
 
