@@ -442,11 +442,11 @@ def _expect(name: str, t, shape, dtype):
 _entry = {}  # entry points of the loaded library by name
 
 
-def _launch(fn: str, stream, args, tensors):
-    """Call entry point ``fn`` with ``args`` and the stream, on the device that all of ``tensors`` (None: skipped)
-    share."""
+def _launch(fn: str, stream, tensors, *args, index=None):
+    """Call entry point ``fn`` with the pointers of ``tensors`` (None: NULL), ``args`` and the stream, on the device
+    that the tensors, and those of ``index``, share."""
     dev = tensors[0].get_device()
-    for t in tensors:
+    for t in tensors if index is None else (*tensors, *index):
         if t is not None and t.get_device() != dev:
             dev = -1
     if dev < 0:
@@ -454,12 +454,13 @@ def _launch(fn: str, stream, args, tensors):
     call = _entry.get(fn)
     if call is None:
         call = _entry[fn] = getattr(load_library(), fn)
-    st = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+    ptrs = [None if t is None else t.data_ptr() for t in tensors]
+    stream = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
-            st = call(*args, st)
+            st = call(*ptrs, *args, stream)
     else:
-        st = call(*args, st)
+        st = call(*ptrs, *args, stream)
     if st != 0:
         _check(fn, st)
 
@@ -477,8 +478,7 @@ def fa_fwd_window(q, k, v, o, lse, window: int, sinks: int = 0, scale: float | N
     _expect("lse", lse, (B, H, Sq), torch.float32)
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     ts = (q, k, v, o, lse)
-    _launch("fa_fwd_window", stream, (*map(_ptr, ts), B, H, Hkv, Sq, Sk, D, int(window), int(sinks), float(scale),
-                                      code), ts)
+    _launch("fa_fwd_window", stream, ts, B, H, Hkv, Sq, Sk, D, int(window), int(sinks), float(scale), code)
 
 
 def fa_fwd_window_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, window: int, sinks: int = 0,
@@ -497,8 +497,8 @@ def fa_fwd_window_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen
     _expect("cu_seqlens_k", cu_seqlens_k, (n + 1,), torch.int32)
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     ts = (q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k)
-    _launch("fa_fwd_window_varlen", stream, (*map(_ptr, ts), n, Tq, Tk, int(max_seqlen_q), H, Hkv, D, int(window),
-                                             int(sinks), float(scale), code), ts)
+    _launch("fa_fwd_window_varlen", stream, ts, n, Tq, Tk, int(max_seqlen_q), H, Hkv, D, int(window), int(sinks),
+            float(scale), code)
 
 
 def fa_bwd_window_workspace_bytes(B: int, H: int, Hkv: int, Sq: int, Sk: int, D: int, window: int,
@@ -529,8 +529,8 @@ def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sin
     _need_contig(workspace)
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     ts = (q, k, v, o, dout, lse, dq, dk, dv, workspace)
-    _launch("fa_bwd_window", stream, (*map(_ptr, ts), workspace.numel() * workspace.element_size(), B, H, Hkv, Sq, Sk,
-                                      D, int(window), int(sinks), float(scale), code), ts)
+    _launch("fa_bwd_window", stream, ts, workspace.numel() * workspace.element_size(), B, H, Hkv, Sq, Sk, D,
+            int(window), int(sinks), float(scale), code)
 
 
 def fa_bwd_window_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
@@ -553,10 +553,9 @@ def fa_bwd_window_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlen
     _need_contig(workspace)
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     ts = (q, k, v, o, dout, lse, dq, dk, dv, workspace)
-    _launch("fa_bwd_window_varlen", stream,
-            (*map(_ptr, ts), workspace.numel() * workspace.element_size(), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), n,
-             Tq, Tk, int(max_seqlen_q), int(max_seqlen_k), H, Hkv, D, int(window), int(sinks), float(scale), code),
-            (*ts, cu_seqlens_q, cu_seqlens_k))
+    _launch("fa_bwd_window_varlen", stream, ts, workspace.numel() * workspace.element_size(), cu_seqlens_q.data_ptr(),
+            cu_seqlens_k.data_ptr(), n, Tq, Tk, int(max_seqlen_q), int(max_seqlen_k), H, Hkv, D, int(window),
+            int(sinks), float(scale), code, index=(cu_seqlens_q, cu_seqlens_k))
 
 
 def flash_attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None, stream=None):
@@ -646,9 +645,8 @@ def _kv_q4(fn, k, v, cache, block_table, cu_seqlens, max_seqlen, starts, stream)
     _expect("block_table", block_table, (n, block_table.shape[-1]), torch.int32)
     if starts is not None:
         _expect("starts", starts, (n,), torch.int32)
-    args = (_ptr(k), _ptr(v), *map(_ptr, cache), _ptr(block_table), _ptr(cu_seqlens), _ptr(starts), n, total,
-            int(max_seqlen), Hkv, D, num_blocks, block_size, block_table.shape[1], code)
-    _launch(fn, stream, args, (k, v, *cache, block_table, cu_seqlens, starts))
+    _launch(fn, stream, (k, v, *cache, block_table, cu_seqlens, starts), n, total, int(max_seqlen), Hkv, D,
+            num_blocks, block_size, block_table.shape[1], code)
 
 
 def fa_kv_write_q4(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, max_seqlen: int, starts=None,
@@ -668,7 +666,10 @@ def fa_kv_read_q4(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_se
 
 def fa_decode_splits(B: int, H: int, Hkv: int, max_keys: int) -> int:
     """A num_splits that fills the current GPU (see include/fa.h)."""
-    return int(load_library().fa_decode_splits(B, H, Hkv, max_keys))
+    call = _entry.get("fa_decode_splits")
+    if call is None:
+        call = _entry["fa_decode_splits"] = load_library().fa_decode_splits
+    return call(B, H, Hkv, max_keys)
 
 
 def _decode_gqa(fn, q, cache, page_shape, block_table, seq_lens, o, lse, o_part, m_part, l_part, counters, num_splits,
@@ -682,17 +683,14 @@ def _decode_gqa(fn, q, cache, page_shape, block_table, seq_lens, o, lse, o_part,
     _expect("seq_lens", seq_lens, (B,), torch.int32)
     _expect("o", o, (B, H, 1, D), q.dtype)
     _expect("lse", lse, (B, H), torch.float32)
-    for name, t, need in (("o_part", o_part, B * H * S * D), ("m_part", m_part, B * H * S),
-                          ("l_part", l_part, B * H * S)):
-        if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() < need:
-            raise ValueError(f"{name} must be contiguous float32 of at least {need} elements")
-    if counters.dtype != torch.int32 or not counters.is_contiguous() or counters.numel() < B * H:
-        raise ValueError(f"counters must be contiguous int32 of at least {B * H} elements")
+    rows = B * H * S
+    for name, t, need, dtype in (("o_part", o_part, rows * D, torch.float32), ("m_part", m_part, rows, torch.float32),
+                                 ("l_part", l_part, rows, torch.float32), ("counters", counters, B * H, torch.int32)):
+        if t.numel() < need or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {dtype} of at least {need} elements")
     scale = 1.0 / math.sqrt(D) if scale is None else scale
-    outs = (o, lse, o_part, m_part, l_part, counters)
-    args = (_ptr(q), *map(_ptr, cache), _ptr(block_table), _ptr(seq_lens), *map(_ptr, outs), B, H, Hkv, D, num_blocks,
-            block_size, block_table.shape[1], S, int(window), int(sinks), float(scale), code)
-    _launch(fn, stream, args, (q, *cache, block_table, seq_lens, *outs))
+    _launch(fn, stream, (q, *cache, block_table, seq_lens, o, lse, o_part, m_part, l_part, counters), B, H, Hkv, D,
+            num_blocks, block_size, block_table.shape[1], S, int(window), int(sinks), float(scale), code)
 
 
 def fa_decode_paged_window(q, k_cache, v_cache, block_table, seq_lens, o, lse, o_part, m_part, l_part, counters,
@@ -741,17 +739,17 @@ def _flash_decode_gqa(fn, q, cache, block_table, seq_lens, window, sinks, num_sp
     if q.dim() != 4 or cache[0].dim() != 4 or block_table.dim() != 2:
         raise ValueError("q must be [B,H,1,D], pages 4-dimensional and block_table [B,max_blocks]")
     B, H, _, D = q.shape
+    _, Hkv, block_size, _ = cache[0].shape
     if num_splits is None:
-        keys = block_table.shape[1] * cache[0].shape[2]
+        keys = block_table.shape[1] * block_size
         if window > 0:
             keys = min(keys, window + sinks)
-        num_splits = fa_decode_splits(B, H, cache[0].shape[1], keys)
+        num_splits = fa_decode_splits(B, H, Hkv, keys)
         if workspace is not None:
             num_splits = min(num_splits, workspace[1].numel() // (B * H))
     if workspace is None:
         workspace = _decode_workspace(B, H, num_splits, D, q.device, True)
-    o = torch.empty(B, H, 1, D, dtype=q.dtype, device=q.device)
-    lse = torch.empty(B, H, dtype=torch.float32, device=q.device)
+    o, lse = torch.empty_like(q), torch.empty((B, H), dtype=torch.float32, device=q.device)
     fn(q, *cache, block_table, seq_lens, o, lse, *workspace, num_splits, window, sinks, scale, stream)
     return o, lse
 

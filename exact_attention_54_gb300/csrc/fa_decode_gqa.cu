@@ -5,6 +5,10 @@
 // A warp takes 16 keys at a time, straight from global memory into the
 // registers that feed the products (8 KB a tile at D = 128): the next tile's
 // keys and values are loaded as soon as the products have taken this one's.
+// (Tensor copies into a ring per warp, two tiles ahead, were as fast per byte
+// and started later: 55 us against 52 us for 16 sequences of 4100 visible keys
+// and 8 key heads, where the bytes alone take 40 us and a launch with nothing to
+// read 6 us.)
 // Per query head it keeps a running maximum m of the scores in base-2 units
 // (moved only when a score exceeds it by 2^8), l = sum 2^(x - m) and
 // O = sum 2^(x - m) v; the weights are rounded to the cache's type for the
@@ -17,6 +21,9 @@
 namespace fa {
 namespace gqa {
 
+template <int NT>
+constexpr int kWindowCtas = NT == 1 ? 3 : 2;  // per SM
+
 template <int D>
 struct Tile16 {
     static constexpr int kKWords = D / 8, kVWords = D / 16;
@@ -27,7 +34,7 @@ struct Tile16 {
 };
 
 template <int D, bool BF16, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) fa_decode_window_kernel(const GqaDecodeParams p) {
+__global__ void __launch_bounds__(kThreads, kWindowCtas<NT>) fa_decode_window_kernel(const GqaDecodeParams p) {
     using T = Tile16<D>;
     constexpr int MT = D / 16, HT = 8 * NT, kRow = 2 * D;
     __shared__ Plan<16, HT> plan;
@@ -255,42 +262,50 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) fa_decode_window_ke
 }
 
 template <int D, bool BF16, int NT>
-static cudaError_t launch_t(const GqaDecodeParams &p, unsigned grid, cudaStream_t st) {
+static cudaError_t launch_t(GqaDecodeParams p, int sms, cudaStream_t st) {
+    const unsigned grid = decode_gqa_grid(p, sms, kWindowCtas<NT>, 8 * NT);
     fa_decode_window_kernel<D, BF16, NT><<<grid, kThreads, 0, st>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace gqa
 
+// Whether the balanced plan serves: the tables hold more than 32 tiles of 16
+// keys for each CTA of a wave (the plan costs a CTA about 2 us), and all tiles
+// can be counted in 32 bits.
+static bool gqa_balanced(long long units, long long keys, long long wave) {
+    const long long tiles = units * (keys / 16 + 2);
+    return tiles > 32 * wave && tiles <= INT_MAX;
+}
+
 int decode_gqa_splits(int sms, int B, int H, int Hkv, int max_keys) {
-    // The balanced plan cuts the longest sequence into as many parts as its
-    // share of the batch asks for: enough for one sequence of twice the mean
-    // length on four CTAs per SM, and two more for parts that straddle units.
     const int group = H / Hkv < 1 ? 1 : H / Hkv;
     const long long units = static_cast<long long>(B) * Hkv * ((group + 15) / 16);
-    const long long s = 8LL * sms / units + 3;
-    const long long most = (static_cast<long long>(max_keys) + 127) / 128 + 1;  // runs of at least 128 keys
-    return static_cast<int>(s < most ? (s < 64 ? s : 64) : (most < 64 ? most : 64));
+    const long long wave = 3LL * sms;
+    // Little work: one wave of CTAs, none with fewer than 256 keys (joining
+    // parts costs 4 us, a second wave as much again). More: the balanced plan,
+    // which cuts the longest sequence into as many parts as its share of the
+    // batch asks for, and two more for parts that straddle units.
+    const long long plain = wave / units > 1 ? wave / units : 1, keys = (static_cast<long long>(max_keys) + 255) / 256;
+    const long long balanced = 8LL * sms / units + 3;
+    const long long s = gqa_balanced(units, max_keys, wave) ? balanced : (plain < keys ? plain : keys);
+    return static_cast<int>(s < 64 ? s : 64);
 }
 
 unsigned decode_gqa_grid(GqaDecodeParams &p, int sms, int ctas_per_sm, int heads_per_unit) {
     const long long units = static_cast<long long>(p.B) * p.Hkv * ((p.group + heads_per_unit - 1) / heads_per_unit);
     const long long all = units * p.num_splits, wave = static_cast<long long>(sms) * ctas_per_sm;
-    // Balanced where the tables hold more than a few tiles for each CTA of a
-    // wave: the plan costs a CTA about 2 us.
-    const long long keys = static_cast<long long>(p.max_blocks) << p.log2_bs;
-    const long long seen = p.window > 0 && static_cast<long long>(p.window) + p.sinks < keys ? p.window + p.sinks : keys;
-    const long long tiles = units * (seen / 16 + 2);
-    p.balanced = p.num_splits > 1 && p.B <= gqa::kPlanSeqs && tiles > 32 * wave && tiles <= INT_MAX;
+    const long long cap = static_cast<long long>(p.max_blocks) << p.log2_bs;
+    const long long seen = p.window > 0 && static_cast<long long>(p.window) + p.sinks < cap ? p.window + p.sinks : cap;
+    p.balanced = p.num_splits > 1 && p.B <= gqa::kPlanSeqs && gqa_balanced(units, seen, wave);
     return static_cast<unsigned>(p.balanced && wave < all ? wave : all);
 }
 
-cudaError_t launch_decode_window(int D, bool bf16, GqaDecodeParams p, int sms, cudaStream_t st) {
+cudaError_t launch_decode_window(int D, bool bf16, const GqaDecodeParams &p, int sms, cudaStream_t st) {
     // one column tile of 8 query heads, or two where a group has more
     const int NT = p.group > 8 ? 2 : 1;
-    const unsigned grid = decode_gqa_grid(p, sms, NT == 1 ? 3 : 2, 8 * NT);
 #define FA_GQA(DD, BB, NN) \
-    if (D == DD && bf16 == BB && NT == NN) return gqa::launch_t<DD, BB, NN>(p, grid, st);
+    if (D == DD && bf16 == BB && NT == NN) return gqa::launch_t<DD, BB, NN>(p, sms, st);
     FA_GQA(64, false, 1) FA_GQA(64, false, 2) FA_GQA(64, true, 1) FA_GQA(64, true, 2)
     FA_GQA(128, false, 1) FA_GQA(128, false, 2) FA_GQA(128, true, 1) FA_GQA(128, true, 2)
 #undef FA_GQA

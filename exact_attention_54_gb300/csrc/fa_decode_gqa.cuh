@@ -304,13 +304,17 @@ __device__ __forceinline__ void merge(const GqaDecodeParams &p, const Part &job,
     }
     // ---- the last part of these heads merges them: a warp per head ----
     __shared__ int is_last;
-    if (splits > 1) __threadfence();
     __syncthreads();
     if (splits == 1) return;
-    if (threadIdx.x == 0) is_last = atomicAdd(p.counters + unit, 1) == splits - 1;
+    if (threadIdx.x == 0) {
+        // the barriers order the CTA's writes before this thread's fence, and
+        // its second fence before the CTA's reads
+        __threadfence();
+        is_last = atomicAdd(p.counters + unit, 1) == splits - 1;
+        __threadfence();
+    }
     __syncthreads();
     if (!is_last) return;
-    __threadfence();
     for (int h = warp; h < heads; h += kWarps) {
         const size_t at = (bh0 + h) * stride;
         float M = -CUDART_INF_F;

@@ -517,23 +517,24 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
 }
 
 template <int D, bool BF16, int NT>
-static cudaError_t launch_t(const GqaDecodeParams &p, unsigned grid, cudaStream_t st) {
+static cudaError_t launch_t(GqaDecodeParams p, int sms, cudaStream_t st) {
+    using S = Q4Shape<D, NT>;
     auto kern = fa_decode_q4_kernel<D, BF16, NT>;
-    constexpr int kSmem = Q4Shape<D, NT>::kSmemBytes;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const unsigned grid = decode_gqa_grid(p, sms, S::kCtas, 8 * NT);
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), S::kSmemBytes, done);
     if (e != cudaSuccess) return e;
-    kern<<<grid, kThreads, kSmem, st>>>(p);
+    kern<<<grid, kThreads, S::kSmemBytes, st>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace gqa
 
-cudaError_t launch_decode_q4(int D, bool bf16, GqaDecodeParams p, int sms, cudaStream_t st) {
+cudaError_t launch_decode_q4(int D, bool bf16, const GqaDecodeParams &p, int sms, cudaStream_t st) {
     // one column tile of 8 query heads, or two where a group has more
     const int NT = p.group > 8 ? 2 : 1;
-    const unsigned grid = decode_gqa_grid(p, sms, NT == 1 ? gqa::Q4Shape<128, 1>::kCtas : gqa::Q4Shape<128, 2>::kCtas, 8 * NT);
 #define FA_Q4(DD, BB, NN) \
-    if (D == DD && bf16 == BB && NT == NN) return gqa::launch_t<DD, BB, NN>(p, grid, st);
+    if (D == DD && bf16 == BB && NT == NN) return gqa::launch_t<DD, BB, NN>(p, sms, st);
     FA_Q4(64, false, 1) FA_Q4(64, false, 2) FA_Q4(64, true, 1) FA_Q4(64, true, 2)
     FA_Q4(128, false, 1) FA_Q4(128, false, 2) FA_Q4(128, true, 1) FA_Q4(128, true, 2)
 #undef FA_Q4

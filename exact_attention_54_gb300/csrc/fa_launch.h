@@ -4,9 +4,24 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 namespace fa {
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device.
+// Set once per device and kernel (`done`: a static of the caller's, one bit
+// per device): the attribute stays, and setting it costs a launch's time.
+inline cudaError_t allow_smem(const void *kern, int bytes, std::atomic<unsigned long long> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Values written to the device error word: a kernel abandoned a wait, met an
 // out-of-range device-side index (a page number in a block table), or found
@@ -204,8 +219,8 @@ struct GqaDecodeParams {
     int *err;                   // device error word
 };
 
-cudaError_t launch_decode_window(int D, bool bf16, GqaDecodeParams p, int sms, cudaStream_t stream);
-cudaError_t launch_decode_q4(int D, bool bf16, GqaDecodeParams p, int sms, cudaStream_t stream);
+cudaError_t launch_decode_window(int D, bool bf16, const GqaDecodeParams &p, int sms, cudaStream_t stream);
+cudaError_t launch_decode_q4(int D, bool bf16, const GqaDecodeParams &p, int sms, cudaStream_t stream);
 // CTAs of either launch: a wave of ctas_per_sm per SM where the balanced plan
 // serves, else one per unit (heads_per_unit query heads) and partition (sets p.balanced).
 unsigned decode_gqa_grid(GqaDecodeParams &p, int sms, int ctas_per_sm, int heads_per_unit);
