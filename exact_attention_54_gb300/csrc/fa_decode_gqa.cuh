@@ -81,17 +81,12 @@ __device__ __forceinline__ void load_words(uint32_t *r, const void *p) {
         asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(r[0]) : "l"(p));
 }
 
-// Two fp16 values: the larger of each; whether both a <= b.
-__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
+// Two fp16 values: a - b.
+__device__ __forceinline__ uint32_t sub16x2(uint32_t a, uint32_t b) {
     uint32_t d;
-    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-__device__ __forceinline__ bool both_le16x2(uint32_t a, uint32_t b) {
-    const __half2 x = *reinterpret_cast<const __half2 *>(&a), y = *reinterpret_cast<const __half2 *>(&b);
-    return __hble2(x, y);
-}
-
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));

@@ -11,7 +11,8 @@
 // 16-bit lane is the fp16 number u 2^-24 and nibble 1 is u 2^-20 (below the
 // normal numbers, which the tensor core takes exactly), so two values cost one
 // logical operation. The factor 16 goes into q (keys) or stays in the rows of
-// O (values); the term in 8 is one more product with a constant matrix. The
+// O (values); the term in 8 is where the sum starts (keys: it is the same for
+// all of them) or one more product with a constant matrix (values). The
 // weights p_j s_j are rounded to fp16 (11 bits, for either type of cache)
 // after a power-of-two factor r per head and column group that keeps the
 // largest of them near 1 whatever the scales; products are exact, sums fp32.
@@ -42,8 +43,10 @@ struct Q4Shape {
     static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
     static constexpr int kMergeBytes = kWarps * 8 * NT * D * 4;
     static constexpr int kBars = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;  // offset of the barriers
-    static constexpr int kQ = kBars + kWarps * kStages * 8;  // offset of Q's fragments: [NT][kW][32 lanes][4 words]
-    static constexpr int kSmemBytes = kQ + NT * kW * 512;
+    // offsets of Q's fragments and of -8 sum q as accumulators: [NT][kW][32 lanes][4 words]
+    static constexpr int kSeen = kBars + kWarps * kStages * 8;  // offset of the stages' visible keys
+    static constexpr int kQ = kSeen + kWarps * kStages * 4, kQSum = kQ + NT * kW * 512;
+    static constexpr int kSmemBytes = kQSum + NT * kW * 512;
     static constexpr int kCtas = NT == 1 ? 4 : 2;  // per SM
 };
 
@@ -55,6 +58,11 @@ __device__ __forceinline__ void unpack_codes(uint32_t x, uint32_t (&out)[4]) {
     out[1] = x & 0x00f000f0u;
     out[2] = y & 0x000f000fu;
     out[3] = y & 0x00f000f0u;
+}
+// ... less 8.
+__device__ __forceinline__ void minus8(uint32_t (&x)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = sub16x2(x[i], i % 2 == 0 ? 0x00080008u : 0x00800080u);
 }
 constexpr uint32_t kMinus8Lo = 0x80088008u;  // fp16 pair -8 2^-24
 constexpr uint32_t kMinus8Hi = 0x80808080u;  // fp16 pair -8 2^-20
@@ -72,6 +80,8 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
     const bool ring = p.log2_bs >= 4;  // 16 keys of a page follow one another: bulk copies
     const uint32_t stage0 = ptx::smem_addr(smem) + warp * S::kStages * S::kStageBytes;
     const uint32_t bars = ptx::smem_addr(smem) + S::kBars + warp * S::kStages * 8;
+    const uint32_t seen_at = ptx::smem_addr(smem) + S::kSeen + warp * S::kStages * 4;
+    const unsigned page_mask = (1u << p.log2_bs) - 1;
     if (lane == 0) {
         for (int st = 0; st < S::kStages; ++st) ptx::bar_init(bars + 8 * st, 1);
         ptx::bar_init_fence();
@@ -105,30 +115,38 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
     };
     int base = 0;  // tile of pages0, lane 0
     int pages0 = page_of(lane / 2), pages1 = page_of(16 + lane / 2);
-    auto page_at = [&](int i, int half) {
-        const int src = 2 * (i & 15) + half;
-        const int a = __shfl_sync(kFull, pages0, src), b = __shfl_sync(kFull, pages1, src);
-        return i - base < 16 ? a : b;
-    };
 
     // ---- bulk copies: lanes 0..7 take one array of one half each ----
-    const int arr = lane & 3, half_l = (lane >> 2) & 1;
+    const int arr = lane & 3;
+    const bool half_l = (lane & 4) != 0;
     const char *const arr_base = static_cast<const char *>(arr == 0 ? p.k : arr == 1 ? p.v : arr == 2 ? p.ks : p.vs);
     const unsigned arr_row = arr < 2 ? S::kRow : S::kSRow;
     const uint32_t arr_dst = stage0 + (arr == 0 ? 0 : arr == 1 ? S::kV : arr == 2 ? S::kKS : S::kVS) +
-                             16 * half_l * arr_row;
-    auto start = [&](int i, int st) {
-        const int page = page_at(i, half_l);
-        const unsigned there = __ballot_sync(kFull, page >= 0);
-        if (lane == 0)
-            ptx::bar_arrive_expect_tx(bars + 8 * st, ((there & 1u) + ((there >> 4) & 1u)) * (S::kStageBytes / 2));
+                             (half_l ? 16 * arr_row : 0u);
+    // Tiles are started in order. Leaves the tile's visible keys with its stage.
+    auto start = [&](int i, int stage) {
+        if (i - base == 16) {
+            base += 16;
+            pages0 = pages1;
+            pages1 = page_of(base + 16 + lane / 2);
+        }
+        const int key0 = key0_of(i);
+        const int page_a = __shfl_sync(kFull, pages0, 2 * (i & 15)), page_b = __shfl_sync(kFull, pages0, 2 * (i & 15) + 1);
+        uint32_t seen = kFull;
+        if ((page_a | page_b) < 0 || key0 < list.w_lo || key0 + 32 > list.L)
+            seen = __ballot_sync(kFull, (lane < 16 ? page_a : page_b) >= 0 && list.sees(key0 + lane));
+        if (lane == 0) {
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(seen_at + 4 * stage), "r"(seen) : "memory");
+            ptx::bar_arrive_expect_tx(bars + 8 * stage, ((page_a >= 0) + (page_b >= 0)) * (S::kStageBytes / 2));
+        }
+        const int page = half_l ? page_b : page_a;
         if (lane < 8 && page >= 0) {
-            const unsigned in_page = (key0_of(i) + 16 * half_l) & ((1u << p.log2_bs) - 1);
+            const unsigned in_page = (key0 + (half_l ? 16 : 0)) & page_mask;
             const char *src = arr_base +
                               static_cast<unsigned long long>(static_cast<unsigned>(page) * p.Hkv + job.hk) *
                                   (arr_row << p.log2_bs) +
                               in_page * arr_row;
-            ptx::bulk_load(arr_dst + st * S::kStageBytes, src, 16 * arr_row, bars + 8 * st);
+            ptx::bulk_load(arr_dst + stage * S::kStageBytes, src, 16 * arr_row, bars + 8 * stage);
         }
         __syncwarp();
     };
@@ -204,10 +222,16 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
                 const float by = i % 2 == 0 ? up : up * 0.0625f;
                 f[i] = pack16<false>(x[w][i] * by, x[w][4 + i] * by);
             }
-            // every warp has the same: one writes
-            if (warp == 0)
+            // -8 sum_d q_d of the group, where the product of a tile starts
+            float acc[4];
+            mma16816<false>(acc, kMinus8Lo, kMinus8Lo, kMinus8Hi, kMinus8Hi, f[0], f[1], 0.f, 0.f, 0.f, 0.f);
+            mma16816<false>(acc, kMinus8Lo, kMinus8Lo, kMinus8Hi, kMinus8Hi, f[2], f[3]);
+            if (warp == 0) {  // every warp has the same: one writes
                 *reinterpret_cast<uint4 *>(smem + S::kQ + (t * W + w) * 512 + 16 * lane) =
                     make_uint4(f[0], f[1], f[2], f[3]);
+                *reinterpret_cast<float4 *>(smem + S::kQSum + (t * W + w) * 512 + 16 * lane) =
+                    make_float4(acc[0], acc[1], acc[2], acc[3]);
+            }
         }
         to_log2[t][0] = __shfl_sync(kFull, down, 8 * c);
         to_log2[t][1] = __shfl_sync(kFull, down, 8 * c + 4);
@@ -263,9 +287,11 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
                 for (int n = 0; n < NT; ++n) {
                     uint32_t q[4];
                     shared_words<4>(q, q_at + (n * W + w) * 512);
+                    uint32_t start_at[4];
+                    shared_words<4>(start_at, q_at + S::kQSum - S::kQ + (n * W + w) * 512);
                     float acc[4];
-                    mma16816<false>(acc, kMinus8Lo, kMinus8Lo, kMinus8Hi, kMinus8Hi, q[0], q[1], 0.f, 0.f, 0.f, 0.f);
-                    mma16816<false>(acc, kMinus8Lo, kMinus8Lo, kMinus8Hi, kMinus8Hi, q[2], q[3]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[j] = __uint_as_float(start_at[j]);
                     mma16816<false>(acc, a[0][0], a[1][0], a[0][1], a[1][1], q[0], q[1]);
                     mma16816<false>(acc, a[0][2], a[1][2], a[0][3], a[1][3], q[2], q[3]);
 #pragma unroll
@@ -289,17 +315,18 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
         }
         // ---- weights, maximum moved when a score exceeds it by 2^8 ----
         float e[2][NT][4];  // exponents x to_log2 - m
-        bool move = false;
+        float most_e[NT];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    e[h][n][k] = fmaf(x[h][n][k], to_log2[n][k % 2], -m[n][k % 2]);
-                    move |= e[h][n][k] > kMoveMax;
-                }
-        if (__any_sync(kFull, move)) {
+                for (int k = 0; k < 4; ++k) e[h][n][k] = fmaf(x[h][n][k], to_log2[n][k % 2], -m[n][k % 2]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            most_e[n] = fmaxf(ptx::fmax3(ptx::fmax3(e[0][n][0], e[0][n][1], e[0][n][2]),
+                                         ptx::fmax3(e[0][n][3], e[1][n][0], e[1][n][1]), e[1][n][2]), e[1][n][3]);
+        if (__any_sync(kFull, (NT == 1 ? most_e[0] : fmaxf(most_e[0], most_e[NT - 1])) > kMoveMax)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float a[2];
@@ -434,12 +461,13 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
                 uint32_t a0[4], a1[4];
                 unpack_codes(__byte_perm(v[0][w / 2], v[1][w / 2], sel), a0);
                 unpack_codes(__byte_perm(v[2][w / 2], v[3][w / 2], sel), a1);
+                minus8(a0);
+                minus8(a1);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const uint32_t b0 = transpose8x8(pw[n][w][0]), b1 = transpose8x8(pw[n][w][1]);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        mma16816<false>(o[2 * w + i][n], kMinus8Lo, kMinus8Hi, kMinus8Lo, kMinus8Hi, b0, b1);
                         mma16816<false>(o[2 * w + i][n], a0[2 * i], a0[2 * i + 1], a1[2 * i], a1[2 * i + 1], b0, b1);
                     }
                 }
@@ -451,21 +479,15 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
         int done = 0;
         bool timed_out = false;
         for (; done < mine; ++done) {
-            const int key0 = key0_of(done);
-            const int page = page_at(done, lane >> 4);
-            const uint32_t seen = __ballot_sync(kFull, page >= 0 && list.sees(key0 + lane));
             if (!ptx::warp_all(ptx::bar_wait(bars + 8 * st, parity, nullptr, kWaitTimeoutNs))) {
                 timed_out = true;
                 break;
             }
+            uint32_t seen;
+            shared_words<1>(&seen, seen_at + 4 * st);
             consume(stage0 + st * S::kStageBytes, seen);
             __syncwarp();  // the stage is read: it may be filled again
             if (done + S::kStages < mine) start(done + S::kStages, st);
-            if (done + 1 - base >= 16) {
-                base += 16;
-                pages0 = pages1;
-                pages1 = page_of(base + 16 + lane / 2);
-            }
             if (++st == S::kStages) {
                 st = 0;
                 parity ^= 1;
