@@ -19,13 +19,26 @@
 //
 // What bounds it: HBM wants 24 bytes (48 values) per SM and cycle, so the few
 // instructions a value costs fill the issue slots; everything above is there
-// to save instructions. Tiles of 32 keys come by bulk copies into a ring per
-// warp (4.5 KB a tile at D = 128, two in flight), which leaves the registers
-// to the accumulators: four CTAs (16 warps) per SM.
+// to save instructions. Tiles of 32 keys come by asynchronous copies into a
+// ring per warp (4.5 KB a tile at D = 128, two in flight), which leaves the
+// registers to the accumulators: four CTAs (16 warps) per SM. (Bulk copies,
+// eight per tile with 16-key pages, cost a loop over the issuing lanes each:
+// 128 us against Q4US us for 16 sequences of 16384 to 32768 keys, 8 key heads;
+// the bytes alone take 70 us.)
 #include "fa_decode_gqa.cuh"
 
 namespace fa {
 namespace gqa {
+
+// 16 bytes from global to shared memory, in this thread's current copy group.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>  // wait until all but the newest N groups have landed
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 constexpr float kMostWeight = 2.f;  // weights of this size and more choose their factor r again
 constexpr float kMostFactor = 1.2676506002282294e30f;  // 2^100: r before any weight is known
@@ -42,9 +55,9 @@ struct Q4Shape {
     static constexpr int kStageBytes = kVS + kTile * kSRow;
     static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
     static constexpr int kMergeBytes = kWarps * 8 * NT * D * 4;
-    static constexpr int kBars = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;  // offset of the barriers
-    // offsets of Q's fragments and of -8 sum q as accumulators: [NT][kW][32 lanes][4 words]
-    static constexpr int kSeen = kBars + kWarps * kStages * 8;  // offset of the stages' visible keys
+    // offsets of the stages' visible keys, of Q's fragments and of -8 sum q as
+    // accumulators ([NT][kW][32 lanes][4 words])
+    static constexpr int kSeen = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
     static constexpr int kQ = kSeen + kWarps * kStages * 4, kQSum = kQ + NT * kW * 512;
     static constexpr int kSmemBytes = kQSum + NT * kW * 512;
     static constexpr int kCtas = NT == 1 ? 4 : 2;  // per SM
@@ -77,18 +90,11 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
     auto sm_o = reinterpret_cast<float (*)[HT][D]>(smem);  // over the rings, once every warp is done with its own
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int g = lane / 4, c = lane % 4;
-    const bool ring = p.log2_bs >= 4;  // 16 keys of a page follow one another: bulk copies
-    const uint32_t stage0 = ptx::smem_addr(smem) + warp * S::kStages * S::kStageBytes;
-    const uint32_t bars = ptx::smem_addr(smem) + S::kBars + warp * S::kStages * 8;
+    const bool ring = p.log2_bs >= 4;  // 16 keys of a page follow one another
+    uint8_t *const my_ring = smem + warp * S::kStages * S::kStageBytes;
+    const uint32_t stage0 = ptx::smem_addr(my_ring);
     const uint32_t seen_at = ptx::smem_addr(smem) + S::kSeen + warp * S::kStages * 4;
     const unsigned page_mask = (1u << p.log2_bs) - 1;
-    if (lane == 0) {
-        for (int st = 0; st < S::kStages; ++st) ptx::bar_init(bars + 8 * st, 1);
-        ptx::bar_init_fence();
-    }
-    __syncwarp();
-    int st = 0;  // ring stage of the next tile, and the parity of its phase
-    uint32_t parity = 0;
     plan.make(p);
     for (;;) {
     plan.next(p);
@@ -116,39 +122,47 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
     int base = 0;  // tile of pages0, lane 0
     int pages0 = page_of(lane / 2), pages1 = page_of(16 + lane / 2);
 
-    // ---- bulk copies: lanes 0..7 take one array of one half each ----
-    const int arr = lane & 3;
-    const bool half_l = (lane & 4) != 0;
-    const char *const arr_base = static_cast<const char *>(arr == 0 ? p.k : arr == 1 ? p.v : arr == 2 ? p.ks : p.vs);
-    const unsigned arr_row = arr < 2 ? S::kRow : S::kSRow;
-    const uint32_t arr_dst = stage0 + (arr == 0 ? 0 : arr == 1 ? S::kV : arr == 2 ? S::kKS : S::kVS) +
-                             (half_l ? 16 * arr_row : 0u);
-    // Tiles are started in order. Leaves the tile's visible keys with its stage.
+    // ---- asynchronous copies, 16 bytes a lane: 16 keys' codes are 16 kRow
+    // bytes in a row of each array, their scales 16 kSRow bytes ----
+    const bool v_scales = lane >= 16;  // the scales: half a warp each
+    const bool scale_lane = (lane & 15) < S::kSRow;
+    const char *const scale_base = static_cast<const char *>(v_scales ? p.vs : p.ks) + 16 * (lane & 15);
+    const uint32_t scale_dst = stage0 + (v_scales ? S::kVS : S::kKS) + 16 * (lane & 15);
+    auto copy_half = [&](int half, int key, int page, uint32_t at) {
+        const unsigned row = static_cast<unsigned>(page) * p.Hkv + job.hk, in_page = key & page_mask;
+        const unsigned long long codes = static_cast<unsigned long long>(row) * (S::kRow << p.log2_bs) +
+                                         in_page * S::kRow + 16 * lane;
+        const char *k = static_cast<const char *>(p.k) + codes, *v = static_cast<const char *>(p.v) + codes;
+#pragma unroll
+        for (int j = 0; j < 16 * S::kRow / 512; ++j) {
+            copy16(at + half * 16 * S::kRow + 512 * j + 16 * lane, k + 512 * j);
+            copy16(at + S::kV + half * 16 * S::kRow + 512 * j + 16 * lane, v + 512 * j);
+        }
+        if (scale_lane)
+            copy16(scale_dst + (at - stage0) + half * 16 * S::kSRow,
+                   scale_base + static_cast<unsigned long long>(row) * (S::kSRow << p.log2_bs) + in_page * S::kSRow);
+    };
+    // Tiles are started in order, one copy group each (empty past the last).
+    // Leaves the tile's visible keys with its stage.
     auto start = [&](int i, int stage) {
-        if (i - base == 16) {
-            base += 16;
-            pages0 = pages1;
-            pages1 = page_of(base + 16 + lane / 2);
+        if (i < mine) {
+            if (i - base == 16) {
+                base += 16;
+                pages0 = pages1;
+                pages1 = page_of(base + 16 + lane / 2);
+            }
+            const int key0 = key0_of(i);
+            const int page_a = __shfl_sync(kFull, pages0, 2 * (i & 15)),
+                      page_b = __shfl_sync(kFull, pages0, 2 * (i & 15) + 1);
+            uint32_t seen = kFull;
+            if ((page_a | page_b) < 0 || key0 < list.w_lo || key0 + 32 > list.L)
+                seen = __ballot_sync(kFull, (lane < 16 ? page_a : page_b) >= 0 && list.sees(key0 + lane));
+            if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(seen_at + 4 * stage), "r"(seen) : "memory");
+            const uint32_t at = stage0 + stage * S::kStageBytes;
+            if (page_a >= 0) copy_half(0, key0, page_a, at);
+            if (page_b >= 0) copy_half(1, key0 + 16, page_b, at);
         }
-        const int key0 = key0_of(i);
-        const int page_a = __shfl_sync(kFull, pages0, 2 * (i & 15)), page_b = __shfl_sync(kFull, pages0, 2 * (i & 15) + 1);
-        uint32_t seen = kFull;
-        if ((page_a | page_b) < 0 || key0 < list.w_lo || key0 + 32 > list.L)
-            seen = __ballot_sync(kFull, (lane < 16 ? page_a : page_b) >= 0 && list.sees(key0 + lane));
-        if (lane == 0) {
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(seen_at + 4 * stage), "r"(seen) : "memory");
-            ptx::bar_arrive_expect_tx(bars + 8 * stage, ((page_a >= 0) + (page_b >= 0)) * (S::kStageBytes / 2));
-        }
-        const int page = half_l ? page_b : page_a;
-        if (lane < 8 && page >= 0) {
-            const unsigned in_page = (key0 + (half_l ? 16 : 0)) & page_mask;
-            const char *src = arr_base +
-                              static_cast<unsigned long long>(static_cast<unsigned>(page) * p.Hkv + job.hk) *
-                                  (arr_row << p.log2_bs) +
-                              in_page * arr_row;
-            ptx::bulk_load(arr_dst + stage * S::kStageBytes, src, 16 * arr_row, bars + 8 * stage);
-        }
-        __syncwarp();
+        copy_commit();
     };
     // Pages of fewer than 16 keys: a lane copies one key's rows by itself.
     // Returns the tile's visible keys.
@@ -162,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
             if (ok) {
                 const size_t row = ((static_cast<size_t>(page) * p.Hkv + job.hk) << p.log2_bs) +
                                    (key & ((1 << p.log2_bs) - 1));
-                uint8_t *dst = smem + warp * S::kStages * S::kStageBytes;
+                uint8_t *dst = my_ring;
                 const uint4 *k = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.k) + row * S::kRow);
                 const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.v) + row * S::kRow);
 #pragma unroll
@@ -184,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
         return seen;
     };
     if (ring)
-        for (int i = 0; i < min(mine, S::kStages); ++i) start(i, st + i < S::kStages ? st + i : st + i - S::kStages);
+        for (int i = 0; i < S::kStages; ++i) start(i, i);
 
     // ---- Q as the B operand: head 8 t + g, in the order of the key words
     // (nibble pairs of group w; the odd ones' q / 16); in shared memory, the
@@ -476,32 +490,17 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
     };
 
     if (ring) {
-        int done = 0;
-        bool timed_out = false;
-        for (; done < mine; ++done) {
-            if (!ptx::warp_all(ptx::bar_wait(bars + 8 * st, parity, nullptr, kWaitTimeoutNs))) {
-                timed_out = true;
-                break;
-            }
+        int st = 0;
+        for (int i = 0; i < mine; ++i) {
+            copy_wait<S::kStages - 1>();  // this lane's copies of tile i, and all lanes' after the barrier
+            __syncwarp();
             uint32_t seen;
             shared_words<1>(&seen, seen_at + 4 * st);
             consume(stage0 + st * S::kStageBytes, seen);
             __syncwarp();  // the stage is read: it may be filled again
-            if (done + S::kStages < mine) start(done + S::kStages, st);
-            if (++st == S::kStages) {
-                st = 0;
-                parity ^= 1;
-            }
+            start(i + S::kStages, st);
+            st = st + 1 == S::kStages ? 0 : st + 1;
         }
-        // after a timeout: wait (again bounded) for the copies still in flight
-        for (int i = done; timed_out && i < min(mine, done + S::kStages); ++i) {
-            ptx::bar_wait(bars + 8 * st, parity, nullptr, kWaitTimeoutNs);
-            if (++st == S::kStages) {
-                st = 0;
-                parity ^= 1;
-            }
-        }
-        if (timed_out && lane == 0) atomicExch(p.err, kDeviceErrTimeout);
     } else {
         for (int i = 0; i < mine; ++i) {
             const uint32_t seen = copy_rows(key0_of(i));
@@ -533,8 +532,7 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
             }
         }
     merge<D, BF16, HT>(p, job, sm_m, sm_l, sm_o);
-    ptx::fence_proxy_async_smem();  // sm_o was read and written; the next part's copies go there
-    __syncthreads();
+    __syncthreads();  // sm_o is read: the next part's copies go there
     }
 }
 
