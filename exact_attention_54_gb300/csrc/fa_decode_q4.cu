@@ -15,7 +15,8 @@
 // all of them) or one more product with a constant matrix (values). The
 // weights p_j s_j are rounded to fp16 (11 bits, for either type of cache)
 // after a power-of-two factor r per head and column group that keeps the
-// largest of them near 1 whatever the scales; products are exact, sums fp32.
+// largest of them between 2^-4 and 2 whatever the scales (a move of m may halve
+// it: weights 2^-20 of the largest keep few bits); products exact, sums fp32.
 //
 // What bounds it: HBM wants 24 bytes (48 values) per SM and cycle, so the few
 // instructions a value costs fill the issue slots; everything above is there
@@ -23,7 +24,7 @@
 // ring per warp (4.5 KB a tile at D = 128, two in flight), which leaves the
 // registers to the accumulators: four CTAs (16 warps) per SM. (Bulk copies,
 // eight per tile with 16-key pages, cost a loop over the issuing lanes each:
-// 128 us against Q4US us for 16 sequences of 16384 to 32768 keys, 8 key heads;
+// 128 us against 120 us for 16 sequences of 16384 to 32768 keys, 8 key heads;
 // the bytes alone take 70 us.)
 #include "fa_decode_gqa.cuh"
 

@@ -77,9 +77,14 @@ def softmax_attention(q, k, v, seen, scale):
 
 def decode(q, values, table, lens, block, window, sinks, scale):
     """q [B,H,1,D]; values(page, head) -> (k, v, s) double [block, D] of one page, s the value's scale (4-bit cache) or
-    0; the definition of the paged decode. Returns o [B,H,D], lse [B,H] and what meets in o: sum p (|v| + s / 4)."""
+    0; the definition of the paged decode. Returns o [B,H,D], lse [B,H], what meets in o: sum p |v|, and ``low``:
+
+    The 4-bit cache's weights p s are rounded to fp16 after a factor r that brings the largest to at least 2^-4, where
+    they lose up to 2^-25 each below the normal numbers: 2^-21 max(p s) |n| in o. r follows the running maximum by
+    whole powers of two, so the largest may halve with each of its moves by 2^8 or more; after M moves p is under
+    2^(8 - 8M), so it is only the largest of p s while s differs by more: M <= 1 + log2(max s / min s) / 8."""
     B, H, _, D = q.shape
-    o, size = torch.zeros(B, H, D, dtype=torch.float64), torch.zeros(B, H, D, dtype=torch.float64)
+    o, size, low = (torch.zeros(B, H, D, dtype=torch.float64) for _ in range(3))
     lse = torch.full((B, H), -math.inf, dtype=torch.float64)
     for b in range(B):
         n = int(lens[b])
@@ -91,29 +96,29 @@ def decode(q, values, table, lens, block, window, sinks, scale):
             pages = {int(x): values(int(table[b, x]), h) for x in torch.unique(keys // block)}
             k = torch.stack([pages[int(j) // block][0][int(j) % block] for j in keys])
             v = torch.stack([pages[int(j) // block][1][int(j) % block] for j in keys])
-            step = torch.stack([pages[int(j) // block][2][int(j) % block] for j in keys])
+            s = torch.stack([pages[int(j) // block][2][int(j) % block] for j in keys])
             r = softmax_attention(q[b, h].double(), k, v, torch.ones(1, len(keys), dtype=torch.bool), scale)
-            o[b, h], lse[b, h], size[b, h] = r[0][0], r[1][0], r[3][0] + (r[2] @ step)[0] / 4
-    return o, lse, size
+            o[b, h], lse[b, h], size[b, h] = r[0][0], r[1][0], r[3][0]
+            if (s > 0).any():
+                moves = 1 + math.floor(math.log2(float(s.max() / s[s > 0].min())) / 8)
+                n = (v / torch.where(s > 0, s, torch.ones_like(s))).abs()
+                low[b, h] = 2.0 ** (moves - 21) * (r[2][0][:, None] * s).amax(0) * n.sum(0)
+    return o, lse, size, low
 
 
-def assert_attention_close(o, lse, ro, rl, size, dtype, what=""):
-    """O within half a step of its own rounding, half a step of the 16-bit type on each weight, and 2^-13 of
-    what meets in the sum for the rest; LSE within 4e-5 + 2^-21 |LSE|.
+def assert_attention_close(o, lse, ro, rl, size, low, dtype, what=""):
+    """O within half a step of its own rounding, half a step of the 16-bit type on each weight, 2^-13 of
+    what meets in the sum for the rest, and ``low`` (see decode); LSE within 4e-5 + 2^-21 |LSE|.
 
     The rest: a score is an fp32 sum of D products, |error| <= 2^-24 * 16 * sum |q k| scale (16: depth of the
     sums), under 2^-24 * 16 * 40 = 2^-14.7 for the inputs here; it enters a weight as a relative error, once in
     the numerator and once in the sum; 2^x and the fp32 sums add a few 2^-22. LSE carries the score's error and
-    the rounding of its own value (fp32, two operations).
-
-    The 4-bit cache's sum of s n is taken as that of s (n + 8) less 8 times that of s: its fp32 terms are up to 23 s
-    where n may be 0. A warp adds up to 11 tiles of 16 keys there, each time off by at most 2^-23 of the partial
-    sum: 11 * 23 * 2^-23 < 2^-15 of sum p s, the 2^-13 of ``size``'s sum p s / 4."""
+    the rounding of its own value (fp32, two operations)."""
     o, lse = o.double().cpu().reshape(ro.shape), lse.double().cpu().reshape(rl.shape)
     assert torch.equal(torch.isnan(o), torch.isnan(ro)) and torch.equal(torch.isnan(lse), torch.isnan(rl)), what
     h = half_step(dtype)
     tiny = torch.finfo(dtype).smallest_normal * h * 2
-    bound = h * ro.abs() * (1 + 2 * h) + (h * (1 + h) + 2.0 ** -13) * size + tiny
+    bound = h * ro.abs() * (1 + 2 * h) + (h * (1 + h) + 2.0 ** -13) * size + low + tiny
     bad = ((o - ro).abs() > bound) & ~torch.isnan(ro)
     assert not bad.any(), (what, "o", float(((o - ro).abs() / bound).nan_to_num().max()), torch.nonzero(bad)[0].tolist())
     empty = torch.isinf(rl)

@@ -153,6 +153,69 @@ def test_matches_definition(q4, H, Hkv, D, block, lens, dtype, window, sinks, sp
     assert_attention_close(o, lse, *ref, dtype)
 
 
+DEALT = [
+    # H, Hkv, D, lens, dtype, window, sinks, splits: tables with room for 46080 keys a sequence and at least 10 units,
+    # 28000 tiles of 16 keys: over 32 for each of the 608 CTAs that 152 SMs hold, so runs of tiles are dealt out
+    (16, 2, 128, [0, 5, 3000, 700, 1], torch.bfloat16, 0, 0, None),
+    (4, 2, 64, [3000, 2800, 3000, 3000, 2999], torch.float16, 0, 0, 2),        # runs as long as a unit
+    (2, 2, 128, [0, 0, 0, 0, 0], torch.float16, 0, 0, 5),
+    (20, 1, 64, [2500, 0, 60, 1024, 1025, 2047, 31, 33, 3], torch.bfloat16, 45000, 700, 7),  # 20 heads to a key head
+    (10, 10, 128, [4000], torch.bfloat16, 45000, 9, 64),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q4", [False, True], ids=["16bit", "q4"])
+@pytest.mark.parametrize("H,Hkv,D,lens,dtype,window,sinks,splits", DEALT)
+def test_tiles_dealt_out_over_one_wave(q4, H, Hkv, D, lens, dtype, window, sinks, splits):
+    block = 1024
+    q, cache, table, sl = make(len(lens), H, Hkv, D, block, lens, dtype, q4, seed=sum(lens) + H)
+    table = torch.nn.functional.pad(table, (0, 45 - table.shape[1]), value=-1)
+    o, lse = run(q, cache, table, sl, window, sinks, q4, num_splits=splits)
+    fa.fa_check_device_error()
+    ref = plain_ops.decode(q, values(cache, q4, H // Hkv), table, lens, block, window, sinks, D ** -0.5)
+    assert_attention_close(o, lse, *ref, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q4", [False, True], ids=["16bit", "q4"])
+@pytest.mark.parametrize("B", [512, 513])
+def test_many_sequences(q4, B):
+    """As many sequences as the dealing out holds, and one more."""
+    H, Hkv, D, block = 2, 1, 64, 64
+    lens = [(37 * b) % 150 for b in range(B)]
+    q, cache, table, sl = make(B, H, Hkv, D, block, lens, torch.float16, q4, seed=B)
+    table = torch.nn.functional.pad(table, (0, 12 - table.shape[1]), value=-1)
+    o, lse = run(q, cache, table, sl, 0, 0, q4, num_splits=3)
+    fa.fa_check_device_error()
+    ref = plain_ops.decode(q, values(cache, q4, H // Hkv), table, lens, block, 0, 0, D ** -0.5)
+    assert_attention_close(o, lse, *ref, torch.float16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q4", [False, True], ids=["16bit", "q4"])
+def test_two_calls_at_once_and_pages_shared(q4):
+    """Two streams, each with its own workspace; sequences that share a prefix's pages; the same call twice gives
+    the same bits."""
+    H, Hkv, D, block, lens = 8, 2, 128, 16, [900, 900, 640]
+    q, cache, table, sl = make(3, H, Hkv, D, block, lens, torch.bfloat16, q4, seed=17)
+    table[1, :30] = table[0, :30]
+    ref = plain_ops.decode(q, values(cache, q4, H // Hkv), table, lens, block, 0, 0, D ** -0.5)
+    dev = tuple(t.cuda() for t in cache)
+    qd, td, sd = q.cuda(), table.cuda(), sl.cuda()
+    f = (lambda: fa.flash_decode_paged_q4(qd, fa.KVCacheQ4(*dev), td, sd)) if q4 else \
+        (lambda: fa.flash_decode_paged_window(qd, *dev, td, sd, 0))
+    torch.cuda.synchronize()
+    streams, out = [torch.cuda.Stream() for _ in range(2)], []
+    for i in range(8):
+        with torch.cuda.stream(streams[i % 2]):
+            out.append(f())
+    torch.cuda.synchronize()
+    fa.fa_check_device_error()
+    assert_attention_close(*out[0], *ref, torch.bfloat16)
+    assert all(torch.equal(a, b) for x in out[1:] for a, b in zip(x, out[0]))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("q4", [False, True], ids=["16bit", "q4"])
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
@@ -175,11 +238,11 @@ def test_sizes_of_values(q4, dtype):
         # scores up to 0.5 * 8 * 128 * 4: their fp32 error is that of sum |q k| scale, at most 2^-24 * 16 * 2000
         # relative in a weight and absolute in LSE, so both bounds are widened by it
         wide = 2.0 ** -24 * 16 * 2000 if scale == 0.5 else 2.0 ** -24 * 16 * 400
-        ro, rl, size = ref
+        ro, rl, size, low = ref
         h = plain_ops.half_step(dtype)
         tiny = torch.finfo(dtype).smallest_normal * 2 * h
         err = (o.double().cpu().view(ro.shape) - ro).abs()
-        assert (err <= h * ro.abs() * 1.01 + (h * 1.01 + 2.0 ** -13 + 2 * wide) * size + tiny).all()
+        assert (err <= h * ro.abs() * 1.01 + (h * 1.01 + 2.0 ** -13 + 2 * wide) * size + low + tiny).all()
         assert ((lse.double().cpu() - rl).abs() <= 4e-5 + wide + 2.0 ** -21 * rl.abs()).all()
 
 

@@ -158,6 +158,11 @@ CASES = [
     (1, 2, 1, 500, 130, 128, torch.bfloat16, 40, 3),          # and with sinks: those alone
     (3, 8, 1, 257, 257, 128, torch.float16, 64, 16),
     (1, 1, 1, 2050, 2050, 64, torch.bfloat16, 511, 5),
+    # few key tiles, each long: cut into segments
+    (1, 16, 1, 1000, 1000, 128, torch.bfloat16, 600, 0),
+    (1, 16, 1, 900, 900, 128, torch.float16, 400, 130),
+    (2, 32, 2, 700, 500, 64, torch.float16, 2000, 3),
+    (1, 32, 1, 300, 520, 128, torch.bfloat16, 250, 0),        # and key tiles that no query sees
 ]
 
 
@@ -188,6 +193,9 @@ PACKED = [
     ([300, 10], [100, 500], 4, 1, 64, torch.bfloat16, 33, 0),                 # rows that see nothing
     ([17] * 300, [17] * 300, 2, 2, 64, torch.bfloat16, 5, 2),                 # more sequences than a schedule table
     ([600, 450, 512], [600, 450, 512], 8, 2, 128, torch.bfloat16, 256, 140),
+    # segments, some of them with nothing to do
+    ([700, 300, 0, 60], [700, 300, 50, 0], 16, 1, 128, torch.bfloat16, 500, 0),
+    ([130, 600], [500, 600], 32, 1, 64, torch.float16, 10 ** 6, 200),
 ]
 
 
@@ -210,6 +218,17 @@ def test_packed_matches_definition(lq, lk, H, Hkv, D, dtype, window, sinks):
         ref = plain_ops.window_attention(t(q[sq]), t(k[sk]), t(v[sk]), window, sinks, D ** -0.5, t(do[sq]), dtype)
         got = {"o": t(o[sq]), "lse": lse[:, sq], "dq": t(dq[sq]), "dk": t(dk[sk]), "dv": t(dv[sk])}
         plain_ops.assert_window_close(got, ref, f"sequence {b}")
+
+
+def test_long_key_tiles_take_more_workspace(lib):
+    """The cases above that are to be cut into segments are."""
+    for B, H, Hkv, Sq, Sk, D, _, window, sinks in CASES[-4:]:
+        assert lib.fa_bwd_window_workspace_bytes(B, H, Hkv, Sq, Sk, D, window, sinks) >= \
+            lib.fa_bwd_workspace_bytes(B, H, Sq, D) + B * Hkv * 2 * 128 * D * 4 * 8
+    for lq, lk, H, Hkv, D, _, window, sinks in PACKED[-2:]:
+        assert lib.fa_bwd_window_varlen_workspace_bytes(len(lq), sum(lq), max(lq), max(lk), H, Hkv, D, window,
+                                                        sinks) >= \
+            lib.fa_bwd_varlen_workspace_bytes(sum(lq), H, D) + len(lq) * Hkv * 2 * 128 * D * 4 * 8
 
 
 @pytest.mark.gpu
