@@ -6,13 +6,14 @@
 // its keys; m is moved only when a score exceeds it by 2^8. The cache holds
 // k = s (u - 8), u a nibble, s per 32 columns w, so
 //   x = scale log2(e) sum_w s_w (sum_d q_d u_d - 8 sum_d q_d),
-//   O = sum_j (p_j s_j) u_j - 8 sum_j (p_j s_j).
+//   O = sum_j (p_j s_j) (u_j - 8).
 // A nibble is a number as it stands: masked out of its word, nibble 0 of a
 // 16-bit lane is the fp16 number u 2^-24 and nibble 1 is u 2^-20 (below the
 // normal numbers, which the tensor core takes exactly), so two values cost one
 // logical operation. The factor 16 goes into q (keys) or stays in the rows of
-// O (values); the term in 8 is where the sum starts (keys: it is the same for
-// all of them) or one more product with a constant matrix (values). The
+// O (values); the 8 is where the sum starts (keys: the term is the same for
+// all of them) or goes off pairs of values by one fp16 subtraction, exactly
+// (values: each key has its weight, and no digits are lost to 8 sum p s). The
 // weights p_j s_j are rounded to fp16 (11 bits, for either type of cache)
 // after a power-of-two factor r per head and column group that keeps the
 // largest of them between 2^-4 and 2 whatever the scales (a move of m may halve
