@@ -440,22 +440,30 @@ def _expect(name: str, t, shape, dtype):
 
 
 _entry = {}  # entry points of the loaded library by name
+_raw_stream = torch._C._cuda_getCurrentRawStream  # handle of a device's current stream, without a Stream object
 
 
 def _launch(fn: str, stream, tensors, *args, index=None):
     """Call entry point ``fn`` with the pointers of ``tensors`` (None: NULL), ``args`` and the stream, on the device
     that the tensors, and those of ``index``, share."""
     dev = tensors[0].get_device()
-    for t in tensors if index is None else (*tensors, *index):
-        if t is not None and t.get_device() != dev:
+    ptrs = []
+    for t in tensors:
+        if t is None:
+            ptrs.append(None)
+        elif t.get_device() == dev:
+            ptrs.append(t.data_ptr())
+        else:
+            dev = -1
+    for t in index or ():
+        if t.get_device() != dev:
             dev = -1
     if dev < 0:
         raise ValueError(f"{fn}: all tensors must be on one CUDA device")
     call = _entry.get(fn)
     if call is None:
         call = _entry[fn] = getattr(load_library(), fn)
-    ptrs = [None if t is None else t.data_ptr() for t in tensors]
-    stream = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+    stream = _raw_stream(dev) if stream is None else _stream(stream)
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             st = call(*ptrs, *args, stream)
@@ -624,12 +632,13 @@ def kv_cache_q4(num_blocks: int, Hkv: int, block_size: int, D: int, dtype=torch.
 
 
 def _check_q4(k_codes, k_scales, v_codes, v_scales, Hkv, D, dtype):
-    rows = (k_codes.shape[0], Hkv, k_codes.shape[2]) if k_codes.dim() == 4 else (None, Hkv, None)
-    for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
-        _expect(name, t, rows + (D // 2,), torch.uint8)
-    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        _expect(name, t, rows + (D // FA_Q4_GROUP,), dtype)
-    return rows[0], rows[2]
+    num_blocks, block_size = (k_codes.shape[0], k_codes.shape[2]) if k_codes.dim() == 4 else (None, None)
+    codes, scales = (num_blocks, Hkv, block_size, D // 2), (num_blocks, Hkv, block_size, D // FA_Q4_GROUP)
+    _expect("k_codes", k_codes, codes, torch.uint8)
+    _expect("v_codes", v_codes, codes, torch.uint8)
+    _expect("k_scales", k_scales, scales, dtype)
+    _expect("v_scales", v_scales, scales, dtype)
+    return num_blocks, block_size
 
 
 def _kv_q4(fn, k, v, cache, block_table, cu_seqlens, max_seqlen, starts, stream):
@@ -672,17 +681,27 @@ def fa_decode_splits(B: int, H: int, Hkv: int, max_keys: int) -> int:
     return call(B, H, Hkv, max_keys)
 
 
-def _decode_gqa(fn, q, cache, page_shape, block_table, seq_lens, o, lse, o_part, m_part, l_part, counters, num_splits,
-                window, sinks, scale, stream):
+def _decode_gqa(q, cache, block_table, seq_lens, o, lse, o_part, m_part, l_part, counters, num_splits, window, sinks,
+                scale, stream):
+    if q.dim() != 4 or cache[0].dim() != 4 or block_table.dim() != 2:
+        raise ValueError("q must be [B,H,1,D], pages 4-dimensional and block_table [B,max_blocks]")
     B, H, _, D = q.shape
-    num_blocks, Hkv, block_size = page_shape
-    S = int(num_splits)
+    num_blocks, Hkv, block_size, _ = cache[0].shape
     code = _dtype_code(q)
+    if len(cache) == 4:
+        fn = "fa_decode_paged_q4"
+        _check_q4(*cache, Hkv, D, q.dtype)
+    else:
+        fn = "fa_decode_paged_window"
+        _expect("k_cache", cache[0], (num_blocks, Hkv, block_size, D), q.dtype)
+        _expect("v_cache", cache[1], (num_blocks, Hkv, block_size, D), q.dtype)
+    max_blocks = block_table.shape[1]
     _expect("q", q, (B, H, 1, D), q.dtype)
-    _expect("block_table", block_table, (B, block_table.shape[-1]), torch.int32)
+    _expect("block_table", block_table, (B, max_blocks), torch.int32)
     _expect("seq_lens", seq_lens, (B,), torch.int32)
     _expect("o", o, (B, H, 1, D), q.dtype)
     _expect("lse", lse, (B, H), torch.float32)
+    S = int(num_splits)
     rows = B * H * S
     for name, t, need, dtype in (("o_part", o_part, rows * D, torch.float32), ("m_part", m_part, rows, torch.float32),
                                  ("l_part", l_part, rows, torch.float32), ("counters", counters, B * H, torch.int32)):
@@ -690,7 +709,7 @@ def _decode_gqa(fn, q, cache, page_shape, block_table, seq_lens, o, lse, o_part,
             raise ValueError(f"{name} must be contiguous {dtype} of at least {need} elements")
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     _launch(fn, stream, (q, *cache, block_table, seq_lens, o, lse, o_part, m_part, l_part, counters), B, H, Hkv, D,
-            num_blocks, block_size, block_table.shape[1], S, int(window), int(sinks), float(scale), code)
+            num_blocks, block_size, max_blocks, S, int(window), int(sinks), float(scale), code)
 
 
 def fa_decode_paged_window(q, k_cache, v_cache, block_table, seq_lens, o, lse, o_part, m_part, l_part, counters,
@@ -698,31 +717,21 @@ def fa_decode_paged_window(q, k_cache, v_cache, block_table, seq_lens, o, lse, o
     """One-token attention over a paged cache: q [B,H,1,D]; k_cache, v_cache [num_blocks,Hkv,block_size,D]; the token
     sees its last ``window`` keys (0: all) and the first ``sinks``. o_part [B,H,num_splits,D], m_part and l_part
     [B,H,num_splits] fp32 and counters int32 [B*H] (zero between calls) may be larger than that."""
-    if q.dim() != 4 or k_cache.dim() != 4:
-        raise ValueError("q must be [B,H,1,D] and the caches [num_blocks,Hkv,block_size,D]")
-    num_blocks, Hkv, block_size, _ = k_cache.shape
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _expect(name, t, (num_blocks, Hkv, block_size, q.shape[3]), q.dtype)
-    _decode_gqa("fa_decode_paged_window", q, (k_cache, v_cache), (num_blocks, Hkv, block_size), block_table, seq_lens,
-                o, lse, o_part, m_part, l_part, counters, num_splits, window, sinks, scale, stream)
+    _decode_gqa(q, (k_cache, v_cache), block_table, seq_lens, o, lse, o_part, m_part, l_part, counters, num_splits,
+                window, sinks, scale, stream)
 
 
 def fa_decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, o, lse, o_part, m_part, l_part,
                        counters, num_splits: int, window: int = 0, sinks: int = 0, scale: float | None = None,
                        stream=None):
     """fa_decode_paged_window over the 4-bit cache (scales in the dtype of q)."""
-    if q.dim() != 4 or k_codes.dim() != 4:
-        raise ValueError("q must be [B,H,1,D] and the codes [num_blocks,Hkv,block_size,D/2]")
-    Hkv = k_codes.shape[1]
-    num_blocks, block_size = _check_q4(k_codes, k_scales, v_codes, v_scales, Hkv, q.shape[3], q.dtype)
-    _decode_gqa("fa_decode_paged_q4", q, (k_codes, k_scales, v_codes, v_scales), (num_blocks, Hkv, block_size),
-                block_table, seq_lens, o, lse, o_part, m_part, l_part, counters, num_splits, window, sinks, scale,
-                stream)
+    _decode_gqa(q, (k_codes, k_scales, v_codes, v_scales), block_table, seq_lens, o, lse, o_part, m_part, l_part,
+                counters, num_splits, window, sinks, scale, stream)
 
 
 def flash_kv_write_q4(k, v, cache: KVCacheQ4, block_table, cu_seqlens, max_seqlen: int, starts=None, stream=None):
     """fa_kv_write_q4 into the four tensors of ``cache``."""
-    fa_kv_write_q4(k, v, *cache, block_table, cu_seqlens, max_seqlen, starts, stream)
+    _kv_q4("fa_kv_write_q4", k, v, cache, block_table, cu_seqlens, max_seqlen, starts, stream)
 
 
 def flash_kv_read_q4(cache: KVCacheQ4, block_table, cu_seqlens, total: int, max_seqlen: int, starts=None, stream=None):
@@ -731,11 +740,11 @@ def flash_kv_read_q4(cache: KVCacheQ4, block_table, cu_seqlens, total: int, max_
     codes, scales = cache[0], cache[1]
     k = torch.empty(int(total), codes.shape[1], 2 * codes.shape[3], dtype=scales.dtype, device=codes.device)
     v = torch.empty_like(k)
-    fa_kv_read_q4(k, v, *cache, block_table, cu_seqlens, max_seqlen, starts, stream)
+    _kv_q4("fa_kv_read_q4", k, v, cache, block_table, cu_seqlens, max_seqlen, starts, stream)
     return k, v
 
 
-def _flash_decode_gqa(fn, q, cache, block_table, seq_lens, window, sinks, num_splits, scale, stream, workspace):
+def _flash_decode_gqa(q, cache, block_table, seq_lens, window, sinks, num_splits, scale, stream, workspace):
     if q.dim() != 4 or cache[0].dim() != 4 or block_table.dim() != 2:
         raise ValueError("q must be [B,H,1,D], pages 4-dimensional and block_table [B,max_blocks]")
     B, H, _, D = q.shape
@@ -750,7 +759,7 @@ def _flash_decode_gqa(fn, q, cache, block_table, seq_lens, window, sinks, num_sp
     if workspace is None:
         workspace = _decode_workspace(B, H, num_splits, D, q.device, True)
     o, lse = torch.empty_like(q), torch.empty((B, H), dtype=torch.float32, device=q.device)
-    fn(q, *cache, block_table, seq_lens, o, lse, *workspace, num_splits, window, sinks, scale, stream)
+    _decode_gqa(q, cache, block_table, seq_lens, o, lse, *workspace, num_splits, window, sinks, scale, stream)
     return o, lse
 
 
@@ -759,12 +768,12 @@ def flash_decode_paged_window(q, k_cache, v_cache, block_table, seq_lens, window
     """One-token attention over a paged cache with shared key heads, a sliding window (0: none) and sinks. Returns
     (o [B,H,1,D], lse [B,H]). ``workspace`` may pass (o_part, m_part, l_part, counters), counters zero; num_splits
     None takes fa_decode_splits, within the workspace."""
-    return _flash_decode_gqa(fa_decode_paged_window, q, (k_cache, v_cache), block_table, seq_lens, window, sinks,
+    return _flash_decode_gqa(q, (k_cache, v_cache), block_table, seq_lens, window, sinks,
                              num_splits, scale, stream, workspace)
 
 
 def flash_decode_paged_q4(q, cache: KVCacheQ4, block_table, seq_lens, window: int = 0, sinks: int = 0,
                           num_splits: int | None = None, scale: float | None = None, stream=None, workspace=None):
     """flash_decode_paged_window over the 4-bit cache."""
-    return _flash_decode_gqa(fa_decode_paged_q4, q, tuple(cache), block_table, seq_lens, window, sinks, num_splits,
-                             scale, stream, workspace)
+    return _flash_decode_gqa(q, tuple(cache), block_table, seq_lens, window, sinks, num_splits, scale, stream,
+                             workspace)
