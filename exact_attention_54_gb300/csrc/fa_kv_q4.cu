@@ -78,27 +78,39 @@ struct Walk {
     }
 };
 
+// 1 / x for normal x and 1 / x, relative error under 2^-22.
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Codes (n + 8 in nibble e: column e of x's eight) for scale s.
 template <bool BF16>
 __device__ __forceinline__ uint32_t quantise8(const uint4 &x, float s) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     // Where s is a normal number (and 1 / s is one): x / s is a tie n + 1/2 or
     // at least 2^-12 away from one, for x and s of at most 11 bits, and at most
-    // 7.04. x * (1 / s) is off by less than 2^-20, so rounding it to multiples
-    // of 2^-14 restores the ties and moves nothing else across one; adding 1.5
-    // 2^23 + 8 then rounds to the nearest even integer, which stands, plus 8,
-    // in the sum's low bits. The sum of 16^e times those words (mod 2^32) holds
-    // the nibbles, but for a constant.
+    // 7.04. x * (1 / s), the reciprocal good to 2^-22, is off by less than
+    // 2^-18, so rounding it to multiples of 2^-14 restores the ties and moves
+    // nothing else across one; adding 1.5 2^23 + 8 then rounds to the nearest
+    // even integer, which stands, plus 8, in the sum's low bits. The sum of
+    // 16^e times those words (mod 2^32) holds the nibbles, but for a constant.
+    // Two columns at a time.
     if (s >= (BF16 ? 1e-30f : 6.103515625e-5f)) {
         constexpr float kSnap = 768.f;          // 1.5 2^23 2^-14
         constexpr float kInt = 12582920.f;      // 1.5 2^23 + 8: bits 0x4b400008
-        const float inv = 1.f / s;
+        const float r = rcp_approx(s);
+        const uint64_t inv = ptx::pk2(r, r), snap = ptx::pk2(kSnap, kSnap), less = ptx::pk2(-kSnap, -kSnap),
+                       whole = ptx::pk2(kInt, kInt);
         uint32_t word = 0u - 0x4b400000u * 0x11111111u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float v = from16<BF16>(static_cast<uint16_t>(w[e / 2] >> (16 * (e % 2))));
-            const float t = __fsub_rn(__fmaf_rn(v, inv, kSnap), kSnap);
-            word += __float_as_uint(__fadd_rn(t, kInt)) * (1u << (4 * e));
+        for (int e = 0; e < 8; e += 2) {
+            const uint64_t v = ptx::pk2(from16<BF16>(static_cast<uint16_t>(w[e / 2])),
+                                        from16<BF16>(static_cast<uint16_t>(w[e / 2] >> 16)));
+            float n0, n1;
+            ptx::upk2(ptx::fadd2(ptx::fadd2(ptx::ffma2(v, inv, snap), less), whole), n0, n1);
+            word += __float_as_uint(n0) * (1u << (4 * e)) + __float_as_uint(n1) * (1u << (4 * e + 4));
         }
         return word;
     }
@@ -124,7 +136,11 @@ __device__ __forceinline__ void quantise_row(const uint4 &x, uint8_t *codes, uin
     mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     mx = max(mx & 0xffffu, mx >> 16);
     const bool finite = mx < (BF16 ? 0x7f80u : 0x7c00u);
-    const uint16_t s16 = finite ? to16<BF16>(from16<BF16>(static_cast<uint16_t>(mx)) / 7.f) : uint16_t(0x7fff);
+    // max / 7 is no tie of 16-bit numbers (7 m with m odd has too many bits to
+    // be one itself) and at least 1/7 of half a step away from each, so the
+    // fp32 product with 1/7 rounds like the quotient.
+    const uint16_t s16 =
+        finite ? to16<BF16>(from16<BF16>(static_cast<uint16_t>(mx)) * (1.f / 7.f)) : uint16_t(0x7fff);
     const uint32_t word = quantise8<BF16>(x, from16<BF16>(s16));  // a NaN scale takes the slow way: all n = 0
     // Lane (w, c) of a row has columns 32 w + 8 c + (0..7): the 16 bits of
     // group w in pieces 2 c and 2 c + 1. The lanes of groups w and w ^ 1
