@@ -7,9 +7,10 @@
 //
 // Grid: a chunk of tokens of one sequence per CTA (sequence = blockIdx.x /
 // chunks), so that a token's sequence needs no search in cu_seqlens; the
-// chunk's cache rows are looked up once, into shared memory. D / 8 lanes share
-// a row of one key head, 8 columns (16 bytes) each; a thread takes the key row
-// and the value row of kPasses (token, head) pairs with all loads in flight.
+// chunk's cache rows are looked up once, into shared memory. Writing, D / 16
+// lanes share a row of one key head, 16 columns each; reading, D / 8 lanes, 8
+// columns (16 bytes) each; a thread takes the key row and the value row of
+// several (token, head) pairs with all loads in flight.
 #include "fa_kv_q4.cuh"
 #include "fa_launch.h"
 
@@ -85,10 +86,14 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return y;
 }
 
-// Codes (n + 8 in nibble e: column e of x's eight) for scale s.
+// Sixteen columns of a row, as a lane of the write kernel holds them.
+struct Half {
+    uint4 x[2];
+};
+
+// Codes (n + 8 in nibble e of word j: column 8 j + e of x) for scale s.
 template <bool BF16>
-__device__ __forceinline__ uint32_t quantise8(const uint4 &x, float s) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+__device__ __forceinline__ void quantise16(const Half &x, float s, uint32_t (&word)[2]) {
     // Where s is a normal number (and 1 / s is one): x / s is a tie n + 1/2 or
     // at least 2^-12 away from one, for x and s of at most 11 bits, and at most
     // 7.04. x * (1 / s), the reciprocal good to 2^-22, is off by less than
@@ -103,37 +108,47 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 &x, float s) {
         const float r = rcp_approx(s);
         const uint64_t inv = ptx::pk2(r, r), snap = ptx::pk2(kSnap, kSnap), less = ptx::pk2(-kSnap, -kSnap),
                        whole = ptx::pk2(kInt, kInt);
-        uint32_t word = 0u - 0x4b400000u * 0x11111111u;
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            const uint64_t v = ptx::pk2(from16<BF16>(static_cast<uint16_t>(w[e / 2])),
-                                        from16<BF16>(static_cast<uint16_t>(w[e / 2] >> 16)));
-            float n0, n1;
-            ptx::upk2(ptx::fadd2(ptx::fadd2(ptx::ffma2(v, inv, snap), less), whole), n0, n1);
-            word += __float_as_uint(n0) * (1u << (4 * e)) + __float_as_uint(n1) * (1u << (4 * e + 4));
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t w[4] = {x.x[j].x, x.x[j].y, x.x[j].z, x.x[j].w};
+            word[j] = 0u - 0x4b400000u * 0x11111111u;
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const uint64_t v = ptx::pk2(from16<BF16>(static_cast<uint16_t>(w[e / 2])),
+                                            from16<BF16>(static_cast<uint16_t>(w[e / 2] >> 16)));
+                float n0, n1;
+                ptx::upk2(ptx::fadd2(ptx::fadd2(ptx::ffma2(v, inv, snap), less), whole), n0, n1);
+                word[j] += __float_as_uint(n0) * (1u << (4 * e)) + __float_as_uint(n1) * (1u << (4 * e + 4));
+            }
         }
-        return word;
+        return;
     }
-    uint32_t word = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        word[j] = 0;
 #pragma unroll 1
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t pair = e < 2 ? w[0] : e < 4 ? w[1] : e < 6 ? w[2] : w[3];
-        const float v = from16<BF16>(static_cast<uint16_t>(pair >> (16 * (e % 2))));
-        const float n = s > 0.f ? fminf(fmaxf(rintf(v / s), -7.f), 7.f) : 0.f;
-        word |= static_cast<uint32_t>(static_cast<int>(n) + 8) << (4 * e);
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t pair = e < 2 ? x.x[j].x : e < 4 ? x.x[j].y : e < 6 ? x.x[j].z : x.x[j].w;
+            const float v = from16<BF16>(static_cast<uint16_t>(pair >> (16 * (e % 2))));
+            const float n = s > 0.f ? fminf(fmaxf(rintf(v / s), -7.f), 7.f) : 0.f;
+            word[j] |= static_cast<uint32_t>(static_cast<int>(n) + 8) << (4 * e);
+        }
     }
-    return word;
 }
 
+// Codes and scales of a row. Lane sub = 2 w + h has columns 32 w + 16 h +
+// (0..15) in x.
 template <int D, bool BF16>
-__device__ __forceinline__ void quantise_row(const uint4 &x, uint8_t *codes, uint16_t *scales, long long row,
-                                             int sub) {
+__device__ __forceinline__ void quantise_row(const Half &x, uint8_t *codes, uint16_t *scales, long long row, int sub) {
     // max|x| of the group on the bits (16-bit floats without their sign order
     // like integers, infinities and NaNs last)
-    uint32_t mx = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                           __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        mx = __vmaxu2(mx, __vmaxu2(x.x[i].x & 0x7fff7fffu, x.x[i].y & 0x7fff7fffu));
+        mx = __vmaxu2(mx, __vmaxu2(x.x[i].z & 0x7fff7fffu, x.x[i].w & 0x7fff7fffu));
+    }
     mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     mx = max(mx & 0xffffu, mx >> 16);
     const bool finite = mx < (BF16 ? 0x7f80u : 0x7c00u);
     // max / 7 is no tie of 16-bit numbers (7 m with m odd has too many bits to
@@ -141,18 +156,19 @@ __device__ __forceinline__ void quantise_row(const uint4 &x, uint8_t *codes, uin
     // fp32 product with 1/7 rounds like the quotient.
     const uint16_t s16 =
         finite ? to16<BF16>(from16<BF16>(static_cast<uint16_t>(mx)) * (1.f / 7.f)) : uint16_t(0x7fff);
-    const uint32_t word = quantise8<BF16>(x, from16<BF16>(s16));  // a NaN scale takes the slow way: all n = 0
-    // Lane (w, c) of a row has columns 32 w + 8 c + (0..7): the 16 bits of
-    // group w in pieces 2 c and 2 c + 1. The lanes of groups w and w ^ 1
-    // exchange halves: even w keeps piece 2 c, odd w piece 2 c + 1, and each
-    // stores one whole word.
-    const int grp = sub / 4, c = sub % 4;
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 4);
-    const uint32_t out = grp % 2 == 0 ? __byte_perm(word, other, 0x5410) : __byte_perm(other, word, 0x7632);
+    uint32_t word[2];  // pieces 4 h, 4 h + 1 and 4 h + 2, 4 h + 3: 16 bits of group w each
+    quantise16<BF16>(x, from16<BF16>(s16), word);  // a NaN scale takes the slow way: all n = 0
+    // The lanes of groups w and w ^ 1 exchange a word: even w stores the first
+    // two pieces, odd w the others, whole words.
+    const int w = sub / 2, h = sub % 2;
+    const bool odd = w % 2 != 0;
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? word[0] : word[1], 2);
+    const uint32_t lo = odd ? other : word[0], hi = odd ? word[1] : other;
     if (row >= 0) {
-        uint32_t *dst = reinterpret_cast<uint32_t *>(codes + row * (D / 2));
-        dst[(2 * c + grp % 2) * (D / 64) + grp / 2] = out;
-        if (c == 0) scales[row * (D / kGroup) + grp] = s16;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(codes + row * (D / 2)) + (4 * h + 2 * (w % 2)) * (D / 64) + w / 2;
+        dst[0] = __byte_perm(lo, hi, 0x5410);
+        dst[D / 64] = __byte_perm(lo, hi, 0x7632);
+        if (h == 0) scales[row * (D / kGroup) + w] = s16;
     }
 }
 
@@ -161,26 +177,30 @@ __global__ void __launch_bounds__(kThreads) fa_kv_write_q4_kernel(const KvQ4Para
     __shared__ long long rows[kMaxTokens];
     Chunk c;
     if (!chunk_of(p, c)) return;
-    constexpr int kLanes = D / 8, kStep = kThreads / kLanes;
+    constexpr int kLanes = D / 16, kStep = kThreads / kLanes, kPairs = kPasses / 2;  // as many rows a CTA as reading
     const int sub = threadIdx.x % kLanes;
     const int pairs = c.count * p.Hkv;
     // whole warps run every pass: the group maxima are exchanged within a warp
-    for (int r0 = 0; r0 < pairs; r0 += kPasses * kStep) {
+    for (int r0 = 0; r0 < pairs; r0 += kPairs * kStep) {
         const int r = r0 + static_cast<int>(threadIdx.x) / kLanes;
-        uint4 kx[kPasses], vx[kPasses];
+        Half kx[kPairs], vx[kPairs];
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            kx[i] = vx[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (r + i * kStep < pairs) {
-                const size_t at = (static_cast<size_t>(c.first) * p.Hkv + r + i * kStep) * D + sub * 8;
-                kx[i] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.k) + at));
-                vx[i] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.v) + at));
+        for (int i = 0; i < kPairs; ++i) {
+            const bool there = r + i * kStep < pairs;
+            const size_t at = (static_cast<size_t>(c.first) * p.Hkv + r + i * kStep) * D + sub * 16;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                kx[i].x[j] = vx[i].x[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (there) {
+                    kx[i].x[j] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.k) + at) + j);
+                    vx[i].x[j] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.v) + at) + j);
+                }
             }
         }
         if (r0 == 0) look_up(p, c, rows);  // behind the loads
         Walk w(r, kStep, p.Hkv);
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
+        for (int i = 0; i < kPairs; ++i) {
             if (r0 + i * kStep >= pairs) break;  // the same for the whole CTA
             const long long first = r + i * kStep < pairs ? rows[w.t] : -1;
             const long long row = first < 0 ? -1 : first + (static_cast<long long>(w.h) << p.log2_bs);
