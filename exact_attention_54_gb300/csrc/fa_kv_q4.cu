@@ -7,10 +7,9 @@
 //
 // Grid: a chunk of tokens of one sequence per CTA (sequence = blockIdx.x /
 // chunks), so that a token's sequence needs no search in cu_seqlens; the
-// chunk's cache rows are looked up once, into shared memory. Writing, D / 16
-// lanes share a row of one key head, 16 columns each; reading, D / 8 lanes, 8
-// columns (16 bytes) each; a thread takes the key row and the value row of
-// several (token, head) pairs with all loads in flight.
+// chunk's cache rows are looked up once, into shared memory. D / 16 lanes share
+// a row of one key head, 16 columns each; a thread takes the key row and the
+// value row of kPasses (token, head) pairs with all loads in flight.
 #include "fa_kv_q4.cuh"
 #include "fa_launch.h"
 
@@ -18,12 +17,12 @@ namespace fa {
 namespace q4 {
 
 constexpr int kThreads = 256;
-constexpr int kPasses = 4;  // (token, head) pairs per lane group and CTA, when a sequence has that many
-constexpr int kMaxTokens = kPasses * kThreads / 8;  // of a CTA: D = 64, one key head
+constexpr int kPasses = 2;  // (token, head) pairs per lane group and CTA, when a sequence has that many
+constexpr int kMaxTokens = kPasses * kThreads / 4;  // of a CTA: D = 64, one key head
 
 // Tokens of one CTA: kPasses rows for each of its lane groups.
 static int tokens_per_cta(int D, int Hkv) {
-    const int rows = kPasses * kThreads / (D / 8);
+    const int rows = kPasses * kThreads / (D / 16);
     return Hkv >= rows ? 1 : rows / Hkv;
 }
 
@@ -177,15 +176,15 @@ __global__ void __launch_bounds__(kThreads) fa_kv_write_q4_kernel(const KvQ4Para
     __shared__ long long rows[kMaxTokens];
     Chunk c;
     if (!chunk_of(p, c)) return;
-    constexpr int kLanes = D / 16, kStep = kThreads / kLanes, kPairs = kPasses / 2;  // as many rows a CTA as reading
+    constexpr int kLanes = D / 16, kStep = kThreads / kLanes;
     const int sub = threadIdx.x % kLanes;
     const int pairs = c.count * p.Hkv;
     // whole warps run every pass: the group maxima are exchanged within a warp
-    for (int r0 = 0; r0 < pairs; r0 += kPairs * kStep) {
+    for (int r0 = 0; r0 < pairs; r0 += kPasses * kStep) {
         const int r = r0 + static_cast<int>(threadIdx.x) / kLanes;
-        Half kx[kPairs], vx[kPairs];
+        Half kx[kPasses], vx[kPasses];
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
+        for (int i = 0; i < kPasses; ++i) {
             const bool there = r + i * kStep < pairs;
             const size_t at = (static_cast<size_t>(c.first) * p.Hkv + r + i * kStep) * D + sub * 16;
 #pragma unroll
@@ -200,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) fa_kv_write_q4_kernel(const KvQ4Para
         if (r0 == 0) look_up(p, c, rows);  // behind the loads
         Walk w(r, kStep, p.Hkv);
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
+        for (int i = 0; i < kPasses; ++i) {
             if (r0 + i * kStep >= pairs) break;  // the same for the whole CTA
             const long long first = r + i * kStep < pairs ? rows[w.t] : -1;
             const long long row = first < 0 ? -1 : first + (static_cast<long long>(w.h) << p.log2_bs);
@@ -213,26 +212,27 @@ __global__ void __launch_bounds__(kThreads) fa_kv_write_q4_kernel(const KvQ4Para
     }
 }
 
-// Eight columns of a row as loaded: the words that hold piece 2c and piece
-// 2c + 1 of the lane's group, and its scale.
-struct Packed8 {
+// A lane's words of a row as loaded, and its group's scale. Lane sub = 2 w + h
+// loads two of the four pieces that hold columns 32 w + 16 h + (0..15), for
+// its own group and the one that shares the words with it (see quantise_row).
+struct Packed {
     uint32_t a, b;
     uint16_t s;
 };
 
 template <int D>
-__device__ __forceinline__ Packed8 load8(const uint8_t *codes, const uint16_t *scales, long long row, int sub) {
-    const int grp = sub / 4, c = sub % 4;
-    const uint32_t *src = reinterpret_cast<const uint32_t *>(codes + row * (D / 2));
-    return {src[2 * c * (D / 64) + grp / 2], src[(2 * c + 1) * (D / 64) + grp / 2], scales[row * (D / kGroup) + grp]};
+__device__ __forceinline__ Packed load_half(const uint8_t *codes, const uint16_t *scales, long long row, int sub) {
+    const int w = sub / 2, h = sub % 2;
+    const uint32_t *src =
+        reinterpret_cast<const uint32_t *>(codes + row * (D / 2)) + (4 * h + 2 * (w % 2)) * (D / 64) + w / 2;
+    return {src[0], src[D / 64], scales[row * (D / kGroup) + w]};
 }
 
 // s * n of the eight, rounded once: n is exact in either 16-bit type (u + 1024
 // or u + 128, as masked into the mantissa, less 1032 or 136), so a 16-bit
 // product is the rounded one.
-template <int D, bool BF16>
-__device__ __forceinline__ uint4 unpack8(const Packed8 &x, int sub) {
-    const uint32_t word = __byte_perm(x.a, x.b, sub / 4 % 2 == 0 ? 0x5410 : 0x7632);
+template <bool BF16>
+__device__ __forceinline__ uint4 unpack8(uint32_t word, uint16_t s) {
     uint32_t v[4];  // columns i and 4 + i
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -240,11 +240,11 @@ __device__ __forceinline__ uint4 unpack8(const Packed8 &x, int sub) {
         if constexpr (BF16) {
             const __nv_bfloat162 n = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&u),
                                              __bfloat162bfloat162(__ushort_as_bfloat16(0x4308)));  // 136
-            const __nv_bfloat162 y = __hmul2_rn(n, __bfloat162bfloat162(__ushort_as_bfloat16(x.s)));
+            const __nv_bfloat162 y = __hmul2_rn(n, __bfloat162bfloat162(__ushort_as_bfloat16(s)));
             v[i] = *reinterpret_cast<const uint32_t *>(&y);
         } else {
             const __half2 n = __hsub2(*reinterpret_cast<const __half2 *>(&u), __half2half2(__ushort_as_half(0x6408)));  // 1032
-            const __half2 y = __hmul2_rn(n, __half2half2(__ushort_as_half(x.s)));
+            const __half2 y = __hmul2_rn(n, __half2half2(__ushort_as_half(s)));
             v[i] = *reinterpret_cast<const uint32_t *>(&y);
         }
     }
@@ -252,38 +252,61 @@ __device__ __forceinline__ uint4 unpack8(const Packed8 &x, int sub) {
                       __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
 }
 
+// Sixteen columns of every lane's row; the whole warp calls it. `dst` NULL:
+// not stored.
+template <bool BF16>
+__device__ __forceinline__ void store_half(uint16_t *dst, const Packed &x, int sub, bool v8, uint64_t policy) {
+    const bool odd = sub / 2 % 2 != 0;
+    const uint32_t lo = __byte_perm(x.a, x.b, 0x5410), hi = __byte_perm(x.a, x.b, 0x7632);
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 2);
+    if (dst == nullptr) return;
+    const uint4 y0 = unpack8<BF16>(odd ? other : lo, x.s), y1 = unpack8<BF16>(odd ? hi : other, x.s);
+    if (v8) {
+        const uint32_t y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+        ptx::st_global_v8_hint(dst, y, policy);
+    } else {
+        __stcs(reinterpret_cast<uint4 *>(dst), y0);
+        __stcs(reinterpret_cast<uint4 *>(dst) + 1, y1);
+    }
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads) fa_kv_read_q4_kernel(const KvQ4Params p) {
     __shared__ long long rows[kMaxTokens];
     Chunk c;
     if (!chunk_of(p, c)) return;
-    constexpr int kLanes = D / 8, kStep = kThreads / kLanes;
+    constexpr int kLanes = D / 16, kStep = kThreads / kLanes;
     const int sub = threadIdx.x % kLanes;
     const int pairs = c.count * p.Hkv;
+    const bool v8 = ((reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) & 31) == 0;
+    const uint64_t policy = ptx::l2_policy_evict_first();
     look_up(p, c, rows);
-    for (int r = static_cast<int>(threadIdx.x) / kLanes; r < pairs; r += kPasses * kStep) {
+    // whole warps run every pass: lanes exchange words
+    for (int r0 = 0; r0 < pairs; r0 += kPasses * kStep) {
+        const int r = r0 + static_cast<int>(threadIdx.x) / kLanes;
         Walk w(r, kStep, p.Hkv);
-        Packed8 k[kPasses], v[kPasses];
+        Packed k[kPasses], v[kPasses];
         bool there[kPasses];
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             const long long first = r + i * kStep < pairs ? rows[w.t] : -1;
             there[i] = first >= 0;
+            k[i] = v[i] = Packed{0u, 0u, 0};
             if (there[i]) {
                 const long long row = first + (static_cast<long long>(w.h) << p.log2_bs);
-                k[i] = load8<D>(static_cast<const uint8_t *>(p.k_codes), static_cast<const uint16_t *>(p.k_scales),
-                                row, sub);
-                v[i] = load8<D>(static_cast<const uint8_t *>(p.v_codes), static_cast<const uint16_t *>(p.v_scales),
-                                row, sub);
+                k[i] = load_half<D>(static_cast<const uint8_t *>(p.k_codes), static_cast<const uint16_t *>(p.k_scales),
+                                    row, sub);
+                v[i] = load_half<D>(static_cast<const uint8_t *>(p.v_codes), static_cast<const uint16_t *>(p.v_scales),
+                                    row, sub);
             }
             w.next();
         }
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
-            if (!there[i]) continue;
-            const size_t at = (static_cast<size_t>(c.first) * p.Hkv + r + i * kStep) * D + sub * 8;
-            __stcs(reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.k) + at), unpack8<D, BF16>(k[i], sub));
-            __stcs(reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.v) + at), unpack8<D, BF16>(v[i], sub));
+            if (r0 + i * kStep >= pairs) break;  // the same for the whole CTA
+            const size_t at = (static_cast<size_t>(c.first) * p.Hkv + r + i * kStep) * D + sub * 16;
+            store_half<BF16>(there[i] ? static_cast<uint16_t *>(p.k) + at : nullptr, k[i], sub, v8, policy);
+            store_half<BF16>(there[i] ? static_cast<uint16_t *>(p.v) + at : nullptr, v[i], sub, v8, policy);
         }
     }
 }
