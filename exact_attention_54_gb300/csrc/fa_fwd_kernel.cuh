@@ -197,24 +197,24 @@ __device__ __forceinline__ void finish_work(const FwdParams &p, Work &k, int pai
         }
         k.lo = max(k.lo, k.ns);
         k.n_kv_max = k.ns + max(end - k.lo, 0);
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int qs = (2 * pair + t) * kBlockM;
-        k.q_start[t] = qs;
-        const int rows = k.Lq - qs;
-        k.rows[t] = rows <= 0 ? 0 : (rows < kBlockM ? rows : kBlockM);
-        int nkv = 0;
-        if (k.rows[t] > 0) {
-            nkv = nk_all;
-            if (CAUSAL) {
-                const int last = (qs + k.rows[t] - 1) / kBlockN + 1;
-                nkv = last < nk_all ? last : nk_all;
+        for (int t = 0; t < 2; ++t) {
+            const int qs = (2 * pair + t) * kBlockM;
+            k.q_start[t] = qs;
+            const int rows = k.Lq - qs;
+            k.rows[t] = rows <= 0 ? 0 : (rows < kBlockM ? rows : kBlockM);
+            int nkv = 0;
+            if (k.rows[t] > 0) {
+                nkv = nk_all;
+                if (CAUSAL) {
+                    const int last = (qs + k.rows[t] - 1) / kBlockN + 1;
+                    nkv = last < nk_all ? last : nk_all;
+                }
             }
+            k.n_kv[t] = nkv;
+            k.n_kv_max = nkv > k.n_kv_max ? nkv : k.n_kv_max;
         }
-        k.n_kv[t] = nkv;
-        k.n_kv_max = nkv > k.n_kv_max ? nkv : k.n_kv_max;
     }
 }
 
