@@ -275,7 +275,7 @@ static cudaError_t launch_t(GqaDecodeParams p, int sms, cudaStream_t st) {
 // can be counted in 32 bits.
 static bool gqa_balanced(long long units, long long keys, long long wave) {
     const long long tiles = units * (keys / 16 + 2);
-    return tiles > 32 * wave && tiles <= INT_MAX;
+    return tiles > 32 * wave && units * (keys / 16 + 16) <= INT_MAX;
 }
 
 int decode_gqa_splits(int sms, int B, int H, int Hkv, int max_keys) {

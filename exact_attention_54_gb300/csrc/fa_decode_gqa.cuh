@@ -156,6 +156,10 @@ constexpr int kPlanSeqs = 512;  // sequences the balanced plan holds
 // It lives in shared memory: the kernels need their registers.
 template <int TILE, int HT>
 struct Plan {
+    // what a unit's start costs, in tiles (4 bits, 8 key heads: 16 sequences of
+    // 16384 to 32768 keys 120.7 -> 118.2 us, 64 of 1000 to 8000 101.7 -> 94.2 us;
+    // 8 and 16 are worse by up to 2 %)
+    static constexpr unsigned kStart = 12;
     unsigned prefix[kPlanSeqs + 1];  // balanced: tiles of one key head of the sequences before b
     unsigned run, at, end;           // balanced: tiles per CTA; this CTA's (all units' tiles fit 32 bits)
     Part part;
@@ -174,8 +178,10 @@ struct Plan {
             __syncthreads();
             return;
         }
-        // a sequence without keys still gets a part, which writes its result
-        for (int b = threadIdx.x; b < p.B; b += kThreads) prefix[b + 1] = max(KeyList<TILE>(p, b).n, 1);
+        // a unit starts with kStart tiles that are not there: a CTA whose run
+        // straddles units has that much less to read, and a sequence without
+        // keys still gets a part, which writes its result
+        for (int b = threadIdx.x; b < p.B; b += kThreads) prefix[b + 1] = KeyList<TILE>(p, b).n + kStart;
         __syncthreads();
         if (threadIdx.x < 32) {
             const int each = (p.B + 31) / 32, b0 = threadIdx.x * each;
@@ -222,11 +228,12 @@ struct Plan {
                     in_seq = (at - first) / n;
                     const unsigned start = first + in_seq * n;
                     part.b = b;
-                    part.lo = at - start;
-                    part.hi = min(end - start, n);
+                    const int lo = at - start, hi = min(end - start, n);
+                    part.lo = max(lo - static_cast<int>(kStart), 0);
+                    part.hi = max(hi - static_cast<int>(kStart), 0);
                     part.slot = blockIdx.x - start / run;
                     part.parts = (start + n - 1) / run - start / run + 1;
-                    at = start + part.hi;
+                    at = start + hi;
                 } else {
                     const int unit = static_cast<int>(blockIdx.x) / p.num_splits;
                     part.b = unit / units_b;
