@@ -367,3 +367,38 @@ def test_prefill_write_decode_together():
     plain_ops.assert_window_close({"o": o.transpose(0, 1), "lse": lse}, ref)
     fa.flash_decode_paged_q4(qd[:, :, -1:].contiguous(), cache, table, sl, W, sinks)
     fa.fa_check_device_error()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("packed", [False, True])
+def test_gives_up_on_a_withheld_load_and_the_next_call_is_correct(D, packed):
+    """Forward and backward, whose waits run out when one tile load never comes (see fa_test_withhold_load)."""
+    q, k, v, do = draw(1, 16, 1, 900, 900, D, torch.bfloat16, seed=30 + D)
+    ref = plain_ops.window_attention(q[0], k[0], v[0], 400, 130, D ** -0.5, do[0])
+    qd, kd, vd, dd = ((x[0].transpose(0, 1).contiguous() if packed else x).cuda() for x in (q, k, v, do))
+    cu = torch.tensor([0, 900], dtype=torch.int32, device="cuda")
+    if packed:
+        fwd = lambda: fa.flash_attention_window_varlen(qd, kd, vd, cu, cu, 900, 400, 130)  # noqa: E731
+        bwd = lambda o, lse: fa.flash_attention_window_varlen_bwd(qd, kd, vd, o, lse, dd, cu, cu, 900, 900, 400, 130)  # noqa: E731
+    else:
+        fwd = lambda: fa.flash_attention_window(qd, kd, vd, 400, 130)  # noqa: E731
+        bwd = lambda o, lse: fa.flash_attention_window_bwd(qd, kd, vd, o, lse, dd, 400, 130)  # noqa: E731
+    good = fwd()
+    fa.fa_check_device_error()
+    try:
+        for f, args in ((fwd, ()), (bwd, good)):
+            torch.cuda.synchronize()
+            fa.fa_test_withhold_load(2, 20_000_000)
+            f(*args)
+            with pytest.raises(fa.FAError) as e:
+                fa.fa_check_device_error()
+            assert e.value.status == -9
+            fa.fa_test_withhold_load(0, 0)
+    finally:
+        fa.fa_test_withhold_load(0, 0)
+    o, lse = fwd()
+    got = {"o": o, "lse": lse, **dict(zip(("dq", "dk", "dv"), bwd(o, lse)))}
+    fa.fa_check_device_error()
+    plain_ops.assert_window_close({n: x if n == "lse" and packed else x.transpose(0, 1) if packed else x[0]
+                                   for n, x in got.items()}, ref)
