@@ -440,7 +440,9 @@ def _expect(name: str, t, shape, dtype):
 
 
 _entry = {}  # entry points of the loaded library by name
-_raw_stream = torch._C._cuda_getCurrentRawStream  # handle of a device's current stream, without a Stream object
+# handle of a device's current stream, without a Stream object where PyTorch has that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _launch(fn: str, stream, tensors, *args, index=None):

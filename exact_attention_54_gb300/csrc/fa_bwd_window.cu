@@ -1,5 +1,17 @@
 // Sliding-window instantiations of the backward pass, dense [B,H,S,D] and
 // packed [T,H,D]: causal, with sinks and shared key heads.
+//
+// Mathematics: dV = P^T dO, dS = P (dP - D_i), dK = scale dS^T Q and dQ = scale
+// dS K over the visible pairs; dK and dV of a shared key head are sums over its
+// query heads, taken in one CTA's accumulators. A key tile takes the queries from
+// its own position to the reach of its window, to the end if it holds sinks.
+//
+// Bound by the chain of a step (two products, softmax, three products), as in
+// the causal kernel. 16 packed sequences of 123 to 1994 tokens, 16 heads on 4,
+// D = 128, bf16, window 512, 4 sinks: 394 us, of which the row pass (D_i, zeroed
+// dQ accumulator) 54 at 5.7 TB/s, the main kernel 282 (tensor pipe 46 % active;
+// without sinks about 40 less), dQ's conversion 37 at 6.3 TB/s, the joining of
+// segments 9.
 #include "fa_bwd.cuh"
 
 namespace fa {

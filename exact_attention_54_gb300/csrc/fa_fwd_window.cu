@@ -1,5 +1,18 @@
 // Sliding-window instantiations of the forward kernel, dense [B,H,S,D] and
 // packed [T,H,D]: causal, with sinks and shared key heads.
+//
+// Mathematics: query i sees the keys j <= i with i - j < window or j < sinks, so
+// a 128-query tile visits two runs of 128-key tiles, those with sinks and those
+// its window reaches; masks apply to the tiles at the ends of the runs alone.
+// Query head h reads key head h / group through the tensor map.
+//
+// Bound by the chain of a step (product, softmax, product), as in the causal
+// kernel: (1, 32 heads, 4096 tokens, D = 128, bf16), window 1024, 4 sinks: 68 us,
+// 890 TFLOP/s of the visible pairs and 1250 of the tiles visited (a tile at each
+// end of the window counts whole, and so does the one with sinks); tensor pipe
+// 50 % active. Taking the first 32 keys alone of the tile with sinks gained 2 %
+// and is not done. 16 packed sequences of 123 to 1994 tokens, 16
+// heads on 4, window 512: 122 us.
 #include "fa_fwd_kernel.cuh"
 
 namespace fa {
