@@ -877,8 +877,7 @@ static fa_status_t kv_q4(bool write, const void *k, const void *v, const void *k
     if (total == 0) return FA_OK;
     p.err = device_error_word();
     if (p.err == nullptr) return FA_ERR_CUDA;
-    const cudaError_t e = fa::launch_kv_q4(D, dtype == FA_BF16, write, p, static_cast<int>(grid),
-                                           static_cast<cudaStream_t>(stream));
+    const cudaError_t e = fa::launch_kv_q4(D, dtype == FA_BF16, write, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -5,14 +5,15 @@
 // read and D / 2 + D / 16 written per row; read: the reverse), bound by HBM
 // bandwidth, or by launch latency for a few tokens.
 //
-// Measured over 264 M values (16 sequences, 8 key heads, D = 128): reading 84 us,
-// 6.3 TB/s. Writing the 45 M values of 16 prompts: about 24 us, 4.8 TB/s, most of
-// it instructions (some 90 for 16 columns); a step of 64 tokens, write and read
-// back, 10 us. CTAs of 128 threads: 256 and 512 lose 1 and 6 % writing; one row
-// per lane group loses 15 %, four 4 %.
+// Measured: reading 206 M values (100,527 tokens in 16 sequences, 8 key heads,
+// D = 128) 84 us, 6.3 TB/s; writing the 45 M values of 16 prompts and reading
+// them back 41 us, 5.0 TB/s, where instructions take as long as the bytes; a
+// step of 64 tokens, written and read back, 10 us. CTAs of 128 threads: 256 and
+// 512 lost 1 and 6 % on the prompts; one row per lane group lost 15 %, four 4 %;
+// a lane took 8 columns before, 20 % slower; divisions by Hkv in the kernels, 8 %.
 //
-// Grid: a chunk of tokens of one sequence per CTA (sequence = blockIdx.x /
-// chunks), so that a token's sequence needs no search in cu_seqlens; the
+// Grid: a chunk of tokens (x) of one sequence (y, z) per CTA, so that a token's
+// sequence needs no search in cu_seqlens and no division; the
 // chunk's cache rows are looked up once, into shared memory. D / 16 lanes share
 // a row of one key head, 16 columns each; a thread takes the key row and the
 // value row of kPasses (token, head) pairs with all loads in flight.
@@ -40,8 +41,9 @@ struct Chunk {
 };
 
 __device__ __forceinline__ bool chunk_of(const KvQ4Params &p, Chunk &c) {
-    const int b = static_cast<int>(blockIdx.x) / p.chunks;
-    const int i0 = static_cast<int>(blockIdx.x) % p.chunks * p.tokens;
+    const int b = static_cast<int>(blockIdx.z * gridDim.y + blockIdx.y);
+    if (b >= p.num_seqs) return false;
+    const int i0 = static_cast<int>(blockIdx.x) * p.tokens;
     const int t0 = p.cu_seqlens[b], t1 = p.cu_seqlens[b + 1];
     const int start = p.starts == nullptr ? 0 : p.starts[b];
     if (t0 < 0 || t1 < t0 || t1 > p.total || t1 - t0 > p.max_seqlen || start < 0) {
@@ -69,16 +71,22 @@ __device__ __forceinline__ void look_up(const KvQ4Params &p, const Chunk &c, lon
     __syncthreads();
 }
 
-// This lane group's (token, head) pairs: the first, then every `step`-th.
+// This lane group's (token, head) pairs: the first, then every step-th. The
+// divisions by Hkv are the host's: first / Hkv is a product with inv_hkv, just
+// above 2^31 / Hkv (exact while first * Hkv < 2^31: a CTA of several tokens has
+// at most 2 kThreads pairs, of one token t = 0 and inv_hkv = 0).
 struct Walk {
-    int t, h, dt, dh, Hkv;
-    __device__ __forceinline__ Walk(int first, int step, int Hkv_)
-        : t(first / Hkv_), h(first % Hkv_), dt(step / Hkv_), dh(step % Hkv_), Hkv(Hkv_) {}
+    int t, h;
+    const KvQ4Params &p;
+    __device__ __forceinline__ Walk(const KvQ4Params &p_, int first) : p(p_) {
+        t = static_cast<int>(static_cast<unsigned long long>(first) * p.inv_hkv >> 31);
+        h = first - t * p.Hkv;
+    }
     __device__ __forceinline__ void next() {
-        t += dt;
-        h += dh;
-        if (h >= Hkv) {
-            h -= Hkv;
+        t += p.step_t;
+        h += p.step_h;
+        if (h >= p.Hkv) {
+            h -= p.Hkv;
             ++t;
         }
     }
@@ -203,7 +211,7 @@ __global__ void __launch_bounds__(kThreads) fa_kv_write_q4_kernel(const KvQ4Para
             }
         }
         if (r0 == 0) look_up(p, c, rows);  // behind the loads
-        Walk w(r, kStep, p.Hkv);
+        Walk w(p, r);
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             if (r0 + i * kStep >= pairs) break;  // the same for the whole CTA
@@ -290,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) fa_kv_read_q4_kernel(const KvQ4Param
     // whole warps run every pass: lanes exchange words
     for (int r0 = 0; r0 < pairs; r0 += kPasses * kStep) {
         const int r = r0 + static_cast<int>(threadIdx.x) / kLanes;
-        Walk w(r, kStep, p.Hkv);
+        Walk w(p, r);
         Packed k[kPasses], v[kPasses];
         bool there[kPasses];
 #pragma unroll
@@ -318,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) fa_kv_read_q4_kernel(const KvQ4Param
 }
 
 template <int D, bool BF16>
-static cudaError_t launch_t(bool write, const KvQ4Params &p, unsigned grid, cudaStream_t st) {
+static cudaError_t launch_t(bool write, const KvQ4Params &p, dim3 grid, cudaStream_t st) {
     if (write) fa_kv_write_q4_kernel<D, BF16><<<grid, kThreads, 0, st>>>(p);
     else fa_kv_read_q4_kernel<D, BF16><<<grid, kThreads, 0, st>>>(p);
     return cudaGetLastError();
@@ -327,13 +335,20 @@ static cudaError_t launch_t(bool write, const KvQ4Params &p, unsigned grid, cuda
 }  // namespace q4
 
 long long kv_q4_grid(int D, int num_seqs, KvQ4Params &p) {
+    const int step = q4::kThreads / (D / 16);
+    p.num_seqs = num_seqs;
     p.tokens = q4::tokens_per_cta(D, p.Hkv);
     p.chunks = (p.max_seqlen - 1) / p.tokens + 1;
+    p.inv_hkv = p.tokens == 1 ? 0u : (1u << 31) / static_cast<unsigned>(p.Hkv) + 1u;
+    p.step_t = step / p.Hkv;
+    p.step_h = step % p.Hkv;
     return static_cast<long long>(num_seqs) * p.chunks;
 }
 
-cudaError_t launch_kv_q4(int D, bool bf16, bool write, const KvQ4Params &p, int grid, cudaStream_t st) {
-    const unsigned g = static_cast<unsigned>(grid);
+cudaError_t launch_kv_q4(int D, bool bf16, bool write, const KvQ4Params &p, cudaStream_t st) {
+    // sequences over y and z (at most 65535 each)
+    const unsigned seqs = static_cast<unsigned>(p.num_seqs), y = seqs < 65535u ? seqs : 65535u;
+    const dim3 g(static_cast<unsigned>(p.chunks), y, (seqs + y - 1) / y);
     if (D == 64) return bf16 ? q4::launch_t<64, true>(write, p, g, st) : q4::launch_t<64, false>(write, p, g, st);
     return bf16 ? q4::launch_t<128, true>(write, p, g, st) : q4::launch_t<128, false>(write, p, g, st);
 }

@@ -191,13 +191,17 @@ struct KvQ4Params {
     const int *starts;          // [num_seqs] or nullptr
     int total, max_seqlen, Hkv;
     int num_blocks, log2_bs, max_blocks;
-    int tokens, chunks;         // tokens per CTA, CTAs per sequence (set by kv_q4_grid)
+    // set by kv_q4_grid: sequences, tokens per CTA, CTAs per sequence, and what
+    // spares the kernels divisions by Hkv
+    int num_seqs, tokens, chunks;
+    unsigned inv_hkv;
+    int step_t, step_h;
     int *err;                   // device error word
 };
 
-// CTAs of the write or read launch (sets p.tokens and p.chunks).
+// CTAs of the write or read launch (sets the launch's fields of p).
 long long kv_q4_grid(int D, int num_seqs, KvQ4Params &p);
-cudaError_t launch_kv_q4(int D, bool bf16, bool write, const KvQ4Params &p, int grid, cudaStream_t stream);
+cudaError_t launch_kv_q4(int D, bool bf16, bool write, const KvQ4Params &p, cudaStream_t stream);
 
 // Parameters of the paged decode kernels with shared key heads.
 struct GqaDecodeParams {

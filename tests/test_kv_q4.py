@@ -160,6 +160,9 @@ CASES = [
     ([9, 40], [5, 0], 5, 128, 4, torch.bfloat16),
     ([300], [1000], 1, 64, 1024, torch.float16),
     ([3, 2], [0, 6], 40, 128, 16, torch.float16),  # more key heads than rows of a CTA's pass
+    ([61, 3], [2, 30], 7, 128, 8, torch.bfloat16),
+    ([11, 4], [0, 5], 31, 64, 64, torch.float16),
+    ([5], [1], 32, 128, 16, torch.bfloat16),
 ]
 
 
@@ -232,6 +235,44 @@ def test_bad_device_arrays_are_reported_and_skipped(fault, status):
     assert e.value.status == status
     fa.fa_check_device_error()
     assert all(same_bits(a.cpu(), b) for a, b in zip(dev, want))
+
+
+@pytest.mark.gpu
+def test_rows_that_are_16_byte_aligned_only():
+    k, v, cache, table, cu, st = make([20, 33], [0, 0], 2, 128, 16, torch.bfloat16, seed=7)
+    want = write_plain(k, v, cache, table, cu, st, 16)
+    shifted = lambda t: torch.cat([torch.zeros(8, dtype=t.dtype), t.flatten()]).cuda()[8:].view(t.shape)  # noqa: E731
+    dev, td, cd = [shifted(t) if t.dtype != torch.uint8 else t.cuda() for t in cache], table.cuda(), cu.cuda()
+    fa.flash_kv_write_q4(shifted(k), shifted(v), fa.KVCacheQ4(*dev), td, cd, 33)
+    assert all(same_bits(a.cpu(), b) for a, b in zip(dev, want))
+    kr, vr = fa.flash_kv_read_q4(fa.KVCacheQ4(*dev), td, cd, 53, 33)
+    ko, vo = shifted(torch.zeros_like(k)), shifted(torch.zeros_like(v))
+    assert ko.data_ptr() % 32 == 16
+    fa.fa_kv_read_q4(ko, vo, *dev, td, cd, 33)
+    fa.fa_check_device_error()
+    assert same_bits(ko.cpu(), kr.cpu()) and same_bits(vo.cpu(), vr.cpu())
+
+
+@pytest.mark.gpu
+def test_more_sequences_than_a_grid_dimension():
+    """70000 sequences, most of them without tokens."""
+    n, D = 70000, 64
+    lens = torch.zeros(n, dtype=torch.int64)
+    lens[[0, 1, 65534, 65535, 65536, n - 1]] = torch.tensor([2, 1, 1, 2, 1, 2])
+    cu = torch.zeros(n + 1, dtype=torch.int32)
+    cu[1:] = lens.cumsum(0)
+    T = int(cu[-1])
+    k = inputs.randn((T, 1, D), torch.float16, torch.Generator().manual_seed(8))
+    table = torch.full((n, 1), -1, dtype=torch.int32)
+    used = torch.nonzero(lens).flatten()
+    table[used, 0] = torch.arange(len(used), dtype=torch.int32)
+    c = fa.kv_cache_q4(len(used), 1, 2, D, torch.float16)
+    fa.flash_kv_write_q4(k.cuda(), (-k).cuda(), c, table.cuda(), cu.cuda(), 2)
+    kr, vr = fa.flash_kv_read_q4(c, table.cuda(), cu.cuda(), T, 2)
+    fa.fa_check_device_error()
+    codes, scales = plain_ops.q4_quantise(k)
+    want = plain_ops.q4_values(plain_ops.q4_pack(codes), scales).to(torch.float16)
+    assert torch.equal(kr.cpu(), want) and torch.equal(vr.cpu(), -want)
 
 
 @pytest.mark.gpu
