@@ -8,7 +8,7 @@
 //
 // Bound by the chain of a step (product, softmax, product), as in the causal
 // kernel: (1, 32 heads, 4096 tokens, D = 128, bf16), window 1024, 4 sinks: 68 us,
-// 890 TFLOP/s of the visible pairs and 1250 of the tiles visited (a tile at each
+// 890 TFLOP/s of the visible pairs and 1090 of the tiles visited (a tile at each
 // end of the window counts whole, and so does the one with sinks); tensor pipe
 // 50 % active. Taking the first 32 keys alone of the tile with sinks gained 2 %
 // and is not done. 16 packed sequences of 123 to 1994 tokens, 16
