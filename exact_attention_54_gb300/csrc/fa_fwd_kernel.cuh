@@ -628,18 +628,26 @@ __device__ void fwd_softmax(const FwdParams &p, uint32_t sbase, uint32_t tmem, i
             }
             if (need_mask || need_lo) {
                 // masked tile: the maximum is taken again after the mask
-                if (!WIN || need_mask) {
+                if constexpr (WIN) {
+                    // the columns c < x as bits of chunk b: its low x - 32 b
+                    auto below = [](int x, int b) -> uint32_t {
+                        const int n = min(max(x - 32 * b, 0), 32);
+                        return static_cast<uint32_t>((1ull << n) - 1);
+                    };
+                    const int lim = min(wk.Lk, q_row + 1) - k0, wl = q_row - p.window + 1 - k0, sk = p.sinks - k0;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const uint32_t seen = below(lim, b) & (below(sk, b) | ~below(wl, b));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(seen & (1u << i))) s[b][i] = 0xff800000u;  // -inf
+                    }
+                } else {
                     int lim = wk.Lk - k0;
                     if (CAUSAL) lim = min(lim, q_row + 1 - k0);
 #pragma unroll
                     for (int c = 0; c < kBlockN; ++c)
                         if (c >= lim) s[c / 32][c % 32] = 0xff800000u;  // -inf
-                }
-                if (WIN && need_lo) {
-                    const int wl = q_row - p.window + 1 - k0, sk = p.sinks - k0;
-#pragma unroll
-                    for (int c = 0; c < kBlockN; ++c)
-                        if (c >= sk && c < wl) s[c / 32][c % 32] = 0xff800000u;
                 }
 #pragma unroll
                 for (int c = 0; c < 4; ++c) mx4[c] = -CUDART_INF_F;
