@@ -368,6 +368,13 @@ __device__ __forceinline__ BwdUnit query_side(const BwdParams &p, const BwdUnit 
     return q;
 }
 
+// The queries lo <= i < hi of a chunk as bits (a mask test is then one
+// instruction).
+__device__ __forceinline__ uint32_t query_bits(int lo, int hi) {
+    auto below = [](int x) { return static_cast<uint32_t>((1ull << min(max(x, 0), 32)) - 1); };
+    return below(hi) & ~below(lo);
+}
+
 // Queries of a chunk [qc, qc + 32) that see `key`: lo <= i < hi.
 template <bool CAUSAL, bool WIN>
 __device__ __forceinline__ void seen_queries(const BwdParams &p, const BwdUnit &u, int key, int qc, int &lo, int &hi) {
@@ -663,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int lo, hi;
                 seen_queries<CAUSAL, WIN>(p, u, key, qc, lo, hi);
                 const bool need_mask = (CAUSAL && key > qc) || key >= u.Lk || (WIN && hi < 32);
+                const uint32_t seen = WIN ? query_bits(lo, hi) : 0u;
                 uint32_t pp[16], dd[16];
                 const float4 *lq = reinterpret_cast<const float4 *>(rows_lse + 32 * c);
                 const float4 *dq4 = reinterpret_cast<const float4 *>(rows_lse + 128 + 32 * c);
@@ -675,8 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float e0 = ptx::ex2(fmaf(__uint_as_float(sv[j]), p.scale_log2, -l0));
                     float e1 = ptx::ex2(fmaf(__uint_as_float(sv[j + 1]), p.scale_log2, -l1));
                     if (need_mask) {
-                        if (j < lo || (WIN && j >= hi)) e0 = 0.f;
-                        if (j + 1 < lo || (WIN && j + 1 >= hi)) e1 = 0.f;
+                        if (WIN ? !(seen & (1u << j)) : j < lo) e0 = 0.f;
+                        if (WIN ? !(seen & (2u << j)) : j + 1 < lo) e1 = 0.f;
                     }
                     pp[j / 2] = ptx::pack2<BF16>(e0, e1);
                     dd[j / 2] = ptx::pack2<BF16>(e0 * (__uint_as_float(dpv[j]) - d0),
@@ -1297,6 +1305,7 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
             int lo, hi;  // queries i < lo and i >= hi do not see the key
             seen_queries<CAUSAL, WIN>(p, u, key, qc, lo, hi);
             const bool need_mask = (CAUSAL && key > qc) || key >= u.Lk || (WIN && hi < 32);
+            const uint32_t seen = WIN ? query_bits(lo, hi) : 0u;
             const float *rows = reinterpret_cast<const float *>(smem_raw + S::kOffRows + b * 2 * S::kQ * 4);
             const float4 *lq = reinterpret_cast<const float4 *>(rows + 32 * h);
             const float4 *dq4 = reinterpret_cast<const float4 *>(rows + S::kQ + 32 * h);
@@ -1308,8 +1317,8 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
                 float e0 = ptx::ex2(fmaf(__uint_as_float(sv[i]), p.scale_log2, -l0));
                 float e1 = ptx::ex2(fmaf(__uint_as_float(sv[i + 1]), p.scale_log2, -l1));
                 if (need_mask) {
-                    if (i < lo || (WIN && i >= hi)) e0 = 0.f;
-                    if (i + 1 < lo || (WIN && i + 1 >= hi)) e1 = 0.f;
+                    if (WIN ? !(seen & (1u << i)) : i < lo) e0 = 0.f;
+                    if (WIN ? !(seen & (2u << i)) : i + 1 < lo) e1 = 0.f;
                 }
                 pp[i / 2] = ptx::pack2<BF16>(e0, e1);
                 if constexpr (WIN) {  // for dS, below
