@@ -642,11 +642,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ds_row = sbase + S::kOffDS + (r >> 3) * 1024 + (r & 7) * 128;
         const uint32_t row_off = (r >> 3) * 1024 + (r & 7) * 128;
         bool ok = true;
+        int next_block = WIN && n > 0 ? first % n_blocks : 0;
         for (int it = 0; it < n; ++it) {
             const int s = it & 1;
-            int qb;
-            query_side<WIN>(p, u, first + it, n_blocks, qb);
-            const int q0 = (qt0 + qb) * kBlock;
+            const int q0 = (qt0 + (WIN ? next_block : it)) * kBlock;
+            if (WIN && ++next_block == n_blocks) next_block = 0;
             // the step's LSE and D values and the free dS^T buffer are ready
             // well before S^T and dP^T: wait for them first, so that only one
             // wait separates the tensor core's commit from the key-row work
