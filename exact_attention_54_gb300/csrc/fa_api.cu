@@ -916,6 +916,8 @@ static fa_status_t decode_gqa(bool q4, const void *q, const void *k, const void 
     if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || window < 0 || sinks < 0) return FA_ERR_SHAPE;
     int log2_bs = 0;
     if (!pages_ok(Hkv, num_blocks, block_size, max_blocks_per_seq, log2_bs)) return FA_ERR_SHAPE;
+    // the 4-bit kernel counts rows in sixteens, in 32 bits (4 TB of codes)
+    if (q4 && (static_cast<long long>(num_blocks) * Hkv << log2_bs) / 16 >= 0xffffffffLL) return FA_ERR_SHAPE;
     if (num_splits < 1 || num_splits > FA_MAX_SPLITS) return FA_ERR_SPLITS;
     if (static_cast<long long>(B) * H * num_splits > INT_MAX) return FA_ERR_SHAPE;
     if (!scale_ok(scale)) return FA_ERR_SCALE;

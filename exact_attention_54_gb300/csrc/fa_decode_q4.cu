@@ -110,19 +110,22 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
     const int mine = hi - lo > warp ? (hi - lo - warp + kWarps - 1) / kWarps : 0;
     auto key0_of = [&](int i) { return list.key0(lo + warp + kWarps * i); };
     bool bad_page = false;
-    // Lane j holds the page of keys 16 (j % 2) .. + 15 of tile 16 n + j / 2, or
-    // -1 (no visible key there, or no such page); two batches, one read ahead.
-    auto page_of = [&](int i) {
-        if (!ring || i >= mine) return -1;
+    // Lane j holds where keys 16 (j % 2) .. + 15 of tile 16 n + j / 2 are, in
+    // units of 16 rows (they fit 32 bits), or kNone (no visible key there, or no
+    // such page); two batches, one read ahead.
+    constexpr unsigned kNone = 0xffffffffu;
+    auto place_of = [&](int i) {
+        if (!ring || i >= mine) return kNone;
         const int key = key0_of(i) + 16 * (lane & 1);
-        if (!list.sees16(key)) return -1;
+        if (!list.sees16(key)) return kNone;
         const int page = table[key >> p.log2_bs];
         const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_blocks);
         bad_page |= !ok;
-        return ok ? page : -1;
+        if (!ok) return kNone;
+        return ((static_cast<unsigned>(page) * p.Hkv + job.hk) << (p.log2_bs - 4)) + ((key & page_mask) >> 4);
     };
-    int base = 0;  // tile of pages0, lane 0
-    int pages0 = page_of(lane / 2), pages1 = page_of(16 + lane / 2);
+    int base = 0;  // tile of places0, lane 0
+    unsigned places0 = place_of(lane / 2), places1 = place_of(16 + lane / 2);
 
     // ---- asynchronous copies, 16 bytes a lane: 16 keys' codes are 16 kRow
     // bytes in a row of each array, their scales 16 kSRow bytes ----
@@ -130,11 +133,11 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
     const bool scale_lane = (lane & 15) < S::kSRow;
     const char *const scale_base = static_cast<const char *>(v_scales ? p.vs : p.ks) + 16 * (lane & 15);
     const uint32_t scale_dst = stage0 + (v_scales ? S::kVS : S::kKS) + 16 * (lane & 15);
-    auto copy_half = [&](int half, int key, int page, uint32_t at) {
-        const unsigned row = static_cast<unsigned>(page) * p.Hkv + job.hk, in_page = key & page_mask;
-        const unsigned long long codes = static_cast<unsigned long long>(row) * (S::kRow << p.log2_bs) +
-                                         in_page * S::kRow + 16 * lane;
-        const char *k = static_cast<const char *>(p.k) + codes, *v = static_cast<const char *>(p.v) + codes;
+    const char *const k_base = static_cast<const char *>(p.k) + 16 * lane;
+    const char *const v_base = static_cast<const char *>(p.v) + 16 * lane;
+    auto copy_half = [&](int half, unsigned place, uint32_t at) {
+        const unsigned long long codes = static_cast<unsigned long long>(place) * (16 * S::kRow);
+        const char *k = k_base + codes, *v = v_base + codes;
 #pragma unroll
         for (int j = 0; j < 16 * S::kRow / 512; ++j) {
             copy16(at + half * 16 * S::kRow + 512 * j + 16 * lane, k + 512 * j);
@@ -142,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
         }
         if (scale_lane)
             copy16(scale_dst + (at - stage0) + half * 16 * S::kSRow,
-                   scale_base + static_cast<unsigned long long>(row) * (S::kSRow << p.log2_bs) + in_page * S::kSRow);
+                   scale_base + static_cast<unsigned long long>(place) * (16 * S::kSRow));
     };
     // Tiles are started in order, one copy group each (empty past the last).
     // Leaves the tile's visible keys with its stage.
@@ -150,19 +153,19 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
         if (i < mine) {
             if (i - base == 16) {
                 base += 16;
-                pages0 = pages1;
-                pages1 = page_of(base + 16 + lane / 2);
+                places0 = places1;
+                places1 = place_of(base + 16 + lane / 2);
             }
             const int key0 = key0_of(i);
-            const int page_a = __shfl_sync(kFull, pages0, 2 * (i & 15)),
-                      page_b = __shfl_sync(kFull, pages0, 2 * (i & 15) + 1);
+            const unsigned a = __shfl_sync(kFull, places0, 2 * (i & 15)),
+                           b = __shfl_sync(kFull, places0, 2 * (i & 15) + 1);
             uint32_t seen = kFull;
-            if ((page_a | page_b) < 0 || key0 < list.w_lo || key0 + 32 > list.L)
-                seen = __ballot_sync(kFull, (lane < 16 ? page_a : page_b) >= 0 && list.sees(key0 + lane));
+            if (a == kNone || b == kNone || key0 < list.w_lo || key0 + 32 > list.L)
+                seen = __ballot_sync(kFull, (lane < 16 ? a : b) != kNone && list.sees(key0 + lane));
             if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(seen_at + 4 * stage), "r"(seen) : "memory");
             const uint32_t at = stage0 + stage * S::kStageBytes;
-            if (page_a >= 0) copy_half(0, key0, page_a, at);
-            if (page_b >= 0) copy_half(1, key0 + 16, page_b, at);
+            if (a != kNone) copy_half(0, a, at);
+            if (b != kNone) copy_half(1, b, at);
         }
         copy_commit();
     };

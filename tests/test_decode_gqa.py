@@ -41,6 +41,8 @@ def test_validation(lib, q4):
     for kw in ({"B": 0}, {"H": 0}, {"Hkv": 0}, {"Hkv": 3}, {"H": 2, "Hkv": 4}, {"nb": 0}, {"bs": 0}, {"bs": 24},
                {"bs": 2048}, {"mb": 0}, {"mb": 1 << 27}, {"window": -1}, {"sinks": -1}, {"B": 1 << 20, "H": 1 << 10}):
         assert call(**kw) == SHAPE, kw
+    if q4:  # rows in sixteens past 32 bits
+        assert call(nb=1 << 26, Hkv=1, bs=1024) == SHAPE
     for s in (0, -1, 1025):
         assert call(S=s) == SPLITS
     for s in (0.0, -1.0, float("nan"), float("inf")):
