@@ -8,9 +8,9 @@
 //
 // Bound by the chain of a step (two products, softmax, three products), as in
 // the causal kernel. 16 packed sequences of 123 to 1994 tokens, 16 heads on 4,
-// D = 128, bf16, window 512, 4 sinks: 394 us, of which the row pass (D_i, zeroed
-// dQ accumulator) 54 at 5.7 TB/s, the main kernel 282 (tensor pipe 46 % active;
-// without sinks about 40 less), dQ's conversion 37 at 6.3 TB/s, the joining of
+// D = 128, bf16, window 512, 4 sinks: 389 us, of which the row pass (D_i, zeroed
+// dQ accumulator) 54 at 5.7 TB/s, the main kernel 277 (tensor pipe 47 % active;
+// without sinks about 45 less), dQ's conversion 37 at 6.3 TB/s, the joining of
 // segments 9.
 #include "fa_bwd.cuh"
 
