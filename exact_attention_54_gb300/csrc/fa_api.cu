@@ -689,14 +689,26 @@ static WindowCut window_cut(size_t base, long long units, int H, int Hkv, int Sq
     // the longest sequence
     const long long reach = 128LL + window < Sq ? 128LL + window : Sq;
     const long long plain = group * ((reach + block - 1) / block), sunk = group * ((Sq + block - 1) / block);
-    // Plain tiles: at least two units for each SM, in up to four segments.
+    // Plain tiles: the count of segments (up to 6, 1024 units in all) that makes
+    // the launch shortest, in half steps: waves of units, each as long as its
+    // steps and 3 to start and end; joining costs one for 64 columns and segment.
+    // A wave takes some units more than there are SMs: the last ones are light.
+    // (16 on 2 heads, 4 x 777 tokens, D = 128, window 200: 84, 56, 47, 56 us with 1 to
+    // 4 segments, 3 taken; 6 on 2 heads, 2 x 777, D = 64, window 300: 35, 25, 21,
+    // 18.5, 4 taken; 8 on 8 heads, 2048, D = 128, window 512: 29, 39, 43, 1 taken.)
+    constexpr long long kSms = 152, kWave = 170;
+    const long long tiles = units * n_kt;
+    long long segs = 1, best = 0;
+    for (long long n = 1; n <= 6 && (n == 1 || tiles * n <= 1024); ++n) {
+        const long long waves = (tiles * n + kWave - 1) / kWave, steps = (plain + n - 1) / n + 3;
+        const long long cost = 2 * waves * steps + (n > 1 ? n * (D / 64) : 0);
+        if (n == 1 || cost < best) {
+            best = cost;
+            segs = n;
+        }
+    }
     // Tiles with sinks: no longer than the plain ones, or a quarter of an SM's
     // share where that is more.
-    constexpr long long kSms = 152;
-    const long long tiles = units * n_kt;
-    long long segs = (2 * kSms + tiles - 1) / tiles;
-    segs = segs < 4 ? segs : 4;
-    if (segs * 8 > plain) segs = 1;
     const long long others = units * (n_kt - c.sink_tiles);
     const long long share = (others * plain + units * c.sink_tiles * sunk) / (4 * kSms);
     const long long most = others > 0 && plain / segs > share ? plain / segs : (share > 8 ? share : 8);

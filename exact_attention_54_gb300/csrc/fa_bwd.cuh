@@ -189,13 +189,10 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------ postprocess --
 
+// Eight values of dQ.
 template <bool BF16>
-__global__ void __launch_bounds__(256) fa_bwd_dq_kernel(const float *__restrict__ acc, uint16_t *__restrict__ dq,
-                                                        long long n8, float scale) {
-    // launched as a dependent of the main kernel: its reductions must be complete
-    ptx::grid_dependency_wait();
-    const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (i >= n8) return;
+__device__ __forceinline__ void convert_dq(const float *__restrict__ acc, uint16_t *__restrict__ dq, long long i,
+                                           float scale) {
     const float4 a = reinterpret_cast<const float4 *>(acc)[2 * i];
     const float4 b = reinterpret_cast<const float4 *>(acc)[2 * i + 1];
     uint4 out;
@@ -204,6 +201,15 @@ __global__ void __launch_bounds__(256) fa_bwd_dq_kernel(const float *__restrict_
     out.z = ptx::pack2<BF16>(b.x * scale, b.y * scale);
     out.w = ptx::pack2<BF16>(b.z * scale, b.w * scale);
     reinterpret_cast<uint4 *>(dq)[i] = out;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) fa_bwd_dq_kernel(const float *__restrict__ acc, uint16_t *__restrict__ dq,
+                                                        long long n8, float scale) {
+    // launched as a dependent of the main kernel: its reductions must be complete
+    ptx::grid_dependency_wait();
+    const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i < n8) convert_dq<BF16>(acc, dq, i, scale);
 }
 
 // ------------------------------------------------------------ main kernel --
@@ -317,7 +323,7 @@ __device__ __forceinline__ int query_blocks(const BwdParams &p, const BwdUnit &u
 // Segments: a unit's steps grow with the query heads that share its key head,
 // and a tile of sinks is seen by all later queries, so one CTA would still be
 // busy with a few such units when the others are done. Cut, each segment's dK
-// and dV go to the workspace in fp32 and fa_bwd_join_kernel adds them up in
+// and dV go to the workspace in fp32 and the last launch adds them up in
 // order. (32 query heads on 8 key heads, 4096 tokens, window 1024, 4 sinks: the
 // longest units have 256 steps of 64 queries, the others 72.)
 struct WinSteps {
@@ -1542,10 +1548,10 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
 constexpr int kJoinCtas = 8;
 
 template <int D, bool BF16, bool VARLEN>
-__global__ void __launch_bounds__(256) fa_bwd_join_kernel(const BwdParams p) {
+__device__ __forceinline__ void join_segments(const BwdParams &p, int item, int part) {
     constexpr int kBlockQ = D == 64 ? 128 : ShapeQ64::kQ;
     const int tiles = p.segs > 1 ? p.n_ktiles : p.sink_tiles;
-    const int unit = static_cast<int>(blockIdx.x) / tiles, kt = static_cast<int>(blockIdx.x) % tiles;
+    const int unit = item / tiles, kt = item % tiles;
     BwdUnit u{};
     u.kt = kt;
     int heads = 1;
@@ -1569,7 +1575,7 @@ __global__ void __launch_bounds__(256) fa_bwd_join_kernel(const BwdParams p) {
     if (k0 >= u.Lk) return;
     const int parts = unit_steps<true, true, kBlockQ>(p, u, k0).parts;
     if (parts < 2) return;
-    for (int i = blockIdx.y * 256 + threadIdx.x; i < 2 * kBlock * (D / 8); i += kJoinCtas * 256) {
+    for (int i = part * 256 + threadIdx.x; i < 2 * kBlock * (D / 8); i += kJoinCtas * 256) {
         const int r = i % kBlock, c8 = i / kBlock % (D / 8), t = i / (kBlock * (D / 8));
         if (k0 + r >= u.Lk) continue;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
@@ -1586,6 +1592,21 @@ __global__ void __launch_bounds__(256) fa_bwd_join_kernel(const BwdParams p) {
             make_uint4(ptx::pack2<BF16>(a.x * f, a.y * f), ptx::pack2<BF16>(a.z * f, a.w * f),
                        ptx::pack2<BF16>(b.x * f, b.y * f), ptx::pack2<BF16>(b.z * f, b.w * f));
     }
+}
+
+// The last launch where key tiles were cut: the first `join_ctas` CTAs join
+// segments, the others convert dQ.
+template <int D, bool BF16, bool VARLEN>
+__global__ void __launch_bounds__(256) fa_bwd_finish_kernel(const BwdParams p, uint16_t *__restrict__ dq, long long n8,
+                                                            int join_ctas) {
+    ptx::grid_dependency_wait();  // a dependent of the main kernel, as fa_bwd_dq_kernel
+    const int x = static_cast<int>(blockIdx.x);
+    if (x < join_ctas) {
+        join_segments<D, BF16, VARLEN>(p, x / kJoinCtas, x % kJoinCtas);
+        return;
+    }
+    const long long i = static_cast<long long>(x - join_ctas) * 256 + threadIdx.x;
+    if (i < n8) convert_dq<BF16>(p.dq_acc, dq, i, p.scale);
 }
 
 template <int D, bool BF16, bool CAUSAL, bool VARLEN, bool WIN = false>
@@ -1631,15 +1652,16 @@ cudaError_t launch_t(const CUtensorMap *maps, const void *o, const void *dout, c
     cfg2.stream = st;
     cfg2.attrs = pdl;
     cfg2.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg2, fa_bwd_dq_kernel<BF16>, static_cast<const float *>(p.dq_acc),
-                           static_cast<uint16_t *>(dq), n8, p.scale);
     if constexpr (WIN) {
-        if (e != cudaSuccess || (p.segs == 1 && p.segs_sink == 1)) return e;
-        const unsigned tiles = p.segs > 1 ? p.n_ktiles : p.sink_tiles;
-        fa_bwd_join_kernel<D, BF16, VARLEN><<<dim3(p.units * tiles, kJoinCtas), 256, 0, st>>>(p);
-        e = cudaGetLastError();
+        if (p.segs > 1 || p.segs_sink > 1) {  // fewer than 608 such tiles (see the cut)
+            const int join_ctas = p.units * (p.segs > 1 ? p.n_ktiles : p.sink_tiles) * kJoinCtas;
+            cfg2.gridDim.x += join_ctas;
+            return cudaLaunchKernelEx(&cfg2, fa_bwd_finish_kernel<D, BF16, VARLEN>, p, static_cast<uint16_t *>(dq), n8,
+                                      join_ctas);
+        }
     }
-    return e;
+    return cudaLaunchKernelEx(&cfg2, fa_bwd_dq_kernel<BF16>, static_cast<const float *>(p.dq_acc),
+                              static_cast<uint16_t *>(dq), n8, p.scale);
 }
 
 }  // namespace bwd

@@ -10,8 +10,8 @@
 // the causal kernel. 16 packed sequences of 123 to 1994 tokens, 16 heads on 4,
 // D = 128, bf16, window 512, 4 sinks: 389 us, of which the row pass (D_i, zeroed
 // dQ accumulator) 54 at 5.7 TB/s, the main kernel 277 (tensor pipe 47 % active;
-// without sinks about 45 less), dQ's conversion 37 at 6.3 TB/s, the joining of
-// segments 9.
+// without sinks about 45 less), the conversion of dQ, at 6.3 TB/s by itself, and
+// the joining of segments the rest.
 #include "fa_bwd.cuh"
 
 namespace fa {

@@ -384,7 +384,7 @@ FA_API size_t fa_bwd_window_varlen_workspace_bytes(int num_seqs, int total_q, in
  * that share a key head. workspace: at least fa_bwd_window_workspace_bytes
  * bytes, otherwise as for fa_bwd. Queries that see no key get dq = 0, keys that
  * no query sees dk = dv = 0. dk and dv are deterministic, dq rounds as in
- * fa_bwd. Three launches, or four.
+ * fa_bwd. Three launches.
  * Errors: as fa_bwd and fa_fwd_window.
  */
 FA_API fa_status_t fa_bwd_window(const void *q, const void *k, const void *v, const void *o, const void *dout,

@@ -233,14 +233,15 @@ def test_long_key_tiles_take_more_workspace(lib):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("D", [64, 128])
-def test_wide_window_is_causal_attention_bit_for_bit(D):
+def test_wide_window_is_causal_attention(D):
+    """Forward: bit for bit. The gradients' sums may be cut elsewhere: against the definition."""
     q, k, v, do = draw(2, 3, 3, 600, 600, D, torch.bfloat16, seed=3)
     got = run_dense(q, k, v, do, 600, 0)
-    qd, kd, vd, dd = (x.cuda() for x in (q, k, v, do))
-    o, lse = fa.flash_attention(qd, kd, vd, causal=True)
-    _, dk, dv = fa.flash_attention_bwd(qd, kd, vd, o, lse, dd, causal=True)
-    for n, x in (("o", o), ("lse", lse), ("dv", dv)) + ((("dk", dk),) if D == 64 else ()):  # D = 128: dS from fp32 P
-        assert torch.equal(got[n], x), n
+    o, lse = fa.flash_attention(*(x.cuda() for x in (q, k, v)), causal=True)
+    assert torch.equal(got["o"], o) and torch.equal(got["lse"], lse)
+    for b in range(2):
+        ref = plain_ops.window_attention(q[b], k[b], v[b], 600, 0, D ** -0.5, do[b])
+        plain_ops.assert_window_close({n: x[b] for n, x in got.items()}, ref, f"sequence {b}")
 
 
 @pytest.mark.gpu
