@@ -11,8 +11,9 @@
 // read 6 us.)
 // Per query head it keeps a running maximum m of the scores in base-2 units
 // (moved only when a score exceeds it by 2^8), l = sum 2^(x - m) and
-// O = sum 2^(x - m) v; the weights are rounded to the cache's type for the
-// second product, as in the prefill kernels; sums are fp32. Bound by HBM: K and
+// O = sum 2^(x - m) v; a weight enters the second product as two numbers of the
+// cache's type (its rounding and the rest), which costs nothing here; sums are
+// fp32. Bound by HBM: K and
 // V of the visible keys are read once for a group of up to 16 query heads.
 #include <climits>
 
@@ -211,7 +212,10 @@ __global__ void __launch_bounds__(kThreads, kWindowCtas<NT>) fa_decode_window_ke
                 for (int k = 0; k < 4; ++k) e[n][k] = fmaf(x[n][k], p.scale_log2, -m[n][k % 2]);
             }
         }
-        uint32_t b0[NT], b1[NT];
+        uint32_t b0[NT], b1[NT], r0[NT], r1[NT];  // weights, and what their rounding leaves
+        auto rest = [](uint32_t w, float lo, float hi) {
+            return pack16<BF16>(lo - ptx::unpack_lo<BF16>(w), hi - ptx::unpack_hi<BF16>(w));
+        };
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -219,8 +223,11 @@ __global__ void __launch_bounds__(kThreads, kWindowCtas<NT>) fa_decode_window_ke
                 x[n][k] = ptx::ex2(e[n][k]);
                 l[n][k % 2] += x[n][k];
             }
-            b0[n] = transpose8x8(pack16<BF16>(x[n][0], x[n][1]));
-            b1[n] = transpose8x8(pack16<BF16>(x[n][2], x[n][3]));
+            const uint32_t w0 = pack16<BF16>(x[n][0], x[n][1]), w1 = pack16<BF16>(x[n][2], x[n][3]);
+            b0[n] = transpose8x8(w0);
+            b1[n] = transpose8x8(w1);
+            r0[n] = transpose8x8(rest(w0, x[n][0], x[n][1]));
+            r1[n] = transpose8x8(rest(w1, x[n][2], x[n][3]));
         }
         // ---- O^T += V^T P^T ----
 #pragma unroll
@@ -230,7 +237,10 @@ __global__ void __launch_bounds__(kThreads, kWindowCtas<NT>) fa_decode_window_ke
             const uint32_t a2 = __byte_perm(t.v[2][j], t.v[3][j], 0x5410);
             const uint32_t a3 = __byte_perm(t.v[2][j], t.v[3][j], 0x7632);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816<BF16>(o[j][n], a0, a1, a2, a3, b0[n], b1[n]);
+            for (int n = 0; n < NT; ++n) {
+                mma16816<BF16>(o[j][n], a0, a1, a2, a3, b0[n], b1[n]);
+                mma16816<BF16>(o[j][n], a0, a1, a2, a3, r0[n], r1[n]);
+            }
         }
         if (i + 1 - base >= 32) {
             base += 32;

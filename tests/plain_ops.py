@@ -77,11 +77,15 @@ def softmax_attention(q, k, v, seen, scale):
 
 def decode(q, values, table, lens, block, window, sinks, scale):
     """q [B,H,1,D]; values(page, head) -> (k, v, s) double [block, D] of one page, s the value's scale (4-bit cache) or
-    0; the definition of the paged decode. Returns o [B,H,D], lse [B,H], what meets in o: sum p |v|, and ``low``:
+    0; the definition of the paged decode. Returns o [B,H,D], lse [B,H], what meets in o: sum p |v|, and ``low``, what
+    the rounding of the weights allows:
 
-    The 4-bit cache's weights p s are rounded to fp16 after a factor r that brings the largest to at least 2^-4, where
-    they lose up to 2^-25 each below the normal numbers: 2^-21 max(p s) |n| in o. r follows the running maximum by
-    whole powers of two, so the largest may halve with each of its moves by 2^8 or more; after M moves p is under
+    16-bit cache: a weight is the sum of two numbers of its type, off by h^2 relative (h: half a step) and, below
+    fp16's normal numbers, 2^-25 of the largest, which is at least 1.
+
+    4-bit cache: p s is rounded to fp16 (2^-11) after a factor r that brings the largest to at least 2^-4, where they
+    lose up to 2^-25 each below the normal numbers: 2^-21 max(p s) |n| in o. r follows the running maximum by whole
+    powers of two, so the largest may halve with each of its moves by 2^8 or more; after M moves p is under
     2^(8 - 8M), so it is only the largest of p s while s differs by more: M <= 1 + log2(max s / min s) / 8."""
     B, H, _, D = q.shape
     o, size, low = (torch.zeros(B, H, D, dtype=torch.float64) for _ in range(3))
@@ -102,13 +106,15 @@ def decode(q, values, table, lens, block, window, sinks, scale):
             if (s > 0).any():
                 moves = 1 + math.floor(math.log2(float(s.max() / s[s > 0].min())) / 8)
                 n = (v / torch.where(s > 0, s, torch.ones_like(s))).abs()
-                low[b, h] = 2.0 ** (moves - 21) * (r[2][0][:, None] * s).amax(0) * n.sum(0)
+                low[b, h] = 2.0 ** (moves - 21) * (r[2][0][:, None] * s).amax(0) * n.sum(0) + 2.0 ** -11 * size[b, h]
+            else:
+                low[b, h] = half_step(q.dtype) ** 2 * size[b, h] + 2.0 ** -25 * v.abs().sum(0)
     return o, lse, size, low
 
 
 def assert_attention_close(o, lse, ro, rl, size, low, dtype, what=""):
-    """O within half a step of its own rounding, half a step of the 16-bit type on each weight, 2^-13 of
-    what meets in the sum for the rest, and ``low`` (see decode); LSE within 4e-5 + 2^-21 |LSE|.
+    """O within half a step of its own rounding, ``low`` for its weights (see decode), and 2^-13 of what meets in the
+    sum for the rest; LSE within 4e-5 + 2^-21 |LSE|.
 
     The rest: a score is an fp32 sum of D products, |error| <= 2^-24 * 16 * sum |q k| scale (16: depth of the
     sums), under 2^-24 * 16 * 40 = 2^-14.7 for the inputs here; it enters a weight as a relative error, once in
@@ -118,7 +124,7 @@ def assert_attention_close(o, lse, ro, rl, size, low, dtype, what=""):
     assert torch.equal(torch.isnan(o), torch.isnan(ro)) and torch.equal(torch.isnan(lse), torch.isnan(rl)), what
     h = half_step(dtype)
     tiny = torch.finfo(dtype).smallest_normal * h * 2
-    bound = h * ro.abs() * (1 + 2 * h) + (h * (1 + h) + 2.0 ** -13) * size + low + tiny
+    bound = h * ro.abs() * (1 + 2 * h) + 2.0 ** -13 * size + low * (1 + 2 * h) + tiny
     bad = ((o - ro).abs() > bound) & ~torch.isnan(ro)
     assert not bad.any(), (what, "o", float(((o - ro).abs() / bound).nan_to_num().max()), torch.nonzero(bad)[0].tolist())
     empty = torch.isinf(rl)

@@ -244,7 +244,7 @@ def test_sizes_of_values(q4, dtype):
         h = plain_ops.half_step(dtype)
         tiny = torch.finfo(dtype).smallest_normal * 2 * h
         err = (o.double().cpu().view(ro.shape) - ro).abs()
-        assert (err <= h * ro.abs() * 1.01 + (h * 1.01 + 2.0 ** -13 + 2 * wide) * size + low + tiny).all()
+        assert (err <= h * ro.abs() * 1.01 + (2.0 ** -13 + 2 * wide) * size + low * 1.01 + tiny).all()
         assert ((lse.double().cpu() - rl).abs() <= 4e-5 + wide + 2.0 ** -21 * rl.abs()).all()
 
 
