@@ -378,3 +378,38 @@ def test_written_cache_decodes_like_what_is_read_back():
     assert torch.equal(kr.cpu(), plain_ops.q4_values(plain_ops.q4_pack(n), s).float().to(dtype))
     n, s = plain_ops.q4_quantise(v.cpu())
     assert torch.equal(vr.cpu(), plain_ops.q4_values(plain_ops.q4_pack(n), s).float().to(dtype))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q4", [False, True], ids=["16bit", "q4"])
+def test_pages_past_4_gb(q4):
+    """The same pages at the start of a small cache and at the end of one whose arrays pass 2^32 bytes."""
+    H, Hkv, D, block, lens = 8, 8, 128, 16, [100, 65]
+    q, cache, table, sl = make(2, H, Hkv, D, block, lens, torch.bfloat16, q4, seed=23)
+    base = run(q, cache, table, sl, 0, 0, q4)
+    n = cache[0].shape[0]
+    page_bytes = cache[0][0].numel() * cache[0].element_size()
+    blocks = (1 << 32) // page_bytes + 1000
+    big = []
+    for t in cache:
+        x = torch.empty((blocks,) + t.shape[1:], dtype=t.dtype, device="cuda")
+        x[-n:] = t.cuda()
+        big.append(x)
+    far = torch.where(table >= 0, table + (blocks - n), table).to(torch.int32).cuda()
+    if q4:
+        c = fa.KVCacheQ4(*big)
+        got = fa.flash_decode_paged_q4(q.cuda(), c, far, sl.cuda())
+        # and rows written and read there
+        k, v = (inputs.randn((165, Hkv, D), torch.bfloat16, torch.Generator().manual_seed(i)).cuda() for i in (24, 25))
+        cu = inputs.cu_from_lengths(lens).cuda()
+        fa.flash_kv_write_q4(k, v, c, far, cu, 100)
+        small = fa.KVCacheQ4(*(t.cuda() for t in cache))
+        fa.flash_kv_write_q4(k, v, small, table.cuda(), cu, 100)
+        for a, b in zip(c, small):
+            assert torch.equal(a[-n:].view(torch.uint8), b.view(torch.uint8))
+        for a, b in zip(fa.flash_kv_read_q4(c, far, cu, 165, 100), fa.flash_kv_read_q4(small, table.cuda(), cu, 165, 100)):
+            assert torch.equal(a, b)
+    else:
+        got = fa.flash_decode_paged_window(q.cuda(), *big, far, sl.cuda(), 0)
+    fa.fa_check_device_error()
+    assert torch.equal(got[0], base[0]) and torch.equal(got[1], base[1])
