@@ -13,10 +13,10 @@
 // a lane took 8 columns before, 20 % slower; divisions by Hkv in the kernels, 8 %.
 //
 // Grid: a chunk of tokens (x) of one sequence (y, z) per CTA, so that a token's
-// sequence needs no search in cu_seqlens and no division; the
-// chunk's cache rows are looked up once, into shared memory. D / 16 lanes share
-// a row of one key head, 16 columns each; a thread takes the key row and the
-// value row of kPasses (token, head) pairs with all loads in flight.
+// sequence needs no search in cu_seqlens and no division; the chunk's cache rows
+// are looked up once, into shared memory. D / 16 lanes share a row of one key
+// head, 16 columns each; a thread takes the key row and the value row of kPasses
+// (token, head) pairs with all loads in flight.
 #include "fa_kv_q4.cuh"
 #include "fa_launch.h"
 
@@ -257,7 +257,8 @@ __device__ __forceinline__ uint4 unpack8(uint32_t word, uint16_t s) {
             const __nv_bfloat162 y = __hmul2_rn(n, __bfloat162bfloat162(__ushort_as_bfloat16(s)));
             v[i] = *reinterpret_cast<const uint32_t *>(&y);
         } else {
-            const __half2 n = __hsub2(*reinterpret_cast<const __half2 *>(&u), __half2half2(__ushort_as_half(0x6408)));  // 1032
+            const __half2 n = __hsub2(*reinterpret_cast<const __half2 *>(&u),
+                                      __half2half2(__ushort_as_half(0x6408)));  // 1032
             const __half2 y = __hmul2_rn(n, __half2half2(__ushort_as_half(s)));
             v[i] = *reinterpret_cast<const uint32_t *>(&y);
         }

@@ -22,12 +22,6 @@ namespace q4 {
 
 constexpr int kGroup = 32;  // columns per scale
 
-// byte of a row that holds column d (its nibble is d % 2)
-template <int D>
-__host__ __device__ constexpr int code_byte(int d) {
-    return (d % kGroup / 4) * (D / 16) + 2 * (d / kGroup) + d % 4 / 2;
-}
-
 template <bool BF16>
 __device__ __forceinline__ float from16(uint16_t x) {
     if constexpr (BF16) return __uint_as_float(static_cast<uint32_t>(x) << 16);
