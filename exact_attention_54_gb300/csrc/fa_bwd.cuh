@@ -1594,8 +1594,8 @@ __device__ __forceinline__ void join_segments(const BwdParams &p, int item, int 
     }
 }
 
-// The last launch where key tiles were cut: the first `join_ctas` CTAs join
-// segments, the others convert dQ.
+// WIN: the last launch. The first `join_ctas` CTAs join segments, the others
+// convert dQ.
 template <int D, bool BF16, bool VARLEN>
 __global__ void __launch_bounds__(256) fa_bwd_finish_kernel(const BwdParams p, uint16_t *__restrict__ dq, long long n8,
                                                             int join_ctas) {
@@ -1605,7 +1605,8 @@ __global__ void __launch_bounds__(256) fa_bwd_finish_kernel(const BwdParams p, u
         join_segments<D, BF16, VARLEN>(p, x / kJoinCtas, x % kJoinCtas);
         return;
     }
-    const long long i = static_cast<long long>(x - join_ctas) * 256 + threadIdx.x;
+    // from the end: the accumulator's last rows are in L2 still
+    const long long i = static_cast<long long>(gridDim.x - 1 - x) * 256 + threadIdx.x;
     if (i < n8) convert_dq<BF16>(p.dq_acc, dq, i, p.scale);
 }
 
@@ -1653,15 +1654,17 @@ cudaError_t launch_t(const CUtensorMap *maps, const void *o, const void *dout, c
     cfg2.attrs = pdl;
     cfg2.numAttrs = 1;
     if constexpr (WIN) {
-        if (p.segs > 1 || p.segs_sink > 1) {  // fewer than 608 such tiles (see the cut)
-            const int join_ctas = p.units * (p.segs > 1 ? p.n_ktiles : p.sink_tiles) * kJoinCtas;
-            cfg2.gridDim.x += join_ctas;
-            return cudaLaunchKernelEx(&cfg2, fa_bwd_finish_kernel<D, BF16, VARLEN>, p, static_cast<uint16_t *>(dq), n8,
-                                      join_ctas);
-        }
+        // fewer than 608 tiles are cut (see the cut)
+        const int join_ctas = p.segs > 1 || p.segs_sink > 1
+                                  ? p.units * (p.segs > 1 ? p.n_ktiles : p.sink_tiles) * kJoinCtas
+                                  : 0;
+        cfg2.gridDim.x += join_ctas;
+        return cudaLaunchKernelEx(&cfg2, fa_bwd_finish_kernel<D, BF16, VARLEN>, p, static_cast<uint16_t *>(dq), n8,
+                                  join_ctas);
+    } else {
+        return cudaLaunchKernelEx(&cfg2, fa_bwd_dq_kernel<BF16>, static_cast<const float *>(p.dq_acc),
+                                  static_cast<uint16_t *>(dq), n8, p.scale);
     }
-    return cudaLaunchKernelEx(&cfg2, fa_bwd_dq_kernel<BF16>, static_cast<const float *>(p.dq_acc),
-                              static_cast<uint16_t *>(dq), n8, p.scale);
 }
 
 }  // namespace bwd
