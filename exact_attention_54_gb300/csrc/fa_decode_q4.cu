@@ -24,9 +24,9 @@
 // to save instructions. Tiles of 32 keys come by asynchronous copies into a
 // ring per warp (4.5 KB a tile at D = 128, two in flight), which leaves the
 // registers to the accumulators: four CTAs (16 warps) per SM. 16 sequences of
-// 16384 to 32768 keys, 8 key heads, 32 heads, D = 128: 117 us, 4.1 TB/s, where
-// the bytes alone take 70 us; some 350 warp instructions per 16 keys, the ALU
-// pipe 53 % active. (Bulk copies in place of these, eight per tile with 16-key
+// 16384 to 32768 keys, 8 key heads, 32 heads, D = 128: 113 us, 4.2 TB/s, where
+// the bytes alone take 70 us; some 330 warp instructions per 16 keys, the ALU
+// pipe half of the time. (Bulk copies in place of these, eight per tile with 16-key
 // pages, cost a loop over the issuing lanes each and 8 us of it.)
 #include "fa_decode_gqa.cuh"
 
@@ -258,13 +258,13 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
     }
 
     __syncthreads();
-    float o[MT][NT][4], m[NT][2], l[NT][2];
+    float o[MT][NT][4], nm[NT][2], l[NT][2];  // nm: -m, as the exponents take it
     float r[NT][W][2];  // power-of-two factor of the weights of group w
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            m[t][k] = kNoMax;
+            nm[t][k] = -kNoMax;
             l[t][k] = 0.f;
 #pragma unroll
             for (int w = 0; w < W; ++w) r[t][w][k] = kMostFactor;
@@ -341,7 +341,10 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) e[h][n][k] = fmaf(x[h][n][k], to_log2[n][k % 2], -m[n][k % 2]);
+                for (int k = 0; k < 4; k += 2)
+                    ptx::upk2(ptx::ffma2(ptx::pk2(x[h][n][k], x[h][n][k + 1]), ptx::pk2(to_log2[n][0], to_log2[n][1]),
+                                         ptx::pk2(nm[n][0], nm[n][1])),
+                              e[h][n][k], e[h][n][k + 1]);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             most_e[n] = fmaxf(ptx::fmax3(ptx::fmax3(e[0][n][0], e[0][n][1], e[0][n][2]),
@@ -356,10 +359,10 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
                     a[k] = 1.f;
-                    if (fmaf(mx, to_log2[n][k], -m[n][k]) > kMoveMax) {  // per head: no head depends on another
+                    if (fmaf(mx, to_log2[n][k], nm[n][k]) > kMoveMax) {  // per head: no head depends on another
                         const float next = mx * to_log2[n][k];
-                        a[k] = ptx::ex2(m[n][k] - next);
-                        m[n][k] = next;
+                        a[k] = ptx::ex2(-nm[n][k] - next);
+                        nm[n][k] = -next;
                     }
                     l[n][k] *= a[k];
                 }
@@ -389,16 +392,18 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) e[h][n][k] = fmaf(x[h][n][k], to_log2[n][k % 2], -m[n][k % 2]);
+                    for (int k = 0; k < 4; ++k) e[h][n][k] = fmaf(x[h][n][k], to_log2[n][k % 2], nm[n][k % 2]);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 4; k += 2) {
                     x[h][n][k] = ptx::ex2(e[h][n][k]);
-                    l[n][k % 2] += x[h][n][k];
+                    x[h][n][k + 1] = ptx::ex2(e[h][n][k + 1]);
+                    ptx::upk2(ptx::fadd2(ptx::pk2(l[n][0], l[n][1]), ptx::pk2(x[h][n][k], x[h][n][k + 1])), l[n][0],
+                              l[n][1]);
                 }
         // ---- O^T += V^T P^T, 16 keys at a time ----
 #pragma unroll
@@ -525,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
             for (int off = 4; off < 32; off <<= 1) l[t][k] += __shfl_xor_sync(kFull, l[t][k], off);
             const int head = 8 * t + 2 * c + k;
             if (g == 0) {
-                sm_m[warp][head] = m[t][k] == kNoMax ? -CUDART_INF_F : m[t][k];
+                sm_m[warp][head] = nm[t][k] == -kNoMax ? -CUDART_INF_F : -nm[t][k];
                 sm_l[warp][head] = l[t][k];
             }
 #pragma unroll
