@@ -315,8 +315,11 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
                     mma16816<false>(acc, a[0][0], a[1][0], a[0][1], a[1][1], q[0], q[1]);
                     mma16816<false>(acc, a[0][2], a[1][2], a[0][3], a[1][3], q[2], q[3]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        x[h][n][j] = w == 0 ? sc[j / 2] * acc[j] : fmaf(sc[j / 2], acc[j], x[h][n][j]);
+                    for (int j = 0; j < 4; j += 2) {
+                        const uint64_t s2 = ptx::pk2(sc[j / 2], sc[j / 2]), y = ptx::pk2(acc[j], acc[j + 1]);
+                        ptx::upk2(w == 0 ? mul2(s2, y) : ptx::ffma2(s2, y, ptx::pk2(x[h][n][j], x[h][n][j + 1])),
+                                  x[h][n][j], x[h][n][j + 1]);
+                    }
                 }
             }
         }
