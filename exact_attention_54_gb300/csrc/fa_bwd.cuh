@@ -374,6 +374,26 @@ __device__ __forceinline__ BwdUnit query_side(const BwdParams &p, const BwdUnit 
     return q;
 }
 
+// WIN: P of two queries, 2^(s scale - lse2), and dS = P (dP - D_i), two at a time.
+__device__ __forceinline__ void weights2(uint32_t s0, uint32_t s1, float minus_scale, float l0, float l1, float &e0,
+                                         float &e1) {
+    float y0, y1;
+    ptx::upk2(ptx::ffma2(ptx::pk2(__uint_as_float(s0), __uint_as_float(s1)), ptx::pk2(minus_scale, minus_scale),
+                         ptx::pk2(l0, l1)),
+              y0, y1);
+    e0 = ptx::ex2(-y0);
+    e1 = ptx::ex2(-y1);
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t ds2(float e0, float e1, uint32_t dp0, uint32_t dp1, float d0, float d1) {
+    const uint64_t x = ptx::ffma2(ptx::pk2(d0, d1), ptx::pk2(-1.f, -1.f),
+                                  ptx::pk2(__uint_as_float(dp0), __uint_as_float(dp1)));
+    float y0, y1;
+    ptx::upk2(ptx::fmul2(ptx::pk2(e0, e1), x), y0, y1);
+    return ptx::pack2<BF16>(y0, y1);
+}
+
 // The queries lo <= i < hi of a chunk as bits (a mask test is then one
 // instruction).
 __device__ __forceinline__ uint32_t query_bits(int lo, int hi) {
@@ -686,15 +706,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float4 lv = lq[j / 4], dv4 = dq4[j / 4];
                     const float l0 = (j % 4 == 0) ? lv.x : lv.z, l1 = (j % 4 == 0) ? lv.y : lv.w;
                     const float d0 = (j % 4 == 0) ? dv4.x : dv4.z, d1 = (j % 4 == 0) ? dv4.y : dv4.w;
-                    float e0 = ptx::ex2(fmaf(__uint_as_float(sv[j]), p.scale_log2, -l0));
-                    float e1 = ptx::ex2(fmaf(__uint_as_float(sv[j + 1]), p.scale_log2, -l1));
+                    float e0, e1;
+                    if constexpr (WIN) {
+                        weights2(sv[j], sv[j + 1], -p.scale_log2, l0, l1, e0, e1);
+                    } else {
+                        e0 = ptx::ex2(fmaf(__uint_as_float(sv[j]), p.scale_log2, -l0));
+                        e1 = ptx::ex2(fmaf(__uint_as_float(sv[j + 1]), p.scale_log2, -l1));
+                    }
                     if (need_mask) {
                         if (WIN ? !(seen & (1u << j)) : j < lo) e0 = 0.f;
                         if (WIN ? !(seen & (2u << j)) : j + 1 < lo) e1 = 0.f;
                     }
                     pp[j / 2] = ptx::pack2<BF16>(e0, e1);
-                    dd[j / 2] = ptx::pack2<BF16>(e0 * (__uint_as_float(dpv[j]) - d0),
-                                                 e1 * (__uint_as_float(dpv[j + 1]) - d1));
+                    dd[j / 2] = WIN ? ds2<BF16>(e0, e1, dpv[j], dpv[j + 1], d0, d1)
+                                    : ptx::pack2<BF16>(e0 * (__uint_as_float(dpv[j]) - d0),
+                                                       e1 * (__uint_as_float(dpv[j + 1]) - d1));
                 }
                 // P^T for queries [32c, 32c+32) goes to columns 64h + 16 cl: inside
                 // this half's own S^T columns, which it has already read
@@ -1320,8 +1346,13 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
             for (int i = 0; i < 32; i += 2) {
                 const float4 lv = lq[i / 4];
                 const float l0 = (i % 4 == 0) ? lv.x : lv.z, l1 = (i % 4 == 0) ? lv.y : lv.w;
-                float e0 = ptx::ex2(fmaf(__uint_as_float(sv[i]), p.scale_log2, -l0));
-                float e1 = ptx::ex2(fmaf(__uint_as_float(sv[i + 1]), p.scale_log2, -l1));
+                float e0, e1;
+                if constexpr (WIN) {
+                    weights2(sv[i], sv[i + 1], -p.scale_log2, l0, l1, e0, e1);
+                } else {
+                    e0 = ptx::ex2(fmaf(__uint_as_float(sv[i]), p.scale_log2, -l0));
+                    e1 = ptx::ex2(fmaf(__uint_as_float(sv[i + 1]), p.scale_log2, -l1));
+                }
                 if (need_mask) {
                     if (WIN ? !(seen & (1u << i)) : i < lo) e0 = 0.f;
                     if (WIN ? !(seen & (2u << i)) : i + 1 < lo) e1 = 0.f;
@@ -1353,8 +1384,9 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
                 const float d0 = (i % 4 == 0) ? dv4.x : dv4.z, d1 = (i % 4 == 0) ? dv4.y : dv4.w;
                 const float e0 = WIN ? __uint_as_float(sv[i]) : ptx::unpack_lo<BF16>(pp[i / 2]);
                 const float e1 = WIN ? __uint_as_float(sv[i + 1]) : ptx::unpack_hi<BF16>(pp[i / 2]);
-                dd[i / 2] = ptx::pack2<BF16>(e0 * (__uint_as_float(dpv[i]) - d0),
-                                             e1 * (__uint_as_float(dpv[i + 1]) - d1));
+                dd[i / 2] = WIN ? ds2<BF16>(e0, e1, dpv[i], dpv[i + 1], d0, d1)
+                                : ptx::pack2<BF16>(e0 * (__uint_as_float(dpv[i]) - d0),
+                                                   e1 * (__uint_as_float(dpv[i + 1]) - d1));
             }
             // dS^T buffer b is free once sub-step J-2's dQ_t^T and dK have read it
             if (J >= 2 && !(ok = wait(S::kDSFree + b, ((J - 2) >> 1) & 1))) break;

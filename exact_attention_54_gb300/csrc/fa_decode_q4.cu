@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
 #pragma unroll
                     for (int j = 0; j < 4; j += 2) {
                         const uint64_t s2 = ptx::pk2(sc[j / 2], sc[j / 2]), y = ptx::pk2(acc[j], acc[j + 1]);
-                        ptx::upk2(w == 0 ? mul2(s2, y) : ptx::ffma2(s2, y, ptx::pk2(x[h][n][j], x[h][n][j + 1])),
+                        ptx::upk2(w == 0 ? ptx::fmul2(s2, y) : ptx::ffma2(s2, y, ptx::pk2(x[h][n][j], x[h][n][j + 1])),
                                   x[h][n][j], x[h][n][j + 1]);
                     }
                 }
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, (Q4Shape<D, NT>::kCtas)) fa_decode_q
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const float s = v_scale(i, w);
-                    const uint64_t y = mul2(mul2(ptx::pk2(x[h][n][2 * i], x[h][n][2 * i + 1]), ptx::pk2(s, s)), rr);
+                    const uint64_t y = ptx::fmul2(ptx::fmul2(ptx::pk2(x[h][n][2 * i], x[h][n][2 * i + 1]), ptx::pk2(s, s)), rr);
                     float y0, y1;
                     ptx::upk2(y, y0, y1);
                     pw[n][w][i] = pack16<false>(y0, y1);
