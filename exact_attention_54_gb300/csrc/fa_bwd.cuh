@@ -1315,10 +1315,11 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
           const BwdUnit &u = uv.u;
           const int k0 = uv.k0, qs0 = uv.qs0, n = uv.n;
           const int key = k0 + r;
+          int next_block = WIN && n > 0 ? uv.first % uv.blocks : 0;
           for (int j = 0; j < n; ++j, ++J) {
             const int b = J & 1;
-            int block;
-            query_side<WIN>(p, u, uv.first + j, uv.blocks, block);
+            const int block = WIN ? next_block : j;
+            if (WIN && ++next_block == uv.blocks) next_block = 0;
             const int qc = qs0 + block * S::kQ + 32 * h;  // first query of this warp's chunk
             const uint32_t tb = tmem + lane_base + S::kTmemBuf + 128 * b;
             // the sub-step's rows, then S^T: one test of both first, the
