@@ -8,10 +8,10 @@
 //
 // Bound by the chain of a step (two products, softmax, three products), as in
 // the causal kernel. 16 packed sequences of 123 to 1994 tokens, 16 heads on 4,
-// D = 128, bf16, window 512, 4 sinks: 389 us, of which the row pass (D_i, zeroed
-// dQ accumulator) 54 at 5.7 TB/s, the main kernel 277 (tensor pipe 47 % active;
-// without sinks about 45 less), the conversion of dQ, at 6.3 TB/s by itself, and
-// the joining of segments the rest.
+// D = 128, bf16, window 512, 4 sinks: 382 us, of which the row pass (D_i, zeroed
+// dQ accumulator) 54 at 5.7 TB/s, the main kernel 276 (tensor pipe 47 % active;
+// without sinks about 43 less), the conversion of dQ and the joining of segments,
+// in one launch, 44.
 #include "fa_bwd.cuh"
 
 namespace fa {
