@@ -738,7 +738,7 @@ def flash_kv_write_q4(k, v, cache: KVCacheQ4, block_table, cu_seqlens, max_seqle
 
 def flash_kv_read_q4(cache: KVCacheQ4, block_table, cu_seqlens, total: int, max_seqlen: int, starts=None, stream=None):
     """Returns (k, v) [total,Hkv,D] with positions starts[b].. of each sequence, packed by cu_seqlens. Rows that belong
-    to no sequence are not initialised."""
+    to no sequence (total above cu_seqlens[-1]) are not initialised: clear them before attention runs over them."""
     codes, scales = cache[0], cache[1]
     k = torch.empty(int(total), codes.shape[1], 2 * codes.shape[3], dtype=scales.dtype, device=codes.device)
     v = torch.empty_like(k)

@@ -359,7 +359,9 @@ FA_API fa_status_t fa_fwd_window(const void *q, const void *k, const void *v, vo
 /*
  * fa_fwd_window_varlen - fa_fwd_window over packed sequences: arguments and
  * device-side checks as fa_fwd_varlen (positions, the window and the sinks
- * count from each sequence's start), k and v [total_k,Hkv,D].
+ * count from each sequence's start), k and v [total_k,Hkv,D]. The hidden keys
+ * and values that must be finite include the up to 127 rows behind a sequence's
+ * last, of the next sequence or of none (rows past total_k are not read).
  * Errors: as fa_fwd_varlen and fa_fwd_window.
  */
 FA_API fa_status_t fa_fwd_window_varlen(const void *q, const void *k, const void *v, void *o, float *lse,
@@ -394,8 +396,9 @@ FA_API fa_status_t fa_bwd_window(const void *q, const void *k, const void *v, co
 
 /*
  * fa_bwd_window_varlen - the gradients of fa_fwd_window_varlen: arguments,
- * device-side checks and rows outside the sequences as fa_bwd_varlen, the
- * workspace of fa_bwd_window_varlen_workspace_bytes, dk and dv [total_k,Hkv,D].
+ * device-side checks and rows outside the sequences as fa_bwd_varlen, finite
+ * rows as fa_fwd_window_varlen (q, o, dout and lse too), the workspace of
+ * fa_bwd_window_varlen_workspace_bytes, dk and dv [total_k,Hkv,D].
  * Errors: as fa_bwd_varlen and fa_fwd_window.
  */
 FA_API fa_status_t fa_bwd_window_varlen(const void *q, const void *k, const void *v, const void *o, const void *dout,
@@ -461,7 +464,7 @@ FA_API fa_status_t fa_kv_write_q4(const void *k, const void *v, void *k_codes, v
  *
  *   k, v         [total,Hkv,D] outputs, dtype of the scales; rows outside
  *                every sequence, and rows that are skipped, are left as they
- *                were
+ *                were (attention over them wants finite values there)
  *   all other arguments as fa_kv_write_q4: row cu[b] + i receives position
  *   starts[b] + i of sequence b.
  * Offsets, positions and page numbers are checked on the device as by
