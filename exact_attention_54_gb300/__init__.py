@@ -10,9 +10,16 @@ and check the returned status. ``flash_attention``, ``flash_attention_varlen``
 and ``flash_decode`` additionally allocate the outputs (and the decode
 workspace) with torch. Every step of the computation runs in the library's
 kernels; there is no fallback. If libfa.so is missing, the first call raises.
+
+``stream`` (a torch stream or a raw handle) is where a call's work goes; None is
+the current stream. The calls that allocate (``flash_*``) behave with a given
+stream as under ``torch.cuda.stream(stream)``, behind the work queued so far on
+the current stream: outputs belong to that stream's order, and inputs must not
+be freed or overwritten before it is done with them.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -146,6 +153,28 @@ def _stream(stream) -> int | None:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+@contextlib.contextmanager
+def _on_stream(stream, t):
+    """Makes the caller's ``stream`` the current one (of the device of ``t``), behind the work queued so far on the one
+    that was. What a call allocates, clears and launches inside is in that stream's order, and so is what the
+    allocator does with the memory afterwards."""
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError("all tensors must be on one CUDA device")
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream must be one of {dev}, got one of {stream.device}")
+    before = torch.cuda.current_stream(dev)
+    outside = torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        # (a stream that is being captured cannot wait for one that is not)
+        if stream.cuda_stream != before.cuda_stream and (outside or not torch.cuda.is_current_stream_capturing()):
+            stream.wait_stream(before)
+        yield
 
 
 def _need_contig(*ts):
@@ -570,15 +599,21 @@ def fa_bwd_window_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlen
 
 def flash_attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None, stream=None):
     """Returns (o, lse) of causal attention with a sliding window and sinks: q [B,H,Sq,D], k, v [B,Hkv,Sk,D]."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return flash_attention_window(q, k, v, window, sinks, scale)
     o = torch.empty_like(q)
     lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-    fa_fwd_window(q, k, v, o, lse, window, sinks, scale, stream)
+    fa_fwd_window(q, k, v, o, lse, window, sinks, scale)
     return o, lse
 
 
 def flash_attention_window_bwd(q, k, v, o, lse, dout, window: int, sinks: int = 0, scale: float | None = None,
                                stream=None, workspace=None):
     """Returns (dq, dk, dv) of flash_attention_window, given its o and lse."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return flash_attention_window_bwd(q, k, v, o, lse, dout, window, sinks, scale, workspace=workspace)
     if workspace is None:
         if q.dim() != 4 or k.dim() != 4:
             raise ValueError("q must be [B,H,Sq,D] and k, v [B,Hkv,Sk,D]")
@@ -586,16 +621,20 @@ def flash_attention_window_bwd(q, k, v, o, lse, dout, window: int, sinks: int = 
         workspace = torch.empty(fa_bwd_window_workspace_bytes(B, H, Hkv, Sq, Sk, D, window, sinks) // 4,
                                 dtype=torch.float32, device=q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window, sinks, scale, stream)
+    fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window, sinks, scale)
     return dq, dk, dv
 
 
 def flash_attention_window_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, window: int, sinks: int = 0,
                                   scale: float | None = None, stream=None):
     """Returns (o [total_q,H,D], lse [H,total_q]) for packed sequences; k, v [total_k,Hkv,D]."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return flash_attention_window_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, window, sinks,
+                                                 scale)
     o = torch.empty_like(q)
     lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device)
-    fa_fwd_window_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, window, sinks, scale, stream)
+    fa_fwd_window_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, window, sinks, scale)
     return o, lse
 
 
@@ -603,6 +642,10 @@ def flash_attention_window_varlen_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_se
                                       max_seqlen_k: int, window: int, sinks: int = 0, scale: float | None = None,
                                       stream=None, workspace=None):
     """Returns (dq, dk, dv) of flash_attention_window_varlen, given its o and lse."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return flash_attention_window_varlen_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                                                     max_seqlen_k, window, sinks, scale, workspace=workspace)
     if workspace is None:
         if q.dim() != 3 or k.dim() != 3:
             raise ValueError("q must be [total_q,H,D] and k, v [total_k,Hkv,D]")
@@ -612,7 +655,7 @@ def flash_attention_window_varlen_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_se
         workspace = torch.empty(n // 4, dtype=torch.float32, device=q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fa_bwd_window_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
-                         max_seqlen_k, window, sinks, scale, stream)
+                         max_seqlen_k, window, sinks, scale)
     return dq, dk, dv
 
 
@@ -739,14 +782,20 @@ def flash_kv_write_q4(k, v, cache: KVCacheQ4, block_table, cu_seqlens, max_seqle
 def flash_kv_read_q4(cache: KVCacheQ4, block_table, cu_seqlens, total: int, max_seqlen: int, starts=None, stream=None):
     """Returns (k, v) [total,Hkv,D] with positions starts[b].. of each sequence, packed by cu_seqlens. Rows that belong
     to no sequence (total above cu_seqlens[-1]) are not initialised: clear them before attention runs over them."""
+    if stream is not None:
+        with _on_stream(stream, cache[0]):
+            return flash_kv_read_q4(cache, block_table, cu_seqlens, total, max_seqlen, starts)
     codes, scales = cache[0], cache[1]
     k = torch.empty(int(total), codes.shape[1], 2 * codes.shape[3], dtype=scales.dtype, device=codes.device)
     v = torch.empty_like(k)
-    _kv_q4("fa_kv_read_q4", k, v, cache, block_table, cu_seqlens, max_seqlen, starts, stream)
+    _kv_q4("fa_kv_read_q4", k, v, cache, block_table, cu_seqlens, max_seqlen, starts, None)
     return k, v
 
 
 def _flash_decode_gqa(q, cache, block_table, seq_lens, window, sinks, num_splits, scale, stream, workspace):
+    if stream is not None:
+        with _on_stream(stream, q):
+            return _flash_decode_gqa(q, cache, block_table, seq_lens, window, sinks, num_splits, scale, None, workspace)
     if q.dim() != 4 or cache[0].dim() != 4 or block_table.dim() != 2:
         raise ValueError("q must be [B,H,1,D], pages 4-dimensional and block_table [B,max_blocks]")
     B, H, _, D = q.shape
@@ -761,7 +810,7 @@ def _flash_decode_gqa(q, cache, block_table, seq_lens, window, sinks, num_splits
     if workspace is None:
         workspace = _decode_workspace(B, H, num_splits, D, q.device, True)
     o, lse = torch.empty_like(q), torch.empty((B, H), dtype=torch.float32, device=q.device)
-    _decode_gqa(q, cache, block_table, seq_lens, o, lse, *workspace, num_splits, window, sinks, scale, stream)
+    _decode_gqa(q, cache, block_table, seq_lens, o, lse, *workspace, num_splits, window, sinks, scale, None)
     return o, lse
 
 
