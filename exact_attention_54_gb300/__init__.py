@@ -346,10 +346,13 @@ def fa_check_device_error(stream=None):
 
 def flash_attention(q, k, v, causal: bool = False, scale: float | None = None, stream=None):
     """Returns (o, lse) for dense [B,H,S,D] CUDA tensors."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return flash_attention(q, k, v, causal, scale)
     B, H, Sq, D = q.shape
     o = torch.empty_like(q)
     lse = torch.empty(B, H, Sq, dtype=torch.float32, device=q.device)
-    fa_fwd(q, k, v, o, lse, causal, scale, stream)
+    fa_fwd(q, k, v, o, lse, causal, scale)
     return o, lse
 
 
@@ -357,11 +360,14 @@ def flash_attention_bwd(q, k, v, o, lse, dout, causal: bool = False, scale: floa
                         workspace=None):
     """Returns (dq, dk, dv) for dense [B,H,S,D] CUDA tensors, given the
     forward's o and lse."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return flash_attention_bwd(q, k, v, o, lse, dout, causal, scale, workspace=workspace)
     B, H, Sq, D = q.shape
     if workspace is None:
         workspace = torch.empty(fa_bwd_workspace_bytes(B, H, Sq, D) // 4, dtype=torch.float32, device=q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    fa_bwd(q, k, v, o, dout, lse, dq, dk, dv, workspace, causal, scale, stream)
+    fa_bwd(q, k, v, o, dout, lse, dq, dk, dv, workspace, causal, scale)
     return dq, dk, dv
 
 
@@ -369,22 +375,29 @@ def flash_attention_varlen_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k
                                max_seqlen_k: int, causal: bool = False, scale: float | None = None, stream=None,
                                workspace=None):
     """Returns (dq, dk, dv) for packed sequences, given fa_fwd_varlen's o and lse."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return flash_attention_varlen_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                                              max_seqlen_k, causal, scale, workspace=workspace)
     Tq, H, D = q.shape
     if workspace is None:
         workspace = torch.empty(fa_bwd_varlen_workspace_bytes(Tq, H, D) // 4, dtype=torch.float32, device=q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fa_bwd_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
-                  max_seqlen_k, causal, scale, stream)
+                  max_seqlen_k, causal, scale)
     return dq, dk, dv
 
 
 def flash_attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, causal: bool = False,
                            scale: float | None = None, stream=None):
     """Returns (o [total_q,H,D], lse [H,total_q]) for packed sequences."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return flash_attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, causal, scale)
     Tq, H, D = q.shape
     o = torch.empty_like(q)
     lse = torch.empty(H, Tq, dtype=torch.float32, device=q.device)
-    fa_fwd_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, causal, scale, stream)
+    fa_fwd_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, causal, scale)
     return o, lse
 
 
@@ -400,6 +413,10 @@ def flash_decode_paged(q, k_cache, v_cache, block_table, seq_lens, num_splits: i
     """Split-KV decoding over a paged cache (phase 1 + phase 2). Returns
     (o [B,H,1,D], lse [B,H]). ``workspace`` may pass preallocated (o_part,
     m_part, l_part), plus the int32 [B*H] counters when ``fused``."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return flash_decode_paged(q, k_cache, v_cache, block_table, seq_lens, num_splits, scale,
+                                      workspace=workspace, fused=fused)
     B, H = q.shape[0], q.shape[1]
     D = k_cache.shape[3]
     if workspace is None:
@@ -408,12 +425,11 @@ def flash_decode_paged(q, k_cache, v_cache, block_table, seq_lens, num_splits: i
     lse = torch.empty(B, H, dtype=torch.float32, device=q.device)
     if fused:
         fa_decode_paged_splitkv_fused(q, k_cache, v_cache, block_table, seq_lens, o, lse, *workspace, num_splits,
-                                      scale, stream)
+                                      scale)
         return o, lse
     o_part, m_part, l_part = workspace[:3]
-    fa_decode_paged_splitkv(q, k_cache, v_cache, block_table, seq_lens, o_part, m_part, l_part, num_splits, scale,
-                            stream)
-    fa_splitkv_merge(o_part, m_part, l_part, o, lse, stream)
+    fa_decode_paged_splitkv(q, k_cache, v_cache, block_table, seq_lens, o_part, m_part, l_part, num_splits, scale)
+    fa_splitkv_merge(o_part, m_part, l_part, o, lse)
     return o, lse
 
 
@@ -422,17 +438,20 @@ def flash_decode(q, k, v, num_splits: int, scale: float | None = None, stream=No
     """Split-KV decoding (phase 1 + phase 2). Returns (o [B,H,1,D], lse [B,H]).
     ``workspace`` may pass preallocated (o_part, m_part, l_part), plus the
     int32 [B*H] counters when ``fused`` (one launch instead of two)."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return flash_decode(q, k, v, num_splits, scale, workspace=workspace, fused=fused)
     B, H, Sk, D = k.shape
     if workspace is None:
         workspace = _decode_workspace(B, H, num_splits, D, k.device, fused)
     o = torch.empty(B, H, 1, D, dtype=k.dtype, device=k.device)
     lse = torch.empty(B, H, dtype=torch.float32, device=k.device)
     if fused:
-        fa_decode_splitkv_fused(q, k, v, o, lse, *workspace, num_splits, scale, stream)
+        fa_decode_splitkv_fused(q, k, v, o, lse, *workspace, num_splits, scale)
         return o, lse
     o_part, m_part, l_part = workspace[:3]
-    fa_decode_splitkv(q, k, v, o_part, m_part, l_part, num_splits, scale, stream)
-    fa_splitkv_merge(o_part, m_part, l_part, o, lse, stream)
+    fa_decode_splitkv(q, k, v, o_part, m_part, l_part, num_splits, scale)
+    fa_splitkv_merge(o_part, m_part, l_part, o, lse)
     return o, lse
 
 

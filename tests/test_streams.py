@@ -1,5 +1,6 @@
 """Calls with ``stream=``: what they allocate, clear and launch is in that stream's order, behind the current one's."""
 import contextlib
+import inspect
 
 import pytest
 import torch
@@ -10,8 +11,8 @@ from exact_attention_54_gb300 import build as fabuild
 from exact_attention_54_gb300 import inputs
 
 
-def _window_calls(dev, dtype=torch.float16, seed=0):
-    """Every allocating call of the window operators and the 4-bit cache by name, and the 16-bit inputs they read."""
+def _calls(dev, dtype=torch.float16, seed=0):
+    """Every allocating call by name, and the 16-bit inputs they read."""
     g = torch.Generator().manual_seed(seed)
     read = []
 
@@ -31,7 +32,7 @@ def _window_calls(dev, dtype=torch.float16, seed=0):
     cache = fa.kv_cache_q4(B * nb, Hkv, block, D, dtype, device=dev)
     cache = fa.KVCacheQ4(cache.k_codes + 83, r(*cache.k_scales.shape).abs(), cache.v_codes + 196,
                          r(*cache.v_scales.shape).abs())
-    q1 = r(B, H, 1, D)
+    q1, q2 = r(B, H, 1, D), r(B, Hkv, 1, D)
     return read, {
         "window": lambda **kw: fa.flash_attention_window(q, k, v, W, sinks, **kw),
         "window_bwd": lambda **kw: fa.flash_attention_window_bwd(q, k, v, q, lse, do, W, sinks, **kw),
@@ -40,11 +41,20 @@ def _window_calls(dev, dtype=torch.float16, seed=0):
                                                                                sinks, **kw),
         "read": lambda **kw: fa.flash_kv_read_q4(cache, table, cu, T, S, **kw),
         "decode": lambda **kw: fa.flash_decode_paged_window(q1, *pages, table, lens, W, sinks, **kw),
+        "dense": lambda **kw: fa.flash_attention(q, q, q, True, **kw),
+        "dense_bwd": lambda **kw: fa.flash_attention_bwd(q, q, q, q, lse, do, True, **kw),
+        "varlen": lambda **kw: fa.flash_attention_varlen(qp, qp, qp, cu, cu, S, True, **kw),
+        "varlen_bwd": lambda **kw: fa.flash_attention_varlen_bwd(qp, qp, qp, qp, lsep, dop, cu, cu, S, S, True, **kw),
+        "splitkv": lambda **kw: fa.flash_decode(q1, q, q, 9, **kw),
+        "splitkv_fused": lambda **kw: fa.flash_decode(q1, q, q, 9, fused=True, **kw),
+        "paged": lambda **kw: fa.flash_decode_paged(q2, *pages, table, lens, 9, **kw),
+        "paged_fused": lambda **kw: fa.flash_decode_paged(q2, *pages, table, lens, 9, fused=True, **kw),
         "decode_q4": lambda **kw: fa.flash_decode_paged_q4(q1, cache, table, lens, W, sinks, **kw),
     }
 
 
-NAMES = ["window", "window_bwd", "window_varlen", "window_varlen_bwd", "read", "decode", "decode_q4"]
+NAMES = ["window", "window_bwd", "window_varlen", "window_varlen_bwd", "read", "decode", "decode_q4", "dense",
+         "dense_bwd", "varlen", "varlen_bwd", "splitkv", "splitkv_fused", "paged", "paged_fused"]
 
 
 # -------------------------------------------------------------- on the CPU --
@@ -83,8 +93,12 @@ def streams(monkeypatch):
         log["launched"].append(log["now"].cuda_stream if stream is None else fa._stream(stream))
 
     monkeypatch.setattr(fa, "_launch", launched)
+    for name in ("fa_fwd", "fa_fwd_varlen", "fa_bwd", "fa_bwd_varlen", "fa_decode_splitkv", "fa_decode_splitkv_fused",
+                 "fa_splitkv_merge", "fa_decode_paged_splitkv", "fa_decode_paged_splitkv_fused"):
+        at = list(inspect.signature(getattr(fa, name)).parameters).index("stream")
+        monkeypatch.setattr(fa, name, lambda *a, _at=at: launched(None, a[_at] if len(a) > _at else None))
     with FakeTensorMode():
-        _, calls = _window_calls("cuda")
+        _, calls = _calls("cuda")
         for name in ("empty", "zeros", "empty_like"):
             def made(*a, _f=getattr(torch, name), **kw):
                 log["made"].append(log["now"].cuda_stream)
@@ -134,7 +148,7 @@ def test_given_stream_without_synchronising(name):
     sizes = (16, 1 << 12, 1 << 20, 1 << 22)
     fill = lambda n: torch.full((n,), 0x7fc00005, dtype=torch.int32, device="cuda")  # noqa: E731
     for seed in (1, 2):
-        read, calls = _window_calls("cuda", seed=seed)
+        read, calls = _calls("cuda", seed=seed)
         want = [t.clone() for t in calls[name]()]
         kept = [t.clone() for t in read]
         for t in read:
@@ -157,8 +171,10 @@ def test_given_stream_without_synchronising(name):
         torch.cuda.synchronize()
         fa.fa_check_device_error()
         for i, (a, b) in enumerate(zip(got, want)):
+            # (the LSE given is no forward's: some values pass the 16-bit type's range, in both calls alike)
+            a, b = a.double(), b.double()
+            close = (a == b) | (torch.isnan(a) & torch.isnan(b))
             if name.endswith("bwd") and i == 0:  # dq: fp32 sums in any order, then one rounding
-                room = 2 * plain_ops.half_step(a.dtype) * b.float().abs() + 2.0 ** -13 * b.float().abs().amax()
-                assert ((a.float() - b.float()).abs() <= room).all(), (seed, "dq")
-            else:
-                assert torch.equal(a, b), (seed, i)
+                h, fine = plain_ops.half_step(got[0].dtype), torch.isfinite(b)
+                close |= fine & ((a - b).abs() <= 2 * h * b.abs() + 2.0 ** -13 * b[fine].abs().amax())
+            assert bool(close.all()), (seed, i)
