@@ -331,8 +331,8 @@ def fa_bwd_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens_q, cu
 
 
 def fa_test_withhold_load(load: int, wait_limit_ns: int = 0):
-    """Test support: make CTA 0 of later prefill launches withhold one tile
-    load so that their bounded wait runs out (see include/fa.h); (0, 0) turns
+    """Test support: make the CTA with the first work item of later prefill
+    launches withhold one tile load so that their bounded wait runs out (see include/fa.h); (0, 0) turns
     it off."""
     _check("fa_test_withhold_load", load_library().fa_test_withhold_load(int(load), int(wait_limit_ns)))
 

@@ -1066,7 +1066,7 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
         const uint64_t once = ptx::l2_policy_evict_first();
         int J = 0, wi = 0;   // sub-steps and units with work so far
         int nq = 0, nl = 0;  // Q/dO and row-value loads issued
-        bool ok = true;
+        bool ok = true, has_first = false;  // has_first: this CTA took the counter's first unit
         for (int i = 0; ok; ++i) {
             const int s = i % S::kRing;
             // slot s held unit i - kRing until every role had read it
@@ -1079,6 +1079,7 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
                 int got = 0;
                 if (lane == 0) got = atomicAdd(p.work_counter, 1);
                 w = __shfl_sync(0xffffffffu, got, 0);
+                has_first |= w == 0;
                 if (w >= p.total_units) break;
                 u = bwd_unit_at<VARLEN, WIN>(p, w);
                 if constexpr (VARLEN) {
@@ -1137,7 +1138,7 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
                 int qy, qz;
                 unit_coords<VARLEN>(uq, false, q0, qy, qz);
                 if (J >= S::kStages && !(ok = wait(S::kStageFreeQ + st, ((J / S::kStages) - 1) & 1))) break;
-                if (leader && !withheld(p.withhold, static_cast<uint32_t>(J))) {
+                if (leader && !withheld(p.withhold, static_cast<uint32_t>(J), has_first)) {
                     ptx::bar_arrive_expect_tx(bar(S::kQFull + st), S::kQTileBytes);
                     for (int c = 0; c < 2; ++c)
                         ptx::tma_load_3d(qb + c * S::kQBoxBytes, &tm_q, bar(S::kQFull + st), c * 64, qy, qz);

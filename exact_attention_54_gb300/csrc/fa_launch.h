@@ -117,7 +117,7 @@ struct BwdParams {
     float scale, scale_log2;
     int *err;              // device error word
     unsigned long long timeout_ns;
-    int withhold;          // test support, 0 = off: CTA 0 never issues its Q/dO load number withhold - 1
+    int withhold;          // test support, 0 = off: the CTA with the first unit never issues its Q/dO load number withhold - 1
     int *work_counter;     // D = 128: next work unit to hand out (in the workspace, zeroed by the prep kernel)
     int total_units;       // D = 128: work units of the launch (BH * n_ktiles)
     int grid;              // D = 128: persistent CTAs (at most one per SM)
@@ -132,8 +132,13 @@ struct BwdParams {
 // Test support: a launch that withholds one load (see FwdParams::withhold)
 // leaves a wait that nothing completes, so the kernel's bounded wait runs
 // out and its abort path (drain, TMEM release, error word) runs.
+// `first`: whether this CTA has the launch's first work item (CTA 0, where
+// items are handed out in block order).
+__device__ __forceinline__ bool withheld(int withhold, uint32_t load, bool first) {
+    return withhold > 0 && first && load + 1 == static_cast<uint32_t>(withhold);
+}
 __device__ __forceinline__ bool withheld(int withhold, uint32_t load) {
-    return withhold > 0 && blockIdx.x == 0 && load + 1 == static_cast<uint32_t>(withhold);
+    return withheld(withhold, load, blockIdx.x == 0);
 }
 
 // maps: {Q, K, V, dO, dQ accumulator (fp32)}; lse dense [B*H][Sq] | packed

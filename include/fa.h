@@ -552,9 +552,10 @@ FA_API fa_status_t fa_check_device_error(void *stream);
 
 /*
  * fa_test_withhold_load - test support for the failure path of the prefill
- * kernels (fa_fwd, fa_fwd_varlen, fa_bwd, fa_bwd_varlen). With load = n > 0,
- * CTA 0 of every later launch of those kernels never issues one of its tile
- * loads (the forward's V tile n - 1, the backward's Q/dO step n - 1), so the
+ * kernels (fa_fwd, fa_fwd_varlen, fa_bwd, fa_bwd_varlen and the window forms).
+ * With load = n > 0, the CTA with the first work item of every later launch of
+ * those kernels never issues one of its tile loads (the forward's V tile
+ * n - 1, the backward's Q/dO step n - 1; an item with n of them), so the
  * wait for it cannot complete: the kernel's bounded wait runs out after
  * `wait_limit_ns`, its CTAs drain the copies they issued, release tensor
  * memory and stop, and fa_check_device_error returns FA_ERR_DEVICE_TIMEOUT.

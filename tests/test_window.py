@@ -403,3 +403,30 @@ def test_gives_up_on_a_withheld_load_and_the_next_call_is_correct(D, packed):
     fa.fa_check_device_error()
     plain_ops.assert_window_close({n: x if n == "lse" and packed else x.transpose(0, 1) if packed else x[0]
                                    for n, x in got.items()}, ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("packed", [False, True])
+def test_a_withheld_load_is_always_missed(packed):
+    """D = 128, gradients: CTAs take units from a counter, and some of them none; the load is withheld wherever the
+    first unit went."""
+    q, k, v, do = draw(1, 16, 1, 900, 900, 128, torch.bfloat16, seed=31)
+    qd, kd, vd, dd = ((x[0].transpose(0, 1).contiguous() if packed else x).cuda() for x in (q, k, v, do))
+    cu = torch.tensor([0, 900], dtype=torch.int32, device="cuda")
+    if packed:
+        o, lse = fa.flash_attention_window_varlen(qd, kd, vd, cu, cu, 900, 400, 130)
+    else:
+        o, lse = fa.flash_attention_window(qd, kd, vd, 400, 130)
+    fa.fa_check_device_error()
+    try:
+        fa.fa_test_withhold_load(2, 2_000_000)
+        for i in range(40):
+            if packed:
+                fa.flash_attention_window_varlen_bwd(qd, kd, vd, o, lse, dd, cu, cu, 900, 900, 400, 130)
+            else:
+                fa.flash_attention_window_bwd(qd, kd, vd, o, lse, dd, 400, 130)
+            with pytest.raises(fa.FAError) as e:
+                fa.fa_check_device_error()
+            assert e.value.status == -9, i
+    finally:
+        fa.fa_test_withhold_load(0, 0)
