@@ -76,7 +76,8 @@ struct FwdShape {
     static constexpr int kPFull2 = kPFull + 2;           // +t: P keys [64,128) written
     static constexpr int kODone = kPFull2 + 2;           // +t
     static constexpr int kFirstQ = kODone + 2;           // the CTA's first Q pair has landed (one phase only)
-    static constexpr int kNumBars = kFirstQ + 1;
+    static constexpr int kVCut = kFirstQ + 1;            // packed, sliding window: a V tile that ends its sequence landed
+    static constexpr int kNumBars = kVCut + 1;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
     // packed-sequence schedule (varlen): see VarlenSched
     static constexpr int kOffSched = (kOffMisc + 16 + 15) & ~15;
@@ -404,6 +405,7 @@ __device__ void fwd_producer_v(const CUtensorMap *tv, const FwdParams &p, uint32
     auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
     const bool leader = ptx::elect_one();
     uint32_t it = 0;
+    uint32_t cuts = 0, cut_done = 0;  // tiles that end a sequence: loaded, landed
     bool ok = true;
     for (int r = 0; ok; ++r) {
         const int w = work_index(r);
@@ -418,13 +420,33 @@ __device__ void fwd_producer_v(const CUtensorMap *tv, const FwdParams &p, uint32
                 !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kVEmpty + stage), ((it / S::kVStages) - 1) & 1, abort_flag,
                                      p.timeout_ns))))
                 break;
+            const uint32_t dst = sbase + S::kOffV + stage * S::kTileBytes;
+            if constexpr (VARLEN && WIN) {
+                // The tile that ends a sequence holds rows of the next one (or
+                // of none) behind it. Their weights are zero, but a NaN or an
+                // infinity there would make 0 x NaN: the rows are zeroed before
+                // the tile is handed on.
+                const int rows = wk.Lk - kv_tile<WIN>(wk, j) * kBlockN;
+                if (rows < kBlockN && wk.seq_k0 + wk.Lk < p.total_k && !withheld(p.withhold, it)) {
+                    if (leader) {
+                        ptx::bar_arrive_expect_tx(bar(S::kVCut), S::kTileBytes);
+                        load_kv_tile<D, VARLEN, WIN>(tv, dst, bar(S::kVCut), wk, j, p);
+                    }
+                    if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kVCut), cuts++ & 1, abort_flag, p.timeout_ns)))) break;
+                    ++cut_done;
+                    ptx::zero_rows(dst, S::kColBlocks, kBlockN, rows);
+                    __syncwarp();
+                    if (leader) ptx::bar_arrive(bar(S::kVFull + stage));
+                    continue;
+                }
+            }
             if (leader && !withheld(p.withhold, it)) {
                 ptx::bar_arrive_expect_tx(bar(S::kVFull + stage), S::kTileBytes);
-                load_kv_tile<D, VARLEN, WIN>(tv, sbase + S::kOffV + stage * S::kTileBytes, bar(S::kVFull + stage), wk,
-                                             j, p);
+                load_kv_tile<D, VARLEN, WIN>(tv, dst, bar(S::kVFull + stage), wk, j, p);
             }
         }
     }
+    if (cuts > cut_done) ptx::bar_wait(bar(S::kVCut), (cuts - 1) & 1, nullptr, p.timeout_ns);
     for (uint32_t s = 0; s < S::kVStages && s < it; ++s) {
         const uint32_t last = (it - 1) - ((it - 1 - s) % S::kVStages);
         ptx::bar_wait(bar(S::kVFull + s), (last / S::kVStages) & 1, nullptr, p.timeout_ns);

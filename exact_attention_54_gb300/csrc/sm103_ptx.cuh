@@ -217,6 +217,18 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Zeroes the rows from `row` on of a tile of `boxes` boxes of `rows` rows of
+// 128 bytes (any swizzle stays within a row), for the tensor core to read:
+// after it, a __syncwarp orders the whole warp's writes for one lane's arrival.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int boxes, int rows, int row) {
+    const uint32_t lane = threadIdx.x % 32;
+    for (int c = 0; c < boxes; ++c)
+        for (uint32_t at = tile + c * rows * 128 + row * 128 + lane * 16, end = tile + (c + 1) * rows * 128; at < end;
+             at += 512)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
+    fence_proxy_async_smem();
+}
+
 // ----------------------------------------------------------------- tcgen05 --
 
 // Allocate `ncols` TMEM columns (power of two, 32..512); the whole warp must

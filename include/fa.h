@@ -359,9 +359,9 @@ FA_API fa_status_t fa_fwd_window(const void *q, const void *k, const void *v, vo
 /*
  * fa_fwd_window_varlen - fa_fwd_window over packed sequences: arguments and
  * device-side checks as fa_fwd_varlen (positions, the window and the sinks
- * count from each sequence's start), k and v [total_k,Hkv,D]. The hidden keys
- * and values that must be finite include the up to 127 rows behind a sequence's
- * last, of the next sequence or of none (rows past total_k are not read).
+ * count from each sequence's start), k and v [total_k,Hkv,D]. Hidden keys and
+ * values of a sequence itself must be finite, as there; rows that are not its
+ * own may hold anything, NaNs included.
  * Errors: as fa_fwd_varlen and fa_fwd_window.
  */
 FA_API fa_status_t fa_fwd_window_varlen(const void *q, const void *k, const void *v, void *o, float *lse,
@@ -396,9 +396,10 @@ FA_API fa_status_t fa_bwd_window(const void *q, const void *k, const void *v, co
 
 /*
  * fa_bwd_window_varlen - the gradients of fa_fwd_window_varlen: arguments,
- * device-side checks and rows outside the sequences as fa_bwd_varlen, finite
- * rows as fa_fwd_window_varlen (q, o, dout and lse too), the workspace of
- * fa_bwd_window_varlen_workspace_bytes, dk and dv [total_k,Hkv,D].
+ * device-side checks and rows outside the sequences as fa_bwd_varlen, the
+ * workspace of fa_bwd_window_varlen_workspace_bytes, dk and dv [total_k,Hkv,D].
+ * The up to 127 rows behind a sequence's last, of another or of none, must be
+ * finite (of q, k, v, o, dout and lse).
  * Errors: as fa_bwd_varlen and fa_fwd_window.
  */
 FA_API fa_status_t fa_bwd_window_varlen(const void *q, const void *k, const void *v, const void *o, const void *dout,
