@@ -91,7 +91,8 @@ struct Shape {
     static constexpr int kStageFree = 14;   // +s: the bulk reduction has read stage s (1 thread)
     static constexpr int kLFull = 16;       // the step's LSE and D values are in shared memory (bulk copy)
     static constexpr int kTeardown = 17;
-    static constexpr int kNumBars = 18;
+    static constexpr int kCut = 18;         // packed, sliding window: K and V that end their sequence landed (TMA)
+    static constexpr int kNumBars = 19;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
     static constexpr int kOffRows = 256;                     // float lse2[128], delta[128]
     static constexpr int kSmallBytes = kOffRows + 2 * 128 * 4;
@@ -440,6 +441,20 @@ __device__ __forceinline__ void load_rows_packed(const BwdParams &p, const BwdUn
     if (leader) ptx::bar_arrive(bar);
 }
 
+// Packed, sliding window: rows of its own sequence in a tile of `block` rows
+// from row r0 on, where it ends that sequence inside the tensor (length `len`,
+// token offset t0, of `total` tokens); else `block`. The rows behind are another
+// sequence's, or of none, and may hold anything; P and dS there are zero, but
+// 0 x NaN is not. So they are zeroed: in K and V by the loader, in Q, dO, S^T and
+// dP^T by the key-row warps before they form P and dS, and in dQ_t before it is
+// added to rows that are not this sequence's. The steps of other tiles do
+// nothing for it (testing for it in their masks instead cost them 3 %).
+template <bool VARLEN, bool WIN>
+__device__ __forceinline__ int own_rows(int block, int r0, int len, int t0, int total) {
+    if constexpr (VARLEN && WIN) return len - r0 < block && t0 + len < total ? len - r0 : block;
+    return block;
+}
+
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr)
@@ -535,10 +550,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0 && n > 0) {
         // ---- TMA producer ----
         const bool leader = ptx::elect_one();
+        const int k_rows = own_rows<VARLEN, WIN>(kBlock, k0, u.Lk, u.tk0, p.total_k);
+        const int kv_bar = k_rows < kBlock ? S::kCut : S::kKVFull;
         if (leader) {
-            ptx::bar_arrive_expect_tx(bar(S::kKVFull), 2 * S::kTileBytes);
-            load_rows(&tm_k, u, sbase + S::kOffK, bar(S::kKVFull), k0, true);
-            load_rows(&tm_v, u, sbase + S::kOffV, bar(S::kKVFull), k0, true);
+            ptx::bar_arrive_expect_tx(bar(kv_bar), 2 * S::kTileBytes);
+            load_rows(&tm_k, u, sbase + S::kOffK, bar(kv_bar), k0, true);
+            load_rows(&tm_v, u, sbase + S::kOffV, bar(kv_bar), k0, true);
         }
         int nq = 0, nl = 0;  // Q/dO steps and row-value steps loaded
         for (int it = 0; it < n; ++it) {
@@ -554,6 +571,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load_rows(&tm_do, uq, sbase + S::kOffDO + s * S::kTileBytes, bar(S::kQFull + s), q0, false);
             }
             ++nq;
+            if (it == 0 && k_rows < kBlock) {  // handed on without what is behind the sequence (see own_rows)
+                if (!wait(S::kCut, 0)) break;
+                ptx::zero_rows(sbase + S::kOffK, D / 64, kBlock, k_rows, kBlock);
+                ptx::zero_rows(sbase + S::kOffV, D / 64, kBlock, k_rows, kBlock);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (leader) ptx::bar_arrive(bar(S::kKVFull));
+            }
             // the single row-value buffer is free once every compute warp has
             // finished the previous step's P^T and dS^T (its four chunks)
             if (it >= 1) {
@@ -573,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++nl;
         }
         // never leave with copies in flight
-        ptx::bar_wait(bar(S::kKVFull), 0, nullptr, p.timeout_ns);
+        ptx::bar_wait(bar(kv_bar), 0, nullptr, p.timeout_ns);
         if (nl > 0) ptx::bar_wait(bar(S::kLFull), (nl - 1) & 1, nullptr, p.timeout_ns);
         for (int s = 0; s < 2 && s < nq; ++s) {
             const int last = (nq - 1) - ((nq - 1 - s) % 2);
@@ -680,6 +705,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (it > 0 && !(ok = wait(S::kDSFree, (it - 1) & 1))) break;
             if (!(ok = wait(S::kSFull, it & 1))) break;
             ptx::tc_fence_after();
+            if (VARLEN && WIN && next_block == 0) {  // the last block: see own_rows
+                const int own = own_rows<VARLEN, WIN>(kBlock, q0, u.Lq, u.tq0, p.total_q);
+                if (own < 64 * h + 64) {
+                    if (!(ok = wait(S::kQFull + s, (it >> 1) & 1))) break;
+                    const int from = max(own, 64 * h);
+                    ptx::zero_rows(sbase + S::kOffQ + s * S::kTileBytes, D / 64, kBlock, from, 64 * h + 64, wq, 4);
+                    ptx::zero_rows(sbase + S::kOffDO + s * S::kTileBytes, D / 64, kBlock, from, 64 * h + 64, wq, 4);
+#pragma unroll 1
+                    for (int c = 2 * h; c < 2 * h + 2; ++c)
+                        ptx::tmem_zero_from(tmem + lane_base + S::kTmemS + 32 * c,
+                                            tmem + lane_base + S::kTmemDP + 32 * c, own - 32 * c);
+                }
+            }
 #pragma unroll 1
             for (int cl = 0; cl < 2; ++cl) {
                 const int c = 2 * h + cl;  // 32-query chunk of the tile
@@ -740,6 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) ptx::bar_arrive(bar(S::kPChunk + c));
             }
 
+
             // dQ_t, this half's columns of query row r
             if (!(ok = wait(S::kDQFull, it & 1))) break;
             ptx::tc_fence_after();
@@ -765,6 +804,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int m = 0; m < 8; ++m)
                     st_shared_v4(box + row_off + ((m ^ (r & 7)) * 16), v[c][4 * m], v[c][4 * m + 1], v[c][4 * m + 2],
                                  v[c][4 * m + 3]);
+                if (VARLEN && WIN && next_block == 0) {  // the last block: rows that are another's add nothing
+                    const int own = own_rows<VARLEN, WIN>(kBlock, q0, u.Lq, u.tq0, p.total_q);
+                    __syncwarp();
+                    if (own < 32 * wq + 32) ptx::zero_rows(box, 1, kBlock, max(own, 32 * wq), 32 * wq + 32);
+                }
             }
             ptx::fence_proxy_async_smem();  // the bulk reduction reads the stage next
             __syncwarp();
@@ -942,9 +986,10 @@ struct ShapeQ64 {
     static constexpr int kDPFull = 44;     // +b: dP^T of the buffer written (MMA commit)
     static constexpr int kDOFull = 46;     // +stage: dO_j landed (TMA)
     static constexpr int kStageFreeQ = 50; // +stage: the boxes over Q_j read (1 thread)
-    static constexpr int kNumBars = 54;
+    static constexpr int kCut = 54;        // packed, sliding window: K and V that end their sequence landed (TMA)
+    static constexpr int kNumBars = 55;
     static constexpr int kOffMisc = kNumBars * 8;
-    static constexpr int kOffRows = 448;   // + b * 512: float lse2[64], delta[64]
+    static constexpr int kOffRows = 464;   // + b * 512: float lse2[64], delta[64]
     // + slot * 32: int {live, kt, z, hh, tq0, tk0, Lq, Lk} of a published unit
     static constexpr int kOffUnits = kOffRows + 2 * 2 * kQ * 4;
     static constexpr int kSmallBytes = kOffUnits + kRing * 32;
@@ -1066,6 +1111,8 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
         const uint64_t once = ptx::l2_policy_evict_first();
         int J = 0, wi = 0;   // sub-steps and units with work so far
         int nq = 0, nl = 0;  // Q/dO and row-value loads issued
+        uint32_t cuts = 0;   // units whose K and V end their sequence
+        bool kv_cut = false;  // K and V on kCut not yet handed on
         bool ok = true, has_first = false;  // has_first: this CTA took the counter's first unit
         for (int i = 0; ok; ++i) {
             const int s = i % S::kRing;
@@ -1115,15 +1162,16 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
             if (n == 0) continue;  // no query sees these keys: zero dK and dV only
             // K and V of the unit once the previous unit's products are done with theirs
             if (wi >= 1 && !(ok = wait(S::kKVEmpty, (wi - 1) & 1))) break;
+            const int k_rows = own_rows<VARLEN, WIN>(kBlock, k0, u.Lk, u.tk0, p.total_k);
+            kv_cut = k_rows < kBlock;
             if (leader) {
-                ptx::bar_arrive_expect_tx(bar(S::kKVFull), 2 * S::kKTileBytes);
+                const uint32_t kv_bar = bar(kv_cut ? S::kCut : S::kKVFull);
+                ptx::bar_arrive_expect_tx(kv_bar, 2 * S::kKTileBytes);
                 int ky, kz;
                 unit_coords<VARLEN>(u, true, k0, ky, kz);
                 for (int c = 0; c < 2; ++c) {
-                    ptx::tma_load_3d_hint(sbase + S::kOffK + c * S::kKBoxBytes, &tm_k, bar(S::kKVFull), c * 64, ky,
-                                          kz, once);
-                    ptx::tma_load_3d_hint(sbase + S::kOffV + c * S::kKBoxBytes, &tm_v, bar(S::kKVFull), c * 64, ky,
-                                          kz, once);
+                    ptx::tma_load_3d_hint(sbase + S::kOffK + c * S::kKBoxBytes, &tm_k, kv_bar, c * 64, ky, kz, once);
+                    ptx::tma_load_3d_hint(sbase + S::kOffV + c * S::kKBoxBytes, &tm_v, kv_bar, c * 64, ky, kz, once);
                 }
             }
             ++wi;
@@ -1151,6 +1199,16 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
                                          c * 64, qy, qz);
                 }
                 ++nq;
+                if (kv_cut) {  // handed on without what is behind the sequence (see own_rows)
+                    if (!(ok = wait(S::kCut, cuts & 1))) break;
+                    ++cuts;
+                    kv_cut = false;
+                    ptx::zero_rows(sbase + S::kOffK, 2, kBlock, k_rows, kBlock);
+                    ptx::zero_rows(sbase + S::kOffV, 2, kBlock, k_rows, kBlock);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (leader) ptx::bar_arrive(bar(S::kKVFull));
+                }
                 // row buffer b is free once the key-row warps are done with sub-step J-2
                 if (J >= 2 && !(ok = wait(S::kPFull + b, ((J - 2) >> 1) & 1))) break;
                 if constexpr (VARLEN) {
@@ -1168,7 +1226,8 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
             }
         }
         // never leave with copies in flight
-        if (wi > 0) ptx::bar_wait(bar(S::kKVFull), (wi - 1) & 1, nullptr, p.timeout_ns);
+        if (kv_cut) ptx::bar_wait(bar(S::kCut), cuts & 1, nullptr, p.timeout_ns);
+        else if (wi > 0) ptx::bar_wait(bar(S::kKVFull), (wi - 1) & 1, nullptr, p.timeout_ns);
         for (int st = 0; st < S::kStages && st < nq; ++st) {
             const int last = (nq - 1) - ((nq - 1 - st) % S::kStages);
             ptx::bar_wait(bar(S::kQFull + st), (last / S::kStages) & 1, nullptr, p.timeout_ns);
@@ -1332,6 +1391,21 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
                 if (!(ok = wait(S::kSFull + b, (J >> 1) & 1))) break;
             }
             ptx::tc_fence_after();
+            if (VARLEN && WIN && next_block == 0) {  // the last block: see own_rows
+                const int own = own_rows<VARLEN, WIN>(S::kQ, qc - 32 * h, u.Lq, u.tq0, p.total_q);
+                if (own < S::kQ) {
+                    // Q_J, dO_J have been read by S^T and dP^T, and are this
+                    // unit's still: dV waits for P^T and dK for dS^T of every warp
+                    const int st = J % S::kStages;
+                    if (!(ok = wait(S::kQFull + st, (J / S::kStages) & 1))) break;
+                    if (!(ok = wait(S::kDOFull + st, (J / S::kStages) & 1))) break;
+                    if (!(ok = wait(S::kDPFull + b, (J >> 1) & 1))) break;
+                    ptx::tc_fence_after();
+                    ptx::zero_rows(sbase + S::kOffQ + st * S::kStageBytes, 4, S::kQ, own, S::kQ, warp - 4, 8);
+                    ptx::fence_proxy_async_smem();
+                    ptx::tmem_zero_from(tb + 32 * h, tb + 64 + 32 * h, own - 32 * h);
+                }
+            }
             uint32_t sv[32], dpv[32];
             ptx::tmem_ld32(tb + 32 * h, sv);
             ptx::tmem_ld_wait();
@@ -1500,8 +1574,11 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
         for (int iu = 0; ok; ++iu) {
           UnitView uv;
           if (!(ok = read_unit(iu, uv)) || !uv.live) break;
+          int next_block = VARLEN && WIN && uv.n > 0 ? uv.first % uv.blocks : 0;
           for (int j = 0; j < uv.n; ++j, ++J) {
             const int b = J & 1, st = J % S::kStages;
+            const int block = next_block;
+            if (VARLEN && WIN && ++next_block == uv.blocks) next_block = 0;
             if (!(ok = wait(S::kDQFull + b, (J >> 1) & 1))) break;
             ptx::tc_fence_after();
             uint32_t v0[32], v1[32];
@@ -1523,6 +1600,11 @@ __global__ void __launch_bounds__(kThreadsQ64, 1)
                 asm volatile("st.shared.b32 [%0], %1;" ::"r"(col + i * 128 + chunk * 16),
                              "r"(i < 32 ? v0[i] : v1[i - 32])
                              : "memory");
+            }
+            if (VARLEN && WIN && next_block == 0) {  // the last block: rows that are another's add nothing
+                const int own = own_rows<VARLEN, WIN>(S::kQ, uv.qs0 + block * S::kQ, uv.u.Lq, uv.u.tq0, p.total_q);
+                __syncwarp();
+                ptx::zero_rows(sbase + S::kOffQ + st * S::kStageBytes + wq * S::kDQBoxBytes, 1, S::kQ, own, S::kQ);
             }
             ptx::fence_proxy_async_smem();  // the bulk reduction reads the tile next
             __syncwarp();

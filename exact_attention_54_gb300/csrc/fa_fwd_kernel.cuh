@@ -434,7 +434,8 @@ __device__ void fwd_producer_v(const CUtensorMap *tv, const FwdParams &p, uint32
                     }
                     if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kVCut), cuts++ & 1, abort_flag, p.timeout_ns)))) break;
                     ++cut_done;
-                    ptx::zero_rows(dst, S::kColBlocks, kBlockN, rows);
+                    ptx::zero_rows(dst, S::kColBlocks, kBlockN, rows, kBlockN);
+                    ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (leader) ptx::bar_arrive(bar(S::kVFull + stage));
                     continue;

@@ -217,16 +217,19 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Zeroes the rows from `row` on of a tile of `boxes` boxes of `rows` rows of
-// 128 bytes (any swizzle stays within a row), for the tensor core to read:
-// after it, a __syncwarp orders the whole warp's writes for one lane's arrival.
-__device__ __forceinline__ void zero_rows(uint32_t tile, int boxes, int rows, int row) {
+// Zeroes rows [row, end) of a tile of `boxes` boxes of `rows` rows of 128
+// bytes (any swizzle stays within a row). `parts` warps share the work; this one
+// is `part`. Where the tensor core or a bulk copy reads them next,
+// fence_proxy_async_smem comes after, and a __syncwarp before one lane's arrival.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int boxes, int rows, int row, int end, int part = 0,
+                                          int parts = 1) {
     const uint32_t lane = threadIdx.x % 32;
-    for (int c = 0; c < boxes; ++c)
-        for (uint32_t at = tile + c * rows * 128 + row * 128 + lane * 16, end = tile + (c + 1) * rows * 128; at < end;
-             at += 512)
+    for (int c = 0; c < boxes; ++c) {
+        const uint32_t stop = tile + (c * rows + end) * 128;
+#pragma unroll 4
+        for (uint32_t at = tile + (c * rows + row) * 128 + (part * 32 + lane) * 16; at < stop; at += parts * 512)
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
-    fence_proxy_async_smem();
+    }
 }
 
 // ----------------------------------------------------------------- tcgen05 --
@@ -358,6 +361,25 @@ __device__ __forceinline__ void reg_fence(uint32_t (&r)[32]) {
                    "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
                    "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
                    "+r"(r[30]), "+r"(r[31]));
+}
+
+// Zeroes columns [from, 32) of the 32 at `a` and of the 32 at `b`, the warp's
+// 32 lanes (x1 stores, a column at a time, cost three times as much).
+__device__ __forceinline__ void tmem_zero_from(uint32_t a, uint32_t b, int from) {
+    uint32_t x[32], y[32];
+    tmem_ld32(a, x);
+    tmem_ld32(b, y);
+    tmem_ld_wait();
+    reg_fence(x);
+    reg_fence(y);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        x[i] = i < from ? x[i] : 0u;
+        y[i] = i < from ? y[i] : 0u;
+    }
+    tmem_st32(a, x);
+    tmem_st32(b, y);
+    tmem_st_wait();
 }
 
 // ------------------------------------------------------------- descriptors --

@@ -398,8 +398,8 @@ FA_API fa_status_t fa_bwd_window(const void *q, const void *k, const void *v, co
  * fa_bwd_window_varlen - the gradients of fa_fwd_window_varlen: arguments,
  * device-side checks and rows outside the sequences as fa_bwd_varlen, the
  * workspace of fa_bwd_window_varlen_workspace_bytes, dk and dv [total_k,Hkv,D].
- * The up to 127 rows behind a sequence's last, of another or of none, must be
- * finite (of q, k, v, o, dout and lse).
+ * As in the forward, rows that are not a sequence's own (of q, k, v, o, dout and
+ * lse) may hold anything.
  * Errors: as fa_bwd_varlen and fa_fwd_window.
  */
 FA_API fa_status_t fa_bwd_window_varlen(const void *q, const void *k, const void *v, const void *o, const void *dout,

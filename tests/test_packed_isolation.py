@@ -57,3 +57,66 @@ def test_forward_keeps_to_its_sequence(lq, lk, H, Hkv, D, dtype, window, sinks, 
     fa.fa_check_device_error()
     rows = _whole(cq, every)
     assert torch.equal(o[rows], o2[rows]) and torch.equal(lse[:, rows], lse2[:, rows])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+@pytest.mark.parametrize("every", [0, 1])
+@pytest.mark.parametrize("lq,lk,H,Hkv,D,dtype,window,sinks,pad", CASES)
+def test_gradients_keep_to_their_sequence(lq, lk, H, Hkv, D, dtype, window, sinks, pad, every, what):
+    lk = lk or lq
+    cq, ck, q, k, v, do = _make(lq, lk, H, Hkv, D, dtype, pad)
+    c, d = cq.cuda(), ck.cuda()
+
+    def run(q, k, v, do):
+        q, k, v, do = (t.cuda() for t in (q, k, v, do))
+        o, lse = fa.flash_attention_window_varlen(q, k, v, c, d, max(lq), window, sinks)
+        if pad:  # rows of no sequence are left as they were made
+            o[int(cq[-1]):], lse[:, int(cq[-1]):] = what, what
+        return fa.flash_attention_window_varlen_bwd(q, k, v, o, lse, do, c, d, max(lq), max(lk), window, sinks)
+
+    dq, dk, dv = run(q, k, v, do)
+    dq2, dk2, dv2 = run(*(_spoiled(u, every, what, x) for u, x in ((cq, q), (ck, k), (ck, v), (cq, do))))
+    fa.fa_check_device_error()
+    rows, keys = _whole(cq, every), _whole(ck, every)
+    assert torch.equal(dk[keys], dk2[keys]) and torch.equal(dv[keys], dv2[keys])
+    # dq: fp32 sums in any order (under 2^-13 of the largest: some 20 addends, each off by 2^-24), one rounding each
+    a, b = dq[rows].double(), dq2[rows].double()
+    if a.numel():
+        h = torch.finfo(dtype).eps / 2
+        assert bool(((a - b).abs() <= 2 * h * a.abs() * (1 + h) + 2.0 ** -13 * a.abs().amax()).all())
+    if pad:
+        assert bool((dq2[int(cq[-1]):] == 0).all()) and bool((dq[int(cq[-1]):] == 0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_gives_up_on_a_withheld_load_that_ends_a_sequence(D):
+    """The second V tile, and the second step of queries, of a sequence that ends inside them: the call ends with an
+    error, and the next one is correct."""
+    n, tail = (200, 50) if D == 64 else (100, 50)
+    lens = {"fwd": [200, tail], "bwd": [n, tail]}
+    for which in ("fwd", "bwd"):
+        cq, _, q, k, v, do = _make(lens[which], lens[which], 1, 1, D, torch.bfloat16, 30)
+        c = cq.cuda()
+        q, k, v, do = (t.cuda() for t in (q, k, v, do))
+        mx = max(lens[which])
+        fwd = lambda: fa.flash_attention_window_varlen(q, k, v, c, c, mx, 1000, 0)  # noqa: E731
+        bwd = lambda o, lse: fa.flash_attention_window_varlen_bwd(q, k, v, o, lse, do, c, c, mx, mx, 1000, 0)  # noqa: E731
+        good = fwd()
+        want = bwd(*good) if which == "bwd" else good
+        fa.fa_check_device_error()
+        try:
+            fa.fa_test_withhold_load(2, 20_000_000)
+            bwd(*good) if which == "bwd" else fwd()
+            with pytest.raises(fa.FAError) as e:
+                fa.fa_check_device_error()
+            assert e.value.status == -9
+        finally:
+            fa.fa_test_withhold_load(0, 0)
+        got = bwd(*good) if which == "bwd" else fwd()
+        fa.fa_check_device_error()
+        T = int(cq[-1])
+        for a, b in list(zip(got, want))[1 if which == "bwd" else 0:]:  # (dq's sums come in any order)
+            a, b = (a[:, :T], b[:, :T]) if a.dim() == 2 else (a[:T], b[:T])
+            assert torch.equal(a, b)
