@@ -738,7 +738,7 @@ def fa_kv_read_q4(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_se
 
 
 def fa_decode_splits(B: int, H: int, Hkv: int, max_keys: int) -> int:
-    """A num_splits that fills the current GPU (see include/fa.h)."""
+    """A num_splits that is fast on the current GPU (see include/fa.h)."""
     call = _entry.get("fa_decode_splits")
     if call is None:
         call = _entry["fa_decode_splits"] = load_library().fa_decode_splits

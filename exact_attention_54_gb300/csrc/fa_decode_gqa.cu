@@ -16,7 +16,9 @@
 // fp32. Bound by HBM: K and
 // V of the visible keys are read once for a group of up to 16 query heads.
 #include <climits>
+#include <cmath>
 
+#include "fa.h"
 #include "fa_decode_gqa.cuh"
 
 namespace fa {
@@ -299,7 +301,16 @@ int decode_gqa_splits(int sms, int B, int H, int Hkv, int max_keys) {
     const long long plain = wave / units > 1 ? wave / units : 1, keys = (static_cast<long long>(max_keys) + 255) / 256;
     const long long balanced = 8LL * sms / units + 3;
     const long long s = gqa_balanced(units, max_keys, wave) ? balanced : (plain < keys ? plain : keys);
-    return static_cast<int>(s < 64 ? s : 64);
+    // Parts are read side by side and joined by one CTA (0.14, 0.25 and 0.54 us
+    // each for 1, 8 and 16 heads), so few units do best with a number that grows
+    // as the square root of their keys: 64 up to 131072 of them. (One key head, 8
+    // query heads, D = 128, us over 16-bit pages / the 4-bit cache with 32, 64, 96,
+    // 152, 192, 256 and 456 parts: 16384 keys 29/29, 33/35, 39/41, 52/53, 64/64,
+    // 78/78, 133/133; 131072: 90/64, 64/55, 61/59, 68/67, 76/78, 89/89, 141/139; 2^20:
+    // 620/297, 330/174, 240/141, 186/125, 176/133, 173/137, 208/176.)
+    const long long most = max_keys > 131072 ? static_cast<long long>(64 * std::sqrt(max_keys / 131072.0)) : 64;
+    const long long cap = most < FA_MAX_SPLITS ? most : FA_MAX_SPLITS;
+    return static_cast<int>(s < cap ? s : cap);
 }
 
 unsigned decode_gqa_grid(GqaDecodeParams &p, int sms, int ctas_per_sm, int heads_per_unit) {

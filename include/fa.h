@@ -480,10 +480,11 @@ FA_API fa_status_t fa_kv_read_q4(void *k, void *v, const void *k_codes, const vo
 
 /*
  * fa_decode_splits - a number of partitions for fa_decode_paged_window and
- * fa_decode_paged_q4 that fills the current GPU: for a batch of B sequences,
- * Hkv key heads and at most max_keys visible keys a sequence (window + sinks,
- * or the longest sequence). At least 1, at most FA_MAX_SPLITS; 1 where the
- * arguments are not positive.
+ * fa_decode_paged_q4 that is fast on the current GPU: it fills the GPU, but for
+ * few heads of sequences too short to repay the joining of so many parts. For a
+ * batch of B sequences, Hkv key heads and at most max_keys visible keys a
+ * sequence (window + sinks, or the longest sequence). At least 1, at most
+ * FA_MAX_SPLITS; 1 where the arguments are not positive.
  */
 FA_API int fa_decode_splits(int B, int H, int Hkv, int max_keys);
 
