@@ -861,7 +861,9 @@ static fa_status_t kv_q4(bool write, const void *k, const void *v, const void *k
     if ((!k || !v) && total != 0) return FA_ERR_NULL;
     if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_DTYPE;
     if (D != 64 && D != 128) return FA_ERR_HEADDIM;
-    if (num_seqs < 1 || total < 0 || total > kMaxLen || max_seqlen < 1 || max_seqlen > kMaxLen || Hkv < 1)
+    // (no tokens at all: the longest sequence may have none)
+    if (num_seqs < 1 || total < 0 || total > kMaxLen || max_seqlen < (total > 0 ? 1 : 0) || max_seqlen > kMaxLen ||
+        Hkv < 1)
         return FA_ERR_SHAPE;
     int log2_bs = 0;
     if (!pages_ok(Hkv, num_blocks, block_size, max_blocks_per_seq, log2_bs)) return FA_ERR_SHAPE;

@@ -448,7 +448,8 @@ FA_API fa_status_t fa_bwd_window_varlen(const void *q, const void *k, const void
  * start is negative, is skipped and the next fa_check_device_error returns
  * FA_ERR_DEVICE_SEQLENS; a position past max_blocks_per_seq * block_size or a
  * page number outside [0, num_blocks) is skipped and reported as
- * FA_ERR_DEVICE_INDEX. total = 0 is allowed and does nothing.
+ * FA_ERR_DEVICE_INDEX. total = 0 is allowed (max_seqlen may then be 0) and
+ * does nothing.
  * Errors: FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_HEADDIM, FA_ERR_DTYPE,
  * FA_ERR_ALIGN, FA_ERR_CUDA.
  */

@@ -283,3 +283,24 @@ def test_no_tokens():
     fa.flash_kv_write_q4(k, k, c, bt, cu, 1)
     fa.fa_check_device_error()
     assert int(c.k_codes.sum()) == 0
+
+
+@pytest.mark.parametrize("name", ["fa_kv_write_q4", "fa_kv_read_q4"])
+def test_a_longest_sequence_of_no_tokens(name, lib):
+    """max_seqlen is at least every number of new tokens: 0 is, where there are none (and only there)."""
+    def call(total, mx, k=A, v=A):
+        return getattr(lib, name)(k, v, A, A, A, A, A, A, None, 2, total, mx, 2, 64, 4, 16, 3, 1, None)
+    assert call(0, 0) == 0 and call(0, 0, None, None) == 0
+    assert call(0, -1) == SHAPE and call(1, 0) == SHAPE and call(-1, 0) == SHAPE
+
+
+@pytest.mark.gpu
+def test_a_step_without_new_tokens():
+    """What a serving loop passes where no sequence has any: nothing is written, nothing comes back."""
+    c = fa.kv_cache_q4(2, 2, 16, 64, torch.float16)
+    cu, bt = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    k = torch.empty(0, 2, 64, dtype=torch.float16, device="cuda")
+    fa.flash_kv_write_q4(k, k, c, bt, cu, 0)
+    kr, vr = fa.flash_kv_read_q4(c, bt, cu, 0, 0)
+    fa.fa_check_device_error()
+    assert kr.shape == vr.shape == (0, 2, 64) and not any(int((t != 0).sum()) for t in c)
