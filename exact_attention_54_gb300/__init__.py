@@ -475,6 +475,12 @@ def fa_decode_noalloc(q, k, v, o, lse, num_splits: int, scale: float | None = No
 
 # ------------------------------------- shared key heads, windows, 4-bit cache --
 
+def _int32(n) -> int:
+    """A whole number as a C int, the nearest one where it does not fit (ctypes would drop its upper bits)."""
+    n = int(n)
+    return n if -0x80000000 <= n <= 0x7fffffff else 0x7fffffff if n > 0 else -0x80000000
+
+
 def _expect(name: str, t, shape, dtype):
     """Refuse a tensor that is not a contiguous one of this shape and dtype (None in ``shape``: any size)."""
     if t.dtype == dtype and t.shape == shape and t.is_contiguous():
@@ -536,7 +542,7 @@ def fa_fwd_window(q, k, v, o, lse, window: int, sinks: int = 0, scale: float | N
     _expect("lse", lse, (B, H, Sq), torch.float32)
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     ts = (q, k, v, o, lse)
-    _launch("fa_fwd_window", stream, ts, B, H, Hkv, Sq, Sk, D, int(window), int(sinks), float(scale), code)
+    _launch("fa_fwd_window", stream, ts, B, H, Hkv, Sq, Sk, D, _int32(window), _int32(sinks), float(scale), code)
 
 
 def fa_fwd_window_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, window: int, sinks: int = 0,
@@ -555,19 +561,19 @@ def fa_fwd_window_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen
     _expect("cu_seqlens_k", cu_seqlens_k, (n + 1,), torch.int32)
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     ts = (q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k)
-    _launch("fa_fwd_window_varlen", stream, ts, n, Tq, Tk, int(max_seqlen_q), H, Hkv, D, int(window), int(sinks),
-            float(scale), code)
+    _launch("fa_fwd_window_varlen", stream, ts, n, Tq, Tk, _int32(max_seqlen_q), H, Hkv, D, _int32(window),
+            _int32(sinks), float(scale), code)
 
 
 def fa_bwd_window_workspace_bytes(B: int, H: int, Hkv: int, Sq: int, Sk: int, D: int, window: int,
                                   sinks: int = 0) -> int:
-    return int(load_library().fa_bwd_window_workspace_bytes(B, H, Hkv, Sq, Sk, D, window, sinks))
+    return int(load_library().fa_bwd_window_workspace_bytes(*map(_int32, (B, H, Hkv, Sq, Sk, D, window, sinks))))
 
 
 def fa_bwd_window_varlen_workspace_bytes(num_seqs: int, total_q: int, max_seqlen_q: int, max_seqlen_k: int, H: int,
                                          Hkv: int, D: int, window: int, sinks: int = 0) -> int:
-    return int(load_library().fa_bwd_window_varlen_workspace_bytes(num_seqs, total_q, max_seqlen_q, max_seqlen_k, H,
-                                                                   Hkv, D, window, sinks))
+    args = (num_seqs, total_q, max_seqlen_q, max_seqlen_k, H, Hkv, D, window, sinks)
+    return int(load_library().fa_bwd_window_varlen_workspace_bytes(*map(_int32, args)))
 
 
 def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sinks: int = 0,
@@ -588,7 +594,7 @@ def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sin
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     ts = (q, k, v, o, dout, lse, dq, dk, dv, workspace)
     _launch("fa_bwd_window", stream, ts, workspace.numel() * workspace.element_size(), B, H, Hkv, Sq, Sk, D,
-            int(window), int(sinks), float(scale), code)
+            _int32(window), _int32(sinks), float(scale), code)
 
 
 def fa_bwd_window_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
@@ -612,8 +618,8 @@ def fa_bwd_window_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlen
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     ts = (q, k, v, o, dout, lse, dq, dk, dv, workspace)
     _launch("fa_bwd_window_varlen", stream, ts, workspace.numel() * workspace.element_size(), cu_seqlens_q.data_ptr(),
-            cu_seqlens_k.data_ptr(), n, Tq, Tk, int(max_seqlen_q), int(max_seqlen_k), H, Hkv, D, int(window),
-            int(sinks), float(scale), code, index=(cu_seqlens_q, cu_seqlens_k))
+            cu_seqlens_k.data_ptr(), n, Tq, Tk, _int32(max_seqlen_q), _int32(max_seqlen_k), H, Hkv, D, _int32(window),
+            _int32(sinks), float(scale), code, index=(cu_seqlens_q, cu_seqlens_k))
 
 
 def flash_attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None, stream=None):
@@ -718,7 +724,7 @@ def _kv_q4(fn, k, v, cache, block_table, cu_seqlens, max_seqlen, starts, stream)
     _expect("block_table", block_table, (n, block_table.shape[-1]), torch.int32)
     if starts is not None:
         _expect("starts", starts, (n,), torch.int32)
-    _launch(fn, stream, (k, v, *cache, block_table, cu_seqlens, starts), n, total, int(max_seqlen), Hkv, D,
+    _launch(fn, stream, (k, v, *cache, block_table, cu_seqlens, starts), n, total, _int32(max_seqlen), Hkv, D,
             num_blocks, block_size, block_table.shape[1], code)
 
 
@@ -742,7 +748,7 @@ def fa_decode_splits(B: int, H: int, Hkv: int, max_keys: int) -> int:
     call = _entry.get("fa_decode_splits")
     if call is None:
         call = _entry["fa_decode_splits"] = load_library().fa_decode_splits
-    return call(B, H, Hkv, max_keys)
+    return call(B, H, Hkv, _int32(max_keys))
 
 
 def _decode_gqa(q, cache, block_table, seq_lens, o, lse, o_part, m_part, l_part, counters, num_splits, window, sinks,
@@ -765,7 +771,7 @@ def _decode_gqa(q, cache, block_table, seq_lens, o, lse, o_part, m_part, l_part,
     _expect("seq_lens", seq_lens, (B,), torch.int32)
     _expect("o", o, (B, H, 1, D), q.dtype)
     _expect("lse", lse, (B, H), torch.float32)
-    S = int(num_splits)
+    S = _int32(num_splits)
     rows = B * H * S
     for name, t, need, dtype in (("o_part", o_part, rows * D, torch.float32), ("m_part", m_part, rows, torch.float32),
                                  ("l_part", l_part, rows, torch.float32), ("counters", counters, B * H, torch.int32)):
@@ -773,7 +779,7 @@ def _decode_gqa(q, cache, block_table, seq_lens, o, lse, o_part, m_part, l_part,
             raise ValueError(f"{name} must be contiguous {dtype} of at least {need} elements")
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     _launch(fn, stream, (q, *cache, block_table, seq_lens, o, lse, o_part, m_part, l_part, counters), B, H, Hkv, D,
-            num_blocks, block_size, max_blocks, S, int(window), int(sinks), float(scale), code)
+            num_blocks, block_size, max_blocks, S, _int32(window), _int32(sinks), float(scale), code)
 
 
 def fa_decode_paged_window(q, k_cache, v_cache, block_table, seq_lens, o, lse, o_part, m_part, l_part, counters,
