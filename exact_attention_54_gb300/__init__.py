@@ -344,6 +344,12 @@ def fa_check_device_error(stream=None):
 
 # ------------------------------------------------------ allocating helpers --
 
+def _words(n: int) -> int:
+    """fp32 elements of a workspace of n bytes; one where n is 0, so that a call with sizes that the library refuses
+    gets that refusal and not one of a NULL pointer."""
+    return max(n // 4, 1)
+
+
 def flash_attention(q, k, v, causal: bool = False, scale: float | None = None, stream=None):
     """Returns (o, lse) for dense [B,H,S,D] CUDA tensors."""
     if stream is not None:
@@ -365,7 +371,7 @@ def flash_attention_bwd(q, k, v, o, lse, dout, causal: bool = False, scale: floa
             return flash_attention_bwd(q, k, v, o, lse, dout, causal, scale, workspace=workspace)
     B, H, Sq, D = q.shape
     if workspace is None:
-        workspace = torch.empty(fa_bwd_workspace_bytes(B, H, Sq, D) // 4, dtype=torch.float32, device=q.device)
+        workspace = torch.empty(_words(fa_bwd_workspace_bytes(B, H, Sq, D)), dtype=torch.float32, device=q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fa_bwd(q, k, v, o, dout, lse, dq, dk, dv, workspace, causal, scale)
     return dq, dk, dv
@@ -381,7 +387,7 @@ def flash_attention_varlen_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k
                                               max_seqlen_k, causal, scale, workspace=workspace)
     Tq, H, D = q.shape
     if workspace is None:
-        workspace = torch.empty(fa_bwd_varlen_workspace_bytes(Tq, H, D) // 4, dtype=torch.float32, device=q.device)
+        workspace = torch.empty(_words(fa_bwd_varlen_workspace_bytes(Tq, H, D)), dtype=torch.float32, device=q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fa_bwd_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                   max_seqlen_k, causal, scale)
@@ -643,7 +649,7 @@ def flash_attention_window_bwd(q, k, v, o, lse, dout, window: int, sinks: int = 
         if q.dim() != 4 or k.dim() != 4:
             raise ValueError("q must be [B,H,Sq,D] and k, v [B,Hkv,Sk,D]")
         (B, H, Sq, D), (_, Hkv, Sk, _) = q.shape, k.shape
-        workspace = torch.empty(fa_bwd_window_workspace_bytes(B, H, Hkv, Sq, Sk, D, window, sinks) // 4,
+        workspace = torch.empty(_words(fa_bwd_window_workspace_bytes(B, H, Hkv, Sq, Sk, D, window, sinks)),
                                 dtype=torch.float32, device=q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window, sinks, scale)
@@ -677,7 +683,7 @@ def flash_attention_window_varlen_bwd(q, k, v, o, lse, dout, cu_seqlens_q, cu_se
         Tq, H, D = q.shape
         n = fa_bwd_window_varlen_workspace_bytes(cu_seqlens_q.numel() - 1, Tq, max_seqlen_q, max_seqlen_k, H,
                                                  k.shape[1], D, window, sinks)
-        workspace = torch.empty(n // 4, dtype=torch.float32, device=q.device)
+        workspace = torch.empty(_words(n), dtype=torch.float32, device=q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fa_bwd_window_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                          max_seqlen_k, window, sinks, scale)
@@ -831,7 +837,7 @@ def _flash_decode_gqa(q, cache, block_table, seq_lens, window, sinks, num_splits
             keys = min(keys, window + sinks)
         num_splits = fa_decode_splits(B, H, Hkv, keys)
         if workspace is not None:
-            num_splits = min(num_splits, workspace[1].numel() // (B * H))
+            num_splits = min(num_splits, workspace[1].numel() // max(B * H, 1))
     if workspace is None:
         workspace = _decode_workspace(B, H, num_splits, D, q.device, True)
     o, lse = torch.empty_like(q), torch.empty((B, H), dtype=torch.float32, device=q.device)
