@@ -430,3 +430,37 @@ def test_a_withheld_load_is_always_missed(packed):
             assert e.value.status == -9, i
     finally:
         fa.fa_test_withhold_load(0, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,Hkv,D,dtype,W,sinks", [(8, 2, 128, torch.bfloat16, 90, 4), (6, 3, 64, torch.float16, 40, 0)])
+def test_decode_behind_a_prefill_and_a_written_prompt(H, Hkv, D, dtype, W, sinks):
+    """A prompt prefilled and written to the 4-bit cache, then single tokens one after the other, each written and then
+    attended to: every token's o and lse are those of the definition over what the cache stands for, not rounded."""
+    block, n, more = 16, 150, 3
+    q, k, v, _ = draw(1, H, Hkv, n + more, n + more, D, dtype, seed=14 + D)
+    qd, kd, vd = (x[0].transpose(0, 1).contiguous().cuda() for x in (q, k, v))
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    o, lse = fa.flash_attention_window_varlen(qd[:n], kd[:n], vd[:n], cu, cu, n, W, sinks)
+    ref = plain_ops.window_attention(q[0, :, :n], k[0, :, :n], v[0, :, :n], W, sinks, D ** -0.5, dtype=dtype)
+    plain_ops.assert_window_close({"o": o.transpose(0, 1), "lse": lse}, ref)
+    nb = -(-(n + more) // block)
+    table = torch.arange(nb, dtype=torch.int32, device="cuda").flip(0).view(1, nb).contiguous()
+    cache = fa.kv_cache_q4(nb, Hkv, block, D, dtype)
+    fa.flash_kv_write_q4(kd[:n], vd[:n], cache, table, cu, n)
+    one = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    G = H // Hkv
+    for t in range(n, n + more):
+        at = torch.tensor([t], dtype=torch.int32, device="cuda")
+        fa.flash_kv_write_q4(kd[t:t + 1], vd[t:t + 1], cache, table, one, 1, starts=at)
+        o, lse = fa.flash_decode_paged_q4(qd[t].view(1, H, 1, D), cache, table, at + 1, W, sinks)
+        fa.fa_check_device_error()
+        c = [x.cpu() for x in cache]
+
+        def values(page, h):
+            return (plain_ops.q4_values(c[0][page, h // G], c[1][page, h // G]),
+                    plain_ops.q4_values(c[2][page, h // G], c[3][page, h // G]),
+                    c[3][page, h // G].double().repeat_interleave(32, -1))
+
+        ref = plain_ops.decode(q[:, :, t:t + 1], values, table.cpu(), [t + 1], block, W, sinks, D ** -0.5)
+        plain_ops.assert_attention_close(o, lse, *ref, dtype, f"token {t}")
