@@ -30,8 +30,8 @@ def _calls(dev, dtype=torch.float16, seed=0):
     lens = torch.full((B,), S, dtype=torch.int32).to(dev)
     pages = [r(B * nb, Hkv, block, D) for _ in range(2)]
     cache = fa.kv_cache_q4(B * nb, Hkv, block, D, dtype, device=dev)
-    cache = fa.KVCacheQ4(cache.k_codes + 83, r(*cache.k_scales.shape).abs(), cache.v_codes + 196,
-                         r(*cache.v_scales.shape).abs())
+    cache = fa.KVCacheQ4(cache.k_codes + 83, r(*cache.k_scales.shape).abs_(), cache.v_codes + 196,
+                         r(*cache.v_scales.shape).abs_())
     q1, q2 = r(B, H, 1, D), r(B, Hkv, 1, D)
     return read, {
         "window": lambda **kw: fa.flash_attention_window(q, k, v, W, sinks, **kw),
@@ -178,3 +178,52 @@ def test_given_stream_without_synchronising(name):
                 h, fine = plain_ops.half_step(got[0].dtype), torch.isfinite(b)
                 close |= fine & ((a - b).abs() <= 2 * h * b.abs() + 2.0 ** -13 * b[fine].abs().amax())
             assert bool(close.all()), (seed, i)
+
+
+def _same(a, b):
+    a, b = a.double(), b.double()
+    return bool(((a == b) | (torch.isnan(a) & torch.isnan(b))).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["window", "window_varlen", "read", "decode", "decode_q4", "dense", "splitkv_fused"])
+def test_handle_and_default_stream(name):
+    """A raw handle in place of the stream, and 0 for the default stream, from inside another one."""
+    _, calls = _calls("cuda")
+    want = calls[name]()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for handle in (s.cuda_stream, 0):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = calls[name](stream=handle)
+            assert torch.cuda.current_stream() != s
+        torch.cuda.synchronize()
+        fa.fa_check_device_error()
+        assert all(_same(a, b) for a, b in zip(got, want)), handle
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["window", "decode", "decode_q4", "read"])
+def test_side_stream_in_a_captured_graph(name):
+    """Captured with ``stream=`` another stream than the graph's: it joins the capture, and replays see new inputs."""
+    read, calls = _calls("cuda")
+    want = [t.clone() for t in calls[name]()]
+    kept = [t.clone() for t in read]
+    s = torch.cuda.Stream()
+    calls[name](stream=s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = calls[name](stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+    for t in read:
+        t.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert not all(_same(a, b) for a, b in zip(out, want))
+    for t, x in zip(read, kept):
+        t.copy_(x)
+    g.replay()
+    torch.cuda.synchronize()
+    fa.fa_check_device_error()
+    assert all(_same(a, b) for a, b in zip(out, want))
