@@ -16,6 +16,9 @@ the current stream. The calls that allocate (``flash_*``) behave with a given
 stream as under ``torch.cuda.stream(stream)``, behind the work queued so far on
 the current stream: outputs belong to that stream's order, and inputs must not
 be freed or overwritten before it is done with them.
+
+No call is recorded by autograd, whether or not its inputs require a gradient:
+gradients come from the calls named ``*_bwd``.
 """
 from __future__ import annotations
 
@@ -629,7 +632,8 @@ def fa_bwd_window_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlen
 
 
 def flash_attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None, stream=None):
-    """Returns (o, lse) of causal attention with a sliding window and sinks: q [B,H,Sq,D], k, v [B,Hkv,Sk,D]."""
+    """Returns (o, lse) of causal attention with a sliding window and sinks: q [B,H,Sq,D], k, v [B,Hkv,Sk,D]. Not
+    recorded by autograd: flash_attention_window_bwd gives the gradients."""
     if stream is not None:
         with _on_stream(stream, q):
             return flash_attention_window(q, k, v, window, sinks, scale)
@@ -812,7 +816,8 @@ def flash_kv_write_q4(k, v, cache: KVCacheQ4, block_table, cu_seqlens, max_seqle
 
 def flash_kv_read_q4(cache: KVCacheQ4, block_table, cu_seqlens, total: int, max_seqlen: int, starts=None, stream=None):
     """Returns (k, v) [total,Hkv,D] with positions starts[b].. of each sequence, packed by cu_seqlens. Rows that belong
-    to no sequence (total above cu_seqlens[-1]) are not initialised: clear them before attention runs over them."""
+    to no sequence (total above cu_seqlens[-1]) are not initialised: flash_attention_window_varlen takes no notice of
+    them, for flash_attention_varlen they have to be cleared."""
     if stream is not None:
         with _on_stream(stream, cache[0]):
             return flash_kv_read_q4(cache, block_table, cu_seqlens, total, max_seqlen, starts)

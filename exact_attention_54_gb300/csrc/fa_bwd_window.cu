@@ -8,10 +8,12 @@
 //
 // Bound by the chain of a step (two products, softmax, three products), as in
 // the causal kernel. 16 packed sequences of 123 to 1994 tokens, 16 heads on 4,
-// D = 128, bf16, window 512, 4 sinks: 382 us, of which the row pass (D_i, zeroed
-// dQ accumulator) 54 at 5.7 TB/s, the main kernel 276 (tensor pipe 47 % active;
+// D = 128, bf16, window 512, 4 sinks: 385 us, of which the row pass (D_i, zeroed
+// dQ accumulator) 54 at 5.7 TB/s, the main kernel 279 (tensor pipe 46 % active;
 // without sinks about 43 less), the conversion of dQ and the joining of segments,
-// in one launch, 44.
+// in one launch, 44. D = 64, (1, 32 heads, 4096 tokens, window 1024, 4 sinks): 180
+// us, 0.21 of the bf16 rate: one buffer for S^T and dP^T, so the products and the
+// key-row work take turns (tensor pipe 26 % active).
 #include "fa_bwd.cuh"
 
 namespace fa {

@@ -25,7 +25,7 @@
 // ring per warp (4.5 KB a tile at D = 128, two in flight), which leaves the
 // registers to the accumulators: four CTAs (16 warps) per SM. 16 sequences of
 // 16384 to 32768 keys, 8 key heads, 32 heads, D = 128: 113 us, 4.2 TB/s, where
-// the bytes alone take 70 us; some 330 warp instructions per 16 keys, the ALU
+// the bytes alone take 70 us; some 324 warp instructions per 16 keys, the ALU
 // pipe half of the time. (Bulk copies in place of these, eight per tile with 16-key
 // pages, cost a loop over the issuing lanes each and 8 us of it.)
 #include "fa_decode_gqa.cuh"

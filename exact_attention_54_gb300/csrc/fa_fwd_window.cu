@@ -13,7 +13,9 @@
 // end of the window counts whole, and so does the one with sinks); tensor pipe
 // 53 % active. Taking the first 32 keys alone of the tile with sinks gained 2 %
 // and is not done. 16 packed sequences of 123 to 1994 tokens, 16
-// heads on 4, window 512: 116 us.
+// heads on 4, window 512: 115 us, 662 TFLOP/s of the visible pairs and 975 of the
+// tiles visited (an item visits 9 tiles where that prefill's visits 17, so its
+// start and end, and the tile with sinks, weigh twice as much).
 #include "fa_fwd_kernel.cuh"
 
 namespace fa {

@@ -122,7 +122,9 @@ FA_API fa_status_t fa_fwd(const void *q, const void *k, const void *v, void *o, 
  *   cu_seqlens_k  device int32[num_seqs+1], same rules with total_k
  *   max_seqlen_q  >= every query length (sizes the launch)
  * Sequence i attends its own keys only; causal positions are counted from the
- * start of each sequence. Zero-length sequences are allowed.
+ * start of each sequence. Zero-length sequences are allowed. A tile that ends a
+ * sequence is multiplied whole, so the up to 127 rows behind it in the tensors
+ * must be finite (the window forms below have no such rule).
  * The offsets are checked on the device (the host cannot read them without a
  * synchronisation): if cu_seqlens_q or cu_seqlens_k is negative, decreasing or
  * beyond total_q / total_k, or a query sequence is longer than max_seqlen_q,
@@ -305,7 +307,8 @@ FA_API size_t fa_bwd_varlen_workspace_bytes(int total_q, int H, int D);
  * Length Sequences): the gradients of fa_fwd_varlen. Each sequence is an
  * independent attention over its own keys, so its gradients are those of
  * fa_bwd on that sequence alone; causal positions count from each sequence's
- * start (top-left, as in fa_fwd_varlen).
+ * start (top-left, as in fa_fwd_varlen). Rows behind a sequence must be finite,
+ * as there.
  *
  *   q, o, dout    [total_q,H,D]  fp16/bf16   k, v [total_k,H,D]  same dtype
  *   lse           [H,total_q] fp32, as written by fa_fwd_varlen
@@ -342,7 +345,9 @@ FA_API fa_status_t fa_bwd_varlen(const void *q, const void *k, const void *v, co
  * i - j < window or j < sinks: its own key and the window - 1 before it, and
  * the first `sinks` keys. window >= 1, sinks >= 0; a window of Sq or more is
  * plain causal attention. Key tiles that no query of a tile sees are not read,
- * so the work grows with Sq * (window + sinks).
+ * so the work grows with Sq * (window + sinks). Query 0 is at position 0: there
+ * is no offset for queries that come behind a cached prefix (their prefix's
+ * queries are passed too, or the new tokens decoded one by one).
  *
  *   q, o [B,H,Sq,D], lse [B,H,Sq], k, v [B,Hkv,Sk,D] as in fa_fwd; query head
  *   h reads key head h / (H / Hkv); Hkv divides H; D is 64 or 128.
@@ -466,7 +471,7 @@ FA_API fa_status_t fa_kv_write_q4(const void *k, const void *v, void *k_codes, v
  *
  *   k, v         [total,Hkv,D] outputs, dtype of the scales; rows outside
  *                every sequence, and rows that are skipped, are left as they
- *                were (attention over them wants finite values there)
+ *                were (fa_fwd_varlen wants finite values there)
  *   all other arguments as fa_kv_write_q4: row cu[b] + i receives position
  *   starts[b] + i of sequence b.
  * Offsets, positions and page numbers are checked on the device as by
