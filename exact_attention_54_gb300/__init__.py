@@ -43,6 +43,8 @@ __all__ = ["FAError", "fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_decode
            "flash_decode", "flash_decode_paged", "fa_kv_write_q4", "fa_kv_read_q4", "fa_decode_paged_window",
            "fa_decode_paged_q4", "fa_decode_splits", "KVCacheQ4", "kv_cache_q4", "flash_kv_write_q4",
            "flash_kv_read_q4", "flash_decode_paged_window", "flash_decode_paged_q4",
+           "fa_rope", "fa_rope_kv_write", "fa_kv_evict",
+           "rope_frequencies", "flash_rope", "flash_rope_bwd", "flash_rope_kv_write", "flash_kv_evict",
            "library_path", "load_library", "EXPORTED_SYMBOLS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -59,7 +61,7 @@ EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_decode_p
                     "fa_version", "fa_test_withhold_load", "fa_kv_write_q4", "fa_kv_read_q4", "fa_decode_splits",
                     "fa_fwd_window", "fa_fwd_window_varlen", "fa_bwd_window", "fa_bwd_window_varlen",
                     "fa_bwd_window_workspace_bytes", "fa_bwd_window_varlen_workspace_bytes",
-                    "fa_decode_paged_window", "fa_decode_paged_q4")
+                    "fa_decode_paged_window", "fa_decode_paged_q4", "fa_rope", "fa_rope_kv_write", "fa_kv_evict")
 
 
 class FAError(RuntimeError):
@@ -117,6 +119,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.fa_decode_splits.argtypes = [i, i, i, i]
         lib.fa_decode_paged_window.argtypes = [vp] * 11 + [i] * 10 + [f, i, vp]
         lib.fa_decode_paged_q4.argtypes = [vp] * 13 + [i] * 10 + [f, i, vp]
+        ll = ctypes.c_int64
+        lib.fa_rope.argtypes = [vp] * 4 + [i] * 5 + [ll] * 6 + [i, i, f, i, vp]
+        lib.fa_rope_kv_write.argtypes = [vp] * 11 + [i] * 7 + [ll] * 3 + [i] * 4 + [f, i, vp]
+        lib.fa_kv_evict.argtypes = [vp] * 9 + [i] * 11 + [vp]
         lib.fa_check_device_error.argtypes = [vp]
         lib.fa_status_string.argtypes = [i]
         lib.fa_status_string.restype = ctypes.c_char_p
@@ -124,7 +130,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         for name in ("fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_splitkv_merge", "fa_decode_splitkv_fused",
                      "fa_decode_paged_splitkv_fused", "fa_check_device_error", "fa_version", "fa_kv_write_q4",
                      "fa_fwd_window", "fa_fwd_window_varlen", "fa_bwd_window", "fa_bwd_window_varlen",
-                     "fa_kv_read_q4", "fa_decode_splits", "fa_decode_paged_window", "fa_decode_paged_q4"):
+                     "fa_kv_read_q4", "fa_decode_splits", "fa_decode_paged_window", "fa_decode_paged_q4", "fa_rope",
+                     "fa_rope_kv_write", "fa_kv_evict"):
             getattr(lib, name).restype = ctypes.c_int
         if path is None:
             _lib = lib
@@ -511,7 +518,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 def _launch(fn: str, stream, tensors, *args, index=None):
     """Call entry point ``fn`` with the pointers of ``tensors`` (None: NULL), ``args`` and the stream, on the device
     that the tensors, and those of ``index``, share."""
-    dev = tensors[0].get_device()
+    dev = (tensors[1] if tensors[0] is None else tensors[0]).get_device()
     ptrs = []
     for t in tensors:
         if t is None:
@@ -864,3 +871,183 @@ def flash_decode_paged_q4(q, cache: KVCacheQ4, block_table, seq_lens, window: in
     """flash_decode_paged_window over the 4-bit cache."""
     return _flash_decode_gqa(q, tuple(cache), block_table, seq_lens, window, sinks, num_splits, scale, stream,
                              workspace)
+
+
+# ------------------------------------- rotary positions, eviction from a cache --
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_len: int = 4096, low: float = 1.0, high: float = 32.0, device="cuda"):
+    """(inv_freq fp32 [rot_dim/2], mscale) for fa_rope: base^(-2i / rot_dim), for contexts ``factor`` times as long as
+    a model was trained on (``original_len``) scaled by one of
+
+    "linear"  every frequency divided by factor;
+    "base"    base times factor^(rot_dim / (rot_dim - 2)): the lowest frequency divided by factor, the highest kept;
+    "parts"   frequencies with under ``low`` turns in original_len divided by factor, those with over ``high`` kept, a
+              linear blend between; mscale = 0.1 ln(factor) + 1."""
+    if rot_dim < 16 or rot_dim % 16 != 0:
+        raise ValueError(f"rot_dim must be a positive multiple of 16, got {rot_dim}")
+    if scaling not in ("none", "linear", "base", "parts"):
+        raise ValueError(f"scaling must be none, linear, base or parts, got {scaling!r}")
+    if not (base > 0 and factor > 0 and original_len > 0 and high > low):
+        raise ValueError("base, factor and original_len must be positive, and high above low")
+    if scaling == "base":
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
+    mscale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        keep = ((original_len * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+        mscale = 0.1 * math.log(factor) + 1.0
+    return f.float().to(device), mscale
+
+
+def _rows(name, t, dtype):
+    """Batch, token and head strides of [total,H,D] or [B,H,S,D] rows of whole 16-byte pieces (0 for a dimension of
+    one)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    st = [0 if n == 1 else s for n, s in zip(t.shape, t.stride())]
+    if t.shape[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if any(s % 8 for s in st[:-1]):
+        raise ValueError(f"{name}: strides must be multiples of 8 elements, got {tuple(t.stride())}")
+    return (0, st[0], st[1]) if t.dim() == 3 else (st[0], st[2], st[1])
+
+
+def fa_rope(x, y, inv_freq, positions=None, interleaved: bool = False, mscale: float = 1.0, inverse: bool = False,
+            stream=None):
+    """Rotate rows x [total,H,D] or [B,H,S,D] into y (which may be x), or with ``inverse`` their gradient; any strides
+    that are multiples of 8. positions int32 [total] or [B,S] (None: 0, 1, ...); inv_freq fp32 [rot_dim/2]."""
+    if x.dim() not in (3, 4):
+        raise ValueError("x must be [total,H,D] or [B,H,S,D]")
+    (B, S, H), D = ((1, *x.shape[:2]) if x.dim() == 3 else (x.shape[0], x.shape[2], x.shape[1])), x.shape[-1]
+    code = _dtype_code(x)
+    xs, ys = _rows("x", x, x.dtype), _rows("y", y, x.dtype)
+    if y.shape != x.shape:
+        raise ValueError(f"y must have shape {tuple(x.shape)}, got {tuple(y.shape)}")
+    _expect("inv_freq", inv_freq, (inv_freq.numel(),), torch.float32)
+    if positions is not None:
+        _expect("positions", positions, (S,) if x.dim() == 3 else (B, S), torch.int32)
+    _launch("fa_rope", stream, (x, y, inv_freq, positions), B, S, H, D, 2 * inv_freq.numel(), *xs, *ys,
+            int(bool(interleaved)), int(bool(inverse)), float(mscale), code)
+
+
+def fa_rope_kv_write(q, k, v, q_out, k_cache, v_cache, block_table, cu_seqlens, max_seqlen: int, inv_freq=None,
+                     starts=None, positions=None, interleaved: bool = False, mscale: float = 1.0, stream=None):
+    """New tokens' q [total,H,D] rotated into q_out (which may be q; both None: keys and values only), k [total,Hkv,D]
+    rotated and v as it is into pages [num_blocks,Hkv,block_size,D], at positions starts[b].. (zero when None) of their
+    sequences; inv_freq None: nothing is rotated. q, k and v may be parts of a wider row (any stride between tokens)."""
+    if k.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("k must be [total,Hkv,D] and k_cache [num_blocks,Hkv,block_size,D]")
+    total, Hkv, D = k.shape
+    code = _dtype_code(k)
+    num_blocks, _, block_size, _ = k_cache.shape
+    H, strides = 0, []
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t is None and name == "q":
+            strides.append(0)
+            continue
+        if t.dim() != 3 or t.shape[0] != total or t.shape[2] != D or (name == "v" and t.shape[1] != Hkv):
+            raise ValueError(f"{name} must be [total,heads,D] with the total and D of k, got {tuple(t.shape)}")
+        _, token, head = _rows(name, t, k.dtype)
+        if t.shape[1] > 1 and head != D:
+            raise ValueError(f"{name}: a token's heads must be contiguous")
+        strides.append(token)
+    if q is not None:
+        H = q.shape[1]
+        _expect("q_out", q_out, (total, H, D), k.dtype)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _expect(name, t, (num_blocks, Hkv, block_size, D), k.dtype)
+    n = cu_seqlens.numel() - 1
+    _expect("cu_seqlens", cu_seqlens, (n + 1,), torch.int32)
+    _expect("block_table", block_table, (n, block_table.shape[-1]), torch.int32)
+    if starts is not None:
+        _expect("starts", starts, (n,), torch.int32)
+    if positions is not None:
+        _expect("positions", positions, (total,), torch.int32)
+    rot_dim = 0
+    if inv_freq is not None:
+        _expect("inv_freq", inv_freq, (inv_freq.numel(),), torch.float32)
+        rot_dim = 2 * inv_freq.numel()
+    _launch("fa_rope_kv_write", stream, (q, k, v, q_out, k_cache, v_cache, inv_freq, positions, block_table,
+                                         cu_seqlens, starts),
+            n, total, _int32(max_seqlen), H, Hkv, D, rot_dim, *strides, num_blocks, block_size, block_table.shape[1],
+            int(bool(interleaved)), float(mscale), code)
+
+
+def fa_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, kept, new_lens, new_weights, sinks: int = 0,
+                recent: int = 0, stream=None):
+    """Move the first ``sinks``, the last ``recent`` and the heaviest other keys of each sequence, kept.shape[2] in all,
+    to the pages of new_table: caches [num_blocks,Hkv,block_size,D], weights fp32 [B,Hkv,max_blocks*block_size], tables
+    int32 [B,max_blocks]; outputs kept int32 [B,Hkv,keep], new_lens int32 [B], new_weights as weights for new_table."""
+    if k_cache.dim() != 4 or block_table.dim() != 2 or new_table.dim() != 2 or kept.dim() != 3:
+        raise ValueError("caches must be [num_blocks,Hkv,block_size,D], tables [B,max_blocks] and kept [B,Hkv,keep]")
+    num_blocks, Hkv, block_size, D = k_cache.shape
+    code = _dtype_code(k_cache)
+    B, keep = block_table.shape[0], kept.shape[2]
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _expect(name, t, (num_blocks, Hkv, block_size, D), k_cache.dtype)
+    _expect("block_table", block_table, (B, block_table.shape[1]), torch.int32)
+    _expect("new_table", new_table, (B, new_table.shape[1]), torch.int32)
+    _expect("weights", weights, (B, Hkv, block_table.shape[1] * block_size), torch.float32)
+    _expect("new_weights", new_weights, (B, Hkv, new_table.shape[1] * block_size), torch.float32)
+    _expect("seq_lens", seq_lens, (B,), torch.int32)
+    _expect("new_lens", new_lens, (B,), torch.int32)
+    _expect("kept", kept, (B, Hkv, keep), torch.int32)
+    _launch("fa_kv_evict", stream, (k_cache, v_cache, weights, block_table, seq_lens, new_table, kept, new_lens,
+                                    new_weights),
+            B, Hkv, D, num_blocks, block_size, block_table.shape[1], new_table.shape[1], keep, _int32(sinks),
+            _int32(recent), code)
+
+
+def flash_rope(x, inv_freq, positions=None, interleaved: bool = False, mscale: float = 1.0, stream=None):
+    """Returns x [total,H,D] or [B,H,S,D] with rotary positions (see fa_rope), contiguous."""
+    if stream is not None:
+        with _on_stream(stream, x):
+            return flash_rope(x, inv_freq, positions, interleaved, mscale)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    fa_rope(x, y, inv_freq, positions, interleaved, mscale)
+    return y
+
+
+def flash_rope_bwd(dy, inv_freq, positions=None, interleaved: bool = False, mscale: float = 1.0, stream=None):
+    """Returns the gradient of flash_rope's x, given that of its result."""
+    if stream is not None:
+        with _on_stream(stream, dy):
+            return flash_rope_bwd(dy, inv_freq, positions, interleaved, mscale)
+    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+    fa_rope(dy, dx, inv_freq, positions, interleaved, mscale, inverse=True)
+    return dx
+
+
+def flash_rope_kv_write(q, k, v, k_cache, v_cache, block_table, cu_seqlens, max_seqlen: int, inv_freq=None, starts=None,
+                        positions=None, interleaved: bool = False, mscale: float = 1.0, stream=None):
+    """fa_rope_kv_write; returns the rotated queries [total,H,D] (None where q is). Rows that belong to no sequence
+    (total above cu_seqlens[-1]) are not initialised."""
+    if stream is not None:
+        with _on_stream(stream, k):
+            return flash_rope_kv_write(q, k, v, k_cache, v_cache, block_table, cu_seqlens, max_seqlen, inv_freq, starts,
+                                       positions, interleaved, mscale)
+    q_out = None if q is None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    fa_rope_kv_write(q, k, v, q_out, k_cache, v_cache, block_table, cu_seqlens, max_seqlen, inv_freq, starts, positions,
+                     interleaved, mscale)
+    return q_out
+
+
+def flash_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, keep: int, sinks: int = 0,
+                   recent: int = 0, stream=None):
+    """Evict all but ``keep`` keys of each sequence and key head into the pages of new_table (see fa_kv_evict). Returns
+    (kept [B,Hkv,keep], new_lens [B], new_weights [B,Hkv,new_max_blocks*block_size])."""
+    if stream is not None:
+        with _on_stream(stream, k_cache):
+            return flash_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, keep, sinks, recent)
+    B, Hkv, dev = block_table.shape[0], k_cache.shape[1], k_cache.device
+    kept = torch.empty((B, Hkv, int(keep)), dtype=torch.int32, device=dev)
+    new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+    new_weights = torch.empty((B, Hkv, new_table.shape[1] * k_cache.shape[2]), dtype=torch.float32, device=dev)
+    fa_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, kept, new_lens, new_weights, sinks, recent)
+    return kept, new_lens, new_weights

@@ -994,6 +994,152 @@ fa_status_t fa_decode_paged_q4(const void *q, const void *k_codes, const void *k
                       sinks, scale, dtype, stream);
 }
 
+// Strides of rows are whole 16-byte pieces, and far enough from 64-bit limits.
+static bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s <= (int64_t(1) << 40); }
+
+static bool rot_ok(int rot_dim, int D) { return rot_dim >= 0 && rot_dim <= D && rot_dim % 16 == 0; }
+
+fa_status_t fa_rope(const void *x, void *y, const float *inv_freq, const int32_t *positions, int B, int S, int H,
+                    int D, int rot_dim, int64_t x_batch, int64_t x_token, int64_t x_head, int64_t y_batch,
+                    int64_t y_token, int64_t y_head, int interleaved, int inverse, float mscale, fa_dtype_t dtype,
+                    void *stream) {
+    if ((!x || !y) && S != 0) return FA_ERR_NULL;
+    if (!inv_freq) return FA_ERR_NULL;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_DTYPE;
+    if (!fwd_head_dim_ok(D)) return FA_ERR_HEADDIM;
+    if (B < 1 || S < 0 || H < 1 || S > kMaxLen || H > (1 << 24) || rot_dim == 0 ||
+        !rot_ok(rot_dim, D) || !stride_ok(x_batch) || !stride_ok(x_token) || !stride_ok(x_head) ||
+        !stride_ok(y_batch) || !stride_ok(y_token) || !stride_ok(y_head))
+        return FA_ERR_SHAPE;
+    if (!std::isfinite(mscale)) return FA_ERR_SCALE;
+    if (!aligned16(x) || !aligned16(y) || !aligned4(inv_freq) || !aligned4(positions)) return FA_ERR_ALIGN;
+    if (S == 0) return FA_OK;
+    fa::RopeParams p{};
+    p.q = x;
+    p.q_out = y;
+    p.inv_freq = inv_freq;
+    p.positions = positions;
+    p.q_batch = x_batch;
+    p.q_stride = x_token;
+    p.q_head = x_head;
+    p.o_batch = y_batch;
+    p.o_stride = y_token;
+    p.o_head = y_head;
+    p.num_seqs = B;
+    p.total = S;
+    p.H = H;
+    p.D = D;
+    p.rot_dim = rot_dim;
+    p.interleaved = interleaved != 0;
+    p.inverse = inverse != 0;
+    p.mscale = mscale;
+    const int sms = num_sms();
+    if (sms <= 0) return FA_ERR_CUDA;
+    const cudaError_t e = fa::launch_rope(false, dtype == FA_BF16, p, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status_t fa_rope_kv_write(const void *q, const void *k, const void *v, void *q_out, void *k_cache, void *v_cache,
+                             const float *inv_freq, const int32_t *positions, const int32_t *block_table,
+                             const int32_t *cu_seqlens, const int32_t *starts, int num_seqs, int total,
+                             int max_seqlen, int H, int Hkv, int D, int rot_dim, int64_t q_token, int64_t k_token,
+                             int64_t v_token, int num_blocks, int block_size, int max_blocks_per_seq, int interleaved,
+                             float mscale, fa_dtype_t dtype, void *stream) {
+    if (!k_cache || !v_cache || !block_table || !cu_seqlens || (rot_dim > 0 && !inv_freq)) return FA_ERR_NULL;
+    if (total != 0 && (!k || !v || (H > 0 && (!q || !q_out)))) return FA_ERR_NULL;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_DTYPE;
+    if (D != 64 && D != 128) return FA_ERR_HEADDIM;
+    if (num_seqs < 1 || total < 0 || total > kMaxLen || max_seqlen < (total > 0 ? 1 : 0) || max_seqlen > kMaxLen ||
+        H < 0 || Hkv < 1 || static_cast<long long>(H) + 2LL * Hkv > (1 << 24) || !rot_ok(rot_dim, D) ||
+        !stride_ok(q_token) || !stride_ok(k_token) || !stride_ok(v_token))
+        return FA_ERR_SHAPE;
+    int log2_bs = 0;
+    if (!pages_ok(Hkv, num_blocks, block_size, max_blocks_per_seq, log2_bs)) return FA_ERR_SHAPE;
+    if (!std::isfinite(mscale)) return FA_ERR_SCALE;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_cache) ||
+        !aligned16(v_cache) || !aligned4(inv_freq) || !aligned4(positions) || !aligned4(block_table) ||
+        !aligned4(cu_seqlens) || !aligned4(starts))
+        return FA_ERR_ALIGN;
+    if (total == 0) return FA_OK;
+    fa::RopeParams p{};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_out = q_out;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.inv_freq = inv_freq;
+    p.positions = positions;
+    p.block_table = block_table;
+    p.cu_seqlens = cu_seqlens;
+    p.starts = starts;
+    p.q_stride = q_token;
+    p.k_stride = k_token;
+    p.v_stride = v_token;
+    p.num_seqs = num_seqs;
+    p.total = total;
+    p.max_seqlen = max_seqlen < total ? max_seqlen : total;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.rot_dim = rot_dim;
+    p.interleaved = interleaved != 0;
+    p.mscale = mscale;
+    p.log2_bs = log2_bs;
+    p.num_blocks = num_blocks;
+    p.max_blocks = max_blocks_per_seq;
+    p.err = device_error_word();
+    const int sms = num_sms();
+    if (p.err == nullptr || sms <= 0) return FA_ERR_CUDA;
+    const cudaError_t e = fa::launch_rope(true, dtype == FA_BF16, p, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status_t fa_kv_evict(void *k_cache, void *v_cache, const float *weights, const int32_t *block_table,
+                        const int32_t *seq_lens, const int32_t *new_table, int32_t *kept, int32_t *new_lens,
+                        float *new_weights, int B, int Hkv, int D, int num_blocks, int block_size,
+                        int max_blocks_per_seq, int new_max_blocks_per_seq, int keep, int sinks, int recent,
+                        fa_dtype_t dtype, void *stream) {
+    if (!k_cache || !v_cache || !weights || !block_table || !seq_lens || !new_table || !kept || !new_lens ||
+        !new_weights)
+        return FA_ERR_NULL;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_DTYPE;
+    if (D != 64 && D != 128) return FA_ERR_HEADDIM;
+    int log2_bs = 0;
+    if (B < 1 || Hkv < 1 || static_cast<long long>(B) * Hkv > INT_MAX ||
+        !pages_ok(Hkv, num_blocks, block_size, max_blocks_per_seq, log2_bs) ||
+        !pages_ok(Hkv, num_blocks, block_size, new_max_blocks_per_seq, log2_bs) || keep < 1 || keep > kMaxLen ||
+        sinks < 0 || recent < 0 || static_cast<long long>(sinks) + recent > keep)
+        return FA_ERR_SHAPE;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(weights) || !aligned4(block_table) ||
+        !aligned4(seq_lens) || !aligned4(new_table) || !aligned4(kept) || !aligned4(new_lens) ||
+        !aligned4(new_weights))
+        return FA_ERR_ALIGN;
+    fa::EvictParams p{};
+    p.k_cache = static_cast<uint16_t *>(k_cache);
+    p.v_cache = static_cast<uint16_t *>(v_cache);
+    p.weights = weights;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.new_table = new_table;
+    p.kept = kept;
+    p.new_lens = new_lens;
+    p.new_weights = new_weights;
+    p.B = B;
+    p.Hkv = Hkv;
+    p.num_blocks = num_blocks;
+    p.log2_bs = log2_bs;
+    p.max_blocks = max_blocks_per_seq;
+    p.new_max_blocks = new_max_blocks_per_seq;
+    p.keep = keep;
+    p.sinks = sinks;
+    p.recent = recent;
+    p.err = device_error_word();
+    if (p.err == nullptr) return FA_ERR_CUDA;
+    const cudaError_t e = fa::launch_kv_evict(D, p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 fa_status_t fa_test_withhold_load(int load, unsigned long long wait_limit_ns) {
     if (load < 0) return FA_ERR_SHAPE;
     g_withhold.store(load);

@@ -236,4 +236,47 @@ unsigned decode_gqa_grid(GqaDecodeParams &p, int sms, int ctas_per_sm, int heads
 // Partitions that fill `sms` SMs (fa_decode_splits).
 int decode_gqa_splits(int sms, int B, int H, int Hkv, int max_keys);
 
+// Parameters of the rotary kernels: rows of any strides (fa_rope: q and q_out
+// only, [num_seqs, total] tokens of H heads), or packed tokens into a paged
+// 16-bit cache (fa_rope_kv_write).
+struct RopeParams {
+    const void *q, *k, *v;
+    void *q_out, *k_cache, *v_cache;
+    const float *inv_freq;      // [rot_dim / 2]
+    const int *positions;       // rope: [num_seqs, total], write: [total]; or nullptr
+    const int *block_table;     // write: [num_seqs, max_blocks]
+    const int *cu_seqlens;      // write: [num_seqs + 1]
+    const int *starts;          // write: [num_seqs] or nullptr
+    long long q_batch, o_batch; // rope: elements between sequences
+    long long q_stride, k_stride, v_stride, o_stride;  // elements between tokens
+    long long q_head, o_head;   // rope: elements between heads
+    int num_seqs, total, max_seqlen;  // rope: total tokens each
+    int H, Hkv, D, rot_dim;
+    int interleaved, inverse;
+    float mscale;
+    int log2_bs, num_blocks, max_blocks;
+    int tokens;                 // per CTA (set by launch_rope)
+    int *err;                   // write: device error word
+};
+
+cudaError_t launch_rope(bool write, bool bf16, RopeParams p, int sms, cudaStream_t stream);
+
+// Parameters of the eviction kernels.
+struct EvictParams {
+    uint16_t *k_cache, *v_cache;  // pages [num_blocks, Hkv, block_size, D]
+    const float *weights;       // [B, Hkv, max_blocks * block_size]
+    const int *block_table;     // [B, max_blocks]
+    const int *seq_lens;        // [B]
+    const int *new_table;       // [B, new_max_blocks]
+    int *kept;                  // [B, Hkv, keep]
+    int *new_lens;              // [B]
+    float *new_weights;         // [B, Hkv, new_max_blocks * block_size]
+    int B, Hkv, num_blocks, log2_bs, max_blocks, new_max_blocks;
+    int keep, sinks, recent;
+    int cached;                 // keys in shared memory (set by launch_kv_evict)
+    int *err;                   // device error word
+};
+
+cudaError_t launch_kv_evict(int D, EvictParams p, cudaStream_t stream);
+
 }  // namespace fa

@@ -1,0 +1,223 @@
+// Rotary positions: rows of queries and keys with pairs of their columns turned
+// by position-dependent angles (fa_rope, its gradient with inverse angles), and
+// the same on the way into a paged 16-bit cache (fa_rope_kv_write).
+//
+// Pair i of a row, (a, b), at position p becomes m (a cos t - b sin t,
+// b cos t + a sin t), t = p inv_freq[i]; the gradient is the same with -t. Every
+// row is read and written once: a stream, bound by HBM, by launch latency for a
+// few tokens.
+//
+// Angles: all heads of a token share them, so a CTA forms the cosines and sines
+// of its tokens once, in shared memory. An angle in turns is the fraction of
+// p inv_freq / 2 pi; far positions lose it in 32 bits (2^20 inv_freq is off by
+// 2^-5 rad), so inv_freq / 2 pi is held as a 64-bit fraction and its product
+// with p wraps as turns do: one integer product, off by 2^-53 of p turns at
+// most. The fraction's upper 32 bits, rounded to 24, go into sincospi.
+//
+// Grid: a chunk of tokens (x) of one sequence (y, z) per CTA, as in the 4-bit
+// cache's kernels. D / 16 lanes share a row, two 16-byte pieces each: the
+// pieces that pair up (half layout), or neighbouring ones.
+#include "fa_kv_q4.cuh"
+#include "fa_launch.h"
+
+namespace fa {
+namespace rope {
+
+constexpr int kThreads = 128;
+constexpr int kInFlight = 4;   // rows of a lane group with their loads in flight
+constexpr int kMaxTokens = 8;  // of a CTA
+constexpr int kMaxPairs = 512; // D = 1024
+
+// Two pieces of 8 columns of a row.
+struct Pieces {
+    uint4 a, b;
+};
+
+__device__ __forceinline__ uint32_t &word(uint4 &x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; }
+
+// Turns the 8 pairs of a lane. turn: their (cos, sin), mscale in both.
+// INTER: pairs are neighbouring columns of a (4) and b (4); else column i of a
+// pairs with column i of b.
+template <bool BF16, bool INTER>
+__device__ __forceinline__ void rotate(Pieces &x, const float2 *turn) {
+    if constexpr (INTER) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t &w = i < 4 ? word(x.a, i) : word(x.b, i - 4);
+            const float a = ptx::unpack_lo<BF16>(w), b = ptx::unpack_hi<BF16>(w);
+            const float2 t = turn[i];
+            w = ptx::pack2<BF16>(a * t.x - b * t.y, b * t.x + a * t.y);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t &wa = word(x.a, i), &wb = word(x.b, i);
+            const float a0 = ptx::unpack_lo<BF16>(wa), a1 = ptx::unpack_hi<BF16>(wa);
+            const float b0 = ptx::unpack_lo<BF16>(wb), b1 = ptx::unpack_hi<BF16>(wb);
+            const float2 t0 = turn[2 * i], t1 = turn[2 * i + 1];
+            wa = ptx::pack2<BF16>(a0 * t0.x - b0 * t0.y, a1 * t1.x - b1 * t1.y);
+            wb = ptx::pack2<BF16>(b0 * t0.x + a0 * t0.y, b1 * t1.x + a1 * t1.y);
+        }
+    }
+}
+
+// Cosines and sines (times mscale) of `tokens` tokens, pos(i) the position of
+// token i. The whole CTA calls it; ends synchronised.
+template <class Pos>
+__device__ __forceinline__ void fill_turns(const RopeParams &p, float2 *turns, int tokens, Pos pos) {
+    const int pairs = p.rot_dim / 2;
+    for (int i = threadIdx.x; i < pairs; i += kThreads) {
+        double f = static_cast<double>(p.inv_freq[i]) * 0.15915494309189533577;  // 1 / 2 pi
+        f -= floor(f);
+        const unsigned long long frac = static_cast<unsigned long long>(f * 18446744073709551616.0);
+        for (int t = 0; t < tokens; ++t) {
+            const long long at = static_cast<long long>(static_cast<unsigned long long>(pos(t)) * frac);
+            float s, c;
+            sincospif(static_cast<float>(static_cast<int>(at >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+            turns[t * pairs + i] = make_float2(c * p.mscale, (p.inverse ? -s : s) * p.mscale);
+        }
+    }
+    __syncthreads();
+}
+
+// Columns of a lane's two pieces, and whether they are turned.
+struct Lane {
+    int a, b, pair;
+    bool turned;
+    __device__ __forceinline__ Lane(int sub, int rot_dim, bool inter) {
+        turned = sub < rot_dim / 16;
+        pair = sub * 8;
+        a = turned && !inter ? sub * 8 : sub * 16;
+        b = turned && !inter ? rot_dim / 2 + sub * 8 : sub * 16 + 8;
+    }
+};
+
+// Rows [0, rows) of a CTA, lane group by lane group: row(r, src, dst, token)
+// says where row r is read and written (dst NULL: nowhere) and which of the
+// CTA's tokens turns it (-1: none, copied).
+template <bool BF16, bool INTER, class Row>
+__device__ __forceinline__ void stream_rows(const RopeParams &p, int D, const float2 *turns, int rows, Row row) {
+    const int lanes = D / 16, groups = kThreads / lanes;
+    const int sub = threadIdx.x % lanes, pairs = p.rot_dim / 2;
+    const Lane l(sub, p.rot_dim, INTER);
+    for (int r0 = threadIdx.x / lanes; r0 < rows; r0 += groups * kInFlight) {
+        Pieces x[kInFlight];
+        uint16_t *dst[kInFlight];
+        int token[kInFlight];
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i) {
+            dst[i] = nullptr;
+            if (r0 + i * groups >= rows) continue;
+            const uint16_t *src;
+            row(r0 + i * groups, src, dst[i], token[i]);
+            if (dst[i] == nullptr) continue;
+            x[i].a = __ldcs(reinterpret_cast<const uint4 *>(src + l.a));
+            x[i].b = __ldcs(reinterpret_cast<const uint4 *>(src + l.b));
+        }
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i) {
+            if (dst[i] == nullptr) continue;
+            if (l.turned && token[i] >= 0) rotate<BF16, INTER>(x[i], turns + token[i] * pairs + l.pair);
+            *reinterpret_cast<uint4 *>(dst[i] + l.a) = x[i].a;
+            *reinterpret_cast<uint4 *>(dst[i] + l.b) = x[i].b;
+        }
+    }
+}
+
+template <bool BF16, bool INTER>
+__global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RopeParams p) {
+    extern __shared__ float2 turns[];
+    const long long b = static_cast<long long>(blockIdx.z) * gridDim.y + blockIdx.y;
+    if (b >= p.num_seqs) return;
+    const int s0 = static_cast<int>(blockIdx.x) * p.tokens, n = min(p.tokens, p.total - s0);
+    fill_turns(p, turns, n, [&](int t) -> long long {
+        return p.positions == nullptr ? s0 + t : p.positions[b * p.total + s0 + t];
+    });
+    const uint16_t *src0 = static_cast<const uint16_t *>(p.q) + b * p.q_batch + s0 * p.q_stride;
+    uint16_t *dst0 = static_cast<uint16_t *>(p.q_out) + b * p.o_batch + s0 * p.o_stride;
+    stream_rows<BF16, INTER>(p, p.D, turns, n * p.H, [&](int r, const uint16_t *&src, uint16_t *&dst, int &token) {
+        token = r / p.H;
+        const int h = r - token * p.H;
+        src = src0 + token * p.q_stride + h * p.q_head;
+        dst = dst0 + token * p.o_stride + h * p.o_head;
+    });
+}
+
+template <bool BF16, bool INTER>
+__global__ void __launch_bounds__(kThreads) fa_rope_kv_write_kernel(const RopeParams p) {
+    extern __shared__ float2 turns[];
+    __shared__ long long rows[kMaxTokens];  // first key head's cache row of each token, or -1
+    const long long b = static_cast<long long>(blockIdx.z) * gridDim.y + blockIdx.y;
+    if (b >= p.num_seqs) return;
+    const int i0 = static_cast<int>(blockIdx.x) * p.tokens;
+    const int t0 = p.cu_seqlens[b], t1 = p.cu_seqlens[b + 1];
+    const int start = p.starts == nullptr ? 0 : p.starts[b];
+    if (t0 < 0 || t1 < t0 || t1 > p.total || t1 - t0 > p.max_seqlen || start < 0) {
+        if (threadIdx.x == 0) atomicExch(p.err, kDeviceErrSeqLens);
+        return;
+    }
+    const int first = t0 + i0, n = min(p.tokens, t1 - t0 - i0);
+    if (n <= 0) return;
+    const long long pos0 = static_cast<long long>(start) + i0;
+    if (threadIdx.x < n) {
+        const long long pos = pos0 + threadIdx.x, blk = pos >> p.log2_bs;
+        const int page = blk < p.max_blocks ? p.block_table[b * p.max_blocks + blk] : -1;
+        const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_blocks);
+        if (!ok) atomicExch(p.err, kDeviceErrBadIndex);
+        rows[threadIdx.x] =
+            ok ? ((static_cast<long long>(page) * p.Hkv) << p.log2_bs) + (pos & ((1 << p.log2_bs) - 1)) : -1;
+    }
+    fill_turns(p, turns, n, [&](int t) -> long long {
+        return p.positions == nullptr ? pos0 + t : p.positions[first + t];
+    });
+    const int per = p.H + 2 * p.Hkv;
+    stream_rows<BF16, INTER>(p, p.D, turns, n * per, [&](int r, const uint16_t *&src, uint16_t *&dst, int &token) {
+        const int t = r / per, h = r - t * per;
+        const long long at = first + t;
+        token = t;
+        if (h < p.H) {
+            src = static_cast<const uint16_t *>(p.q) + at * p.q_stride + static_cast<long long>(h) * p.D;
+            dst = static_cast<uint16_t *>(p.q_out) + (at * p.H + h) * p.D;
+            return;
+        }
+        const bool value = h >= p.H + p.Hkv;
+        const int hk = h - p.H - (value ? p.Hkv : 0);
+        src = value ? static_cast<const uint16_t *>(p.v) + at * p.v_stride + static_cast<long long>(hk) * p.D
+                    : static_cast<const uint16_t *>(p.k) + at * p.k_stride + static_cast<long long>(hk) * p.D;
+        if (value) token = -1;
+        if (rows[t] < 0) return;
+        dst = static_cast<uint16_t *>(value ? p.v_cache : p.k_cache) +
+              (rows[t] + (static_cast<long long>(hk) << p.log2_bs)) * p.D;
+    });
+}
+
+}  // namespace rope
+
+// Tokens of a CTA: about kInFlight rows for each of its lane groups twice over,
+// so that the angles of a token (64 sincos at D = 128) are spread over all
+// threads; fewer where there would be less than a wave of CTAs.
+static int rope_tokens(long long sequences, long long longest, int rows_per_token, int D, int sms) {
+    const int groups = rope::kThreads / (D / 16);
+    long long t = (2LL * rope::kInFlight * groups + rows_per_token - 1) / rows_per_token;
+    while (t > 1 && sequences * ((longest + t - 1) / t) < 4LL * sms) t /= 2;
+    return static_cast<int>(t < 1 ? 1 : t < rope::kMaxTokens ? t : rope::kMaxTokens);
+}
+
+cudaError_t launch_rope(bool write, bool bf16, RopeParams p, int sms, cudaStream_t st) {
+    const int rows = write ? p.H + 2 * p.Hkv : p.H;
+    const int longest = write ? p.max_seqlen : p.total;
+    p.tokens = rope_tokens(p.num_seqs, longest, rows, p.D, sms);
+    const unsigned seqs = static_cast<unsigned>(p.num_seqs), y = seqs < 65535u ? seqs : 65535u;
+    const dim3 grid(static_cast<unsigned>((longest - 1) / p.tokens + 1), y, (seqs + y - 1) / y);
+    const int smem = p.tokens * p.rot_dim / 2 * static_cast<int>(sizeof(float2));  // at most 32 KB
+#define FA_ROPE(BB, II)                                                                             \
+    if (bf16 == BB && (p.interleaved != 0) == II) {                                                 \
+        if (write) rope::fa_rope_kv_write_kernel<BB, II><<<grid, rope::kThreads, smem, st>>>(p);    \
+        else rope::fa_rope_kernel<BB, II><<<grid, rope::kThreads, smem, st>>>(p);                   \
+    }
+    FA_ROPE(false, false) FA_ROPE(false, true) FA_ROPE(true, false) FA_ROPE(true, true)
+#undef FA_ROPE
+    return cudaGetLastError();
+}
+
+}  // namespace fa

@@ -17,6 +17,11 @@
  *   fa_decode_paged_window, fa_decode_paged_q4
  *                      one-token attention over a paged 16-bit or 4-bit cache
  *                      with shared key heads, a sliding window and sinks.
+ *   fa_rope            rotary positions of queries and keys, and their gradient.
+ *   fa_rope_kv_write   the same on the way into a paged 16-bit cache.
+ *   fa_fwd_paged       attention of chunks of new tokens over a paged cache.
+ *   fa_kv_weights      the attention weight that each cached key receives.
+ *   fa_kv_evict        the keys of least weight leave a paged cache.
  *
  * Common rules
  *   - Every tensor pointer is a DEVICE pointer owned by the caller. The library
@@ -546,6 +551,107 @@ FA_API fa_status_t fa_decode_paged_q4(const void *q, const void *k_codes, const 
                                       int32_t *counters, int B, int H, int Hkv, int D, int num_blocks,
                                       int block_size, int max_blocks_per_seq, int num_splits, int window, int sinks,
                                       float scale, fa_dtype_t dtype, void *stream);
+
+/*
+ * fa_rope - rotary positions, or (inverse) their gradient.
+ *
+ * Of each row of D columns the first rot_dim are rot_dim / 2 pairs: columns i
+ * and i + rot_dim / 2 (interleaved = 0) or 2 i and 2 i + 1 (interleaved = 1).
+ * Pair i, (a, b), of a token at position p becomes
+ *   mscale * (a cos t - b sin t, b cos t + a sin t),   t = p * inv_freq[i],
+ * rounded once; columns from rot_dim on are copied. inverse = 1 takes -t: the
+ * gradient with respect to x, given that of y. Frequencies scaled for long
+ * contexts are other values of inv_freq and mscale.
+ *
+ *   x, y       rows of D fp16/bf16 columns, row (b, s, h) at element
+ *              b * x_batch + s * x_token + h * x_head of x, and alike of y:
+ *              [B,S,H,D], [B,H,S,D], packed tokens (B = 1, S = total) or a part
+ *              of a wider tensor. Strides are >= 0 and multiples of 8. y may be
+ *              x itself (same strides); otherwise they must not overlap.
+ *   inv_freq   device fp32 [rot_dim / 2]
+ *   positions  device int32 [B,S], or NULL: 0 .. S - 1. Any values: an angle is
+ *              formed as a 64-bit fraction of a turn, so far positions keep
+ *              theirs (off by 2^-53 |p| turns at most, besides 2^-24 of it).
+ *   D          64, 128, 256, 512 or 1024; rot_dim a multiple of 16, 16 .. D
+ * S = 0 is allowed and does nothing. One launch.
+ * Errors: FA_ERR_NULL, FA_ERR_SHAPE (rot_dim and strides too), FA_ERR_HEADDIM,
+ * FA_ERR_DTYPE, FA_ERR_ALIGN, FA_ERR_SCALE (mscale is not finite), FA_ERR_CUDA.
+ */
+FA_API fa_status_t fa_rope(const void *x, void *y, const float *inv_freq, const int32_t *positions, int B, int S,
+                           int H, int D, int rot_dim, int64_t x_batch, int64_t x_token, int64_t x_head,
+                           int64_t y_batch, int64_t y_token, int64_t y_head, int interleaved, int inverse,
+                           float mscale, fa_dtype_t dtype, void *stream);
+
+/*
+ * fa_rope_kv_write - new tokens into a paged 16-bit cache, queries and keys
+ * rotated on the way (as fa_rope does it), in one launch.
+ *
+ *   q, q_out     [total,H,D] queries and where they go, rotated; q_out is
+ *                contiguous and may be q where that is too. H = 0: no queries
+ *                (both may be NULL).
+ *   k, v         [total,Hkv,D]: the new tokens' keys (stored rotated) and
+ *                values (stored as they are); D is 64 or 128
+ *   q_token, k_token, v_token   elements between tokens of q, k and v (H * D,
+ *                Hkv * D for contiguous ones; parts of a joint projection are
+ *                wider); multiples of 8
+ *   k_cache, v_cache [num_blocks,Hkv,block_size,D], as fa_decode_paged_window
+ *                and fa_fwd_paged read them; only the new tokens' rows change
+ *   inv_freq     device fp32 [rot_dim / 2]; rot_dim = 0 rotates nothing
+ *                (inv_freq may be NULL)
+ *   positions    device int32 [total]: rotary position of each packed token, or
+ *                NULL: its position in its sequence's cache, starts[b] + i. They
+ *                differ once keys have been evicted.
+ *   block_table, cu_seqlens, starts, max_seqlen, block_size: as fa_kv_write_q4
+ * Offsets, positions in the cache and page numbers are checked on the device as
+ * by fa_kv_write_q4 (queries of a token without a page are still rotated).
+ * total = 0 is allowed (max_seqlen may then be 0) and does nothing.
+ * Errors: FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_HEADDIM, FA_ERR_DTYPE,
+ * FA_ERR_ALIGN, FA_ERR_SCALE (mscale is not finite), FA_ERR_CUDA.
+ */
+FA_API fa_status_t fa_rope_kv_write(const void *q, const void *k, const void *v, void *q_out, void *k_cache,
+                                    void *v_cache, const float *inv_freq, const int32_t *positions,
+                                    const int32_t *block_table, const int32_t *cu_seqlens, const int32_t *starts,
+                                    int num_seqs, int total, int max_seqlen, int H, int Hkv, int D, int rot_dim,
+                                    int64_t q_token, int64_t k_token, int64_t v_token, int num_blocks,
+                                    int block_size, int max_blocks_per_seq, int interleaved, float mscale,
+                                    fa_dtype_t dtype, void *stream);
+
+/*
+ * fa_kv_evict - the keys of least weight leave a paged 16-bit cache.
+ *
+ * Of a sequence of L = seq_lens[b] keys with L > keep, each key head keeps
+ * `keep`: the first `sinks`, the last `recent`, and of those between them the
+ * ones of greatest weight (ties to the earlier key; a NaN is less than any
+ * number). They keep their order and become keys 0 .. keep - 1 of the new
+ * pages, each head its own. With L <= keep all stay, as keys 0 .. L - 1.
+ *
+ *   k_cache, v_cache [num_blocks,Hkv,block_size,D] fp16/bf16, D 64 or 128
+ *   weights      [B,Hkv,max_blocks_per_seq * block_size] fp32, as fa_kv_weights
+ *                fills it; not changed
+ *   block_table  device int32 [B, max_blocks_per_seq]: the sequences' pages,
+ *                which are only read (they may be shared with other sequences)
+ *   seq_lens     device int32 [B], clamped as by fa_decode_paged_window
+ *   new_table    device int32 [B, new_max_blocks_per_seq]: the pages that the
+ *                kept keys go to, none of them a page that the call reads or
+ *                names twice. Their rows behind the kept keys are not written.
+ *   kept         int32 [B,Hkv,keep] output: what each new key was before
+ *                (-1 behind the last one)
+ *   new_lens     int32 [B] output: min(L, keep); not seq_lens itself
+ *   new_weights  [B,Hkv,new_max_blocks_per_seq * block_size] fp32 output: the
+ *                kept keys' weights, then zeros; not weights itself
+ *   block_size a power of two, 1..1024; keep >= 1, sinks, recent >= 0,
+ *   sinks + recent <= keep
+ * A key whose old or new page is outside [0, num_blocks), or that has no place
+ * in new_table, is not copied and the next fa_check_device_error returns
+ * FA_ERR_DEVICE_INDEX. Two launches.
+ * Errors: FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_HEADDIM, FA_ERR_DTYPE,
+ * FA_ERR_ALIGN, FA_ERR_CUDA.
+ */
+FA_API fa_status_t fa_kv_evict(void *k_cache, void *v_cache, const float *weights, const int32_t *block_table,
+                               const int32_t *seq_lens, const int32_t *new_table, int32_t *kept, int32_t *new_lens,
+                               float *new_weights, int B, int Hkv, int D, int num_blocks, int block_size,
+                               int max_blocks_per_seq, int new_max_blocks_per_seq, int keep, int sinks, int recent,
+                               fa_dtype_t dtype, void *stream);
 
 /*
  * fa_check_device_error - synchronise `stream`, then read and clear the
