@@ -43,8 +43,9 @@ __all__ = ["FAError", "fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_decode
            "flash_decode", "flash_decode_paged", "fa_kv_write_q4", "fa_kv_read_q4", "fa_decode_paged_window",
            "fa_decode_paged_q4", "fa_decode_splits", "KVCacheQ4", "kv_cache_q4", "flash_kv_write_q4",
            "flash_kv_read_q4", "flash_decode_paged_window", "flash_decode_paged_q4",
-           "fa_rope", "fa_rope_kv_write", "fa_kv_evict",
-           "rope_frequencies", "flash_rope", "flash_rope_bwd", "flash_rope_kv_write", "flash_kv_evict",
+           "fa_rope", "fa_rope_kv_write", "fa_fwd_paged", "fa_fwd_paged_workspace_bytes", "fa_kv_evict",
+           "rope_frequencies", "flash_rope", "flash_rope_bwd", "flash_rope_kv_write", "flash_attention_paged",
+           "flash_kv_evict",
            "library_path", "load_library", "EXPORTED_SYMBOLS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -61,7 +62,8 @@ EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_decode_p
                     "fa_version", "fa_test_withhold_load", "fa_kv_write_q4", "fa_kv_read_q4", "fa_decode_splits",
                     "fa_fwd_window", "fa_fwd_window_varlen", "fa_bwd_window", "fa_bwd_window_varlen",
                     "fa_bwd_window_workspace_bytes", "fa_bwd_window_varlen_workspace_bytes",
-                    "fa_decode_paged_window", "fa_decode_paged_q4", "fa_rope", "fa_rope_kv_write", "fa_kv_evict")
+                    "fa_decode_paged_window", "fa_decode_paged_q4", "fa_rope", "fa_rope_kv_write", "fa_fwd_paged",
+                    "fa_fwd_paged_workspace_bytes", "fa_kv_evict")
 
 
 class FAError(RuntimeError):
@@ -122,6 +124,9 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         ll = ctypes.c_int64
         lib.fa_rope.argtypes = [vp] * 4 + [i] * 5 + [ll] * 6 + [i, i, f, i, vp]
         lib.fa_rope_kv_write.argtypes = [vp] * 11 + [i] * 7 + [ll] * 3 + [i] * 4 + [f, i, vp]
+        lib.fa_fwd_paged.argtypes = [vp] * 9 + [sz] + [i] * 11 + [f, i, vp]
+        lib.fa_fwd_paged_workspace_bytes.argtypes = [i] * 4
+        lib.fa_fwd_paged_workspace_bytes.restype = sz
         lib.fa_kv_evict.argtypes = [vp] * 9 + [i] * 11 + [vp]
         lib.fa_check_device_error.argtypes = [vp]
         lib.fa_status_string.argtypes = [i]
@@ -131,7 +136,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                      "fa_decode_paged_splitkv_fused", "fa_check_device_error", "fa_version", "fa_kv_write_q4",
                      "fa_fwd_window", "fa_fwd_window_varlen", "fa_bwd_window", "fa_bwd_window_varlen",
                      "fa_kv_read_q4", "fa_decode_splits", "fa_decode_paged_window", "fa_decode_paged_q4", "fa_rope",
-                     "fa_rope_kv_write", "fa_kv_evict"):
+                     "fa_rope_kv_write", "fa_fwd_paged", "fa_kv_evict"):
             getattr(lib, name).restype = ctypes.c_int
         if path is None:
             _lib = lib
@@ -979,6 +984,37 @@ def fa_rope_kv_write(q, k, v, q_out, k_cache, v_cache, block_table, cu_seqlens, 
             int(bool(interleaved)), float(mscale), code)
 
 
+def fa_fwd_paged_workspace_bytes(max_seqlen_q: int, H: int, Hkv: int, D: int) -> int:
+    return int(load_library().fa_fwd_paged_workspace_bytes(*map(_int32, (max_seqlen_q, H, Hkv, D))))
+
+
+def fa_fwd_paged(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, o, lse, workspace, max_seqlen_q: int,
+                 window: int = 0, sinks: int = 0, scale: float | None = None, stream=None):
+    """Attention of chunks of new tokens, q and o [total_q,H,D] packed by cu_seqlens_q int32 [num_seqs+1], over pages
+    k_cache, v_cache [num_blocks,Hkv,block_size,D] that hold their keys too: block_table int32 [num_seqs,max_blocks],
+    seq_lens int32 [num_seqs] keys with the chunk's; lse [H,total_q] fp32; workspace of at least
+    fa_fwd_paged_workspace_bytes(max_seqlen_q, H, Hkv, D) bytes."""
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [total_q,H,D] and pages [num_blocks,Hkv,block_size,D]")
+    Tq, H, D = q.shape
+    num_blocks, Hkv, block_size, _ = k_cache.shape
+    n = cu_seqlens_q.numel() - 1
+    code = _dtype_code(q)
+    _expect("q", q, (Tq, H, D), q.dtype)
+    _expect("o", o, (Tq, H, D), q.dtype)
+    _expect("k_cache", k_cache, (num_blocks, Hkv, block_size, D), q.dtype)
+    _expect("v_cache", v_cache, (num_blocks, Hkv, block_size, D), q.dtype)
+    _expect("lse", lse, (H, Tq), torch.float32)
+    _expect("cu_seqlens_q", cu_seqlens_q, (n + 1,), torch.int32)
+    _expect("seq_lens", seq_lens, (n,), torch.int32)
+    _expect("block_table", block_table, (n, block_table.shape[-1]), torch.int32)
+    _need_contig(workspace)
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    _launch("fa_fwd_paged", stream, (q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, o, lse, workspace),
+            workspace.numel() * workspace.element_size(), n, Tq, _int32(max_seqlen_q), H, Hkv, D, num_blocks, block_size,
+            block_table.shape[1], _int32(window), _int32(sinks), float(scale), code)
+
+
 def fa_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, kept, new_lens, new_weights, sinks: int = 0,
                 recent: int = 0, stream=None):
     """Move the first ``sinks``, the last ``recent`` and the heaviest other keys of each sequence, kept.shape[2] in all,
@@ -1036,6 +1072,26 @@ def flash_rope_kv_write(q, k, v, k_cache, v_cache, block_table, cu_seqlens, max_
     fa_rope_kv_write(q, k, v, q_out, k_cache, v_cache, block_table, cu_seqlens, max_seqlen, inv_freq, starts, positions,
                      interleaved, mscale)
     return q_out
+
+
+def flash_attention_paged(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, max_seqlen_q: int, window: int = 0,
+                          sinks: int = 0, scale: float | None = None, stream=None, workspace=None):
+    """Returns (o [total_q,H,D], lse [H,total_q]) of chunks of new tokens over a paged cache (see fa_fwd_paged); window
+    0: every key up to the query's own. Rows that belong to no chunk are not initialised."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return flash_attention_paged(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, max_seqlen_q, window,
+                                         sinks, scale, workspace=workspace)
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [total_q,H,D] and pages [num_blocks,Hkv,block_size,D]")
+    Tq, H, D = q.shape
+    if workspace is None:
+        n = fa_fwd_paged_workspace_bytes(max_seqlen_q, H, k_cache.shape[1], D)
+        workspace = torch.empty(_words(n), dtype=torch.float32, device=q.device)
+    o, lse = torch.empty_like(q), torch.empty((H, Tq), dtype=torch.float32, device=q.device)
+    fa_fwd_paged(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, o, lse, workspace, max_seqlen_q, window, sinks,
+                 scale)
+    return o, lse
 
 
 def flash_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, keep: int, sinks: int = 0,

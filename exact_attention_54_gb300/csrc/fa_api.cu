@@ -87,6 +87,22 @@ bool encode_map(CUtensorMap *m, bool bf16, const void *base, uint64_t d0, uint64
     return r == CUDA_SUCCESS;
 }
 
+// 4-D map over packed queries [tokens, Hkv, group, D]: boxes of 64 columns, the
+// heads of a group and box_tokens tokens, which land as rows token * group + head.
+bool encode_map_grouped(CUtensorMap *m, bool bf16, const void *base, uint64_t D, uint64_t group, uint64_t Hkv,
+                        uint64_t tokens, uint32_t box_tokens) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[4] = {D, group, Hkv, tokens};
+    const cuuint64_t strides[3] = {D * 2, D * 2 * group, D * 2 * group * Hkv};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(group), 1, box_tokens};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+              const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 3-D map over an fp32 dQ accumulator with 32-column boxes and 128-byte
 // swizzle: the target of the backward pass's bulk reductions. Dense
 // [B*H][Sq][D]: dims {D, Sq, B*H}, boxes 32 x rows x 1; packed [T][H][D]:
@@ -1092,6 +1108,97 @@ fa_status_t fa_rope_kv_write(const void *q, const void *k, const void *v, void *
     const int sms = num_sms();
     if (p.err == nullptr || sms <= 0) return FA_ERR_CUDA;
     const cudaError_t e = fa::launch_rope(true, dtype == FA_BF16, p, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// Chunk attention's workspace: two parts per CTA (O, then m and l), and a record each.
+struct ChunkSpace {
+    int grid, part_rows;
+    size_t o_floats, ml_floats, bytes;
+};
+
+static ChunkSpace chunk_space(int max_seqlen_q, int H, int Hkv, int D) {
+    ChunkSpace c{};
+    const int sms = num_sms(), group = H / Hkv, tokens = 128 / group;
+    c.grid = sms > 0 ? sms : 152;
+    c.part_rows = max_seqlen_q > tokens ? 256 : max_seqlen_q * group;
+    const size_t rows = static_cast<size_t>(2) * c.grid * c.part_rows;
+    c.o_floats = rows * D;
+    c.ml_floats = (2 * rows + 3) / 4 * 4;
+    c.bytes = 4 * (c.o_floats + c.ml_floats + 4 * static_cast<size_t>(c.grid));
+    return c;
+}
+
+static bool chunk_ok(int max_seqlen_q, int H, int Hkv) {
+    return max_seqlen_q >= 1 && max_seqlen_q <= kMaxWindowLen && H >= 1 && Hkv >= 1 && H % Hkv == 0 && H / Hkv <= 128;
+}
+
+size_t fa_fwd_paged_workspace_bytes(int max_seqlen_q, int H, int Hkv, int D) {
+    if ((D != 64 && D != 128) || !chunk_ok(max_seqlen_q, H, Hkv)) return 0;
+    return chunk_space(max_seqlen_q, H, Hkv, D).bytes;
+}
+
+fa_status_t fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+                         const int32_t *cu_seqlens_q, const int32_t *seq_lens, void *o, float *lse, float *workspace,
+                         size_t workspace_bytes, int num_seqs, int total_q, int max_seqlen_q, int H, int Hkv, int D,
+                         int num_blocks, int block_size, int max_blocks_per_seq, int window, int sinks, float scale,
+                         fa_dtype_t dtype, void *stream) {
+    if (!q || !k_cache || !v_cache || !block_table || !cu_seqlens_q || !seq_lens || !o || !lse || !workspace)
+        return FA_ERR_NULL;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_DTYPE;
+    if (D != 64 && D != 128) return FA_ERR_HEADDIM;
+    int log2_bs = 0;
+    if (num_seqs < 1 || total_q < 1 || total_q > kMaxWindowLen || !chunk_ok(max_seqlen_q, H, Hkv) ||
+        static_cast<long long>(num_seqs) * H > INT_MAX || static_cast<long long>(total_q) * H > INT_MAX ||
+        !pages_ok(Hkv, num_blocks, block_size, max_blocks_per_seq, log2_bs) || window < 0 || sinks < 0)
+        return FA_ERR_SHAPE;
+    if (!scale_ok(scale)) return FA_ERR_SCALE;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(block_table) ||
+        !aligned4(cu_seqlens_q) || !aligned4(seq_lens) || !aligned16(o) || !aligned4(lse) || !aligned16(workspace))
+        return FA_ERR_ALIGN;
+    const ChunkSpace c = chunk_space(max_seqlen_q, H, Hkv, D);
+    if (workspace_bytes < c.bytes) return FA_ERR_WORKSPACE;
+
+    const bool bf16 = dtype == FA_BF16;
+    const int group = H / Hkv, tokens = 128 / group;
+    const uint64_t row = static_cast<uint64_t>(D) * 2, planes = static_cast<uint64_t>(num_blocks) * Hkv;
+    const uint32_t page_rows = block_size < 128 ? block_size : 128;
+    CUtensorMap maps[3];
+    if (!encode_map_grouped(&maps[0], bf16, q, D, group, Hkv, total_q, tokens) ||
+        !encode_map(&maps[1], bf16, k_cache, D, block_size, planes, row, row * block_size, page_rows, 1) ||
+        !encode_map(&maps[2], bf16, v_cache, D, block_size, planes, row, row * block_size, page_rows, 1))
+        return FA_ERR_CUDA;
+    fa::ChunkParams p{};
+    p.o = o;
+    p.lse = lse;
+    p.k = static_cast<const uint16_t *>(k_cache);
+    p.v = static_cast<const uint16_t *>(v_cache);
+    p.cu_q = cu_seqlens_q;
+    p.seq_lens = seq_lens;
+    p.block_table = block_table;
+    p.B = num_seqs;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.group = group;
+    p.total_q = total_q;
+    p.max_q = max_seqlen_q;
+    p.tile_tokens = tokens;
+    p.log2_bs = log2_bs;
+    p.num_blocks = num_blocks;
+    p.max_blocks = max_blocks_per_seq;
+    p.window = window < kMaxWindowLen ? window : kMaxWindowLen;
+    p.sinks = sinks < kMaxWindowLen ? sinks : kMaxWindowLen;
+    p.min_run = 6;
+    p.scale_log2 = scale * kLog2e;
+    p.o_part = workspace;
+    p.ml_part = reinterpret_cast<float2 *>(workspace + c.o_floats);
+    p.part_rows = c.part_rows;
+    p.records = reinterpret_cast<int4 *>(workspace + c.o_floats + c.ml_floats);
+    p.err = device_error_word();
+    p.timeout_ns = g_wait_limit_ns.load();
+    p.withhold = g_withhold.load();
+    if (p.err == nullptr || num_sms() <= 0) return FA_ERR_CUDA;
+    const cudaError_t e = fa::launch_fwd_paged(D, bf16, maps, p, c.grid, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

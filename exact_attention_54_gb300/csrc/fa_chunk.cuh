@@ -1,0 +1,951 @@
+// Attention of chunks of new tokens over a paged cache (fa_fwd_paged), tcgen05
+// with TMEM accumulators.
+//
+// Query t of a sequence's chunk is at position L - Lq + t of its L keys and sees
+// key j if j <= its position and (that is less than `window` away, or window is
+// 0, or j < sinks). The roles, barriers, TMEM columns and the online softmax are
+// those of the packed forward (fa_fwd_kernel.cuh); what differs:
+//
+// Rows. A query tile holds the group's query heads of consecutive tokens (row =
+// token * group + head of the group, floor(128 / group) tokens), so that few
+// tokens still fill a tile and a key head is read once for all of its query
+// heads. One 4-D TMA box brings it.
+//
+// Pages. A 128-key tile of K or V is brought page by page (a lane looks up and
+// loads one page; pages of 128 keys and more: the part of one). Keys that no
+// query of the chunk sees are zeros: whole pages of them are not looked up, a
+// box outside the tensor stands for them, and V's rows are cleared behind the
+// load. Pages of less than 8 rows do not fill a swizzle atom and go through
+// 16-byte asynchronous copies.
+//
+// Work. Lengths are on the device, so the kernel cuts the work itself: units
+// (sequence, key head, pair of query tiles), each as long as the key tiles it
+// visits and kStart, are laid end to end and cut into equal runs, one per CTA,
+// so that one long sequence or many ragged ones keep every SM busy to the end. A
+// unit that falls into several runs leaves its parts (m, l, O in fp32) in the
+// workspace, and a second launch joins them, row by row in the order of keys.
+#pragma once
+
+#include <climits>
+
+#include "fa_fwd_kernel.cuh"
+
+namespace fa {
+namespace chunk {
+
+// What a unit's start (its queries, first keys, and end) costs, in key tiles.
+constexpr int kStart = 2;
+constexpr int kPlanEntries = 4096;  // the plan's table: sums over a sequence, or over several if there are more
+constexpr int kSerialPairs = 16;    // a thread sums the units of a sequence with up to this many, a warp longer ones
+constexpr unsigned kFull = 0xffffffffu;
+
+// Sequence b's chunk: its rows in the packed queries, its keys.
+struct Seq {
+    int q0, Lq, L;
+};
+
+__device__ __forceinline__ Seq load_seq(const ChunkParams &p, int b) {
+    Seq s;
+    s.q0 = p.cu_q[b];
+    s.Lq = p.cu_q[b + 1] - s.q0;
+    s.L = min(max(p.seq_lens[b], 0), p.max_blocks << p.log2_bs);
+    return s;
+}
+
+__device__ __forceinline__ int pairs_of(const ChunkParams &p, const Seq &s) {
+    return (s.Lq + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
+}
+
+// Key tiles of a unit: its steps are tiles [0, ns), which hold sinks, then the
+// tiles from lo on; query tile t visits tiles [0, sink[t]) and [wlo[t], hi[t]).
+struct Tiles {
+    int tok[2], ntok[2];  // first token of each query tile (in the chunk), tokens
+    int ns, lo, steps;
+    int sink[2], wlo[2], hi[2];
+};
+
+__device__ __forceinline__ Tiles tiles_of(const ChunkParams &p, const Seq &s, int pair) {
+    Tiles k;
+    const int pos0 = s.L - s.Lq;
+    const int sink_tiles = p.window > 0 ? p.sinks / kBlockN + (p.sinks % kBlockN != 0) : 0;
+    int end = 0;
+    k.ns = 0;
+    k.lo = INT_MAX;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        k.tok[t] = (2 * pair + t) * p.tile_tokens;
+        k.ntok[t] = min(max(s.Lq - k.tok[t], 0), p.tile_tokens);
+        const int first = pos0 + k.tok[t], last = first + k.ntok[t] - 1;
+        k.hi[t] = k.ntok[t] > 0 && last >= 0 ? last / kBlockN + 1 : 0;
+        k.wlo[t] = p.window > 0 ? max(first - p.window + 1, 0) / kBlockN : 0;
+        k.sink[t] = min(sink_tiles, k.hi[t]);
+        if (k.hi[t] > 0) {
+            k.ns = max(k.ns, k.sink[t]);
+            k.lo = min(k.lo, k.wlo[t]);
+            end = max(end, k.hi[t]);
+        }
+    }
+    k.lo = max(min(k.lo, end), k.ns);
+    k.steps = k.ns + max(end - k.lo, 0);
+    return k;
+}
+
+__device__ __forceinline__ int tile_at(const Tiles &k, int j) { return j < k.ns ? j : j - k.ns + k.lo; }
+
+__device__ __forceinline__ bool visits(const Tiles &k, int t, int j) {
+    const int x = tile_at(k, j);
+    return x < k.hi[t] && (x < k.sink[t] || x >= k.wlo[t]);
+}
+
+// Steps of [s0, s1) that query tile t visits.
+__device__ __forceinline__ int visited(const Tiles &k, int t, int s0, int s1) {
+    auto both = [&](int a, int b) { return max(min(b, s1) - max(a, s0), 0); };
+    const int from = max(k.wlo[t], k.sink[t]);
+    return both(0, k.sink[t]) + both(from, min(k.hi[t], k.ns)) +
+           both(max(from, k.lo) - k.lo + k.ns, k.hi[t] - k.lo + k.ns);
+}
+
+// A CTA's run of the laid-out units, in shared memory.
+struct Run {
+    long long len;     // cost units, 0: no work
+    long long per;     // of every CTA but the last
+    int b, hk, pair;   // the unit it starts in,
+    int off;           // and where
+};
+
+// The parts of a CTA's run, in order; every role walks them for itself.
+struct Part {
+    int b, hk, pair;
+    Seq s;
+    Tiles k;
+    int s0, s1;   // steps
+    bool whole;   // the unit's only part
+    int slot;     // of the CTA's two in the workspace, else
+    int parts;    // first of several parts: their number, else 0
+};
+
+struct Walk {
+    const ChunkParams &p;
+    long long rem, per;
+    int b, hk, pair, off, pairs;
+    bool first = true;
+    Seq s;
+
+    __device__ __forceinline__ Walk(const ChunkParams &p_, const volatile Run *r) : p(p_) {
+        rem = r->len;
+        per = r->per;
+        b = r->b;
+        hk = r->hk;
+        pair = r->pair;
+        off = r->off;
+        pairs = 0;
+        if (rem > 0) {
+            s = load_seq(p, b);
+            pairs = pairs_of(p, s);
+        }
+    }
+    __device__ __forceinline__ bool next(Part &o) {
+        while (rem > 0) {
+            while (pairs == 0) {  // a sequence without queries
+                if (++b >= p.B) return false;
+                s = load_seq(p, b);
+                pairs = pairs_of(p, s);
+            }
+            o.b = b;
+            o.hk = hk;
+            o.pair = pair;
+            o.s = s;
+            o.k = tiles_of(p, s, pair);
+            const int n = o.k.steps + kStart;
+            const int take = static_cast<int>(min(rem, static_cast<long long>(n - off)));
+            o.s0 = max(off - kStart, 0);
+            o.s1 = max(off + take - kStart, 0);
+            o.whole = o.s0 == 0 && o.s1 == o.k.steps;
+            o.slot = first ? 0 : 1;
+            const int rest = n - off - take;
+            o.parts = o.s0 == 0 && o.s1 > 0 && rest > 0 ? 1 + static_cast<int>((rest + per - 1) / per) : 0;
+            const bool some = o.s1 > o.s0 || (o.k.steps == 0 && off == 0);
+            rem -= take;
+            first = false;
+            off = 0;
+            if (++pair == pairs) {
+                pair = 0;
+                if (++hk == p.Hkv) {
+                    hk = 0;
+                    pairs = 0;  // the next sequence is loaded when it is reached
+                }
+            }
+            if (some) return true;
+        }
+        return false;
+    }
+};
+
+// ------------------------------------------------------------------- plan --
+
+__device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+    return v;
+}
+
+// Cost of one key head of a sequence's units; the whole warp calls it.
+__device__ __forceinline__ unsigned long long seq_cost(const ChunkParams &p, const Seq &s, int pairs) {
+    unsigned long long c = 0;
+    for (int i = threadIdx.x % 32; i < pairs; i += 32) c += tiles_of(p, s, i).steps + kStart;
+    return warp_sum(c);
+}
+
+// This CTA's run into `run`; `prefix` is scratch of kPlanEntries + 1 sums. The
+// whole CTA calls it, and synchronises before it reads `run`.
+__device__ void plan(const ChunkParams &p, Run *run, unsigned long long *prefix) {
+    const int each = (p.B + kPlanEntries - 1) / kPlanEntries, entries = (p.B + each - 1) / each;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    for (int i = threadIdx.x; i < entries; i += blockDim.x) prefix[i + 1] = 0;
+    __syncthreads();
+    bool bad = false;
+    for (int b0 = warp * 32; b0 < p.B; b0 += blockDim.x) {
+        const int b = b0 + lane;
+        Seq s{0, 0, 0};
+        int pairs = 0;
+        unsigned long long c = 0;
+        if (b < p.B) {
+            const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
+            if (q0 < 0 || q1 < q0 || q1 > p.total_q || q1 - q0 > p.max_q) {
+                bad = true;
+            } else {
+                s = load_seq(p, b);
+                pairs = pairs_of(p, s);
+                if (pairs <= kSerialPairs)
+                    for (int i = 0; i < pairs; ++i) c += tiles_of(p, s, i).steps + kStart;
+            }
+        }
+        unsigned more = __ballot_sync(kFull, pairs > kSerialPairs);
+        while (more != 0) {
+            const int l = __ffs(more) - 1;
+            more &= more - 1;
+            const Seq x{0, __shfl_sync(kFull, s.Lq, l), __shfl_sync(kFull, s.L, l)};
+            const unsigned long long sum = seq_cost(p, x, __shfl_sync(kFull, pairs, l));
+            if (lane == l) c = sum;
+        }
+        if (c > 0) atomicAdd(&prefix[b / each + 1], c);
+    }
+    bad = __syncthreads_or(bad) != 0;
+    if (bad && threadIdx.x == 0) {
+        atomicExch(p.err, kDeviceErrSeqLens);
+        run->len = 0;
+    }
+    if (bad || warp != 0) return;
+    // prefix sums of the entries; then this CTA's place among them
+    const int mine = (entries + 31) / 32, e0 = lane * mine;
+    unsigned long long sum = 0;
+    for (int e = e0; e < min(e0 + mine, entries); ++e) sum += prefix[e + 1];
+    unsigned long long before = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const unsigned long long v = __shfl_up_sync(kFull, before, off);
+        if (lane >= off) before += v;
+    }
+    const long long total = static_cast<long long>(__shfl_sync(kFull, before, 31)) * p.Hkv;
+    before -= sum;
+    for (int e = e0; e < min(e0 + mine, entries); ++e) prefix[e + 1] = before += prefix[e + 1];
+    if (lane == 0) prefix[0] = 0;
+    __syncwarp();
+    const long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(p.min_run));
+    const long long at = min(static_cast<long long>(blockIdx.x) * per, total);
+    const long long len = min(per, total - at);
+    Run r{len, per, 0, 0, 0, 0};
+    if (len > 0) {
+        int lo = 0, hi = entries;  // the last entry that starts at or before `at`, and is not empty
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (static_cast<long long>(prefix[mid]) * p.Hkv <= at) lo = mid;
+            else hi = mid;
+        }
+        unsigned long long x = static_cast<unsigned long long>(at) - prefix[lo] * p.Hkv;
+        Seq s{};
+        int pairs = 0;
+        unsigned long long c = 0;
+        for (r.b = lo * each;; ++r.b) {
+            s = load_seq(p, r.b);
+            pairs = pairs_of(p, s);
+            c = seq_cost(p, s, pairs);
+            if (x < c * p.Hkv || r.b + 1 >= p.B) break;
+            x -= c * p.Hkv;
+        }
+        r.hk = static_cast<int>(x / c);
+        x -= c * r.hk;
+        // the pair whose share holds x
+        for (int i0 = 0; i0 < pairs; i0 += 32) {
+            const unsigned long long v = i0 + lane < pairs ? tiles_of(p, s, i0 + lane).steps + kStart : 0;
+            unsigned long long upto = v;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const unsigned long long y = __shfl_up_sync(kFull, upto, off);
+                if (lane >= off) upto += y;
+            }
+            const unsigned here = __ballot_sync(kFull, x < upto);
+            if (here != 0) {
+                const int l = __ffs(here) - 1;
+                r.pair = i0 + l;
+                r.off = static_cast<int>(x - __shfl_sync(kFull, upto - v, l));
+                break;
+            }
+            x -= __shfl_sync(kFull, upto, 31);
+        }
+    }
+    if (lane == 0) *run = r;
+}
+
+// ------------------------------------------------------------------ loads --
+
+// Keys that no query of the chunk sees: from L on, and [dead0, dead1).
+struct Dead {
+    int dead0, dead1;
+    __device__ __forceinline__ Dead(const ChunkParams &p, const Seq &s) {
+        dead0 = p.sinks;
+        dead1 = p.window > 0 ? s.L - s.Lq - p.window + 1 : 0;
+    }
+    // all of [a, b)
+    __device__ __forceinline__ bool all(int a, int b) const { return a >= dead0 && b <= dead1; }
+    // any of [a, b)
+    __device__ __forceinline__ bool any(int a, int b) const { return max(a, dead0) < min(b, dead1); }
+};
+
+// The pages of a key tile, one per lane (of the first kBlockN / span).
+struct Pages {
+    int span_log2;  // rows of a page within a tile
+    int count;
+
+    __device__ __forceinline__ Pages(const ChunkParams &p) {
+        span_log2 = min(p.log2_bs, 7);
+        count = kBlockN >> span_log2;
+    }
+    // This lane's page of the tile from key k0 on: its number, -1 where no key
+    // of it is seen (not looked up).
+    __device__ __forceinline__ int look_up(const ChunkParams &p, const Part &u, const Dead &d, int k0) const {
+        const int lane = threadIdx.x % 32, key = k0 + (lane << span_log2);
+        if (lane >= count || key >= u.s.L || d.all(key, min(key + (1 << span_log2), u.s.L))) return -1;
+        return p.block_table[static_cast<size_t>(u.b) * p.max_blocks + (key >> p.log2_bs)];
+    }
+    // Its rows into the tile at `dst`, every lane its page; a page number that
+    // does not exist is reported and stands for zeros, as do keys nobody sees.
+    template <int D>
+    __device__ __forceinline__ void load(const ChunkParams &p, const Part &u, const Dead &d, int k0, int page,
+                                         const CUtensorMap *tm, uint32_t dst, uint32_t bar) const {
+        using S = FwdShape<D>;
+        const int lane = threadIdx.x % 32, key = k0 + (lane << span_log2);
+        if (lane >= count) return;
+        const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_blocks);
+        if (!there && key < u.s.L && !d.all(key, min(key + (1 << span_log2), u.s.L)))
+            atomicExch(p.err, kDeviceErrBadIndex);
+        const int z = there ? page * p.Hkv + u.hk : p.num_blocks * p.Hkv;
+        const int y = key & ((1 << p.log2_bs) - 1);
+#pragma unroll
+        for (int c = 0; c < S::kColBlocks; ++c)
+            ptx::tma_load_3d(dst + c * S::kBlockBytes + ((lane << span_log2) << 7), tm, bar, c * 64, y, z);
+    }
+};
+
+// A tile from pages of less than 8 rows, by the whole warp: 16-byte pieces into
+// the places that the swizzle gives them, zeros for keys nobody sees. Returns
+// with the pieces landed and visible to the tensor core.
+template <int D>
+__device__ __forceinline__ void copy_small_pages(const ChunkParams &p, const Part &u, const Dead &d, int k0,
+                                                 const uint16_t *cache, uint32_t dst) {
+    using S = FwdShape<D>;
+    constexpr int kPieces = D / 8, kRows = 32 / kPieces;
+    const int lane = threadIdx.x % 32, piece = lane % kPieces;
+#pragma unroll 4
+    for (int row = lane / kPieces; row < kBlockN; row += kRows) {
+        const int key = k0 + row;
+        const uint16_t *src = cache;
+        uint32_t bytes = 0;
+        if (key < u.s.L && !d.all(key, key + 1)) {
+            const int page = p.block_table[static_cast<size_t>(u.b) * p.max_blocks + (key >> p.log2_bs)];
+            if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_blocks)) {
+                src += (((static_cast<long long>(page) * p.Hkv + u.hk) << p.log2_bs) + (key & ((1 << p.log2_bs) - 1))) *
+                           D + piece * 8;
+                bytes = 16;
+            } else {
+                atomicExch(p.err, kDeviceErrBadIndex);
+            }
+        }
+        ptx::copy_async16(dst + (piece / 8) * S::kBlockBytes + row * 128 + (((piece % 8) ^ (row % 8)) << 4), src, bytes);
+    }
+    ptx::copy_async_wait_all();
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// ------------------------------------------------------------------ roles --
+
+template <int D>
+__device__ void producer_qk(const CUtensorMap *tq, const CUtensorMap *tk, const ChunkParams &p, uint32_t sbase,
+                            const volatile Run *run, volatile int *abort_flag) {
+    using S = FwdShape<D>;
+    const uint32_t bars = sbase + S::kOffBar;
+    auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
+    const bool leader = ptx::elect_one();
+    const uint64_t stream_pol = ptx::l2_policy_evict_first();
+    const Pages pages(p);
+    const uint32_t tile_q = static_cast<uint32_t>(p.tile_tokens * p.group * 128 * S::kColBlocks);
+    uint32_t it = 0, wi = 0, nq = 0;  // K tiles issued, parts loaded, Q loads issued
+    bool ok = true;
+    Walk walk(p, run);
+    Part u;
+    while (ok && walk.next(u)) {
+        if (u.s1 == u.s0) continue;
+        const Dead dead(p, u.s);
+        auto load_q = [&]() -> bool {
+            if (nq > 0 &&
+                !ptx::warp_all(ptx::bar_wait(bar(S::kQEmpty), (nq - 1) & 1, abort_flag, p.timeout_ns)))
+                return false;
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) bytes += visited(u.k, t, u.s0, u.s1) > 0 ? tile_q : 0;
+            if (leader) ptx::bar_arrive_expect_tx(bar(S::kQFull), bytes);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (visited(u.k, t, u.s0, u.s1) == 0 || !leader) continue;
+#pragma unroll
+                for (int c = 0; c < S::kColBlocks; ++c)
+                    ptx::tma_load_4d_hint(sbase + S::kOffQ + t * S::kTileBytes + c * S::kBlockBytes, tq, bar(S::kQFull),
+                                          c * 64, 0, u.hk, u.s.q0 + u.k.tok[t], stream_pol);
+            }
+            ++nq;
+            return true;
+        };
+        if (wi == 0 && !(ok = load_q())) break;
+        int page = pages.look_up(p, u, dead, tile_at(u.k, u.s0) * kBlockN);
+        for (int j = u.s0; j < u.s1; ++j, ++it) {
+            // the first products need Q and the first K tile only (see the packed forward)
+            if (wi == 0 && j == u.s0 + 1 &&
+                !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kQFull), 0, abort_flag, p.timeout_ns))))
+                break;
+            const uint32_t stage = it % S::kKStages;
+            const int k0 = tile_at(u.k, j) * kBlockN, here = page;
+            if (j + 1 < u.s1) page = pages.look_up(p, u, dead, tile_at(u.k, j + 1) * kBlockN);  // ahead of its use
+            if (it >= S::kKStages &&
+                !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kKEmpty + stage), ((it / S::kKStages) - 1) & 1, abort_flag,
+                                     p.timeout_ns))))
+                break;
+            const uint32_t dst = sbase + S::kOffK + stage * S::kTileBytes;
+            if (p.log2_bs < 3) {
+                copy_small_pages<D>(p, u, dead, k0, p.k, dst);
+                if (leader) ptx::bar_arrive(bar(S::kKFull + stage));
+            } else {
+                if (leader) ptx::bar_arrive_expect_tx(bar(S::kKFull + stage), S::kTileBytes);
+                __syncwarp();
+                pages.load<D>(p, u, dead, k0, here, tk, dst, bar(S::kKFull + stage));
+                __syncwarp();
+            }
+            if (wi > 0 && j == u.s0 && !(ok = load_q())) break;
+        }
+        if (!ok) break;
+        ++wi;
+    }
+    // Never leave with copies in flight (bounded, even after an abort).
+    for (uint32_t s = 0; s < S::kKStages && s < it; ++s) {
+        const uint32_t last = (it - 1) - ((it - 1 - s) % S::kKStages);
+        ptx::bar_wait(bar(S::kKFull + s), (last / S::kKStages) & 1, nullptr, p.timeout_ns);
+    }
+    if (nq > 0) ptx::bar_wait(bar(S::kQFull), (nq - 1) & 1, nullptr, p.timeout_ns);
+}
+
+template <int D>
+__device__ void producer_v(const CUtensorMap *tv, const ChunkParams &p, uint32_t sbase, const volatile Run *run,
+                           volatile int *abort_flag) {
+    using S = FwdShape<D>;
+    const uint32_t bars = sbase + S::kOffBar;
+    auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
+    const bool leader = ptx::elect_one();
+    const Pages pages(p);
+    uint32_t it = 0;
+    uint32_t cuts = 0, cut_done = 0;  // tiles with rows to clear: loaded, landed
+    bool ok = true;
+    Walk walk(p, run);
+    Part u;
+    while (ok && walk.next(u)) {
+        if (u.s1 == u.s0) continue;
+        const Dead dead(p, u.s);
+        int page = pages.look_up(p, u, dead, tile_at(u.k, u.s0) * kBlockN);
+        for (int j = u.s0; j < u.s1; ++j, ++it) {
+            if (it == 1 && !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kFirstQ), 0, abort_flag, p.timeout_ns)))) break;
+            const uint32_t stage = it % S::kVStages;
+            const int k0 = tile_at(u.k, j) * kBlockN, here = page;
+            if (j + 1 < u.s1) page = pages.look_up(p, u, dead, tile_at(u.k, j + 1) * kBlockN);
+            if (it >= S::kVStages &&
+                !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kVEmpty + stage), ((it / S::kVStages) - 1) & 1, abort_flag,
+                                     p.timeout_ns))))
+                break;
+            const uint32_t dst = sbase + S::kOffV + stage * S::kTileBytes, full = bar(S::kVFull + stage);
+            if (withheld(p.withhold, it)) continue;
+            if (p.log2_bs < 3) {
+                copy_small_pages<D>(p, u, dead, k0, p.v, dst);
+                if (leader) ptx::bar_arrive(full);
+                continue;
+            }
+            // Rows of a page that nobody sees may hold anything. Their weights
+            // are zero, but 0 x NaN is not, so they are cleared before the tile
+            // is handed on.
+            const int end = u.s.L - k0;
+            const bool cut = end < kBlockN || dead.any(k0, k0 + kBlockN);
+            const uint32_t lands = cut ? bar(S::kVCut) : full;
+            if (leader) ptx::bar_arrive_expect_tx(lands, S::kTileBytes);
+            __syncwarp();
+            pages.load<D>(p, u, dead, k0, here, tv, dst, lands);
+            __syncwarp();
+            if (cut) {
+                if (!(ok = ptx::warp_all(ptx::bar_wait(lands, cuts++ & 1, abort_flag, p.timeout_ns)))) break;
+                ++cut_done;
+                if (end < kBlockN) ptx::zero_rows(dst, S::kColBlocks, kBlockN, end, kBlockN);
+                const int z0 = max(dead.dead0 - k0, 0), z1 = min(dead.dead1 - k0, kBlockN);
+                if (z0 < z1) ptx::zero_rows(dst, S::kColBlocks, kBlockN, z0, z1);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (leader) ptx::bar_arrive(full);
+            }
+        }
+    }
+    if (cuts > cut_done) ptx::bar_wait(bar(S::kVCut), (cuts - 1) & 1, nullptr, p.timeout_ns);
+    for (uint32_t s = 0; s < S::kVStages && s < it; ++s) {
+        const uint32_t last = (it - 1) - ((it - 1 - s) % S::kVStages);
+        ptx::bar_wait(bar(S::kVFull + s), (last / S::kVStages) & 1, nullptr, p.timeout_ns);
+    }
+}
+
+template <int D, bool BF16>
+__device__ void mma(const ChunkParams &p, uint32_t sbase, uint32_t tmem, const volatile Run *run,
+                    volatile int *abort_flag) {
+    using S = FwdShape<D>;
+    constexpr uint32_t kIdescQK = ptx::idesc_f16(BF16, kBlockM, kBlockN, false);
+    constexpr uint32_t kIdescPV = ptx::idesc_f16(BF16, kBlockM, D, true);
+    const uint32_t bars = sbase + S::kOffBar;
+    auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
+    const bool leader = ptx::elect_one();
+    const uint64_t dq0 = ptx::smem_desc_sw128(sbase + S::kOffQ, 16, 1024);
+    const uint64_t dk0 = ptx::smem_desc_sw128(sbase + S::kOffK, 16, 1024);
+    const uint64_t dv0 = ptx::smem_desc_sw128(sbase + S::kOffV, S::kBlockBytes, 1024);
+    constexpr uint64_t kTile16 = S::kTileBytes >> 4;
+
+    // products as in the packed forward
+    auto issue_qk = [&](int t, uint32_t stage) {
+        const uint64_t qd = dq0 + static_cast<uint64_t>(t) * kTile16, kd = dk0 + static_cast<uint64_t>(stage) * kTile16;
+        const uint32_t dst = tmem + S::kTmemS + t * 128;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            constexpr uint64_t kBlock16 = S::kBlockBytes >> 4;
+            const uint64_t off = (kk / 4) * kBlock16 + (kk % 4) * 2;
+            ptx::mma_ss(dst, qd + off, kd + off, kIdescQK, kk > 0);
+        }
+    };
+    auto issue_pv = [&](int t, uint32_t stage, bool accumulate, int half) {
+        const uint64_t vd = dv0 + static_cast<uint64_t>(stage) * kTile16;
+        const uint32_t dst = tmem + S::kTmemO + t * D, pa = tmem + S::kTmemS + t * 128;
+#pragma unroll
+        for (int k4 = 0; k4 < kBlockN / 32; ++k4) {
+            const int kk = half * (kBlockN / 32) + k4;
+            ptx::mma_ts(dst, pa + kk * 8, vd + kk * (2048 >> 4), kIdescPV, (accumulate || kk > 0) ? 1u : 0u);
+        }
+    };
+
+    uint32_t it = 0, wi = 0;   // K/V tiles consumed, parts consumed
+    uint32_t cnt[2] = {0, 0};  // PV steps issued per query tile
+    bool ok = true;
+    Walk walk(p, run);
+    Part u;
+    while (ok && walk.next(u)) {
+        const int n = u.s1 - u.s0;
+        if (n == 0) continue;
+        const int total[2] = {visited(u.k, 0, u.s0, u.s1), visited(u.k, 1, u.s0, u.s1)};
+        if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kQFull), wi & 1, abort_flag, p.timeout_ns)))) break;
+        if (wi == 0 && leader) ptx::bar_arrive(bar(S::kFirstQ));
+        {
+            const uint32_t ks = it % S::kKStages;
+            if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kKFull + ks), (it / S::kKStages) & 1, abort_flag, p.timeout_ns))))
+                break;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (!visits(u.k, t, u.s0)) continue;
+                if (leader) {
+                    issue_qk(t, ks);
+                    ptx::mma_commit(bar(S::kSFull + t));
+                }
+            }
+            if (leader) ptx::mma_commit(bar(S::kKEmpty + ks));
+            if (n == 1 && leader) ptx::mma_commit(bar(S::kQEmpty));
+        }
+        int done[2] = {0, 0};
+        for (int j = 0; j < n && ok; ++j) {
+            const uint32_t itj = it + j;
+            const uint32_t vs = itj % S::kVStages;
+            const uint32_t kn = (itj + 1) % S::kKStages;
+            bool v_ready = false, k_next_used = false;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (visits(u.k, t, u.s0 + j)) {
+                    if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kPFull + t), cnt[t] & 1, abort_flag, p.timeout_ns))))
+                        break;
+                    if (!v_ready) {
+                        if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kVFull + vs), (itj / S::kVStages) & 1, abort_flag,
+                                                 p.timeout_ns))))
+                            break;
+                        v_ready = true;
+                    }
+                    ptx::tc_fence_after();
+                    if (leader) issue_pv(t, vs, done[t] > 0, 0);
+                    if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kPFull2 + t), cnt[t] & 1, abort_flag, p.timeout_ns))))
+                        break;
+                    ptx::tc_fence_after();
+                    if (leader) {
+                        issue_pv(t, vs, true, 1);
+                        if (done[t] + 1 == total[t]) ptx::mma_commit(bar(S::kODone + t));
+                    }
+                    ++cnt[t];
+                    ++done[t];
+                }
+                if (j + 1 < n && visits(u.k, t, u.s0 + j + 1)) {
+                    if (!k_next_used) {
+                        if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kKFull + kn), ((itj + 1) / S::kKStages) & 1, abort_flag,
+                                                 p.timeout_ns))))
+                            break;
+                        k_next_used = true;
+                    }
+                    ptx::tc_fence_after();
+                    if (leader) {
+                        issue_qk(t, kn);
+                        ptx::mma_commit(bar(S::kSFull + t));
+                    }
+                }
+            }
+            if (!ok) break;
+            if (leader) {
+                ptx::mma_commit(bar(S::kVEmpty + vs));
+                if (k_next_used) ptx::mma_commit(bar(S::kKEmpty + kn));
+                if (j + 2 == n) ptx::mma_commit(bar(S::kQEmpty));
+            }
+        }
+        if (!ok) break;
+        it += n;
+        ++wi;
+    }
+    if (leader) ptx::mma_commit(bar(S::kTeardown));
+    __syncwarp();
+    ptx::bar_wait(bar(S::kTeardown), 0, nullptr, p.timeout_ns);
+}
+
+template <int D, bool BF16>
+__device__ void softmax(const ChunkParams &p, uint32_t sbase, uint32_t tmem, int t, int wq, int lane,
+                        const volatile Run *run, volatile int *abort_flag) {
+    using S = FwdShape<D>;
+    const uint32_t bars = sbase + S::kOffBar;
+    auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
+    const int row = wq * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_base + S::kTmemS + t * 128;
+    const uint32_t tO = tmem + lane_base + S::kTmemO + t * D;
+    const float scale_log2 = p.scale_log2;
+    const int token = row / p.group, head = row - token * p.group;  // within the tile, within the group
+    const bool in_tile = token < p.tile_tokens;
+    uint32_t cnt = 0, items = 0;
+    bool ok = true;
+    Walk walk(p, run);
+    Part u;
+    while (ok && walk.next(u)) {
+        if (u.k.ntok[t] == 0) continue;
+        const int first = u.s.L - u.s.Lq + u.k.tok[t];  // the tile's first position
+        const int pos = first + token, last = first + u.k.ntok[t] - 1;
+        const bool row_valid = in_tile && token < u.k.ntok[t];
+        float m_used = -CUDART_INF_F;
+        float l = 0.f;
+        int mine = 0;  // steps taken
+        for (int j = u.s0; j < u.s1; ++j) {
+            if (!visits(u.k, t, j)) continue;
+            ok = ptx::bar_wait(bar(S::kSFull + t), cnt & 1, abort_flag, p.timeout_ns);
+            if (!__all_sync(kFull, ok)) { ok = false; break; }
+            ptx::tc_fence_after();
+            // the row sees the columns c < lim, but with a window not those with sk <= c < wl
+            const int k0 = tile_at(u.k, j) * kBlockN;
+            const bool need_mask = k0 + kBlockN - 1 > first;
+            const bool need_lo = p.window > 0 && k0 + kBlockN > p.sinks && k0 <= last - p.window;
+            uint32_t s[4][32];
+            float mx4[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ptx::tmem_ld32_max(tS + 32 * c, s[c], mx4[c]);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                ptx::reg_fence(s[c]);
+                asm volatile("" : "+f"(mx4[c]));
+            }
+            if (need_mask || need_lo) {
+                // the columns c < x as bits of chunk b: its low x - 32 b
+                auto below = [](int x, int b) -> uint32_t {
+                    const int n = min(max(x - 32 * b, 0), 32);
+                    return static_cast<uint32_t>((1ull << n) - 1);
+                };
+                const int lim = pos + 1 - k0, wl = p.window > 0 ? pos - p.window + 1 - k0 : 0, sk = p.sinks - k0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const uint32_t seen = below(lim, b) & (below(sk, b) | ~below(wl, b));
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!(seen & (1u << i))) s[b][i] = 0xff800000u;  // -inf
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) mx4[c] = -CUDART_INF_F;
+#pragma unroll
+                for (int c = 0; c < kBlockN; c += 2)
+                    mx4[(c / 2) % 4] = ptx::fmax3(mx4[(c / 2) % 4], __uint_as_float(s[c / 32][c % 32]),
+                                                  __uint_as_float(s[(c + 1) / 32][(c + 1) % 32]));
+            }
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+            const float m_cand = mx * scale_log2;
+            const bool need = m_cand > m_used + kRescaleThreshold;
+            float alpha = 1.f;
+            if (need) {
+                alpha = ptx::ex2(m_used - m_cand);
+                m_used = m_cand;
+            }
+            l *= alpha;
+            const float m_sub = (m_used == -CUDART_INF_F) ? 0.f : m_used;
+            const uint64_t scale2 = ptx::pk2(scale_log2, scale_log2);
+            const uint64_t negm2 = ptx::pk2(-m_sub, -m_sub);
+            uint64_t sum2[2] = {ptx::pk2(0.f, 0.f), ptx::pk2(0.f, 0.f)};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int c = 64 * h + 2 * i;
+                    const uint64_t x = ptx::ffma2(ptx::pk2(__uint_as_float(s[c / 32][c % 32]),
+                                                           __uint_as_float(s[(c + 1) / 32][(c + 1) % 32])),
+                                                  scale2, negm2);
+                    float x0, x1;
+                    ptx::upk2(x, x0, x1);
+                    const float e0 = ptx::ex2(x0), e1 = ptx::ex2(x1);
+                    sum2[i % 2] = ptx::fadd2(sum2[i % 2], ptx::pk2(e0, e1));
+                    pk[i] = ptx::pack2<BF16>(e0, e1);
+                }
+                ptx::tmem_st32(tS + 32 * h, pk);
+                if (h == 0 && mine > 0 && __any_sync(kFull, need)) {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        ptx::tmem_ld32(tO + c * 32, o);
+                        ptx::tmem_ld_wait();
+                        ptx::reg_fence(o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        ptx::tmem_st32(tO + c * 32, o);
+                    }
+                }
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::bar_arrive(bar((h == 0 ? S::kPFull : S::kPFull2) + t));
+            }
+            {
+                float a0, a1, b0, b1;
+                ptx::upk2(sum2[0], a0, a1);
+                ptx::upk2(sum2[1], b0, b1);
+                l += (a0 + a1) + (b0 + b1);
+            }
+            ++cnt;
+            ++mine;
+        }
+        if (!ok) break;
+
+        if (mine > 0) {
+            ok = ptx::bar_wait(bar(S::kODone + t), items & 1, abort_flag, p.timeout_ns);
+            if (!__all_sync(kFull, ok)) { ok = false; break; }
+            ptx::tc_fence_after();
+            ++items;
+        }
+        uint32_t o[D / 32][32];
+        if (mine > 0) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) ptx::tmem_ld32(tO + c * 32, o[c]);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) ptx::reg_fence(o[c]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[c][i] = 0u;
+        }
+        if (!u.whole) {
+            // a part: m, l and O as they are
+            if (row_valid) {
+                const size_t at = static_cast<size_t>(2 * blockIdx.x + u.slot) * p.part_rows + t * kBlockM + row;
+                uint4 *dst = reinterpret_cast<uint4 *>(p.o_part + at * D);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        dst[8 * c + i / 4] = make_uint4(o[c][i], o[c][i + 1], o[c][i + 2], o[c][i + 3]);
+                p.ml_part[at] = make_float2(m_used, l);
+            }
+            continue;
+        }
+        // O / l in the input dtype, LSE = (m + log2 l) * ln 2
+        const float inv_l = l == 0.f ? 0.f : 1.f / l;
+        const float lse = l == 0.f ? -CUDART_INF_F : (m_used + __log2f(l)) * 0.69314718055994531f;
+        if (row_valid) {
+            const size_t tok = static_cast<size_t>(u.s.q0) + u.k.tok[t] + token, h = u.hk * p.group + head;
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o) + (tok * p.H + h) * D);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    auto two = [&](int x) {
+                        return ptx::pack2<BF16>(__uint_as_float(o[c][x]) * inv_l, __uint_as_float(o[c][x + 1]) * inv_l);
+                    };
+                    dst[4 * c + i / 8] = make_uint4(two(i), two(i + 2), two(i + 4), two(i + 6));
+                }
+            p.lse[h * p.total_q + tok] = lse;
+        }
+    }
+}
+
+// ----------------------------------------------------------------- kernels --
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    fa_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
+    using S = FwdShape<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = ptx::smem_addr(smem);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kOffMisc + 4);
+    Run *run = reinterpret_cast<Run *>(smem + S::kOffSched);
+    static_assert(sizeof(Run) <= kSchedInts * 4 && (kPlanEntries + 1) * 8 <= S::kOffBar, "scratch");
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    ptx::grid_launch_dependents();
+    if (threadIdx.x == 0) {
+        const uint32_t bars = sbase + S::kOffBar;
+        for (int i = 0; i < S::kNumBars; ++i) {
+            const bool p_full = i >= S::kPFull && i < S::kODone;
+            ptx::bar_init(bars + 8u * i, p_full ? kBlockM / 32 : 1u);
+        }
+        *abort_flag = 0;
+        ptx::bar_init_fence();
+        ptx::prefetch_tmap(&tm_q);
+        ptx::prefetch_tmap(&tm_k);
+        ptx::prefetch_tmap(&tm_v);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_addr(tmem_slot), S::kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    // the plan's scratch lies where the tiles go
+    plan(p, run, reinterpret_cast<unsigned long long *>(smem));
+    ptx::fence_proxy_async_smem();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        producer_qk<D>(&tm_q, &tm_k, p, sbase, run, abort_flag);
+    } else if (warp == 1) {
+        mma<D, BF16>(p, sbase, tmem, run, abort_flag);
+    } else if (warp == 2) {
+        producer_v<D>(&tm_v, p, sbase, run, abort_flag);
+    } else if (warp == 3) {
+        // the unit that starts here and ends in a later CTA's run, for the joining launch
+        Walk walk(p, run);
+        Part u;
+        int4 rec = make_int4(0, 0, 0, 0);
+        while (walk.next(u))
+            if (u.parts > 0) rec = make_int4(u.b, u.hk, u.pair, 2 * u.parts + u.slot);
+        if (lane == 0) p.records[blockIdx.x] = rec;
+    } else {
+        softmax<D, BF16>(p, sbase, tmem, (warp - 4) / 4, warp % 4, lane, run, abort_flag);
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, S::kTmemCols);
+    }
+    if (threadIdx.x == 0 && *abort_flag) atomicExch(p.err, kDeviceErrTimeout);
+}
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 32;  // of a unit, per CTA
+
+// Joins the parts of units that fell into several runs: CTA x for the unit that
+// started in run x, if any. D / 4 lanes take a row.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kJoinThreads) fa_chunk_join_kernel(const ChunkParams p) {
+    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+    ptx::grid_dependency_wait();
+    const int4 rec = p.records[blockIdx.x];
+    const int parts = min(rec.w / 2, static_cast<int>(gridDim.x - blockIdx.x)), slot = rec.w & 1;
+    if (parts == 0) return;
+    const Seq s = load_seq(p, rec.x);
+    const int d = threadIdx.x % kLanes * 4;
+    for (int i = threadIdx.x / kLanes; i < kJoinRows; i += kGroups) {
+        const int row = blockIdx.y * kJoinRows + i;
+        const int r = row % kBlockM, token = r / p.group, head = r - token * p.group;
+        const int tok = (2 * rec.z + row / kBlockM) * p.tile_tokens + token;
+        if (row >= p.part_rows || token >= p.tile_tokens || tok >= s.Lq) continue;
+        // part 0 is in the slot it was given, later ones in the first of their CTAs
+        auto at = [&](int x) { return static_cast<size_t>(2 * (blockIdx.x + x) + (x == 0 ? slot : 0)) * p.part_rows + row; };
+        float m = -CUDART_INF_F, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int x = 0; x < parts; ++x) {
+            const float2 ml = __ldcg(p.ml_part + at(x));
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.o_part + at(x) * D + d));
+            const float top = fmaxf(m, ml.x);
+            const float f = m == top ? 1.f : ptx::ex2(m - top), g = ml.x == -CUDART_INF_F ? 0.f : ptx::ex2(ml.x - top);
+            m = top;
+            l = fmaf(l, f, ml.y * g);
+            o.x = fmaf(o.x, f, v.x * g);
+            o.y = fmaf(o.y, f, v.y * g);
+            o.z = fmaf(o.z, f, v.z * g);
+            o.w = fmaf(o.w, f, v.w * g);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const size_t t = static_cast<size_t>(s.q0) + tok, h = rec.y * p.group + head;
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + (t * p.H + h) * D + d) =
+            make_uint2(ptx::pack2<BF16>(o.x * inv, o.y * inv), ptx::pack2<BF16>(o.z * inv, o.w * inv));
+        if (d == 0)
+            p.lse[h * p.total_q + t] = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
+    }
+}
+
+template <int D, bool BF16>
+cudaError_t launch_t(const CUtensorMap *maps, const ChunkParams &p, int grid, cudaStream_t st) {
+    static std::atomic<unsigned long long> done{0};
+    auto kern = fa_chunk_kernel<D, BF16>;
+    constexpr int kSmem = FwdShape<D>::kSmemBytes;
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), kSmem, done);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, kFwdThreads, kSmem, st>>>(maps[0], maps[1], maps[2], p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), static_cast<unsigned>((p.part_rows + kJoinRows - 1) / kJoinRows));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fa_chunk_join_kernel<D, BF16>, p);
+}
+
+}  // namespace chunk
+}  // namespace fa

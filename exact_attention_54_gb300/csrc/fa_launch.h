@@ -279,4 +279,32 @@ struct EvictParams {
 
 cudaError_t launch_kv_evict(int D, EvictParams p, cudaStream_t stream);
 
+// Parameters of the attention of chunks over a paged cache.
+struct ChunkParams {
+    void *o;                    // [total_q, H, D]
+    float *lse;                 // [H, total_q]
+    const uint16_t *k, *v;      // pages [num_blocks, Hkv, block_size, D]
+    const int *cu_q;            // [B + 1]
+    const int *seq_lens;        // [B]
+    const int *block_table;     // [B, max_blocks]
+    int B, H, Hkv, group, total_q, max_q;
+    int tile_tokens;            // tokens of a query tile: 128 / group
+    int log2_bs, num_blocks, max_blocks;
+    int window, sinks;          // window 0: every key up to the query's own
+    int min_run;                // least work of a CTA, in key tiles
+    float scale_log2;
+    float *o_part;              // [2 grid][part_rows][D], unnormalised parts of units
+    float2 *ml_part;            // [2 grid][part_rows], their (m, l)
+    int part_rows;              // rows of a unit
+    int4 *records;              // [grid], units to be joined
+    int *err;                   // device error word
+    unsigned long long timeout_ns;
+    int withhold;               // test support (see FwdParams)
+};
+
+// maps: Q {D, group, Hkv, tokens}, boxes 64 x group x 1 x tile_tokens; K and V
+// {D, block_size, num_blocks * Hkv}, boxes of 64 columns and a page's rows (at most 128).
+cudaError_t launch_fwd_paged(int D, bool bf16, const CUtensorMap *maps, const ChunkParams &p, int grid,
+                             cudaStream_t stream);
+
 }  // namespace fa

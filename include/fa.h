@@ -617,6 +617,59 @@ FA_API fa_status_t fa_rope_kv_write(const void *q, const void *k, const void *v,
                                     fa_dtype_t dtype, void *stream);
 
 /*
+ * fa_fwd_paged_workspace_bytes - bytes of workspace fa_fwd_paged needs on the
+ * current GPU (two fp32 parts of up to 256 rows of queries for each SM: 40 MB
+ * at D = 128, 2.5 MB where a chunk is 16 rows); 0 for an invalid shape.
+ */
+FA_API size_t fa_fwd_paged_workspace_bytes(int max_seqlen_q, int H, int Hkv, int D);
+
+/*
+ * fa_fwd_paged - attention of a chunk of new tokens of each sequence over a
+ * paged cache that holds their keys already: a prompt's next piece, drafted
+ * tokens, or a serving batch of both and single tokens.
+ *
+ * The last query of a sequence is at its last key: query t of Lq is at position
+ * p = L - Lq + t of L = seq_lens[b] keys, and sees key j if j <= p and
+ * (p - j < window, or window is 0, or j < sinks).
+ *
+ *   q, o         [total_q,H,D] fp16/bf16, the chunks packed; query head h reads
+ *                key head h / (H / Hkv); Hkv divides H, into groups of at most
+ *                128; D is 64 or 128
+ *   k_cache, v_cache [num_blocks,Hkv,block_size,D], same dtype, as
+ *                fa_rope_kv_write fills them
+ *   block_table  device int32 [num_seqs, max_blocks_per_seq]; entries whose
+ *                keys no query sees are never read
+ *   cu_seqlens_q device int32 [num_seqs + 1], 0 <= cu[0] <= cu[1] <= ... <=
+ *                total_q: sequence b's chunk is rows [cu[b], cu[b+1])
+ *   seq_lens     device int32 [num_seqs]: keys of each sequence, its chunk's
+ *                among them (clamped to [0, max_blocks_per_seq * block_size])
+ *   lse          [H,total_q] fp32 output
+ *   workspace    caller-owned, at least fa_fwd_paged_workspace_bytes bytes,
+ *                16-byte aligned; contents on entry and exit mean nothing. Calls
+ *                that share one must not overlap on the GPU.
+ *   max_seqlen_q >= every chunk's length; window, sinks >= 0
+ *   block_size   a power of two, 1..1024. Pages of 8 rows and more are loaded
+ *                as tiles; smaller ones are slower.
+ * A query that sees no key (more queries than keys) gets o = 0 and lse = -inf.
+ * Rows of o and lse that belong to no chunk are left as they were. Rows of a page
+ * that no query sees may hold anything, NaNs included; the others must be finite
+ * (a key tile is multiplied whole, hidden keys with zero weights).
+ * Offsets outside [0, total_q], decreasing ones, or a chunk longer than
+ * max_seqlen_q: nothing is computed and the next fa_check_device_error returns
+ * FA_ERR_DEVICE_SEQLENS. Page numbers outside [0, num_blocks) are not
+ * dereferenced: their rows count as zeros, and it returns FA_ERR_DEVICE_INDEX.
+ * The result is deterministic. Two launches.
+ * Errors: FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_HEADDIM, FA_ERR_DTYPE,
+ * FA_ERR_ALIGN, FA_ERR_SCALE, FA_ERR_WORKSPACE, FA_ERR_CUDA.
+ */
+FA_API fa_status_t fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+                                const int32_t *cu_seqlens_q, const int32_t *seq_lens, void *o, float *lse,
+                                float *workspace, size_t workspace_bytes, int num_seqs, int total_q,
+                                int max_seqlen_q, int H, int Hkv, int D, int num_blocks, int block_size,
+                                int max_blocks_per_seq, int window, int sinks, float scale, fa_dtype_t dtype,
+                                void *stream);
+
+/*
  * fa_kv_evict - the keys of least weight leave a paged 16-bit cache.
  *
  * Of a sequence of L = seq_lens[b] keys with L > keep, each key head keeps
