@@ -43,9 +43,10 @@ __all__ = ["FAError", "fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_decode
            "flash_decode", "flash_decode_paged", "fa_kv_write_q4", "fa_kv_read_q4", "fa_decode_paged_window",
            "fa_decode_paged_q4", "fa_decode_splits", "KVCacheQ4", "kv_cache_q4", "flash_kv_write_q4",
            "flash_kv_read_q4", "flash_decode_paged_window", "flash_decode_paged_q4",
-           "fa_rope", "fa_rope_kv_write", "fa_fwd_paged", "fa_fwd_paged_workspace_bytes", "fa_kv_evict",
+           "fa_rope", "fa_rope_kv_write", "fa_fwd_paged", "fa_fwd_paged_workspace_bytes", "fa_kv_weights",
+           "fa_kv_evict",
            "rope_frequencies", "flash_rope", "flash_rope_bwd", "flash_rope_kv_write", "flash_attention_paged",
-           "flash_kv_evict",
+           "flash_kv_weights", "flash_kv_evict",
            "library_path", "load_library", "EXPORTED_SYMBOLS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -63,7 +64,7 @@ EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_decode_p
                     "fa_fwd_window", "fa_fwd_window_varlen", "fa_bwd_window", "fa_bwd_window_varlen",
                     "fa_bwd_window_workspace_bytes", "fa_bwd_window_varlen_workspace_bytes",
                     "fa_decode_paged_window", "fa_decode_paged_q4", "fa_rope", "fa_rope_kv_write", "fa_fwd_paged",
-                    "fa_fwd_paged_workspace_bytes", "fa_kv_evict")
+                    "fa_fwd_paged_workspace_bytes", "fa_kv_weights", "fa_kv_evict")
 
 
 class FAError(RuntimeError):
@@ -127,6 +128,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.fa_fwd_paged.argtypes = [vp] * 9 + [sz] + [i] * 11 + [f, i, vp]
         lib.fa_fwd_paged_workspace_bytes.argtypes = [i] * 4
         lib.fa_fwd_paged_workspace_bytes.restype = sz
+        lib.fa_kv_weights.argtypes = [vp] * 7 + [ll] * 2 + [i] * 11 + [f, i, vp]
         lib.fa_kv_evict.argtypes = [vp] * 9 + [i] * 11 + [vp]
         lib.fa_check_device_error.argtypes = [vp]
         lib.fa_status_string.argtypes = [i]
@@ -136,7 +138,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                      "fa_decode_paged_splitkv_fused", "fa_check_device_error", "fa_version", "fa_kv_write_q4",
                      "fa_fwd_window", "fa_fwd_window_varlen", "fa_bwd_window", "fa_bwd_window_varlen",
                      "fa_kv_read_q4", "fa_decode_splits", "fa_decode_paged_window", "fa_decode_paged_q4", "fa_rope",
-                     "fa_rope_kv_write", "fa_fwd_paged", "fa_kv_evict"):
+                     "fa_rope_kv_write", "fa_fwd_paged", "fa_kv_weights", "fa_kv_evict"):
             getattr(lib, name).restype = ctypes.c_int
         if path is None:
             _lib = lib
@@ -1015,6 +1017,33 @@ def fa_fwd_paged(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, o, ls
             block_table.shape[1], _int32(window), _int32(sinks), float(scale), code)
 
 
+def fa_kv_weights(q, lse, k_cache, block_table, cu_seqlens_q, seq_lens, weights, max_seqlen_q: int, window: int = 0,
+                  sinks: int = 0, scale: float | None = None, stream=None):
+    """Add to weights fp32 [num_seqs,Hkv,max_blocks*block_size] what the chunks' queries q [total_q,H,D] gave to each key
+    of pages k_cache [num_blocks,Hkv,block_size,D]; lse fp32 [H,total_q] of that attention, of any strides (the
+    transpose of a decode's [B,H]); the rest as fa_fwd_paged."""
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [total_q,H,D] and pages [num_blocks,Hkv,block_size,D]")
+    Tq, H, D = q.shape
+    num_blocks, Hkv, block_size, _ = k_cache.shape
+    n = cu_seqlens_q.numel() - 1
+    code = _dtype_code(q)
+    _expect("q", q, (Tq, H, D), q.dtype)
+    _expect("k_cache", k_cache, (num_blocks, Hkv, block_size, D), q.dtype)
+    if lse.dtype != torch.float32:
+        raise TypeError(f"lse must be {torch.float32}, got {lse.dtype}")
+    if lse.shape != (H, Tq):
+        raise ValueError(f"lse must have shape {(H, Tq)}, got {tuple(lse.shape)}")
+    _expect("cu_seqlens_q", cu_seqlens_q, (n + 1,), torch.int32)
+    _expect("seq_lens", seq_lens, (n,), torch.int32)
+    _expect("block_table", block_table, (n, block_table.shape[-1]), torch.int32)
+    _expect("weights", weights, (n, Hkv, block_table.shape[1] * block_size), torch.float32)
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    _launch("fa_kv_weights", stream, (q, lse, k_cache, block_table, cu_seqlens_q, seq_lens, weights), *lse.stride(), n, Tq,
+            _int32(max_seqlen_q), H, Hkv, D, num_blocks, block_size, block_table.shape[1], _int32(window), _int32(sinks),
+            float(scale), code)
+
+
 def fa_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, kept, new_lens, new_weights, sinks: int = 0,
                 recent: int = 0, stream=None):
     """Move the first ``sinks``, the last ``recent`` and the heaviest other keys of each sequence, kept.shape[2] in all,
@@ -1092,6 +1121,21 @@ def flash_attention_paged(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_le
     fa_fwd_paged(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, o, lse, workspace, max_seqlen_q, window, sinks,
                  scale)
     return o, lse
+
+
+def flash_kv_weights(q, lse, k_cache, block_table, cu_seqlens_q, seq_lens, max_seqlen_q: int, window: int = 0,
+                     sinks: int = 0, scale: float | None = None, weights=None, stream=None):
+    """Returns ``weights`` [num_seqs,Hkv,max_blocks*block_size] with what the chunks gave to each key added (see
+    fa_kv_weights); None: added to zeros."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return flash_kv_weights(q, lse, k_cache, block_table, cu_seqlens_q, seq_lens, max_seqlen_q, window, sinks,
+                                    scale, weights)
+    if weights is None:
+        weights = torch.zeros((block_table.shape[0], k_cache.shape[1], block_table.shape[-1] * k_cache.shape[2]),
+                              dtype=torch.float32, device=q.device)
+    fa_kv_weights(q, lse, k_cache, block_table, cu_seqlens_q, seq_lens, weights, max_seqlen_q, window, sinks, scale)
+    return weights
 
 
 def flash_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, keep: int, sinks: int = 0,

@@ -1133,6 +1133,49 @@ static bool chunk_ok(int max_seqlen_q, int H, int Hkv) {
     return max_seqlen_q >= 1 && max_seqlen_q <= kMaxWindowLen && H >= 1 && Hkv >= 1 && H % Hkv == 0 && H / Hkv <= 128;
 }
 
+static bool paged_ok(int num_seqs, int total_q, int max_seqlen_q, int H, int Hkv, int num_blocks, int block_size,
+                     int max_blocks, int window, int sinks, int &log2_bs) {
+    return num_seqs >= 1 && total_q >= 1 && total_q <= kMaxWindowLen && chunk_ok(max_seqlen_q, H, Hkv) &&
+           static_cast<long long>(num_seqs) * H <= INT_MAX && static_cast<long long>(total_q) * H <= INT_MAX &&
+           pages_ok(Hkv, num_blocks, block_size, max_blocks, log2_bs) && window >= 0 && sinks >= 0;
+}
+
+// What fa_fwd_paged and fa_kv_weights (v_cache NULL) share; maps: Q, K and V.
+static bool fill_paged(fa::PagedParams &p, CUtensorMap *maps, bool bf16, const void *q, const void *k_cache,
+                       const void *v_cache, const int32_t *block_table, const int32_t *cu_seqlens_q,
+                       const int32_t *seq_lens, int num_seqs, int total_q, int max_seqlen_q, int H, int Hkv, int D,
+                       int num_blocks, int block_size, int log2_bs, int max_blocks, int window, int sinks,
+                       float scale) {
+    p.k = static_cast<const uint16_t *>(k_cache);
+    p.v = static_cast<const uint16_t *>(v_cache);
+    p.cu_q = cu_seqlens_q;
+    p.seq_lens = seq_lens;
+    p.block_table = block_table;
+    p.B = num_seqs;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.group = H / Hkv;
+    p.total_q = total_q;
+    p.max_q = max_seqlen_q;
+    p.tile_tokens = max_seqlen_q < 128 / p.group ? max_seqlen_q : 128 / p.group;
+    p.log2_bs = log2_bs;
+    p.num_blocks = num_blocks;
+    p.max_blocks = max_blocks;
+    p.window = window < kMaxWindowLen ? window : kMaxWindowLen;
+    p.sinks = sinks < kMaxWindowLen ? sinks : kMaxWindowLen;
+    p.scale_log2 = scale * kLog2e;
+    p.err = device_error_word();
+    p.timeout_ns = g_wait_limit_ns.load();
+    p.withhold = g_withhold.load();
+    if (p.err == nullptr || num_sms() <= 0) return false;
+    const uint64_t row = static_cast<uint64_t>(D) * 2, planes = static_cast<uint64_t>(num_blocks) * Hkv;
+    const uint32_t page_rows = block_size < 128 ? block_size : 128;
+    return encode_map_grouped(&maps[0], bf16, q, D, p.group, Hkv, total_q, p.tile_tokens) &&
+           encode_map(&maps[1], bf16, k_cache, D, block_size, planes, row, row * block_size, page_rows, 1) &&
+           (v_cache == nullptr ||
+            encode_map(&maps[2], bf16, v_cache, D, block_size, planes, row, row * block_size, page_rows, 1));
+}
+
 size_t fa_fwd_paged_workspace_bytes(int max_seqlen_q, int H, int Hkv, int D) {
     if ((D != 64 && D != 128) || !chunk_ok(max_seqlen_q, H, Hkv)) return 0;
     return chunk_space(max_seqlen_q, H, Hkv, D).bytes;
@@ -1148,9 +1191,8 @@ fa_status_t fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache
     if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_DTYPE;
     if (D != 64 && D != 128) return FA_ERR_HEADDIM;
     int log2_bs = 0;
-    if (num_seqs < 1 || total_q < 1 || total_q > kMaxWindowLen || !chunk_ok(max_seqlen_q, H, Hkv) ||
-        static_cast<long long>(num_seqs) * H > INT_MAX || static_cast<long long>(total_q) * H > INT_MAX ||
-        !pages_ok(Hkv, num_blocks, block_size, max_blocks_per_seq, log2_bs) || window < 0 || sinks < 0)
+    if (!paged_ok(num_seqs, total_q, max_seqlen_q, H, Hkv, num_blocks, block_size, max_blocks_per_seq, window, sinks,
+                  log2_bs))
         return FA_ERR_SHAPE;
     if (!scale_ok(scale)) return FA_ERR_SCALE;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(block_table) ||
@@ -1160,45 +1202,51 @@ fa_status_t fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache
     if (workspace_bytes < c.bytes) return FA_ERR_WORKSPACE;
 
     const bool bf16 = dtype == FA_BF16;
-    const int group = H / Hkv, tokens = 128 / group;
-    const uint64_t row = static_cast<uint64_t>(D) * 2, planes = static_cast<uint64_t>(num_blocks) * Hkv;
-    const uint32_t page_rows = block_size < 128 ? block_size : 128;
     CUtensorMap maps[3];
-    if (!encode_map_grouped(&maps[0], bf16, q, D, group, Hkv, total_q, tokens) ||
-        !encode_map(&maps[1], bf16, k_cache, D, block_size, planes, row, row * block_size, page_rows, 1) ||
-        !encode_map(&maps[2], bf16, v_cache, D, block_size, planes, row, row * block_size, page_rows, 1))
-        return FA_ERR_CUDA;
     fa::ChunkParams p{};
+    if (!fill_paged(p, maps, bf16, q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, num_seqs, total_q,
+                    max_seqlen_q, H, Hkv, D, num_blocks, block_size, log2_bs, max_blocks_per_seq, window, sinks, scale))
+        return FA_ERR_CUDA;
     p.o = o;
     p.lse = lse;
-    p.k = static_cast<const uint16_t *>(k_cache);
-    p.v = static_cast<const uint16_t *>(v_cache);
-    p.cu_q = cu_seqlens_q;
-    p.seq_lens = seq_lens;
-    p.block_table = block_table;
-    p.B = num_seqs;
-    p.H = H;
-    p.Hkv = Hkv;
-    p.group = group;
-    p.total_q = total_q;
-    p.max_q = max_seqlen_q;
-    p.tile_tokens = tokens;
-    p.log2_bs = log2_bs;
-    p.num_blocks = num_blocks;
-    p.max_blocks = max_blocks_per_seq;
-    p.window = window < kMaxWindowLen ? window : kMaxWindowLen;
-    p.sinks = sinks < kMaxWindowLen ? sinks : kMaxWindowLen;
     p.min_run = 6;
-    p.scale_log2 = scale * kLog2e;
     p.o_part = workspace;
     p.ml_part = reinterpret_cast<float2 *>(workspace + c.o_floats);
     p.part_rows = c.part_rows;
     p.records = reinterpret_cast<int4 *>(workspace + c.o_floats + c.ml_floats);
-    p.err = device_error_word();
-    p.timeout_ns = g_wait_limit_ns.load();
-    p.withhold = g_withhold.load();
-    if (p.err == nullptr || num_sms() <= 0) return FA_ERR_CUDA;
     const cudaError_t e = fa::launch_fwd_paged(D, bf16, maps, p, c.grid, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status_t fa_kv_weights(const void *q, const float *lse, const void *k_cache, const int32_t *block_table,
+                          const int32_t *cu_seqlens_q, const int32_t *seq_lens, float *weights, int64_t lse_head,
+                          int64_t lse_token, int num_seqs, int total_q, int max_seqlen_q, int H, int Hkv, int D,
+                          int num_blocks, int block_size, int max_blocks_per_seq, int window, int sinks, float scale,
+                          fa_dtype_t dtype, void *stream) {
+    if (!q || !lse || !k_cache || !block_table || !cu_seqlens_q || !seq_lens || !weights) return FA_ERR_NULL;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_DTYPE;
+    if (D != 64 && D != 128) return FA_ERR_HEADDIM;
+    int log2_bs = 0;
+    if (!paged_ok(num_seqs, total_q, max_seqlen_q, H, Hkv, num_blocks, block_size, max_blocks_per_seq, window, sinks,
+                  log2_bs) ||
+        lse_head < 0 || lse_token < 0 || lse_head > (int64_t(1) << 40) || lse_token > (int64_t(1) << 30))
+        return FA_ERR_SHAPE;
+    if (!scale_ok(scale)) return FA_ERR_SCALE;
+    if (!aligned16(q) || !aligned4(lse) || !aligned16(k_cache) || !aligned4(block_table) || !aligned4(cu_seqlens_q) ||
+        !aligned4(seq_lens) || !aligned4(weights))
+        return FA_ERR_ALIGN;
+    const bool bf16 = dtype == FA_BF16;
+    CUtensorMap maps[3];
+    fa::WeightsParams p{};
+    if (!fill_paged(p, maps, bf16, q, k_cache, nullptr, block_table, cu_seqlens_q, seq_lens, num_seqs, total_q,
+                    max_seqlen_q, H, Hkv, D, num_blocks, block_size, log2_bs, max_blocks_per_seq, window, sinks, scale))
+        return FA_ERR_CUDA;
+    p.lse = lse;
+    p.lse_head = lse_head;
+    p.lse_token = lse_token;
+    p.weights = weights;
+    p.min_run = 1;
+    const cudaError_t e = fa::launch_kv_weights(D, bf16, maps, p, num_sms(), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

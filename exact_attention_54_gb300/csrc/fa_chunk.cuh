@@ -26,31 +26,15 @@
 // workspace, and a second launch joins them, row by row in the order of keys.
 #pragma once
 
-#include <climits>
-
-#include "fa_fwd_kernel.cuh"
+#include "fa_paged.cuh"
 
 namespace fa {
 namespace chunk {
 
+using namespace paged;
+
 // What a unit's start (its queries, first keys, and end) costs, in key tiles.
 constexpr int kStart = 2;
-constexpr int kPlanEntries = 4096;  // the plan's table: sums over a sequence, or over several if there are more
-constexpr int kSerialPairs = 16;    // a thread sums the units of a sequence with up to this many, a warp longer ones
-constexpr unsigned kFull = 0xffffffffu;
-
-// Sequence b's chunk: its rows in the packed queries, its keys.
-struct Seq {
-    int q0, Lq, L;
-};
-
-__device__ __forceinline__ Seq load_seq(const ChunkParams &p, int b) {
-    Seq s;
-    s.q0 = p.cu_q[b];
-    s.Lq = p.cu_q[b + 1] - s.q0;
-    s.L = min(max(p.seq_lens[b], 0), p.max_blocks << p.log2_bs);
-    return s;
-}
 
 __device__ __forceinline__ int pairs_of(const ChunkParams &p, const Seq &s) {
     return (s.Lq + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
@@ -105,12 +89,11 @@ __device__ __forceinline__ int visited(const Tiles &k, int t, int s0, int s1) {
            both(max(from, k.lo) - k.lo + k.ns, k.hi[t] - k.lo + k.ns);
 }
 
-// A CTA's run of the laid-out units, in shared memory.
-struct Run {
-    long long len;     // cost units, 0: no work
-    long long per;     // of every CTA but the last
-    int b, hk, pair;   // the unit it starts in,
-    int off;           // and where
+// What the plan lays out: pairs of query tiles.
+struct Units {
+    const ChunkParams &p;
+    __device__ __forceinline__ int count(const Seq &s) const { return pairs_of(p, s); }
+    __device__ __forceinline__ int cost(const Seq &s, int i) const { return tiles_of(p, s, i).steps + kStart; }
 };
 
 // The parts of a CTA's run, in order; every role walks them for itself.
@@ -136,7 +119,7 @@ struct Walk {
         per = r->per;
         b = r->b;
         hk = r->hk;
-        pair = r->pair;
+        pair = r->unit;
         off = r->off;
         pairs = 0;
         if (rem > 0) {
@@ -181,203 +164,6 @@ struct Walk {
     }
 };
 
-// ------------------------------------------------------------------- plan --
-
-__device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
-    return v;
-}
-
-// Cost of one key head of a sequence's units; the whole warp calls it.
-__device__ __forceinline__ unsigned long long seq_cost(const ChunkParams &p, const Seq &s, int pairs) {
-    unsigned long long c = 0;
-    for (int i = threadIdx.x % 32; i < pairs; i += 32) c += tiles_of(p, s, i).steps + kStart;
-    return warp_sum(c);
-}
-
-// This CTA's run into `run`; `prefix` is scratch of kPlanEntries + 1 sums. The
-// whole CTA calls it, and synchronises before it reads `run`.
-__device__ void plan(const ChunkParams &p, Run *run, unsigned long long *prefix) {
-    const int each = (p.B + kPlanEntries - 1) / kPlanEntries, entries = (p.B + each - 1) / each;
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    for (int i = threadIdx.x; i < entries; i += blockDim.x) prefix[i + 1] = 0;
-    __syncthreads();
-    bool bad = false;
-    for (int b0 = warp * 32; b0 < p.B; b0 += blockDim.x) {
-        const int b = b0 + lane;
-        Seq s{0, 0, 0};
-        int pairs = 0;
-        unsigned long long c = 0;
-        if (b < p.B) {
-            const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
-            if (q0 < 0 || q1 < q0 || q1 > p.total_q || q1 - q0 > p.max_q) {
-                bad = true;
-            } else {
-                s = load_seq(p, b);
-                pairs = pairs_of(p, s);
-                if (pairs <= kSerialPairs)
-                    for (int i = 0; i < pairs; ++i) c += tiles_of(p, s, i).steps + kStart;
-            }
-        }
-        unsigned more = __ballot_sync(kFull, pairs > kSerialPairs);
-        while (more != 0) {
-            const int l = __ffs(more) - 1;
-            more &= more - 1;
-            const Seq x{0, __shfl_sync(kFull, s.Lq, l), __shfl_sync(kFull, s.L, l)};
-            const unsigned long long sum = seq_cost(p, x, __shfl_sync(kFull, pairs, l));
-            if (lane == l) c = sum;
-        }
-        if (c > 0) atomicAdd(&prefix[b / each + 1], c);
-    }
-    bad = __syncthreads_or(bad) != 0;
-    if (bad && threadIdx.x == 0) {
-        atomicExch(p.err, kDeviceErrSeqLens);
-        run->len = 0;
-    }
-    if (bad || warp != 0) return;
-    // prefix sums of the entries; then this CTA's place among them
-    const int mine = (entries + 31) / 32, e0 = lane * mine;
-    unsigned long long sum = 0;
-    for (int e = e0; e < min(e0 + mine, entries); ++e) sum += prefix[e + 1];
-    unsigned long long before = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const unsigned long long v = __shfl_up_sync(kFull, before, off);
-        if (lane >= off) before += v;
-    }
-    const long long total = static_cast<long long>(__shfl_sync(kFull, before, 31)) * p.Hkv;
-    before -= sum;
-    for (int e = e0; e < min(e0 + mine, entries); ++e) prefix[e + 1] = before += prefix[e + 1];
-    if (lane == 0) prefix[0] = 0;
-    __syncwarp();
-    const long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(p.min_run));
-    const long long at = min(static_cast<long long>(blockIdx.x) * per, total);
-    const long long len = min(per, total - at);
-    Run r{len, per, 0, 0, 0, 0};
-    if (len > 0) {
-        int lo = 0, hi = entries;  // the last entry that starts at or before `at`, and is not empty
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (static_cast<long long>(prefix[mid]) * p.Hkv <= at) lo = mid;
-            else hi = mid;
-        }
-        unsigned long long x = static_cast<unsigned long long>(at) - prefix[lo] * p.Hkv;
-        Seq s{};
-        int pairs = 0;
-        unsigned long long c = 0;
-        for (r.b = lo * each;; ++r.b) {
-            s = load_seq(p, r.b);
-            pairs = pairs_of(p, s);
-            c = seq_cost(p, s, pairs);
-            if (x < c * p.Hkv || r.b + 1 >= p.B) break;
-            x -= c * p.Hkv;
-        }
-        r.hk = static_cast<int>(x / c);
-        x -= c * r.hk;
-        // the pair whose share holds x
-        for (int i0 = 0; i0 < pairs; i0 += 32) {
-            const unsigned long long v = i0 + lane < pairs ? tiles_of(p, s, i0 + lane).steps + kStart : 0;
-            unsigned long long upto = v;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const unsigned long long y = __shfl_up_sync(kFull, upto, off);
-                if (lane >= off) upto += y;
-            }
-            const unsigned here = __ballot_sync(kFull, x < upto);
-            if (here != 0) {
-                const int l = __ffs(here) - 1;
-                r.pair = i0 + l;
-                r.off = static_cast<int>(x - __shfl_sync(kFull, upto - v, l));
-                break;
-            }
-            x -= __shfl_sync(kFull, upto, 31);
-        }
-    }
-    if (lane == 0) *run = r;
-}
-
-// ------------------------------------------------------------------ loads --
-
-// Keys that no query of the chunk sees: from L on, and [dead0, dead1).
-struct Dead {
-    int dead0, dead1;
-    __device__ __forceinline__ Dead(const ChunkParams &p, const Seq &s) {
-        dead0 = p.sinks;
-        dead1 = p.window > 0 ? s.L - s.Lq - p.window + 1 : 0;
-    }
-    // all of [a, b)
-    __device__ __forceinline__ bool all(int a, int b) const { return a >= dead0 && b <= dead1; }
-    // any of [a, b)
-    __device__ __forceinline__ bool any(int a, int b) const { return max(a, dead0) < min(b, dead1); }
-};
-
-// The pages of a key tile, one per lane (of the first kBlockN / span).
-struct Pages {
-    int span_log2;  // rows of a page within a tile
-    int count;
-
-    __device__ __forceinline__ Pages(const ChunkParams &p) {
-        span_log2 = min(p.log2_bs, 7);
-        count = kBlockN >> span_log2;
-    }
-    // This lane's page of the tile from key k0 on: its number, -1 where no key
-    // of it is seen (not looked up).
-    __device__ __forceinline__ int look_up(const ChunkParams &p, const Part &u, const Dead &d, int k0) const {
-        const int lane = threadIdx.x % 32, key = k0 + (lane << span_log2);
-        if (lane >= count || key >= u.s.L || d.all(key, min(key + (1 << span_log2), u.s.L))) return -1;
-        return p.block_table[static_cast<size_t>(u.b) * p.max_blocks + (key >> p.log2_bs)];
-    }
-    // Its rows into the tile at `dst`, every lane its page; a page number that
-    // does not exist is reported and stands for zeros, as do keys nobody sees.
-    template <int D>
-    __device__ __forceinline__ void load(const ChunkParams &p, const Part &u, const Dead &d, int k0, int page,
-                                         const CUtensorMap *tm, uint32_t dst, uint32_t bar) const {
-        using S = FwdShape<D>;
-        const int lane = threadIdx.x % 32, key = k0 + (lane << span_log2);
-        if (lane >= count) return;
-        const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_blocks);
-        if (!there && key < u.s.L && !d.all(key, min(key + (1 << span_log2), u.s.L)))
-            atomicExch(p.err, kDeviceErrBadIndex);
-        const int z = there ? page * p.Hkv + u.hk : p.num_blocks * p.Hkv;
-        const int y = key & ((1 << p.log2_bs) - 1);
-#pragma unroll
-        for (int c = 0; c < S::kColBlocks; ++c)
-            ptx::tma_load_3d(dst + c * S::kBlockBytes + ((lane << span_log2) << 7), tm, bar, c * 64, y, z);
-    }
-};
-
-// A tile from pages of less than 8 rows, by the whole warp: 16-byte pieces into
-// the places that the swizzle gives them, zeros for keys nobody sees. Returns
-// with the pieces landed and visible to the tensor core.
-template <int D>
-__device__ __forceinline__ void copy_small_pages(const ChunkParams &p, const Part &u, const Dead &d, int k0,
-                                                 const uint16_t *cache, uint32_t dst) {
-    using S = FwdShape<D>;
-    constexpr int kPieces = D / 8, kRows = 32 / kPieces;
-    const int lane = threadIdx.x % 32, piece = lane % kPieces;
-#pragma unroll 4
-    for (int row = lane / kPieces; row < kBlockN; row += kRows) {
-        const int key = k0 + row;
-        const uint16_t *src = cache;
-        uint32_t bytes = 0;
-        if (key < u.s.L && !d.all(key, key + 1)) {
-            const int page = p.block_table[static_cast<size_t>(u.b) * p.max_blocks + (key >> p.log2_bs)];
-            if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_blocks)) {
-                src += (((static_cast<long long>(page) * p.Hkv + u.hk) << p.log2_bs) + (key & ((1 << p.log2_bs) - 1))) *
-                           D + piece * 8;
-                bytes = 16;
-            } else {
-                atomicExch(p.err, kDeviceErrBadIndex);
-            }
-        }
-        ptx::copy_async16(dst + (piece / 8) * S::kBlockBytes + row * 128 + (((piece % 8) ^ (row % 8)) << 4), src, bytes);
-    }
-    ptx::copy_async_wait_all();
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-}
-
 // ------------------------------------------------------------------ roles --
 
 template <int D>
@@ -397,6 +183,7 @@ __device__ void producer_qk(const CUtensorMap *tq, const CUtensorMap *tk, const 
     while (ok && walk.next(u)) {
         if (u.s1 == u.s0) continue;
         const Dead dead(p, u.s);
+        const Head at{u.b, u.hk, u.s.L};
         auto load_q = [&]() -> bool {
             if (nq > 0 &&
                 !ptx::warp_all(ptx::bar_wait(bar(S::kQEmpty), (nq - 1) & 1, abort_flag, p.timeout_ns)))
@@ -417,7 +204,7 @@ __device__ void producer_qk(const CUtensorMap *tq, const CUtensorMap *tk, const 
             return true;
         };
         if (wi == 0 && !(ok = load_q())) break;
-        int page = pages.look_up(p, u, dead, tile_at(u.k, u.s0) * kBlockN);
+        int page = pages.look_up(p, at, dead, tile_at(u.k, u.s0) * kBlockN);
         for (int j = u.s0; j < u.s1; ++j, ++it) {
             // the first products need Q and the first K tile only (see the packed forward)
             if (wi == 0 && j == u.s0 + 1 &&
@@ -425,19 +212,19 @@ __device__ void producer_qk(const CUtensorMap *tq, const CUtensorMap *tk, const 
                 break;
             const uint32_t stage = it % S::kKStages;
             const int k0 = tile_at(u.k, j) * kBlockN, here = page;
-            if (j + 1 < u.s1) page = pages.look_up(p, u, dead, tile_at(u.k, j + 1) * kBlockN);  // ahead of its use
+            if (j + 1 < u.s1) page = pages.look_up(p, at, dead, tile_at(u.k, j + 1) * kBlockN);  // ahead of its use
             if (it >= S::kKStages &&
                 !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kKEmpty + stage), ((it / S::kKStages) - 1) & 1, abort_flag,
                                      p.timeout_ns))))
                 break;
             const uint32_t dst = sbase + S::kOffK + stage * S::kTileBytes;
             if (p.log2_bs < 3) {
-                copy_small_pages<D>(p, u, dead, k0, p.k, dst);
+                copy_small_pages<D>(p, at, dead, k0, p.k, dst);
                 if (leader) ptx::bar_arrive(bar(S::kKFull + stage));
             } else {
                 if (leader) ptx::bar_arrive_expect_tx(bar(S::kKFull + stage), S::kTileBytes);
                 __syncwarp();
-                pages.load<D>(p, u, dead, k0, here, tk, dst, bar(S::kKFull + stage));
+                pages.load<D>(p, at, dead, k0, here, tk, dst, bar(S::kKFull + stage));
                 __syncwarp();
             }
             if (wi > 0 && j == u.s0 && !(ok = load_q())) break;
@@ -469,12 +256,13 @@ __device__ void producer_v(const CUtensorMap *tv, const ChunkParams &p, uint32_t
     while (ok && walk.next(u)) {
         if (u.s1 == u.s0) continue;
         const Dead dead(p, u.s);
-        int page = pages.look_up(p, u, dead, tile_at(u.k, u.s0) * kBlockN);
+        const Head at{u.b, u.hk, u.s.L};
+        int page = pages.look_up(p, at, dead, tile_at(u.k, u.s0) * kBlockN);
         for (int j = u.s0; j < u.s1; ++j, ++it) {
             if (it == 1 && !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kFirstQ), 0, abort_flag, p.timeout_ns)))) break;
             const uint32_t stage = it % S::kVStages;
             const int k0 = tile_at(u.k, j) * kBlockN, here = page;
-            if (j + 1 < u.s1) page = pages.look_up(p, u, dead, tile_at(u.k, j + 1) * kBlockN);
+            if (j + 1 < u.s1) page = pages.look_up(p, at, dead, tile_at(u.k, j + 1) * kBlockN);
             if (it >= S::kVStages &&
                 !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kVEmpty + stage), ((it / S::kVStages) - 1) & 1, abort_flag,
                                      p.timeout_ns))))
@@ -482,7 +270,7 @@ __device__ void producer_v(const CUtensorMap *tv, const ChunkParams &p, uint32_t
             const uint32_t dst = sbase + S::kOffV + stage * S::kTileBytes, full = bar(S::kVFull + stage);
             if (withheld(p.withhold, it)) continue;
             if (p.log2_bs < 3) {
-                copy_small_pages<D>(p, u, dead, k0, p.v, dst);
+                copy_small_pages<D>(p, at, dead, k0, p.v, dst);
                 if (leader) ptx::bar_arrive(full);
                 continue;
             }
@@ -494,7 +282,7 @@ __device__ void producer_v(const CUtensorMap *tv, const ChunkParams &p, uint32_t
             const uint32_t lands = cut ? bar(S::kVCut) : full;
             if (leader) ptx::bar_arrive_expect_tx(lands, S::kTileBytes);
             __syncwarp();
-            pages.load<D>(p, u, dead, k0, here, tv, dst, lands);
+            pages.load<D>(p, at, dead, k0, here, tv, dst, lands);
             __syncwarp();
             if (cut) {
                 if (!(ok = ptx::warp_all(ptx::bar_wait(lands, cuts++ & 1, abort_flag, p.timeout_ns)))) break;
@@ -845,7 +633,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         ptx::tmem_relinquish();
     }
     // the plan's scratch lies where the tiles go
-    plan(p, run, reinterpret_cast<unsigned long long *>(smem));
+    plan(p, Units{p}, run, reinterpret_cast<unsigned long long *>(smem));
     ptx::fence_proxy_async_smem();
     ptx::tc_fence_before();
     __syncthreads();

@@ -279,10 +279,8 @@ struct EvictParams {
 
 cudaError_t launch_kv_evict(int D, EvictParams p, cudaStream_t stream);
 
-// Parameters of the attention of chunks over a paged cache.
-struct ChunkParams {
-    void *o;                    // [total_q, H, D]
-    float *lse;                 // [H, total_q]
+// What the kernels of chunks of queries over a paged 16-bit cache share.
+struct PagedParams {
     const uint16_t *k, *v;      // pages [num_blocks, Hkv, block_size, D]
     const int *cu_q;            // [B + 1]
     const int *seq_lens;        // [B]
@@ -291,20 +289,38 @@ struct ChunkParams {
     int tile_tokens;            // tokens of a query tile: 128 / group
     int log2_bs, num_blocks, max_blocks;
     int window, sinks;          // window 0: every key up to the query's own
-    int min_run;                // least work of a CTA, in key tiles
+    int min_run;                // least work of a CTA, in the plan's cost
     float scale_log2;
+    int *err;                   // device error word
+    unsigned long long timeout_ns;
+    int withhold;               // test support (see FwdParams)
+};
+
+// Parameters of the attention of chunks.
+struct ChunkParams : PagedParams {
+    void *o;                    // [total_q, H, D]
+    float *lse;                 // [H, total_q]
     float *o_part;              // [2 grid][part_rows][D], unnormalised parts of units
     float2 *ml_part;            // [2 grid][part_rows], their (m, l)
     int part_rows;              // rows of a unit
     int4 *records;              // [grid], units to be joined
-    int *err;                   // device error word
-    unsigned long long timeout_ns;
-    int withhold;               // test support (see FwdParams)
 };
 
 // maps: Q {D, group, Hkv, tokens}, boxes 64 x group x 1 x tile_tokens; K and V
 // {D, block_size, num_blocks * Hkv}, boxes of 64 columns and a page's rows (at most 128).
 cudaError_t launch_fwd_paged(int D, bool bf16, const CUtensorMap *maps, const ChunkParams &p, int grid,
                              cudaStream_t stream);
+
+// Parameters of the kernel that sums the weights of keys.
+struct WeightsParams : PagedParams {
+    const float *lse;           // row (head, packed token) at head * lse_head + token * lse_token
+    long long lse_head, lse_token;
+    float *weights;             // [B, Hkv, max_blocks * block_size]
+    int chunks;                 // columns of a step, in 32s (set by launch_kv_weights)
+};
+
+// maps: Q and K as launch_fwd_paged's.
+cudaError_t launch_kv_weights(int D, bool bf16, const CUtensorMap *maps, WeightsParams p, int grid,
+                              cudaStream_t stream);
 
 }  // namespace fa

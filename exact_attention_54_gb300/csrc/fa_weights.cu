@@ -1,0 +1,455 @@
+// The attention weight that each key of a paged cache receives from a chunk of
+// queries (fa_kv_weights): w[b, hk, j] += sum over the chunk's queries i that see
+// key j and the query heads g of key head hk of exp(scale q_ig . k_j - lse_ig),
+// the softmax weights of the attention that gave lse.
+//
+// S^T = K Q^T on the tensor core, keys down the TMEM lanes: a thread owns a key
+// and sums its row, so the sums need no exchange, no atomics, and come in one
+// order. A unit is two key tiles of one key head, which stay in shared memory
+// while the query tiles that see any of them stream past (rows as in
+// fa_chunk.cuh); with one key tile, queries would come from L2 at 64 bytes a clock
+// and SM, twice what it gives. Each key tile has a warpgroup and two TMEM buffers
+// of 128 columns, so the products of a step run while the step before is
+// exponentiated. -lse log2 e of a step's columns comes through shared memory,
+// -inf where a column is no query.
+//
+// Bound: long chunks by the exponentials (a 128 x 128 tile: 512 clocks of the SM
+// for them and 512 of the tensor core for the product, side by side); single
+// tokens by reading the keys.
+#include "fa_paged.cuh"
+
+namespace fa {
+namespace weights {
+
+using namespace paged;
+
+constexpr int kThreads = 384;
+constexpr int kUnitKeys = 2 * kBlockN;
+constexpr int kStart = 1;  // what a unit's start costs, in query tiles
+
+template <int D>
+struct Shape {
+    static constexpr int kColBlocks = D / 64;
+    static constexpr int kBlockBytes = FwdShape<D>::kBlockBytes;
+    static constexpr int kTileBytes = FwdShape<D>::kTileBytes;
+    static constexpr int kKUnits = D == 128 ? 2 : 4;   // units whose keys are loaded or loading
+    static constexpr int kQStages = D == 128 ? 3 : 4;
+    static constexpr int kLStages = 3;
+    static constexpr int kOffK = 0;
+    static constexpr int kOffQ = kOffK + kKUnits * 2 * kTileBytes;
+    static constexpr int kOffL = kOffQ + kQStages * kTileBytes;
+    static constexpr int kOffBar = kOffL + kLStages * 512;
+    static constexpr int kKFull = 0, kKEmpty = kKFull + kKUnits;
+    static constexpr int kQFull = kKEmpty + kKUnits, kQEmpty = kQFull + kQStages;
+    static constexpr int kLFull = kQEmpty + kQStages, kLEmpty = kLFull + kLStages;
+    static constexpr int kSFull = kLEmpty + kLStages, kSEmpty = kSFull + 4;  // + 2 t + buffer
+    static constexpr int kTeardown = kSEmpty + 4, kNumBars = kTeardown + 1;
+    static constexpr int kOffMisc = (kOffBar + 8 * kNumBars + 15) & ~15;
+    static constexpr int kOffRun = kOffMisc + 16;
+    static constexpr int kSmemBytes = kOffRun + sizeof(Run) + 1024;
+    static_assert(kSmemBytes <= 227 * 1024 && (kPlanEntries + 1) * 8 <= kOffQ, "shared memory budget");
+};
+
+// Tokens [t0, t1) of a chunk that see a key of [k0, k0 + kUnitKeys).
+struct Tokens {
+    int t0, t1;
+    __device__ __forceinline__ Tokens(const PagedParams &p, const Seq &s, int k0) {
+        const int pos0 = s.L - s.Lq;
+        t0 = max(k0 - pos0, 0);
+        t1 = s.Lq;
+        if (p.window > 0 && k0 >= p.sinks) t1 = min(t1, max(k0 + kUnitKeys - 1 + p.window - pos0, 0));
+    }
+    __device__ __forceinline__ int tiles(const PagedParams &p) const {
+        return t1 > t0 ? (t1 - t0 + p.tile_tokens - 1) / p.tile_tokens : 0;
+    }
+};
+
+struct Units {
+    const PagedParams &p;
+    __device__ __forceinline__ int count(const Seq &s) const { return s.Lq > 0 ? (s.L + kUnitKeys - 1) / kUnitKeys : 0; }
+    __device__ __forceinline__ int cost(const Seq &s, int i) const {
+        const int n = Tokens(p, s, i * kUnitKeys).tiles(p);
+        return n > 0 ? n + kStart : 0;
+    }
+};
+
+// The units that start in a CTA's run; every role walks them for itself.
+struct Unit {
+    int b, hk, k0, steps, t0, t1;
+    Seq s;
+};
+
+struct Walk {
+    const PagedParams &p;
+    long long rem;
+    int b, hk, unit, off, n;
+    Seq s;
+
+    __device__ __forceinline__ Walk(const PagedParams &p_, const volatile Run *r) : p(p_) {
+        rem = r->len;
+        b = r->b;
+        hk = r->hk;
+        unit = r->unit;
+        off = r->off;
+        n = 0;
+        if (rem > 0) {
+            s = load_seq(p, b);
+            n = Units{p}.count(s);
+        }
+    }
+    __device__ __forceinline__ bool next(Unit &o) {
+        while (rem > 0) {
+            if (unit >= n) {
+                unit = 0;
+                if (n == 0 || ++hk == p.Hkv) {
+                    hk = 0;
+                    if (++b >= p.B) return false;
+                    s = load_seq(p, b);
+                    n = Units{p}.count(s);
+                    continue;
+                }
+            }
+            const Tokens t(p, s, unit * kUnitKeys);
+            const int tiles = t.tiles(p), cost = tiles > 0 ? tiles + kStart : 0;
+            const bool starts = off == 0 && tiles > 0;
+            o = Unit{b, hk, unit * kUnitKeys, tiles, t.t0, t.t1, s};
+            rem -= cost - off;
+            off = 0;
+            ++unit;
+            if (starts) return true;
+        }
+        return false;
+    }
+};
+
+template <int D>
+__device__ void producer_k(const CUtensorMap *tk, const WeightsParams &p, uint32_t sbase, const volatile Run *run,
+                           volatile int *abort_flag) {
+    using S = Shape<D>;
+    auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
+    const bool leader = ptx::elect_one();
+    const Pages pages(p);
+    uint32_t it = 0;  // units loaded
+    bool ok = true;
+    Walk walk(p, run);
+    Unit u;
+    for (; ok && walk.next(u); ++it) {
+        const Dead dead(p, u.s);
+        const Head at{u.b, u.hk, u.s.L};
+        const int page[2] = {pages.look_up(p, at, dead, u.k0), pages.look_up(p, at, dead, u.k0 + kBlockN)};
+        const uint32_t stage = it % S::kKUnits;
+        if (it >= S::kKUnits &&
+            !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kKEmpty + stage), ((it / S::kKUnits) - 1) & 1, abort_flag,
+                                 p.timeout_ns))))
+            break;
+        const uint32_t dst = sbase + S::kOffK + stage * 2 * S::kTileBytes, full = bar(S::kKFull + stage);
+        if (p.log2_bs < 3) {
+            copy_small_pages<D>(p, at, dead, u.k0, p.k, dst);
+            copy_small_pages<D>(p, at, dead, u.k0 + kBlockN, p.k, dst + S::kTileBytes);
+            if (leader) ptx::bar_arrive(full);
+            continue;
+        }
+        if (leader) ptx::bar_arrive_expect_tx(full, 2 * S::kTileBytes);
+        __syncwarp();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            pages.load<D>(p, at, dead, u.k0 + t * kBlockN, page[t], tk, dst + t * S::kTileBytes, full);
+        __syncwarp();
+    }
+    for (uint32_t s = 0; s < S::kKUnits && s < it; ++s) {
+        const uint32_t last = (it - 1) - ((it - 1 - s) % S::kKUnits);
+        ptx::bar_wait(bar(S::kKFull + s), (last / S::kKUnits) & 1, nullptr, p.timeout_ns);
+    }
+}
+
+template <int D>
+__device__ void producer_q(const CUtensorMap *tq, const WeightsParams &p, uint32_t sbase, const volatile Run *run,
+                           volatile int *abort_flag) {
+    using S = Shape<D>;
+    auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
+    const bool leader = ptx::elect_one();
+    const uint32_t bytes = static_cast<uint32_t>(p.tile_tokens * p.group * 128 * S::kColBlocks);
+    uint32_t it = 0;
+    bool ok = true;
+    Walk walk(p, run);
+    Unit u;
+    while (ok && walk.next(u)) {
+        for (int j = 0; j < u.steps; ++j, ++it) {
+            const uint32_t stage = it % S::kQStages;
+            if (it >= S::kQStages &&
+                !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kQEmpty + stage), ((it / S::kQStages) - 1) & 1, abort_flag,
+                                     p.timeout_ns))))
+                break;
+            if (leader && !withheld(p.withhold, it)) {
+                ptx::bar_arrive_expect_tx(bar(S::kQFull + stage), bytes);
+#pragma unroll
+                for (int c = 0; c < S::kColBlocks; ++c)
+                    ptx::tma_load_4d(sbase + S::kOffQ + stage * S::kTileBytes + c * S::kBlockBytes, tq,
+                                     bar(S::kQFull + stage), c * 64, 0, u.hk, u.s.q0 + u.t0 + j * p.tile_tokens);
+            }
+        }
+    }
+    for (uint32_t s = 0; s < S::kQStages && s < it; ++s) {
+        const uint32_t last = (it - 1) - ((it - 1 - s) % S::kQStages);
+        ptx::bar_wait(bar(S::kQFull + s), (last / S::kQStages) & 1, nullptr, p.timeout_ns);
+    }
+}
+
+// -lse log2 e of each column of each step; -inf for columns that are no query,
+// and for queries that see nothing.
+template <int D>
+__device__ void producer_lse(const WeightsParams &p, uint32_t sbase, float *ring, const volatile Run *run,
+                             volatile int *abort_flag) {
+    using S = Shape<D>;
+    auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
+    const int lane = threadIdx.x % 32;
+    int token[4], head[4];  // of columns lane, lane + 32, ...
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        token[i] = (lane + 32 * i) / p.group;
+        head[i] = lane + 32 * i - token[i] * p.group;
+    }
+    uint32_t it = 0;
+    bool ok = true;
+    Walk walk(p, run);
+    Unit u;
+    while (ok && walk.next(u)) {
+        for (int j = 0; j < u.steps; ++j, ++it) {
+            const int t0 = u.t0 + j * p.tile_tokens, n = min(p.tile_tokens, u.t1 - t0);
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = CUDART_INF_F;
+                if (token[i] < n)
+                    x[i] = __ldg(p.lse + static_cast<long long>(u.hk * p.group + head[i]) * p.lse_head +
+                                 static_cast<long long>(u.s.q0 + t0 + token[i]) * p.lse_token);
+            }
+            const uint32_t stage = it % S::kLStages;
+            if (it >= S::kLStages &&
+                !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kLEmpty + stage), ((it / S::kLStages) - 1) & 1, abort_flag,
+                                     p.timeout_ns))))
+                break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                ring[stage * 128 + lane + 32 * i] =
+                    x[i] == -CUDART_INF_F ? -CUDART_INF_F : x[i] * -1.4426950408889634f;
+            __syncwarp();
+            if (lane == 0) ptx::bar_arrive(bar(S::kLFull + stage));
+        }
+    }
+}
+
+template <int D, bool BF16>
+__device__ void mma(const WeightsParams &p, uint32_t sbase, uint32_t tmem, const volatile Run *run,
+                    volatile int *abort_flag) {
+    using S = Shape<D>;
+    auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
+    const uint32_t idesc = ptx::idesc_f16(BF16, kBlockN, 32 * p.chunks, false);
+    const bool leader = ptx::elect_one();
+    const uint64_t dq0 = ptx::smem_desc_sw128(sbase + S::kOffQ, 16, 1024);
+    const uint64_t dk0 = ptx::smem_desc_sw128(sbase + S::kOffK, 16, 1024);
+    constexpr uint64_t kTile16 = S::kTileBytes >> 4, kBlock16 = S::kBlockBytes >> 4;
+    uint32_t units = 0, it = 0;
+    bool ok = true;
+    Walk walk(p, run);
+    Unit u;
+    for (; ok && walk.next(u); ++units) {
+        const uint32_t ks = units % S::kKUnits;
+        if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kKFull + ks), (units / S::kKUnits) & 1, abort_flag, p.timeout_ns))))
+            break;
+        for (int j = 0; j < u.steps; ++j, ++it) {
+            const uint32_t qs = it % S::kQStages, buf = it % 2;
+            if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kQFull + qs), (it / S::kQStages) & 1, abort_flag, p.timeout_ns))))
+                break;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (it >= 2 && !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kSEmpty + 2 * t + buf), (it / 2 - 1) & 1,
+                                                                  abort_flag, p.timeout_ns))))
+                    break;
+                ptx::tc_fence_after();
+                if (leader) {
+                    const uint64_t kd = dk0 + (2 * ks + t) * kTile16, qd = dq0 + qs * kTile16;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t off = (kk / 4) * kBlock16 + (kk % 4) * 2;
+                        ptx::mma_ss(tmem + 128 * (2 * t + buf), kd + off, qd + off, idesc, kk > 0);
+                    }
+                    ptx::mma_commit(bar(S::kSFull + 2 * t + buf));
+                }
+            }
+            if (!ok) break;
+            if (leader) {
+                ptx::mma_commit(bar(S::kQEmpty + qs));
+                if (j + 1 == u.steps) ptx::mma_commit(bar(S::kKEmpty + ks));
+            }
+        }
+    }
+    if (leader) ptx::mma_commit(bar(S::kTeardown));
+    __syncwarp();
+    ptx::bar_wait(bar(S::kTeardown), 0, nullptr, p.timeout_ns);
+}
+
+// Sums of one key tile's rows, one key per thread.
+template <int D>
+__device__ void sums(const WeightsParams &p, uint32_t sbase, uint32_t tmem, int t, int wq, int lane,
+                     const volatile Run *run, volatile int *abort_flag) {
+    using S = Shape<D>;
+    auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
+    const uint32_t tS = tmem + (static_cast<uint32_t>(wq * 32) << 16) + 256 * t;
+    const int row = wq * 32 + lane;
+    const uint64_t scale2 = ptx::pk2(p.scale_log2, p.scale_log2);
+    uint32_t it = 0;
+    bool ok = true;
+    Walk walk(p, run);
+    Unit u;
+    while (ok && walk.next(u)) {
+        const int k0 = u.k0 + t * kBlockN, key = k0 + row;
+        const int pos0 = u.s.L - u.s.Lq;
+        uint64_t sum[4] = {0, 0, 0, 0};  // pairs of zeros
+        for (int j = 0; j < u.steps; ++j, ++it) {
+            const int t0 = u.t0 + j * p.tile_tokens, n = min(p.tile_tokens, u.t1 - t0), first = pos0 + t0;
+            // columns that are no query of the chunk but hold one's row (the
+            // last tile), or queries that do not see all of this tile's keys
+            const bool masked = n < p.tile_tokens || k0 + kBlockN - 1 > first ||
+                                (p.window > 0 && k0 + kBlockN > p.sinks && k0 <= first + n - 1 - p.window);
+            const uint32_t buf = it % 2, ls = it % S::kLStages;
+            ok = ptx::bar_wait(bar(S::kLFull + ls), (it / S::kLStages) & 1, abort_flag, p.timeout_ns) &&
+                 ptx::bar_wait(bar(S::kSFull + 2 * t + buf), (it / 2) & 1, abort_flag, p.timeout_ns);
+            if (!__all_sync(kFull, ok)) { ok = false; break; }
+            ptx::tc_fence_after();
+            // a key is seen by the columns [c0, c1): queries at its position or later, and in its window
+            int c0 = 0, c1 = 128;
+            if (masked) {
+                c0 = min(max(key - first, 0), 128) * p.group;
+                c1 = n;
+                if (p.window > 0 && key >= p.sinks) c1 = min(c1, max(key + p.window - first, 0));
+                c1 *= p.group;
+            }
+            const uint32_t ring = sbase + S::kOffL + ls * 512;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                if (b >= p.chunks) break;
+                uint32_t s[32];
+                ptx::tmem_ld32(tS + 128 * buf + 32 * b, s);
+                ptx::tmem_ld_wait();
+                ptx::reg_fence(s);
+                uint32_t seen = 0xffffffffu;
+                if (masked) {
+                    auto below = [](int x) -> uint32_t {
+                        return static_cast<uint32_t>((1ull << min(max(x, 0), 32)) - 1);
+                    };
+                    seen = below(c1 - 32 * b) & ~below(c0 - 32 * b);
+                }
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    uint64_t nl[2];
+                    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];"
+                                 : "=l"(nl[0]), "=l"(nl[1])
+                                 : "r"(ring + 128 * b + 4 * i));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int c = i + 2 * h;
+                        float x0, x1;
+                        ptx::upk2(ptx::ffma2(ptx::pk2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, nl[h]),
+                                  x0, x1);
+                        float e0 = ptx::ex2(x0), e1 = ptx::ex2(x1);
+                        if (masked) {
+                            if (!(seen & (1u << c))) e0 = 0.f;
+                            if (!(seen & (2u << c))) e1 = 0.f;
+                        }
+                        sum[(c / 2) % 4] = ptx::fadd2(sum[(c / 2) % 4], ptx::pk2(e0, e1));
+                    }
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                ptx::bar_arrive(bar(S::kSEmpty + 2 * t + buf));
+                ptx::bar_arrive(bar(S::kLEmpty + ls));
+            }
+        }
+        if (!ok) break;
+        if (key < u.s.L) {
+            float a0, a1, b0, b1;
+            ptx::upk2(ptx::fadd2(sum[0], sum[1]), a0, a1);
+            ptx::upk2(ptx::fadd2(sum[2], sum[3]), b0, b1);
+            float *w = p.weights + (static_cast<size_t>(u.b) * p.Hkv + u.hk) * (static_cast<size_t>(p.max_blocks) << p.log2_bs);
+            w[key] += (a0 + a1) + (b0 + b1);
+        }
+    }
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    fa_kv_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const WeightsParams p) {
+    using S = Shape<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = ptx::smem_addr(smem);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kOffMisc + 4);
+    Run *run = reinterpret_cast<Run *>(smem + S::kOffRun);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kNumBars; ++i) {
+            const bool s_empty = i >= S::kSEmpty && i < S::kTeardown, l_empty = i >= S::kLEmpty && i < S::kSFull;
+            ptx::bar_init(sbase + S::kOffBar + 8u * i, s_empty ? 4u : l_empty ? 8u : 1u);  // one arrival per warp
+        }
+        *abort_flag = 0;
+        ptx::bar_init_fence();
+        ptx::prefetch_tmap(&tm_q);
+        ptx::prefetch_tmap(&tm_k);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_addr(tmem_slot), 512);
+        ptx::tmem_relinquish();
+    }
+    // rows that no box reaches are zeros: their scores are finite, their weights 0
+    for (int i = warp; i < S::kQStages; i += kThreads / 32)
+        ptx::zero_rows(sbase + S::kOffQ + i * S::kTileBytes, S::kColBlocks, kBlockM, p.tile_tokens * p.group, kBlockM);
+    // the plan's scratch lies where the keys go
+    plan(p, Units{p}, run, reinterpret_cast<unsigned long long *>(smem));
+    ptx::fence_proxy_async_smem();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) producer_k<D>(&tm_k, p, sbase, run, abort_flag);
+    else if (warp == 1) mma<D, BF16>(p, sbase, tmem, run, abort_flag);
+    else if (warp == 2) producer_lse<D>(p, sbase, reinterpret_cast<float *>(smem + S::kOffL), run, abort_flag);
+    else if (warp == 3) producer_q<D>(&tm_q, p, sbase, run, abort_flag);
+    else sums<D>(p, sbase, tmem, (warp - 4) / 4, warp % 4, lane, run, abort_flag);
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && *abort_flag) atomicExch(p.err, kDeviceErrTimeout);
+}
+
+template <int D, bool BF16>
+static cudaError_t launch_t(const CUtensorMap *maps, const WeightsParams &p, int grid, cudaStream_t st) {
+    static std::atomic<unsigned long long> done{0};
+    auto kern = fa_kv_weights_kernel<D, BF16>;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), Shape<D>::kSmemBytes, done);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, kThreads, Shape<D>::kSmemBytes, st>>>(maps[0], maps[1], p);
+    return cudaGetLastError();
+}
+
+}  // namespace weights
+
+cudaError_t launch_kv_weights(int D, bool bf16, const CUtensorMap *maps, WeightsParams p, int grid, cudaStream_t st) {
+    p.chunks = (p.tile_tokens * p.group + 31) / 32;
+    if (D == 64)
+        return bf16 ? weights::launch_t<64, true>(maps, p, grid, st) : weights::launch_t<64, false>(maps, p, grid, st);
+    return bf16 ? weights::launch_t<128, true>(maps, p, grid, st) : weights::launch_t<128, false>(maps, p, grid, st);
+}
+
+}  // namespace fa

@@ -670,6 +670,36 @@ FA_API fa_status_t fa_fwd_paged(const void *q, const void *k_cache, const void *
                                 void *stream);
 
 /*
+ * fa_kv_weights - what a chunk of queries gave to each key of a paged cache: the
+ * softmax weights of the attention that has run, summed over the chunk's
+ * queries and the query heads of a key head, and added to what is there:
+ *
+ *   weights[b, hk, j] += sum over queries t that see key j, and heads h of key
+ *                        head hk, of exp(scale * q_th . k_j - lse_th)
+ *
+ * fa_kv_evict takes them. What a query sees is as in fa_fwd_paged, whose
+ * arguments these are, but for
+ *
+ *   lse        fp32, of the attention over the same keys: (head h, packed token
+ *              t) at element h * lse_head + t * lse_token: (total_q, 1) for the
+ *              [H,total_q] of fa_fwd_paged, (1, H) for the [B,H] of a decode
+ *              (total_q = B queries, one each)
+ *   weights    [num_seqs,Hkv,max_blocks_per_seq * block_size] fp32, in and out;
+ *              keys that no query sees keep theirs
+ * Queries with lse = -inf give nothing. Rows of the cache that no query sees, and
+ * rows of q and lse that belong to no chunk, may hold anything. Offsets and page
+ * numbers are checked as by fa_fwd_paged (a page that does not exist counts as
+ * zeros). The result is deterministic. One launch, no workspace.
+ * Errors: FA_ERR_NULL, FA_ERR_SHAPE (negative strides too), FA_ERR_HEADDIM,
+ * FA_ERR_DTYPE, FA_ERR_ALIGN, FA_ERR_SCALE, FA_ERR_CUDA.
+ */
+FA_API fa_status_t fa_kv_weights(const void *q, const float *lse, const void *k_cache, const int32_t *block_table,
+                                 const int32_t *cu_seqlens_q, const int32_t *seq_lens, float *weights,
+                                 int64_t lse_head, int64_t lse_token, int num_seqs, int total_q, int max_seqlen_q,
+                                 int H, int Hkv, int D, int num_blocks, int block_size, int max_blocks_per_seq,
+                                 int window, int sinks, float scale, fa_dtype_t dtype, void *stream);
+
+/*
  * fa_kv_evict - the keys of least weight leave a paged 16-bit cache.
  *
  * Of a sequence of L = seq_lens[b] keys with L > keep, each key head keeps
@@ -719,10 +749,12 @@ FA_API fa_status_t fa_check_device_error(void *stream);
 
 /*
  * fa_test_withhold_load - test support for the failure path of the prefill
- * kernels (fa_fwd, fa_fwd_varlen, fa_bwd, fa_bwd_varlen and the window forms).
+ * kernels (fa_fwd, fa_fwd_varlen, fa_bwd, fa_bwd_varlen, the window forms,
+ * fa_fwd_paged and fa_kv_weights).
  * With load = n > 0, the CTA with the first work item of every later launch of
  * those kernels never issues one of its tile loads (the forward's V tile
- * n - 1, the backward's Q/dO step n - 1; an item with n of them), so the
+ * n - 1, the backward's Q/dO step n - 1, the query tile n - 1 of fa_kv_weights;
+ * an item with n of them), so the
  * wait for it cannot complete: the kernel's bounded wait runs out after
  * `wait_limit_ns`, its CTAs drain the copies they issued, release tensor
  * memory and stop, and fa_check_device_error returns FA_ERR_DEVICE_TIMEOUT.
