@@ -107,27 +107,28 @@ struct Part {
     int parts;    // first of several parts: their number, else 0
 };
 
+// Where a role is in its CTA's run.
 struct Walk {
-    const ChunkParams &p;
     long long rem, per;
-    int b, hk, pair, off, pairs;
-    bool first = true;
+    int b, hk, pair, off, pairs, first;
     Seq s;
 
-    __device__ __forceinline__ Walk(const ChunkParams &p_, const volatile Run *r) : p(p_) {
+    __device__ __forceinline__ void start(const ChunkParams &p, const volatile Run *r) {
         rem = r->len;
         per = r->per;
         b = r->b;
         hk = r->hk;
         pair = r->unit;
         off = r->off;
+        first = 1;
         pairs = 0;
+        s = Seq{0, 0, 0};
         if (rem > 0) {
             s = load_seq(p, b);
             pairs = pairs_of(p, s);
         }
     }
-    __device__ __forceinline__ bool next(Part &o) {
+    __device__ __forceinline__ bool next(const ChunkParams &p, Part &o) {
         while (rem > 0) {
             while (pairs == 0) {  // a sequence without queries
                 if (++b >= p.B) return false;
@@ -149,7 +150,7 @@ struct Walk {
             o.parts = o.s0 == 0 && o.s1 > 0 && rest > 0 ? 1 + static_cast<int>((rest + per - 1) / per) : 0;
             const bool some = o.s1 > o.s0 || (o.k.steps == 0 && off == 0);
             rem -= take;
-            first = false;
+            first = 0;
             off = 0;
             if (++pair == pairs) {
                 pair = 0;
@@ -162,6 +163,13 @@ struct Walk {
         }
         return false;
     }
+};
+
+// A softmax warp's place in the run and what its part needs at the end: kept in
+// shared memory while the steps need the registers.
+struct Kept {
+    Walk walk;
+    int tok0, ntok, h0, dest;  // packed row of the tile's first token; tokens; first head; slot, or -1: the unit's only part
 };
 
 // ------------------------------------------------------------------ roles --
@@ -178,9 +186,10 @@ __device__ void producer_qk(const CUtensorMap *tq, const CUtensorMap *tk, const 
     const uint32_t tile_q = static_cast<uint32_t>(p.tile_tokens * p.group * 128 * S::kColBlocks);
     uint32_t it = 0, wi = 0, nq = 0;  // K tiles issued, parts loaded, Q loads issued
     bool ok = true;
-    Walk walk(p, run);
+    Walk walk;
+    walk.start(p, run);
     Part u;
-    while (ok && walk.next(u)) {
+    while (ok && walk.next(p, u)) {
         if (u.s1 == u.s0) continue;
         const Dead dead(p, u.s);
         const Head at{u.b, u.hk, u.s.L};
@@ -251,9 +260,10 @@ __device__ void producer_v(const CUtensorMap *tv, const ChunkParams &p, uint32_t
     uint32_t it = 0;
     uint32_t cuts = 0, cut_done = 0;  // tiles with rows to clear: loaded, landed
     bool ok = true;
-    Walk walk(p, run);
+    Walk walk;
+    walk.start(p, run);
     Part u;
-    while (ok && walk.next(u)) {
+    while (ok && walk.next(p, u)) {
         if (u.s1 == u.s0) continue;
         const Dead dead(p, u.s);
         const Head at{u.b, u.hk, u.s.L};
@@ -341,9 +351,10 @@ __device__ void mma(const ChunkParams &p, uint32_t sbase, uint32_t tmem, const v
     uint32_t it = 0, wi = 0;   // K/V tiles consumed, parts consumed
     uint32_t cnt[2] = {0, 0};  // PV steps issued per query tile
     bool ok = true;
-    Walk walk(p, run);
+    Walk walk;
+    walk.start(p, run);
     Part u;
-    while (ok && walk.next(u)) {
+    while (ok && walk.next(p, u)) {
         const int n = u.s1 - u.s0;
         if (n == 0) continue;
         const int total[2] = {visited(u.k, 0, u.s0, u.s1), visited(u.k, 1, u.s0, u.s1)};
@@ -426,7 +437,7 @@ __device__ void mma(const ChunkParams &p, uint32_t sbase, uint32_t tmem, const v
 
 template <int D, bool BF16>
 __device__ void softmax(const ChunkParams &p, uint32_t sbase, uint32_t tmem, int t, int wq, int lane,
-                        const volatile Run *run, volatile int *abort_flag) {
+                        const volatile Run *run, Kept *kept, volatile int *abort_flag) {
     using S = FwdShape<D>;
     const uint32_t bars = sbase + S::kOffBar;
     auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
@@ -435,29 +446,51 @@ __device__ void softmax(const ChunkParams &p, uint32_t sbase, uint32_t tmem, int
     const uint32_t tS = tmem + lane_base + S::kTmemS + t * 128;
     const uint32_t tO = tmem + lane_base + S::kTmemO + t * D;
     const float scale_log2 = p.scale_log2;
-    const int token = row / p.group, head = row - token * p.group;  // within the tile, within the group
-    const bool in_tile = token < p.tile_tokens;
     uint32_t cnt = 0, items = 0;
     bool ok = true;
-    Walk walk(p, run);
-    Part u;
-    while (ok && walk.next(u)) {
-        if (u.k.ntok[t] == 0) continue;
-        const int first = u.s.L - u.s.Lq + u.k.tok[t];  // the tile's first position
-        const int pos = first + token, last = first + u.k.ntok[t] - 1;
-        const bool row_valid = in_tile && token < u.k.ntok[t];
+    if (lane == 0) kept->walk.start(p, run);
+    __syncwarp();
+    while (ok) {
+        // the key tiles of this part that the query tile visits: [x, x1), then [x2, x3)
+        int x, x1, x2, x3, first, behind;
+        {
+            Walk walk = kept->walk;
+            Part u;
+            if (!walk.next(p, u)) break;
+            auto mine = [&](const int (&v)[2]) { return t == 0 ? v[0] : v[1]; };
+            const int up = u.k.lo - u.k.ns, ntok = mine(u.k.ntok);
+            x = u.s0;
+            x1 = min(u.s1, mine(u.k.sink));
+            x2 = max(max(mine(u.k.wlo), u.k.ns), u.s0 + up);
+            x3 = min(mine(u.k.hi), u.s1 + up);
+            if (x >= x1) x1 = x = x2;  // no first run
+            first = u.s.L - u.s.Lq + mine(u.k.tok);  // the tile's first position
+            behind = p.window > 0 ? first + ntok - 1 - p.window : -1;  // the last key behind its last window
+            __syncwarp();
+            if (lane == 0) {
+                kept->walk = walk;
+                kept->tok0 = u.s.q0 + mine(u.k.tok);
+                kept->ntok = ntok;
+                kept->h0 = u.hk * p.group;
+                kept->dest = u.whole ? -1 : u.slot;
+            }
+            __syncwarp();
+            if (ntok == 0) continue;
+        }
+        const int pos = first + row / p.group;
         float m_used = -CUDART_INF_F;
         float l = 0.f;
         int mine = 0;  // steps taken
-        for (int j = u.s0; j < u.s1; ++j) {
-            if (!visits(u.k, t, j)) continue;
+        for (;; ++x) {
+            if (x == x1) x = x2;
+            if (x >= x3 && x >= x1) break;
             ok = ptx::bar_wait(bar(S::kSFull + t), cnt & 1, abort_flag, p.timeout_ns);
             if (!__all_sync(kFull, ok)) { ok = false; break; }
             ptx::tc_fence_after();
             // the row sees the columns c < lim, but with a window not those with sk <= c < wl
-            const int k0 = tile_at(u.k, j) * kBlockN;
+            const int k0 = x * kBlockN;
             const bool need_mask = k0 + kBlockN - 1 > first;
-            const bool need_lo = p.window > 0 && k0 + kBlockN > p.sinks && k0 <= last - p.window;
+            const bool need_lo = k0 + kBlockN > p.sinks && k0 <= behind;
             uint32_t s[4][32];
             float mx4[4];
 #pragma unroll
@@ -565,10 +598,13 @@ __device__ void softmax(const ChunkParams &p, uint32_t sbase, uint32_t tmem, int
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[c][i] = 0u;
         }
-        if (!u.whole) {
+        const volatile Kept *end = kept;
+        const int dest = end->dest, token = row / p.group;  // token within the tile
+        const bool row_valid = token < end->ntok;           // (it has at most tile_tokens)
+        if (dest >= 0) {
             // a part: m, l and O as they are
             if (row_valid) {
-                const size_t at = static_cast<size_t>(2 * blockIdx.x + u.slot) * p.part_rows + t * kBlockM + row;
+                const size_t at = static_cast<size_t>(2 * blockIdx.x + dest) * p.part_rows + t * kBlockM + row;
                 uint4 *dst = reinterpret_cast<uint4 *>(p.o_part + at * D);
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c)
@@ -583,7 +619,7 @@ __device__ void softmax(const ChunkParams &p, uint32_t sbase, uint32_t tmem, int
         const float inv_l = l == 0.f ? 0.f : 1.f / l;
         const float lse = l == 0.f ? -CUDART_INF_F : (m_used + __log2f(l)) * 0.69314718055994531f;
         if (row_valid) {
-            const size_t tok = static_cast<size_t>(u.s.q0) + u.k.tok[t] + token, h = u.hk * p.group + head;
+            const size_t tok = static_cast<size_t>(end->tok0) + token, h = end->h0 + row - token * p.group;
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o) + (tok * p.H + h) * D);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c)
@@ -612,7 +648,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kOffMisc + 4);
     Run *run = reinterpret_cast<Run *>(smem + S::kOffSched);
-    static_assert(sizeof(Run) <= kSchedInts * 4 && (kPlanEntries + 1) * 8 <= S::kOffBar, "scratch");
+    static_assert(sizeof(Run) + 8 * sizeof(Kept) <= kSchedInts * 4 && (kPlanEntries + 1) * 8 <= S::kOffBar, "scratch");
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
     ptx::grid_launch_dependents();
@@ -648,14 +684,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         producer_v<D>(&tm_v, p, sbase, run, abort_flag);
     } else if (warp == 3) {
         // the unit that starts here and ends in a later CTA's run, for the joining launch
-        Walk walk(p, run);
+        Walk walk;
+        walk.start(p, run);
         Part u;
         int4 rec = make_int4(0, 0, 0, 0);
-        while (walk.next(u))
+        while (walk.next(p, u))
             if (u.parts > 0) rec = make_int4(u.b, u.hk, u.pair, 2 * u.parts + u.slot);
         if (lane == 0) p.records[blockIdx.x] = rec;
     } else {
-        softmax<D, BF16>(p, sbase, tmem, (warp - 4) / 4, warp % 4, lane, run, abort_flag);
+        softmax<D, BF16>(p, sbase, tmem, (warp - 4) / 4, warp % 4, lane, run,
+                         reinterpret_cast<Kept *>(run + 1) + (warp - 4), abort_flag);
     }
 
     ptx::tc_fence_before();
