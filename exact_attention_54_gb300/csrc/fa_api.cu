@@ -1290,8 +1290,9 @@ fa_status_t fa_kv_evict(void *k_cache, void *v_cache, const float *weights, cons
     p.sinks = sinks;
     p.recent = recent;
     p.err = device_error_word();
-    if (p.err == nullptr) return FA_ERR_CUDA;
-    const cudaError_t e = fa::launch_kv_evict(D, p, static_cast<cudaStream_t>(stream));
+    const int sms = num_sms();
+    if (p.err == nullptr || sms <= 0) return FA_ERR_CUDA;
+    const cudaError_t e = fa::launch_kv_evict(D, p, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

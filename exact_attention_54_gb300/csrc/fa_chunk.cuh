@@ -105,6 +105,9 @@ struct Part {
     bool whole;   // the unit's only part
     int slot;     // of the CTA's two in the workspace, else
     int parts;    // first of several parts: their number, else 0
+    // One query tile, several key tiles: both softmax warpgroups take it, every
+    // second key tile each, so that its steps overlap like two query tiles' do.
+    __device__ __forceinline__ bool solo() const { return k.ntok[1] == 0 && s1 - s0 > 1; }
 };
 
 // Where a role is in its CTA's run.
@@ -171,6 +174,17 @@ struct Kept {
     Walk walk;
     int tok0, ntok, h0, dest;  // packed row of the tile's first token; tokens; first head; slot, or -1: the unit's only part
 };
+
+// Shared memory behind the barriers.
+struct Shared {
+    Run run;
+    unsigned long long solo_ml, solo_done;  // barriers: warpgroup 1's m and l are written; its O has been read
+    Kept kept[8];
+    float2 ml[kBlockM];
+};
+
+template <int D>
+constexpr int kSmemBytes = FwdShape<D>::kSmemBytes + 128;  // Shared is larger than the packed forward's table
 
 // ------------------------------------------------------------------ roles --
 
@@ -328,8 +342,8 @@ __device__ void mma(const ChunkParams &p, uint32_t sbase, uint32_t tmem, const v
     constexpr uint64_t kTile16 = S::kTileBytes >> 4;
 
     // products as in the packed forward
-    auto issue_qk = [&](int t, uint32_t stage) {
-        const uint64_t qd = dq0 + static_cast<uint64_t>(t) * kTile16, kd = dk0 + static_cast<uint64_t>(stage) * kTile16;
+    auto issue_qk = [&](int t, uint32_t stage, int q_tile) {
+        const uint64_t qd = dq0 + static_cast<uint64_t>(q_tile) * kTile16, kd = dk0 + static_cast<uint64_t>(stage) * kTile16;
         const uint32_t dst = tmem + S::kTmemS + t * 128;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -360,6 +374,45 @@ __device__ void mma(const ChunkParams &p, uint32_t sbase, uint32_t tmem, const v
         const int total[2] = {visited(u.k, 0, u.s0, u.s1), visited(u.k, 1, u.s0, u.s1)};
         if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kQFull), wi & 1, abort_flag, p.timeout_ns)))) break;
         if (wi == 0 && leader) ptx::bar_arrive(bar(S::kFirstQ));
+        if (u.solo()) {
+            // S of step j goes to buffer j % 2; step j + 2's is issued behind step j's P V
+            auto qk = [&](int j) -> bool {
+                const uint32_t ks = (it + j) % S::kKStages;
+                if (!ptx::warp_all(ptx::bar_wait(bar(S::kKFull + ks), ((it + j) / S::kKStages) & 1, abort_flag, p.timeout_ns)))
+                    return false;
+                ptx::tc_fence_after();
+                if (leader) {
+                    issue_qk(j & 1, ks, 0);
+                    ptx::mma_commit(bar(S::kSFull + (j & 1)));
+                    ptx::mma_commit(bar(S::kKEmpty + ks));
+                    if (j + 1 == n) ptx::mma_commit(bar(S::kQEmpty));
+                }
+                return true;
+            };
+            ok = qk(0) && qk(1);
+            for (int j = 0; j < n && ok; ++j) {
+                const int t = j & 1;
+                const uint32_t vs = (it + j) % S::kVStages;
+                ok = ptx::warp_all(ptx::bar_wait(bar(S::kPFull + t), cnt[t] & 1, abort_flag, p.timeout_ns)) &&
+                     ptx::warp_all(ptx::bar_wait(bar(S::kVFull + vs), ((it + j) / S::kVStages) & 1, abort_flag, p.timeout_ns));
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (leader) issue_pv(t, vs, j > 1, 0);
+                if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kPFull2 + t), cnt[t] & 1, abort_flag, p.timeout_ns)))) break;
+                ptx::tc_fence_after();
+                if (leader) {
+                    issue_pv(t, vs, true, 1);
+                    if (j + 2 >= n) ptx::mma_commit(bar(S::kODone + t));
+                    ptx::mma_commit(bar(S::kVEmpty + vs));
+                }
+                ++cnt[t];
+                if (j + 2 < n) ok = qk(j + 2);
+            }
+            if (!ok) break;
+            it += n;
+            ++wi;
+            continue;
+        }
         {
             const uint32_t ks = it % S::kKStages;
             if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kKFull + ks), (it / S::kKStages) & 1, abort_flag, p.timeout_ns))))
@@ -369,7 +422,7 @@ __device__ void mma(const ChunkParams &p, uint32_t sbase, uint32_t tmem, const v
             for (int t = 0; t < 2; ++t) {
                 if (!visits(u.k, t, u.s0)) continue;
                 if (leader) {
-                    issue_qk(t, ks);
+                    issue_qk(t, ks, t);
                     ptx::mma_commit(bar(S::kSFull + t));
                 }
             }
@@ -414,7 +467,7 @@ __device__ void mma(const ChunkParams &p, uint32_t sbase, uint32_t tmem, const v
                     }
                     ptx::tc_fence_after();
                     if (leader) {
-                        issue_qk(t, kn);
+                        issue_qk(t, kn, t);
                         ptx::mma_commit(bar(S::kSFull + t));
                     }
                 }
@@ -437,7 +490,7 @@ __device__ void mma(const ChunkParams &p, uint32_t sbase, uint32_t tmem, const v
 
 template <int D, bool BF16>
 __device__ void softmax(const ChunkParams &p, uint32_t sbase, uint32_t tmem, int t, int wq, int lane,
-                        const volatile Run *run, Kept *kept, volatile int *abort_flag) {
+                        Shared *sh, volatile int *abort_flag) {
     using S = FwdShape<D>;
     const uint32_t bars = sbase + S::kOffBar;
     auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
@@ -448,22 +501,29 @@ __device__ void softmax(const ChunkParams &p, uint32_t sbase, uint32_t tmem, int
     const float scale_log2 = p.scale_log2;
     uint32_t cnt = 0, items = 0;
     bool ok = true;
-    if (lane == 0) kept->walk.start(p, run);
+    Kept *kept = sh->kept + 4 * t + wq;
+    const uint32_t solo_ml = ptx::smem_addr(&sh->solo_ml), solo_done = ptx::smem_addr(&sh->solo_done);
+    uint32_t solos = 0;
+    if (lane == 0) kept->walk.start(p, &sh->run);
     __syncwarp();
     while (ok) {
         // the key tiles of this part that the query tile visits: [x, x1), then [x2, x3)
-        int x, x1, x2, x3, first, behind;
+        // (of a tile that both warpgroups take: every second one of them)
+        int x, x1, x2, x3, stride, first, behind;
         {
             Walk walk = kept->walk;
             Part u;
             if (!walk.next(p, u)) break;
-            auto mine = [&](const int (&v)[2]) { return t == 0 ? v[0] : v[1]; };
+            const bool solo = u.solo();  // (then its other query tile is empty)
+            auto mine = [&](const int (&v)[2]) { return t == 0 || solo ? v[0] : v[1]; };
             const int up = u.k.lo - u.k.ns, ntok = mine(u.k.ntok);
+            stride = solo ? 2 : 1;
             x = u.s0;
             x1 = min(u.s1, mine(u.k.sink));
             x2 = max(max(mine(u.k.wlo), u.k.ns), u.s0 + up);
             x3 = min(mine(u.k.hi), u.s1 + up);
             if (x >= x1) x1 = x = x2;  // no first run
+            if (solo) x += t;
             first = u.s.L - u.s.Lq + mine(u.k.tok);  // the tile's first position
             behind = p.window > 0 ? first + ntok - 1 - p.window : -1;  // the last key behind its last window
             __syncwarp();
@@ -481,9 +541,12 @@ __device__ void softmax(const ChunkParams &p, uint32_t sbase, uint32_t tmem, int
         float m_used = -CUDART_INF_F;
         float l = 0.f;
         int mine = 0;  // steps taken
-        for (;; ++x) {
-            if (x == x1) x = x2;
-            if (x >= x3 && x >= x1) break;
+        for (;; x += stride) {
+            if (x >= x1) {
+                x += x2 - x1;
+                x1 = INT_MAX;
+            }
+            if (x1 == INT_MAX && x >= x3) break;
             ok = ptx::bar_wait(bar(S::kSFull + t), cnt & 1, abort_flag, p.timeout_ns);
             if (!__all_sync(kFull, ok)) { ok = false; break; }
             ptx::tc_fence_after();
@@ -585,6 +648,65 @@ __device__ void softmax(const ChunkParams &p, uint32_t sbase, uint32_t tmem, int
             ptx::tc_fence_after();
             ++items;
         }
+        const volatile Kept *end = kept;
+        const int dest = end->dest, token = row / p.group;  // token within the tile
+        const bool row_valid = token < end->ntok;           // (it has at most tile_tokens)
+        const size_t part = static_cast<size_t>(2 * blockIdx.x + (dest < 0 ? 0 : dest)) * p.part_rows + t * kBlockM + row;
+        const size_t tok = static_cast<size_t>(end->tok0) + token, h = end->h0 + row - token * p.group;
+        uint16_t *orow = static_cast<uint16_t *>(p.o) + (tok * p.H + h) * D;
+        if (stride == 2) {
+            // the two warpgroups' halves of the keys: warpgroup 0 joins them, a row of
+            // both O is in the same TMEM lane
+            if (t == 1) {
+                sh->ml[row] = make_float2(m_used, l);
+                __syncwarp();
+                if (lane == 0) ptx::bar_arrive(solo_ml);
+                ok = ptx::bar_wait(solo_done, solos++ & 1, abort_flag, p.timeout_ns);
+                if (!__all_sync(kFull, ok)) { ok = false; break; }
+                continue;
+            }
+            ok = ptx::bar_wait(solo_ml, solos++ & 1, abort_flag, p.timeout_ns);
+            if (!__all_sync(kFull, ok)) { ok = false; break; }
+            ptx::tc_fence_after();
+            const float2 other = sh->ml[row];
+            const float m = fmaxf(m_used, other.x);
+            const float f0 = m_used == -CUDART_INF_F ? 0.f : ptx::ex2(m_used - m);
+            const float f1 = other.x == -CUDART_INF_F ? 0.f : ptx::ex2(other.x - m);
+            l = l * f0 + other.y * f1;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const float g0 = dest >= 0 ? f0 : f0 * inv, g1 = dest >= 0 ? f1 : f1 * inv;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t a[32], b[32];
+                ptx::tmem_ld32(tO + c * 32, a);
+                ptx::tmem_ld32(tO + D + c * 32, b);
+                ptx::tmem_ld_wait();
+                ptx::reg_fence(a);
+                ptx::reg_fence(b);
+                auto v = [&](int i) { return fmaf(__uint_as_float(a[i]), g0, __uint_as_float(b[i]) * g1); };
+                if (row_valid && dest >= 0) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        reinterpret_cast<float4 *>(p.o_part + part * D)[8 * c + i / 4] =
+                            make_float4(v(i), v(i + 1), v(i + 2), v(i + 3));
+                } else if (row_valid) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        reinterpret_cast<uint4 *>(orow)[4 * c + i / 8] =
+                            make_uint4(ptx::pack2<BF16>(v(i), v(i + 1)), ptx::pack2<BF16>(v(i + 2), v(i + 3)),
+                                       ptx::pack2<BF16>(v(i + 4), v(i + 5)), ptx::pack2<BF16>(v(i + 6), v(i + 7)));
+                }
+                __syncwarp();  // the next loads are the warp's
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::bar_arrive(solo_done);
+            if (row_valid) {
+                if (dest >= 0) p.ml_part[part] = make_float2(m, l);
+                else p.lse[h * p.total_q + tok] = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
+            }
+            continue;
+        }
         uint32_t o[D / 32][32];
         if (mine > 0) {
 #pragma unroll
@@ -598,20 +720,16 @@ __device__ void softmax(const ChunkParams &p, uint32_t sbase, uint32_t tmem, int
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[c][i] = 0u;
         }
-        const volatile Kept *end = kept;
-        const int dest = end->dest, token = row / p.group;  // token within the tile
-        const bool row_valid = token < end->ntok;           // (it has at most tile_tokens)
         if (dest >= 0) {
             // a part: m, l and O as they are
             if (row_valid) {
-                const size_t at = static_cast<size_t>(2 * blockIdx.x + dest) * p.part_rows + t * kBlockM + row;
-                uint4 *dst = reinterpret_cast<uint4 *>(p.o_part + at * D);
+                uint4 *dst = reinterpret_cast<uint4 *>(p.o_part + part * D);
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c)
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
                         dst[8 * c + i / 4] = make_uint4(o[c][i], o[c][i + 1], o[c][i + 2], o[c][i + 3]);
-                p.ml_part[at] = make_float2(m_used, l);
+                p.ml_part[part] = make_float2(m_used, l);
             }
             continue;
         }
@@ -619,8 +737,7 @@ __device__ void softmax(const ChunkParams &p, uint32_t sbase, uint32_t tmem, int
         const float inv_l = l == 0.f ? 0.f : 1.f / l;
         const float lse = l == 0.f ? -CUDART_INF_F : (m_used + __log2f(l)) * 0.69314718055994531f;
         if (row_valid) {
-            const size_t tok = static_cast<size_t>(end->tok0) + token, h = end->h0 + row - token * p.group;
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o) + (tok * p.H + h) * D);
+            uint4 *dst = reinterpret_cast<uint4 *>(orow);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c)
 #pragma unroll
@@ -647,8 +764,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t sbase = ptx::smem_addr(smem);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kOffMisc + 4);
-    Run *run = reinterpret_cast<Run *>(smem + S::kOffSched);
-    static_assert(sizeof(Run) + 8 * sizeof(Kept) <= kSchedInts * 4 && (kPlanEntries + 1) * 8 <= S::kOffBar, "scratch");
+    Shared *sh = reinterpret_cast<Shared *>(smem + S::kOffSched);
+    Run *run = &sh->run;
+    static_assert(S::kOffSched + sizeof(Shared) + 1024 <= kSmemBytes<D> && kSmemBytes<D> <= 227 * 1024 &&
+                      (kPlanEntries + 1) * 8 <= S::kOffBar,
+                  "shared memory budget");
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
     ptx::grid_launch_dependents();
@@ -658,6 +778,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const bool p_full = i >= S::kPFull && i < S::kODone;
             ptx::bar_init(bars + 8u * i, p_full ? kBlockM / 32 : 1u);
         }
+        ptx::bar_init(ptx::smem_addr(&sh->solo_ml), kBlockM / 32);
+        ptx::bar_init(ptx::smem_addr(&sh->solo_done), kBlockM / 32);
         *abort_flag = 0;
         ptx::bar_init_fence();
         ptx::prefetch_tmap(&tm_q);
@@ -692,8 +814,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (u.parts > 0) rec = make_int4(u.b, u.hk, u.pair, 2 * u.parts + u.slot);
         if (lane == 0) p.records[blockIdx.x] = rec;
     } else {
-        softmax<D, BF16>(p, sbase, tmem, (warp - 4) / 4, warp % 4, lane, run,
-                         reinterpret_cast<Kept *>(run + 1) + (warp - 4), abort_flag);
+        softmax<D, BF16>(p, sbase, tmem, (warp - 4) / 4, warp % 4, lane, sh, abort_flag);
     }
 
     ptx::tc_fence_before();
@@ -755,7 +876,7 @@ template <int D, bool BF16>
 cudaError_t launch_t(const CUtensorMap *maps, const ChunkParams &p, int grid, cudaStream_t st) {
     static std::atomic<unsigned long long> done{0};
     auto kern = fa_chunk_kernel<D, BF16>;
-    constexpr int kSmem = FwdShape<D>::kSmemBytes;
+    constexpr int kSmem = kSmemBytes<D>;
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), kSmem, done);
     if (e != cudaSuccess) return e;
     kern<<<grid, kFwdThreads, kSmem, st>>>(maps[0], maps[1], maps[2], p);

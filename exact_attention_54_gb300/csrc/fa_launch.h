@@ -277,7 +277,7 @@ struct EvictParams {
     int *err;                   // device error word
 };
 
-cudaError_t launch_kv_evict(int D, EvictParams p, cudaStream_t stream);
+cudaError_t launch_kv_evict(int D, EvictParams p, int sms, cudaStream_t stream);
 
 // What the kernels of chunks of queries over a paged 16-bit cache share.
 struct PagedParams {

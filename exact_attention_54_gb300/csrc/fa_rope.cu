@@ -23,10 +23,9 @@
 namespace fa {
 namespace rope {
 
-constexpr int kThreads = 128;
-constexpr int kInFlight = 4;   // rows of a lane group with their loads in flight
+constexpr int kThreads = 64;
+constexpr int kInFlight = 2;   // rows of a lane group with their loads in flight
 constexpr int kMaxTokens = 8;  // of a CTA
-constexpr int kMaxPairs = 512; // D = 1024
 
 // Two pieces of 8 columns of a row.
 struct Pieces {
@@ -92,34 +91,38 @@ struct Lane {
     }
 };
 
-// Rows [0, rows) of a CTA, lane group by lane group: row(r, src, dst, token)
-// says where row r is read and written (dst NULL: nowhere) and which of the
-// CTA's tokens turns it (-1: none, copied).
-template <bool BF16, bool INTER, class Row>
-__device__ __forceinline__ void stream_rows(const RopeParams &p, int D, const float2 *turns, int rows, Row row) {
-    const int lanes = D / 16, groups = kThreads / lanes;
+// Rows [0, rows) of a CTA, lane group by lane group: source(r) is where row r is
+// read; target(r, dst, token) where it is written (dst NULL: nowhere) and which of
+// the CTA's tokens turns it (-1: none, copied). ready() is called once, behind
+// the first loads; what target and the turning need may be made there.
+template <bool BF16, bool INTER, class Source, class Ready, class Target>
+__device__ __forceinline__ void stream_rows(const RopeParams &p, const float2 *turns, int rows, Source source,
+                                            Ready ready, Target target) {
+    const int lanes = p.D / 16, groups = kThreads / lanes;
     const int sub = threadIdx.x % lanes, pairs = p.rot_dim / 2;
     const Lane l(sub, p.rot_dim, INTER);
-    for (int r0 = threadIdx.x / lanes; r0 < rows; r0 += groups * kInFlight) {
+    bool first = true;
+    for (int r0 = threadIdx.x / lanes; first || r0 < rows; r0 += groups * kInFlight) {
         Pieces x[kInFlight];
-        uint16_t *dst[kInFlight];
-        int token[kInFlight];
 #pragma unroll
         for (int i = 0; i < kInFlight; ++i) {
-            dst[i] = nullptr;
             if (r0 + i * groups >= rows) continue;
-            const uint16_t *src;
-            row(r0 + i * groups, src, dst[i], token[i]);
-            if (dst[i] == nullptr) continue;
+            const uint16_t *src = source(r0 + i * groups);
             x[i].a = __ldcs(reinterpret_cast<const uint4 *>(src + l.a));
             x[i].b = __ldcs(reinterpret_cast<const uint4 *>(src + l.b));
         }
+        if (first) ready();
+        first = false;
 #pragma unroll
         for (int i = 0; i < kInFlight; ++i) {
-            if (dst[i] == nullptr) continue;
-            if (l.turned && token[i] >= 0) rotate<BF16, INTER>(x[i], turns + token[i] * pairs + l.pair);
-            *reinterpret_cast<uint4 *>(dst[i] + l.a) = x[i].a;
-            *reinterpret_cast<uint4 *>(dst[i] + l.b) = x[i].b;
+            if (r0 + i * groups >= rows) continue;
+            uint16_t *dst;
+            int token;
+            target(r0 + i * groups, dst, token);
+            if (dst == nullptr) continue;
+            if (l.turned && token >= 0) rotate<BF16, INTER>(x[i], turns + token * pairs + l.pair);
+            *reinterpret_cast<uint4 *>(dst + l.a) = x[i].a;
+            *reinterpret_cast<uint4 *>(dst + l.b) = x[i].b;
         }
     }
 }
@@ -130,17 +133,23 @@ __global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RopeParams p) {
     const long long b = static_cast<long long>(blockIdx.z) * gridDim.y + blockIdx.y;
     if (b >= p.num_seqs) return;
     const int s0 = static_cast<int>(blockIdx.x) * p.tokens, n = min(p.tokens, p.total - s0);
-    fill_turns(p, turns, n, [&](int t) -> long long {
-        return p.positions == nullptr ? s0 + t : p.positions[b * p.total + s0 + t];
-    });
     const uint16_t *src0 = static_cast<const uint16_t *>(p.q) + b * p.q_batch + s0 * p.q_stride;
     uint16_t *dst0 = static_cast<uint16_t *>(p.q_out) + b * p.o_batch + s0 * p.o_stride;
-    stream_rows<BF16, INTER>(p, p.D, turns, n * p.H, [&](int r, const uint16_t *&src, uint16_t *&dst, int &token) {
-        token = r / p.H;
-        const int h = r - token * p.H;
-        src = src0 + token * p.q_stride + h * p.q_head;
-        dst = dst0 + token * p.o_stride + h * p.o_head;
-    });
+    stream_rows<BF16, INTER>(
+        p, turns, n * p.H,
+        [&](int r) {
+            const int t = r / p.H;
+            return src0 + t * p.q_stride + (r - t * p.H) * p.q_head;
+        },
+        [&] {
+            fill_turns(p, turns, n, [&](int t) -> long long {
+                return p.positions == nullptr ? s0 + t : p.positions[b * p.total + s0 + t];
+            });
+        },
+        [&](int r, uint16_t *&dst, int &token) {
+            token = r / p.H;
+            dst = dst0 + token * p.o_stride + (r - token * p.H) * p.o_head;
+        });
 }
 
 template <bool BF16, bool INTER>
@@ -159,36 +168,44 @@ __global__ void __launch_bounds__(kThreads) fa_rope_kv_write_kernel(const RopePa
     const int first = t0 + i0, n = min(p.tokens, t1 - t0 - i0);
     if (n <= 0) return;
     const long long pos0 = static_cast<long long>(start) + i0;
-    if (threadIdx.x < n) {
-        const long long pos = pos0 + threadIdx.x, blk = pos >> p.log2_bs;
-        const int page = blk < p.max_blocks ? p.block_table[b * p.max_blocks + blk] : -1;
-        const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_blocks);
-        if (!ok) atomicExch(p.err, kDeviceErrBadIndex);
-        rows[threadIdx.x] =
-            ok ? ((static_cast<long long>(page) * p.Hkv) << p.log2_bs) + (pos & ((1 << p.log2_bs) - 1)) : -1;
-    }
-    fill_turns(p, turns, n, [&](int t) -> long long {
-        return p.positions == nullptr ? pos0 + t : p.positions[first + t];
-    });
     const int per = p.H + 2 * p.Hkv;
-    stream_rows<BF16, INTER>(p, p.D, turns, n * per, [&](int r, const uint16_t *&src, uint16_t *&dst, int &token) {
-        const int t = r / per, h = r - t * per;
-        const long long at = first + t;
-        token = t;
-        if (h < p.H) {
-            src = static_cast<const uint16_t *>(p.q) + at * p.q_stride + static_cast<long long>(h) * p.D;
-            dst = static_cast<uint16_t *>(p.q_out) + (at * p.H + h) * p.D;
-            return;
-        }
-        const bool value = h >= p.H + p.Hkv;
-        const int hk = h - p.H - (value ? p.Hkv : 0);
-        src = value ? static_cast<const uint16_t *>(p.v) + at * p.v_stride + static_cast<long long>(hk) * p.D
-                    : static_cast<const uint16_t *>(p.k) + at * p.k_stride + static_cast<long long>(hk) * p.D;
-        if (value) token = -1;
-        if (rows[t] < 0) return;
-        dst = static_cast<uint16_t *>(value ? p.v_cache : p.k_cache) +
-              (rows[t] + (static_cast<long long>(hk) << p.log2_bs)) * p.D;
-    });
+    stream_rows<BF16, INTER>(
+        p, turns, n * per,
+        [&](int r) {
+            const int t = r / per, h = r - t * per;
+            const long long at = first + t;
+            if (h < p.H) return static_cast<const uint16_t *>(p.q) + at * p.q_stride + static_cast<long long>(h) * p.D;
+            if (h < p.H + p.Hkv)
+                return static_cast<const uint16_t *>(p.k) + at * p.k_stride + static_cast<long long>(h - p.H) * p.D;
+            return static_cast<const uint16_t *>(p.v) + at * p.v_stride + static_cast<long long>(h - p.H - p.Hkv) * p.D;
+        },
+        [&] {
+            if (threadIdx.x < n) {
+                const long long pos = pos0 + threadIdx.x, blk = pos >> p.log2_bs;
+                const int page = blk < p.max_blocks ? p.block_table[b * p.max_blocks + blk] : -1;
+                const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_blocks);
+                if (!ok) atomicExch(p.err, kDeviceErrBadIndex);
+                rows[threadIdx.x] =
+                    ok ? ((static_cast<long long>(page) * p.Hkv) << p.log2_bs) + (pos & ((1 << p.log2_bs) - 1)) : -1;
+            }
+            fill_turns(p, turns, n, [&](int t) -> long long {
+                return p.positions == nullptr ? pos0 + t : p.positions[first + t];
+            });
+        },
+        [&](int r, uint16_t *&dst, int &token) {
+            const int t = r / per, h = r - t * per;
+            if (h < p.H) {
+                token = t;
+                dst = static_cast<uint16_t *>(p.q_out) + (static_cast<long long>(first + t) * p.H + h) * p.D;
+                return;
+            }
+            const bool value = h >= p.H + p.Hkv;
+            const int hk = h - p.H - (value ? p.Hkv : 0);
+            token = value ? -1 : t;
+            dst = rows[t] < 0 ? nullptr
+                              : static_cast<uint16_t *>(value ? p.v_cache : p.k_cache) +
+                                    (rows[t] + (static_cast<long long>(hk) << p.log2_bs)) * p.D;
+        });
 }
 
 }  // namespace rope

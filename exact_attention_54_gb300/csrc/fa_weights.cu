@@ -289,6 +289,10 @@ __device__ void mma(const WeightsParams &p, uint32_t sbase, uint32_t tmem, const
     ptx::bar_wait(bar(S::kTeardown), 0, nullptr, p.timeout_ns);
 }
 
+__device__ __forceinline__ void load_pairs(uint32_t at, uint64_t (&x)[2]) {
+    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(x[0]), "=l"(x[1]) : "r"(at));
+}
+
 // Sums of one key tile's rows, one key per thread.
 template <int D>
 __device__ void sums(const WeightsParams &p, uint32_t sbase, uint32_t tmem, int t, int wq, int lane,
@@ -305,6 +309,8 @@ __device__ void sums(const WeightsParams &p, uint32_t sbase, uint32_t tmem, int 
     while (ok && walk.next(u)) {
         const int k0 = u.k0 + t * kBlockN, key = k0 + row;
         const int pos0 = u.s.L - u.s.Lq;
+        float *w = p.weights + (static_cast<size_t>(u.b) * p.Hkv + u.hk) * (static_cast<size_t>(p.max_blocks) << p.log2_bs);
+        const float before = key < u.s.L ? w[key] : 0.f;  // ahead of its use
         uint64_t sum[4] = {0, 0, 0, 0};  // pairs of zeros
         for (int j = 0; j < u.steps; ++j, ++it) {
             const int t0 = u.t0 + j * p.tile_tokens, n = min(p.tile_tokens, u.t1 - t0), first = pos0 + t0;
@@ -326,55 +332,72 @@ __device__ void sums(const WeightsParams &p, uint32_t sbase, uint32_t tmem, int 
                 c1 *= p.group;
             }
             const uint32_t ring = sbase + S::kOffL + ls * 512;
+            // exponentials of columns c and c + 1 of a chunk of 32
+            auto pair = [&](const uint32_t (&s)[32], int c, uint64_t nl, float &e0, float &e1) {
+                float x0, x1;
+                ptx::upk2(ptx::ffma2(ptx::pk2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, nl), x0, x1);
+                e0 = ptx::ex2(x0);
+                e1 = ptx::ex2(x1);
+            };
+            if (!masked && p.chunks == 4) {
+                // the whole row at once: one wait, and the buffer is free again
+                uint32_t s[4][32];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (b >= p.chunks) break;
-                uint32_t s[32];
-                ptx::tmem_ld32(tS + 128 * buf + 32 * b, s);
+                for (int b = 0; b < 4; ++b) ptx::tmem_ld32(tS + 128 * buf + 32 * b, s[b]);
                 ptx::tmem_ld_wait();
-                ptx::reg_fence(s);
-                uint32_t seen = 0xffffffffu;
-                if (masked) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b) ptx::reg_fence(s[b]);
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::bar_arrive(bar(S::kSEmpty + 2 * t + buf));
+#pragma unroll
+                for (int c = 0; c < 128; c += 4) {
+                    uint64_t nl[2];
+                    load_pairs(ring + 4 * c, nl);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float e0, e1;
+                        pair(s[c / 32], c % 32 + 2 * h, nl[h], e0, e1);
+                        sum[(c / 2 + h) % 4] = ptx::fadd2(sum[(c / 2 + h) % 4], ptx::pk2(e0, e1));
+                    }
+                }
+            } else {
+                for (int b = 0; b < p.chunks; ++b) {
+                    uint32_t s[32];
+                    ptx::tmem_ld32(tS + 128 * buf + 32 * b, s);
+                    ptx::tmem_ld_wait();
+                    ptx::reg_fence(s);
                     auto below = [](int x) -> uint32_t {
                         return static_cast<uint32_t>((1ull << min(max(x, 0), 32)) - 1);
                     };
-                    seen = below(c1 - 32 * b) & ~below(c0 - 32 * b);
-                }
+                    const uint32_t seen = below(c1 - 32 * b) & ~below(c0 - 32 * b);
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    uint64_t nl[2];
-                    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];"
-                                 : "=l"(nl[0]), "=l"(nl[1])
-                                 : "r"(ring + 128 * b + 4 * i));
+                    for (int c = 0; c < 32; c += 4) {
+                        uint64_t nl[2];
+                        load_pairs(ring + 128 * b + 4 * c, nl);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int c = i + 2 * h;
-                        float x0, x1;
-                        ptx::upk2(ptx::ffma2(ptx::pk2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, nl[h]),
-                                  x0, x1);
-                        float e0 = ptx::ex2(x0), e1 = ptx::ex2(x1);
-                        if (masked) {
-                            if (!(seen & (1u << c))) e0 = 0.f;
-                            if (!(seen & (2u << c))) e1 = 0.f;
+                        for (int h = 0; h < 2; ++h) {
+                            float e0, e1;
+                            pair(s, c + 2 * h, nl[h], e0, e1);
+                            if (!(seen & (1u << (c + 2 * h)))) e0 = 0.f;
+                            if (!(seen & (2u << (c + 2 * h)))) e1 = 0.f;
+                            sum[(c / 2 + h) % 4] = ptx::fadd2(sum[(c / 2 + h) % 4], ptx::pk2(e0, e1));
                         }
-                        sum[(c / 2) % 4] = ptx::fadd2(sum[(c / 2) % 4], ptx::pk2(e0, e1));
                     }
                 }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::bar_arrive(bar(S::kSEmpty + 2 * t + buf));
             }
-            ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                ptx::bar_arrive(bar(S::kSEmpty + 2 * t + buf));
-                ptx::bar_arrive(bar(S::kLEmpty + ls));
-            }
+            if (lane == 0) ptx::bar_arrive(bar(S::kLEmpty + ls));
         }
         if (!ok) break;
         if (key < u.s.L) {
             float a0, a1, b0, b1;
             ptx::upk2(ptx::fadd2(sum[0], sum[1]), a0, a1);
             ptx::upk2(ptx::fadd2(sum[2], sum[3]), b0, b1);
-            float *w = p.weights + (static_cast<size_t>(u.b) * p.Hkv + u.hk) * (static_cast<size_t>(p.max_blocks) << p.log2_bs);
-            w[key] += (a0 + a1) + (b0 + b1);
+            w[key] = before + ((a0 + a1) + (b0 + b1));
         }
     }
 }
