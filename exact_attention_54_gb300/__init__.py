@@ -128,7 +128,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.fa_fwd_paged.argtypes = [vp] * 9 + [sz] + [i] * 11 + [f, i, vp]
         lib.fa_fwd_paged_workspace_bytes.argtypes = [i] * 4
         lib.fa_fwd_paged_workspace_bytes.restype = sz
-        lib.fa_kv_weights.argtypes = [vp] * 7 + [ll] * 2 + [i] * 11 + [f, i, vp]
+        lib.fa_kv_weights.argtypes = [vp] * 7 + [ll] * 2 + [i] * 12 + [f, i, vp]
         lib.fa_kv_evict.argtypes = [vp] * 9 + [i] * 11 + [vp]
         lib.fa_check_device_error.argtypes = [vp]
         lib.fa_status_string.argtypes = [i]
@@ -520,6 +520,7 @@ _entry = {}  # entry points of the loaded library by name
 # handle of a device's current stream, without a Stream object where PyTorch has that
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _launch(fn: str, stream, tensors, *args, index=None):
@@ -543,7 +544,7 @@ def _launch(fn: str, stream, tensors, *args, index=None):
     if call is None:
         call = _entry[fn] = getattr(load_library(), fn)
     stream = _raw_stream(dev) if stream is None else _stream(stream)
-    if torch.cuda.current_device() != dev:
+    if _current_device() != dev:
         with torch.cuda.device(dev):
             st = call(*ptrs, *args, stream)
     else:
@@ -915,6 +916,12 @@ def _rows(name, t, dtype):
     one)."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.is_contiguous():
+        if len(t.shape) == 3:
+            _, H, D = t.shape
+            return 0, H * D, D
+        _, H, S, D = t.shape
+        return H * S * D, D, S * D
     st = [0 if n == 1 else s for n, s in zip(t.shape, t.stride())]
     if t.shape[-1] > 1 and st[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
@@ -927,18 +934,22 @@ def fa_rope(x, y, inv_freq, positions=None, interleaved: bool = False, mscale: f
             stream=None):
     """Rotate rows x [total,H,D] or [B,H,S,D] into y (which may be x), or with ``inverse`` their gradient; any strides
     that are multiples of 8. positions int32 [total] or [B,S] (None: 0, 1, ...); inv_freq fp32 [rot_dim/2]."""
-    if x.dim() not in (3, 4):
+    shape = x.shape
+    if len(shape) == 3:
+        B, (S, H, D) = 1, shape
+    elif len(shape) == 4:
+        B, H, S, D = shape
+    else:
         raise ValueError("x must be [total,H,D] or [B,H,S,D]")
-    (B, S, H), D = ((1, *x.shape[:2]) if x.dim() == 3 else (x.shape[0], x.shape[2], x.shape[1])), x.shape[-1]
     code = _dtype_code(x)
-    xs, ys = _rows("x", x, x.dtype), _rows("y", y, x.dtype)
-    if y.shape != x.shape:
-        raise ValueError(f"y must have shape {tuple(x.shape)}, got {tuple(y.shape)}")
-    _expect("inv_freq", inv_freq, (inv_freq.numel(),), torch.float32)
+    if y.shape != shape:
+        raise ValueError(f"y must have shape {tuple(shape)}, got {tuple(y.shape)}")
+    pairs = inv_freq.numel()
+    _expect("inv_freq", inv_freq, (pairs,), torch.float32)
     if positions is not None:
-        _expect("positions", positions, (S,) if x.dim() == 3 else (B, S), torch.int32)
-    _launch("fa_rope", stream, (x, y, inv_freq, positions), B, S, H, D, 2 * inv_freq.numel(), *xs, *ys,
-            int(bool(interleaved)), int(bool(inverse)), float(mscale), code)
+        _expect("positions", positions, (S,) if len(shape) == 3 else (B, S), torch.int32)
+    _launch("fa_rope", stream, (x, y, inv_freq, positions), B, S, H, D, 2 * pairs, *_rows("x", x, x.dtype),
+            *_rows("y", y, x.dtype), int(bool(interleaved)), int(bool(inverse)), float(mscale), code)
 
 
 def fa_rope_kv_write(q, k, v, q_out, k_cache, v_cache, block_table, cu_seqlens, max_seqlen: int, inv_freq=None,
@@ -956,10 +967,11 @@ def fa_rope_kv_write(q, k, v, q_out, k_cache, v_cache, block_table, cu_seqlens, 
         if t is None and name == "q":
             strides.append(0)
             continue
-        if t.dim() != 3 or t.shape[0] != total or t.shape[2] != D or (name == "v" and t.shape[1] != Hkv):
-            raise ValueError(f"{name} must be [total,heads,D] with the total and D of k, got {tuple(t.shape)}")
+        shape = t.shape
+        if len(shape) != 3 or shape[0] != total or shape[2] != D or (name == "v" and shape[1] != Hkv):
+            raise ValueError(f"{name} must be [total,heads,D] with the total and D of k, got {tuple(shape)}")
         _, token, head = _rows(name, t, k.dtype)
-        if t.shape[1] > 1 and head != D:
+        if shape[1] > 1 and head != D:
             raise ValueError(f"{name}: a token's heads must be contiguous")
         strides.append(token)
     if q is not None:
@@ -967,11 +979,12 @@ def fa_rope_kv_write(q, k, v, q_out, k_cache, v_cache, block_table, cu_seqlens, 
         _expect("q_out", q_out, (total, H, D), k.dtype)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _expect(name, t, (num_blocks, Hkv, block_size, D), k.dtype)
-    n = cu_seqlens.numel() - 1
+    pages = (num_blocks, Hkv, block_size, D)
+    _expect("k_cache", k_cache, pages, k.dtype)
+    _expect("v_cache", v_cache, pages, k.dtype)
+    n, max_blocks = cu_seqlens.numel() - 1, block_table.shape[-1]
     _expect("cu_seqlens", cu_seqlens, (n + 1,), torch.int32)
-    _expect("block_table", block_table, (n, block_table.shape[-1]), torch.int32)
+    _expect("block_table", block_table, (n, max_blocks), torch.int32)
     if starts is not None:
         _expect("starts", starts, (n,), torch.int32)
     if positions is not None:
@@ -982,12 +995,15 @@ def fa_rope_kv_write(q, k, v, q_out, k_cache, v_cache, block_table, cu_seqlens, 
         rot_dim = 2 * inv_freq.numel()
     _launch("fa_rope_kv_write", stream, (q, k, v, q_out, k_cache, v_cache, inv_freq, positions, block_table,
                                          cu_seqlens, starts),
-            n, total, _int32(max_seqlen), H, Hkv, D, rot_dim, *strides, num_blocks, block_size, block_table.shape[1],
+            n, total, _int32(max_seqlen), H, Hkv, D, rot_dim, *strides, num_blocks, block_size, max_blocks,
             int(bool(interleaved)), float(mscale), code)
 
 
 def fa_fwd_paged_workspace_bytes(max_seqlen_q: int, H: int, Hkv: int, D: int) -> int:
-    return int(load_library().fa_fwd_paged_workspace_bytes(*map(_int32, (max_seqlen_q, H, Hkv, D))))
+    call = _entry.get("fa_fwd_paged_workspace_bytes")
+    if call is None:
+        call = _entry["fa_fwd_paged_workspace_bytes"] = load_library().fa_fwd_paged_workspace_bytes
+    return call(_int32(max_seqlen_q), _int32(H), _int32(Hkv), _int32(D))
 
 
 def fa_fwd_paged(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, o, lse, workspace, max_seqlen_q: int,
@@ -1018,9 +1034,9 @@ def fa_fwd_paged(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, o, ls
 
 
 def fa_kv_weights(q, lse, k_cache, block_table, cu_seqlens_q, seq_lens, weights, max_seqlen_q: int, window: int = 0,
-                  sinks: int = 0, scale: float | None = None, stream=None):
-    """Add to weights fp32 [num_seqs,Hkv,max_blocks*block_size] what the chunks' queries q [total_q,H,D] gave to each key
-    of pages k_cache [num_blocks,Hkv,block_size,D]; lse fp32 [H,total_q] of that attention, of any strides (the
+                  sinks: int = 0, scale: float | None = None, add: bool = True, stream=None):
+    """Add to (or with add False put into) weights fp32 [num_seqs,Hkv,max_blocks*block_size] what the chunks' queries q
+    [total_q,H,D] gave to each key of pages k_cache [num_blocks,Hkv,block_size,D]; lse fp32 [H,total_q] of that attention, of any strides (the
     transpose of a decode's [B,H]); the rest as fa_fwd_paged."""
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [total_q,H,D] and pages [num_blocks,Hkv,block_size,D]")
@@ -1041,7 +1057,7 @@ def fa_kv_weights(q, lse, k_cache, block_table, cu_seqlens_q, seq_lens, weights,
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     _launch("fa_kv_weights", stream, (q, lse, k_cache, block_table, cu_seqlens_q, seq_lens, weights), *lse.stride(), n, Tq,
             _int32(max_seqlen_q), H, Hkv, D, num_blocks, block_size, block_table.shape[1], _int32(window), _int32(sinks),
-            float(scale), code)
+            int(bool(add)), float(scale), code)
 
 
 def fa_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, kept, new_lens, new_weights, sinks: int = 0,
@@ -1069,12 +1085,17 @@ def fa_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, kep
             _int32(recent), code)
 
 
+def _empty_as(t):
+    """An uninitialised contiguous tensor of the shape of ``t``."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def flash_rope(x, inv_freq, positions=None, interleaved: bool = False, mscale: float = 1.0, stream=None):
     """Returns x [total,H,D] or [B,H,S,D] with rotary positions (see fa_rope), contiguous."""
     if stream is not None:
         with _on_stream(stream, x):
             return flash_rope(x, inv_freq, positions, interleaved, mscale)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = _empty_as(x)
     fa_rope(x, y, inv_freq, positions, interleaved, mscale)
     return y
 
@@ -1084,7 +1105,7 @@ def flash_rope_bwd(dy, inv_freq, positions=None, interleaved: bool = False, msca
     if stream is not None:
         with _on_stream(stream, dy):
             return flash_rope_bwd(dy, inv_freq, positions, interleaved, mscale)
-    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+    dx = _empty_as(dy)
     fa_rope(dy, dx, inv_freq, positions, interleaved, mscale, inverse=True)
     return dx
 
@@ -1097,7 +1118,7 @@ def flash_rope_kv_write(q, k, v, k_cache, v_cache, block_table, cu_seqlens, max_
         with _on_stream(stream, k):
             return flash_rope_kv_write(q, k, v, k_cache, v_cache, block_table, cu_seqlens, max_seqlen, inv_freq, starts,
                                        positions, interleaved, mscale)
-    q_out = None if q is None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    q_out = None if q is None else _empty_as(q)
     fa_rope_kv_write(q, k, v, q_out, k_cache, v_cache, block_table, cu_seqlens, max_seqlen, inv_freq, starts, positions,
                      interleaved, mscale)
     return q_out
@@ -1115,7 +1136,12 @@ def flash_attention_paged(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_le
         raise ValueError("q must be [total_q,H,D] and pages [num_blocks,Hkv,block_size,D]")
     Tq, H, D = q.shape
     if workspace is None:
-        n = fa_fwd_paged_workspace_bytes(max_seqlen_q, H, k_cache.shape[1], D)
+        dev = q.get_device()
+        if dev >= 0 and dev != _current_device():  # (its size depends on the GPU)
+            with torch.cuda.device(dev):
+                n = fa_fwd_paged_workspace_bytes(max_seqlen_q, H, k_cache.shape[1], D)
+        else:
+            n = fa_fwd_paged_workspace_bytes(max_seqlen_q, H, k_cache.shape[1], D)
         workspace = torch.empty(_words(n), dtype=torch.float32, device=q.device)
     o, lse = torch.empty_like(q), torch.empty((H, Tq), dtype=torch.float32, device=q.device)
     fa_fwd_paged(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_lens, o, lse, workspace, max_seqlen_q, window, sinks,
@@ -1126,15 +1152,16 @@ def flash_attention_paged(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_le
 def flash_kv_weights(q, lse, k_cache, block_table, cu_seqlens_q, seq_lens, max_seqlen_q: int, window: int = 0,
                      sinks: int = 0, scale: float | None = None, weights=None, stream=None):
     """Returns ``weights`` [num_seqs,Hkv,max_blocks*block_size] with what the chunks gave to each key added (see
-    fa_kv_weights); None: added to zeros."""
+    fa_kv_weights); None: a new tensor with that alone."""
     if stream is not None:
         with _on_stream(stream, q):
             return flash_kv_weights(q, lse, k_cache, block_table, cu_seqlens_q, seq_lens, max_seqlen_q, window, sinks,
                                     scale, weights)
-    if weights is None:
-        weights = torch.zeros((block_table.shape[0], k_cache.shape[1], block_table.shape[-1] * k_cache.shape[2]),
+    add = weights is not None
+    if not add:
+        weights = torch.empty((block_table.shape[0], k_cache.shape[1], block_table.shape[-1] * k_cache.shape[2]),
                               dtype=torch.float32, device=q.device)
-    fa_kv_weights(q, lse, k_cache, block_table, cu_seqlens_q, seq_lens, weights, max_seqlen_q, window, sinks, scale)
+    fa_kv_weights(q, lse, k_cache, block_table, cu_seqlens_q, seq_lens, weights, max_seqlen_q, window, sinks, scale, add)
     return weights
 
 

@@ -1209,7 +1209,7 @@ fa_status_t fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache
         return FA_ERR_CUDA;
     p.o = o;
     p.lse = lse;
-    p.min_run = 6;
+    p.min_run = 1;
     p.o_part = workspace;
     p.ml_part = reinterpret_cast<float2 *>(workspace + c.o_floats);
     p.part_rows = c.part_rows;
@@ -1221,8 +1221,8 @@ fa_status_t fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache
 fa_status_t fa_kv_weights(const void *q, const float *lse, const void *k_cache, const int32_t *block_table,
                           const int32_t *cu_seqlens_q, const int32_t *seq_lens, float *weights, int64_t lse_head,
                           int64_t lse_token, int num_seqs, int total_q, int max_seqlen_q, int H, int Hkv, int D,
-                          int num_blocks, int block_size, int max_blocks_per_seq, int window, int sinks, float scale,
-                          fa_dtype_t dtype, void *stream) {
+                          int num_blocks, int block_size, int max_blocks_per_seq, int window, int sinks, int add,
+                          float scale, fa_dtype_t dtype, void *stream) {
     if (!q || !lse || !k_cache || !block_table || !cu_seqlens_q || !seq_lens || !weights) return FA_ERR_NULL;
     if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_DTYPE;
     if (D != 64 && D != 128) return FA_ERR_HEADDIM;
@@ -1245,6 +1245,7 @@ fa_status_t fa_kv_weights(const void *q, const float *lse, const void *k_cache, 
     p.lse_head = lse_head;
     p.lse_token = lse_token;
     p.weights = weights;
+    p.add = add != 0;
     p.min_run = 1;
     const cudaError_t e = fa::launch_kv_weights(D, bf16, maps, p, num_sms(), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;

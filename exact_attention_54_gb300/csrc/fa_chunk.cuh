@@ -94,6 +94,7 @@ struct Units {
     const ChunkParams &p;
     __device__ __forceinline__ int count(const Seq &s) const { return pairs_of(p, s); }
     __device__ __forceinline__ int cost(const Seq &s, int i) const { return tiles_of(p, s, i).steps + kStart; }
+    __device__ __forceinline__ int2 flat(const Seq &, int) const { return make_int2(0, 0); }
 };
 
 // The parts of a CTA's run, in order; every role walks them for itself.
@@ -125,11 +126,10 @@ struct Walk {
         off = r->off;
         first = 1;
         pairs = 0;
-        s = Seq{0, 0, 0};
-        if (rem > 0) {
-            s = load_seq(p, b);
-            pairs = pairs_of(p, s);
-        }
+        s.q0 = r->s.q0;
+        s.Lq = r->s.Lq;
+        s.L = r->s.L;
+        if (rem > 0) pairs = pairs_of(p, s);
     }
     __device__ __forceinline__ bool next(const ChunkParams &p, Part &o) {
         while (rem > 0) {
@@ -271,6 +271,8 @@ __device__ void producer_v(const CUtensorMap *tv, const ChunkParams &p, uint32_t
     auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
     const bool leader = ptx::elect_one();
     const Pages pages(p);
+    // (test support: the CTA with the first unit's first step)
+    const bool first = blockIdx.x * run->per <= kStart && (blockIdx.x + 1) * run->per > kStart;
     uint32_t it = 0;
     uint32_t cuts = 0, cut_done = 0;  // tiles with rows to clear: loaded, landed
     bool ok = true;
@@ -292,7 +294,7 @@ __device__ void producer_v(const CUtensorMap *tv, const ChunkParams &p, uint32_t
                                      p.timeout_ns))))
                 break;
             const uint32_t dst = sbase + S::kOffV + stage * S::kTileBytes, full = bar(S::kVFull + stage);
-            if (withheld(p.withhold, it)) continue;
+            if (withheld(p.withhold, it, first)) continue;
             if (p.log2_bs < 3) {
                 copy_small_pages<D>(p, at, dead, k0, p.v, dst);
                 if (leader) ptx::bar_arrive(full);
@@ -767,31 +769,33 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     Shared *sh = reinterpret_cast<Shared *>(smem + S::kOffSched);
     Run *run = &sh->run;
     static_assert(S::kOffSched + sizeof(Shared) + 1024 <= kSmemBytes<D> && kSmemBytes<D> <= 227 * 1024 &&
-                      (kPlanEntries + 1) * 8 <= S::kOffBar,
+                      kPlanBytes <= S::kOffBar,
                   "shared memory budget");
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
     ptx::grid_launch_dependents();
-    if (threadIdx.x == 0) {
-        const uint32_t bars = sbase + S::kOffBar;
-        for (int i = 0; i < S::kNumBars; ++i) {
-            const bool p_full = i >= S::kPFull && i < S::kODone;
-            ptx::bar_init(bars + 8u * i, p_full ? kBlockM / 32 : 1u);
+    // the plan's scratch lies where the tiles go
+    plan(p, Units{p}, run, smem);
+    if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t bars = sbase + S::kOffBar;
+            for (int i = 0; i < S::kNumBars; ++i) {
+                const bool p_full = i >= S::kPFull && i < S::kODone;
+                ptx::bar_init(bars + 8u * i, p_full ? kBlockM / 32 : 1u);
+            }
+            ptx::bar_init(ptx::smem_addr(&sh->solo_ml), kBlockM / 32);
+            ptx::bar_init(ptx::smem_addr(&sh->solo_done), kBlockM / 32);
+            *abort_flag = 0;
+            ptx::bar_init_fence();
         }
-        ptx::bar_init(ptx::smem_addr(&sh->solo_ml), kBlockM / 32);
-        ptx::bar_init(ptx::smem_addr(&sh->solo_done), kBlockM / 32);
-        *abort_flag = 0;
-        ptx::bar_init_fence();
+        __syncwarp();
+        ptx::tmem_alloc(ptx::smem_addr(tmem_slot), S::kTmemCols);
+        ptx::tmem_relinquish();
+    } else if (warp == 2 && lane == 0) {
         ptx::prefetch_tmap(&tm_q);
         ptx::prefetch_tmap(&tm_k);
         ptx::prefetch_tmap(&tm_v);
     }
-    if (warp == 1) {
-        ptx::tmem_alloc(ptx::smem_addr(tmem_slot), S::kTmemCols);
-        ptx::tmem_relinquish();
-    }
-    // the plan's scratch lies where the tiles go
-    plan(p, Units{p}, run, reinterpret_cast<unsigned long long *>(smem));
     ptx::fence_proxy_async_smem();
     ptx::tc_fence_before();
     __syncthreads();
@@ -811,7 +815,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         Part u;
         int4 rec = make_int4(0, 0, 0, 0);
         while (walk.next(p, u))
-            if (u.parts > 0) rec = make_int4(u.b, u.hk, u.pair, 2 * u.parts + u.slot);
+            if (u.parts > 0)
+                rec = make_int4(u.s.q0 + u.k.tok[0], u.k.ntok[0] + u.k.ntok[1], u.hk * p.group, 2 * u.parts + u.slot);
         if (lane == 0) p.records[blockIdx.x] = rec;
     } else {
         softmax<D, BF16>(p, sbase, tmem, (warp - 4) / 4, warp % 4, lane, sh, abort_flag);
@@ -836,16 +841,15 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) fa_chunk_join_kernel(const ChunkParams p) {
     constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
     ptx::grid_dependency_wait();
-    const int4 rec = p.records[blockIdx.x];
+    const int4 rec = __ldcg(p.records + blockIdx.x);  // first packed row, tokens, first head, 2 parts + slot of the first
     const int parts = min(rec.w / 2, static_cast<int>(gridDim.x - blockIdx.x)), slot = rec.w & 1;
     if (parts == 0) return;
-    const Seq s = load_seq(p, rec.x);
     const int d = threadIdx.x % kLanes * 4;
     for (int i = threadIdx.x / kLanes; i < kJoinRows; i += kGroups) {
         const int row = blockIdx.y * kJoinRows + i;
         const int r = row % kBlockM, token = r / p.group, head = r - token * p.group;
-        const int tok = (2 * rec.z + row / kBlockM) * p.tile_tokens + token;
-        if (row >= p.part_rows || token >= p.tile_tokens || tok >= s.Lq) continue;
+        const int tok = row / kBlockM * p.tile_tokens + token;
+        if (row >= p.part_rows || token >= p.tile_tokens || tok >= rec.y) continue;
         // part 0 is in the slot it was given, later ones in the first of their CTAs
         auto at = [&](int x) { return static_cast<size_t>(2 * (blockIdx.x + x) + (x == 0 ? slot : 0)) * p.part_rows + row; };
         float m = -CUDART_INF_F, l = 0.f;
@@ -864,7 +868,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_chunk_join_kernel(const Chunk
             o.w = fmaf(o.w, f, v.w * g);
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const size_t t = static_cast<size_t>(s.q0) + tok, h = rec.y * p.group + head;
+        const size_t t = static_cast<size_t>(rec.x) + tok, h = rec.z + head;
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + (t * p.H + h) * D + d) =
             make_uint2(ptx::pack2<BF16>(o.x * inv, o.y * inv), ptx::pack2<BF16>(o.z * inv, o.w * inv));
         if (d == 0)

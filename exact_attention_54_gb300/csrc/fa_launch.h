@@ -316,6 +316,7 @@ struct WeightsParams : PagedParams {
     const float *lse;           // row (head, packed token) at head * lse_head + token * lse_token
     long long lse_head, lse_token;
     float *weights;             // [B, Hkv, max_blocks * block_size]
+    int add;                    // to what is there
     int chunks;                 // columns of a step, in 32s (set by launch_kv_weights)
 };
 

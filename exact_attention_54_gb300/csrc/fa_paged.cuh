@@ -11,7 +11,9 @@ namespace fa {
 namespace paged {
 
 constexpr int kPlanEntries = 4096;  // the plan's table: sums over a sequence, or over several if there are more
-constexpr int kSerialUnits = 16;    // a thread sums the units of a sequence with up to this many, a warp longer ones
+constexpr int kSerialUnits = 16;    // units of a sequence that a thread adds up, rather than a warp,
+constexpr int kPlanLong = 4096;     // where a sequence has more and there are no more than this many such
+constexpr int kPlanBytes = 8 * (kPlanEntries + 1) + 4 * (kPlanLong + 1);
 constexpr unsigned kFull = 0xffffffffu;
 
 // Sequence b's chunk: its rows in the packed queries, its keys.
@@ -30,12 +32,19 @@ __device__ __forceinline__ Seq load_seq(const PagedParams &p, int b) {
 // A CTA's run of the laid-out units, in shared memory.
 struct Run {
     long long len;     // cost units, 0: no work
-    long long per;     // of every CTA but the last
+    long long per;     // of every CTA but the last; 0: nothing is computed
     int b, hk, unit;   // the unit it starts in,
-    int off;           // and where
+    int off;           // and where,
+    Seq s;             // its sequence
 };
 
 // ------------------------------------------------------------------- plan --
+
+// a / b; a 64-bit division costs some 500 clocks of latency.
+__device__ __forceinline__ unsigned long long divide(unsigned long long a, unsigned long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+    return a / b;
+}
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 #pragma unroll
@@ -43,56 +52,80 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
     return v;
 }
 
-// Cost of one key head of a sequence's n units; the whole warp calls it.
+// Cost of one key head of a sequence's n units. Units [flat.x, flat.y) cost the
+// same, the others are added up: by `lanes` threads, of which this is `lane`.
 template <class Units>
-__device__ __forceinline__ unsigned long long seq_cost(const Units &units, const Seq &s, int n) {
+__device__ __forceinline__ unsigned long long seq_cost(const Units &units, const Seq &s, int n, int2 flat, int lane,
+                                                       int lanes) {
     unsigned long long c = 0;
-    for (int i = threadIdx.x % 32; i < n; i += 32) c += units.cost(s, i);
-    return warp_sum(c);
+    for (int i = lane; i < flat.x; i += lanes) c += units.cost(s, i);
+    for (int i = flat.y + lane; i < n; i += lanes) c += units.cost(s, i);
+    if (lane == 0 && flat.y > flat.x) c += static_cast<unsigned long long>(flat.y - flat.x) * units.cost(s, flat.x);
+    return c;
 }
 
-// This CTA's run into `run`; `prefix` is scratch of kPlanEntries + 1 sums.
-// units: count(s) units of each key head of a sequence, cost(s, i) of the i-th.
-// The whole CTA calls it, and synchronises before it reads `run`.
+// This CTA's run into `run`; scratch: kPlanBytes of shared memory. units:
+// count(s) units of each key head of a sequence, cost(s, i) of the i-th, flat(s, n)
+// a range of them that cost the same. The whole CTA calls it, and synchronises
+// before it reads `run`; all warps but the first return while that one looks for
+// the CTA's place, so what else a kernel sets up comes behind this. It stands between
+// a launch and its first load (with one warp adding up all units: 8 us for 16
+// sequences of up to 8192 keys), so a thread takes a sequence with few units to add
+// up, warps share out the others, and nothing divides in 64 bits without need.
 template <class Units>
-__device__ void plan(const PagedParams &p, const Units units, Run *run, unsigned long long *prefix) {
+__device__ void plan(const PagedParams &p, const Units units, Run *run, void *scratch) {
+    unsigned long long *prefix = static_cast<unsigned long long *>(scratch);
+    int *many = reinterpret_cast<int *>(prefix + kPlanEntries + 1), *n_many = many + kPlanLong;
     const int each = (p.B + kPlanEntries - 1) / kPlanEntries, entries = (p.B + each - 1) / each;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    // (a thread's first loads are ahead of the scratch's clearing)
+    int q0 = 0, q1 = 0, keys = 0;
+    if (threadIdx.x < p.B) {
+        q0 = p.cu_q[threadIdx.x];
+        q1 = p.cu_q[threadIdx.x + 1];
+        keys = p.seq_lens[threadIdx.x];
+    }
+    if (threadIdx.x == 0) *n_many = 0;
     for (int i = threadIdx.x; i < entries; i += blockDim.x) prefix[i + 1] = 0;
     __syncthreads();
     bool bad = false;
-    for (int b0 = warp * 32; b0 < p.B; b0 += blockDim.x) {
-        const int b = b0 + lane;
-        Seq s{0, 0, 0};
-        int n = 0;
-        unsigned long long c = 0;
-        if (b < p.B) {
-            const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
-            if (q0 < 0 || q1 < q0 || q1 > p.total_q || q1 - q0 > p.max_q) {
-                bad = true;
-            } else {
-                s = load_seq(p, b);
-                n = units.count(s);
-                if (n <= kSerialUnits)
-                    for (int i = 0; i < n; ++i) c += units.cost(s, i);
-            }
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+        if (b >= blockDim.x) {
+            q0 = p.cu_q[b];
+            q1 = p.cu_q[b + 1];
+            keys = p.seq_lens[b];
         }
-        unsigned more = __ballot_sync(kFull, n > kSerialUnits);
-        while (more != 0) {
-            const int l = __ffs(more) - 1;
-            more &= more - 1;
-            const Seq x{0, __shfl_sync(kFull, s.Lq, l), __shfl_sync(kFull, s.L, l)};
-            const unsigned long long sum = seq_cost(units, x, __shfl_sync(kFull, n, l));
-            if (lane == l) c = sum;
+        const Seq s{q0, q1 - q0, min(max(keys, 0), p.max_blocks << p.log2_bs)};
+        if (q0 < 0 || q1 < q0 || q1 > p.total_q || q1 - q0 > p.max_q) {
+            bad = true;
+            continue;
         }
-        if (c > 0) atomicAdd(&prefix[b / each + 1], c);
+        const int n = units.count(s);
+        const int2 flat = units.flat(s, n);
+        const int at = n - (flat.y - flat.x) > kSerialUnits ? atomicAdd(n_many, 1) : kPlanLong;
+        if (at < kPlanLong) {
+            many[at] = b;
+        } else if (n > 0) {
+            const unsigned long long c = seq_cost(units, s, n, flat, 0, 1);
+            if (c > 0) atomicAdd(&prefix[b / each + 1], c);
+        }
     }
     bad = __syncthreads_or(bad) != 0;
-    if (bad && threadIdx.x == 0) {
-        atomicExch(p.err, kDeviceErrSeqLens);
-        run->len = 0;
+    if (bad) {
+        if (threadIdx.x == 0) {
+            atomicExch(p.err, kDeviceErrSeqLens);
+            run->len = run->per = 0;
+        }
+        return;
     }
-    if (bad || warp != 0) return;
+    for (int i = warp; i < min(*n_many, kPlanLong); i += blockDim.x / 32) {
+        const Seq s = load_seq(p, many[i]);
+        const int n = units.count(s);
+        const unsigned long long c = warp_sum(seq_cost(units, s, n, units.flat(s, n), lane, 32));
+        if (lane == 0 && c > 0) atomicAdd(&prefix[many[i] / each + 1], c);
+    }
+    __syncthreads();
+    if (warp != 0) return;
     // prefix sums of the entries; then this CTA's place among them
     const int mine = (entries + 31) / 32, e0 = lane * mine;
     unsigned long long sum = 0;
@@ -108,10 +141,10 @@ __device__ void plan(const PagedParams &p, const Units units, Run *run, unsigned
     for (int e = e0; e < min(e0 + mine, entries); ++e) prefix[e + 1] = before += prefix[e + 1];
     if (lane == 0) prefix[0] = 0;
     __syncwarp();
-    const long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(p.min_run));
+    const long long per = max(static_cast<long long>(divide(total + gridDim.x - 1, gridDim.x)), static_cast<long long>(p.min_run));
     const long long at = min(static_cast<long long>(blockIdx.x) * per, total);
     const long long len = min(per, total - at);
-    Run r{len, per, 0, 0, 0, 0};
+    Run r{len, per, 0, 0, 0, 0, Seq{0, 0, 0}};
     if (len > 0) {
         int lo = 0, hi = entries;  // the last entry that starts at or before `at`, and is not empty
         while (hi - lo > 1) {
@@ -122,33 +155,51 @@ __device__ void plan(const PagedParams &p, const Units units, Run *run, unsigned
         unsigned long long x = static_cast<unsigned long long>(at) - prefix[lo] * p.Hkv;
         Seq s{};
         int n = 0;
+        int2 flat{};
         unsigned long long c = 0;
         for (r.b = lo * each;; ++r.b) {
             s = load_seq(p, r.b);
             n = units.count(s);
-            c = seq_cost(units, s, n);
+            flat = units.flat(s, n);
+            c = each == 1 ? prefix[r.b + 1] - prefix[r.b] : warp_sum(seq_cost(units, s, n, flat, lane, 32));
             if (x < c * p.Hkv || r.b + 1 >= p.B) break;
             x -= c * p.Hkv;
         }
-        r.hk = static_cast<int>(x / c);
+        r.s = s;
+        r.hk = static_cast<int>(divide(x, c));
         x -= c * r.hk;
-        // the unit whose share holds x
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const unsigned long long v = i0 + lane < n ? units.cost(s, i0 + lane) : 0;
-            unsigned long long upto = v;
+        // the unit whose share holds x: of [i0, i1), one by one
+        auto among = [&](int i0, int i1) {
+            for (; i0 < i1; i0 += 32) {
+                const unsigned long long v = i0 + lane < i1 ? units.cost(s, i0 + lane) : 0;
+                unsigned long long upto = v;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const unsigned long long y = __shfl_up_sync(kFull, upto, off);
-                if (lane >= off) upto += y;
+                for (int off = 1; off < 32; off <<= 1) {
+                    const unsigned long long y = __shfl_up_sync(kFull, upto, off);
+                    if (lane >= off) upto += y;
+                }
+                const unsigned here = __ballot_sync(kFull, x < upto);
+                if (here != 0) {
+                    const int l = __ffs(here) - 1;
+                    r.unit = i0 + l;
+                    r.off = static_cast<int>(x - __shfl_sync(kFull, upto - v, l));
+                    return true;
+                }
+                x -= __shfl_sync(kFull, upto, 31);
             }
-            const unsigned here = __ballot_sync(kFull, x < upto);
-            if (here != 0) {
-                const int l = __ffs(here) - 1;
-                r.unit = i0 + l;
-                r.off = static_cast<int>(x - __shfl_sync(kFull, upto - v, l));
-                break;
+            return false;
+        };
+        if (!among(0, flat.x)) {
+            const unsigned one = flat.y > flat.x ? units.cost(s, flat.x) : 0;
+            const unsigned long long all = static_cast<unsigned long long>(flat.y - flat.x) * one;
+            if (x < all) {
+                const unsigned at = static_cast<unsigned>(divide(x, one));
+                r.unit = flat.x + static_cast<int>(at);
+                r.off = static_cast<int>(x - static_cast<unsigned long long>(at) * one);
+            } else {
+                x -= all;
+                among(flat.y, n);
             }
-            x -= __shfl_sync(kFull, upto, 31);
         }
     }
     if (lane == 0) *run = r;

@@ -8,14 +8,17 @@
 // order. A unit is two key tiles of one key head, which stay in shared memory
 // while the query tiles that see any of them stream past (rows as in
 // fa_chunk.cuh); with one key tile, queries would come from L2 at 64 bytes a clock
-// and SM, twice what it gives. Each key tile has a warpgroup and two TMEM buffers
-// of 128 columns, so the products of a step run while the step before is
-// exponentiated. -lse log2 e of a step's columns comes through shared memory,
-// -inf where a column is no query.
+// and SM, twice what it gives. Each key tile has two TMEM buffers of 128 columns, so
+// the products of a step run while the step before is exponentiated, by two
+// warpgroups that share the columns (one alone, four warps fewer to hide each
+// other's latencies: 229 us for the case below). -lse log2 e of a step's columns
+// comes through shared memory, -inf where a column is no query.
 //
 // Bound: long chunks by the exponentials (a 128 x 128 tile: 512 clocks of the SM
 // for them and 512 of the tensor core for the product, side by side); single
 // tokens by reading the keys.
+#include <type_traits>
+
 #include "fa_paged.cuh"
 
 namespace fa {
@@ -42,12 +45,14 @@ struct Shape {
     static constexpr int kKFull = 0, kKEmpty = kKFull + kKUnits;
     static constexpr int kQFull = kKEmpty + kKUnits, kQEmpty = kQFull + kQStages;
     static constexpr int kLFull = kQEmpty + kQStages, kLEmpty = kLFull + kLStages;
-    static constexpr int kSFull = kLEmpty + kLStages, kSEmpty = kSFull + 4;  // + 2 t + buffer
-    static constexpr int kTeardown = kSEmpty + 4, kNumBars = kTeardown + 1;
+    static constexpr int kSFull = kLEmpty + kLStages, kSEmpty = kSFull + 2;  // + buffer
+    static constexpr int kPartFull = kSEmpty + 2, kPartEmpty = kPartFull + 1;
+    static constexpr int kTeardown = kPartEmpty + 1, kNumBars = kTeardown + 1;
     static constexpr int kOffMisc = (kOffBar + 8 * kNumBars + 15) & ~15;
     static constexpr int kOffRun = kOffMisc + 16;
-    static constexpr int kSmemBytes = kOffRun + sizeof(Run) + 1024;
-    static_assert(kSmemBytes <= 227 * 1024 && (kPlanEntries + 1) * 8 <= kOffQ, "shared memory budget");
+    static constexpr int kOffPart = (kOffRun + static_cast<int>(sizeof(Run)) + 15) & ~15;  // [2][128] sums
+    static constexpr int kSmemBytes = kOffPart + 1024;
+    static_assert(kSmemBytes <= 227 * 1024 && kPlanBytes <= kOffQ, "shared memory budget");
 };
 
 // Tokens [t0, t1) of a chunk that see a key of [k0, k0 + kUnitKeys).
@@ -71,6 +76,13 @@ struct Units {
         const int n = Tokens(p, s, i * kUnitKeys).tiles(p);
         return n > 0 ? n + kStart : 0;
     }
+    // units that all of the chunk sees: from 0 on those that start ahead of it (with a window: and hold sinks)
+    __device__ __forceinline__ int2 flat(const Seq &s, int n) const {
+        const int pos0 = s.L - s.Lq;
+        int to = pos0 >= 0 ? min(n, pos0 / kUnitKeys + 1) : 0;
+        if (p.window > 0) to = min(to, (p.sinks + kUnitKeys - 1) / kUnitKeys);
+        return make_int2(0, to);
+    }
 };
 
 // The units that start in a CTA's run; every role walks them for itself.
@@ -92,10 +104,10 @@ struct Walk {
         unit = r->unit;
         off = r->off;
         n = 0;
-        if (rem > 0) {
-            s = load_seq(p, b);
-            n = Units{p}.count(s);
-        }
+        s.q0 = r->s.q0;
+        s.Lq = r->s.Lq;
+        s.L = r->s.L;
+        if (rem > 0) n = Units{p}.count(s);
     }
     __device__ __forceinline__ bool next(Unit &o) {
         while (rem > 0) {
@@ -132,11 +144,25 @@ __device__ void producer_k(const CUtensorMap *tk, const WeightsParams &p, uint32
     uint32_t it = 0;  // units loaded
     bool ok = true;
     Walk walk(p, run);
-    Unit u;
-    for (; ok && walk.next(u); ++it) {
+    // a unit's pages are looked up while the one before it is waited for and loaded
+    Unit u, after;
+    int page[2], page_after[2];
+    auto look_up = [&](const Unit &x, int (&to)[2]) {
+        const Dead dead(p, x.s);
+        const Head at{x.b, x.hk, x.s.L};
+        to[0] = pages.look_up(p, at, dead, x.k0);
+        to[1] = pages.look_up(p, at, dead, x.k0 + kBlockN);
+    };
+    bool more = walk.next(u);
+    if (more) look_up(u, page);
+    for (; more; ++it) {
+        bool next = false;
+        if (it > 0) {  // (the first is not kept waiting)
+            next = walk.next(after);
+            if (next) look_up(after, page_after);
+        }
         const Dead dead(p, u.s);
         const Head at{u.b, u.hk, u.s.L};
-        const int page[2] = {pages.look_up(p, at, dead, u.k0), pages.look_up(p, at, dead, u.k0 + kBlockN)};
         const uint32_t stage = it % S::kKUnits;
         if (it >= S::kKUnits &&
             !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kKEmpty + stage), ((it / S::kKUnits) - 1) & 1, abort_flag,
@@ -147,14 +173,22 @@ __device__ void producer_k(const CUtensorMap *tk, const WeightsParams &p, uint32
             copy_small_pages<D>(p, at, dead, u.k0, p.k, dst);
             copy_small_pages<D>(p, at, dead, u.k0 + kBlockN, p.k, dst + S::kTileBytes);
             if (leader) ptx::bar_arrive(full);
-            continue;
-        }
-        if (leader) ptx::bar_arrive_expect_tx(full, 2 * S::kTileBytes);
-        __syncwarp();
+        } else {
+            if (leader) ptx::bar_arrive_expect_tx(full, 2 * S::kTileBytes);
+            __syncwarp();
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-            pages.load<D>(p, at, dead, u.k0 + t * kBlockN, page[t], tk, dst + t * S::kTileBytes, full);
-        __syncwarp();
+            for (int t = 0; t < 2; ++t)
+                pages.load<D>(p, at, dead, u.k0 + t * kBlockN, page[t], tk, dst + t * S::kTileBytes, full);
+            __syncwarp();
+        }
+        if (it == 0) {
+            next = walk.next(after);
+            if (next) look_up(after, page_after);
+        }
+        more = next;
+        u = after;
+        page[0] = page_after[0];
+        page[1] = page_after[1];
     }
     for (uint32_t s = 0; s < S::kKUnits && s < it; ++s) {
         const uint32_t last = (it - 1) - ((it - 1 - s) % S::kKUnits);
@@ -212,30 +246,41 @@ __device__ void producer_lse(const WeightsParams &p, uint32_t sbase, float *ring
     uint32_t it = 0;
     bool ok = true;
     Walk walk(p, run);
-    Unit u;
-    while (ok && walk.next(u)) {
-        for (int j = 0; j < u.steps; ++j, ++it) {
-            const int t0 = u.t0 + j * p.tile_tokens, n = min(p.tile_tokens, u.t1 - t0);
-            float x[4];
+    Unit u{};
+    int j = 0;
+    // values of the step at (u, j), which moves on; a step's are loaded while the
+    // ring's place for the one before it is waited for
+    auto load = [&](float (&x)[4]) {
+        const int t0 = u.t0 + j * p.tile_tokens, n = min(p.tile_tokens, u.t1 - t0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = CUDART_INF_F;
-                if (token[i] < n)
-                    x[i] = __ldg(p.lse + static_cast<long long>(u.hk * p.group + head[i]) * p.lse_head +
-                                 static_cast<long long>(u.s.q0 + t0 + token[i]) * p.lse_token);
-            }
-            const uint32_t stage = it % S::kLStages;
-            if (it >= S::kLStages &&
-                !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kLEmpty + stage), ((it / S::kLStages) - 1) & 1, abort_flag,
-                                     p.timeout_ns))))
-                break;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                ring[stage * 128 + lane + 32 * i] =
-                    x[i] == -CUDART_INF_F ? -CUDART_INF_F : x[i] * -1.4426950408889634f;
-            __syncwarp();
-            if (lane == 0) ptx::bar_arrive(bar(S::kLFull + stage));
+        for (int i = 0; i < 4; ++i) {
+            x[i] = CUDART_INF_F;
+            if (token[i] < n)
+                x[i] = __ldg(p.lse + static_cast<long long>(u.hk * p.group + head[i]) * p.lse_head +
+                             static_cast<long long>(u.s.q0 + t0 + token[i]) * p.lse_token);
         }
+        if (++j < u.steps) return true;
+        j = 0;
+        return walk.next(u);
+    };
+    float x[4], after[4];
+    bool more = walk.next(u), next = false;
+    if (more) next = load(x);
+    for (; more; ++it) {
+        more = next;
+        if (more) next = load(after);
+        const uint32_t stage = it % S::kLStages;
+        if (it >= S::kLStages &&
+            !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kLEmpty + stage), ((it / S::kLStages) - 1) & 1, abort_flag,
+                                 p.timeout_ns))))
+            break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ring[stage * 128 + lane + 32 * i] = x[i] == -CUDART_INF_F ? -CUDART_INF_F : x[i] * -1.4426950408889634f;
+            x[i] = after[i];
+        }
+        __syncwarp();
+        if (lane == 0) ptx::bar_arrive(bar(S::kLFull + stage));
     }
 }
 
@@ -261,24 +306,21 @@ __device__ void mma(const WeightsParams &p, uint32_t sbase, uint32_t tmem, const
             const uint32_t qs = it % S::kQStages, buf = it % 2;
             if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kQFull + qs), (it / S::kQStages) & 1, abort_flag, p.timeout_ns))))
                 break;
+            if (it >= 2 &&
+                !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kSEmpty + buf), (it / 2 - 1) & 1, abort_flag, p.timeout_ns))))
+                break;
+            ptx::tc_fence_after();
+            if (leader) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (it >= 2 && !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kSEmpty + 2 * t + buf), (it / 2 - 1) & 1,
-                                                                  abort_flag, p.timeout_ns))))
-                    break;
-                ptx::tc_fence_after();
-                if (leader) {
+                for (int t = 0; t < 2; ++t) {
                     const uint64_t kd = dk0 + (2 * ks + t) * kTile16, qd = dq0 + qs * kTile16;
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint64_t off = (kk / 4) * kBlock16 + (kk % 4) * 2;
                         ptx::mma_ss(tmem + 128 * (2 * t + buf), kd + off, qd + off, idesc, kk > 0);
                     }
-                    ptx::mma_commit(bar(S::kSFull + 2 * t + buf));
                 }
-            }
-            if (!ok) break;
-            if (leader) {
+                ptx::mma_commit(bar(S::kSFull + buf));
                 ptx::mma_commit(bar(S::kQEmpty + qs));
                 if (j + 1 == u.steps) ptx::mma_commit(bar(S::kKEmpty + ks));
             }
@@ -293,111 +335,171 @@ __device__ __forceinline__ void load_pairs(uint32_t at, uint64_t (&x)[2]) {
     asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(x[0]), "=l"(x[1]) : "r"(at));
 }
 
-// Sums of one key tile's rows, one key per thread.
+// Zeros for the keys that no unit writes: those behind a sequence, and its units
+// that no query sees. Threads [first, kThreads) of all CTAs share the rows.
+__device__ __forceinline__ void clear_rest(const WeightsParams &p, int first) {
+    const int threads = kThreads - first, width = p.max_blocks << p.log2_bs;
+    const long long rows = static_cast<long long>(p.B) * p.Hkv;
+    for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+        const Seq s = load_seq(p, static_cast<int>(row / p.Hkv));
+        float *w = p.weights + static_cast<size_t>(row) * width;
+        const int seen = s.Lq > 0 ? s.L : 0;
+        for (int k = seen + threadIdx.x - first; k < width; k += threads) w[k] = 0.f;
+        if (p.window == 0 && s.L >= s.Lq) continue;  // a query sees every key
+        for (int k = threadIdx.x - first; k < seen; k += threads)
+            if (Tokens(p, s, k / kUnitKeys * kUnitKeys).tiles(p) == 0) w[k] = 0.f;
+    }
+}
+
+// Sums of both key tiles' rows over every second step: a thread has a key of each.
+// The two warpgroups are a step apart, so one waits for its scores while the other
+// keeps the exponentials going.
 template <int D>
-__device__ void sums(const WeightsParams &p, uint32_t sbase, uint32_t tmem, int t, int wq, int lane,
-                     const volatile Run *run, volatile int *abort_flag) {
+__device__ void sums(const WeightsParams &p, uint32_t sbase, uint32_t tmem, float *part, uint32_t mine, int wq,
+                     int lane, const volatile Run *run, volatile int *abort_flag) {
     using S = Shape<D>;
     auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
-    const uint32_t tS = tmem + (static_cast<uint32_t>(wq * 32) << 16) + 256 * t;
+    const uint32_t tS = tmem + (static_cast<uint32_t>(wq * 32) << 16) + 128 * mine;
     const int row = wq * 32 + lane;
     const uint64_t scale2 = ptx::pk2(p.scale_log2, p.scale_log2);
-    uint32_t it = 0;
+    uint32_t it = 0, shared = 0;              // steps; units whose steps both warpgroups took
     bool ok = true;
     Walk walk(p, run);
     Unit u;
     while (ok && walk.next(u)) {
-        const int k0 = u.k0 + t * kBlockN, key = k0 + row;
-        const int pos0 = u.s.L - u.s.Lq;
+        const int pos0 = u.s.L - u.s.Lq, key = u.k0 + row;  // and key + kBlockN
         float *w = p.weights + (static_cast<size_t>(u.b) * p.Hkv + u.hk) * (static_cast<size_t>(p.max_blocks) << p.log2_bs);
-        const float before = key < u.s.L ? w[key] : 0.f;  // ahead of its use
-        uint64_t sum[4] = {0, 0, 0, 0};  // pairs of zeros
-        for (int j = 0; j < u.steps; ++j, ++it) {
-            const int t0 = u.t0 + j * p.tile_tokens, n = min(p.tile_tokens, u.t1 - t0), first = pos0 + t0;
-            // columns that are no query of the chunk but hold one's row (the
-            // last tile), or queries that do not see all of this tile's keys
-            const bool masked = n < p.tile_tokens || k0 + kBlockN - 1 > first ||
-                                (p.window > 0 && k0 + kBlockN > p.sinks && k0 <= first + n - 1 - p.window);
-            const uint32_t buf = it % 2, ls = it % S::kLStages;
-            ok = ptx::bar_wait(bar(S::kLFull + ls), (it / S::kLStages) & 1, abort_flag, p.timeout_ns) &&
-                 ptx::bar_wait(bar(S::kSFull + 2 * t + buf), (it / 2) & 1, abort_flag, p.timeout_ns);
+        // who writes the unit's sums: the one that takes its first step
+        const bool writes = it % 2 == mine;
+        float before[2] = {0.f, 0.f};
+        if (p.add && writes) {  // (ahead of their use)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                if (key + t * kBlockN < u.s.L) before[t] = w[key + t * kBlockN];
+        }
+        float sum[2][4] = {};  // of column c: c % 4
+        for (int j = writes ? 0 : 1; j < u.steps; j += 2) {
+            const uint32_t i = it + j, ls = i % S::kLStages;
+            ok = ptx::bar_wait(bar(S::kLFull + ls), (i / S::kLStages) & 1, abort_flag, p.timeout_ns) &&
+                 ptx::bar_wait(bar(S::kSFull + mine), (i / 2) & 1, abort_flag, p.timeout_ns);
             if (!__all_sync(kFull, ok)) { ok = false; break; }
             ptx::tc_fence_after();
-            // a key is seen by the columns [c0, c1): queries at its position or later, and in its window
-            int c0 = 0, c1 = 128;
-            if (masked) {
-                c0 = min(max(key - first, 0), 128) * p.group;
-                c1 = n;
-                if (p.window > 0 && key >= p.sinks) c1 = min(c1, max(key + p.window - first, 0));
-                c1 *= p.group;
-            }
-            const uint32_t ring = sbase + S::kOffL + ls * 512;
-            // exponentials of columns c and c + 1 of a chunk of 32
-            auto pair = [&](const uint32_t (&s)[32], int c, uint64_t nl, float &e0, float &e1) {
-                float x0, x1;
-                ptx::upk2(ptx::ffma2(ptx::pk2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale2, nl), x0, x1);
-                e0 = ptx::ex2(x0);
-                e1 = ptx::ex2(x1);
-            };
-            if (!masked && p.chunks == 4) {
-                // the whole row at once: one wait, and the buffer is free again
-                uint32_t s[4][32];
+            const int t0 = u.t0 + j * p.tile_tokens, n = min(p.tile_tokens, u.t1 - t0), first = pos0 + t0;
+            const uint32_t nl_at = sbase + S::kOffL + ls * 512;
+            // the weights of columns 4 c to 4 c + 3 of the 32 in x
+            auto exps = [&](const uint32_t (&x)[32], int c, uint32_t at, float (&e)[4]) {
+                uint64_t nl[2];
+                load_pairs(at + 16 * c, nl);
 #pragma unroll
-                for (int b = 0; b < 4; ++b) ptx::tmem_ld32(tS + 128 * buf + 32 * b, s[b]);
-                ptx::tmem_ld_wait();
-#pragma unroll
-                for (int b = 0; b < 4; ++b) ptx::reg_fence(s[b]);
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::bar_arrive(bar(S::kSEmpty + 2 * t + buf));
-#pragma unroll
-                for (int c = 0; c < 128; c += 4) {
-                    uint64_t nl[2];
-                    load_pairs(ring + 4 * c, nl);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float e0, e1;
-                        pair(s[c / 32], c % 32 + 2 * h, nl[h], e0, e1);
-                        sum[(c / 2 + h) % 4] = ptx::fadd2(sum[(c / 2 + h) % 4], ptx::pk2(e0, e1));
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    float x0, x1;
+                    ptx::upk2(ptx::ffma2(ptx::pk2(__uint_as_float(x[4 * c + 2 * h]), __uint_as_float(x[4 * c + 2 * h + 1])),
+                                         scale2, nl[h]), x0, x1);
+                    e[2 * h] = ptx::ex2(x0);
+                    e[2 * h + 1] = ptx::ex2(x1);
                 }
-            } else {
-                for (int b = 0; b < p.chunks; ++b) {
-                    uint32_t s[32];
-                    ptx::tmem_ld32(tS + 128 * buf + 32 * b, s);
-                    ptx::tmem_ld_wait();
-                    ptx::reg_fence(s);
-                    auto below = [](int x) -> uint32_t {
-                        return static_cast<uint32_t>((1ull << min(max(x, 0), 32)) - 1);
-                    };
-                    const uint32_t seen = below(c1 - 32 * b) & ~below(c0 - 32 * b);
+            };
+            // adds 32 columns of both tiles
+            auto both = [&](const uint32_t (&x)[2][32], uint32_t at) {
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        uint64_t nl[2];
-                        load_pairs(ring + 128 * b + 4 * c, nl);
+                for (int c = 0; c < 32; c += 4) {
+                    uint64_t nl[2];
+                    load_pairs(at + 4 * c, nl);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float e0, e1;
-                            pair(s, c + 2 * h, nl[h], e0, e1);
-                            if (!(seen & (1u << (c + 2 * h)))) e0 = 0.f;
-                            if (!(seen & (2u << (c + 2 * h)))) e1 = 0.f;
-                            sum[(c / 2 + h) % 4] = ptx::fadd2(sum[(c / 2 + h) % 4], ptx::pk2(e0, e1));
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            float x0, x1;
+                            ptx::upk2(ptx::ffma2(ptx::pk2(__uint_as_float(x[t][c + 2 * h]), __uint_as_float(x[t][c + 2 * h + 1])),
+                                                 scale2, nl[h]), x0, x1);
+                            sum[t][2 * h] += ptx::ex2(x0);
+                            sum[t][2 * h + 1] += ptx::ex2(x1);
+                        }
+                }
+            };
+            // Some columns do not count for some keys: queries ahead of a key or too far
+            // behind it, columns that are no query of the chunk but hold one's row (a
+            // chunk's last step), or nobody's (an odd number of 32s).
+            const bool masked = n < p.tile_tokens || u.k0 + kUnitKeys - 1 > first || p.chunks % 2 != 0 ||
+                                (p.window > 0 && u.k0 + kUnitKeys > p.sinks && u.k0 <= first + n - 1 - p.window);
+            if (masked) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int k = key + t * kBlockN;  // seen by the columns [c0, c1)
+                    const int c0 = min(max(k - first, 0), 128) * p.group;
+                    int c1 = n;
+                    if (p.window > 0 && k >= p.sinks) c1 = min(c1, max(k + p.window - first, 0));
+                    c1 *= p.group;
+#pragma unroll 1
+                    for (int b = 0; b < p.chunks; ++b) {
+                        auto below = [&](int c) { return static_cast<uint32_t>((1ull << min(max(c - 32 * b, 0), 32)) - 1); };
+                        const uint32_t seen = below(c1) & ~below(c0);
+                        uint32_t x[32];
+                        ptx::tmem_ld32(tS + 256 * t + 32 * b, x);
+                        ptx::tmem_ld_wait();
+                        ptx::reg_fence(x);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            float e[4];
+                            exps(x, c, nl_at + 128 * b, e);
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) sum[t][h] += seen >> (4 * c + h) & 1 ? e[h] : 0.f;
                         }
                     }
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::bar_arrive(bar(S::kSEmpty + 2 * t + buf));
+                if (lane == 0) ptx::bar_arrive(bar(S::kSEmpty + mine));
+            } else {
+                const int halves = p.chunks / 2;  // of 64 columns
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (half >= halves) break;
+                    uint32_t x[2][2][32];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) ptx::tmem_ld32(tS + 256 * t + 64 * half + 32 * b, x[b][t]);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) ptx::reg_fence(x[b][t]);
+                    if (half + 1 == halves) {
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::bar_arrive(bar(S::kSEmpty + mine));
+                    }
+                    both(x[0], nl_at + 256 * half);
+                    both(x[1], nl_at + 256 * half + 128);
+                }
             }
             __syncwarp();
             if (lane == 0) ptx::bar_arrive(bar(S::kLEmpty + ls));
         }
         if (!ok) break;
-        if (key < u.s.L) {
-            float a0, a1, b0, b1;
-            ptx::upk2(ptx::fadd2(sum[0], sum[1]), a0, a1);
-            ptx::upk2(ptx::fadd2(sum[2], sum[3]), b0, b1);
-            w[key] = before + ((a0 + a1) + (b0 + b1));
+        it += u.steps;
+        float total[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) total[t] = (sum[t][0] + sum[t][1]) + (sum[t][2] + sum[t][3]);
+        if (u.steps > 1) {
+            // the other's sums go through shared memory to the one that writes
+            ok = writes ? ptx::bar_wait(bar(S::kPartFull), shared & 1, abort_flag, p.timeout_ns)
+                        : shared == 0 || ptx::bar_wait(bar(S::kPartEmpty), (shared - 1) & 1, abort_flag, p.timeout_ns);
+            if (!__all_sync(kFull, ok)) { ok = false; break; }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (writes) total[t] += part[t * kBlockN + row];
+                else part[t * kBlockN + row] = total[t];
+            }
+            __syncwarp();
+            if (lane == 0) ptx::bar_arrive(bar(writes ? S::kPartEmpty : S::kPartFull));
+            ++shared;
+        }
+        if (writes) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                if (key + t * kBlockN < u.s.L) w[key + t * kBlockN] = before[t] + total[t];
         }
     }
 }
@@ -407,33 +509,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     fa_kv_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const WeightsParams p) {
     using S = Shape<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];  // (there is no room to align it)
     const uint32_t sbase = ptx::smem_addr(smem);
+    if ((sbase & 1023) != 0) {
+        if (threadIdx.x == 0) atomicExch(p.err, kDeviceErrTimeout);
+        return;
+    }
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kOffMisc + 4);
     Run *run = reinterpret_cast<Run *>(smem + S::kOffRun);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kNumBars; ++i) {
-            const bool s_empty = i >= S::kSEmpty && i < S::kTeardown, l_empty = i >= S::kLEmpty && i < S::kSFull;
-            ptx::bar_init(sbase + S::kOffBar + 8u * i, s_empty ? 4u : l_empty ? 8u : 1u);  // one arrival per warp
-        }
-        *abort_flag = 0;
-        ptx::bar_init_fence();
-        ptx::prefetch_tmap(&tm_q);
-        ptx::prefetch_tmap(&tm_k);
-    }
+    // the plan's scratch lies where the keys go
+    plan(p, Units{p}, run, smem);
     if (warp == 1) {
+        if (lane == 0) {
+            for (int i = 0; i < S::kNumBars; ++i) {
+                const bool s_empty = i >= S::kSEmpty && i < S::kPartFull, l_empty = i >= S::kLEmpty && i < S::kSFull;
+                const bool sums = i >= S::kPartFull && i < S::kTeardown;
+                // one arrival per warp
+                ptx::bar_init(sbase + S::kOffBar + 8u * i, s_empty || l_empty || sums ? 4u : 1u);
+            }
+            *abort_flag = 0;
+            ptx::bar_init_fence();
+        }
+        __syncwarp();
         ptx::tmem_alloc(ptx::smem_addr(tmem_slot), 512);
         ptx::tmem_relinquish();
+    } else if (warp == 2 && lane == 0) {
+        ptx::prefetch_tmap(&tm_q);
+        ptx::prefetch_tmap(&tm_k);
+    } else if (warp >= 4 && warp < 4 + S::kQStages) {
+        // rows that no box reaches are zeros: their scores are finite, their weights 0
+        ptx::zero_rows(sbase + S::kOffQ + (warp - 4) * S::kTileBytes, S::kColBlocks, kBlockM, p.tile_tokens * p.group,
+                       kBlockM);
     }
-    // rows that no box reaches are zeros: their scores are finite, their weights 0
-    for (int i = warp; i < S::kQStages; i += kThreads / 32)
-        ptx::zero_rows(sbase + S::kOffQ + i * S::kTileBytes, S::kColBlocks, kBlockM, p.tile_tokens * p.group, kBlockM);
-    // the plan's scratch lies where the keys go
-    plan(p, Units{p}, run, reinterpret_cast<unsigned long long *>(smem));
     ptx::fence_proxy_async_smem();
     ptx::tc_fence_before();
     __syncthreads();
@@ -444,7 +554,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (warp == 1) mma<D, BF16>(p, sbase, tmem, run, abort_flag);
     else if (warp == 2) producer_lse<D>(p, sbase, reinterpret_cast<float *>(smem + S::kOffL), run, abort_flag);
     else if (warp == 3) producer_q<D>(&tm_q, p, sbase, run, abort_flag);
-    else sums<D>(p, sbase, tmem, (warp - 4) / 4, warp % 4, lane, run, abort_flag);
+    else {
+        if (!p.add && run->per > 0) clear_rest(p, 128);  // (while the first keys are on their way)
+        sums<D>(p, sbase, tmem, reinterpret_cast<float *>(smem + S::kOffPart), (warp - 4) / 4, warp % 4, lane, run,
+                abort_flag);
+    }
 
     ptx::tc_fence_before();
     __syncthreads();

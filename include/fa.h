@@ -672,10 +672,11 @@ FA_API fa_status_t fa_fwd_paged(const void *q, const void *k_cache, const void *
 /*
  * fa_kv_weights - what a chunk of queries gave to each key of a paged cache: the
  * softmax weights of the attention that has run, summed over the chunk's
- * queries and the query heads of a key head, and added to what is there:
+ * queries and the query heads of a key head, and (add = 1) added to what is there
+ * or (add = 0) put there:
  *
- *   weights[b, hk, j] += sum over queries t that see key j, and heads h of key
- *                        head hk, of exp(scale * q_th . k_j - lse_th)
+ *   weights[b, hk, j] (+)= sum over queries t that see key j, and heads h of key
+ *                          head hk, of exp(scale * q_th . k_j - lse_th)
  *
  * fa_kv_evict takes them. What a query sees is as in fa_fwd_paged, whose
  * arguments these are, but for
@@ -684,8 +685,9 @@ FA_API fa_status_t fa_fwd_paged(const void *q, const void *k_cache, const void *
  *              t) at element h * lse_head + t * lse_token: (total_q, 1) for the
  *              [H,total_q] of fa_fwd_paged, (1, H) for the [B,H] of a decode
  *              (total_q = B queries, one each)
- *   weights    [num_seqs,Hkv,max_blocks_per_seq * block_size] fp32, in and out;
- *              keys that no query sees keep theirs
+ *   weights    [num_seqs,Hkv,max_blocks_per_seq * block_size] fp32, in and out:
+ *              keys that no query sees keep theirs (add = 1) or get zeros, those
+ *              behind a sequence too (add = 0)
  * Queries with lse = -inf give nothing. Rows of the cache that no query sees, and
  * rows of q and lse that belong to no chunk, may hold anything. Offsets and page
  * numbers are checked as by fa_fwd_paged (a page that does not exist counts as
@@ -697,7 +699,7 @@ FA_API fa_status_t fa_kv_weights(const void *q, const float *lse, const void *k_
                                  const int32_t *cu_seqlens_q, const int32_t *seq_lens, float *weights,
                                  int64_t lse_head, int64_t lse_token, int num_seqs, int total_q, int max_seqlen_q,
                                  int H, int Hkv, int D, int num_blocks, int block_size, int max_blocks_per_seq,
-                                 int window, int sinks, float scale, fa_dtype_t dtype, void *stream);
+                                 int window, int sinks, int add, float scale, fa_dtype_t dtype, void *stream);
 
 /*
  * fa_kv_evict - the keys of least weight leave a paged 16-bit cache.

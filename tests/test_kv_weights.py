@@ -58,9 +58,9 @@ def true_lse(q, kc, table, lens, cu, window, sinks, scale):
 
 def test_validation(lib):
     def call(q=A, lse=A, kc=A, bt=A, cu=A, sl=A, w=A, lh=100, lt=1, n=2, total=100, mx=64, H=8, Hkv=2, D=128, nb=8, bs=16,
-             mb=4, window=0, sinks=0, scale=0.1, dtype=1):
+             mb=4, window=0, sinks=0, add=1, scale=0.1, dtype=1):
         return lib.fa_kv_weights(q, lse, kc, bt, cu, sl, w, lh, lt, n, total, mx, H, Hkv, D, nb, bs, mb, window, sinks,
-                                 scale, dtype, None)
+                                 add, scale, dtype, None)
 
     for kw in ("q", "lse", "kc", "bt", "cu", "sl", "w"):
         assert call(**{kw: None}) == NULL, kw
@@ -126,6 +126,10 @@ def test_weights(chunks, lens, H, Hkv, D, block, window, sinks, dtype):
     w = fa.flash_kv_weights(*args, max(chunks), window, sinks)
     fa.fa_check_device_error()
     check_weights(w, ref)
+    # put where anything was, keys that nobody sees included
+    old = torch.full(w.shape, math.nan, device="cuda")
+    fa.fa_kv_weights(*args, old, max(chunks), window, sinks, add=False)
+    assert torch.equal(old, w)
     # every query that sees a key gives 1 for each head, in all
     give = sum(int(visible_behind(n, L, window, sinks).any(1).sum()) for n, L in zip(chunks, lens) if n and L)
     assert abs(float(w.double().sum()) - give * H) <= 2.0 ** -12 * give * H + 1e-9
