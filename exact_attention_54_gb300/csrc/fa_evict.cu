@@ -22,10 +22,9 @@ namespace fa {
 namespace evict {
 
 constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCached = 46 * 1024;  // keys whose weights shared memory holds
+constexpr int kMaxCtas = 8;            // of a cluster (the portable size)
+constexpr int kMaxCached = 44 * 1024;  // keys whose weights a CTA's shared memory holds
 constexpr int kBins = 2048;
-constexpr int kEach = 4;               // consecutive keys of a thread, compaction
 constexpr unsigned kFull = 0xffffffffu;
 
 // A weight's bits, ordered like the weights as unsigned integers: -0 is +0, a NaN is below everything.
@@ -35,39 +34,35 @@ __device__ __forceinline__ uint32_t order(float w) {
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-// Sum of v over the threads before this one; `total`: over all. The whole CTA calls it.
-__device__ __forceinline__ uint32_t prefix_sum(uint32_t v, uint32_t *sums, uint32_t &total) {
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    uint32_t x = v;
+// Sum of v over this lane and those before it.
+__device__ __forceinline__ uint32_t scan(uint32_t v) {
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t y = __shfl_up_sync(kFull, x, off);
-        if (lane >= off) x += y;
+        const uint32_t y = __shfl_up_sync(kFull, v, off);
+        if (static_cast<int>(threadIdx.x % 32) >= off) v += y;
     }
-    __syncthreads();  // sums of the previous call are read
-    if (lane == 31) sums[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        uint32_t s = sums[lane];
-#pragma unroll
-        for (int off = 1; off < kWarps; off <<= 1) {
-            const uint32_t y = __shfl_up_sync(kFull, s, off);
-            if (lane >= off) s += y;
-        }
-        sums[lane] = s;
-    }
-    __syncthreads();
-    total = sums[kWarps - 1];
-    return x - v + (warp > 0 ? sums[warp - 1] : 0u);
+    return v;
 }
 
+// Barriers cost a few hundred clocks each, so a digit takes two: the counts are
+// there, and the sums over each warp's bins are; every warp then finds the digit
+// for itself. The keys that stay are written warp by warp, each over a run of keys.
+// (Prefix sums of the whole CTA for each: 8 barriers a digit and 3 every 4096 keys,
+// 20 us for four caches of 16384 to 32768 keys, DELTA now.)
 __global__ void __launch_bounds__(kThreads, 1) fa_kv_evict_select_kernel(const EvictParams p) {
-    extern __shared__ uint4 cached4[];  // the order of this CTA's first p.cached keys
-    __shared__ uint32_t hist[3][kBins], sums[kWarps], pick[2], mine[2];
-    uint32_t *cached = reinterpret_cast<uint32_t *>(cached4);
+    constexpr int kWarps = kThreads / 32, kOfWarp = kBins / kWarps;  // bins
+    static_assert(kOfWarp == 64, "two bins a lane");
+    extern __shared__ uint32_t cached[];  // the order of this CTA's first p.cached keys
+    __shared__ uint32_t hist[3][kBins], sum[kBins], of_warp[3][kWarps];
+    __shared__ uint2 counts[kWarps];  // of a warp's keys: above the last that stays, equal to it
     auto cluster = cooperative_groups::this_cluster();
     const int ctas = static_cast<int>(cluster.num_blocks()), cta = static_cast<int>(cluster.block_rank());
-    const int tid = static_cast<int>(threadIdx.x), all = cta * kThreads + tid, step = ctas * kThreads;
+    const int tid = static_cast<int>(threadIdx.x), lane = tid % 32, warp = tid / 32;
+    const int all = cta * kThreads + tid, step = ctas * kThreads;
+    auto sync = [&] {
+        if (ctas > 1) cluster.sync();
+        else __syncthreads();
+    };
     ptx::grid_launch_dependents();
     const size_t bh = blockIdx.x / ctas;
     const int b = static_cast<int>(bh / p.Hkv);
@@ -76,133 +71,133 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv_evict_select_kernel(const E
     const float *w = p.weights + bh * width;
     int *kept = p.kept + bh * p.keep;
     float *out = p.new_weights + bh * new_width;
-    auto store = [&](int at, int j) {
+    auto store = [&](int at, int j, float x) {
         kept[at] = j;
-        if (at < new_width) out[at] = w[j];
+        if (at < new_width) out[at] = x;
     };
+    // the candidates: this CTA's are `count` from key `base` on
+    const int room = p.keep - p.sinks - p.recent;  // for fewer than all of them, where L > keep
+    const bool choose = L > p.keep && room > 0;
+    const int candidates = L - p.sinks - p.recent, each = (candidates + ctas - 1) / ctas;
+    const int base = p.sinks + min(cta * each, candidates), count = min(each, p.sinks + candidates - base);
+    const int held = min(count, p.cached);
+    if (choose) {
+        for (int i = tid; i < 3 * kBins; i += kThreads) hist[0][i] = 0;
+        for (int j0 = 0; j0 < held; j0 += 8 * kThreads) {  // eight loads of a thread in flight
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = j0 + i * kThreads + tid;
+                x[i] = j < held ? w[base + j] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = j0 + i * kThreads + tid;
+                if (j < held) cached[j] = order(x[i]);
+            }
+        }
+    }
     if (bh % p.Hkv == 0 && all == 0) p.new_lens[b] = n;
     for (int i = n + all; i < p.keep; i += step) kept[i] = -1;
     for (int i = n + all; i < new_width; i += step) out[i] = 0.f;
     if (L <= p.keep) {
-        for (int i = all; i < L; i += step) store(i, i);
+        for (int i = all; i < L; i += step) store(i, i, w[i]);
         return;
     }
-    for (int i = all; i < p.sinks; i += step) store(i, i);
-    for (int i = all; i < p.recent; i += step) store(p.keep - p.recent + i, L - p.recent + i);
-    const int room = p.keep - p.sinks - p.recent;  // fewer than the candidates
-    if (room == 0) return;
-
-    // this CTA's candidates: count of them from key `base` on
-    const int candidates = L - p.sinks - p.recent, each = (candidates + ctas - 1) / ctas;
-    const int base = p.sinks + min(cta * each, candidates), count = min(each, p.sinks + candidates - base);
-    const int held = min(count, p.cached);
-    for (int j0 = 0; j0 < held; j0 += 8 * kThreads) {  // eight loads of a thread in flight
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int j = j0 + i * kThreads + tid;
-            x[i] = j < held ? w[base + j] : 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int j = j0 + i * kThreads + tid;
-            if (j < held) cached[j] = order(x[i]);
-        }
-    }
-    for (int i = tid; i < 3 * kBins; i += kThreads) hist[0][i] = 0;
+    for (int i = all; i < p.sinks; i += step) store(i, i, w[i]);
+    for (int i = all; i < p.recent; i += step) store(p.keep - p.recent + i, L - p.recent + i, w[L - p.recent + i]);
+    if (!choose) return;
     __syncthreads();
-    // the orders of candidates j .. j + 3 (0 behind the last)
-    auto four = [&](int j, uint32_t (&k)[kEach]) {
-        if (j + kEach <= held) {
-            const uint4 v = cached4[j / kEach];
-            k[0] = v.x;
-            k[1] = v.y;
-            k[2] = v.z;
-            k[3] = v.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < kEach; ++i)
-                k[i] = j + i < held ? cached[j + i] : j + i < count ? order(w[base + j + i]) : 0u;
-        }
-    };
+
+    auto rank = [&](int j) { return j < held ? cached[j] : order(w[base + j]); };
     uint32_t last = 0, left = static_cast<uint32_t>(room);  // the rank of the last key that stays, so far; keys of it that stay
-    uint32_t above = 0;                                     // of this CTA's keys, in this thread's bins
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
         uint32_t *h = hist[pass];
-        for (int j = tid * kEach; j < count; j += kThreads * kEach) {
-            uint32_t k[kEach];
-            four(j, k);
+        for (int j = tid; j < count; j += kThreads) {
+            const uint32_t k = rank(j);
+            if (pass == 0 || (k ^ last) >> (shift + bits) == 0) atomicAdd(&h[(k >> shift) & ((1u << bits) - 1)], 1u);
+        }
+        sync();
+        // bins from the top, two a lane: a warp sums its own, over the cluster (all
+        // of the other CTAs' counts are on their way at once)
+        const int top = kBins - 2 - 2 * lane, here = top - warp * kOfWarp;  // the lower one of the two
+        uint2 mine = *reinterpret_cast<const uint2 *>(h + here), other[kMaxCtas - 1];
 #pragma unroll
-            for (int i = 0; i < kEach; ++i)
-                if (j + i < count && (pass == 0 || (k[i] ^ last) >> (shift + bits) == 0))
-                    atomicAdd(&h[(k[i] >> shift) & ((1u << bits) - 1)], 1u);
+        for (int x = 1; x < kMaxCtas; ++x) {
+            const int rank = cta + x < ctas ? cta + x : cta + x - ctas;
+            other[x - 1] = x < ctas ? *reinterpret_cast<const uint2 *>(cluster.map_shared_rank(h, static_cast<unsigned>(rank)) + here)
+                                    : make_uint2(0u, 0u);
         }
-        cluster.sync();
-        // bins from the top, two a thread: the one in which the count of keys reaches `left`
-        const int top = kBins - 1 - 2 * tid;
-        const uint32_t l0 = h[top], l1 = h[top - 1];
-        uint32_t c0 = l0, c1 = l1;
-        for (int c = 1; c < ctas; ++c) {
-            const uint32_t *other = cluster.map_shared_rank(h, static_cast<unsigned>((cta + c) % ctas));
-            c0 += other[top];
-            c1 += other[top - 1];
+#pragma unroll
+        for (int x = 0; x < kMaxCtas - 1; ++x) {
+            mine.x += other[x].x;
+            mine.y += other[x].y;
         }
-        uint32_t total;
-        const uint32_t before = prefix_sum(c0 + c1, sums, total);
-        if (before < left && left <= before + c0 + c1) {
-            const bool first = left <= before + c0;
-            pick[0] = static_cast<uint32_t>(first ? top : top - 1);
-            pick[1] = left - (first ? before : before + c0);
-        }
+        *reinterpret_cast<uint2 *>(sum + here) = mine;
+        const uint32_t own = __reduce_add_sync(kFull, mine.x + mine.y);
+        if (lane == 0) of_warp[pass][warp] = own;
         __syncthreads();
-        const int bin = static_cast<int>(pick[0]);
-        above += (top > bin ? l0 : 0u) + (top - 1 > bin ? l1 : 0u);
+        // the warp, the lane and the bin in which the count of keys from the top reaches `left`
+        const uint32_t v = of_warp[pass][lane];
+        uint32_t upto = scan(v);
+        int at = __ffs(__ballot_sync(kFull, upto >= left)) - 1;
+        left -= __shfl_sync(kFull, upto - v, at);
+        const int low = top - at * kOfWarp;
+        const uint2 two = *reinterpret_cast<const uint2 *>(sum + low);
+        upto = scan(two.x + two.y);
+        at = __ffs(__ballot_sync(kFull, upto >= left)) - 1;
+        left -= __shfl_sync(kFull, upto - two.x - two.y, at);
+        int bin = __shfl_sync(kFull, low, at);
+        const uint32_t upper = __shfl_sync(kFull, two.y, at);
+        if (upper >= left) ++bin;
+        else left -= upper;
         last |= static_cast<uint32_t>(bin) << shift;
-        left = pick[1];
-    }
-    // keys above `last`, and its equals, of the CTAs before this one
-    uint32_t at_above = 0, at_equal = 0;
-    {
-        uint32_t total;
-        prefix_sum(above, sums, total);
-        if (tid == 0) {
-            mine[0] = total;
-            mine[1] = hist[2][last & 1023u];
-        }
-        cluster.sync();
-        for (int c = 0; c < cta; ++c) {
-            const uint32_t *other = cluster.map_shared_rank(mine, static_cast<unsigned>(c));
-            at_above += other[0];
-            at_equal += other[1];
-        }
     }
     // the keys above `last`, and the first `left` of its equals, in order
-    for (int j0 = 0; j0 < count; j0 += kThreads * kEach) {
-        const int j = j0 + tid * kEach;
-        uint32_t k[kEach], some = 0;  // above: upper 16 bits, equal: lower
-        four(j, k);
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) some += j + i >= count ? 0u : k[i] > last ? 0x10000u : k[i] == last ? 1u : 0u;
-        uint32_t total;
-        const uint32_t before = prefix_sum(some, sums, total);
-        uint32_t a = at_above + (before >> 16), e = at_equal + (before & 0xffffu);
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            if (j + i >= count) break;
-            if (k[i] > last) {
-                store(p.sinks + static_cast<int>(a + min(e, left)), base + j + i);
-                ++a;
-            } else if (k[i] == last) {
-                if (e < left) store(p.sinks + static_cast<int>(a + e), base + j + i);
-                ++e;
-            }
-        }
-        at_above += total >> 16;
-        at_equal += total & 0xffffu;
+    const int run = (count + kWarps * 32 - 1) / (kWarps * 32) * 32;  // keys of a warp
+    const int j0 = min(warp * run, count), j1 = min(j0 + run, count);
+    uint32_t above = 0, equal = 0;
+    for (int j = j0; j < j1; j += 32) {
+        const uint32_t k = j + lane < j1 ? rank(j + lane) : 0u;
+        above += __popc(__ballot_sync(kFull, j + lane < j1 && k > last));
+        equal += __popc(__ballot_sync(kFull, j + lane < j1 && k == last));
     }
-    cluster.sync();  // the others have read what they need of this CTA
+    if (lane == 0) counts[warp] = make_uint2(above, equal);
+    sync();
+    above = equal = 0;  // of the warps before this one
+    for (int x = 0; x <= cta; ++x) {
+        const uint2 *c = x == cta ? counts : cluster.map_shared_rank(counts, static_cast<unsigned>(x));
+        if (lane < (x == cta ? warp : kWarps)) {
+            const uint2 v = c[lane];
+            above += v.x;
+            equal += v.y;
+        }
+    }
+    above = __reduce_add_sync(kFull, above);
+    equal = __reduce_add_sync(kFull, equal);
+    const unsigned before = (1u << lane) - 1;
+    for (int i0 = j0; i0 < j1; i0 += 4 * 32) {
+        float x[4];  // (loaded ahead of their stores)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = i0 + 32 * i + lane;
+            x[i] = j < j1 ? w[base + j] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = i0 + 32 * i + lane;
+            const uint32_t k = j < j1 ? rank(j) : 0u;
+            const bool is_above = j < j1 && k > last, is_equal = j < j1 && k == last;
+            const unsigned up = __ballot_sync(kFull, is_above), eq = __ballot_sync(kFull, is_equal);
+            const uint32_t a = above + __popc(up & before), e = equal + __popc(eq & before);
+            if (is_above || (is_equal && e < left)) store(p.sinks + static_cast<int>(a + min(e, left)), base + j, x[i]);
+            above += __popc(up);
+            equal += __popc(eq);
+        }
+    }
+    if (ctas > 1) cluster.sync();  // the others have read what they need of this CTA
 }
 
 constexpr int kCopyThreads = 128;
@@ -260,11 +255,11 @@ cudaError_t launch_kv_evict(int D, EvictParams p, int sms, cudaStream_t st) {
     static std::atomic<unsigned long long> done{0};
     const long long width = static_cast<long long>(p.max_blocks) << p.log2_bs;
     const unsigned units = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.Hkv);
-    // a cluster of up to 8 CTAs (the portable size) where SMs and keys (a thousand each) are there for them
+    // a cluster of as many CTAs as there are SMs and keys (a thousand each) for
     int ctas = 1;
-    while (ctas < 8 && 2LL * ctas * units <= sms && width > 1024LL * ctas) ctas *= 2;
+    while (ctas < evict::kMaxCtas && 2LL * ctas * units <= sms && width > 1024LL * ctas) ctas *= 2;
     const long long each = (width + ctas - 1) / ctas;
-    p.cached = static_cast<int>(each < evict::kMaxCached ? (each + 3) / 4 * 4 : evict::kMaxCached);
+    p.cached = static_cast<int>(each < evict::kMaxCached ? each : evict::kMaxCached);
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(evict::fa_kv_evict_select_kernel),
                                evict::kMaxCached * static_cast<int>(sizeof(uint32_t)), done);
     if (e != cudaSuccess) return e;
