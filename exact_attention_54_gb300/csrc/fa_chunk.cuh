@@ -34,7 +34,7 @@ namespace chunk {
 using namespace paged;
 
 // What a unit's start (its queries, first keys, and end) costs, in key tiles.
-constexpr int kStart = 2;
+constexpr int kStart = 3;
 
 __device__ __forceinline__ int pairs_of(const ChunkParams &p, const Seq &s) {
     return (s.Lq + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
@@ -106,9 +106,6 @@ struct Part {
     bool whole;   // the unit's only part
     int slot;     // of the CTA's two in the workspace, else
     int parts;    // first of several parts: their number, else 0
-    // One query tile, several key tiles: both softmax warpgroups take it, every
-    // second key tile each, so that its steps overlap like two query tiles' do.
-    __device__ __forceinline__ bool solo() const { return k.ntok[1] == 0 && s1 - s0 > 1; }
 };
 
 // Where a role is in its CTA's run.
@@ -178,13 +175,8 @@ struct Kept {
 // Shared memory behind the barriers.
 struct Shared {
     Run run;
-    unsigned long long solo_ml, solo_done;  // barriers: warpgroup 1's m and l are written; its O has been read
     Kept kept[8];
-    float2 ml[kBlockM];
 };
-
-template <int D>
-constexpr int kSmemBytes = FwdShape<D>::kSmemBytes + 128;  // Shared is larger than the packed forward's table
 
 // ------------------------------------------------------------------ roles --
 
@@ -344,8 +336,8 @@ __device__ void mma(const ChunkParams &p, uint32_t sbase, uint32_t tmem, const v
     constexpr uint64_t kTile16 = S::kTileBytes >> 4;
 
     // products as in the packed forward
-    auto issue_qk = [&](int t, uint32_t stage, int q_tile) {
-        const uint64_t qd = dq0 + static_cast<uint64_t>(q_tile) * kTile16, kd = dk0 + static_cast<uint64_t>(stage) * kTile16;
+    auto issue_qk = [&](int t, uint32_t stage) {
+        const uint64_t qd = dq0 + static_cast<uint64_t>(t) * kTile16, kd = dk0 + static_cast<uint64_t>(stage) * kTile16;
         const uint32_t dst = tmem + S::kTmemS + t * 128;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -376,45 +368,6 @@ __device__ void mma(const ChunkParams &p, uint32_t sbase, uint32_t tmem, const v
         const int total[2] = {visited(u.k, 0, u.s0, u.s1), visited(u.k, 1, u.s0, u.s1)};
         if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kQFull), wi & 1, abort_flag, p.timeout_ns)))) break;
         if (wi == 0 && leader) ptx::bar_arrive(bar(S::kFirstQ));
-        if (u.solo()) {
-            // S of step j goes to buffer j % 2; step j + 2's is issued behind step j's P V
-            auto qk = [&](int j) -> bool {
-                const uint32_t ks = (it + j) % S::kKStages;
-                if (!ptx::warp_all(ptx::bar_wait(bar(S::kKFull + ks), ((it + j) / S::kKStages) & 1, abort_flag, p.timeout_ns)))
-                    return false;
-                ptx::tc_fence_after();
-                if (leader) {
-                    issue_qk(j & 1, ks, 0);
-                    ptx::mma_commit(bar(S::kSFull + (j & 1)));
-                    ptx::mma_commit(bar(S::kKEmpty + ks));
-                    if (j + 1 == n) ptx::mma_commit(bar(S::kQEmpty));
-                }
-                return true;
-            };
-            ok = qk(0) && qk(1);
-            for (int j = 0; j < n && ok; ++j) {
-                const int t = j & 1;
-                const uint32_t vs = (it + j) % S::kVStages;
-                ok = ptx::warp_all(ptx::bar_wait(bar(S::kPFull + t), cnt[t] & 1, abort_flag, p.timeout_ns)) &&
-                     ptx::warp_all(ptx::bar_wait(bar(S::kVFull + vs), ((it + j) / S::kVStages) & 1, abort_flag, p.timeout_ns));
-                if (!ok) break;
-                ptx::tc_fence_after();
-                if (leader) issue_pv(t, vs, j > 1, 0);
-                if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kPFull2 + t), cnt[t] & 1, abort_flag, p.timeout_ns)))) break;
-                ptx::tc_fence_after();
-                if (leader) {
-                    issue_pv(t, vs, true, 1);
-                    if (j + 2 >= n) ptx::mma_commit(bar(S::kODone + t));
-                    ptx::mma_commit(bar(S::kVEmpty + vs));
-                }
-                ++cnt[t];
-                if (j + 2 < n) ok = qk(j + 2);
-            }
-            if (!ok) break;
-            it += n;
-            ++wi;
-            continue;
-        }
         {
             const uint32_t ks = it % S::kKStages;
             if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kKFull + ks), (it / S::kKStages) & 1, abort_flag, p.timeout_ns))))
@@ -424,7 +377,7 @@ __device__ void mma(const ChunkParams &p, uint32_t sbase, uint32_t tmem, const v
             for (int t = 0; t < 2; ++t) {
                 if (!visits(u.k, t, u.s0)) continue;
                 if (leader) {
-                    issue_qk(t, ks, t);
+                    issue_qk(t, ks);
                     ptx::mma_commit(bar(S::kSFull + t));
                 }
             }
@@ -469,7 +422,7 @@ __device__ void mma(const ChunkParams &p, uint32_t sbase, uint32_t tmem, const v
                     }
                     ptx::tc_fence_after();
                     if (leader) {
-                        issue_qk(t, kn, t);
+                        issue_qk(t, kn);
                         ptx::mma_commit(bar(S::kSFull + t));
                     }
                 }
@@ -501,31 +454,26 @@ __device__ void softmax(const ChunkParams &p, uint32_t sbase, uint32_t tmem, int
     const uint32_t tS = tmem + lane_base + S::kTmemS + t * 128;
     const uint32_t tO = tmem + lane_base + S::kTmemO + t * D;
     const float scale_log2 = p.scale_log2;
+    const uint64_t stream_pol = ptx::l2_policy_evict_first();
     uint32_t cnt = 0, items = 0;
     bool ok = true;
     Kept *kept = sh->kept + 4 * t + wq;
-    const uint32_t solo_ml = ptx::smem_addr(&sh->solo_ml), solo_done = ptx::smem_addr(&sh->solo_done);
-    uint32_t solos = 0;
     if (lane == 0) kept->walk.start(p, &sh->run);
     __syncwarp();
     while (ok) {
         // the key tiles of this part that the query tile visits: [x, x1), then [x2, x3)
-        // (of a tile that both warpgroups take: every second one of them)
-        int x, x1, x2, x3, stride, first, behind;
+        int x, x1, x2, x3, first, behind;
         {
             Walk walk = kept->walk;
             Part u;
             if (!walk.next(p, u)) break;
-            const bool solo = u.solo();  // (then its other query tile is empty)
-            auto mine = [&](const int (&v)[2]) { return t == 0 || solo ? v[0] : v[1]; };
+            auto mine = [&](const int (&v)[2]) { return t == 0 ? v[0] : v[1]; };
             const int up = u.k.lo - u.k.ns, ntok = mine(u.k.ntok);
-            stride = solo ? 2 : 1;
             x = u.s0;
             x1 = min(u.s1, mine(u.k.sink));
             x2 = max(max(mine(u.k.wlo), u.k.ns), u.s0 + up);
             x3 = min(mine(u.k.hi), u.s1 + up);
             if (x >= x1) x1 = x = x2;  // no first run
-            if (solo) x += t;
             first = u.s.L - u.s.Lq + mine(u.k.tok);  // the tile's first position
             behind = p.window > 0 ? first + ntok - 1 - p.window : -1;  // the last key behind its last window
             __syncwarp();
@@ -543,12 +491,9 @@ __device__ void softmax(const ChunkParams &p, uint32_t sbase, uint32_t tmem, int
         float m_used = -CUDART_INF_F;
         float l = 0.f;
         int mine = 0;  // steps taken
-        for (;; x += stride) {
-            if (x >= x1) {
-                x += x2 - x1;
-                x1 = INT_MAX;
-            }
-            if (x1 == INT_MAX && x >= x3) break;
+        for (;; ++x) {
+            if (x == x1) x = x2;
+            if (x >= x3 && x >= x1) break;
             ok = ptx::bar_wait(bar(S::kSFull + t), cnt & 1, abort_flag, p.timeout_ns);
             if (!__all_sync(kFull, ok)) { ok = false; break; }
             ptx::tc_fence_after();
@@ -653,62 +598,6 @@ __device__ void softmax(const ChunkParams &p, uint32_t sbase, uint32_t tmem, int
         const volatile Kept *end = kept;
         const int dest = end->dest, token = row / p.group;  // token within the tile
         const bool row_valid = token < end->ntok;           // (it has at most tile_tokens)
-        const size_t part = static_cast<size_t>(2 * blockIdx.x + (dest < 0 ? 0 : dest)) * p.part_rows + t * kBlockM + row;
-        const size_t tok = static_cast<size_t>(end->tok0) + token, h = end->h0 + row - token * p.group;
-        uint16_t *orow = static_cast<uint16_t *>(p.o) + (tok * p.H + h) * D;
-        if (stride == 2) {
-            // the two warpgroups' halves of the keys: warpgroup 0 joins them, a row of
-            // both O is in the same TMEM lane
-            if (t == 1) {
-                sh->ml[row] = make_float2(m_used, l);
-                __syncwarp();
-                if (lane == 0) ptx::bar_arrive(solo_ml);
-                ok = ptx::bar_wait(solo_done, solos++ & 1, abort_flag, p.timeout_ns);
-                if (!__all_sync(kFull, ok)) { ok = false; break; }
-                continue;
-            }
-            ok = ptx::bar_wait(solo_ml, solos++ & 1, abort_flag, p.timeout_ns);
-            if (!__all_sync(kFull, ok)) { ok = false; break; }
-            ptx::tc_fence_after();
-            const float2 other = sh->ml[row];
-            const float m = fmaxf(m_used, other.x);
-            const float f0 = m_used == -CUDART_INF_F ? 0.f : ptx::ex2(m_used - m);
-            const float f1 = other.x == -CUDART_INF_F ? 0.f : ptx::ex2(other.x - m);
-            l = l * f0 + other.y * f1;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const float g0 = dest >= 0 ? f0 : f0 * inv, g1 = dest >= 0 ? f1 : f1 * inv;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t a[32], b[32];
-                ptx::tmem_ld32(tO + c * 32, a);
-                ptx::tmem_ld32(tO + D + c * 32, b);
-                ptx::tmem_ld_wait();
-                ptx::reg_fence(a);
-                ptx::reg_fence(b);
-                auto v = [&](int i) { return fmaf(__uint_as_float(a[i]), g0, __uint_as_float(b[i]) * g1); };
-                if (row_valid && dest >= 0) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        reinterpret_cast<float4 *>(p.o_part + part * D)[8 * c + i / 4] =
-                            make_float4(v(i), v(i + 1), v(i + 2), v(i + 3));
-                } else if (row_valid) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        reinterpret_cast<uint4 *>(orow)[4 * c + i / 8] =
-                            make_uint4(ptx::pack2<BF16>(v(i), v(i + 1)), ptx::pack2<BF16>(v(i + 2), v(i + 3)),
-                                       ptx::pack2<BF16>(v(i + 4), v(i + 5)), ptx::pack2<BF16>(v(i + 6), v(i + 7)));
-                }
-                __syncwarp();  // the next loads are the warp's
-            }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::bar_arrive(solo_done);
-            if (row_valid) {
-                if (dest >= 0) p.ml_part[part] = make_float2(m, l);
-                else p.lse[h * p.total_q + tok] = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
-            }
-            continue;
-        }
         uint32_t o[D / 32][32];
         if (mine > 0) {
 #pragma unroll
@@ -723,15 +612,17 @@ __device__ void softmax(const ChunkParams &p, uint32_t sbase, uint32_t tmem, int
                 for (int i = 0; i < 32; ++i) o[c][i] = 0u;
         }
         if (dest >= 0) {
-            // a part: m, l and O as they are
+            // a part: m, l and O as they are, four columns of all rows after another, so
+            // that a warp's stores are whole lines
             if (row_valid) {
-                uint4 *dst = reinterpret_cast<uint4 *>(p.o_part + part * D);
+                const size_t part = 2 * blockIdx.x + dest, r = t * kBlockM + row;
+                float4 *dst = reinterpret_cast<float4 *>(p.o_part) + part * (D / 4) * p.part_rows + r;
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        dst[8 * c + i / 4] = make_uint4(o[c][i], o[c][i + 1], o[c][i + 2], o[c][i + 3]);
-                p.ml_part[part] = make_float2(m_used, l);
+                for (int c = 0; c < D; c += 4)
+                    dst[c / 4 * p.part_rows] =
+                        make_float4(__uint_as_float(o[c / 32][c % 32]), __uint_as_float(o[c / 32][c % 32 + 1]),
+                                    __uint_as_float(o[c / 32][c % 32 + 2]), __uint_as_float(o[c / 32][c % 32 + 3]));
+                p.ml_part[part * p.part_rows + r] = make_float2(m_used, l);
             }
             continue;
         }
@@ -739,16 +630,24 @@ __device__ void softmax(const ChunkParams &p, uint32_t sbase, uint32_t tmem, int
         const float inv_l = l == 0.f ? 0.f : 1.f / l;
         const float lse = l == 0.f ? -CUDART_INF_F : (m_used + __log2f(l)) * 0.69314718055994531f;
         if (row_valid) {
-            uint4 *dst = reinterpret_cast<uint4 *>(orow);
+            const size_t tok = static_cast<size_t>(end->tok0) + token, h = end->h0 + row - token * p.group;
+            uint16_t *orow = static_cast<uint16_t *>(p.o) + (tok * p.H + h) * D;
+            const bool v8 = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c)
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t pk[16];
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    auto two = [&](int x) {
-                        return ptx::pack2<BF16>(__uint_as_float(o[c][x]) * inv_l, __uint_as_float(o[c][x + 1]) * inv_l);
-                    };
-                    dst[4 * c + i / 8] = make_uint4(two(i), two(i + 2), two(i + 4), two(i + 6));
+                for (int i = 0; i < 16; ++i)
+                    pk[i] = ptx::pack2<BF16>(__uint_as_float(o[c][2 * i]) * inv_l, __uint_as_float(o[c][2 * i + 1]) * inv_l);
+                uint4 *dst = reinterpret_cast<uint4 *>(orow + c * 32);
+                if (v8) {
+                    ptx::st_global_v8_hint(dst, pk, stream_pol);
+                    ptx::st_global_v8_hint(dst + 2, pk + 8, stream_pol);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
                 }
+            }
             p.lse[h * p.total_q + tok] = lse;
         }
     }
@@ -768,9 +667,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kOffMisc + 4);
     Shared *sh = reinterpret_cast<Shared *>(smem + S::kOffSched);
     Run *run = &sh->run;
-    static_assert(S::kOffSched + sizeof(Shared) + 1024 <= kSmemBytes<D> && kSmemBytes<D> <= 227 * 1024 &&
-                      kPlanBytes <= S::kOffBar,
-                  "shared memory budget");
+    static_assert(sizeof(Shared) <= kSchedInts * 4 && kPlanBytes <= S::kOffBar, "shared memory budget");
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
     ptx::grid_launch_dependents();
@@ -783,8 +680,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 const bool p_full = i >= S::kPFull && i < S::kODone;
                 ptx::bar_init(bars + 8u * i, p_full ? kBlockM / 32 : 1u);
             }
-            ptx::bar_init(ptx::smem_addr(&sh->solo_ml), kBlockM / 32);
-            ptx::bar_init(ptx::smem_addr(&sh->solo_done), kBlockM / 32);
             *abort_flag = 0;
             ptx::bar_init_fence();
         }
@@ -836,43 +731,65 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 32;  // of a unit, per CTA
 
 // Joins the parts of units that fell into several runs: CTA x for the unit that
-// started in run x, if any. D / 4 lanes take a row.
+// started in run x, if any. A lane has a row, a warp D / 8 of its columns (reads are
+// whole lines); the rows go out through shared memory.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) fa_chunk_join_kernel(const ChunkParams p) {
-    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+    constexpr int kWarps = kJoinThreads / 32, kQuads = D / 4 / kWarps;  // of four columns, a warp
+    __shared__ uint2 tile[kJoinRows][D / 4 + 1];
     ptx::grid_dependency_wait();
     const int4 rec = __ldcg(p.records + blockIdx.x);  // first packed row, tokens, first head, 2 parts + slot of the first
     const int parts = min(rec.w / 2, static_cast<int>(gridDim.x - blockIdx.x)), slot = rec.w & 1;
     if (parts == 0) return;
-    const int d = threadIdx.x % kLanes * 4;
-    for (int i = threadIdx.x / kLanes; i < kJoinRows; i += kGroups) {
-        const int row = blockIdx.y * kJoinRows + i;
-        const int r = row % kBlockM, token = r / p.group, head = r - token * p.group;
-        const int tok = row / kBlockM * p.tile_tokens + token;
-        if (row >= p.part_rows || token >= p.tile_tokens || tok >= rec.y) continue;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    // token (of the unit) and head (of the group) of row r, -1 where it is none
+    auto where = [&](int r, int &head) {
+        const int token = r % kBlockM / p.group, tok = r / kBlockM * p.tile_tokens + token;
+        head = r % kBlockM - token * p.group;
+        return r < p.part_rows && token < p.tile_tokens && tok < rec.y ? tok : -1;
+    };
+    const int row = blockIdx.y * kJoinRows + lane;
+    int head;
+    const int tok = where(row, head);
+    if (tok >= 0) {
         // part 0 is in the slot it was given, later ones in the first of their CTAs
-        auto at = [&](int x) { return static_cast<size_t>(2 * (blockIdx.x + x) + (x == 0 ? slot : 0)) * p.part_rows + row; };
+        auto at = [&](int x) { return static_cast<size_t>(2 * (blockIdx.x + x) + (x == 0 ? slot : 0)); };
         float m = -CUDART_INF_F, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
+        for (int x = 0; x < parts; ++x) m = fmaxf(m, __ldcg(p.ml_part + at(x) * p.part_rows + row).x);
+        float4 o[kQuads];
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
         for (int x = 0; x < parts; ++x) {
-            const float2 ml = __ldcg(p.ml_part + at(x));
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.o_part + at(x) * D + d));
-            const float top = fmaxf(m, ml.x);
-            const float f = m == top ? 1.f : ptx::ex2(m - top), g = ml.x == -CUDART_INF_F ? 0.f : ptx::ex2(ml.x - top);
-            m = top;
-            l = fmaf(l, f, ml.y * g);
-            o.x = fmaf(o.x, f, v.x * g);
-            o.y = fmaf(o.y, f, v.y * g);
-            o.z = fmaf(o.z, f, v.z * g);
-            o.w = fmaf(o.w, f, v.w * g);
+            const float2 ml = __ldcg(p.ml_part + at(x) * p.part_rows + row);
+            const float4 *v = reinterpret_cast<const float4 *>(p.o_part) + (at(x) * (D / 4) + warp * kQuads) * p.part_rows + row;
+            const float f = ml.x == -CUDART_INF_F ? 0.f : ptx::ex2(ml.x - m);
+            l = fmaf(ml.y, f, l);
+#pragma unroll
+            for (int i = 0; i < kQuads; ++i) {
+                const float4 y = __ldcg(v + i * p.part_rows);
+                o[i].x = fmaf(y.x, f, o[i].x);
+                o[i].y = fmaf(y.y, f, o[i].y);
+                o[i].z = fmaf(y.z, f, o[i].z);
+                o[i].w = fmaf(y.w, f, o[i].w);
+            }
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const size_t t = static_cast<size_t>(rec.x) + tok, h = rec.z + head;
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + (t * p.H + h) * D + d) =
-            make_uint2(ptx::pack2<BF16>(o.x * inv, o.y * inv), ptx::pack2<BF16>(o.z * inv, o.w * inv));
-        if (d == 0)
-            p.lse[h * p.total_q + t] = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i)
+            tile[lane][warp * kQuads + i] = make_uint2(ptx::pack2<BF16>(o[i].x * inv, o[i].y * inv),
+                                                       ptx::pack2<BF16>(o[i].z * inv, o[i].w * inv));
+        if (warp == 0)
+            p.lse[static_cast<size_t>(rec.z + head) * p.total_q + rec.x + tok] =
+                l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kJoinRows * (D / 4); i += kJoinThreads) {
+        const int r = i / (D / 4), c = i % (D / 4), t = where(blockIdx.y * kJoinRows + r, head);
+        if (t >= 0)
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) +
+                                       (static_cast<size_t>(rec.x + t) * p.H + rec.z + head) * D + 4 * c) = tile[r][c];
     }
 }
 
@@ -880,7 +797,7 @@ template <int D, bool BF16>
 cudaError_t launch_t(const CUtensorMap *maps, const ChunkParams &p, int grid, cudaStream_t st) {
     static std::atomic<unsigned long long> done{0};
     auto kern = fa_chunk_kernel<D, BF16>;
-    constexpr int kSmem = kSmemBytes<D>;
+    constexpr int kSmem = FwdShape<D>::kSmemBytes;
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), kSmem, done);
     if (e != cudaSuccess) return e;
     kern<<<grid, kFwdThreads, kSmem, st>>>(maps[0], maps[1], maps[2], p);

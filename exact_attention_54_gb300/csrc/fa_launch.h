@@ -300,7 +300,7 @@ struct PagedParams {
 struct ChunkParams : PagedParams {
     void *o;                    // [total_q, H, D]
     float *lse;                 // [H, total_q]
-    float *o_part;              // [2 grid][part_rows][D], unnormalised parts of units
+    float *o_part;              // [2 grid][D / 4][part_rows][4], unnormalised parts of units
     float2 *ml_part;            // [2 grid][part_rows], their (m, l)
     int part_rows;              // rows of a unit
     int4 *records;              // [grid], units to be joined

@@ -297,7 +297,7 @@ def test_like_prefill_and_like_decode():
 @pytest.mark.gpu
 @pytest.mark.parametrize("load", [1, 3])
 def test_withheld_load_ends_with_an_error(load):
-    q, kc, vc, table, sl, cu = make([40], [13000], 16, 8, 64, 16, BF, 5)  # several steps in every CTA
+    q, kc, vc, table, sl, cu = make([40], [20000], 16, 8, 64, 16, BF, 5)  # several steps in every CTA
     good = run(q, kc, vc, table, sl, cu, 40)
     fa.fa_test_withhold_load(load, 20_000_000)
     try:

@@ -7,7 +7,7 @@ import random
 
 import pytest
 
-START = 2  # a unit's start, in key tiles
+START = 3  # a unit's start, in key tiles
 
 
 def tiles(pos0, Lq, tokens, window, sinks, pair):
