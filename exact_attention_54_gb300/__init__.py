@@ -1070,6 +1070,8 @@ def fa_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, kep
     num_blocks, Hkv, block_size, D = k_cache.shape
     code = _dtype_code(k_cache)
     B, keep = block_table.shape[0], kept.shape[2]
+    if keep < 1:
+        raise ValueError(f"kept must be [B,Hkv,keep] with keep at least 1, got {tuple(kept.shape)}")
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         _expect(name, t, (num_blocks, Hkv, block_size, D), k_cache.dtype)
     _expect("block_table", block_table, (B, block_table.shape[1]), torch.int32)
@@ -1172,6 +1174,8 @@ def flash_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, 
     if stream is not None:
         with _on_stream(stream, k_cache):
             return flash_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, keep, sinks, recent)
+    if int(keep) < 1:
+        raise ValueError(f"keep must be at least 1, got {keep}")
     B, Hkv, dev = block_table.shape[0], k_cache.shape[1], k_cache.device
     kept = torch.empty((B, Hkv, int(keep)), dtype=torch.int32, device=dev)
     new_lens = torch.empty((B,), dtype=torch.int32, device=dev)

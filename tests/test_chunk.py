@@ -341,3 +341,59 @@ def test_streams_graphs_and_workspaces():
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(call(a, 20), graphs[0][1]))
     fa.fa_check_device_error()
+
+
+@pytest.mark.gpu
+def test_many_long_chunks_among_many():
+    """More sequences with many query tiles than the plan's list holds: the same as in two calls of half as many."""
+    B, n, H = 4200, 36, 128  # one token a tile, 18 pairs a sequence
+    g = torch.Generator("cuda").manual_seed(3)
+    q = torch.randn(B * n, H, 64, generator=g, device="cuda").to(BF)
+    kc, vc = (torch.randn(B, 1, 64, 64, generator=g, device="cuda").to(BF) for _ in range(2))
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None]
+    sl = (torch.arange(B, device="cuda") % 29 + n).int()
+    cu = (torch.arange(B + 1, device="cuda") * n).int()
+    o, lse = fa.flash_attention_paged(q, kc, vc, table, cu, sl, n)
+    w = fa.flash_kv_weights(q, lse, kc, table, cu, sl, n)
+    half = B // 2
+    for sel, rows in ((slice(0, half), slice(0, half * n)), (slice(half, B), slice(half * n, B * n))):
+        part = (table[sel].contiguous(), cu[:half + 1].contiguous(), sl[sel].contiguous())
+        qp = q[rows].contiguous()
+        po, pl = fa.flash_attention_paged(qp, kc, vc, *part, n)
+        # (units may be cut at other places: the same but for the joins' rounding)
+        assert (po.float() - o[rows].float()).abs().max() <= 2.0 ** -6 and (pl - lse[:, rows]).abs().max() <= 1e-5
+        assert torch.equal(fa.flash_kv_weights(qp, lse[:, rows], kc, *part, n), w[sel])
+    fa.fa_check_device_error()
+    want = reference(q[:n].cpu(), kc.cpu(), vc.cpu(), table.cpu(), sl[:1].cpu(), cu[:2].cpu(), 0, 0, 0.125)
+    check(o[:n], lse[:, :n], want)
+
+
+@pytest.mark.gpu
+def test_caches_past_32_bits():
+    """Pages behind 2^32 bytes and 2^31 elements of a cache: written, attended, weighed and evicted from, as in a small
+    cache with the same rows."""
+    Hkv, block, D, H = 8, 16, 128, 16
+    count = (1 << 32) // (Hkv * block * D) + 40  # 2^32 elements and some more
+    g = torch.Generator().manual_seed(6)
+    big = [torch.empty(count, Hkv, block, D, dtype=BF, device="cuda") for _ in range(2)]
+    small = [torch.empty(24, Hkv, block, D, dtype=BF, device="cuda") for _ in range(2)]
+    far = torch.tensor([count - 1 - 3 * i for i in range(12)] + [5, (1 << 31) // (Hkv * block * D) + 1] +
+                       [count - 2 - 3 * i for i in range(10)], dtype=torch.int32)
+    near = torch.arange(24, dtype=torch.int32)
+    n = 14 * block - 5  # keys
+    q, k, v = (inputs.randn((n, h, D), BF, g).cuda() for h in (H, Hkv, Hkv))
+    f, _ = fa.rope_frequencies(D)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    sl = torch.tensor([n], dtype=torch.int32, device="cuda")
+    results = []
+    for (kc, vc), pages in ((big, far), (small, near)):
+        table, new = pages[None, :14].contiguous().cuda(), pages[None, 14:18].contiguous().cuda()
+        qr = fa.flash_rope_kv_write(q, k, v, kc, vc, table, cu, n, f)
+        o, lse = fa.flash_attention_paged(qr, kc, vc, table, cu, sl, n)
+        w = fa.flash_kv_weights(qr, lse, kc, table, cu, sl, n)
+        kept, left, nw = fa.flash_kv_evict(kc, vc, w, table, sl, new, 60, 2, 10)
+        last = fa.flash_attention_paged(qr[-3:].contiguous(), kc, vc, new, torch.tensor([0, 3], dtype=torch.int32).cuda(),
+                                        left, 3)
+        fa.fa_check_device_error()
+        results.append((qr, o, lse, w, kept, nw, *last))
+    assert all(torch.equal(a, b) for a, b in zip(*results))

@@ -71,6 +71,9 @@ def test_binding_refuses():
         call(nt=torch.zeros(2, 2, dtype=torch.int32))
     with pytest.raises(TypeError, match="seq_lens"):
         call(sl=sl.long())
+    for keep in (0, -1):
+        with pytest.raises(ValueError, match="keep"):
+            call(keep=keep)
 
 
 def test_definition():

@@ -373,3 +373,30 @@ def test_streams_and_graphs():
     assert torch.equal(out, fa.flash_rope(x.flip(0).contiguous(), f))
     empty = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
     assert fa.flash_rope(empty, f).shape == empty.shape
+
+
+@pytest.mark.gpu
+def test_write_of_no_tokens():
+    k = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    c = torch.ones(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = fa.flash_rope_kv_write(k, k, k, c, c, torch.zeros(2, 2, dtype=torch.int32, device="cuda"), i32(0, 0, 0), 0)
+    fa.fa_check_device_error()
+    assert q.shape == k.shape and (c == 1).all()
+
+
+@pytest.mark.gpu
+def test_one_token_in_each_of_many_sequences():
+    """Sequences over two dimensions of the grid (more than 65535)."""
+    B = 70000
+    g = torch.Generator("cuda").manual_seed(1)
+    k = torch.randn(B, 1, 64, generator=g, device="cuda").to(torch.float16)
+    kc, vc = (torch.zeros(B, 1, 1, 64, dtype=torch.float16, device="cuda") for _ in range(2))
+    table = torch.randperm(B, generator=g, device="cuda").to(torch.int32)[:, None].contiguous()
+    f, _ = fa.rope_frequencies(64)
+    pos = torch.randint(0, 1 << 20, (B,), generator=g, device="cuda").to(torch.int32)
+    q = fa.flash_rope_kv_write(k, k, k, kc, vc, table, torch.arange(B + 1, dtype=torch.int32, device="cuda"), 1, f, positions=pos)
+    fa.fa_check_device_error()
+    assert torch.equal(q, fa.flash_rope(k, f, pos))
+    at = table[:, 0].long()
+    assert torch.equal(kc[at, :, 0], q) and torch.equal(vc[at, :, 0], k)
