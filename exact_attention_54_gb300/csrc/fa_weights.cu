@@ -8,17 +8,19 @@
 // order. A unit is two key tiles of one key head, which stay in shared memory
 // while the query tiles that see any of them stream past (rows as in
 // fa_chunk.cuh); with one key tile, queries would come from L2 at 64 bytes a clock
-// and SM, twice what it gives. Each key tile has two TMEM buffers of 128 columns, so
-// the products of a step run while the step before is exponentiated, by two
-// warpgroups that share the columns (one alone, four warps fewer to hide each
-// other's latencies: 229 us for the case below). -lse log2 e of a step's columns
-// comes through shared memory, -inf where a column is no query.
+// and SM, twice what it gives. Two warpgroups take the steps in turn, each with a
+// TMEM buffer of 128 columns for each key tile: one waits for its scores while the
+// other keeps the exponentials going. -lse log2 e of a step's columns comes through
+// shared memory, -inf where a column is no query.
 //
-// Bound: long chunks by the exponentials (a 128 x 128 tile: 512 clocks of the SM
-// for them and 512 of the tensor core for the product, side by side); single
-// tokens by reading the keys.
-#include <type_traits>
-
+// Bound: single tokens by reading the keys (16 sequences of 4100 to 8192 keys, 8 key
+// heads, D = 128: 47 us, 4.4 TB/s, of which 8 us are the launch and the way to the first
+// keys). Long chunks by the exponentials: 512 tokens of four sequences of 8704 to 16896
+// keys, 32 heads on 8, take 210 us, 1190 TFLOP/s, 53 % of the rate of ex2; without the
+// products 204, products and loads alone 169 (both operands come from shared memory).
+// Measured beside this: both warpgroups on every step, half of the columns each, 229;
+// a step's scores loaded while the step before is added up, 265 to 317; sums two at a
+// time 248; four warpgroups 225.
 #include "fa_paged.cuh"
 
 namespace fa {
@@ -362,7 +364,7 @@ __device__ void sums(const WeightsParams &p, uint32_t sbase, uint32_t tmem, floa
     const uint32_t tS = tmem + (static_cast<uint32_t>(wq * 32) << 16) + 128 * mine;
     const int row = wq * 32 + lane;
     const uint64_t scale2 = ptx::pk2(p.scale_log2, p.scale_log2);
-    uint32_t it = 0, shared = 0;              // steps; units whose steps both warpgroups took
+    uint32_t it = 0, shared = 0;  // steps; units whose steps both warpgroups took
     bool ok = true;
     Walk walk(p, run);
     Unit u;
@@ -386,36 +388,12 @@ __device__ void sums(const WeightsParams &p, uint32_t sbase, uint32_t tmem, floa
             ptx::tc_fence_after();
             const int t0 = u.t0 + j * p.tile_tokens, n = min(p.tile_tokens, u.t1 - t0), first = pos0 + t0;
             const uint32_t nl_at = sbase + S::kOffL + ls * 512;
-            // the weights of columns 4 c to 4 c + 3 of the 32 in x
-            auto exps = [&](const uint32_t (&x)[32], int c, uint32_t at, float (&e)[4]) {
-                uint64_t nl[2];
-                load_pairs(at + 16 * c, nl);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x0, x1;
-                    ptx::upk2(ptx::ffma2(ptx::pk2(__uint_as_float(x[4 * c + 2 * h]), __uint_as_float(x[4 * c + 2 * h + 1])),
-                                         scale2, nl[h]), x0, x1);
-                    e[2 * h] = ptx::ex2(x0);
-                    e[2 * h + 1] = ptx::ex2(x1);
-                }
-            };
-            // adds 32 columns of both tiles
-            auto both = [&](const uint32_t (&x)[2][32], uint32_t at) {
-#pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    uint64_t nl[2];
-                    load_pairs(at + 4 * c, nl);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            float x0, x1;
-                            ptx::upk2(ptx::ffma2(ptx::pk2(__uint_as_float(x[t][c + 2 * h]), __uint_as_float(x[t][c + 2 * h + 1])),
-                                                 scale2, nl[h]), x0, x1);
-                            sum[t][2 * h] += ptx::ex2(x0);
-                            sum[t][2 * h + 1] += ptx::ex2(x1);
-                        }
-                }
+            // the weights of columns c and c + 1 of the 32 in x
+            auto exps = [&](const uint32_t (&x)[32], int c, uint64_t nl, float &e0, float &e1) {
+                float x0, x1;
+                ptx::upk2(ptx::ffma2(ptx::pk2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, nl), x0, x1);
+                e0 = ptx::ex2(x0);
+                e1 = ptx::ex2(x1);
             };
             // Some columns do not count for some keys: queries ahead of a key or too far
             // behind it, columns that are no query of the chunk but hold one's row (a
@@ -439,11 +417,16 @@ __device__ void sums(const WeightsParams &p, uint32_t sbase, uint32_t tmem, floa
                         ptx::tmem_ld_wait();
                         ptx::reg_fence(x);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            float e[4];
-                            exps(x, c, nl_at + 128 * b, e);
+                        for (int c = 0; c < 32; c += 4) {
+                            uint64_t nl[2];
+                            load_pairs(nl_at + 128 * b + 4 * c, nl);
 #pragma unroll
-                            for (int h = 0; h < 4; ++h) sum[t][h] += seen >> (4 * c + h) & 1 ? e[h] : 0.f;
+                            for (int h = 0; h < 4; h += 2) {
+                                float e0, e1;
+                                exps(x, c + h, nl[h / 2], e0, e1);
+                                sum[t][h] += seen >> (c + h) & 1 ? e0 : 0.f;
+                                sum[t][h + 1] += seen >> (c + h) & 2 ? e1 : 0.f;
+                            }
                         }
                     }
                 }
@@ -451,27 +434,34 @@ __device__ void sums(const WeightsParams &p, uint32_t sbase, uint32_t tmem, floa
                 __syncwarp();
                 if (lane == 0) ptx::bar_arrive(bar(S::kSEmpty + mine));
             } else {
-                const int halves = p.chunks / 2;  // of 64 columns
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (half >= halves) break;
-                    uint32_t x[2][2][32];
+                for (int c = 0; c < 4; ++c) {
+                    if (c >= p.chunks) break;
+                    uint32_t x[2][32];
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) ptx::tmem_ld32(tS + 256 * t + 64 * half + 32 * b, x[b][t]);
+                    for (int t = 0; t < 2; ++t) ptx::tmem_ld32(tS + 256 * t + 32 * c, x[t]);
                     ptx::tmem_ld_wait();
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) ptx::reg_fence(x[b][t]);
-                    if (half + 1 == halves) {
+                    ptx::reg_fence(x[0]);
+                    ptx::reg_fence(x[1]);
+                    if (c + 1 == p.chunks) {
                         ptx::tc_fence_before();
                         __syncwarp();
                         if (lane == 0) ptx::bar_arrive(bar(S::kSEmpty + mine));
                     }
-                    both(x[0], nl_at + 256 * half);
-                    both(x[1], nl_at + 256 * half + 128);
+#pragma unroll
+                    for (int d = 0; d < 32; d += 4) {
+                        uint64_t nl[2];
+                        load_pairs(nl_at + 128 * c + 4 * d, nl);
+#pragma unroll
+                        for (int h = 0; h < 4; h += 2)
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                float e0, e1;
+                                exps(x[t], d + h, nl[h / 2], e0, e1);
+                                sum[t][h] += e0;
+                                sum[t][h + 1] += e1;
+                            }
+                    }
                 }
             }
             __syncwarp();
@@ -483,9 +473,11 @@ __device__ void sums(const WeightsParams &p, uint32_t sbase, uint32_t tmem, floa
 #pragma unroll
         for (int t = 0; t < 2; ++t) total[t] = (sum[t][0] + sum[t][1]) + (sum[t][2] + sum[t][3]);
         if (u.steps > 1) {
-            // the other's sums go through shared memory to the one that writes
-            ok = writes ? ptx::bar_wait(bar(S::kPartFull), shared & 1, abort_flag, p.timeout_ns)
-                        : shared == 0 || ptx::bar_wait(bar(S::kPartEmpty), (shared - 1) & 1, abort_flag, p.timeout_ns);
+            // The other's sums go through shared memory to the one that writes. Both wait
+            // for the unit before to be through: neither barrier is then more than a
+            // phase away.
+            ok = shared == 0 || ptx::bar_wait(bar(S::kPartEmpty), (shared - 1) & 1, abort_flag, p.timeout_ns);
+            ok = ok && (!writes || ptx::bar_wait(bar(S::kPartFull), shared & 1, abort_flag, p.timeout_ns));
             if (!__all_sync(kFull, ok)) { ok = false; break; }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
