@@ -567,7 +567,8 @@ FA_API fa_status_t fa_decode_paged_q4(const void *q, const void *k_codes, const 
  *              b * x_batch + s * x_token + h * x_head of x, and alike of y:
  *              [B,S,H,D], [B,H,S,D], packed tokens (B = 1, S = total) or a part
  *              of a wider tensor. Strides are >= 0 and multiples of 8. y may be
- *              x itself (same strides); otherwise they must not overlap.
+ *              x itself (same strides); otherwise they must not overlap, nor
+ *              may y's rows each other.
  *   inv_freq   device fp32 [rot_dim / 2]
  *   positions  device int32 [B,S], or NULL: 0 .. S - 1. Any values: an angle is
  *              formed as a 64-bit fraction of a turn, so far positions keep

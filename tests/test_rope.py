@@ -81,6 +81,8 @@ def test_validation(lib):
     for kw in ({"B": 0}, {"S": -1}, {"S": (1 << 30) + 1}, {"H": 0}, {"H": 1 << 25}, {"rot": 0}, {"rot": 8}, {"rot": 144},
                {"rot": -16}, {"xs": (1920, 384, 4)}, {"ys": (-1920, 384, 128)}, {"xs": (1 << 41, 384, 128)}):
         assert call(**kw) == SHAPE, kw
+    for ys in ((0, 384, 128), (1920, 0, 128), (1920, 384, 0)):  # rows of y on one another
+        assert call(ys=ys) == SHAPE, ys
     assert call(m=float("nan")) == SCALE
     for kw in ("x", "y"):
         assert call(**{kw: MIS}) == ALIGN, kw
