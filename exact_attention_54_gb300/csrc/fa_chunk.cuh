@@ -671,6 +671,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
     ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     // the plan's scratch lies where the tiles go
     plan(p, Units{p}, run, smem);
     if (warp == 1) {
@@ -737,6 +738,7 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) fa_chunk_join_kernel(const ChunkParams p) {
     constexpr int kWarps = kJoinThreads / 32, kQuads = D / 4 / kWarps;  // of four columns, a warp
     __shared__ uint2 tile[kJoinRows][D / 4 + 1];
+    ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     const int4 rec = __ldcg(p.records + blockIdx.x);  // first packed row, tokens, first head, 2 parts + slot of the first
     const int parts = min(rec.w / 2, static_cast<int>(gridDim.x - blockIdx.x)), slot = rec.w & 1;
@@ -800,19 +802,16 @@ cudaError_t launch_t(const CUtensorMap *maps, const ChunkParams &p, int grid, cu
     constexpr int kSmem = FwdShape<D>::kSmemBytes;
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), kSmem, done);
     if (e != cudaSuccess) return e;
-    kern<<<grid, kFwdThreads, kSmem, st>>>(maps[0], maps[1], maps[2], p);
-    e = cudaGetLastError();
+    // Early where there is a unit for an SM at most (two short chunks 16.7 -> 14.5 us, 5
+    // tokens of 16 sequences of up to 8192 keys 79 -> 78). With more units it costs: the
+    // CTAs then lie where SMs came free first, not in their order (16 chunks of 1 to 512
+    // tokens 292 -> 303, 2048 tokens behind 30000 keys 627 -> 650).
+    const long long units = (static_cast<long long>(p.total_q / (2 * p.tile_tokens)) + p.B) * p.Hkv;
+    e = launch_early(kern, dim3(static_cast<unsigned>(grid)), kFwdThreads, kSmem, st, units <= grid, maps[0], maps[1],
+                     maps[2], p);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute pdl[1];
-    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), static_cast<unsigned>((p.part_rows + kJoinRows - 1) / kJoinRows));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = st;
-    cfg.attrs = pdl;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa_chunk_join_kernel<D, BF16>, p);
+    const dim3 join(static_cast<unsigned>(grid), static_cast<unsigned>((p.part_rows + kJoinRows - 1) / kJoinRows));
+    return launch_early(fa_chunk_join_kernel<D, BF16>, join, kJoinThreads, 0, st, true, p);
 }
 
 }  // namespace chunk

@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv_evict_select_kernel(const E
         else __syncthreads();
     };
     ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     const size_t bh = blockIdx.x / ctas;
     const int b = static_cast<int>(bh / p.Hkv);
     const int width = p.max_blocks << p.log2_bs, new_width = p.new_max_blocks << p.log2_bs;
@@ -208,6 +209,7 @@ template <int D>
 __global__ void __launch_bounds__(kCopyThreads) fa_kv_evict_copy_kernel(const EvictParams p) {
     constexpr int kLanes = D / 8, kGroups = kCopyThreads / kLanes;
     const long long bh = static_cast<long long>(blockIdx.z) * gridDim.y + blockIdx.y;
+    ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     if (bh >= static_cast<long long>(p.B) * p.Hkv) return;
     const int b = static_cast<int>(bh / p.Hkv), hk = static_cast<int>(bh % p.Hkv);
@@ -264,34 +266,28 @@ cudaError_t launch_kv_evict(int D, EvictParams p, int sms, cudaStream_t st) {
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(evict::fa_kv_evict_select_kernel),
                                evict::kMaxCached * static_cast<int>(sizeof(uint32_t)), done);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute cluster[1];
-    cluster[0].id = cudaLaunchAttributeClusterDimension;
-    cluster[0].val.clusterDim.x = static_cast<unsigned>(ctas);
-    cluster[0].val.clusterDim.y = 1;
-    cluster[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeClusterDimension;
+    attrs[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attrs[0].val.clusterDim.y = 1;
+    attrs[0].val.clusterDim.z = 1;
+    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_early
+    attrs[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t sel = {};
     sel.gridDim = dim3(units * static_cast<unsigned>(ctas));
     sel.blockDim = dim3(evict::kThreads);
     sel.dynamicSmemBytes = static_cast<size_t>(p.cached) * sizeof(uint32_t);
     sel.stream = st;
-    sel.attrs = cluster;
-    sel.numAttrs = 1;
+    sel.attrs = attrs;
+    sel.numAttrs = 2;
     e = cudaLaunchKernelEx(&sel, evict::fa_kv_evict_select_kernel, p);
     if (e != cudaSuccess) return e;
     const unsigned rows = static_cast<unsigned>(evict::kCopyThreads / (D / 8) * evict::kInFlight);
     const unsigned long long most = width < p.keep ? static_cast<unsigned long long>(width) : p.keep;
     const unsigned y = units < 65535u ? units : 65535u;
-    cudaLaunchAttribute pdl[1];
-    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((most + rows - 1) / rows), y, (units + y - 1) / y);
-    cfg.blockDim = dim3(evict::kCopyThreads);
-    cfg.stream = st;
-    cfg.attrs = pdl;
-    cfg.numAttrs = 1;
-    return D == 64 ? cudaLaunchKernelEx(&cfg, evict::fa_kv_evict_copy_kernel<64>, p)
-                   : cudaLaunchKernelEx(&cfg, evict::fa_kv_evict_copy_kernel<128>, p);
+    const dim3 grid(static_cast<unsigned>((most + rows - 1) / rows), y, (units + y - 1) / y);
+    return launch_early(D == 64 ? evict::fa_kv_evict_copy_kernel<64> : evict::fa_kv_evict_copy_kernel<128>, grid,
+                        evict::kCopyThreads, 0, st, true, p);
 }
 
 }  // namespace fa

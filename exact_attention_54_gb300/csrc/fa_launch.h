@@ -23,6 +23,25 @@ inline cudaError_t allow_smem(const void *kern, int bytes, std::atomic<unsigned 
     return e;
 }
 
+// Launches a kernel that (early) may start while the one before it in the stream
+// ends: it calls ptx::grid_dependency_wait() in every CTA, ahead of its first access
+// to global memory.
+template <class... Params, class... Args>
+inline cudaError_t launch_early(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
+                                bool early, const Args &...args) {
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = pdl;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Values written to the device error word: a kernel abandoned a wait, met an
 // out-of-range device-side index (a page number in a block table), or found
 // packed-sequence offsets that do not describe sequences inside the tensors

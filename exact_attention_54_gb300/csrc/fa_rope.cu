@@ -130,6 +130,8 @@ __device__ __forceinline__ void stream_rows(const RopeParams &p, const float2 *t
 template <bool BF16, bool INTER>
 __global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RopeParams p) {
     extern __shared__ float2 turns[];
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     const long long b = static_cast<long long>(blockIdx.z) * gridDim.y + blockIdx.y;
     if (b >= p.num_seqs) return;
     const int s0 = static_cast<int>(blockIdx.x) * p.tokens, n = min(p.tokens, p.total - s0);
@@ -156,6 +158,8 @@ template <bool BF16, bool INTER>
 __global__ void __launch_bounds__(kThreads) fa_rope_kv_write_kernel(const RopeParams p) {
     extern __shared__ float2 turns[];
     __shared__ long long rows[kMaxTokens];  // first key head's cache row of each token, or -1
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     const long long b = static_cast<long long>(blockIdx.z) * gridDim.y + blockIdx.y;
     if (b >= p.num_seqs) return;
     const int i0 = static_cast<int>(blockIdx.x) * p.tokens;
@@ -227,14 +231,14 @@ cudaError_t launch_rope(bool write, bool bf16, RopeParams p, int sms, cudaStream
     const unsigned seqs = static_cast<unsigned>(p.num_seqs), y = seqs < 65535u ? seqs : 65535u;
     const dim3 grid(static_cast<unsigned>((longest - 1) / p.tokens + 1), y, (seqs + y - 1) / y);
     const int smem = p.tokens * p.rot_dim / 2 * static_cast<int>(sizeof(float2));  // at most 32 KB
-#define FA_ROPE(BB, II)                                                                             \
-    if (bf16 == BB && (p.interleaved != 0) == II) {                                                 \
-        if (write) rope::fa_rope_kv_write_kernel<BB, II><<<grid, rope::kThreads, smem, st>>>(p);    \
-        else rope::fa_rope_kernel<BB, II><<<grid, rope::kThreads, smem, st>>>(p);                   \
-    }
-    FA_ROPE(false, false) FA_ROPE(false, true) FA_ROPE(true, false) FA_ROPE(true, true)
-#undef FA_ROPE
-    return cudaGetLastError();
+    using Kernel = void (*)(RopeParams);
+    static const Kernel kernels[2][2][2] = {
+        {{rope::fa_rope_kernel<false, false>, rope::fa_rope_kernel<false, true>},
+         {rope::fa_rope_kernel<true, false>, rope::fa_rope_kernel<true, true>}},
+        {{rope::fa_rope_kv_write_kernel<false, false>, rope::fa_rope_kv_write_kernel<false, true>},
+         {rope::fa_rope_kv_write_kernel<true, false>, rope::fa_rope_kv_write_kernel<true, true>}}};
+    return launch_early(kernels[write][bf16][p.interleaved != 0], grid, rope::kThreads, static_cast<size_t>(smem), st, true,
+                        p);
 }
 
 }  // namespace fa

@@ -258,7 +258,7 @@ __device__ void producer_lse(const WeightsParams &p, uint32_t sbase, float *ring
         for (int i = 0; i < 4; ++i) {
             x[i] = CUDART_INF_F;
             if (token[i] < n)
-                x[i] = __ldg(p.lse + static_cast<long long>(u.hk * p.group + head[i]) * p.lse_head +
+                x[i] = __ldcg(p.lse + static_cast<long long>(u.hk * p.group + head[i]) * p.lse_head +
                              static_cast<long long>(u.s.q0 + t0 + token[i]) * p.lse_token);
         }
         if (++j < u.steps) return true;
@@ -503,6 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     using S = Shape<D>;
     extern __shared__ __align__(1024) uint8_t smem[];  // (there is no room to align it)
     const uint32_t sbase = ptx::smem_addr(smem);
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     if ((sbase & 1023) != 0) {
         if (threadIdx.x == 0) atomicExch(p.err, kDeviceErrTimeout);
         return;
@@ -568,8 +570,8 @@ static cudaError_t launch_t(const CUtensorMap *maps, const WeightsParams &p, int
     auto kern = fa_kv_weights_kernel<D, BF16>;
     const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), Shape<D>::kSmemBytes, done);
     if (e != cudaSuccess) return e;
-    kern<<<grid, kThreads, Shape<D>::kSmemBytes, st>>>(maps[0], maps[1], p);
-    return cudaGetLastError();
+    return launch_early(kern, dim3(static_cast<unsigned>(grid)), kThreads, Shape<D>::kSmemBytes, st, true, maps[0],
+                        maps[1], p);
 }
 
 }  // namespace weights
