@@ -44,7 +44,7 @@ struct Shape {
     static constexpr int kOffQ = kOffK + kKUnits * 2 * kTileBytes;
     static constexpr int kOffL = kOffQ + kQStages * kTileBytes;
     static constexpr int kOffBar = kOffL + kLStages * 512;
-    static constexpr int kKFull = 0, kKEmpty = kKFull + kKUnits;
+    static constexpr int kKFull = 0, kKEmpty = kKFull + 2 * kKUnits;  // full: 2 unit + tile
     static constexpr int kQFull = kKEmpty + kKUnits, kQEmpty = kQFull + kQStages;
     static constexpr int kLFull = kQEmpty + kQStages, kLEmpty = kLFull + kLStages;
     static constexpr int kSFull = kLEmpty + kLStages, kSEmpty = kSFull + 2;  // + buffer
@@ -136,96 +136,83 @@ struct Walk {
     }
 };
 
-template <int D>
-__device__ void producer_k(const CUtensorMap *tk, const WeightsParams &p, uint32_t sbase, const volatile Run *run,
-                           volatile int *abort_flag) {
-    using S = Shape<D>;
-    auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
-    const bool leader = ptx::elect_one();
-    const Pages pages(p);
-    uint32_t it = 0;  // units loaded
-    bool ok = true;
-    Walk walk(p, run);
-    // a unit's pages are looked up while the one before it is waited for and loaded
-    Unit u, after;
-    int page[2], page_after[2];
-    auto look_up = [&](const Unit &x, int (&to)[2]) {
-        const Dead dead(p, x.s);
-        const Head at{x.b, x.hk, x.s.L};
-        to[0] = pages.look_up(p, at, dead, x.k0);
-        to[1] = pages.look_up(p, at, dead, x.k0 + kBlockN);
-    };
-    bool more = walk.next(u);
-    if (more) look_up(u, page);
-    for (; more; ++it) {
-        bool next = false;
-        if (it > 0) {  // (the first is not kept waiting)
-            next = walk.next(after);
-            if (next) look_up(after, page_after);
-        }
-        const Dead dead(p, u.s);
-        const Head at{u.b, u.hk, u.s.L};
-        const uint32_t stage = it % S::kKUnits;
-        if (it >= S::kKUnits &&
-            !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kKEmpty + stage), ((it / S::kKUnits) - 1) & 1, abort_flag,
-                                 p.timeout_ns))))
-            break;
-        const uint32_t dst = sbase + S::kOffK + stage * 2 * S::kTileBytes, full = bar(S::kKFull + stage);
-        if (p.log2_bs < 3) {
-            copy_small_pages<D>(p, at, dead, u.k0, p.k, dst);
-            copy_small_pages<D>(p, at, dead, u.k0 + kBlockN, p.k, dst + S::kTileBytes);
-            if (leader) ptx::bar_arrive(full);
-        } else {
-            if (leader) ptx::bar_arrive_expect_tx(full, 2 * S::kTileBytes);
-            __syncwarp();
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-                pages.load<D>(p, at, dead, u.k0 + t * kBlockN, page[t], tk, dst + t * S::kTileBytes, full);
-            __syncwarp();
-        }
-        if (it == 0) {
-            next = walk.next(after);
-            if (next) look_up(after, page_after);
-        }
-        more = next;
-        u = after;
-        page[0] = page_after[0];
-        page[1] = page_after[1];
-    }
-    for (uint32_t s = 0; s < S::kKUnits && s < it; ++s) {
-        const uint32_t last = (it - 1) - ((it - 1 - s) % S::kKUnits);
-        ptx::bar_wait(bar(S::kKFull + s), (last / S::kKUnits) & 1, nullptr, p.timeout_ns);
-    }
-}
-
-template <int D>
-__device__ void producer_q(const CUtensorMap *tq, const WeightsParams &p, uint32_t sbase, const volatile Run *run,
-                           volatile int *abort_flag) {
+// Key tile T of each unit, and (T = 1) the query tiles of its steps. One warp for
+// both key tiles issues 16-key pages' boxes (32 a unit) no faster than 5.4 TB/s; two
+// get 6.4.
+template <int D, int T>
+__device__ void producer(const CUtensorMap *tq, const CUtensorMap *tk, const WeightsParams &p, uint32_t sbase,
+                         const volatile Run *run, volatile int *abort_flag) {
     using S = Shape<D>;
     auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
     const bool leader = ptx::elect_one();
     const uint32_t bytes = static_cast<uint32_t>(p.tile_tokens * p.group * 128 * S::kColBlocks);
-    uint32_t it = 0;
+    const Pages pages(p);
+    uint32_t units = 0, it = 0;  // loaded: key tiles, query tiles
     bool ok = true;
     Walk walk(p, run);
-    Unit u;
-    while (ok && walk.next(u)) {
-        for (int j = 0; j < u.steps; ++j, ++it) {
-            const uint32_t stage = it % S::kQStages;
-            if (it >= S::kQStages &&
-                !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kQEmpty + stage), ((it / S::kQStages) - 1) & 1, abort_flag,
-                                     p.timeout_ns))))
-                break;
-            if (leader && !withheld(p.withhold, it)) {
-                ptx::bar_arrive_expect_tx(bar(S::kQFull + stage), bytes);
+    // a unit's pages are looked up while the one before it is waited for and loaded
+    Unit u, after;
+    int page = -1, page_after = -1;
+    auto look_up = [&](const Unit &x) {
+        return pages.look_up(p, Head{x.b, x.hk, x.s.L}, Dead(p, x.s), x.k0 + T * kBlockN);
+    };
+    bool more = walk.next(u);
+    if (more) page = look_up(u);
+    for (; more; ++units) {
+        bool next = false;
+        auto look_ahead = [&] {
+            next = walk.next(after);
+            if (next) page_after = look_up(after);
+        };
+        if (units > 0) look_ahead();  // (the first is not kept waiting)
+        const Dead dead(p, u.s);
+        const Head at{u.b, u.hk, u.s.L};
+        const uint32_t stage = units % S::kKUnits;
+        if (units >= S::kKUnits &&
+            !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kKEmpty + stage), ((units / S::kKUnits) - 1) & 1, abort_flag,
+                                 p.timeout_ns))))
+            break;
+        const uint32_t dst = sbase + S::kOffK + (2 * stage + T) * S::kTileBytes, full = bar(S::kKFull + 2 * stage + T);
+        if (p.log2_bs < 3) {
+            copy_small_pages<D>(p, at, dead, u.k0 + T * kBlockN, p.k, dst);
+            if (leader) ptx::bar_arrive(full);
+        } else {
+            if (leader) ptx::bar_arrive_expect_tx(full, S::kTileBytes);
+            __syncwarp();
+            pages.load<D>(p, at, dead, u.k0 + T * kBlockN, page, tk, dst, full);
+            __syncwarp();
+        }
+        if (T == 1) {
+            for (int j = 0; j < u.steps; ++j, ++it) {
+                const uint32_t qs = it % S::kQStages;
+                if (it >= S::kQStages &&
+                    !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kQEmpty + qs), ((it / S::kQStages) - 1) & 1, abort_flag,
+                                         p.timeout_ns))))
+                    break;
+                if (leader && !withheld(p.withhold, it)) {
+                    ptx::bar_arrive_expect_tx(bar(S::kQFull + qs), bytes);
 #pragma unroll
-                for (int c = 0; c < S::kColBlocks; ++c)
-                    ptx::tma_load_4d(sbase + S::kOffQ + stage * S::kTileBytes + c * S::kBlockBytes, tq,
-                                     bar(S::kQFull + stage), c * 64, 0, u.hk, u.s.q0 + u.t0 + j * p.tile_tokens);
+                    for (int c = 0; c < S::kColBlocks; ++c)
+                        ptx::tma_load_4d(sbase + S::kOffQ + qs * S::kTileBytes + c * S::kBlockBytes, tq,
+                                         bar(S::kQFull + qs), c * 64, 0, u.hk, u.s.q0 + u.t0 + j * p.tile_tokens);
+                }
             }
         }
+        if (units == 0) look_ahead();
+        if (!ok) {
+            ++units;
+            break;
+        }
+        more = next;
+        u = after;
+        page = page_after;
     }
-    for (uint32_t s = 0; s < S::kQStages && s < it; ++s) {
+    // never leave with copies in flight (bounded, even after an abort)
+    for (uint32_t s = 0; s < S::kKUnits && s < units; ++s) {
+        const uint32_t last = (units - 1) - ((units - 1 - s) % S::kKUnits);
+        ptx::bar_wait(bar(S::kKFull + 2 * s + T), (last / S::kKUnits) & 1, nullptr, p.timeout_ns);
+    }
+    for (uint32_t s = 0; T == 1 && s < S::kQStages && s < it; ++s) {
         const uint32_t last = (it - 1) - ((it - 1 - s) % S::kQStages);
         ptx::bar_wait(bar(S::kQFull + s), (last / S::kQStages) & 1, nullptr, p.timeout_ns);
     }
@@ -302,8 +289,11 @@ __device__ void mma(const WeightsParams &p, uint32_t sbase, uint32_t tmem, const
     Unit u;
     for (; ok && walk.next(u); ++units) {
         const uint32_t ks = units % S::kKUnits;
-        if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kKFull + ks), (units / S::kKUnits) & 1, abort_flag, p.timeout_ns))))
-            break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            ok = ok && ptx::warp_all(ptx::bar_wait(bar(S::kKFull + 2 * ks + t), (units / S::kKUnits) & 1, abort_flag,
+                                                   p.timeout_ns));
+        if (!ok) break;
         for (int j = 0; j < u.steps; ++j, ++it) {
             const uint32_t qs = it % S::kQStages, buf = it % 2;
             if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kQFull + qs), (it / S::kQStages) & 1, abort_flag, p.timeout_ns))))
@@ -544,10 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 0) producer_k<D>(&tm_k, p, sbase, run, abort_flag);
+    if (warp == 0) producer<D, 0>(&tm_q, &tm_k, p, sbase, run, abort_flag);
     else if (warp == 1) mma<D, BF16>(p, sbase, tmem, run, abort_flag);
     else if (warp == 2) producer_lse<D>(p, sbase, reinterpret_cast<float *>(smem + S::kOffL), run, abort_flag);
-    else if (warp == 3) producer_q<D>(&tm_q, p, sbase, run, abort_flag);
+    else if (warp == 3) producer<D, 1>(&tm_q, &tm_k, p, sbase, run, abort_flag);
     else {
         if (!p.add && run->per > 0) clear_rest(p, 128);  // (while the first keys are on their way)
         sums<D>(p, sbase, tmem, reinterpret_cast<float *>(smem + S::kOffPart), (warp - 4) / 4, warp % 4, lane, run,
