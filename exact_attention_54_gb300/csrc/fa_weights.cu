@@ -39,11 +39,11 @@ struct Shape {
     static constexpr int kTileBytes = FwdShape<D>::kTileBytes;
     static constexpr int kKUnits = D == 128 ? 2 : 4;   // units whose keys are loaded or loading
     static constexpr int kQStages = D == 128 ? 3 : 4;
-    static constexpr int kLStages = 3;
+    static constexpr int kLStages = 3, kLBytes = 512 + 32;  // -lse log2 e of 128 columns, and the step's Step
     static constexpr int kOffK = 0;
     static constexpr int kOffQ = kOffK + kKUnits * 2 * kTileBytes;
     static constexpr int kOffL = kOffQ + kQStages * kTileBytes;
-    static constexpr int kOffBar = kOffL + kLStages * 512;
+    static constexpr int kOffBar = kOffL + kLStages * kLBytes;
     static constexpr int kKFull = 0, kKEmpty = kKFull + 2 * kKUnits;  // full: 2 unit + tile
     static constexpr int kQFull = kKEmpty + kKUnits, kQEmpty = kQFull + kQStages;
     static constexpr int kLFull = kQEmpty + kQStages, kLEmpty = kLFull + kLStages;
@@ -51,10 +51,12 @@ struct Shape {
     static constexpr int kPartFull = kSEmpty + 2, kPartEmpty = kPartFull + 1;
     static constexpr int kTeardown = kPartEmpty + 1, kNumBars = kTeardown + 1;
     static constexpr int kOffMisc = (kOffBar + 8 * kNumBars + 15) & ~15;
-    static constexpr int kOffRun = kOffMisc + 16;
+    static constexpr int kOffSteps = kOffMisc + 16;  // int [kKUnits]: steps of the unit there, 0: no more units
+    static constexpr int kOffRun = kOffMisc + 32;
     static constexpr int kOffPart = (kOffRun + static_cast<int>(sizeof(Run)) + 15) & ~15;  // [2][128] sums
     static constexpr int kSmemBytes = kOffPart + 1024;
     static_assert(kSmemBytes <= 227 * 1024 && kPlanBytes <= kOffQ, "shared memory budget");
+    static_assert(kKUnits <= 4 && kLStages >= 2);
 };
 
 // Tokens [t0, t1) of a chunk that see a key of [k0, k0 + kUnitKeys).
@@ -87,10 +89,19 @@ struct Units {
     }
 };
 
-// The units that start in a CTA's run; every role walks them for itself.
+// The units that start in a CTA's run; the warps that load walk them, each for itself.
 struct Unit {
     int b, hk, k0, steps, t0, t1;
     Seq s;
+};
+
+// What the warps that add up need to know of a step: tokens [., . + n) of the
+// chunk, the first at position `first`; 0: no more steps.
+struct __align__(16) Step {
+    int n, first;
+    int j, steps;    // the step in its unit, the unit's
+    int k0, L, row;  // the unit's first key, the sequence's keys, its row of the weights
+    int pad;
 };
 
 struct Walk {
@@ -137,11 +148,10 @@ struct Walk {
 };
 
 // Key tile T of each unit, and (T = 1) the query tiles of its steps. One warp for
-// both key tiles issues 16-key pages' boxes (32 a unit) no faster than 5.4 TB/s; two
-// get 6.4.
+// both key tiles: 45.4 us for the first of the cases above in place of 42.0.
 template <int D, int T>
 __device__ void producer(const CUtensorMap *tq, const CUtensorMap *tk, const WeightsParams &p, uint32_t sbase,
-                         const volatile Run *run, volatile int *abort_flag) {
+                         volatile int *steps, const volatile Run *run, volatile int *abort_flag) {
     using S = Shape<D>;
     auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
     const bool leader = ptx::elect_one();
@@ -150,37 +160,33 @@ __device__ void producer(const CUtensorMap *tq, const CUtensorMap *tk, const Wei
     uint32_t units = 0, it = 0;  // loaded: key tiles, query tiles
     bool ok = true;
     Walk walk(p, run);
-    // a unit's pages are looked up while the one before it is waited for and loaded
-    Unit u, after;
-    int page = -1, page_after = -1;
-    auto look_up = [&](const Unit &x) {
-        return pages.look_up(p, Head{x.b, x.hk, x.s.L}, Dead(p, x.s), x.k0 + T * kBlockN);
-    };
-    bool more = walk.next(u);
-    if (more) page = look_up(u);
-    for (; more; ++units) {
-        bool next = false;
-        auto look_ahead = [&] {
-            next = walk.next(after);
-            if (next) page_after = look_up(after);
-        };
-        if (units > 0) look_ahead();  // (the first is not kept waiting)
+    Unit u{};
+    for (;; ++units) {
+        // the next unit's pages are on their way while its place is waited for
+        const bool more = walk.next(u);
+        if (T == 0 && !more) break;
         const Dead dead(p, u.s);
         const Head at{u.b, u.hk, u.s.L};
+        const int k0 = u.k0 + T * kBlockN, page = more ? pages.look_up(p, at, dead, k0) : -1;
         const uint32_t stage = units % S::kKUnits;
         if (units >= S::kKUnits &&
             !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kKEmpty + stage), ((units / S::kKUnits) - 1) & 1, abort_flag,
                                  p.timeout_ns))))
             break;
         const uint32_t dst = sbase + S::kOffK + (2 * stage + T) * S::kTileBytes, full = bar(S::kKFull + 2 * stage + T);
-        if (p.log2_bs < 3) {
-            copy_small_pages<D>(p, at, dead, u.k0 + T * kBlockN, p.k, dst);
+        if (T == 1 && leader) steps[stage] = more ? u.steps : 0;
+        if (!more || p.log2_bs < 3) {
+            if (more) copy_small_pages<D>(p, at, dead, k0, p.k, dst);
             if (leader) ptx::bar_arrive(full);
         } else {
             if (leader) ptx::bar_arrive_expect_tx(full, S::kTileBytes);
             __syncwarp();
-            pages.load<D>(p, at, dead, u.k0 + T * kBlockN, page, tk, dst, full);
+            pages.load<D>(p, at, dead, k0, page, tk, dst, full);
             __syncwarp();
+        }
+        if (!more) {
+            ++units;
+            break;
         }
         if (T == 1) {
             for (int j = 0; j < u.steps; ++j, ++it) {
@@ -197,15 +203,11 @@ __device__ void producer(const CUtensorMap *tq, const CUtensorMap *tk, const Wei
                                          bar(S::kQFull + qs), c * 64, 0, u.hk, u.s.q0 + u.t0 + j * p.tile_tokens);
                 }
             }
+            if (!ok) {
+                ++units;
+                break;
+            }
         }
-        if (units == 0) look_ahead();
-        if (!ok) {
-            ++units;
-            break;
-        }
-        more = next;
-        u = after;
-        page = page_after;
     }
     // never leave with copies in flight (bounded, even after an abort)
     for (uint32_t s = 0; s < S::kKUnits && s < units; ++s) {
@@ -218,10 +220,11 @@ __device__ void producer(const CUtensorMap *tq, const CUtensorMap *tk, const Wei
     }
 }
 
-// -lse log2 e of each column of each step; -inf for columns that are no query,
-// and for queries that see nothing.
+// Of each step its Step and -lse log2 e of its columns; -inf for columns that are no
+// query, and for queries that see nothing. Then a Step without tokens for each
+// warpgroup.
 template <int D>
-__device__ void producer_lse(const WeightsParams &p, uint32_t sbase, float *ring, const volatile Run *run,
+__device__ void producer_lse(const WeightsParams &p, uint32_t sbase, uint8_t *ring, const volatile Run *run,
                              volatile int *abort_flag) {
     using S = Shape<D>;
     auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
@@ -233,48 +236,47 @@ __device__ void producer_lse(const WeightsParams &p, uint32_t sbase, float *ring
         head[i] = lane + 32 * i - token[i] * p.group;
     }
     uint32_t it = 0;
-    bool ok = true;
     Walk walk(p, run);
     Unit u{};
-    int j = 0;
-    // values of the step at (u, j), which moves on; a step's are loaded while the
-    // ring's place for the one before it is waited for
-    auto load = [&](float (&x)[4]) {
-        const int t0 = u.t0 + j * p.tile_tokens, n = min(p.tile_tokens, u.t1 - t0);
+    int j = 0, end = 0;
+    while (end < 2) {
+        if (j >= u.steps && end == 0) {
+            j = 0;
+            if (!walk.next(u)) end = 1;
+        } else if (end == 1) {
+            end = 2;
+        }
+        const int t0 = u.t0 + j * p.tile_tokens, n = end > 0 ? 0 : min(p.tile_tokens, u.t1 - t0);
+        float x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             x[i] = CUDART_INF_F;
             if (token[i] < n)
                 x[i] = __ldcg(p.lse + static_cast<long long>(u.hk * p.group + head[i]) * p.lse_head +
-                             static_cast<long long>(u.s.q0 + t0 + token[i]) * p.lse_token);
+                              static_cast<long long>(u.s.q0 + t0 + token[i]) * p.lse_token);
         }
-        if (++j < u.steps) return true;
-        j = 0;
-        return walk.next(u);
-    };
-    float x[4], after[4];
-    bool more = walk.next(u), next = false;
-    if (more) next = load(x);
-    for (; more; ++it) {
-        more = next;
-        if (more) next = load(after);
         const uint32_t stage = it % S::kLStages;
         if (it >= S::kLStages &&
-            !(ok = ptx::warp_all(ptx::bar_wait(bar(S::kLEmpty + stage), ((it / S::kLStages) - 1) & 1, abort_flag,
-                                 p.timeout_ns))))
+            !ptx::warp_all(ptx::bar_wait(bar(S::kLEmpty + stage), ((it / S::kLStages) - 1) & 1, abort_flag,
+                                         p.timeout_ns)))
             break;
+        uint8_t *to = ring + stage * S::kLBytes;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            ring[stage * 128 + lane + 32 * i] = x[i] == -CUDART_INF_F ? -CUDART_INF_F : x[i] * -1.4426950408889634f;
-            x[i] = after[i];
-        }
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<float *>(to)[lane + 32 * i] =
+                x[i] == -CUDART_INF_F ? -CUDART_INF_F : x[i] * -1.4426950408889634f;
+        if (lane == 0)
+            *reinterpret_cast<Step *>(to + 512) =
+                Step{n, u.s.L - u.s.Lq + t0, j, u.steps, u.k0, u.s.L, u.b * p.Hkv + u.hk, 0};
         __syncwarp();
         if (lane == 0) ptx::bar_arrive(bar(S::kLFull + stage));
+        ++it;
+        ++j;
     }
 }
 
 template <int D, bool BF16>
-__device__ void mma(const WeightsParams &p, uint32_t sbase, uint32_t tmem, const volatile Run *run,
+__device__ void mma(const WeightsParams &p, uint32_t sbase, uint32_t tmem, const volatile int *steps,
                     volatile int *abort_flag) {
     using S = Shape<D>;
     auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
@@ -283,18 +285,18 @@ __device__ void mma(const WeightsParams &p, uint32_t sbase, uint32_t tmem, const
     const uint64_t dq0 = ptx::smem_desc_sw128(sbase + S::kOffQ, 16, 1024);
     const uint64_t dk0 = ptx::smem_desc_sw128(sbase + S::kOffK, 16, 1024);
     constexpr uint64_t kTile16 = S::kTileBytes >> 4, kBlock16 = S::kBlockBytes >> 4;
-    uint32_t units = 0, it = 0;
+    uint32_t it = 0;
     bool ok = true;
-    Walk walk(p, run);
-    Unit u;
-    for (; ok && walk.next(u); ++units) {
+    for (uint32_t units = 0; ok; ++units) {
         const uint32_t ks = units % S::kKUnits;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-            ok = ok && ptx::warp_all(ptx::bar_wait(bar(S::kKFull + 2 * ks + t), (units / S::kKUnits) & 1, abort_flag,
-                                                   p.timeout_ns));
-        if (!ok) break;
-        for (int j = 0; j < u.steps; ++j, ++it) {
+        auto wait_k = [&](int t) {
+            return ptx::warp_all(ptx::bar_wait(bar(S::kKFull + 2 * ks + t), (units / S::kKUnits) & 1, abort_flag,
+                                               p.timeout_ns));
+        };
+        if (!(ok = wait_k(1))) break;
+        const int n = steps[ks];
+        if (n == 0 || !(ok = wait_k(0))) break;
+        for (int j = 0; j < n; ++j, ++it) {
             const uint32_t qs = it % S::kQStages, buf = it % 2;
             if (!(ok = ptx::warp_all(ptx::bar_wait(bar(S::kQFull + qs), (it / S::kQStages) & 1, abort_flag, p.timeout_ns))))
                 break;
@@ -303,7 +305,7 @@ __device__ void mma(const WeightsParams &p, uint32_t sbase, uint32_t tmem, const
                 break;
             ptx::tc_fence_after();
             if (leader) {
-#pragma unroll
+#pragma unroll 1
                 for (int t = 0; t < 2; ++t) {
                     const uint64_t kd = dk0 + (2 * ks + t) * kTile16, qd = dq0 + qs * kTile16;
 #pragma unroll
@@ -314,7 +316,7 @@ __device__ void mma(const WeightsParams &p, uint32_t sbase, uint32_t tmem, const
                 }
                 ptx::mma_commit(bar(S::kSFull + buf));
                 ptx::mma_commit(bar(S::kQEmpty + qs));
-                if (j + 1 == u.steps) ptx::mma_commit(bar(S::kKEmpty + ks));
+                if (j + 1 == n) ptx::mma_commit(bar(S::kKEmpty + ks));
             }
         }
     }
@@ -345,120 +347,128 @@ __device__ __forceinline__ void clear_rest(const WeightsParams &p, int first) {
 
 // Sums of both key tiles' rows over every second step: a thread has a key of each.
 // The two warpgroups are a step apart, so one waits for its scores while the other
-// keeps the exponentials going.
+// keeps the exponentials going. Who takes a unit's first step writes its sums.
 template <int D>
-__device__ void sums(const WeightsParams &p, uint32_t sbase, uint32_t tmem, float *part, uint32_t mine, int wq,
-                     int lane, const volatile Run *run, volatile int *abort_flag) {
+__device__ void sums(const WeightsParams &p, uint32_t sbase, uint32_t tmem, float *part, const uint8_t *ring, uint32_t mine,
+                     int wq, int lane, volatile int *abort_flag) {
     using S = Shape<D>;
     auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
     const uint32_t tS = tmem + (static_cast<uint32_t>(wq * 32) << 16) + 128 * mine;
     const int row = wq * 32 + lane;
     const uint64_t scale2 = ptx::pk2(p.scale_log2, p.scale_log2);
-    uint32_t it = 0, shared = 0;  // steps; units whose steps both warpgroups took
-    bool ok = true;
-    Walk walk(p, run);
-    Unit u;
-    while (ok && walk.next(u)) {
-        const int pos0 = u.s.L - u.s.Lq, key = u.k0 + row;  // and key + kBlockN
-        float *w = p.weights + (static_cast<size_t>(u.b) * p.Hkv + u.hk) * (static_cast<size_t>(p.max_blocks) << p.log2_bs);
-        // who writes the unit's sums: the one that takes its first step
-        const bool writes = it % 2 == mine;
-        float before[2] = {0.f, 0.f};
-        if (p.add && writes) {  // (ahead of their use)
+    uint32_t shared = 0;  // units whose steps both warpgroups took
+    float before[2], sum[2][4];  // of column c: c % 4
+    for (uint32_t it = mine;; it += 2) {
+        const uint32_t ls = it % S::kLStages;
+        bool ok = ptx::bar_wait(bar(S::kLFull + ls), (it / S::kLStages) & 1, abort_flag, p.timeout_ns);
+        if (!__all_sync(kFull, ok)) break;
+        const Step u = *reinterpret_cast<const Step *>(ring + ls * S::kLBytes + 512);
+        if (u.n == 0) break;
+        const bool writes = u.j % 2 == 0;
+        const int key = u.k0 + row;  // and key + kBlockN
+        float *w = p.weights + static_cast<size_t>(u.row) * (static_cast<size_t>(p.max_blocks) << p.log2_bs);
+        if (u.j < 2) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-                if (key + t * kBlockN < u.s.L) before[t] = w[key + t * kBlockN];
+            for (int t = 0; t < 2; ++t) {
+                before[t] = 0.f;
+                if (p.add && writes && key + t * kBlockN < u.L) before[t] = w[key + t * kBlockN];  // (ahead of its use)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) sum[t][c] = 0.f;
+            }
         }
-        float sum[2][4] = {};  // of column c: c % 4
-        for (int j = writes ? 0 : 1; j < u.steps; j += 2) {
-            const uint32_t i = it + j, ls = i % S::kLStages;
-            ok = ptx::bar_wait(bar(S::kLFull + ls), (i / S::kLStages) & 1, abort_flag, p.timeout_ns) &&
-                 ptx::bar_wait(bar(S::kSFull + mine), (i / 2) & 1, abort_flag, p.timeout_ns);
-            if (!__all_sync(kFull, ok)) { ok = false; break; }
-            ptx::tc_fence_after();
-            const int t0 = u.t0 + j * p.tile_tokens, n = min(p.tile_tokens, u.t1 - t0), first = pos0 + t0;
-            const uint32_t nl_at = sbase + S::kOffL + ls * 512;
-            // the weights of columns c and c + 1 of the 32 in x
-            auto exps = [&](const uint32_t (&x)[32], int c, uint64_t nl, float &e0, float &e1) {
-                float x0, x1;
-                ptx::upk2(ptx::ffma2(ptx::pk2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, nl), x0, x1);
-                e0 = ptx::ex2(x0);
-                e1 = ptx::ex2(x1);
-            };
-            // Some columns do not count for some keys: queries ahead of a key or too far
-            // behind it, columns that are no query of the chunk but hold one's row (a
-            // chunk's last step), or nobody's (an odd number of 32s).
-            const bool masked = n < p.tile_tokens || u.k0 + kUnitKeys - 1 > first || p.chunks % 2 != 0 ||
-                                (p.window > 0 && u.k0 + kUnitKeys > p.sinks && u.k0 <= first + n - 1 - p.window);
-            if (masked) {
+        ok = ptx::bar_wait(bar(S::kSFull + mine), (it / 2) & 1, abort_flag, p.timeout_ns);
+        if (!__all_sync(kFull, ok)) break;
+        ptx::tc_fence_after();
+        const uint32_t nl_at = sbase + S::kOffL + ls * S::kLBytes;
+        // the weights of columns with scores a and b, and -lse in nl
+        auto exps = [&](uint32_t a, uint32_t b, uint64_t nl, float &e0, float &e1) {
+            float x0, x1;
+            ptx::upk2(ptx::ffma2(ptx::pk2(__uint_as_float(a), __uint_as_float(b)), scale2, nl), x0, x1);
+            e0 = ptx::ex2(x0);
+            e1 = ptx::ex2(x1);
+        };
+        // Some columns do not count for some keys: queries ahead of a key or too far
+        // behind it, columns that are no query of the chunk but hold one's row (a
+        // chunk's last step), or nobody's (an odd number of 32s).
+        const bool masked = u.n < p.tile_tokens || u.k0 + kUnitKeys - 1 > u.first || p.chunks % 2 != 0 ||
+                            (p.window > 0 && u.k0 + kUnitKeys > p.sinks && u.k0 <= u.first + u.n - 1 - p.window);
+        if (masked) {
+            int c0[2], c1[2];  // the columns that see the two keys
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int k = key + t * kBlockN;
+                c0[t] = min(max(k - u.first, 0), 128) * p.group;
+                c1[t] = u.n;
+                if (p.window > 0 && k >= p.sinks) c1[t] = min(c1[t], max(k + p.window - u.first, 0));
+                c1[t] *= p.group;
+            }
+#pragma unroll 1
+            for (int b = 0; b < u.n * p.group; b += 16) {
+                uint32_t x[2][16];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) ptx::tmem_ld16(tS + 256 * t + b, x[t]);
+                ptx::tmem_ld_wait();
+                ptx::reg_fence(x[0]);
+                ptx::reg_fence(x[1]);
+                uint32_t seen[2];  // its bits of these columns
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const int k = key + t * kBlockN;  // seen by the columns [c0, c1)
-                    const int c0 = min(max(k - first, 0), 128) * p.group;
-                    int c1 = n;
-                    if (p.window > 0 && k >= p.sinks) c1 = min(c1, max(k + p.window - first, 0));
-                    c1 *= p.group;
-#pragma unroll 1
-                    for (int b = 0; b < p.chunks; ++b) {
-                        auto below = [&](int c) { return static_cast<uint32_t>((1ull << min(max(c - 32 * b, 0), 32)) - 1); };
-                        const uint32_t seen = below(c1) & ~below(c0);
-                        uint32_t x[32];
-                        ptx::tmem_ld32(tS + 256 * t + 32 * b, x);
-                        ptx::tmem_ld_wait();
-                        ptx::reg_fence(x);
-#pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            uint64_t nl[2];
-                            load_pairs(nl_at + 128 * b + 4 * c, nl);
-#pragma unroll
-                            for (int h = 0; h < 4; h += 2) {
-                                float e0, e1;
-                                exps(x, c + h, nl[h / 2], e0, e1);
-                                sum[t][h] += seen >> (c + h) & 1 ? e0 : 0.f;
-                                sum[t][h + 1] += seen >> (c + h) & 2 ? e1 : 0.f;
-                            }
-                        }
-                    }
+                    auto below = [&](int c) { return (1u << min(max(c - b, 0), 16)) - 1; };
+                    seen[t] = below(c1[t]) & ~below(c0[t]);
                 }
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::bar_arrive(bar(S::kSEmpty + mine));
-            } else {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c >= p.chunks) break;
-                    uint32_t x[2][32];
+                for (int c = 0; c < 16; c += 4) {
+                    uint64_t nl[2];
+                    load_pairs(nl_at + 4 * (b + c), nl);
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) ptx::tmem_ld32(tS + 256 * t + 32 * c, x[t]);
-                    ptx::tmem_ld_wait();
-                    ptx::reg_fence(x[0]);
-                    ptx::reg_fence(x[1]);
-                    if (c + 1 == p.chunks) {
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::bar_arrive(bar(S::kSEmpty + mine));
-                    }
+                    for (int h = 0; h < 4; h += 2)
 #pragma unroll
-                    for (int d = 0; d < 32; d += 4) {
-                        uint64_t nl[2];
-                        load_pairs(nl_at + 128 * c + 4 * d, nl);
-#pragma unroll
-                        for (int h = 0; h < 4; h += 2)
-#pragma unroll
-                            for (int t = 0; t < 2; ++t) {
-                                float e0, e1;
-                                exps(x[t], d + h, nl[h / 2], e0, e1);
-                                sum[t][h] += e0;
-                                sum[t][h + 1] += e1;
-                            }
-                    }
+                        for (int t = 0; t < 2; ++t) {
+                            float e0, e1;
+                            exps(x[t][c + h], x[t][c + h + 1], nl[h / 2], e0, e1);
+                            sum[t][h] += seen[t] >> (c + h) & 1 ? e0 : 0.f;
+                            sum[t][h + 1] += seen[t] >> (c + h) & 2 ? e1 : 0.f;
+                        }
                 }
             }
+            ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::bar_arrive(bar(S::kLEmpty + ls));
+            if (lane == 0) ptx::bar_arrive(bar(S::kSEmpty + mine));
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (c >= p.chunks) break;
+                uint32_t x[2][32];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) ptx::tmem_ld32(tS + 256 * t + 32 * c, x[t]);
+                ptx::tmem_ld_wait();
+                ptx::reg_fence(x[0]);
+                ptx::reg_fence(x[1]);
+                if (c + 1 == p.chunks) {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::bar_arrive(bar(S::kSEmpty + mine));
+                }
+#pragma unroll
+                for (int d = 0; d < 32; d += 4) {
+                    uint64_t nl[2];
+                    load_pairs(nl_at + 128 * c + 4 * d, nl);
+#pragma unroll
+                    for (int h = 0; h < 4; h += 2)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            float e0, e1;
+                            exps(x[t][d + h], x[t][d + h + 1], nl[h / 2], e0, e1);
+                            sum[t][h] += e0;
+                            sum[t][h + 1] += e1;
+                        }
+                }
+            }
         }
-        if (!ok) break;
-        it += u.steps;
+        __syncwarp();
+        if (lane == 0) ptx::bar_arrive(bar(S::kLEmpty + ls));
+        if (u.j + 2 < u.steps) continue;
+        // this warpgroup's last step of the unit
         float total[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) total[t] = (sum[t][0] + sum[t][1]) + (sum[t][2] + sum[t][3]);
@@ -468,7 +478,7 @@ __device__ void sums(const WeightsParams &p, uint32_t sbase, uint32_t tmem, floa
             // phase away.
             ok = shared == 0 || ptx::bar_wait(bar(S::kPartEmpty), (shared - 1) & 1, abort_flag, p.timeout_ns);
             ok = ok && (!writes || ptx::bar_wait(bar(S::kPartFull), shared & 1, abort_flag, p.timeout_ns));
-            if (!__all_sync(kFull, ok)) { ok = false; break; }
+            if (!__all_sync(kFull, ok)) break;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (writes) total[t] += part[t * kBlockN + row];
@@ -481,7 +491,7 @@ __device__ void sums(const WeightsParams &p, uint32_t sbase, uint32_t tmem, floa
         if (writes) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
-                if (key + t * kBlockN < u.s.L) w[key + t * kBlockN] = before[t] + total[t];
+                if (key + t * kBlockN < u.L) w[key + t * kBlockN] = before[t] + total[t];
         }
     }
 }
@@ -534,14 +544,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 0) producer<D, 0>(&tm_q, &tm_k, p, sbase, run, abort_flag);
-    else if (warp == 1) mma<D, BF16>(p, sbase, tmem, run, abort_flag);
-    else if (warp == 2) producer_lse<D>(p, sbase, reinterpret_cast<float *>(smem + S::kOffL), run, abort_flag);
-    else if (warp == 3) producer<D, 1>(&tm_q, &tm_k, p, sbase, run, abort_flag);
+    volatile int *steps = reinterpret_cast<volatile int *>(smem + S::kOffSteps);
+    if (warp == 0) producer<D, 0>(&tm_q, &tm_k, p, sbase, steps, run, abort_flag);
+    else if (warp == 1) mma<D, BF16>(p, sbase, tmem, steps, abort_flag);
+    else if (warp == 2) producer_lse<D>(p, sbase, smem + S::kOffL, run, abort_flag);
+    else if (warp == 3) producer<D, 1>(&tm_q, &tm_k, p, sbase, steps, run, abort_flag);
     else {
         if (!p.add && run->per > 0) clear_rest(p, 128);  // (while the first keys are on their way)
-        sums<D>(p, sbase, tmem, reinterpret_cast<float *>(smem + S::kOffPart), (warp - 4) / 4, warp % 4, lane, run,
-                abort_flag);
+        sums<D>(p, sbase, tmem, reinterpret_cast<float *>(smem + S::kOffPart), smem + S::kOffL, (warp - 4) / 4, warp % 4,
+                lane, abort_flag);
     }
 
     ptx::tc_fence_before();
