@@ -25,6 +25,7 @@ constexpr int kThreads = 1024;
 constexpr int kMaxCtas = 8;            // of a cluster (the portable size)
 constexpr int kMaxCached = 44 * 1024;  // keys whose weights a CTA's shared memory holds
 constexpr int kBins = 2048;
+constexpr int kBatch = 8;  // loads of a thread in flight
 constexpr unsigned kFull = 0xffffffffu;
 
 // A weight's bits, ordered like the weights as unsigned integers: -0 is +0, a NaN is below everything.
@@ -83,21 +84,17 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv_evict_select_kernel(const E
     const int candidates = L - p.sinks - p.recent, each = (candidates + ctas - 1) / ctas;
     const int base = p.sinks + min(cta * each, candidates), count = min(each, p.sinks + candidates - base);
     const int held = min(count, p.cached);
-    if (choose) {
-        for (int i = tid; i < 3 * kBins; i += kThreads) hist[0][i] = 0;
-        for (int j0 = 0; j0 < held; j0 += 8 * kThreads) {  // eight loads of a thread in flight
-            float x[8];
+    float v[kBatch];
+    auto load = [&](int j0) {  // all of a thread's loads in flight
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int j = j0 + i * kThreads + tid;
-                x[i] = j < held ? w[base + j] : 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int j = j0 + i * kThreads + tid;
-                if (j < held) cached[j] = order(x[i]);
-            }
+        for (int i = 0; i < kBatch; ++i) {
+            const int j = j0 + i * kThreads + tid;
+            v[i] = j < held ? w[base + j] : 0.f;
         }
+    };
+    if (choose) {
+        load(0);
+        for (int i = tid; i < 3 * kBins; i += kThreads) hist[0][i] = 0;
     }
     if (bh % p.Hkv == 0 && all == 0) p.new_lens[b] = n;
     for (int i = n + all; i < p.keep; i += step) kept[i] = -1;
@@ -109,6 +106,14 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv_evict_select_kernel(const E
     for (int i = all; i < p.sinks; i += step) store(i, i, w[i]);
     for (int i = all; i < p.recent; i += step) store(p.keep - p.recent + i, L - p.recent + i, w[L - p.recent + i]);
     if (!choose) return;
+    for (int j0 = 0; j0 < held; j0 += kBatch * kThreads) {
+        if (j0 > 0) load(j0);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int j = j0 + i * kThreads + tid;
+            if (j < held) cached[j] = order(v[i]);
+        }
+    }
     __syncthreads();
 
     auto rank = [&](int j) { return j < held ? cached[j] : order(w[base + j]); };
@@ -152,15 +157,31 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv_evict_select_kernel(const E
         at = __ffs(__ballot_sync(kFull, upto >= left)) - 1;
         left -= __shfl_sync(kFull, upto - two.x - two.y, at);
         int bin = __shfl_sync(kFull, low, at);
-        const uint32_t upper = __shfl_sync(kFull, two.y, at);
-        if (upper >= left) ++bin;
+        const uint32_t upper = __shfl_sync(kFull, two.y, at), lower = __shfl_sync(kFull, two.x, at);
+        const bool in_upper = upper >= left;
+        if (in_upper) ++bin;
         else left -= upper;
         last |= static_cast<uint32_t>(bin) << shift;
+        // all keys with these digits stay (mostly so after two of them): no more to find
+        if (left == (in_upper ? upper : lower) && last > 0) {
+            --last;
+            left = 0;
+            break;
+        }
     }
     // the keys above `last`, and the first `left` of its equals, in order
     const int run = (count + kWarps * 32 - 1) / (kWarps * 32) * 32;  // keys of a warp
     const int j0 = min(warp * run, count), j1 = min(j0 + run, count);
+    auto load_run = [&](int i0) {  // (ahead of their stores)
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int j = i0 + 32 * i + lane;
+            v[i] = j < j1 ? w[base + j] : 0.f;
+        }
+    };
+    load_run(j0);
     uint32_t above = 0, equal = 0;
+#pragma unroll 4
     for (int j = j0; j < j1; j += 32) {
         const uint32_t k = j + lane < j1 ? rank(j + lane) : 0u;
         above += __popc(__ballot_sync(kFull, j + lane < j1 && k > last));
@@ -180,21 +201,17 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv_evict_select_kernel(const E
     above = __reduce_add_sync(kFull, above);
     equal = __reduce_add_sync(kFull, equal);
     const unsigned before = (1u << lane) - 1;
-    for (int i0 = j0; i0 < j1; i0 += 4 * 32) {
-        float x[4];  // (loaded ahead of their stores)
+    for (int i0 = j0; i0 < j1; i0 += 32 * kBatch) {
+        if (i0 > j0) load_run(i0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = i0 + 32 * i + lane;
-            x[i] = j < j1 ? w[base + j] : 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kBatch; ++i) {
+            if (i0 + 32 * i >= j1) break;
             const int j = i0 + 32 * i + lane;
             const uint32_t k = j < j1 ? rank(j) : 0u;
             const bool is_above = j < j1 && k > last, is_equal = j < j1 && k == last;
             const unsigned up = __ballot_sync(kFull, is_above), eq = __ballot_sync(kFull, is_equal);
             const uint32_t a = above + __popc(up & before), e = equal + __popc(eq & before);
-            if (is_above || (is_equal && e < left)) store(p.sinks + static_cast<int>(a + min(e, left)), base + j, x[i]);
+            if (is_above || (is_equal && e < left)) store(p.sinks + static_cast<int>(a + min(e, left)), base + j, v[i]);
             above += __popc(up);
             equal += __popc(eq);
         }
@@ -203,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv_evict_select_kernel(const E
 }
 
 constexpr int kCopyThreads = 128;
-constexpr int kInFlight = 4;  // keys of a lane group with their loads in flight
+constexpr int kInFlight = 2;  // keys of a lane group with their loads in flight (4: 102 us becomes 108 where 16000 stay)
 
 template <int D>
 __global__ void __launch_bounds__(kCopyThreads) fa_kv_evict_copy_kernel(const EvictParams p) {

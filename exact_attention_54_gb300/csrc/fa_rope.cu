@@ -11,7 +11,7 @@
 // of its tokens once, in shared memory. An angle in turns is the fraction of
 // p inv_freq / 2 pi; far positions lose it in 32 bits (2^20 inv_freq is off by
 // 2^-5 rad), so inv_freq / 2 pi is held as a 64-bit fraction and its product
-// with p wraps as turns do: one integer product, off by 2^-53 of p turns at
+// with p wraps as turns do: one integer product, off by 2^-63 p turns at
 // most. The fraction's upper 32 bits, rounded to 24, go into sincospi.
 //
 // Grid: a chunk of tokens (x) of one sequence (y, z) per CTA, as in the 4-bit
@@ -60,15 +60,29 @@ __device__ __forceinline__ void rotate(Pieces &x, const float2 *turn) {
     }
 }
 
+// f / 2 pi without its whole part, in units of 2^-64: f is m 2^e, so it is m C 2^(e - 2)
+// for C = 2^66 / 2 pi. (In double precision, of which GB300 has little, the queries
+// and keys of 21,915 tokens and their gradients take 154.5 us, so 152.4.)
+__device__ __forceinline__ unsigned long long fraction_of_turn(float f) {
+    const unsigned long long C = 0xa2f9836e4e44152aull;
+    const uint32_t u = __float_as_uint(f);
+    const int exponent = (u >> 23) & 255, shift = 152 - max(exponent, 1);
+    const unsigned long long m = (u & 0x7fffff) | (exponent > 0 ? 0x800000 : 0);
+    const unsigned long long hi = __umul64hi(m, C), lo = m * C;
+    unsigned long long r;
+    if (shift >= 64) r = shift < 128 ? hi >> (shift - 64) : 0;
+    else if (shift > 0) r = hi << (64 - shift) | lo >> shift;
+    else r = shift > -64 ? lo << -shift : 0;
+    return u >> 31 ? 0 - r : r;
+}
+
 // Cosines and sines (times mscale) of `tokens` tokens, pos(i) the position of
 // token i. The whole CTA calls it; ends synchronised.
 template <class Pos>
 __device__ __forceinline__ void fill_turns(const RopeParams &p, float2 *turns, int tokens, Pos pos) {
     const int pairs = p.rot_dim / 2;
     for (int i = threadIdx.x; i < pairs; i += kThreads) {
-        double f = static_cast<double>(p.inv_freq[i]) * 0.15915494309189533577;  // 1 / 2 pi
-        f -= floor(f);
-        const unsigned long long frac = static_cast<unsigned long long>(f * 18446744073709551616.0);
+        const unsigned long long frac = fraction_of_turn(p.inv_freq[i]);
         for (int t = 0; t < tokens; ++t) {
             const long long at = static_cast<long long>(static_cast<unsigned long long>(pos(t)) * frac);
             float s, c;

@@ -572,7 +572,7 @@ FA_API fa_status_t fa_decode_paged_q4(const void *q, const void *k_codes, const 
  *   inv_freq   device fp32 [rot_dim / 2]
  *   positions  device int32 [B,S], or NULL: 0 .. S - 1. Any values: an angle is
  *              formed as a 64-bit fraction of a turn, so far positions keep
- *              theirs (off by 2^-53 |p| turns at most, besides 2^-24 of it).
+ *              theirs (off by 2^-63 |p| turns at most, besides 2^-24 of it).
  *   D          64, 128, 256, 512 or 1024; rot_dim a multiple of 16, 16 .. D
  * S = 0 is allowed and does nothing. One launch.
  * Errors: FA_ERR_NULL, FA_ERR_SHAPE (rot_dim and strides too), FA_ERR_HEADDIM,

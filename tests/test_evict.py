@@ -223,3 +223,35 @@ def test_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(ref, got)) and torch.equal(cache, ref_k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("digits", [1, 2, 3])
+def test_threshold_found_early(digits):
+    """Weights that differ in their first 11 bits, their first 22, or only behind those: the keys that stay are known after
+    so many digits; and a threshold that all keys of a digit pass, zeros and negative weights at the bottom of it."""
+    L, Hkv, D, block = 3000, 2, 64, 16
+    g = torch.Generator().manual_seed(digits)
+    order = torch.stack([torch.randperm(L, generator=g) for _ in range(Hkv)])
+    bits = {1: 1 << 21, 2: 1 << 10, 3: 1}[digits]
+    if digits == 1:  # (there are fewer than 3000 such)
+        order = order // 2
+    w = (0x38000000 - (L // 2 if digits > 1 else 0) * bits + order * bits if digits > 1 else 0x00800000 + (order % 900) * bits)
+    w = w.to(torch.int32).view(torch.float32)
+    for keep in (1, 2, 900, 1500, 2999):
+        for weights in (w, torch.where(w > w.median(), w, torch.zeros_like(w)), -w):
+            kc = torch.randn(400, Hkv, block, D, generator=g).to(torch.bfloat16)
+            vc = torch.randn(400, Hkv, block, D, generator=g).to(torch.bfloat16)
+            pages = (L + block - 1) // block
+            table = torch.arange(pages, dtype=torch.int32)[None]
+            to = torch.arange(pages, 2 * pages, dtype=torch.int32)[None]
+            full = torch.zeros(1, Hkv, pages * block)
+            full[0, :, :L] = weights
+            kd, vd = kc.cuda(), vc.cuda()
+            kept, lens, new = fa.flash_kv_evict(kd, vd, full.cuda(), table.cuda(), torch.tensor([L], dtype=torch.int32).cuda(),
+                                                to.cuda(), keep)
+            for h in range(Hkv):
+                ids = sorted(sorted(range(L), key=lambda j: (-float(weights[h, j]), j))[:keep])
+                assert kept[0, h].tolist() == ids
+                assert torch.equal(new[0, h, :keep].cpu(), weights[h, ids])
+    fa.fa_check_device_error()
