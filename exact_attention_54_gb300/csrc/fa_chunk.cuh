@@ -24,6 +24,17 @@
 // so that one long sequence or many ragged ones keep every SM busy to the end. A
 // unit that falls into several runs leaves its parts (m, l, O in fp32) in the
 // workspace, and a second launch joins them, row by row in the order of keys.
+//
+// Bound: long chunks by the tensor core under the power limit, 2048 tokens behind 30000
+// keys, 32 heads on 8 of D = 128: 630 us, 1650 TFLOP/s. 16 chunks of 1 to 512 tokens
+// behind up to 7680 keys: 294 us, 1260 TFLOP/s (tensor core 65 % active: starts of units,
+// rows without tokens, keys ahead of the chunk's queries). Few tokens by reading the
+// cache: 5 of 16 sequences of up to 8192 keys 79 us, 5.1 TB/s, of which 20 are the launch,
+// the plan, the first loads and the join (at 32000 keys 314 us, 6.7 TB/s).
+// Measured beside this: units in groups of sequences, so that neighbours share keys in
+// L2, 294 and 640 to 660; the softmax warps' place in the run kept in registers, 920
+// (spills) in place of 680; one warpgroup after the other where a unit is one tile, no
+// gain; a start that counts as 1, 2 or 4 tiles, slower.
 #pragma once
 
 #include "fa_paged.cuh"

@@ -13,14 +13,20 @@
 // other keeps the exponentials going. -lse log2 e of a step's columns comes through
 // shared memory, -inf where a column is no query.
 //
+// Only the warps that load walk the units; the others are told of a step by what
+// the -lse ring holds beside it. A kernel whose twelve warps all walked them was bound
+// by its instruction cache where units are short (one token: 19 % of fetches missed it).
+//
 // Bound: single tokens by reading the keys (16 sequences of 4100 to 8192 keys, 8 key
-// heads, D = 128: 47 us, 4.4 TB/s, of which 8 us are the launch and the way to the first
-// keys). Long chunks by the exponentials: 512 tokens of four sequences of 8704 to 16896
-// keys, 32 heads on 8, take 210 us, 1190 TFLOP/s, 53 % of the rate of ex2; without the
-// products 204, products and loads alone 169 (both operands come from shared memory).
+// heads, D = 128: 40 us, 5.2 TB/s, of which some 8 us are the launch and the way to the
+// first keys; of 32000 keys 177 us, 6.0 TB/s, with 128-key pages 6.4). Long chunks by
+// the exponentials: 512 tokens of four sequences of 8704 to 16896 keys, 32 heads on 8,
+// take 207 us, 1205 TFLOP/s, 53 % of the rate of ex2; without the products 204, products
+// and loads alone 169 (both operands come from shared memory).
 // Measured beside this: both warpgroups on every step, half of the columns each, 229;
 // a step's scores loaded while the step before is added up, 265 to 317; sums two at a
-// time 248; four warpgroups 225.
+// time 248; four warpgroups 225. For single tokens: query tiles of 32 rows and three
+// units of keys in flight 43, pages looked up a unit ahead 40 (29 -> 31 at D = 64).
 #include "fa_paged.cuh"
 
 namespace fa {
