@@ -19,10 +19,11 @@
 // pieces that pair up (half layout), or neighbouring ones.
 //
 // Measured: queries and keys of 21,915 tokens (32 and 8 heads of 128 columns) and their
-// gradients, four calls, 152 us, 5.9 TB/s read and written; the same tokens into a cache
-// 86 us, 6.2 TB/s; one token of 64 sequences 6 us. CTAs of 64 threads with two rows a
-// lane group in flight: 256 threads 176 us in place of 161, eight rows 190 (registers
-// then leave too few CTAs to cover the angles). Rows are loaded ahead of the angles.
+// gradients, four calls, 143 us, 6.3 TB/s read and written; the same tokens into a cache
+// 83 us, 6.4 TB/s; one token of 64 sequences 6 us. CTAs of 64 threads with two rows a
+// lane group in flight: 32, 96 and 128 threads 150, 147 and 145 us, one row 148, four 152
+// (registers then leave too few CTAs to cover the angles), twice the tokens 151. Rows are
+// loaded ahead of the angles.
 #include "fa_kv_q4.cuh"
 #include "fa_launch.h"
 
@@ -40,18 +41,23 @@ struct Pieces {
 
 __device__ __forceinline__ uint32_t &word(uint4 &x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; }
 
-// Turns the 8 pairs of a lane. turn: their (cos, sin), mscale in both.
+// Turns the 8 pairs of a lane. turn: their (cos, sin), mscale in both, two pairs
+// after another, then the next of the `lanes` lanes (with all of a lane's together a
+// row's lanes read the same banks: 152 us for the four calls above).
 // INTER: pairs are neighbouring columns of a (4) and b (4); else column i of a
 // pairs with column i of b.
 template <bool BF16, bool INTER>
-__device__ __forceinline__ void rotate(Pieces &x, const float2 *turn) {
+__device__ __forceinline__ void rotate(Pieces &x, const float4 *turn, int lanes) {
     if constexpr (INTER) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t &w = i < 4 ? word(x.a, i) : word(x.b, i - 4);
-            const float a = ptx::unpack_lo<BF16>(w), b = ptx::unpack_hi<BF16>(w);
-            const float2 t = turn[i];
-            w = ptx::pack2<BF16>(a * t.x - b * t.y, b * t.x + a * t.y);
+        for (int i = 0; i < 4; ++i) {
+            const float4 t = turn[i * lanes];
+            auto turn1 = [](uint32_t &w, float c, float s) {
+                const float a = ptx::unpack_lo<BF16>(w), b = ptx::unpack_hi<BF16>(w);
+                w = ptx::pack2<BF16>(a * c - b * s, b * c + a * s);
+            };
+            turn1(i < 2 ? word(x.a, 2 * i) : word(x.b, 2 * i - 4), t.x, t.y);
+            turn1(i < 2 ? word(x.a, 2 * i + 1) : word(x.b, 2 * i - 3), t.z, t.w);
         }
     } else {
 #pragma unroll
@@ -59,16 +65,15 @@ __device__ __forceinline__ void rotate(Pieces &x, const float2 *turn) {
             uint32_t &wa = word(x.a, i), &wb = word(x.b, i);
             const float a0 = ptx::unpack_lo<BF16>(wa), a1 = ptx::unpack_hi<BF16>(wa);
             const float b0 = ptx::unpack_lo<BF16>(wb), b1 = ptx::unpack_hi<BF16>(wb);
-            const float2 t0 = turn[2 * i], t1 = turn[2 * i + 1];
-            wa = ptx::pack2<BF16>(a0 * t0.x - b0 * t0.y, a1 * t1.x - b1 * t1.y);
-            wb = ptx::pack2<BF16>(b0 * t0.x + a0 * t0.y, b1 * t1.x + a1 * t1.y);
+            const float4 t = turn[i * lanes];
+            wa = ptx::pack2<BF16>(a0 * t.x - b0 * t.y, a1 * t.z - b1 * t.w);
+            wb = ptx::pack2<BF16>(b0 * t.x + a0 * t.y, b1 * t.z + a1 * t.w);
         }
     }
 }
 
 // f / 2 pi without its whole part, in units of 2^-64: f is m 2^e, so it is m C 2^(e - 2)
-// for C = 2^66 / 2 pi. (In double precision, of which GB300 has little, the queries
-// and keys of 21,915 tokens and their gradients take 154.5 us, so 152.4.)
+// for C = 2^66 / 2 pi. (Double precision, of which GB300 has little, took 2 us more.)
 __device__ __forceinline__ unsigned long long fraction_of_turn(float f) {
     const unsigned long long C = 0xa2f9836e4e44152aull;
     const uint32_t u = __float_as_uint(f);
@@ -89,11 +94,12 @@ __device__ __forceinline__ void fill_turns(const RopeParams &p, float2 *turns, i
     const int pairs = p.rot_dim / 2;
     for (int i = threadIdx.x; i < pairs; i += kThreads) {
         const unsigned long long frac = fraction_of_turn(p.inv_freq[i]);
+        const int slot = 2 * (i % 8 / 2 * (pairs / 8) + i / 8) + i % 2;  // (see rotate)
         for (int t = 0; t < tokens; ++t) {
             const long long at = static_cast<long long>(static_cast<unsigned long long>(pos(t)) * frac);
             float s, c;
             sincospif(static_cast<float>(static_cast<int>(at >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-            turns[t * pairs + i] = make_float2(c * p.mscale, (p.inverse ? -s : s) * p.mscale);
+            turns[t * pairs + slot] = make_float2(c * p.mscale, (p.inverse ? -s : s) * p.mscale);
         }
     }
     __syncthreads();
@@ -101,11 +107,10 @@ __device__ __forceinline__ void fill_turns(const RopeParams &p, float2 *turns, i
 
 // Columns of a lane's two pieces, and whether they are turned.
 struct Lane {
-    int a, b, pair;
+    int a, b;
     bool turned;
     __device__ __forceinline__ Lane(int sub, int rot_dim, bool inter) {
         turned = sub < rot_dim / 16;
-        pair = sub * 8;
         a = turned && !inter ? sub * 8 : sub * 16;
         b = turned && !inter ? rot_dim / 2 + sub * 8 : sub * 16 + 8;
     }
@@ -140,7 +145,8 @@ __device__ __forceinline__ void stream_rows(const RopeParams &p, const float2 *t
             int token;
             target(r0 + i * groups, dst, token);
             if (dst == nullptr) continue;
-            if (l.turned && token >= 0) rotate<BF16, INTER>(x[i], turns + token * pairs + l.pair);
+            if (l.turned && token >= 0)
+                rotate<BF16, INTER>(x[i], reinterpret_cast<const float4 *>(turns + token * pairs) + sub, pairs / 8);
             *reinterpret_cast<uint4 *>(dst + l.a) = x[i].a;
             *reinterpret_cast<uint4 *>(dst + l.b) = x[i].b;
         }
@@ -149,7 +155,7 @@ __device__ __forceinline__ void stream_rows(const RopeParams &p, const float2 *t
 
 template <bool BF16, bool INTER>
 __global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RopeParams p) {
-    extern __shared__ float2 turns[];
+    extern __shared__ __align__(16) float2 turns[];
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     const long long b = static_cast<long long>(blockIdx.z) * gridDim.y + blockIdx.y;
@@ -176,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RopeParams p) {
 
 template <bool BF16, bool INTER>
 __global__ void __launch_bounds__(kThreads) fa_rope_kv_write_kernel(const RopeParams p) {
-    extern __shared__ float2 turns[];
+    extern __shared__ __align__(16) float2 turns[];
     __shared__ long long rows[kMaxTokens];  // first key head's cache row of each token, or -1
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
