@@ -183,13 +183,28 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv_evict_select_kernel(const E
             v[i] = j < j1 ? w[base + j] : 0.f;
         }
     };
+    uint32_t up[kBatch], eq[kBatch];  // lanes whose key is above, equal
+    auto compare = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int j = i0 + 32 * i + lane;
+            up[i] = eq[i] = 0;
+            if (j - lane >= j1) continue;
+            const uint32_t k = j < j1 ? rank(j) : 0u;
+            up[i] = __ballot_sync(kFull, j < j1 && k > last);
+            eq[i] = __ballot_sync(kFull, j < j1 && k == last);
+        }
+    };
     load_run(j0);
     uint32_t above = 0, equal = 0;
-#pragma unroll 4
-    for (int j = j0; j < j1; j += 32) {
-        const uint32_t k = j + lane < j1 ? rank(j + lane) : 0u;
-        above += __popc(__ballot_sync(kFull, j + lane < j1 && k > last));
-        equal += __popc(__ballot_sync(kFull, j + lane < j1 && k == last));
+    constexpr int kStep = 32 * kBatch;
+    for (int i0 = j0 + max(j1 - j0 - 1, 0) / kStep * kStep; i0 >= j0; i0 -= kStep) {  // (the first ones last: they are needed next)
+        compare(i0);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            above += __popc(up[i]);
+            equal += __popc(eq[i]);
+        }
     }
     if (lane == 0) counts[warp] = make_uint2(above, equal);
     sync();
@@ -204,23 +219,24 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv_evict_select_kernel(const E
     }
     above = __reduce_add_sync(kFull, above);
     equal = __reduce_add_sync(kFull, equal);
+    if (ctas > 1) cluster.barrier_arrive();  // (this CTA has read what it needs of the others)
     const unsigned before = (1u << lane) - 1;
-    for (int i0 = j0; i0 < j1; i0 += 32 * kBatch) {
-        if (i0 > j0) load_run(i0);
+    for (int i0 = j0; i0 < j1; i0 += kStep) {
+        if (i0 > j0) {
+            load_run(i0);
+            compare(i0);
+        }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             if (i0 + 32 * i >= j1) break;
-            const int j = i0 + 32 * i + lane;
-            const uint32_t k = j < j1 ? rank(j) : 0u;
-            const bool is_above = j < j1 && k > last, is_equal = j < j1 && k == last;
-            const unsigned up = __ballot_sync(kFull, is_above), eq = __ballot_sync(kFull, is_equal);
-            const uint32_t a = above + __popc(up & before), e = equal + __popc(eq & before);
-            if (is_above || (is_equal && e < left)) store(p.sinks + static_cast<int>(a + min(e, left)), base + j, v[i]);
-            above += __popc(up);
-            equal += __popc(eq);
+            const uint32_t a = above + __popc(up[i] & before), e = equal + __popc(eq[i] & before);
+            if ((up[i] >> lane & 1) || ((eq[i] >> lane & 1) && e < left))
+                store(p.sinks + static_cast<int>(a + min(e, left)), base + i0 + 32 * i + lane, v[i]);
+            above += __popc(up[i]);
+            equal += __popc(eq[i]);
         }
     }
-    if (ctas > 1) cluster.sync();  // the others have read what they need of this CTA
+    if (ctas > 1) cluster.barrier_wait();  // the others have read what they need of this one
 }
 
 constexpr int kCopyThreads = 128;
