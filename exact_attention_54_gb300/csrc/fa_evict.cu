@@ -14,7 +14,7 @@
 //
 // Bound: the copy by HBM; the selection by latency, of loads, of the cluster's barriers
 // and of its counts (some 1,800 clocks each a digit). Four caches of 16384 to 32768 keys,
-// 8 key heads, D = 128, down to 4096: 39 us, about 14 of them the selection; two caches
+// 8 key heads, D = 128, down to 4096: 38 us, about 13 of them the selection; two caches
 // of at most 777 keys 9 us.
 #include <cooperative_groups.h>
 
@@ -53,7 +53,7 @@ __device__ __forceinline__ uint32_t scan(uint32_t v) {
 // for itself. The search ends where all keys of a digit stay, mostly after two. The
 // keys that stay are written warp by warp, each over a run of keys. (Before: prefix
 // sums of the whole CTA, 8 barriers a digit and 3 every 4096 keys, the others' counts
-// one after another, always three digits: 22 us for the four caches above, 14 now.)
+// one after another, always three digits: 22 us for the four caches above, 13 now.)
 __global__ void __launch_bounds__(kThreads, 1) fa_kv_evict_select_kernel(const EvictParams p) {
     constexpr int kWarps = kThreads / 32, kOfWarp = kBins / kWarps;  // bins
     static_assert(kOfWarp == 64, "two bins a lane");
