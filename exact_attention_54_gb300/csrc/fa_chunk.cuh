@@ -744,7 +744,9 @@ constexpr int kJoinRows = 32;  // of a unit, per CTA
 
 // Joins the parts of units that fell into several runs: CTA x for the unit that
 // started in run x, if any. A lane has a row, a warp D / 8 of its columns (reads are
-// whole lines); the rows go out through shared memory.
+// whole lines); the rows go out through shared memory. Where there are fewer rows
+// than lanes, lanes share out the parts of a row: one token of 8 heads on one key head,
+// 131000 keys in some 150 parts, 45 us in place of 93.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) fa_chunk_join_kernel(const ChunkParams p) {
     constexpr int kWarps = kJoinThreads / 32, kQuads = D / 4 / kWarps;  // of four columns, a warp
@@ -761,33 +763,46 @@ __global__ void __launch_bounds__(kJoinThreads) fa_chunk_join_kernel(const Chunk
         head = r % kBlockM - token * p.group;
         return r < p.part_rows && token < p.tile_tokens && tok < rec.y ? tok : -1;
     };
-    const int row = blockIdx.y * kJoinRows + lane;
+    const int rows = p.part_rows >= 32 ? 32 : 1 << (32 - __clz(p.part_rows - 1)), slices = 32 / rows, slice = lane / rows;
+    const int row = blockIdx.y * kJoinRows + lane % rows;
     int head;
-    const int tok = where(row, head);
-    if (tok >= 0) {
-        // part 0 is in the slot it was given, later ones in the first of their CTAs
-        auto at = [&](int x) { return static_cast<size_t>(2 * (blockIdx.x + x) + (x == 0 ? slot : 0)); };
-        float m = -CUDART_INF_F, l = 0.f;
+    const int tok = where(row, head), end = tok >= 0 ? parts : 0;
+    // part 0 is in the slot it was given, later ones in the first of their CTAs
+    auto at = [&](int x) { return static_cast<size_t>(2 * (blockIdx.x + x) + (x == 0 ? slot : 0)); };
+    float m = -CUDART_INF_F, l = 0.f;
 #pragma unroll 4
-        for (int x = 0; x < parts; ++x) m = fmaxf(m, __ldcg(p.ml_part + at(x) * p.part_rows + row).x);
-        float4 o[kQuads];
+    for (int x = slice; x < end; x += slices) m = fmaxf(m, __ldcg(p.ml_part + at(x) * p.part_rows + row).x);
+    for (int off = rows; off < 32; off *= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+    float4 o[kQuads];
 #pragma unroll
-        for (int i = 0; i < kQuads; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < kQuads; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-        for (int x = 0; x < parts; ++x) {
-            const float2 ml = __ldcg(p.ml_part + at(x) * p.part_rows + row);
-            const float4 *v = reinterpret_cast<const float4 *>(p.o_part) + (at(x) * (D / 4) + warp * kQuads) * p.part_rows + row;
-            const float f = ml.x == -CUDART_INF_F ? 0.f : ptx::ex2(ml.x - m);
-            l = fmaf(ml.y, f, l);
+    for (int x = slice; x < end; x += slices) {
+        const float2 ml = __ldcg(p.ml_part + at(x) * p.part_rows + row);
+        const float4 *v = reinterpret_cast<const float4 *>(p.o_part) + (at(x) * (D / 4) + warp * kQuads) * p.part_rows + row;
+        const float f = ml.x == -CUDART_INF_F ? 0.f : ptx::ex2(ml.x - m);
+        l = fmaf(ml.y, f, l);
 #pragma unroll
-            for (int i = 0; i < kQuads; ++i) {
-                const float4 y = __ldcg(v + i * p.part_rows);
-                o[i].x = fmaf(y.x, f, o[i].x);
-                o[i].y = fmaf(y.y, f, o[i].y);
-                o[i].z = fmaf(y.z, f, o[i].z);
-                o[i].w = fmaf(y.w, f, o[i].w);
-            }
+        for (int i = 0; i < kQuads; ++i) {
+            const float4 y = __ldcg(v + i * p.part_rows);
+            o[i].x = fmaf(y.x, f, o[i].x);
+            o[i].y = fmaf(y.y, f, o[i].y);
+            o[i].z = fmaf(y.z, f, o[i].z);
+            o[i].w = fmaf(y.w, f, o[i].w);
         }
+    }
+    for (int off = rows; off < 32; off *= 2) {
+        auto add = [&](float &a) { a += __shfl_xor_sync(kFull, a, off); };
+        add(l);
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) {
+            add(o[i].x);
+            add(o[i].y);
+            add(o[i].z);
+            add(o[i].w);
+        }
+    }
+    if (tok >= 0 && slice == 0) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
         for (int i = 0; i < kQuads; ++i)

@@ -191,6 +191,16 @@ def test_one_long_sequence_falls_into_many_parts(n, L, Hkv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n,group,D", [(1, 1, 64), (1, 3, 128), (2, 1, 128), (1, 7, 64), (3, 5, 128), (1, 16, 64), (11, 3, 128)])
+def test_parts_of_few_rows(n, group, D):
+    """Rows that do not fill a warp's lanes, in up to as many parts as there are CTAs."""
+    chunks, lens = [n, n], [17001, 700]
+    q, kc, vc, table, sl, cu = make(chunks, lens, group, 1, D, 32, BF, n + group)
+    o, lse = run(q, kc, vc, table, sl, cu, n)
+    check(o, lse, reference(q, kc, vc, table, lens, cu, 0, 0, D ** -0.5))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("B", [300, 5000])
 def test_many_sequences(B):
     g = torch.Generator().manual_seed(B)
