@@ -13,7 +13,7 @@ namespace paged {
 constexpr int kPlanEntries = 4096;  // the plan's table: sums over a sequence, or over several if there are more
 constexpr int kSerialUnits = 16;    // units of a sequence that a thread adds up, rather than a warp,
 constexpr int kPlanLong = 4096;     // where a sequence has more and there are no more than this many such
-constexpr int kPlanBytes = 8 * (kPlanEntries + 1) + 4 * (kPlanLong + 1);
+constexpr int kPlanSeqs = 512;      // sequences that are not loaded again for the CTA's place
 constexpr unsigned kFull = 0xffffffffu;
 
 // Sequence b's chunk: its rows in the packed queries, its keys.
@@ -28,6 +28,8 @@ __device__ __forceinline__ Seq load_seq(const PagedParams &p, int b) {
     s.L = min(max(p.seq_lens[b], 0), p.max_blocks << p.log2_bs);
     return s;
 }
+
+constexpr int kPlanBytes = 8 * (kPlanEntries + 1) + 4 * (kPlanLong + 1) + static_cast<int>(sizeof(Seq)) * kPlanSeqs;
 
 // A CTA's run of the laid-out units, in shared memory.
 struct Run {
@@ -76,6 +78,7 @@ template <class Units>
 __device__ void plan(const PagedParams &p, const Units units, Run *run, void *scratch) {
     unsigned long long *prefix = static_cast<unsigned long long *>(scratch);
     int *many = reinterpret_cast<int *>(prefix + kPlanEntries + 1), *n_many = many + kPlanLong;
+    Seq *seqs = reinterpret_cast<Seq *>(n_many + 1);
     const int each = (p.B + kPlanEntries - 1) / kPlanEntries, entries = (p.B + each - 1) / each;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     // (a thread's first loads are ahead of the scratch's clearing)
@@ -100,6 +103,7 @@ __device__ void plan(const PagedParams &p, const Units units, Run *run, void *sc
             bad = true;
             continue;
         }
+        if (b < kPlanSeqs) seqs[b] = s;
         const int n = units.count(s);
         const int2 flat = units.flat(s, n);
         const int at = n - (flat.y - flat.x) > kSerialUnits ? atomicAdd(n_many, 1) : kPlanLong;
@@ -107,7 +111,8 @@ __device__ void plan(const PagedParams &p, const Units units, Run *run, void *sc
             many[at] = b;
         } else if (n > 0) {
             const unsigned long long c = seq_cost(units, s, n, flat, 0, 1);
-            if (c > 0) atomicAdd(&prefix[b / each + 1], c);
+            if (each == 1) prefix[b + 1] = c;
+            else if (c > 0) atomicAdd(&prefix[b / each + 1], c);
         }
     }
     bad = __syncthreads_or(bad) != 0;
@@ -158,7 +163,7 @@ __device__ void plan(const PagedParams &p, const Units units, Run *run, void *sc
         int2 flat{};
         unsigned long long c = 0;
         for (r.b = lo * each;; ++r.b) {
-            s = load_seq(p, r.b);
+            s = r.b < kPlanSeqs ? seqs[r.b] : load_seq(p, r.b);
             n = units.count(s);
             flat = units.flat(s, n);
             c = each == 1 ? prefix[r.b + 1] - prefix[r.b] : warp_sum(seq_cost(units, s, n, flat, lane, 32));
