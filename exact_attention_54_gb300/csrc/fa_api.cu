@@ -1026,7 +1026,7 @@ fa_status_t fa_rope(const void *x, void *y, const float *inv_freq, const int32_t
     if (B < 1 || S < 0 || H < 1 || S > kMaxLen || H > (1 << 24) || rot_dim == 0 ||
         !rot_ok(rot_dim, D) || !stride_ok(x_batch) || !stride_ok(x_token) || !stride_ok(x_head) ||
         !stride_ok(y_batch) || !stride_ok(y_token) || !stride_ok(y_head) ||
-        (B > 1 && y_batch == 0) || (S > 1 && y_token == 0) || (H > 1 && y_head == 0))  // rows of y on one another
+        (S > 0 && ((B > 1 && y_batch == 0) || (S > 1 && y_token == 0) || (H > 1 && y_head == 0))))  // rows of y on one another
         return FA_ERR_SHAPE;
     if (!std::isfinite(mscale)) return FA_ERR_SCALE;
     if (!aligned16(x) || !aligned16(y) || !aligned4(inv_freq) || !aligned4(positions)) return FA_ERR_ALIGN;

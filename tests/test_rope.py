@@ -91,6 +91,16 @@ def test_validation(lib):
     assert call(S=0, x=None, y=None, p=None) == OK
 
 
+def test_no_tokens_of_any_strides(lib):
+    """S = 0 does nothing, also where the strides are those of an empty contiguous [B,H,0,D] (0 between heads)."""
+    for ys in ((0, 64, 0), (0, 64, 64), (0, 0, 0), (256, 64, 64)):
+        assert lib.fa_rope(None, None, A, None, 2, 0, 4, 64, 64, *ys, *ys, 0, 0, 1.0, 1, None) == OK, ys
+    for B, H in ((1, 4), (2, 1), (2, 4)):
+        x = torch.empty(B, H, 0, 64, dtype=torch.bfloat16)
+        st = fa._rows("x", x, x.dtype)
+        assert lib.fa_rope(A, A, A, None, B, 0, H, 64, 64, *st, *st, 0, 0, 1.0, 1, None) == OK, (B, H)
+
+
 def test_write_validation(lib):
     def call(q=A, k=A, v=A, qo=A, kc=A, vc=A, f=A, p=A, bt=A, cu=A, st=A, n=2, total=10, mx=8, H=4, Hkv=2, D=128, rot=64,
              qs=512, ks=256, vs=256, nb=8, bs=16, mb=4, inter=0, m=1.0, dtype=1):
@@ -375,6 +385,17 @@ def test_streams_and_graphs():
     assert torch.equal(out, fa.flash_rope(x.flip(0).contiguous(), f))
     empty = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
     assert fa.flash_rope(empty, f).shape == empty.shape
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,H", [(1, 4), (2, 1), (3, 2)])
+def test_dense_of_no_tokens(B, H):
+    x = torch.empty(B, H, 0, 64, dtype=torch.bfloat16, device="cuda")
+    f, _ = fa.rope_frequencies(64)
+    pos = torch.empty(B, 0, dtype=torch.int32, device="cuda")
+    for y in (fa.flash_rope(x, f), fa.flash_rope(x, f, pos), fa.flash_rope_bwd(x, f)):
+        assert y.shape == x.shape
+    fa.fa_check_device_error()
 
 
 @pytest.mark.gpu
