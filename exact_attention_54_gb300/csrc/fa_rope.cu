@@ -24,6 +24,8 @@
 // lane group in flight: 32, 96 and 128 threads 150, 147 and 145 us, one row 148, four 152
 // (registers then leave too few CTAs to cover the angles), twice the tokens 151. Rows are
 // loaded ahead of the angles.
+#include <math_constants.h>
+
 #include "fa_kv_q4.cuh"
 #include "fa_launch.h"
 
@@ -93,13 +95,15 @@ template <class Pos>
 __device__ __forceinline__ void fill_turns(const RopeParams &p, float2 *turns, int tokens, Pos pos) {
     const int pairs = p.rot_dim / 2;
     for (int i = threadIdx.x; i < pairs; i += kThreads) {
-        const unsigned long long frac = fraction_of_turn(p.inv_freq[i]);
+        const float freq = p.inv_freq[i];
+        const unsigned long long frac = fraction_of_turn(freq);
+        const float m = isfinite(freq) ? p.mscale : CUDART_NAN_F;  // (the fraction of such a frequency is 0)
         const int slot = 2 * (i % 8 / 2 * (pairs / 8) + i / 8) + i % 2;  // (see rotate)
         for (int t = 0; t < tokens; ++t) {
             const long long at = static_cast<long long>(static_cast<unsigned long long>(pos(t)) * frac);
             float s, c;
             sincospif(static_cast<float>(static_cast<int>(at >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-            turns[t * pairs + slot] = make_float2(c * p.mscale, (p.inverse ? -s : s) * p.mscale);
+            turns[t * pairs + slot] = make_float2(c * m, (p.inverse ? -s : s) * m);
         }
     }
     __syncthreads();

@@ -569,7 +569,8 @@ FA_API fa_status_t fa_decode_paged_q4(const void *q, const void *k_codes, const 
  *              of a wider tensor. Strides are >= 0 and multiples of 8. y may be
  *              x itself (same strides); otherwise they must not overlap, nor
  *              may y's rows each other.
- *   inv_freq   device fp32 [rot_dim / 2]
+ *   inv_freq   device fp32 [rot_dim / 2]; an infinite or NaN one makes its pair
+ *              of columns NaN, at position 0 too
  *   positions  device int32 [B,S], or NULL: 0 .. S - 1. Any values: an angle is
  *              formed as a 64-bit fraction of a turn, so far positions keep
  *              theirs (off by 2^-63 |p| turns at most, besides 2^-24 of it).

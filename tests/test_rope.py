@@ -274,6 +274,32 @@ def test_rope_not_finite_values_stay_in_their_pair():
     assert int((~torch.isfinite(y)).sum()) == 3
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_rope_frequencies_that_are_not_finite(bad, inter):
+    """An angle of p * inf or p * NaN has no cosine: its pair is NaN, at every position; the others are as without it."""
+    g = torch.Generator().manual_seed(3)
+    x = inputs.randn((7, 2, 64), torch.bfloat16, g).cuda()
+    f, _ = fa.rope_frequencies(48)
+    pos = torch.tensor([0, 1, -1, 5, 1 << 20, (1 << 31) - 1, -(1 << 31)], dtype=torch.int32, device="cuda")
+    h = f.clone()
+    h[5], h[23] = bad, bad
+    pair = torch.zeros(64, dtype=torch.bool)
+    for i in (5, 23):
+        pair[[2 * i, 2 * i + 1] if inter else [i, i + 24]] = True
+    c = [torch.zeros(1, 2, 16, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    write = lambda f: fa.flash_rope_kv_write(x, x, x, *c, torch.zeros(1, 1, dtype=torch.int32, device="cuda"),  # noqa: E731
+                                             torch.tensor([0, 7], dtype=torch.int32, device="cuda"), 7, f, positions=pos,
+                                             interleaved=inter)
+    for call in (lambda f: fa.flash_rope(x, f, pos, inter), lambda f: fa.flash_rope_bwd(x, f, pos, inter), write):
+        y, z = call(f).cpu(), call(h).cpu()
+        assert torch.isnan(z[..., pair]).all() and torch.equal(z[..., ~pair], y[..., ~pair])
+    k = c[0][0, :, :7].cpu()
+    assert torch.isnan(k[..., pair]).all() and torch.equal(c[1][0, :, :7], x.transpose(0, 1))
+    fa.fa_check_device_error()
+
+
 def cache_rows(cache, table, b, at, block):
     """Rows [n, Hkv, D] of positions ``at`` of sequence b."""
     at = torch.as_tensor(at)
