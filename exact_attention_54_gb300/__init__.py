@@ -908,7 +908,10 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
         keep = ((original_len * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
         f = f * keep + f / factor * (1 - keep)
         mscale = 0.1 * math.log(factor) + 1.0
-    return f.float().to(device), mscale
+    f = f.float()
+    if not (math.isfinite(mscale) and torch.isfinite(f).all()):
+        raise ValueError(f"frequencies must be finite: base {base}, factor {factor}, low {low}, high {high}")
+    return f.to(device), mscale
 
 
 def _rows(name, t, dtype):

@@ -183,6 +183,15 @@ def test_frequencies():
             fa.rope_frequencies(**{"rot_dim": 64, "device": "cpu", **kw})
 
 
+def test_frequencies_that_are_not_finite_are_refused():
+    for kw in ({"base": 1e-300}, {"scaling": "linear", "factor": 1e-45}, {"scaling": "parts", "factor": math.inf},
+               {"scaling": "parts", "low": -math.inf}):
+        with pytest.raises(ValueError, match="finite"):
+            fa.rope_frequencies(64, device="cpu", **kw)
+    f, m = fa.rope_frequencies(64, base=math.inf, device="cpu")  # only the first pair turns
+    assert f[0] == 1 and (f[1:] == 0).all() and m == 1.0
+
+
 def test_angles_of_whole_numbers():
     """The oracle's angles against 64-bit floating point, where that is good enough."""
     f, _ = fa.rope_frequencies(32, device="cpu")
