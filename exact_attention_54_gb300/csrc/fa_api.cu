@@ -1252,6 +1252,16 @@ fa_status_t fa_kv_weights(const void *q, const float *lse, const void *k_cache, 
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+// Stretches of device memory.
+struct Stretch {
+    const void *at;
+    size_t bytes;
+    bool meets(const Stretch &o) const {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(at), b = reinterpret_cast<uintptr_t>(o.at);
+        return a < b + o.bytes && b < a + bytes;
+    }
+};
+
 fa_status_t fa_kv_evict(void *k_cache, void *v_cache, const float *weights, const int32_t *block_table,
                         const int32_t *seq_lens, const int32_t *new_table, int32_t *kept, int32_t *new_lens,
                         float *new_weights, int B, int Hkv, int D, int num_blocks, int block_size,
@@ -1272,6 +1282,21 @@ fa_status_t fa_kv_evict(void *k_cache, void *v_cache, const float *weights, cons
         !aligned4(seq_lens) || !aligned4(new_table) || !aligned4(kept) || !aligned4(new_lens) ||
         !aligned4(new_weights))
         return FA_ERR_ALIGN;
+    // CTAs read the inputs while others write the outputs
+    const size_t heads = static_cast<size_t>(B) * Hkv, old_keys = static_cast<size_t>(max_blocks_per_seq) << log2_bs;
+    const Stretch out[3] = {{kept, 4 * heads * keep},
+                            {new_lens, 4 * static_cast<size_t>(B)},
+                            {new_weights, 4 * heads * new_max_blocks_per_seq << log2_bs}};
+    const Stretch in[4] = {{weights, 4 * heads * old_keys},
+                           {seq_lens, 4 * static_cast<size_t>(B)},
+                           {block_table, 4 * static_cast<size_t>(B) * max_blocks_per_seq},
+                           {new_table, 4 * static_cast<size_t>(B) * new_max_blocks_per_seq}};
+    for (int i = 0; i < 3; ++i) {
+        for (const Stretch &x : in)
+            if (out[i].meets(x)) return FA_ERR_SHAPE;
+        if (out[i].meets(out[(i + 1) % 3])) return FA_ERR_SHAPE;
+    }
+    if (new_table == block_table) return FA_ERR_SHAPE;  // pages that are read and written
     fa::EvictParams p{};
     p.k_cache = static_cast<uint16_t *>(k_cache);
     p.v_cache = static_cast<uint16_t *>(v_cache);

@@ -723,9 +723,12 @@ FA_API fa_status_t fa_kv_weights(const void *q, const float *lse, const void *k_
  *                names twice. Their rows behind the kept keys are not written.
  *   kept         int32 [B,Hkv,keep] output: what each new key was before
  *                (-1 behind the last one)
- *   new_lens     int32 [B] output: min(L, keep); not seq_lens itself
+ *   new_lens     int32 [B] output: min(L, keep)
  *   new_weights  [B,Hkv,new_max_blocks_per_seq * block_size] fp32 output: the
- *                kept keys' weights, then zeros; not weights itself
+ *                kept keys' weights, then zeros
+ *   Outputs must not overlap the inputs (new_lens is not seq_lens itself,
+ *   new_weights not weights) or one another, and new_table is not block_table:
+ *   such calls are refused with FA_ERR_SHAPE.
  *   block_size a power of two, 1..1024; keep >= 1, sinks, recent >= 0,
  *   sinks + recent <= keep
  * A key whose old or new page is outside [0, num_blocks), or that has no place

@@ -8,7 +8,7 @@ import exact_attention_54_gb300 as fa
 from exact_attention_54_gb300 import build as fabuild
 from exact_attention_54_gb300 import inputs
 
-OK, NULL, SHAPE, HEADDIM, DTYPE, ALIGN = 0, -1, -2, -3, -4, -5
+OK, NULL, SHAPE, HEADDIM, DTYPE, ALIGN, CUDA = 0, -1, -2, -3, -4, -5, -8
 DEV_INDEX = -11
 A, MIS = 0x10000, 0x10008
 
@@ -50,6 +50,32 @@ def test_validation(lib):
         assert call(**{kw: MIS}) == ALIGN, kw
     for kw in ("w", "bt", "sl", "nt", "kept", "nl", "nw"):
         assert call(**{kw: A + 2}) == ALIGN, kw
+
+
+def test_outputs_on_inputs_are_refused(lib):
+    """Each of these would be written while other CTAs read it, or written twice. None gets as far as a launch: the
+    sizes are good ones, so without a GPU a call with arrays apart ends at its launch."""
+    B, Hkv, block, mb, nmb, keep = 2, 2, 16, 4, 2, 20
+    size = {"w": B * Hkv * mb * block * 4, "bt": B * mb * 4, "sl": B * 4, "nt": B * nmb * 4, "kept": B * Hkv * keep * 4,
+            "nl": B * 4, "nw": B * Hkv * nmb * block * 4}
+    apart = {n: 0x100000 * (i + 1) for i, n in enumerate(size)}
+
+    def call(**kw):
+        a = {**apart, **kw}
+        return lib.fa_kv_evict(A, A, a["w"], a["bt"], a["sl"], a["nt"], a["kept"], a["nl"], a["nw"], B, Hkv, 64, 8, block,
+                               mb, nmb, keep, 4, 8, 1, None)
+
+    for out in ("kept", "nl", "nw"):
+        for other in size:
+            if other != out:
+                for at in (0, size[other] - 4, 4 - size[out]):  # the same, its last element, all but its first
+                    assert call(**{out: apart[other] + at}) == SHAPE, (out, other, at)
+    assert call(nt=apart["bt"]) == SHAPE
+    if not torch.cuda.is_available():
+        assert call() == CUDA
+        for out in ("kept", "nl", "nw"):
+            for at in (size["w"], -size[out]):  # side by side
+                assert call(**{out: apart["w"] + at}) == CUDA, (out, at)
 
 
 def test_binding_refuses():
@@ -203,6 +229,26 @@ def test_shared_pages_bad_pages_and_long_lengths():
     with pytest.raises(fa.FAError):
         fa.fa_check_device_error()
     assert nw.shape[2] == 32 and (kept >= 0).all()
+
+
+@pytest.mark.gpu
+def test_neighbouring_arrays_are_accepted():
+    """Inputs and outputs side by side in one allocation, and tables that are halves of one."""
+    lens, keep = [300, 77], 64
+    kc, vc, w, old, new = setup(lens, 2, 64, 16, keep, torch.bfloat16, 13, new_width=4)
+    ref = fa.flash_kv_evict(kc.cuda(), vc.cuda(), w.cuda(), old.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                            new.cuda(), keep, 2, 9)
+    ints = torch.empty(old.numel() + new.numel() + 4 + 4 * keep, dtype=torch.int32, device="cuda")
+    parts = ints.split([old.numel(), new.numel(), 2, 2, 4 * keep])
+    table, to, lens_in, lens_out, kept = (p.view(s) for p, s in zip(parts, (old.shape, new.shape, (2,), (2,), (2, 2, keep))))
+    table.copy_(old), to.copy_(new), lens_in.copy_(torch.tensor(lens))
+    floats = torch.empty(w.numel() + ref[2].numel(), device="cuda")
+    wi, wo = floats[:w.numel()].view(w.shape), floats[w.numel():].view(ref[2].shape)
+    wi.copy_(w)
+    fa.fa_kv_evict(kc.cuda(), vc.cuda(), wi, table, lens_in, to, kept, lens_out, wo, 2, 9)
+    fa.fa_check_device_error()
+    assert torch.equal(kept, ref[0]) and torch.equal(lens_out, ref[1]) and torch.equal(wo, ref[2])
+    assert lens_in.tolist() == lens and torch.equal(wi.cpu(), w)
 
 
 @pytest.mark.gpu
