@@ -1164,6 +1164,8 @@ def flash_kv_weights(q, lse, k_cache, block_table, cu_seqlens_q, seq_lens, max_s
                                     scale, weights)
     add = weights is not None
     if not add:
+        if k_cache.dim() != 4 or block_table.dim() != 2:
+            raise ValueError("pages must be [num_blocks,Hkv,block_size,D] and block_table [num_seqs,max_blocks]")
         weights = torch.empty((block_table.shape[0], k_cache.shape[1], block_table.shape[-1] * k_cache.shape[2]),
                               dtype=torch.float32, device=q.device)
     fa_kv_weights(q, lse, k_cache, block_table, cu_seqlens_q, seq_lens, weights, max_seqlen_q, window, sinks, scale, add)
@@ -1179,6 +1181,8 @@ def flash_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, 
             return flash_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, keep, sinks, recent)
     if int(keep) < 1:
         raise ValueError(f"keep must be at least 1, got {keep}")
+    if k_cache.dim() != 4 or block_table.dim() != 2 or new_table.dim() != 2:
+        raise ValueError("caches must be [num_blocks,Hkv,block_size,D] and tables [B,max_blocks]")
     B, Hkv, dev = block_table.shape[0], k_cache.shape[1], k_cache.device
     kept = torch.empty((B, Hkv, int(keep)), dtype=torch.int32, device=dev)
     new_lens = torch.empty((B,), dtype=torch.int32, device=dev)

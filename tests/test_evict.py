@@ -102,6 +102,14 @@ def test_binding_refuses():
             call(keep=keep)
 
 
+def test_binding_refuses_other_dimensions():
+    c = torch.zeros(8, 2, 16, 64, dtype=torch.bfloat16)
+    bt, sl = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    for kc, old, new in ((c[0, 0], bt, bt), (c, bt[0], bt), (c, bt, bt[0])):
+        with pytest.raises(ValueError, match="tables"):
+            fa.flash_kv_evict(kc, kc, torch.zeros(1, 2, 64), old, sl, new, 20)
+
+
 def test_definition():
     w = [3.0, 1.0, 5.0, 5.0, math.nan, 5.0, 0.0, 2.0]
     assert chosen(w, 8, 1, 1) == list(range(8))

@@ -94,6 +94,14 @@ def test_binding_refuses():
         call(c=c.half())
 
 
+def test_binding_refuses_other_dimensions():
+    q, c, cu = torch.zeros(5, 4, 64, dtype=BF), torch.zeros(8, 2, 16, 64, dtype=BF), torch.tensor([0, 5], dtype=torch.int32)
+    bt = torch.zeros(1, 4, dtype=torch.int32)
+    for kc, table in ((c[0, 0], bt), (c, bt[0]), (c, bt[0, 0])):
+        with pytest.raises(ValueError, match="block_table"):
+            fa.flash_kv_weights(q, torch.zeros(4, 5), kc, table, cu, torch.tensor([5], dtype=torch.int32), 5)
+
+
 # -------------------------------------------------------------- on the GPU --
 
 @pytest.mark.gpu
