@@ -1341,6 +1341,7 @@ fa_status_t fa_check_device_error(void *stream) {
     if (cudaMemcpy(err, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return FA_ERR_CUDA;
     if (host == fa::kDeviceErrBadIndex) return FA_ERR_DEVICE_INDEX;
     if (host == fa::kDeviceErrSeqLens) return FA_ERR_DEVICE_SEQLENS;
+    if (host == fa::kDeviceErrLaunch) return FA_ERR_CUDA;
     return FA_ERR_DEVICE_TIMEOUT;
 }
 

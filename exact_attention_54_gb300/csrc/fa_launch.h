@@ -45,10 +45,12 @@ inline cudaError_t launch_early(void (*kern)(Params...), dim3 grid, unsigned thr
 // Values written to the device error word: a kernel abandoned a wait, met an
 // out-of-range device-side index (a page number in a block table), or found
 // packed-sequence offsets that do not describe sequences inside the tensors
-// (or a query sequence longer than the launch was sized for).
+// (or a query sequence longer than the launch was sized for), or was not given
+// the shared memory that it declares.
 constexpr int kDeviceErrTimeout = 1;
 constexpr int kDeviceErrBadIndex = 2;
 constexpr int kDeviceErrSeqLens = 3;
+constexpr int kDeviceErrLaunch = 4;
 
 // Default bound on any single wait on an on-chip barrier.
 constexpr unsigned long long kWaitTimeoutNs = 1000000000ull;  // 1 s

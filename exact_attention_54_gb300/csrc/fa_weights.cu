@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     if ((sbase & 1023) != 0) {
-        if (threadIdx.x == 0) atomicExch(p.err, kDeviceErrTimeout);
+        if (threadIdx.x == 0) atomicExch(p.err, kDeviceErrLaunch);
         return;
     }
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffMisc);

@@ -750,7 +750,9 @@ FA_API fa_status_t fa_kv_evict(void *k_cache, void *v_cache, const float *weight
  * Returns FA_OK, FA_ERR_DEVICE_TIMEOUT, FA_ERR_DEVICE_INDEX (an out-of-range
  * block-table entry was skipped), FA_ERR_DEVICE_SEQLENS (a packed-sequence
  * launch found inconsistent cu_seqlens: see fa_fwd_varlen, fa_bwd_varlen), or FA_ERR_CUDA
- * when the runtime itself reports an error.
+ * when the runtime itself reports an error, or a kernel was not given the
+ * shared memory that it declares (a base of 1024 bytes' alignment: fa_kv_weights
+ * then computes nothing).
  */
 FA_API fa_status_t fa_check_device_error(void *stream);
 
