@@ -1210,7 +1210,6 @@ fa_status_t fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache
         return FA_ERR_CUDA;
     p.o = o;
     p.lse = lse;
-    p.min_run = 1;
     p.o_part = workspace;
     p.ml_part = reinterpret_cast<float2 *>(workspace + c.o_floats);
     p.part_rows = c.part_rows;
@@ -1247,7 +1246,6 @@ fa_status_t fa_kv_weights(const void *q, const float *lse, const void *k_cache, 
     p.lse_token = lse_token;
     p.weights = weights;
     p.add = add != 0;
-    p.min_run = 1;
     const cudaError_t e = fa::launch_kv_weights(D, bf16, maps, p, num_sms(), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

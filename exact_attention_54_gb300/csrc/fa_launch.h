@@ -310,7 +310,6 @@ struct PagedParams {
     int tile_tokens;            // tokens of a query tile: 128 / group
     int log2_bs, num_blocks, max_blocks;
     int window, sinks;          // window 0: every key up to the query's own
-    int min_run;                // least work of a CTA, in the plan's cost
     float scale_log2;
     int *err;                   // device error word
     unsigned long long timeout_ns;

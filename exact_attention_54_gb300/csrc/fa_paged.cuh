@@ -146,7 +146,7 @@ __device__ void plan(const PagedParams &p, const Units units, Run *run, void *sc
     for (int e = e0; e < min(e0 + mine, entries); ++e) prefix[e + 1] = before += prefix[e + 1];
     if (lane == 0) prefix[0] = 0;
     __syncwarp();
-    const long long per = max(static_cast<long long>(divide(total + gridDim.x - 1, gridDim.x)), static_cast<long long>(p.min_run));
+    const long long per = max(static_cast<long long>(divide(total + gridDim.x - 1, gridDim.x)), 1LL);
     const long long at = min(static_cast<long long>(blockIdx.x) * per, total);
     const long long len = min(per, total - at);
     Run r{len, per, 0, 0, 0, 0, Seq{0, 0, 0}};
