@@ -314,3 +314,165 @@ def test_a_step_from_rotation_to_eviction(captured):
     for b in range(2):
         got = torch.stack([rows_of(hk, new[b].cpu(), h, keep + 3)[keep:] for h in range(Hkv)], 1)
         assert torch.equal(got.to(BF), plain[3 * b:3 * b + 3])
+
+
+def pairs_that_see(give, n, L, window, sinks):
+    """How much each of L keys receives where query t of n gives give[t] (double) to every key that it sees."""
+    t, j = torch.arange(n), torch.arange(L)
+    pos0 = L - n
+    upto = torch.cat((torch.zeros(1, dtype=torch.float64), give.cumsum(0)))
+    first = (j - pos0).clamp(0, n)  # the first query at or behind key j
+    w = upto[n] - upto[first]
+    if window > 0:
+        last = torch.maximum((j + window - pos0).clamp(0, n), first)
+        w = torch.where(j < sinks, w, upto[last] - upto[first])
+    return w
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("chunks,lens,H,Hkv,D,block,window,sinks", [
+    ([4096], [5000], 16, 1, 64, 64, 0, 0),                # 65536 terms a key
+    ([3001, 1, 700], [3001, 900, 4100], 8, 2, 128, 16, 0, 0),
+    ([2048, 777], [2048, 5000], 14, 2, 64, 32, 600, 5),
+    ([1500], [1400], 5, 1, 128, 128, 0, 0),               # more queries than keys
+    ([2000, 300], [6000, 300], 3, 1, 128, 4, 257, 300),
+])
+def test_every_pair_counts_once(chunks, lens, H, Hkv, D, block, window, sinks):
+    """Queries of zeros with lse 0 give exactly 1 to every key that they see, those with lse -inf nothing, so a weight is a
+    count, and sums of ones are exact in fp32 up to 2^24: one pair lost or doubled among tens of thousands shows."""
+    g = torch.Generator().manual_seed(sum(lens))
+    q, kc, _, table, sl, cu = make(chunks, lens, H, Hkv, D, block, BF, 9)
+    q.zero_()
+    G, T = H // Hkv, q.shape[0]
+    for gives in (torch.ones(H, T), (torch.rand(H, T, generator=g) < 0.7).float()):
+        lse = torch.where(gives > 0, torch.zeros(H, T), torch.full((H, T), -math.inf))
+        ref = torch.zeros(len(lens), Hkv, table.shape[1] * block, dtype=torch.float64)
+        for b, (n, L) in enumerate(zip(chunks, lens)):
+            for h in range(Hkv):
+                give = gives[h * G:h * G + G, int(cu[b]):int(cu[b + 1])].double().sum(0)
+                ref[b, h, :L] = pairs_that_see(give, n, L, window, sinks)
+        args = [t.cuda() for t in (q, lse, kc, table, cu, sl)]
+        w = fa.flash_kv_weights(*args, max(chunks), window, sinks)
+        fa.fa_check_device_error()
+        assert torch.equal(w.cpu().double(), ref)
+        fa.flash_kv_weights(*args, max(chunks), window, sinks, weights=w)
+        assert torch.equal(w.cpu().double(), 2 * ref)
+
+
+def test_pairs_that_see():
+    for n, L, window, sinks in ((5, 9, 0, 0), (9, 5, 0, 0), (7, 20, 3, 2), (1, 1, 1, 0), (9, 5, 2, 1)):
+        give = torch.arange(1, n + 1, dtype=torch.float64)
+        seen = visible_behind(n, L, window, sinks).double()
+        assert torch.equal(pairs_that_see(give, n, L, window, sinks), give @ seen)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("chunks,lens,group", [([32], [200], 4), ([1, 1], [900, 50], 8), ([500, 33], [900, 33], 7), ([2000], [2100], 4)])
+def test_error_of_exact_scores(chunks, lens, group):
+    """q and k of few bits, so that products and their sums are exact however they are added, and scale 1/8. What is left of
+    a term's error: the exponent x = s log2(e) / 8 - lse log2(e), whose two products and their constants are rounded to
+    2^-24 each and whose sum to 2^-24 of itself, times ln 2; and 2^x, 2^-22 of itself. A weight is joined from 8 running
+    sums of 32 terms every second step, 2^-24 each and for the joins."""
+    D, H = 64, 2 * group
+    g = torch.Generator().manual_seed(group)
+    _, kc, _, table, sl, cu = make(chunks, lens, H, 2, D, 16, BF, 5)
+    q = (torch.randint(-4, 5, (sum(chunks), H, D), generator=g) / 4).to(BF)
+    kc = (torch.randint(-4, 5, kc.shape, generator=g) / 4).to(BF)
+    lse = true_lse(q, kc, table, lens, cu, 0, 0, 0.125)
+    w = fa.flash_kv_weights(*(t.cuda() for t in (q, lse, kc, table, cu, sl)), max(chunks), scale=0.125)
+    fa.fa_check_device_error()
+    ref = reference_weights(q, lse, kc, table, lens, cu, 0, 0, 0.125)
+    s = D / 8 * 1.4426951  # the largest score there can be, in powers of two
+    z = float(lse.abs().max()) * 1.4426951
+    tile = min(max(chunks), 128 // group)
+    steps = max(-(-n // tile) for n in chunks) + 1
+    bound = math.log(2) * (2 * s + 2 * z + s + z) * 2.0 ** -24 + 2.0 ** -22 + (32 * -(-steps // 2) + 4) * 2.0 ** -24
+    off = (w.double().cpu() - ref).abs()
+    assert (off <= bound * ref + 1e-37).all(), (float((off / (ref + 1e-30)).max()), bound)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window,sinks,block", [(0, 0, 16), (60, 5, 16), (60, 0, 128), (200, 140, 64), (33, 4, 4)])
+def test_rows_of_128_columns_that_nobody_sees(window, sinks, block):
+    """NaNs in them, in pages that do not exist, and in queries and lse of no chunk change no bit of the result."""
+    chunks, lens, D = [20, 3, 140], [333, 1000, 500], 128
+    q, kc, _, table, sl, cu = make(chunks, lens, 6, 2, D, block, BF, 8, pad=9)
+    lse = torch.zeros(6, q.shape[0])
+    lse[:, :163] = true_lse(q[:163], kc, table, lens, cu, window, sinks, D ** -0.5)
+    ref = reference_weights(q, lse, kc, table, lens, cu, window, sinks, D ** -0.5)
+    call = lambda *a: fa.flash_kv_weights(*(t.cuda() for t in a), 150, window, sinks)  # noqa: E731
+    clean = call(q, lse, kc, table, cu, sl)
+    check_weights(clean, ref)
+    q[163:], lse[:, 163:] = math.nan, math.nan
+    seen_rows = torch.zeros(kc.shape[0], block, dtype=torch.bool)
+    for b, (n, L) in enumerate(zip(chunks, lens)):
+        seen = visible_behind(n, L, window, sinks).any(0)
+        at = torch.nonzero(seen).flatten()
+        seen_rows[table[b][at // block].long(), at % block] = True
+        for x in range(-(-L // block)):
+            if not seen[x * block:(x + 1) * block].any():
+                table[b, x] = 1 << 30
+    kc.masked_fill_(~seen_rows[:, None, :, None], math.nan)
+    assert torch.equal(call(q, lse, kc, table, cu, sl), clean)
+    fa.fa_check_device_error()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window", [0, 40])
+def test_a_table_much_wider_than_the_sequences(window):
+    """Weights that are put (add = 0): zeros in all of the table's other places, an odd number of them."""
+    lens, H, Hkv, D, block, wide = [700, 0, 33], 4, 2, 64, 1, 70001
+    chunks = [5, 0, 33]
+    q, kc, _, table, sl, cu = make(chunks, lens, H, Hkv, D, block, BF, 12)
+    lse = true_lse(q, kc, table, lens, cu, window, 0, D ** -0.5)
+    ref = reference_weights(q, lse, kc, table, lens, cu, window, 0, D ** -0.5)
+    far = torch.full((3, wide), -1, dtype=torch.int32)
+    far[:, :table.shape[1]] = table
+    old = torch.full((3 * Hkv * wide + 2,), math.nan, device="cuda")
+    w = old[1:-1].view(3, Hkv, wide)
+    fa.fa_kv_weights(*(t.cuda() for t in (q, lse, kc, far, cu, sl)), w, 33, window, add=False)
+    fa.fa_check_device_error()
+    check_weights(w[:, :, :table.shape[1]], ref)
+    assert (w[:, :, 700:] == 0).all() and torch.isnan(old[0]) and torch.isnan(old[-1])
+
+
+@pytest.mark.gpu
+def test_streams():
+    """stream= of the weights (both forms) and of the write ahead of them: behind what is queued on the current stream."""
+    lens, chunks, H, Hkv, D, block = [900, 400], [20, 7], 4, 2, 64, 16
+    q, kc, vc, table, sl, cu = (t.cuda() for t in make(chunks, lens, H, Hkv, D, block, BF, 14))
+    f, _ = fa.rope_frequencies(D)
+    g = torch.Generator().manual_seed(3)
+    k, v = (inputs.randn((27, Hkv, D), BF, g).cuda() for _ in range(2))
+    starts = sl - torch.tensor(chunks, dtype=torch.int32, device="cuda")
+
+    ref_k, ref_v = kc.clone(), vc.clone()
+    qr = fa.flash_rope_kv_write(q, k, v, ref_k, ref_v, table, cu, 20, f, starts)
+    o, lse = fa.flash_attention_paged(qr, ref_k, ref_v, table, cu, sl, 20)
+    w = fa.flash_kv_weights(qr, lse, ref_k, table, cu, sl, 20)
+    ref = qr, o, lse, w, fa.flash_kv_weights(qr, lse, ref_k, table, cu, sl, 20, weights=w.clone())
+    torch.cuda.synchronize()
+    for raw in (False, True):
+        side = torch.cuda.Stream()
+        a, b, x = kc.clone(), vc.clone(), torch.empty_like(q)
+        torch.cuda._sleep(2_000_000)
+        x.copy_(q)  # still to come when the calls on the other stream are made
+        kw = {"stream": side.cuda_stream if raw else side}
+        qr = fa.flash_rope_kv_write(x, k, v, a, b, table, cu, 20, f, starts, **kw)
+        o, lse = fa.flash_attention_paged(qr, a, b, table, cu, sl, 20, **kw)
+        w = fa.flash_kv_weights(qr, lse, a, table, cu, sl, 20, **kw)
+        with torch.cuda.stream(side):
+            twice = w.clone()
+        got = fa.flash_kv_weights(qr, lse, a, table, cu, sl, 20, weights=twice, **kw)
+        assert got is twice
+        side.synchronize()
+        for n, (y, z) in enumerate(zip((qr, o, lse, w, twice, a, b), (*ref, ref_k, ref_v))):
+            assert torch.equal(y, z), (raw, n)
+        # the entry points themselves take the stream too
+        again = torch.empty_like(w)
+        side.wait_stream(torch.cuda.current_stream())
+        fa.fa_kv_weights(qr, lse, a, table, cu, sl, again, 20, add=False, **kw)
+        fa.fa_rope_kv_write(x, k, v, qr, a, b, table, cu, 20, f, starts, **kw)
+        side.synchronize()
+        assert torch.equal(again, w) and torch.equal(qr, ref[0]) and torch.equal(a, ref_k)
+    fa.fa_check_device_error()
