@@ -1028,6 +1028,9 @@ fa_status_t fa_rope(const void *x, void *y, const float *inv_freq, const int32_t
         !stride_ok(y_batch) || !stride_ok(y_token) || !stride_ok(y_head) ||
         (S > 0 && ((B > 1 && y_batch == 0) || (S > 1 && y_token == 0) || (H > 1 && y_head == 0))))  // rows of y on one another
         return FA_ERR_SHAPE;
+    // in place, each row where it was
+    if (x == y && ((B > 1 && x_batch != y_batch) || (S > 1 && x_token != y_token) || (H > 1 && x_head != y_head)))
+        return FA_ERR_SHAPE;
     if (!std::isfinite(mscale)) return FA_ERR_SCALE;
     if (!aligned16(x) || !aligned16(y) || !aligned4(inv_freq) || !aligned4(positions)) return FA_ERR_ALIGN;
     if (S == 0) return FA_OK;
@@ -1070,6 +1073,7 @@ fa_status_t fa_rope_kv_write(const void *q, const void *k, const void *v, void *
         H < 0 || Hkv < 1 || static_cast<long long>(H) + 2LL * Hkv > (1 << 24) || !rot_ok(rot_dim, D) ||
         !stride_ok(q_token) || !stride_ok(k_token) || !stride_ok(v_token))
         return FA_ERR_SHAPE;
+    if (H > 0 && total > 1 && q == q_out && q_token != static_cast<int64_t>(H) * D) return FA_ERR_SHAPE;
     int log2_bs = 0;
     if (!pages_ok(Hkv, num_blocks, block_size, max_blocks_per_seq, log2_bs)) return FA_ERR_SHAPE;
     if (!std::isfinite(mscale)) return FA_ERR_SCALE;

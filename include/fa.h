@@ -567,8 +567,8 @@ FA_API fa_status_t fa_decode_paged_q4(const void *q, const void *k_codes, const 
  *              b * x_batch + s * x_token + h * x_head of x, and alike of y:
  *              [B,S,H,D], [B,H,S,D], packed tokens (B = 1, S = total) or a part
  *              of a wider tensor. Strides are >= 0 and multiples of 8. y may be
- *              x itself (same strides); otherwise they must not overlap, nor
- *              may y's rows each other.
+ *              x itself with the same strides (with others the call is refused);
+ *              otherwise they must not overlap, nor may y's rows each other.
  *   inv_freq   device fp32 [rot_dim / 2]; an infinite or NaN one makes its pair
  *              of columns NaN, at position 0 too
  *   positions  device int32 [B,S], or NULL: 0 .. S - 1. Any values: an angle is
@@ -589,8 +589,8 @@ FA_API fa_status_t fa_rope(const void *x, void *y, const float *inv_freq, const 
  * rotated on the way (as fa_rope does it), in one launch.
  *
  *   q, q_out     [total,H,D] queries and where they go, rotated; q_out is
- *                contiguous and may be q where that is too. H = 0: no queries
- *                (both may be NULL).
+ *                contiguous and may be q where that is too (refused where it is
+ *                not). H = 0: no queries (both may be NULL).
  *   k, v         [total,Hkv,D]: the new tokens' keys (stored rotated) and
  *                values (stored as they are); D is 64 or 128
  *   q_token, k_token, v_token   elements between tokens of q, k and v (H * D,

@@ -12,7 +12,7 @@ from exact_attention_54_gb300 import build as fabuild
 from exact_attention_54_gb300 import inputs
 from plain_ops import half_step
 
-OK, NULL, SHAPE, HEADDIM, DTYPE, ALIGN, SCALE = 0, -1, -2, -3, -4, -5, -7
+OK, NULL, SHAPE, HEADDIM, DTYPE, ALIGN, SCALE, CUDA = 0, -1, -2, -3, -4, -5, -7, -8
 DEV_INDEX, DEV_SEQLENS = -11, -13
 A, MIS = 0x10000, 0x10008
 
@@ -99,6 +99,28 @@ def test_no_tokens_of_any_strides(lib):
         x = torch.empty(B, H, 0, 64, dtype=torch.bfloat16)
         st = fa._rows("x", x, x.dtype)
         assert lib.fa_rope(A, A, A, None, B, 0, H, 64, 64, *st, *st, 0, 0, 1.0, 1, None) == OK, (B, H)
+
+
+def test_in_place_with_other_strides_is_refused(lib):
+    """Rows would be written where others are still to be read."""
+    def rope(x, y, B, S, H, xs, ys):
+        return lib.fa_rope(x, y, A, None, B, S, H, 64, 64, *xs, *ys, 0, 0, 1.0, 1, None)
+
+    for B, S, H, xs, ys in ((1, 5, 3, (0, 192, 64), (0, 64, 320)), (2, 5, 1, (320, 64, 64), (640, 64, 64)),
+                            (1, 5, 1, (0, 64, 64), (0, 128, 64)), (1, 1, 3, (0, 0, 64), (0, 0, 128))):
+        assert rope(A, A, B, S, H, xs, ys) == SHAPE, (B, S, H)
+        if not torch.cuda.is_available():  # elsewhere, or the same strides but in dimensions of one
+            assert rope(A, 2 * A, B, S, H, xs, ys) == CUDA
+            assert rope(A, A, B, S, H, xs, xs) == CUDA
+
+    def write(q, out, total, stride):
+        return lib.fa_rope_kv_write(q, A, A, out, A, A, A, None, A, A, None, 1, total, total, 4, 2, 64, 64, stride, 128, 128,
+                                    8, 16, 4, 0, 1.0, 1, None)
+
+    assert write(A, A, 5, 512) == SHAPE
+    if not torch.cuda.is_available():
+        assert write(A, 2 * A, 5, 512) == write(A, A, 5, 256) == write(A, A, 1, 512) == CUDA
+        assert rope(A, A, 1, 1, 1, (64, 64, 64), (8, 8, 8)) == CUDA
 
 
 def test_write_validation(lib):
