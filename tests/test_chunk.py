@@ -407,3 +407,100 @@ def test_caches_past_32_bits():
         fa.fa_check_device_error()
         results.append((qr, o, lse, w, kept, nw, *last))
     assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.gpu
+def test_rows_ahead_of_the_first_chunk_and_limits_far_above():
+    """cu_seqlens that begin behind row 0, and a max_seqlen_q of millions: only the chunks' rows are written."""
+    chunks, lens, ahead = [20, 7], [150, 90], 9
+    q, kc, vc, table, sl, cu = make(chunks, lens, 4, 2, 64, 16, BF, 3, pad=ahead + 4)
+    ref = reference(q[ahead:ahead + 27], kc, vc, table, lens, cu, 0, 0, 0.125)
+    q[:ahead], q[ahead + 27:] = math.nan, math.inf
+    qd, kd, vd, td, sd, cd = (t.cuda() for t in (q, kc, vc, table, sl, cu + ahead))
+    for mx in (20, 5_000_000):
+        o, lse = torch.full_like(qd, 3.0), torch.full((4, q.shape[0]), 5.0, device="cuda")
+        ws = torch.full((fa.fa_fwd_paged_workspace_bytes(mx, 4, 2, 64) // 4,), math.nan, device="cuda")
+        fa.fa_fwd_paged(qd, kd, vd, td, cd, sd, o, lse, ws, mx)
+        w = fa.flash_kv_weights(qd, lse, kd, td, cd, sd, mx)
+        fa.fa_check_device_error()
+        mine = slice(ahead, ahead + 27)
+        check(o[mine], lse[:, mine], ref)
+        for r in (slice(0, ahead), slice(ahead + 27, None)):
+            assert (o[r] == 3).all() and (lse[:, r] == 5).all()
+        assert abs(float(w.double().sum()) - 27 * 4) <= 27 * 4 * 2.0 ** -12
+    # the write: rows ahead of the first sequence go nowhere
+    f, _ = fa.rope_frequencies(64)
+    g = torch.Generator().manual_seed(4)
+    k = inputs.randn((q.shape[0], 2, 64), BF, g).cuda()
+    a, b = kd.clone(), vd.clone()
+    starts = sd - torch.tensor(chunks, dtype=torch.int32, device="cuda")
+    qo = torch.full_like(qd, 7.0)
+    fa.fa_rope_kv_write(qd, k, k, qo, a, b, td, cd, 20, f, starts)
+    c, d = kd.clone(), vd.clone()
+    want = fa.flash_rope_kv_write(qd[mine].contiguous(), k[mine].contiguous(), k[mine].contiguous(), c, d, td, cu.cuda(), 20, f,
+                                  starts)
+    fa.fa_check_device_error()
+    assert torch.equal(qo[mine], want) and (qo[:ahead] == 7).all() and (qo[ahead + 27:] == 7).all()
+    assert torch.equal(a, c) and torch.equal(b, d)
+
+
+@pytest.mark.gpu
+def test_no_chunk_has_tokens():
+    q, kc, vc, table, sl, _ = (t.cuda() for t in make([5], [300], 4, 2, 64, 16, BF, 3))
+    for at in (0, 5):
+        cu = torch.tensor([at, at], dtype=torch.int32, device="cuda")
+        o, lse = torch.full_like(q, 3.0), torch.full((4, 5), 5.0, device="cuda")
+        ws = torch.full((fa.fa_fwd_paged_workspace_bytes(5, 4, 2, 64) // 4,), math.nan, device="cuda")
+        fa.fa_fwd_paged(q, kc, vc, table, cu, sl, o, lse, ws, 5)
+        old = torch.full((1, 2, table.shape[1] * 16), math.nan, device="cuda")
+        fa.fa_kv_weights(q, lse, kc, table, cu, sl, old, 5, add=False)
+        more = fa.flash_kv_weights(q, lse, kc, table, cu, sl, 5, weights=torch.ones_like(old))
+        fa.fa_check_device_error()
+        assert (o == 3).all() and (lse == 5).all() and (old == 0).all() and (more == 1).all()
+
+
+@pytest.mark.gpu
+def test_queries_that_are_not_finite_stay_in_their_rows():
+    chunks, lens = [40, 3], [900, 200]
+    q, kc, vc, table, sl, cu = make(chunks, lens, 4, 2, 64, 16, BF, 8)
+    o, lse = run(q, kc, vc, table, sl, cu, 40)
+    bad = q.clone()
+    bad[17, 1], bad[41, 2, 5] = math.nan, math.inf
+    p, l2 = run(bad, kc, vc, table, sl, cu, 40)
+    rest = torch.ones(43, 4, dtype=torch.bool)
+    rest[17, 1] = rest[41, 2] = False
+    assert torch.equal(p.cpu()[rest], o.cpu()[rest]) and torch.equal(l2.t().cpu()[rest], lse.t().cpu()[rest])
+    assert not torch.isfinite(p.cpu()[17, 1]).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("chunks,lens,H,Hkv,D,block,window,sinks,dtype", [
+    ([3], [20001], 2, 1, 64, 64, 0, 0, BF),
+    ([300, 1, 40], [5000, 17000, 40], 8, 2, 128, 16, 0, 0, BF),
+    ([257, 64], [3000, 9000], 14, 2, 64, 32, 700, 5, FP),
+    ([500], [400], 3, 1, 128, 128, 0, 0, FP),
+    ([90, 200], [4000, 6000], 4, 1, 128, 4, 1025, 300, BF),
+])
+def test_every_key_counts_once(chunks, lens, H, Hkv, D, block, window, sinks, dtype):
+    """Queries of zeros give every key that they see a weight of exactly 1, so lse is ln of their number and, with a 1 in
+    column j % D of key j's value, o the share of those in each column: sums of whole numbers, exact up to 2^24. o is off by
+    one reciprocal, one product (2^-23 each) and its rounding, lse by the logarithm (2^-21 of it and 2^-21)."""
+    q, kc, vc, table, sl, cu = make(chunks, lens, H, Hkv, D, block, dtype, 31)
+    q.zero_()
+    vc.zero_()
+    for b, L in enumerate(lens):
+        j = torch.arange(L)
+        vc[table[b][j // block].long(), :, j % block, j % D] = 1
+    o, lse = run(q, kc, vc, table, sl, cu, max(chunks), window, sinks)
+    o, lse = o.double().cpu(), lse.double().cpu()
+    for b, (n, L) in enumerate(zip(chunks, lens)):
+        seen = visible_behind(n, L, window, sinks).double()
+        share = seen @ torch.nn.functional.one_hot(torch.arange(L) % D, D).double()
+        count, rows = seen.sum(1), slice(int(cu[b]), int(cu[b + 1]))
+        want = (share / count.clamp(min=1)[:, None])[:, None].expand(-1, H, -1)
+        assert ((o[rows] - want).abs() <= want * (half_step(dtype) * (1 + 2.0 ** -20) + 2.0 ** -21)).all()
+        ln = torch.log(count)[None].expand(H, -1)
+        none = (count == 0)[None].expand(H, -1)
+        got = lse[:, rows]
+        assert (got[none] == -math.inf).all()
+        assert ((got - ln).abs()[~none] <= (2.0 ** -21 * (1 + ln))[~none]).all()
