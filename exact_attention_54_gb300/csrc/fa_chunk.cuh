@@ -23,10 +23,16 @@
 // visits and kStart, are laid end to end and cut into equal runs, one per CTA,
 // so that one long sequence or many ragged ones keep every SM busy to the end. A
 // unit that falls into several runs leaves its parts (m, l, O in fp32) in the
-// workspace, and a second launch joins them, row by row in the order of keys.
+// workspace, and a second launch joins them, in a fixed order.
+//
+// Rounding. P is rounded to the 16-bit type once, ahead of P V, as in the packed
+// forward: o is then off by 2.3e-3 (root mean square, bf16; 2.7e-4 fp16) where 32-bit
+// products would leave 1.7e-3 (2.1e-4), o's own rounding. P as two 16-bit numbers, as the
+// paged decode of single tokens takes it, would be half as many products again: 551 us ->
+// 826 at the tensor core's rate for the long chunk below.
 //
 // Bound: long chunks by the tensor core under the power limit, 2048 tokens behind 30000
-// keys, 32 heads on 8 of D = 128: 630 us, 1650 TFLOP/s. 16 chunks of 1 to 512 tokens
+// keys, 32 heads on 8 of D = 128: 631 us, 1650 TFLOP/s, sustained 680 to 717. 16 chunks of 1 to 512 tokens
 // behind up to 7680 keys: 294 us, 1260 TFLOP/s (tensor core 65 % active: starts of units,
 // rows without tokens, keys ahead of the chunk's queries). Few tokens by reading the
 // cache: 5 of 16 sequences of up to 8192 keys 79 us, 5.1 TB/s, of which 20 are the launch,

@@ -7,8 +7,9 @@
 // that stays as an order statistic, digit by digit from the top (11, 11 and 10
 // bits of the weight's bits, ordered as integers; the CTAs add up their counts
 // through distributed shared memory), then writes the keys above it, and as many of
-// the equal ones as there is room for, by prefix sums over the keys. The weights
-// are read from memory once and kept in shared memory, as far as they fit. Copy:
+// the equal ones as there is room for, by prefix sums over the keys. The search works
+// on the weights' order in shared memory, as far as it fits (behind that each digit reads
+// the weights again); the weights themselves are read once more, to be written. Copy:
 // lane groups of 16-byte pieces, page by table on both sides; a stream of 2 D bytes
 // read and written per key and value.
 //

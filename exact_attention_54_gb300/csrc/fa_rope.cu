@@ -12,7 +12,7 @@
 // p inv_freq / 2 pi; far positions lose it in 32 bits (2^20 inv_freq is off by
 // 2^-5 rad), so inv_freq / 2 pi is held as a 64-bit fraction and its product
 // with p wraps as turns do: one integer product, off by 2^-63 p turns at
-// most. The fraction's upper 32 bits, rounded to 24, go into sincospi.
+// most (inv_freq / 4 times that where it is above 4). The fraction's upper 32 bits, rounded to 24, go into sincospi.
 //
 // Grid: a chunk of tokens (x) of one sequence (y, z) per CTA, as in the 4-bit
 // cache's kernels. D / 16 lanes share a row, two 16-byte pieces each: the

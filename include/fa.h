@@ -573,7 +573,8 @@ FA_API fa_status_t fa_decode_paged_q4(const void *q, const void *k_codes, const 
  *              of columns NaN, at position 0 too
  *   positions  device int32 [B,S], or NULL: 0 .. S - 1. Any values: an angle is
  *              formed as a 64-bit fraction of a turn, so far positions keep
- *              theirs (off by 2^-63 |p| turns at most, besides 2^-24 of it).
+ *              theirs (off by 2^-63 |p| max(1, inv_freq / 4) turns at most,
+ *              besides 2^-24 of it).
  *   D          64, 128, 256, 512 or 1024; rot_dim a multiple of 16, 16 .. D
  * S = 0 is allowed and does nothing. One launch.
  * Errors: FA_ERR_NULL, FA_ERR_SHAPE (rot_dim and strides too), FA_ERR_HEADDIM,
@@ -656,6 +657,12 @@ FA_API size_t fa_fwd_paged_workspace_bytes(int max_seqlen_q, int H, int Hkv, int
  * Rows of o and lse that belong to no chunk are left as they were. Rows of a page
  * that no query sees may hold anything, NaNs included; the others must be finite
  * (a key tile is multiplied whole, hidden keys with zero weights).
+ * The softmax weights are rounded to the 16-bit type before they meet V, as in
+ * fa_fwd: o is off by 2.3e-3 of itself in bf16 (2.7e-4 in fp16), root mean square,
+ * where its own rounding alone is 1.7e-3 (2.1e-4). fa_decode_paged_window does not
+ * round them so and is nearer to that.
+ * `window` counts places in the cache. Behind fa_kv_evict, whose key heads each
+ * keep keys of their own, that is no longer a distance in tokens.
  * Offsets outside [0, total_q], decreasing ones, or a chunk longer than
  * max_seqlen_q: nothing is computed and the next fa_check_device_error returns
  * FA_ERR_DEVICE_SEQLENS. Page numbers outside [0, num_blocks) are not
@@ -694,6 +701,11 @@ FA_API fa_status_t fa_fwd_paged(const void *q, const void *k_cache, const void *
  * rows of q and lse that belong to no chunk, may hold anything. Offsets and page
  * numbers are checked as by fa_fwd_paged (a page that does not exist counts as
  * zeros). The result is deterministic. One launch, no workspace.
+ * Sums are fp32: of n terms (queries times heads of a group) a key has eight
+ * running ones, so a weight is off by about 2^-27 n of itself at most (1e-7 to
+ * 2.5e-7, root mean square, in practice) besides what a term is off by (some
+ * 2^-22 (1 + |scale q.k| + |lse|)). With add = 1 a call's sum is rounded to the
+ * steps of what is there: below 2^-25 of it, it vanishes.
  * Errors: FA_ERR_NULL, FA_ERR_SHAPE (negative strides too), FA_ERR_HEADDIM,
  * FA_ERR_DTYPE, FA_ERR_ALIGN, FA_ERR_SCALE, FA_ERR_CUDA.
  */
@@ -710,7 +722,8 @@ FA_API fa_status_t fa_kv_weights(const void *q, const float *lse, const void *k_
  * `keep`: the first `sinks`, the last `recent`, and of those between them the
  * ones of greatest weight (ties to the earlier key; a NaN is less than any
  * number). They keep their order and become keys 0 .. keep - 1 of the new
- * pages, each head its own. With L <= keep all stay, as keys 0 .. L - 1.
+ * pages, each head its own. With L <= keep all stay, as keys 0 .. L - 1. (A
+ * window of a later call counts these places, not tokens.)
  *
  *   k_cache, v_cache [num_blocks,Hkv,block_size,D] fp16/bf16, D 64 or 128
  *   weights      [B,Hkv,max_blocks_per_seq * block_size] fp32, as fa_kv_weights
