@@ -1029,7 +1029,8 @@ fa_status_t fa_rope(const void *x, void *y, const float *inv_freq, const int32_t
         (S > 0 && ((B > 1 && y_batch == 0) || (S > 1 && y_token == 0) || (H > 1 && y_head == 0))))  // rows of y on one another
         return FA_ERR_SHAPE;
     // in place, each row where it was
-    if (x == y && ((B > 1 && x_batch != y_batch) || (S > 1 && x_token != y_token) || (H > 1 && x_head != y_head)))
+    if (S > 0 && x == y &&
+        ((B > 1 && x_batch != y_batch) || (S > 1 && x_token != y_token) || (H > 1 && x_head != y_head)))
         return FA_ERR_SHAPE;
     if (!std::isfinite(mscale)) return FA_ERR_SCALE;
     if (!aligned16(x) || !aligned16(y) || !aligned4(inv_freq) || !aligned4(positions)) return FA_ERR_ALIGN;

@@ -65,7 +65,7 @@ extern "C" {
 typedef enum {
     FA_OK = 0,
     FA_ERR_NULL = -1,           /* a required pointer is NULL */
-    FA_ERR_SHAPE = -2,          /* a size is <= 0, or too large for 32-bit indexing */
+    FA_ERR_SHAPE = -2,          /* a size is <= 0, or too large for 32-bit indexing, or arrays lie on one another */
     FA_ERR_HEADDIM = -3,        /* D not supported: forward 64/128/256/512/1024, decode and backward 64/128 */
     FA_ERR_DTYPE = -4,          /* dtype is not FA_FP16 or FA_BF16 */
     FA_ERR_ALIGN = -5,          /* a 16-bit tensor is not 16-byte aligned (fp32: 4-byte) */

@@ -95,6 +95,8 @@ def test_no_tokens_of_any_strides(lib):
     """S = 0 does nothing, also where the strides are those of an empty contiguous [B,H,0,D] (0 between heads)."""
     for ys in ((0, 64, 0), (0, 64, 64), (0, 0, 0), (256, 64, 64)):
         assert lib.fa_rope(None, None, A, None, 2, 0, 4, 64, 64, *ys, *ys, 0, 0, 1.0, 1, None) == OK, ys
+        for at in (None, A):  # "in place", with strides that mean nothing
+            assert lib.fa_rope(at, at, A, None, 2, 0, 4, 64, 64, 512, 128, 64, *ys, 0, 0, 1.0, 1, None) == OK, ys
     for B, H in ((1, 4), (2, 1), (2, 4)):
         x = torch.empty(B, H, 0, 64, dtype=torch.bfloat16)
         st = fa._rows("x", x, x.dtype)
